@@ -12,7 +12,11 @@
  *   4. the GPTQ packer that produces the weight format of 2 and 3,
  *   5. the vocabulary head with fused greedy argmax (2 or 3 reduced to the
  *      largest output per row),
- *   6. the ingest of the compressed-tensors per-output-row packed orientation.
+ *   6. the ingest of the compressed-tensors per-output-row packed orientation,
+ *   7. a W8A8 GEMM with one scale per token and one per output channel over
+ *      the same GPTQ words,
+ *   8. the residual addition fused with RMSNorm and 1, and the logits after
+ *      the vocabulary head adjusted by penalties, biases and grammar masks.
  *
  * Format (all calls): GPTQ qweight / qzeros / scales, no g_idx,
  * desc_act = false, symmetric, groups of exactly 128 contiguous K
@@ -155,6 +159,35 @@ qlin_status_t qlin_silu_mul_act_quant_c16(const uint16_t *gate_up, int64_t M, in
                                           qlin_stream_t stream);
 
 /*
+ * The residual addition fused with the RMSNorm producer above: for each row m
+ *   h[m,k] = bf16(x[m,k] + residual[m,k])   (the new residual stream),
+ * then z and (q, s_a) from h exactly as qlin_rmsnorm_act_quant_i8 forms them
+ * from its x.  A decoder layer adds each sublayer's output to the residual
+ * stream in front of the next norm; fused, the sum is written once and never
+ * read back.
+ *
+ *   x, residual   bf16 [M, K]
+ *   gamma         bf16 [K];  eps >= 0, finite
+ *   residual_out  bf16 [M, K]  output h; may be x or residual itself (in
+ *                 place), but not overlap either of them otherwise
+ *   q, s_a, y     as for the RMSNorm producer (y, z itself, may be NULL)
+ *
+ * A row of h that is all zero gives z = 0, q = 0 and s_a = 0, also with
+ * eps = 0.  Non-finite sums, rows whose mean of h^2 is not a normal fp32
+ * number with eps = 0, and sums of h^2 of 2^127 and more are outside the
+ * contract.  Errors as for the RMSNorm producer.
+ */
+qlin_status_t qlin_add_rmsnorm_act_quant_i8(const uint16_t *x, const uint16_t *residual,
+                                            const uint16_t *gamma, float eps, int64_t M,
+                                            int64_t K, uint16_t *residual_out, int8_t *q,
+                                            float *s_a, uint16_t *y, qlin_stream_t stream);
+
+qlin_status_t qlin_add_rmsnorm_act_quant_c16(const uint16_t *x, const uint16_t *residual,
+                                             const uint16_t *gamma, float eps, int64_t M,
+                                             int64_t K, uint16_t *residual_out, uint16_t *q,
+                                             float *s_a, uint16_t *y, qlin_stream_t stream);
+
+/*
  * W8A8 GS128 linear:  y = bf16( s_a[m] * sum_g s_w[g,n] * P[g,m,n] ),
  * P[g,m,n] = sum_{k = 128g}^{128g+127} q_a[m,k] * q_w[k,n]  (exact integers).
  *
@@ -231,6 +264,39 @@ qlin_status_t qlin_gemm_w8a8_gs128_noalloc(const int8_t *q_a, const float *s_a,
                                            const int32_t *qweight, const uint16_t *scales,
                                            int64_t M, int64_t N, int64_t K, uint16_t *y,
                                            qlin_stream_t stream);
+
+/*
+ * W8A8 linear with one scale per token and one per output channel:
+ *   P[m,n] = sum_k q_a[m,k] * q_w[k,n]   (an exact integer),
+ *   y[m,n] = bf16( (float(P) * s_w[n]) * s_a[m] ), each product rounded to
+ *            fp32, nearest even.
+ *
+ * P is exact for every K the call takes, so a row of y does not depend on M,
+ * on the other rows or on how the library splits K.
+ *
+ *   q_a      int8 [M, K], or (_c16) fp16 [M, K] holding integers in
+ *            [-127, 127]: the codes of the act-quant producers above.  Int8
+ *            codes of -128 are taken as they are; other fp16 values are
+ *            outside the contract.
+ *   s_a      fp32 [M]
+ *   qweight  int32 [K/4, N]  8-bit GPTQ words as for qlin_gemm_w8a8_gs128
+ *   s_w      fp32 [N]        one scale per output channel
+ *   y        bf16 [M, N]     output
+ *   workspace / workspace_bytes (int8 entry only)  at least
+ *            qlin_gemm_w8a8_ch_workspace_bytes(M, N, K) bytes; may be NULL
+ *            where that is 0.  It needs no zeroing and holds nothing between
+ *            calls.  Calls that share a workspace must not overlap.
+ *
+ * K is at most 130,944 (QLIN_ERR_SHAPE above): sums of that many products of
+ * two int8 values fit int32.
+ */
+size_t qlin_gemm_w8a8_ch_workspace_bytes(int64_t M, int64_t N, int64_t K);
+qlin_status_t qlin_gemm_w8a8_ch(const int8_t *q_a, const float *s_a, const int32_t *qweight,
+                                const float *s_w, int64_t M, int64_t N, int64_t K, uint16_t *y,
+                                void *workspace, size_t workspace_bytes, qlin_stream_t stream);
+qlin_status_t qlin_gemm_w8a8_ch_c16(const uint16_t *q_a, const float *s_a,
+                                    const int32_t *qweight, const float *s_w, int64_t M,
+                                    int64_t N, int64_t K, uint16_t *y, qlin_stream_t stream);
 
 /*
  * W4A16 g128 symmetric weight-only linear:
@@ -354,6 +420,60 @@ qlin_status_t qlin_gemm_w4a16_g128_argmax(const uint16_t *x, const int32_t *qwei
                                           size_t workspace_bytes, qlin_stream_t stream);
 
 /*
+ * Logits adjusted for the choice of the next token: penalties for repeated
+ * tokens, biases and a grammar mask, and the greedy token of the result.  For
+ * the heads above that write their logits (the fused argmax heads see the
+ * unadjusted ones only).
+ *
+ * For row m, with n(v) the number of times v occurs among the row's generated
+ * tokens and seen(v) whether it occurs among its prompt or generated tokens,
+ * in fp32 with every operation rounded to nearest even, in this order:
+ *   x <- x > 0 ? x / repetition[m] : x * repetition[m]        where seen(v)
+ *   x <- x - (frequency[m] * n(v) + presence[m])              where n(v) > 0
+ *   x <- x + bias[m,j]                                        where v = bias_ids[m,j]
+ *   x <- -inf                                                 where allowed's bit v is 0
+ * rounded once to the logits' type.  Where several entries of bias_ids[m]
+ * hold the same v, the last one applies.  A masked logit becomes -inf
+ * whatever it was (NaN and infinities included).
+ *
+ *   logits       bf16 (or fp32) [M, V]; V a positive multiple of 8
+ *   tokens       int32 [M, L]  the rows' tokens: prompt_len[m] of the prompt,
+ *                then generated ones up to total_len[m]; positions from
+ *                total_len[m] on are not read.  May be NULL with L = 0.
+ *   prompt_len   int32 [M] or NULL (no prompt: all tokens are generated)
+ *   total_len    int32 [M] or NULL (L for every row).  Lengths outside
+ *                [0, L] are taken as the nearer end.
+ *   repetition, presence, frequency  fp32 [M], finite, repetition > 0, or
+ *                NULL (1, 0 and 0)
+ *   bias_ids     int32 [M, B], bias fp32 [M, B]; may be NULL with B = 0
+ *   allowed      int32 [M, ceil(V/32)] or NULL: bit v % 32 of word v / 32,
+ *                least significant first, is 1 where v is allowed
+ *   out          the adjusted logits, logits' type [M, V], or NULL; may be
+ *                logits itself (in place), but not overlap it otherwise
+ *   argmax       int32 [M] or NULL: the index of the largest adjusted value
+ *                (after rounding), the lowest on ties, NaN never; -1 for a
+ *                row without a value above -inf.  -0 equals +0.
+ *
+ * Ids outside [0, V) in tokens and bias_ids are skipped.  out and argmax
+ * must not both be NULL (QLIN_ERR_NULL).  logits and out are 16-byte
+ * aligned, all other pointers 4-byte.  L and B are at most 2^30.
+ */
+qlin_status_t qlin_adjust_logits_bf16(const uint16_t *logits, int64_t M, int64_t V,
+                                      const int32_t *tokens, int64_t L,
+                                      const int32_t *prompt_len, const int32_t *total_len,
+                                      const float *repetition, const float *presence,
+                                      const float *frequency, const int32_t *bias_ids,
+                                      const float *bias, int64_t B, const int32_t *allowed,
+                                      uint16_t *out, int32_t *argmax, qlin_stream_t stream);
+qlin_status_t qlin_adjust_logits_f32(const float *logits, int64_t M, int64_t V,
+                                     const int32_t *tokens, int64_t L,
+                                     const int32_t *prompt_len, const int32_t *total_len,
+                                     const float *repetition, const float *presence,
+                                     const float *frequency, const int32_t *bias_ids,
+                                     const float *bias, int64_t B, const int32_t *allowed,
+                                     float *out, int32_t *argmax, qlin_stream_t stream);
+
+/*
  * GPTQ packer (offline step; not on the timed path).
  *
  * Passages: "Flint-DFlash2-GPTQ-INT8-PTQR" card, parameter table (GPTQ
@@ -451,7 +571,10 @@ const char *qlin_status_string(qlin_status_t status);
  * calls now take at most 96 rows.  1.3 (103) adds the fp16 activation codes
  * (qlin_act_quant_c16, qlin_rmsnorm_act_quant_c16,
  * qlin_silu_mul_act_quant_c16, qlin_gemm_w8a8_gs128_c16); the workspace of
- * batches of up to 32 tokens grows by M * K bytes. */
+ * batches of up to 32 tokens grows by M * K bytes.  Later additions that
+ * change no earlier call keep 1.3: qlin_add_rmsnorm_act_quant_{i8,c16},
+ * qlin_gemm_w8a8_ch{,_c16} with its workspace size, and
+ * qlin_adjust_logits_{bf16,f32}. */
 int qlin_version(void);
 
 #ifdef __cplusplus

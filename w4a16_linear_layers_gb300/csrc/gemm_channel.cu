@@ -1,0 +1,274 @@
+// gemm_channel.cu -- the INT8 x INT8 linear with one scale per token and one
+// per output channel:
+//
+//   P[m,n] = sum_k q_a[m,k] * q_w[k,n]   (an exact integer),
+//   y[m,n] = bf16( (float(P) * s_w[n]) * s_a[m] ).
+//
+// P is exact whatever the tiling and the split of K: codes are exact in fp16,
+// products and sums of up to 1024 of them stay within 2^24 and so are exact in
+// an fp32 accumulator, and the sums of each 1024 are added as int32.  y
+// therefore does not depend on M, on the split or on the device.
+//
+// Small batches (streaming kernel).  The weights pass once and HBM is the
+// bound.  Every warp streams its own weights from global memory straight into
+// registers (16-byte loads, one 64-wide K block in flight while the previous
+// one is multiplied), widens them to fp16 in place and multiplies them with
+// mma.sync: there is no shared-memory ring, no barrier and no tensor-memory
+// hand-off on the way, so nothing but the loads themselves paces the stream.
+// The legacy tensor path does one m16n8k16 per 2 cycles and SM (measured),
+// 256 weight bytes x 8 tokens; HBM delivers 256 bytes per 11 cycles and SM, so
+// up to 32 tokens (4 products per 256 bytes) it has room to spare.  (The int8
+// form, m16n8k32, takes 16 cycles here.)
+//   * A block's 8 warps share 64 output channels and interleave the 64-wide
+//     K blocks between them; a cluster of up to 8 blocks splits K further where
+//     the channels alone do not fill the machine.  Partials are integers:
+//     they meet in shared memory by atomic addition, and across the cluster
+//     through distributed shared memory, in any order with one result.
+//   * K inside a block is permuted so that a thread's 16 codes of a token are
+//     16 contiguous bytes, and its weights are the words of 4 neighbouring
+//     channels: all loads are 16 bytes.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "qlin_device.cuh"
+#include "qlin_internal.h"
+
+namespace qlin {
+namespace {
+
+constexpr int kSWarps = 8;                 // warps of a block, along K
+constexpr int kSThreads = 32 * kSWarps;
+constexpr int kKB = 64;                    // K of one step of a warp
+constexpr int kExactBlocks = 1024 / kKB;   // steps whose fp32 sums stay exact
+
+struct ChannelParams {
+  const void* act;          // int8 or fp16 codes [M, K]
+  const float* s_a;         // [M]
+  const uint32_t* w;        // 8-bit GPTQ words [K/4, N]
+  const float* s_w;         // [N]
+  uint16_t* y;              // bf16 [M, N]
+  int64_t M, N, K;
+};
+
+__device__ __forceinline__ void mma_f16(float* d, uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint4 ld_stream(const uint32_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+
+__device__ __forceinline__ int ld_cluster_s32(uint32_t local_addr, uint32_t rank) {
+  uint32_t remote;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local_addr), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ uint16_t channel_out(int p, float sw, float sa) {
+  return __bfloat16_as_ushort(__float2bfloat16_rn(__fmul_rn(__fmul_rn(__int2float_rn(p), sw), sa)));
+}
+
+// kHalves x 32 output channels and 8 kTok tokens a block.
+template <int kHalves, int kTok, bool kC16>
+__global__ void __launch_bounds__(kSThreads) stream_kernel(const ChannelParams p, int splits) {
+  constexpr int F = 32 * kHalves;
+  constexpr int T = 8 * kTok;
+  constexpr int kPad = F + 4;                  // words of one token's row of partials
+  __shared__ int part[T * kPad];
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int g = lane >> 2;                     // channel group of 4, and token of a tile of 8
+  const int t = lane & 3;                      // quarter of the 64-wide K block
+  const uint32_t rank = splits > 1 ? cluster_rank() : 0u;
+  const int64_t f0 = static_cast<int64_t>(blockIdx.x / splits) * F;
+  const int64_t m0 = static_cast<int64_t>(blockIdx.y) * T;
+  const int64_t N = p.N, K = p.K;
+  const int nkb = static_cast<int>(K / kKB);
+  const int stride = kSWarps * splits;
+  const int first = static_cast<int>(rank) * kSWarps + warp;
+
+  for (int i = threadIdx.x; i < T * kPad; i += kSThreads) part[i] = 0;
+
+  // this thread's words: rows 4t .. 4t+3 of each K block's 16, channels 4g .. 4g+3 of each 32
+  const uint32_t* wbase = p.w + static_cast<int64_t>(4 * t) * N + f0 + 4 * g;
+  bool have[kHalves];
+#pragma unroll
+  for (int hf = 0; hf < kHalves; ++hf) have[hf] = f0 + 32 * hf + 4 * g < N;   // N is a multiple of 8
+  uint4 w[4 * kHalves];
+  auto load_w = [&](int kb) {
+    const uint32_t* src = wbase + static_cast<int64_t>(kb) * 16 * N;
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int hf = 0; hf < kHalves; ++hf)
+        w[s * kHalves + hf] = have[hf] ? ld_stream(src + s * N + 32 * hf) : make_uint4(0, 0, 0, 0);
+  };
+  if (first < nkb) load_w(first);   // the weights depend on no earlier kernel
+  grid_dep_launch();
+  grid_dep_wait();
+  __syncthreads();
+
+  const char* abase[kTok];
+#pragma unroll
+  for (int i = 0; i < kTok; ++i) {
+    int64_t m = m0 + 8 * i + g;
+    if (m >= p.M) m = p.M - 1;      // computed and not written
+    abase[i] = static_cast<const char*>(p.act) + (m * K + 16 * t) * (kC16 ? 2 : 1);
+  }
+
+  float acc[2 * kHalves][kTok][4];
+#pragma unroll
+  for (int j = 0; j < 2 * kHalves; ++j)
+#pragma unroll
+    for (int i = 0; i < kTok; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[j][i][e] = 0.0f;
+
+  auto flush = [&]() {
+#pragma unroll
+    for (int j = 0; j < 2 * kHalves; ++j)
+#pragma unroll
+      for (int i = 0; i < kTok; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          // row of the 16 x 8 result: channel 4g + 2 (j & 1) + (e >> 1); column: token 2t + (e & 1)
+          const int ch = 32 * (j >> 1) + 4 * g + 2 * (j & 1) + (e >> 1);
+          const int tok = 8 * i + 2 * t + (e & 1);
+          atomicAdd(&part[tok * kPad + ch], __float2int_rn(acc[j][i][e]));
+          acc[j][i][e] = 0.0f;
+        }
+  };
+
+  int done = 0;
+  for (int kb = first; kb < nkb; kb += stride) {
+    uint4 a[kTok][kC16 ? 2 : 1];
+#pragma unroll
+    for (int i = 0; i < kTok; ++i) {
+      const uint4* src = reinterpret_cast<const uint4*>(abase[i] + static_cast<int64_t>(kb) * kKB * (kC16 ? 2 : 1));
+      a[i][0] = src[0];
+      if constexpr (kC16) a[i][1] = src[1];
+    }
+    uint4 cur[4 * kHalves];
+#pragma unroll
+    for (int i = 0; i < 4 * kHalves; ++i) cur[i] = w[i];
+    if (kb + stride < nkb) load_w(kb + stride);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      uint32_t b[kTok][2];
+#pragma unroll
+      for (int i = 0; i < kTok; ++i) {
+        if constexpr (kC16) {
+          const uint4 v = a[i][s >> 1];
+          b[i][0] = (s & 1) ? v.z : v.x;
+          b[i][1] = (s & 1) ? v.w : v.y;
+        } else {
+          const uint4 v = a[i][0];
+          const uint32_t word = s == 0 ? v.x : s == 1 ? v.y : s == 2 ? v.z : v.w;
+          biased_u8x4_to_f16x4(word ^ 0x80808080u, b[i][0], b[i][1]);
+        }
+      }
+#pragma unroll
+      for (int hf = 0; hf < kHalves; ++hf) {
+        const uint4 v = cur[s * kHalves + hf];
+        uint32_t c0[2], c1[2], c2[2], c3[2];
+        biased_u8x4_to_f16x4(v.x, c0[0], c0[1]);
+        biased_u8x4_to_f16x4(v.y, c1[0], c1[1]);
+        biased_u8x4_to_f16x4(v.z, c2[0], c2[1]);
+        biased_u8x4_to_f16x4(v.w, c3[0], c3[1]);
+#pragma unroll
+        for (int i = 0; i < kTok; ++i) {
+          mma_f16(acc[2 * hf][i], c0[0], c1[0], c0[1], c1[1], b[i][0], b[i][1]);
+          mma_f16(acc[2 * hf + 1][i], c2[0], c3[0], c2[1], c3[1], b[i][0], b[i][1]);
+        }
+      }
+    }
+    if (++done == kExactBlocks) {
+      flush();
+      done = 0;
+    }
+  }
+  if (done) flush();
+
+  // each block of the cluster finishes its share of the tile's outputs
+  if (splits > 1) cluster_sync_all();
+  else __syncthreads();
+  const uint32_t pbase = smem_u32(part);
+  constexpr int kPairs = T * F / 2;            // two neighbouring channels at a time
+  for (int o = static_cast<int>(rank) * kSThreads + threadIdx.x; o < kPairs; o += kSThreads * splits) {
+    const int tok = o / (F / 2);
+    const int ch = 2 * (o - tok * (F / 2));
+    const int64_t m = m0 + tok;
+    const int64_t n = f0 + ch;
+    if (m >= p.M || n >= N) continue;
+    int v0 = 0, v1 = 0;
+    const int at = tok * kPad + ch;
+    if (splits > 1) {
+      for (int r = 0; r < splits; ++r) {
+        v0 += ld_cluster_s32(pbase + 4u * at, r);
+        v1 += ld_cluster_s32(pbase + 4u * (at + 1), r);
+      }
+    } else {
+      v0 = part[at];
+      v1 = part[at + 1];
+    }
+    const float sa = __ldg(p.s_a + m);
+    const uint32_t out = static_cast<uint32_t>(channel_out(v0, __ldg(p.s_w + n), sa)) |
+                         (static_cast<uint32_t>(channel_out(v1, __ldg(p.s_w + n + 1), sa)) << 16);
+    *reinterpret_cast<uint32_t*>(p.y + m * N + n) = out;
+  }
+  if (splits > 1) cluster_sync_all();   // no block leaves while another reads its partials
+}
+
+template <int kHalves, int kTok, bool kC16>
+cudaError_t launch_stream(const ChannelParams& p, int splits, cudaStream_t stream) {
+  const int64_t ftiles = (p.N + 32 * kHalves - 1) / (32 * kHalves);
+  const int64_t mtiles = (p.M + 8 * kTok - 1) / (8 * kTok);
+  return launch_cluster_pdl(stream_kernel<kHalves, kTok, kC16>,
+                            dim3(static_cast<unsigned>(ftiles * splits), static_cast<unsigned>(mtiles)),
+                            dim3(kSThreads), 0, splits, stream, p, splits);
+}
+
+template <bool kC16>
+cudaError_t launch_c(const ChannelParams& p, int sm_count, cudaStream_t stream) {
+  const int64_t ftiles = (p.N + 63) / 64;
+  const int64_t mtiles = (p.M + 15) / 16;
+  const int64_t nkb = p.K / kKB;
+  // split K while two blocks an SM are not reached and every warp keeps a K block
+  int splits = 1;
+  while (splits < 8 && ftiles * mtiles * splits < 2 * sm_count && nkb >= 2 * splits * kSWarps) splits *= 2;
+  return p.M <= 8 ? launch_stream<2, 1, kC16>(p, splits, stream)
+                  : launch_stream<2, 2, kC16>(p, splits, stream);
+}
+
+}  // namespace
+
+size_t channel_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
+
+cudaError_t launch_gemm_channel(const ChannelGemmArgs& a, int*, int sm_count, cudaStream_t stream) {
+  const ChannelParams p{a.act, a.s_a, reinterpret_cast<const uint32_t*>(a.qweight), a.s_w, a.y, a.M, a.N, a.K};
+  return a.act_c16 ? launch_c<true>(p, sm_count, stream) : launch_c<false>(p, sm_count, stream);
+}
+
+}  // namespace qlin

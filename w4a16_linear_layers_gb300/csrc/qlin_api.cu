@@ -174,6 +174,70 @@ qlin_status_t run_rmsnorm_quant(const uint16_t* x, const uint16_t* gamma, float 
       launch_rmsnorm_quant(x, gamma, eps, M, K, q, c16, s_a, y, d->err_word, d->sm_count, stream));
 }
 
+qlin_status_t run_add_rmsnorm_quant(const uint16_t* x, const uint16_t* r, const uint16_t* gamma,
+                                    float eps, int64_t M, int64_t K, uint16_t* h, void* q,
+                                    bool c16, float* s_a, uint16_t* y, cudaStream_t stream) {
+  if (gamma == nullptr || (M != 0 && (x == nullptr || r == nullptr || h == nullptr ||
+                                      q == nullptr || s_a == nullptr)))
+    return QLIN_ERR_NULL;
+  if (M < 0 || M > kMaxDim || K < kGroup || K > kMaxDim || (K % kGroup) != 0 || !(eps >= 0.0f) ||
+      !std::isfinite(eps))
+    return QLIN_ERR_SHAPE;
+  if (!aligned16(x) || !aligned16(r) || !aligned16(gamma) || !aligned16(h) || !aligned16(q) ||
+      !aligned16(s_a) || !aligned16(y))
+    return QLIN_ERR_ALIGN;
+  const DeviceInfo* d = nullptr;
+  qlin_status_t st = device_or_error(&d);
+  if (st != QLIN_OK) return st;
+  if (M == 0) return QLIN_OK;
+  return from_cuda(
+      launch_add_rmsnorm_quant(x, r, gamma, eps, M, K, h, q, c16, s_a, y, d->sm_count, stream));
+}
+
+qlin_status_t run_gemm_channel(const void* q_a, bool c16, const float* s_a, const int32_t* qweight,
+                               const float* s_w, int64_t M, int64_t N, int64_t K, uint16_t* y,
+                               void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (qweight == nullptr || s_w == nullptr ||
+      (M != 0 && (q_a == nullptr || s_a == nullptr || y == nullptr)))
+    return QLIN_ERR_NULL;
+  qlin_status_t st = check_gemm_shape(M, N, K);
+  if (st != QLIN_OK) return st;
+  if (K > kChannelMaxK) return QLIN_ERR_SHAPE;
+  if (!aligned16(q_a) || !aligned16(s_a) || !aligned16(qweight) || !aligned16(s_w) ||
+      !aligned16(y) || !aligned16(workspace))
+    return QLIN_ERR_ALIGN;
+  const DeviceInfo* d = nullptr;
+  st = device_or_error(&d);
+  if (st != QLIN_OK) return st;
+  if (M == 0) return QLIN_OK;
+  const size_t need = c16 ? 0 : channel_workspace_bytes(M, N, K);
+  if (need != 0 && (workspace == nullptr || workspace_bytes < need)) return QLIN_ERR_WORKSPACE;
+  const ChannelGemmArgs a{q_a, c16, s_a, qweight, s_w, y, M, N, K, workspace};
+  return from_cuda(launch_gemm_channel(a, d->err_word, d->sm_count, stream));
+}
+
+qlin_status_t run_adjust_logits(const LogitArgs& a, cudaStream_t stream) {
+  constexpr int64_t kMaxList = 1LL << 30;
+  if ((a.out == nullptr && a.argmax == nullptr && a.M != 0) || (a.M != 0 && a.logits == nullptr) ||
+      (a.M != 0 && a.L > 0 && a.tokens == nullptr) ||
+      (a.M != 0 && a.B > 0 && (a.bias_ids == nullptr || a.bias == nullptr)))
+    return QLIN_ERR_NULL;
+  if (a.M < 0 || a.M > kMaxDim || a.V < 8 || a.V > kMaxDim || (a.V % 8) != 0 || a.L < 0 ||
+      a.L > kMaxList || a.B < 0 || a.B > kMaxList)
+    return QLIN_ERR_SHAPE;
+  auto aligned4 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; };
+  if (!aligned16(a.logits) || !aligned16(a.out) || !aligned4(a.tokens) || !aligned4(a.prompt_len) ||
+      !aligned4(a.total_len) || !aligned4(a.repetition) || !aligned4(a.presence) ||
+      !aligned4(a.frequency) || !aligned4(a.bias_ids) || !aligned4(a.bias) ||
+      !aligned4(a.allowed) || !aligned4(a.argmax))
+    return QLIN_ERR_ALIGN;
+  const DeviceInfo* d = nullptr;
+  qlin_status_t st = device_or_error(&d);
+  if (st != QLIN_OK) return st;
+  if (a.M == 0) return QLIN_OK;
+  return from_cuda(launch_adjust_logits(a, d->sm_count, stream));
+}
+
 qlin_status_t run_silu_mul_quant(const uint16_t* gate_up, int64_t M, int64_t I, void* q, bool c16,
                                  float* s_a, uint16_t* y, cudaStream_t stream) {
   if (M != 0 && (gate_up == nullptr || q == nullptr || s_a == nullptr)) return QLIN_ERR_NULL;
@@ -354,6 +418,65 @@ qlin_status_t qlin_pack_tiles(const int32_t* qweight, int64_t K, int64_t N, int 
   if (st != QLIN_OK) return st;
   return from_cuda(launch_pack_tiles(qweight, K, N, bits, tiles,
                                      reinterpret_cast<cudaStream_t>(stream)));
+}
+
+qlin_status_t qlin_add_rmsnorm_act_quant_i8(const uint16_t* x, const uint16_t* residual,
+                                            const uint16_t* gamma, float eps, int64_t M,
+                                            int64_t K, uint16_t* residual_out, int8_t* q,
+                                            float* s_a, uint16_t* y, qlin_stream_t stream) {
+  return run_add_rmsnorm_quant(x, residual, gamma, eps, M, K, residual_out, q, false, s_a, y,
+                               reinterpret_cast<cudaStream_t>(stream));
+}
+
+qlin_status_t qlin_add_rmsnorm_act_quant_c16(const uint16_t* x, const uint16_t* residual,
+                                             const uint16_t* gamma, float eps, int64_t M,
+                                             int64_t K, uint16_t* residual_out, uint16_t* q,
+                                             float* s_a, uint16_t* y, qlin_stream_t stream) {
+  return run_add_rmsnorm_quant(x, residual, gamma, eps, M, K, residual_out, q, true, s_a, y,
+                               reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t qlin_gemm_w8a8_ch_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (check_gemm_shape(M, N, K) != QLIN_OK || K > kChannelMaxK || M == 0) return 0;
+  return channel_workspace_bytes(M, N, K);
+}
+
+qlin_status_t qlin_gemm_w8a8_ch(const int8_t* q_a, const float* s_a, const int32_t* qweight,
+                                const float* s_w, int64_t M, int64_t N, int64_t K, uint16_t* y,
+                                void* workspace, size_t workspace_bytes, qlin_stream_t stream) {
+  return run_gemm_channel(q_a, false, s_a, qweight, s_w, M, N, K, y, workspace, workspace_bytes,
+                          reinterpret_cast<cudaStream_t>(stream));
+}
+
+qlin_status_t qlin_gemm_w8a8_ch_c16(const uint16_t* q_a, const float* s_a, const int32_t* qweight,
+                                    const float* s_w, int64_t M, int64_t N, int64_t K,
+                                    uint16_t* y, qlin_stream_t stream) {
+  return run_gemm_channel(q_a, true, s_a, qweight, s_w, M, N, K, y, nullptr, 0,
+                          reinterpret_cast<cudaStream_t>(stream));
+}
+
+qlin_status_t qlin_adjust_logits_bf16(const uint16_t* logits, int64_t M, int64_t V,
+                                      const int32_t* tokens, int64_t L, const int32_t* prompt_len,
+                                      const int32_t* total_len, const float* repetition,
+                                      const float* presence, const float* frequency,
+                                      const int32_t* bias_ids, const float* bias, int64_t B,
+                                      const int32_t* allowed, uint16_t* out, int32_t* argmax,
+                                      qlin_stream_t stream) {
+  return run_adjust_logits(LogitArgs{logits, false, M, V, tokens, L, prompt_len, total_len, repetition,
+                                     presence, frequency, bias_ids, bias, B, allowed, out, argmax},
+                           reinterpret_cast<cudaStream_t>(stream));
+}
+
+qlin_status_t qlin_adjust_logits_f32(const float* logits, int64_t M, int64_t V,
+                                     const int32_t* tokens, int64_t L, const int32_t* prompt_len,
+                                     const int32_t* total_len, const float* repetition,
+                                     const float* presence, const float* frequency,
+                                     const int32_t* bias_ids, const float* bias, int64_t B,
+                                     const int32_t* allowed, float* out, int32_t* argmax,
+                                     qlin_stream_t stream) {
+  return run_adjust_logits(LogitArgs{logits, true, M, V, tokens, L, prompt_len, total_len, repetition,
+                                     presence, frequency, bias_ids, bias, B, allowed, out, argmax},
+                           reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t qlin_workspace_bytes(int64_t M, int64_t N, int64_t K) {

@@ -32,6 +32,50 @@ cudaError_t launch_silu_mul_quant(const uint16_t* gate_up, int64_t M, int64_t I,
                                   bool c16, float* s, uint16_t* y, int* err, int sm_count,
                                   cudaStream_t stream);
 
+// Residual addition + RMSNorm + act-quant; h (the sum) may be x or r.
+cudaError_t launch_add_rmsnorm_quant(const uint16_t* x, const uint16_t* r, const uint16_t* gamma,
+                                     float eps, int64_t M, int64_t K, uint16_t* h, void* q,
+                                     bool c16, float* s, uint16_t* y, int sm_count,
+                                     cudaStream_t stream);
+
+// The W8A8 linear with one scale per token and one per output channel.
+struct ChannelGemmArgs {
+  const void* act;        // int8 or (act_c16) fp16 codes [M, K]
+  bool act_c16;
+  const float* s_a;       // [M]
+  const int32_t* qweight; // [K/4, N]
+  const float* s_w;       // [N]
+  uint16_t* y;            // bf16 [M, N]
+  int64_t M, N, K;
+  void* workspace;        // channel_workspace_bytes(M, N, K) bytes, int8 codes only
+};
+// Sums of 130944 products of two int8 values stay below 2^31.
+constexpr int64_t kChannelMaxK = 130944;
+size_t channel_workspace_bytes(int64_t M, int64_t N, int64_t K);
+cudaError_t launch_gemm_channel(const ChannelGemmArgs& a, int* err, int sm_count,
+                                cudaStream_t stream);
+
+// Penalties, biases and the grammar mask on logits (f32 or bf16).
+struct LogitArgs {
+  const void* logits;
+  bool f32;
+  int64_t M, V;
+  const int32_t* tokens;      // [M, L] or nullptr
+  int64_t L;
+  const int32_t* prompt_len;  // [M] or nullptr
+  const int32_t* total_len;   // [M] or nullptr
+  const float* repetition;    // [M] or nullptr
+  const float* presence;
+  const float* frequency;
+  const int32_t* bias_ids;    // [M, B] or nullptr
+  const float* bias;
+  int64_t B;
+  const int32_t* allowed;     // [M, ceil(V / 32)] or nullptr
+  void* out;                  // the logits' type, or nullptr
+  int32_t* argmax;            // [M] or nullptr
+};
+cudaError_t launch_adjust_logits(const LogitArgs& a, int sm_count, cudaStream_t stream);
+
 cudaError_t launch_pack(const int8_t* q, int64_t K, int64_t N, int bits, int32_t* qweight,
                         int32_t* qzeros, int* err, cudaStream_t stream);
 
@@ -119,6 +163,27 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
+// launch_pdl in clusters of `cluster` blocks along x (grid.x a multiple of it).
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                               int cluster, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 

@@ -37,9 +37,14 @@ EXPORTS = (
     "qlin_act_quant_c16",
     "qlin_rmsnorm_act_quant_c16",
     "qlin_silu_mul_act_quant_c16",
+    "qlin_add_rmsnorm_act_quant_i8",
+    "qlin_add_rmsnorm_act_quant_c16",
     "qlin_gemm_w8a8_gs128",
     "qlin_gemm_w8a8_gs128_c16",
     "qlin_gemm_w8a8_gs128_noalloc",
+    "qlin_gemm_w8a8_ch",
+    "qlin_gemm_w8a8_ch_c16",
+    "qlin_gemm_w8a8_ch_workspace_bytes",
     "qlin_gemm_w4a16_g128",
     "qlin_gemm_w8a8_gs128_tiled",
     "qlin_gemm_w4a16_g128_tiled",
@@ -48,6 +53,8 @@ EXPORTS = (
     "qlin_gemm_w8a16",
     "qlin_gemm_w8a8_gs128_argmax",
     "qlin_gemm_w4a16_g128_argmax",
+    "qlin_adjust_logits_bf16",
+    "qlin_adjust_logits_f32",
     "qlin_pack_gptq",
     "qlin_ingest_nk",
     "qlin_workspace_bytes",
@@ -93,6 +100,13 @@ def load():
             "qlin_act_quant_c16": ([P, I64, I64, P, P, P], I),
             "qlin_rmsnorm_act_quant_c16": ([P, P, ctypes.c_float, I64, I64, P, P, P, P], I),
             "qlin_silu_mul_act_quant_c16": ([P, I64, I64, P, P, P, P], I),
+            "qlin_add_rmsnorm_act_quant_i8": ([P, P, P, ctypes.c_float, I64, I64, P, P, P, P, P], I),
+            "qlin_add_rmsnorm_act_quant_c16": ([P, P, P, ctypes.c_float, I64, I64, P, P, P, P, P], I),
+            "qlin_gemm_w8a8_ch": ([P, P, P, P, I64, I64, I64, P, P, SZ, P], I),
+            "qlin_gemm_w8a8_ch_c16": ([P, P, P, P, I64, I64, I64, P, P], I),
+            "qlin_gemm_w8a8_ch_workspace_bytes": ([I64, I64, I64], SZ),
+            "qlin_adjust_logits_bf16": ([P, I64, I64, P, I64, P, P, P, P, P, P, P, I64, P, P, P, P], I),
+            "qlin_adjust_logits_f32": ([P, I64, I64, P, I64, P, P, P, P, P, P, P, I64, P, P, P, P], I),
             "qlin_gemm_w8a8_gs128": ([P, P, P, P, I64, I64, I64, P, P, SZ, P], I),
             "qlin_gemm_w8a8_gs128_c16": ([P, P, P, P, I64, I64, I64, P, P, SZ, P], I),
             "qlin_gemm_w8a8_gs128_noalloc": ([P, P, P, P, I64, I64, I64, P, P], I),
@@ -249,6 +263,229 @@ def silu_mul_act_quant_c16(gate_up: torch.Tensor, q=None, s_a=None, y=None, stre
     """silu_mul_act_quant_i8 with the codes as fp16 (q fp16 [M,I])."""
     return _silu_mul_act_quant(load().qlin_silu_mul_act_quant_c16, torch.float16, gate_up, q, s_a,
                                y, stream)
+
+
+# The calls below check their arguments in one pass over (tensor, name, dtype,
+# shape) and launch on the tensors' device, whichever device is current.
+
+def _tensors(device, *specs):
+    """Each spec (tensor, name, dtype, shape): a contiguous tensor of that
+    dtype and shape on `device`."""
+    for t, name, dtype, shape in specs:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+        if t.device != device:
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _lead(t, name, dtypes, ndim):
+    """The argument that the others' shapes follow from; returns its device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dimensions, got {t.dim()}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _run(fn, device, stream, *args):
+    """fn(*args, stream) with `device` current, on `stream` (default: the
+    device's current stream)."""
+    current = torch.cuda.current_device()
+    if device.index == current:
+        _check(fn(*args, _raw_stream(current, stream)))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _raw_stream(device.index, stream)))
+
+
+def _raw_stream(index, stream):
+    if stream is None:
+        return torch.cuda.current_stream(index).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _opt(t):
+    return None if t is None else t.data_ptr()
+
+
+def _add_rmsnorm_act_quant(fn, code_dtype, x, residual, gamma, eps, residual_out, q, s_a, y, stream):
+    device = _lead(x, "x", (torch.bfloat16,), 2)
+    shape = x.shape
+    M, K = shape
+    if residual_out is None:
+        residual_out = torch.empty_like(residual)
+    if q is None:
+        q = torch.empty(shape, dtype=code_dtype, device=device)
+    if s_a is None:
+        s_a = torch.empty((M,), dtype=torch.float32, device=device)
+    bf16 = torch.bfloat16
+    _tensors(device, (x, "x", bf16, shape), (residual, "residual", bf16, shape),
+             (gamma, "gamma", bf16, (K,)), (residual_out, "residual_out", bf16, shape),
+             (q, "q", code_dtype, shape), (s_a, "s_a", torch.float32, (M,)))
+    if y is not None:
+        _tensors(device, (y, "y", bf16, shape))
+    _run(fn, device, stream, x.data_ptr(), residual.data_ptr(), gamma.data_ptr(), eps, M, K,
+         residual_out.data_ptr(), q.data_ptr(), s_a.data_ptr(), _opt(y))
+    return q, s_a, residual_out
+
+
+def add_rmsnorm_act_quant_i8(x: torch.Tensor, residual: torch.Tensor, gamma: torch.Tensor,
+                             eps: float, residual_out=None, q=None, s_a=None, y=None, stream=None):
+    """h = x + residual (bf16 [M,K]), RMSNorm of h with weight gamma bf16 [K],
+    then per-token INT8 act-quant -> (q int8 [M,K], s_a fp32 [M], h).  h is
+    written to residual_out, which may be x or residual (in place).  If y (bf16
+    [M,K]) is given the norm's bf16 output is written there too."""
+    return _add_rmsnorm_act_quant(load().qlin_add_rmsnorm_act_quant_i8, torch.int8, x, residual,
+                                  gamma, eps, residual_out, q, s_a, y, stream)
+
+
+def add_rmsnorm_act_quant_c16(x: torch.Tensor, residual: torch.Tensor, gamma: torch.Tensor,
+                              eps: float, residual_out=None, q=None, s_a=None, y=None, stream=None):
+    """add_rmsnorm_act_quant_i8 with the codes as fp16 (q fp16 [M,K])."""
+    return _add_rmsnorm_act_quant(load().qlin_add_rmsnorm_act_quant_c16, torch.float16, x, residual,
+                                  gamma, eps, residual_out, q, s_a, y, stream)
+
+
+def gemm_w8a8_ch_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(load().qlin_gemm_w8a8_ch_workspace_bytes(int(M), int(N), int(K)))
+
+
+def _ch_inputs(code_dtype, q_a, s_a, qweight, s_w, y):
+    device = _lead(q_a, "q_a", (code_dtype,), 2)
+    _lead(qweight, "qweight", (torch.int32,), 2)
+    M, K = q_a.shape
+    N = qweight.shape[1]
+    if y is None:
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=device)
+    if K % 4:
+        raise ValueError("K must be a multiple of 128")
+    _tensors(device, (q_a, "q_a", code_dtype, (M, K)), (s_a, "s_a", torch.float32, (M,)),
+             (qweight, "qweight", torch.int32, (K // 4, N)), (s_w, "s_w", torch.float32, (N,)),
+             (y, "y", torch.bfloat16, (M, N)))
+    return device, M, N, K, y
+
+
+def gemm_w8a8_ch(q_a: torch.Tensor, s_a: torch.Tensor, qweight: torch.Tensor, s_w: torch.Tensor,
+                 y: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """q_a int8 [M,K], s_a fp32 [M], qweight int32 [K/4,N] (8-bit GPTQ words),
+    s_w fp32 [N] (one scale per output channel) -> y bf16 [M,N].  workspace: a
+    uint8 tensor of gemm_w8a8_ch_workspace_bytes(M, N, K) bytes; allocated for
+    the call when not given and needed."""
+    device, M, N, K, y = _ch_inputs(torch.int8, q_a, s_a, qweight, s_w, y)
+    fn = load().qlin_gemm_w8a8_ch
+    nbytes = 0
+    if workspace is not None:
+        nbytes = workspace.numel() * workspace.element_size()
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous and on {device}")
+    else:
+        nbytes = gemm_w8a8_ch_workspace_bytes(M, N, K)
+        if nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+            if stream is not None:
+                # freed with this call, while `stream` may still use it
+                workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
+                                        else torch.cuda.ExternalStream(int(stream), device=device))
+    _run(fn, device, stream, q_a.data_ptr(), s_a.data_ptr(), qweight.data_ptr(), s_w.data_ptr(),
+         M, N, K, y.data_ptr(), _opt(workspace), nbytes)
+    return y
+
+
+def gemm_w8a8_ch_c16(q_a: torch.Tensor, s_a: torch.Tensor, qweight: torch.Tensor,
+                     s_w: torch.Tensor, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """gemm_w8a8_ch with the activation codes as fp16 (q_a fp16 [M,K], the
+    output of the *_c16 producers); needs no workspace."""
+    device, M, N, K, y = _ch_inputs(torch.float16, q_a, s_a, qweight, s_w, y)
+    _run(load().qlin_gemm_w8a8_ch_c16, device, stream, q_a.data_ptr(), s_a.data_ptr(),
+         qweight.data_ptr(), s_w.data_ptr(), M, N, K, y.data_ptr())
+    return y
+
+
+def _adjust(logits, tokens, prompt_len, total_len, repetition, presence, frequency, bias_ids, bias,
+            allowed, out, argmax, stream):
+    device = _lead(logits, "logits", (torch.bfloat16, torch.float32), 2)
+    M, V = logits.shape
+    i32, f32 = torch.int32, torch.float32
+    specs = [(logits, "logits", logits.dtype, (M, V))]
+    L = B = 0
+    if tokens is not None:
+        _lead(tokens, "tokens", (i32,), 2)
+        L = tokens.shape[1]
+        specs.append((tokens, "tokens", i32, (M, L)))
+    elif prompt_len is not None or total_len is not None:
+        raise ValueError("prompt_len and total_len need tokens")
+    if (bias_ids is None) != (bias is None):
+        raise ValueError("bias_ids and bias go together")
+    if bias_ids is not None:
+        _lead(bias_ids, "bias_ids", (i32,), 2)
+        B = bias_ids.shape[1]
+        specs += [(bias_ids, "bias_ids", i32, (M, B)), (bias, "bias", f32, (M, B))]
+    row = (M,)
+    if prompt_len is not None:
+        specs.append((prompt_len, "prompt_len", i32, row))
+    if total_len is not None:
+        specs.append((total_len, "total_len", i32, row))
+    if repetition is not None:
+        specs.append((repetition, "repetition", f32, row))
+    if presence is not None:
+        specs.append((presence, "presence", f32, row))
+    if frequency is not None:
+        specs.append((frequency, "frequency", f32, row))
+    if allowed is not None:
+        specs.append((allowed, "allowed", i32, (M, (V + 31) // 32)))
+    if out is not None:
+        specs.append((out, "out", logits.dtype, (M, V)))
+    if argmax is not None:
+        specs.append((argmax, "argmax", i32, row))
+    _tensors(device, *specs)
+    lib = load()
+    fn = lib.qlin_adjust_logits_bf16 if logits.dtype == torch.bfloat16 else lib.qlin_adjust_logits_f32
+    _run(fn, device, stream, logits.data_ptr(), M, V, _opt(tokens), L, _opt(prompt_len),
+         _opt(total_len), _opt(repetition), _opt(presence), _opt(frequency), _opt(bias_ids),
+         _opt(bias), B, _opt(allowed), _opt(out), _opt(argmax))
+
+
+def adjust_logits(logits: torch.Tensor, tokens=None, prompt_len=None, total_len=None,
+                  repetition=None, presence=None, frequency=None, bias_ids=None, bias=None,
+                  allowed=None, out=None, stream=None) -> torch.Tensor:
+    """Penalties for repeated tokens, biases and a grammar mask on logits bf16
+    or fp32 [M,V] -> the adjusted logits (out, which may be logits: in place).
+
+    tokens int32 [M,L] holds each row's prompt_len[m] prompt tokens and then
+    generated ones up to total_len[m] (int32 [M]; default no prompt, L tokens);
+    repetition, presence and frequency are fp32 [M]; bias_ids int32 [M,B] with
+    bias fp32 [M,B] (ids outside the vocabulary are skipped, the last entry of
+    an id applies); allowed int32 [M, ceil(V/32)], bit 1 = allowed, least
+    significant first.  Order and rounding: include/qlin.h."""
+    if out is None:
+        out = torch.empty_like(logits)
+    _adjust(logits, tokens, prompt_len, total_len, repetition, presence, frequency, bias_ids, bias,
+            allowed, out, None, stream)
+    return out
+
+
+def adjust_logits_argmax(logits: torch.Tensor, tokens=None, prompt_len=None, total_len=None,
+                         repetition=None, presence=None, frequency=None, bias_ids=None, bias=None,
+                         allowed=None, out=None, argmax=None, stream=None) -> torch.Tensor:
+    """The greedy token of each row after adjust_logits: int32 [M], the lowest
+    index on ties, -1 for a row without a value above -inf.  The adjusted
+    logits are written only if out is given."""
+    if argmax is None:
+        argmax = torch.empty(logits.shape[:1], dtype=torch.int32, device=logits.device)
+    _adjust(logits, tokens, prompt_len, total_len, repetition, presence, frequency, bias_ids, bias,
+            allowed, out, argmax, stream)
+    return argmax
 
 
 def workspace_bytes(M: int, N: int, K: int) -> int:
