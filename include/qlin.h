@@ -282,21 +282,24 @@ qlin_status_t qlin_gemm_w8a8_gs128_noalloc(const int8_t *q_a, const float *s_a,
  *   qweight  int32 [K/4, N]  8-bit GPTQ words as for qlin_gemm_w8a8_gs128
  *   s_w      fp32 [N]        one scale per output channel
  *   y        bf16 [M, N]     output
- *   workspace / workspace_bytes (int8 entry only)  at least
- *            qlin_gemm_w8a8_ch_workspace_bytes(M, N, K) bytes; may be NULL
- *            where that is 0.  It needs no zeroing and holds nothing between
- *            calls.  Calls that share a workspace must not overlap.
+ *   workspace / workspace_bytes  at least
+ *            qlin_gemm_w8a8_ch_workspace_bytes(M, N, K, c16) bytes on the
+ *            current device, c16 being 1 for the _c16 entry and 0 for the
+ *            int8 one; may be NULL where that is 0 (up to 16 rows).  It needs
+ *            no zeroing and holds nothing between calls.  Calls that share a
+ *            workspace must not overlap.
  *
  * K is at most 130,944 (QLIN_ERR_SHAPE above): sums of that many products of
  * two int8 values fit int32.
  */
-size_t qlin_gemm_w8a8_ch_workspace_bytes(int64_t M, int64_t N, int64_t K);
+size_t qlin_gemm_w8a8_ch_workspace_bytes(int64_t M, int64_t N, int64_t K, int c16);
 qlin_status_t qlin_gemm_w8a8_ch(const int8_t *q_a, const float *s_a, const int32_t *qweight,
                                 const float *s_w, int64_t M, int64_t N, int64_t K, uint16_t *y,
                                 void *workspace, size_t workspace_bytes, qlin_stream_t stream);
 qlin_status_t qlin_gemm_w8a8_ch_c16(const uint16_t *q_a, const float *s_a,
                                     const int32_t *qweight, const float *s_w, int64_t M,
-                                    int64_t N, int64_t K, uint16_t *y, qlin_stream_t stream);
+                                    int64_t N, int64_t K, uint16_t *y, void *workspace,
+                                    size_t workspace_bytes, qlin_stream_t stream);
 
 /*
  * W4A16 g128 symmetric weight-only linear:

@@ -585,8 +585,8 @@ def test_channel_refusals(lib):
     def i8(q=OK, s=OK, w=OK, sw=OK, M=4, N=64, K=256, y=OK, ws=None, n=0):
         return _status(lib, "qlin_gemm_w8a8_ch", _p(q), _p(s), _p(w), _p(sw), M, N, K, _p(y), _p(ws), n, None)
 
-    def c16(q=OK, s=OK, w=OK, sw=OK, M=4, N=64, K=256, y=OK):
-        return _status(lib, "qlin_gemm_w8a8_ch_c16", _p(q), _p(s), _p(w), _p(sw), M, N, K, _p(y), None)
+    def c16(q=OK, s=OK, w=OK, sw=OK, M=4, N=64, K=256, y=OK, ws=None, n=0):
+        return _status(lib, "qlin_gemm_w8a8_ch_c16", _p(q), _p(s), _p(w), _p(sw), M, N, K, _p(y), _p(ws), n, None)
     for call in (i8, c16):
         for kw in ({"q": None}, {"s": None}, {"w": None}, {"sw": None}, {"y": None}):
             assert call(**kw) == qlin.QLIN_ERR_NULL
@@ -594,9 +594,10 @@ def test_channel_refusals(lib):
             assert call(**kw) == qlin.QLIN_ERR_SHAPE
         for kw in ({"q": ODD}, {"s": ODD}, {"w": ODD}, {"sw": ODD}, {"y": ODD}):
             assert call(**kw) == qlin.QLIN_ERR_ALIGN
-    assert i8(ws=ODD, n=1 << 30) == qlin.QLIN_ERR_ALIGN
+        assert call(ws=ODD, n=1 << 30) == qlin.QLIN_ERR_ALIGN
     for M, N, K in ((-1, 64, 256), (4, 12, 256), (4, 64, 100), (4, 64, 131072), (0, 64, 256)):
         assert qlin.gemm_w8a8_ch_workspace_bytes(M, N, K) == 0
+        assert qlin.gemm_w8a8_ch_workspace_bytes(M, N, K, True) == 0
 
 
 @pytest.mark.parametrize("name", ["qlin_adjust_logits_bf16", "qlin_adjust_logits_f32"])

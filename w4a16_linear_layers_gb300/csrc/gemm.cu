@@ -60,8 +60,6 @@
 #include <cuda_fp16.h>
 #include <cuda_bf16.h>
 
-#include <cudaTypedefs.h>
-
 #include <cstring>
 #include <mutex>
 
@@ -1224,56 +1222,6 @@ __global__ void __launch_bounds__(128) argmax_finalize_kernel(const unsigned lon
 }
 
 // ------------------------------------------------------------------- host
-
-using EncodeFn = PFN_cuTensorMapEncodeTiled_v12000;
-
-EncodeFn encode_fn() {
-  static EncodeFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeFn>(ptr);
-  });
-  return fn;
-}
-
-// 16-bit activations [M][K] seen as a 3D tensor {64 (k inside a half group),
-// M (rows, stride K*2 bytes), K/64 (half groups, stride 128 bytes)}; a box
-// {64, T, 2g} is g 128-wide K groups as 2g swizzled T x 128 B tiles.
-bool make_act_map(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t M,
-                  uint64_t K, uint32_t T, uint32_t halves) {
-  EncodeFn fn = encode_fn();
-  if (!fn) return false;
-  const cuuint64_t dims[3] = {64, M, K / 64};
-  const cuuint64_t strides[2] = {K * 2, 128};
-  const cuuint32_t box[3] = {64, T, halves};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return fn(map, dtype, 3, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-bool make_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t inner,
-                 uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
-                 CUtensorMapSwizzle swz) {
-  EncodeFn fn = encode_fn();
-  if (!fn) return false;
-  const cuuint64_t dims[2] = {inner, outer};
-  const cuuint64_t strides[1] = {row_bytes};
-  const cuuint32_t box[2] = {box_inner, box_outer};
-  const cuuint32_t estr[2] = {1, 1};
-  return fn(map, dtype, 2, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-}  // namespace
-
-namespace {
 
 template <int kMode, int T, int GPS>
 cudaError_t launch_t(const GemmArgs& a, const GemmPlan& pl_in, int* err, cudaStream_t stream) {

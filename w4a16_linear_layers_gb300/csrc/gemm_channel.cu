@@ -30,6 +30,9 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
+
+#include "gemm_channel_pair.cuh"
 #include "qlin_device.cuh"
 #include "qlin_internal.h"
 
@@ -264,9 +267,164 @@ cudaError_t launch_c(const ChannelParams& p, int sm_count, cudaStream_t stream) 
 
 }  // namespace
 
-size_t channel_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
+namespace {
 
-cudaError_t launch_gemm_channel(const ChannelGemmArgs& a, int*, int sm_count, cudaStream_t stream) {
+// ------------------------------------------------------- larger batches
+
+constexpr int64_t kStreamTokens = 16;     // batches up to this take the streaming kernel
+constexpr size_t kCounterBytes = 1024;    // arrival counters of the cut tiles
+constexpr int64_t kMinShare = 8;          // K steps of a pair's share of the cut tiles, at least
+
+struct PairPlan {
+  int T = 0;
+  int64_t TT = 0, F2 = 0, G = 0, pairs = 0, band = 0, sk_tiles = 0, sk_pairs = 0;
+  bool cut = false;         // some tile is shared between pairs
+  size_t part_bytes = 0;    // int32 partials of the shared tiles
+};
+
+PairPlan plan_pair(int64_t M, int64_t N, int64_t K, int sm_count) {
+  PairPlan pl;
+  const int sizes[5] = {64, 96, 128, 192, 256};
+  int64_t best = 0;
+  for (int T : sizes) {
+    // cycles of a K step, up to a factor: the MMA's 4 T, and what does not depend on T
+    const int64_t cost = (M + T - 1) / T * (4 * T + 128);
+    if (best == 0 || cost < best) {
+      best = cost;
+      pl.T = T;
+    }
+  }
+  pl.TT = (M + pl.T - 1) / pl.T;
+  pl.F2 = (N + 255) / 256;
+  pl.G = K / 128;
+  const int64_t slots = sm_count / 2;
+  const int64_t tiles = pl.TT * pl.F2;
+  const int64_t rest = tiles % slots;
+  pl.pairs = tiles < slots ? tiles : slots;
+  pl.band = pl.TT < 8 ? pl.TT : 8;
+  // the last round's tiles are cut along K unless they nearly fill it
+  if (rest != 0 && rest * 8 < slots * 7) {
+    int64_t n = rest * pl.G / kMinShare;
+    n = n < rest ? rest : n > slots ? slots : n;
+    if (n > rest) {
+      pl.sk_tiles = rest;
+      pl.sk_pairs = n;
+      pl.cut = true;
+      pl.part_bytes = static_cast<size_t>(n) * 4 * pl.T * 128 * sizeof(int32_t);
+      if (pl.pairs < n) pl.pairs = n;
+    }
+  }
+  return pl;
+}
+
+size_t image_bytes(int64_t M, int64_t K) { return static_cast<size_t>(M) * static_cast<size_t>(K) * 2; }
+
+// Before the pair kernel: the counters to zero and, for int8 codes, their
+// exact fp16 image (16 codes a thread).
+__global__ void __launch_bounds__(256) pair_prepare_kernel(int* counters, const int8_t* __restrict__ q,
+                                                           uint16_t* __restrict__ image, int64_t n16) {
+  grid_dep_wait();    // the workspace may still be in use, and the codes come from the previous kernel
+  grid_dep_launch();
+  if (blockIdx.x == 0 && counters != nullptr) counters[threadIdx.x] = 0;
+  for (int64_t i = blockIdx.x * static_cast<int64_t>(256) + threadIdx.x; i < n16;
+       i += static_cast<int64_t>(gridDim.x) * 256) {
+    const uint4 raw = __ldg(reinterpret_cast<const uint4*>(q) + i);
+    uint4 lo, hi;
+    biased_u8x4_to_f16x4(raw.x ^ 0x80808080u, lo.x, lo.y);
+    biased_u8x4_to_f16x4(raw.y ^ 0x80808080u, lo.z, lo.w);
+    biased_u8x4_to_f16x4(raw.z ^ 0x80808080u, hi.x, hi.y);
+    biased_u8x4_to_f16x4(raw.w ^ 0x80808080u, hi.z, hi.w);
+    reinterpret_cast<uint4*>(image)[2 * i] = lo;
+    reinterpret_cast<uint4*>(image)[2 * i + 1] = hi;
+  }
+}
+static_assert(kCounterBytes == 256 * sizeof(int), "one counter a thread");
+
+template <int T>
+cudaError_t launch_pair_t(const CUtensorMap& tw, const CUtensorMap& tx, const pair::Params& p, cudaStream_t stream) {
+  // The kernel's warps trade registers (setmaxnreg) within what the block was
+  // launched with: 128 x 32 + 256 x 64 + 256 x 160.  A build that gave the
+  // block less would wait for them forever, so it is refused here.
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(ready.load(std::memory_order_acquire) & bit)) {
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, pair::pair_kernel<T>);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs * pair::kThreads < 128 * 32 + 256 * 64 + 256 * 160) return cudaErrorLaunchOutOfResources;
+    e = cudaFuncSetAttribute(pair::pair_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(pair::Cfg<T>::kSmem));
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_release);
+  }
+  return launch_pdl(pair::pair_kernel<T>, dim3(static_cast<unsigned>(2 * p.pairs)), dim3(pair::kThreads),
+                    pair::Cfg<T>::kSmem, stream, tw, tx, p);
+}
+
+cudaError_t launch_pair(const ChannelGemmArgs& a, int* err, int sm_count, cudaStream_t stream) {
+  const PairPlan pl = plan_pair(a.M, a.N, a.K, sm_count);
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  const void* codes = a.act;
+  int* counters = nullptr;
+  size_t at = 0;
+  if (pl.cut) {
+    counters = reinterpret_cast<int*>(ws);
+    at = kCounterBytes + pl.part_bytes;
+  }
+  if (pl.cut || !a.act_c16) {
+    const int64_t n16 = a.act_c16 ? 0 : a.M * a.K / 16;
+    uint16_t* image = a.act_c16 ? nullptr : reinterpret_cast<uint16_t*>(ws + at);
+    int64_t blocks = (n16 + 255) / 256;
+    blocks = blocks < 1 ? 1 : blocks > 4096 ? 4096 : blocks;
+    const cudaError_t e = launch_pdl(pair_prepare_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream,
+                                     counters, static_cast<const int8_t*>(a.act), image, n16);
+    if (e != cudaSuccess) return e;
+    if (!a.act_c16) codes = image;
+  }
+  CUtensorMap tw, tx;
+  if (!make_map_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_INT32, a.qweight, a.N, a.K / 4, static_cast<uint64_t>(a.N) * 4, 128,
+                   32, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !make_act_map(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, codes, a.M, a.K, static_cast<uint32_t>(pl.T / 2), 2))
+    return cudaErrorInvalidValue;
+  pair::Params p;
+  p.s_a = a.s_a;
+  p.s_w = a.s_w;
+  p.y = a.y;
+  p.M = a.M;
+  p.N = a.N;
+  p.G = pl.G;
+  p.F2 = pl.F2;
+  p.TT = pl.TT;
+  p.band = pl.band;
+  p.pairs = pl.pairs;
+  p.sk_tiles = pl.sk_tiles;
+  p.sk_pairs = pl.sk_pairs > 0 ? pl.sk_pairs : 1;
+  p.counters = counters;
+  p.part = pl.cut ? reinterpret_cast<int32_t*>(ws + kCounterBytes) : nullptr;
+  p.err = err;
+  p.limit_ns = kWaitLimitNs;
+  switch (pl.T) {
+    case 64: return launch_pair_t<64>(tw, tx, p, stream);
+    case 96: return launch_pair_t<96>(tw, tx, p, stream);
+    case 128: return launch_pair_t<128>(tw, tx, p, stream);
+    case 192: return launch_pair_t<192>(tw, tx, p, stream);
+    default: return launch_pair_t<256>(tw, tx, p, stream);
+  }
+}
+
+}  // namespace
+
+size_t channel_workspace_bytes(int64_t M, int64_t N, int64_t K, bool c16, int sm_count) {
+  if (M <= kStreamTokens) return 0;
+  const PairPlan pl = plan_pair(M, N, K, sm_count);
+  return (pl.cut ? kCounterBytes + pl.part_bytes : 0) + (c16 ? 0 : image_bytes(M, K));
+}
+
+cudaError_t launch_gemm_channel(const ChannelGemmArgs& a, int* err, int sm_count, cudaStream_t stream) {
+  if (a.M > kStreamTokens) return launch_pair(a, err, sm_count, stream);
   const ChannelParams p{a.act, a.s_a, reinterpret_cast<const uint32_t*>(a.qweight), a.s_w, a.y, a.M, a.N, a.K};
   return a.act_c16 ? launch_c<true>(p, sm_count, stream) : launch_c<false>(p, sm_count, stream);
 }

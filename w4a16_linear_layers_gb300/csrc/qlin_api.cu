@@ -210,7 +210,7 @@ qlin_status_t run_gemm_channel(const void* q_a, bool c16, const float* s_a, cons
   st = device_or_error(&d);
   if (st != QLIN_OK) return st;
   if (M == 0) return QLIN_OK;
-  const size_t need = c16 ? 0 : channel_workspace_bytes(M, N, K);
+  const size_t need = channel_workspace_bytes(M, N, K, c16, d->sm_count);
   if (need != 0 && (workspace == nullptr || workspace_bytes < need)) return QLIN_ERR_WORKSPACE;
   const ChannelGemmArgs a{q_a, c16, s_a, qweight, s_w, y, M, N, K, workspace};
   return from_cuda(launch_gemm_channel(a, d->err_word, d->sm_count, stream));
@@ -436,9 +436,11 @@ qlin_status_t qlin_add_rmsnorm_act_quant_c16(const uint16_t* x, const uint16_t* 
                                reinterpret_cast<cudaStream_t>(stream));
 }
 
-size_t qlin_gemm_w8a8_ch_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+size_t qlin_gemm_w8a8_ch_workspace_bytes(int64_t M, int64_t N, int64_t K, int c16) {
   if (check_gemm_shape(M, N, K) != QLIN_OK || K > kChannelMaxK || M == 0) return 0;
-  return channel_workspace_bytes(M, N, K);
+  const DeviceInfo* d = current_device();
+  if (d == nullptr || !d->supported) return 0;
+  return channel_workspace_bytes(M, N, K, c16 != 0, d->sm_count);
 }
 
 qlin_status_t qlin_gemm_w8a8_ch(const int8_t* q_a, const float* s_a, const int32_t* qweight,
@@ -450,8 +452,9 @@ qlin_status_t qlin_gemm_w8a8_ch(const int8_t* q_a, const float* s_a, const int32
 
 qlin_status_t qlin_gemm_w8a8_ch_c16(const uint16_t* q_a, const float* s_a, const int32_t* qweight,
                                     const float* s_w, int64_t M, int64_t N, int64_t K,
-                                    uint16_t* y, qlin_stream_t stream) {
-  return run_gemm_channel(q_a, true, s_a, qweight, s_w, M, N, K, y, nullptr, 0,
+                                    uint16_t* y, void* workspace, size_t workspace_bytes,
+                                    qlin_stream_t stream) {
+  return run_gemm_channel(q_a, true, s_a, qweight, s_w, M, N, K, y, workspace, workspace_bytes,
                           reinterpret_cast<cudaStream_t>(stream));
 }
 

@@ -4,6 +4,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 namespace qlin {
@@ -18,6 +19,15 @@ struct DeviceInfo {
 
 // Returns the cached info of the current device (nullptr if no device).
 const DeviceInfo* current_device();
+
+// TMA descriptors (tensor_map.cu); false if the driver refuses the map.
+// make_act_map: 16-bit codes or activations [M, K] as boxes of `halves`
+// 64-wide K halves x T rows; make_map_2d: a plain row-major matrix.
+bool make_act_map(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t M,
+                  uint64_t K, uint32_t T, uint32_t halves);
+bool make_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t inner,
+                 uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
+                 CUtensorMapSwizzle swz);
 
 // The act-quant producers write the codes q as int8, or (c16) as the same
 // integers in fp16 [M, K].
@@ -47,11 +57,11 @@ struct ChannelGemmArgs {
   const float* s_w;       // [N]
   uint16_t* y;            // bf16 [M, N]
   int64_t M, N, K;
-  void* workspace;        // channel_workspace_bytes(M, N, K) bytes, int8 codes only
+  void* workspace;        // channel_workspace_bytes(M, N, K, act_c16, sm_count) bytes
 };
 // Sums of 130944 products of two int8 values stay below 2^31.
 constexpr int64_t kChannelMaxK = 130944;
-size_t channel_workspace_bytes(int64_t M, int64_t N, int64_t K);
+size_t channel_workspace_bytes(int64_t M, int64_t N, int64_t K, bool c16, int sm_count);
 cudaError_t launch_gemm_channel(const ChannelGemmArgs& a, int* err, int sm_count,
                                 cudaStream_t stream);
 

@@ -103,8 +103,8 @@ def load():
             "qlin_add_rmsnorm_act_quant_i8": ([P, P, P, ctypes.c_float, I64, I64, P, P, P, P, P], I),
             "qlin_add_rmsnorm_act_quant_c16": ([P, P, P, ctypes.c_float, I64, I64, P, P, P, P, P], I),
             "qlin_gemm_w8a8_ch": ([P, P, P, P, I64, I64, I64, P, P, SZ, P], I),
-            "qlin_gemm_w8a8_ch_c16": ([P, P, P, P, I64, I64, I64, P, P], I),
-            "qlin_gemm_w8a8_ch_workspace_bytes": ([I64, I64, I64], SZ),
+            "qlin_gemm_w8a8_ch_c16": ([P, P, P, P, I64, I64, I64, P, P, SZ, P], I),
+            "qlin_gemm_w8a8_ch_workspace_bytes": ([I64, I64, I64, I], SZ),
             "qlin_adjust_logits_bf16": ([P, I64, I64, P, I64, P, P, P, P, P, P, P, I64, P, P, P, P], I),
             "qlin_adjust_logits_f32": ([P, I64, I64, P, I64, P, P, P, P, P, P, P, I64, P, P, P, P], I),
             "qlin_gemm_w8a8_gs128": ([P, P, P, P, I64, I64, I64, P, P, SZ, P], I),
@@ -265,27 +265,31 @@ def silu_mul_act_quant_c16(gate_up: torch.Tensor, q=None, s_a=None, y=None, stre
                                y, stream)
 
 
-# The calls below check their arguments in one pass over (tensor, name, dtype,
-# shape) and launch on the tensors' device, whichever device is current.
+# The calls below launch on their tensors' device, whichever device is current.
+# A small batch's kernel takes less time than Python needs to call it, so they
+# check each argument once, with the cheapest attribute reads, and skip the
+# tensors they allocated themselves.
 
-def _tensors(device, *specs):
-    """Each spec (tensor, name, dtype, shape): a contiguous tensor of that
-    dtype and shape on `device`."""
-    for t, name, dtype, shape in specs:
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-        if t.device != device:
-            raise ValueError(f"{name} must be on {device}, got {t.device}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+def _is(t, dtype, shape, index) -> bool:
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == index and t.is_contiguous())
 
 
-def _lead(t, name, dtypes, ndim):
-    """The argument that the others' shapes follow from; returns its device."""
+def _refuse(t, name, dtype, shape, index):
+    """Raises what is wrong with an argument that _is turned down."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _lead(t, name, dtypes, ndim) -> int:
+    """The argument that the others' shapes follow from; returns its device's index."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in dtypes:
@@ -294,24 +298,25 @@ def _lead(t, name, dtypes, ndim):
         raise ValueError(f"{name} must have {ndim} dimensions, got {t.dim()}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.get_device()
 
 
-def _run(fn, device, stream, *args):
-    """fn(*args, stream) with `device` current, on `stream` (default: the
+def _run(fn, index, stream, *args):
+    """fn(*args, stream) with device `index` current, on `stream` (default: the
     device's current stream)."""
-    current = torch.cuda.current_device()
-    if device.index == current:
-        _check(fn(*args, _raw_stream(current, stream)))
-    else:
-        with torch.cuda.device(device):
-            _check(fn(*args, _raw_stream(device.index, stream)))
-
-
-def _raw_stream(index, stream):
     if stream is None:
-        return torch.cuda.current_stream(index).cuda_stream
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        handle = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, handle)
+    if status != QLIN_OK:
+        _check(status)
 
 
 def _opt(t):
@@ -319,23 +324,30 @@ def _opt(t):
 
 
 def _add_rmsnorm_act_quant(fn, code_dtype, x, residual, gamma, eps, residual_out, q, s_a, y, stream):
-    device = _lead(x, "x", (torch.bfloat16,), 2)
+    bf16 = torch.bfloat16
+    dev = _lead(x, "x", (bf16,), 2)
     shape = x.shape
     M, K = shape
+    if not _is(residual, bf16, shape, dev):
+        _refuse(residual, "residual", bf16, shape, dev)
+    if not _is(gamma, bf16, (K,), dev):
+        _refuse(gamma, "gamma", bf16, (K,), dev)
     if residual_out is None:
         residual_out = torch.empty_like(residual)
+    elif not _is(residual_out, bf16, shape, dev):
+        _refuse(residual_out, "residual_out", bf16, shape, dev)
     if q is None:
-        q = torch.empty(shape, dtype=code_dtype, device=device)
+        q = torch.empty(shape, dtype=code_dtype, device=x.device)
+    elif not _is(q, code_dtype, shape, dev):
+        _refuse(q, "q", code_dtype, shape, dev)
     if s_a is None:
-        s_a = torch.empty((M,), dtype=torch.float32, device=device)
-    bf16 = torch.bfloat16
-    _tensors(device, (x, "x", bf16, shape), (residual, "residual", bf16, shape),
-             (gamma, "gamma", bf16, (K,)), (residual_out, "residual_out", bf16, shape),
-             (q, "q", code_dtype, shape), (s_a, "s_a", torch.float32, (M,)))
-    if y is not None:
-        _tensors(device, (y, "y", bf16, shape))
-    _run(fn, device, stream, x.data_ptr(), residual.data_ptr(), gamma.data_ptr(), eps, M, K,
-         residual_out.data_ptr(), q.data_ptr(), s_a.data_ptr(), _opt(y))
+        s_a = torch.empty((M,), dtype=torch.float32, device=x.device)
+    elif not _is(s_a, torch.float32, (M,), dev):
+        _refuse(s_a, "s_a", torch.float32, (M,), dev)
+    if y is not None and not _is(y, bf16, shape, dev):
+        _refuse(y, "y", bf16, shape, dev)
+    _run(fn, dev, stream, x.data_ptr(), residual.data_ptr(), gamma.data_ptr(), eps, M, K,
+         residual_out.data_ptr(), q.data_ptr(), s_a.data_ptr(), None if y is None else y.data_ptr())
     return q, s_a, residual_out
 
 
@@ -356,23 +368,55 @@ def add_rmsnorm_act_quant_c16(x: torch.Tensor, residual: torch.Tensor, gamma: to
                                   gamma, eps, residual_out, q, s_a, y, stream)
 
 
-def gemm_w8a8_ch_workspace_bytes(M: int, N: int, K: int) -> int:
-    return int(load().qlin_gemm_w8a8_ch_workspace_bytes(int(M), int(N), int(K)))
+def gemm_w8a8_ch_workspace_bytes(M: int, N: int, K: int, c16: bool = False) -> int:
+    return int(load().qlin_gemm_w8a8_ch_workspace_bytes(int(M), int(N), int(K), int(c16)))
 
 
 def _ch_inputs(code_dtype, q_a, s_a, qweight, s_w, y):
-    device = _lead(q_a, "q_a", (code_dtype,), 2)
+    dev = _lead(q_a, "q_a", (code_dtype,), 2)
     _lead(qweight, "qweight", (torch.int32,), 2)
     M, K = q_a.shape
     N = qweight.shape[1]
+    if not _is(qweight, torch.int32, (K // 4, N), dev) or K % 4:
+        if K % 4:
+            raise ValueError("K must be a multiple of 128")
+        _refuse(qweight, "qweight", torch.int32, (K // 4, N), dev)
+    if not _is(s_a, torch.float32, (M,), dev):
+        _refuse(s_a, "s_a", torch.float32, (M,), dev)
+    if not _is(s_w, torch.float32, (N,), dev):
+        _refuse(s_w, "s_w", torch.float32, (N,), dev)
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=device)
-    if K % 4:
-        raise ValueError("K must be a multiple of 128")
-    _tensors(device, (q_a, "q_a", code_dtype, (M, K)), (s_a, "s_a", torch.float32, (M,)),
-             (qweight, "qweight", torch.int32, (K // 4, N)), (s_w, "s_w", torch.float32, (N,)),
-             (y, "y", torch.bfloat16, (M, N)))
-    return device, M, N, K, y
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=q_a.device)
+    elif not _is(y, torch.bfloat16, (M, N), dev):
+        _refuse(y, "y", torch.bfloat16, (M, N), dev)
+    return dev, M, N, K, y
+
+
+def _gemm_ch(fn, c16, q_a, s_a, qweight, s_w, y, workspace, stream):
+    dev, M, N, K, y = _ch_inputs(torch.float16 if c16 else torch.int8, q_a, s_a, qweight, s_w, y)
+    nbytes = 0
+    if workspace is not None:
+        if not workspace.is_cuda or workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous and on cuda:{dev}")
+        nbytes = workspace.numel() * workspace.element_size()
+    else:
+        if torch._C._cuda_getDevice() == dev:
+            nbytes = load().qlin_gemm_w8a8_ch_workspace_bytes(M, N, K, c16)
+        else:
+            with torch.cuda.device(dev):
+                nbytes = load().qlin_gemm_w8a8_ch_workspace_bytes(M, N, K, c16)
+        if nbytes:
+            # its own for every call: calls on several streams, or replayed
+            # graphs, do not meet in it
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q_a.device)
+            if stream is not None:
+                # freed with this call, while `stream` may still use it
+                workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
+                                        torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream),
+                                                                  device=q_a.device))
+    _run(fn, dev, stream, q_a.data_ptr(), s_a.data_ptr(), qweight.data_ptr(), s_w.data_ptr(), M, N, K,
+         y.data_ptr(), _opt(workspace), nbytes)
+    return y
 
 
 def gemm_w8a8_ch(q_a: torch.Tensor, s_a: torch.Tensor, qweight: torch.Tensor, s_w: torch.Tensor,
@@ -382,76 +426,61 @@ def gemm_w8a8_ch(q_a: torch.Tensor, s_a: torch.Tensor, qweight: torch.Tensor, s_
     s_w fp32 [N] (one scale per output channel) -> y bf16 [M,N].  workspace: a
     uint8 tensor of gemm_w8a8_ch_workspace_bytes(M, N, K) bytes; allocated for
     the call when not given and needed."""
-    device, M, N, K, y = _ch_inputs(torch.int8, q_a, s_a, qweight, s_w, y)
-    fn = load().qlin_gemm_w8a8_ch
-    nbytes = 0
-    if workspace is not None:
-        nbytes = workspace.numel() * workspace.element_size()
-        if workspace.device != device or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be contiguous and on {device}")
-    else:
-        nbytes = gemm_w8a8_ch_workspace_bytes(M, N, K)
-        if nbytes:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-            if stream is not None:
-                # freed with this call, while `stream` may still use it
-                workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                                        else torch.cuda.ExternalStream(int(stream), device=device))
-    _run(fn, device, stream, q_a.data_ptr(), s_a.data_ptr(), qweight.data_ptr(), s_w.data_ptr(),
-         M, N, K, y.data_ptr(), _opt(workspace), nbytes)
-    return y
+    return _gemm_ch(load().qlin_gemm_w8a8_ch, 0, q_a, s_a, qweight, s_w, y, workspace, stream)
 
 
 def gemm_w8a8_ch_c16(q_a: torch.Tensor, s_a: torch.Tensor, qweight: torch.Tensor,
-                     s_w: torch.Tensor, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+                     s_w: torch.Tensor, y: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """gemm_w8a8_ch with the activation codes as fp16 (q_a fp16 [M,K], the
-    output of the *_c16 producers); needs no workspace."""
-    device, M, N, K, y = _ch_inputs(torch.float16, q_a, s_a, qweight, s_w, y)
-    _run(load().qlin_gemm_w8a8_ch_c16, device, stream, q_a.data_ptr(), s_a.data_ptr(),
-         qweight.data_ptr(), s_w.data_ptr(), M, N, K, y.data_ptr())
-    return y
+    output of the *_c16 producers); its workspace has
+    gemm_w8a8_ch_workspace_bytes(M, N, K, True) bytes."""
+    return _gemm_ch(load().qlin_gemm_w8a8_ch_c16, 1, q_a, s_a, qweight, s_w, y, workspace, stream)
 
 
 def _adjust(logits, tokens, prompt_len, total_len, repetition, presence, frequency, bias_ids, bias,
             allowed, out, argmax, stream):
-    device = _lead(logits, "logits", (torch.bfloat16, torch.float32), 2)
+    dev = _lead(logits, "logits", (torch.bfloat16, torch.float32), 2)
+    dtype = logits.dtype
     M, V = logits.shape
+    row = (M,)
     i32, f32 = torch.int32, torch.float32
-    specs = [(logits, "logits", logits.dtype, (M, V))]
     L = B = 0
     if tokens is not None:
         _lead(tokens, "tokens", (i32,), 2)
         L = tokens.shape[1]
-        specs.append((tokens, "tokens", i32, (M, L)))
+        if not _is(tokens, i32, (M, L), dev):
+            _refuse(tokens, "tokens", i32, (M, L), dev)
+        if prompt_len is not None and not _is(prompt_len, i32, row, dev):
+            _refuse(prompt_len, "prompt_len", i32, row, dev)
+        if total_len is not None and not _is(total_len, i32, row, dev):
+            _refuse(total_len, "total_len", i32, row, dev)
     elif prompt_len is not None or total_len is not None:
         raise ValueError("prompt_len and total_len need tokens")
-    if (bias_ids is None) != (bias is None):
-        raise ValueError("bias_ids and bias go together")
-    if bias_ids is not None:
+    if bias_ids is not None and bias is not None:
         _lead(bias_ids, "bias_ids", (i32,), 2)
         B = bias_ids.shape[1]
-        specs += [(bias_ids, "bias_ids", i32, (M, B)), (bias, "bias", f32, (M, B))]
-    row = (M,)
-    if prompt_len is not None:
-        specs.append((prompt_len, "prompt_len", i32, row))
-    if total_len is not None:
-        specs.append((total_len, "total_len", i32, row))
-    if repetition is not None:
-        specs.append((repetition, "repetition", f32, row))
-    if presence is not None:
-        specs.append((presence, "presence", f32, row))
-    if frequency is not None:
-        specs.append((frequency, "frequency", f32, row))
-    if allowed is not None:
-        specs.append((allowed, "allowed", i32, (M, (V + 31) // 32)))
-    if out is not None:
-        specs.append((out, "out", logits.dtype, (M, V)))
-    if argmax is not None:
-        specs.append((argmax, "argmax", i32, row))
-    _tensors(device, *specs)
+        if not _is(bias_ids, i32, (M, B), dev):
+            _refuse(bias_ids, "bias_ids", i32, (M, B), dev)
+        if not _is(bias, f32, (M, B), dev):
+            _refuse(bias, "bias", f32, (M, B), dev)
+    elif bias_ids is not None or bias is not None:
+        raise ValueError("bias_ids and bias go together")
+    if repetition is not None and not _is(repetition, f32, row, dev):
+        _refuse(repetition, "repetition", f32, row, dev)
+    if presence is not None and not _is(presence, f32, row, dev):
+        _refuse(presence, "presence", f32, row, dev)
+    if frequency is not None and not _is(frequency, f32, row, dev):
+        _refuse(frequency, "frequency", f32, row, dev)
+    if allowed is not None and not _is(allowed, i32, (M, (V + 31) // 32), dev):
+        _refuse(allowed, "allowed", i32, (M, (V + 31) // 32), dev)
+    if out is not None and not _is(out, dtype, (M, V), dev):
+        _refuse(out, "out", dtype, (M, V), dev)
+    if argmax is not None and not _is(argmax, i32, row, dev):
+        _refuse(argmax, "argmax", i32, row, dev)
     lib = load()
-    fn = lib.qlin_adjust_logits_bf16 if logits.dtype == torch.bfloat16 else lib.qlin_adjust_logits_f32
-    _run(fn, device, stream, logits.data_ptr(), M, V, _opt(tokens), L, _opt(prompt_len),
+    fn = lib.qlin_adjust_logits_bf16 if dtype is torch.bfloat16 else lib.qlin_adjust_logits_f32
+    _run(fn, dev, stream, logits.data_ptr(), M, V, _opt(tokens), L, _opt(prompt_len),
          _opt(total_len), _opt(repetition), _opt(presence), _opt(frequency), _opt(bias_ids),
          _opt(bias), B, _opt(allowed), _opt(out), _opt(argmax))
 
