@@ -235,7 +235,7 @@ qlin_status_t run_adjust_logits(const LogitArgs& a, cudaStream_t stream) {
   qlin_status_t st = device_or_error(&d);
   if (st != QLIN_OK) return st;
   if (a.M == 0) return QLIN_OK;
-  return from_cuda(launch_adjust_logits(a, d->sm_count, stream));
+  return from_cuda(launch_adjust_logits(a, d->err_word, d->sm_count, stream));
 }
 
 qlin_status_t run_silu_mul_quant(const uint16_t* gate_up, int64_t M, int64_t I, void* q, bool c16,

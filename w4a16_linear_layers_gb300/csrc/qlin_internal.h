@@ -84,7 +84,7 @@ struct LogitArgs {
   void* out;                  // the logits' type, or nullptr
   int32_t* argmax;            // [M] or nullptr
 };
-cudaError_t launch_adjust_logits(const LogitArgs& a, int sm_count, cudaStream_t stream);
+cudaError_t launch_adjust_logits(const LogitArgs& a, int* err, int sm_count, cudaStream_t stream);
 
 cudaError_t launch_pack(const int8_t* q, int64_t K, int64_t N, int bits, int32_t* qweight,
                         int32_t* qzeros, int* err, cudaStream_t stream);
