@@ -343,8 +343,8 @@ static_assert(kCounterBytes == 256 * sizeof(int), "one counter a thread");
 template <int T>
 cudaError_t launch_pair_t(const CUtensorMap& tw, const CUtensorMap& tx, const pair::Params& p, cudaStream_t stream) {
   // The kernel's warps trade registers (setmaxnreg) within what the block was
-  // launched with: 128 x 32 + 256 x 64 + 256 x 160.  A build that gave the
-  // block less would wait for them forever, so it is refused here.
+  // launched with.  A build that gave the block less would wait for them
+  // forever, so it is refused here.
   static std::atomic<uint64_t> ready{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -354,7 +354,7 @@ cudaError_t launch_pair_t(const CUtensorMap& tw, const CUtensorMap& tx, const pa
     cudaFuncAttributes fa;
     e = cudaFuncGetAttributes(&fa, pair::pair_kernel<T>);
     if (e != cudaSuccess) return e;
-    if (fa.numRegs * pair::kThreads < 128 * 32 + 256 * 64 + 256 * 160) return cudaErrorLaunchOutOfResources;
+    if (fa.numRegs * pair::kThreads < pair::Cfg<T>::kRegsSum) return cudaErrorLaunchOutOfResources;
     e = cudaFuncSetAttribute(pair::pair_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(pair::Cfg<T>::kSmem));
     if (e != cudaSuccess) return e;
@@ -366,6 +366,7 @@ cudaError_t launch_pair_t(const CUtensorMap& tw, const CUtensorMap& tx, const pa
 
 cudaError_t launch_pair(const ChannelGemmArgs& a, int* err, int sm_count, cudaStream_t stream) {
   const PairPlan pl = plan_pair(a.M, a.N, a.K, sm_count);
+  if (pl.TT * pl.F2 > (1LL << 30)) return cudaErrorInvalidValue;   // y would not fit any memory
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   const void* codes = a.act;
   int* counters = nullptr;
@@ -387,7 +388,8 @@ cudaError_t launch_pair(const ChannelGemmArgs& a, int* err, int sm_count, cudaSt
   CUtensorMap tw, tx;
   if (!make_map_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_INT32, a.qweight, a.N, a.K / 4, static_cast<uint64_t>(a.N) * 4, 128,
                    32, CU_TENSOR_MAP_SWIZZLE_NONE) ||
-      !make_act_map(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, codes, a.M, a.K, static_cast<uint32_t>(pl.T / 2), 2))
+      !make_act_map(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, codes, a.M, a.K, static_cast<uint32_t>(pl.T / 2),
+                    pl.T == 256 ? 2 : 1))
     return cudaErrorInvalidValue;
   pair::Params p;
   p.s_a = a.s_a;
@@ -395,13 +397,13 @@ cudaError_t launch_pair(const ChannelGemmArgs& a, int* err, int sm_count, cudaSt
   p.y = a.y;
   p.M = a.M;
   p.N = a.N;
-  p.G = pl.G;
-  p.F2 = pl.F2;
-  p.TT = pl.TT;
-  p.band = pl.band;
-  p.pairs = pl.pairs;
-  p.sk_tiles = pl.sk_tiles;
-  p.sk_pairs = pl.sk_pairs > 0 ? pl.sk_pairs : 1;
+  p.G = static_cast<int>(pl.G);
+  p.F2 = static_cast<int>(pl.F2);
+  p.TT = static_cast<int>(pl.TT);
+  p.band = static_cast<int>(pl.band);
+  p.pairs = static_cast<int>(pl.pairs);
+  p.sk_tiles = static_cast<int>(pl.sk_tiles);
+  p.sk_pairs = pl.sk_pairs > 0 ? static_cast<int>(pl.sk_pairs) : 1;
   p.counters = counters;
   p.part = pl.cut ? reinterpret_cast<int32_t*>(ws + kCounterBytes) : nullptr;
   p.err = err;

@@ -3,15 +3,25 @@
 // thread blocks (two SMs, tcgen05 cta_group::2) per tile of 256 output channels
 // x T tokens.
 //
-//   * The MMA runs with the weights as operand A (256 rows, 128 from each
-//     block, widened by threads straight into tensor memory) and the tokens as
-//     operand B (T columns, fp16 codes, 128-byte swizzled).  Each block loads
-//     its own 128 channels' words and half of the tokens: the pair reads every
-//     operand byte once, where two single blocks would read the tokens twice.
-//     Per 128-wide K step and SM that is 16 KB of words and T * 128 bytes of
-//     codes against 4 T cycles of MMA: 48 bytes a cycle at T = 256.
+//   * The MMA runs with the weights as operand A (widened by threads straight
+//     into tensor memory, 128 channels a block) and the tokens as operand B
+//     (T columns, fp16 codes, 128-byte swizzled).  Each block loads its own
+//     words and half of the tokens: the pair reads every operand byte once.
+//     - T of 192 and 256: cta_group::2, one MMA of 256 x T for both blocks,
+//       issued by the first, each block's shared memory holding its half of the
+//       tokens: 48 bytes a cycle and SM through L2 at T = 256, and as much
+//       shared-memory traffic.  Such an MMA takes 148 cycles at T = 256, and
+//       137 at T = 96 (measured; 8192 x 5120 x 34816: 1.90 ms, 1538 TF/s).
+//     - T of 64, 96 and 128: that floor would bound a step (16 KB of words a
+//       block) at 1100 cycles, where HBM delivers one in 700, so each block
+//       issues its own MMAs of 128 x T (cta_group::1, 46 to 64 cycles), and the
+//       token halves are multicast into both blocks' shared memory.
 //   * An accumulator takes at most 1024 of K (exact below 2^24); the
-//     epilogue adds each such chunk to int32 registers.
+//     epilogue adds each such chunk to int32 registers, under the next chunk's
+//     MMAs where tensor memory has room for two accumulators (T up to 192; at
+//     T = 256 the tensor pipe is idle for 2000 of every 12,000 cycles).  At
+//     T = 192 that leaves room for 256 of K as operand A, cut into units of
+//     64 instead of 128 to keep four of them on the way.
 //   * Work: whole tiles go round the pairs in bands of token tiles, so the
 //     pairs running at one time share a few channel tiles and one band's
 //     tokens in L2.  The tiles that do not fill a last round are cut along
@@ -20,7 +30,7 @@
 //     tile's counter adds the others' to its own.  Integer sums: the result
 //     does not depend on who is last.
 //   * Roles of a block's 20 warps: 0 streams words and 2 tokens by TMA, 1
-//     issues the MMAs (first block of the pair), 4-11 widen weights (two
+//     issues the MMAs, 4-11 widen weights (two
 //     groups taking alternate steps), 12-19 drain and write.
 //
 // Every wait is bounded; a wait that runs out records an error, aborts the
@@ -36,37 +46,55 @@ namespace qlin {
 namespace pair {
 
 constexpr int kF = 128;                 // channels of one block
-constexpr int kChunk = 8;               // K steps of 128 per accumulator
-constexpr int kBufs = 4;                // A buffers in TMEM and token slots in shared memory
+constexpr int kChunkK = 1024;           // K of an accumulator
+constexpr int kA = 4;                   // operand A buffers in TMEM, one unit of K each
 constexpr uint32_t kWBytes = 32 * kF * 4;
 constexpr int kThreads = 640;
 constexpr int kEpiThreads = 256;
 constexpr uint32_t kCtrl = 1024;
 constexpr uint32_t kSmemMax = 232448;
-constexpr int kMaxW = 6;                // even: a slot stays with one widening group
+constexpr int kMaxW = 8;
+constexpr int kMaxU = 8;
 
 template <int T>
 struct Cfg {
-  static constexpr int kHalf = T / 2;                         // tokens of one block
-  static constexpr uint32_t kXBytes = kHalf * 256u;           // one step's codes of one block
-  static constexpr int kND = T <= 128 ? 2 : 1;                // accumulators
-  static constexpr int kCols = T / 2;                         // accumulator columns of an epilogue thread
-  static constexpr uint32_t kColD = 64 * kBufs;
-  static constexpr int kWSlotsFit = static_cast<int>((kSmemMax - 1024 - kCtrl - kBufs * kXBytes) / kWBytes);
-  static constexpr int kWSlots = kWSlotsFit < kMaxW ? kWSlotsFit : kMaxW;
-  static constexpr uint32_t kSmem = 1024 + kCtrl + kBufs * kXBytes + kWSlots * kWBytes;
+  static constexpr bool k2 = T >= 192;                        // one MMA for both blocks
+  static constexpr int kHalf = T / 2;                         // tokens that one block loads
+  static constexpr int kRows = k2 ? kHalf : T;                // tokens in one block's shared memory
+  static constexpr int kUnit = T == 192 ? 64 : 128;           // K of a unit: one A buffer, one token slot
+  static constexpr int kPerStep = 128 / kUnit;                // units of a K step
+  static constexpr int kChunk = kChunkK / kUnit;              // units of an accumulator
+  static constexpr int kACols = kUnit / 2;
+  static constexpr uint32_t kXBytes = kRows * kUnit * 2u;     // a unit's codes in one block
+  static constexpr int kX = T == 192 ? 8 : 4;                 // token slots
+  static constexpr int kND = T <= 192 ? 2 : 1;                // accumulators
+  static constexpr int kE = T / 2;                            // sums of an epilogue thread
+  static constexpr uint32_t kColD = kA * kACols;
+  static constexpr int kWSlotsFit = static_cast<int>((kSmemMax - 1024 - kCtrl - kX * kXBytes) / kWBytes) & ~1;
+  static constexpr int kWSlots = kWSlotsFit < kMaxW ? kWSlotsFit : kMaxW;   // even: a slot stays with one widening group
+  static constexpr uint32_t kSmem = 1024 + kCtrl + kX * kXBytes + kWSlots * kWBytes;
+  // Registers a thread: the block is launched with 96 and the roles trade them
+  // within that.  (32 for the control warps made the MMA issuer spill: with the
+  // rings there is no L1 to speak of, and a K step took 1100 cycles for it.)
+  static constexpr int kRegsCtl = T > 128 ? 48 : 64;
+  static constexpr int kRegsConv = T > 128 ? 64 : 80;
+  static constexpr int kRegsEpi = T > 128 ? 152 : 128;
+  static constexpr int kRegsSum = 128 * kRegsCtl + 256 * kRegsConv + 256 * kRegsEpi;
+  static_assert(kRegsSum <= 96 * kThreads, "setmaxnreg draws on what the block was launched with");
   static_assert(T % 32 == 0 && T >= 64 && T <= 256, "token tile");
-  static_assert(kColD + kND * T <= 512, "TMEM budget");
+  static_assert(kColD + kND * T <= 512 && kE % 16 == 0, "TMEM budget");
+  static_assert(kX >= kA && kX <= kMaxU && kX % 2 == 0, "token slots");
   static_assert(kWSlots >= 4 && kWSlots % 2 == 0 && kSmem <= kSmemMax, "shared memory");
 };
 
 struct Ctrl {
   uint64_t wfull[kMaxW], wempty[kMaxW];
-  uint64_t xfull[kBufs];      // first block: both halves' codes landed
-  uint64_t a_full[kBufs];     // first block: both blocks' weights are in TMEM
-  uint64_t consumed[kBufs];   // the MMAs of the step completed: A buffer and token slot are free
+  // of a unit; with one MMA for both blocks, the first block's `ready` and
+  // d_empty count both
+  uint64_t ready[kMaxU];      // its weights are in TMEM and its codes landed
+  uint64_t consumed[kMaxU];   // the MMAs that read them completed (both blocks')
   uint64_t d_full[2];
-  uint64_t d_empty[2];        // first block: both blocks drained the accumulator
+  uint64_t d_empty[2];        // the accumulator is drained
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort_flag;
@@ -79,12 +107,12 @@ struct Params {
   const float* s_w;
   uint16_t* y;
   int64_t M, N;
-  int64_t G;          // K / 128
-  int64_t F2, TT;     // tiles of 256 channels, of T tokens
-  int64_t band;       // token tiles of a band
-  int64_t pairs;
-  int64_t sk_tiles;   // tiles cut along K: the last ones of the order
-  int64_t sk_pairs;   // pairs that share them
+  int G;              // K / 128
+  int F2, TT;         // tiles of 256 channels, of T tokens
+  int band;           // token tiles of a band
+  int pairs;
+  int sk_tiles;       // tiles cut along K: the last ones of the order
+  int sk_pairs;       // pairs that share them
   int* counters;      // [sk_tiles][2]
   int32_t* part;      // [pairs][2][2][T][128]
   int* err;
@@ -95,31 +123,28 @@ struct Params {
 // along K, then its whole tiles.
 struct Work {
   const Params& p;
-  int64_t pr, whole;          // pair index; whole tiles of all pairs
-  int64_t s, s1;              // share of the cut tiles' steps
-  int64_t s_first;            // tile (of the cut ones) in which the share starts
-  int64_t q;                  // next whole tile
-  int64_t tile, f, t, g0, g1;
+  int s, s1;              // share of the cut tiles' steps
+  int q;                  // next whole tile
+  int tile, f, t, g0, g1;
   bool cut;
-  __device__ __forceinline__ Work(const Params& p_, int64_t pair) : p(p_), pr(pair) {
-    const int64_t steps = p.sk_tiles * p.G;
-    whole = p.F2 * p.TT - p.sk_tiles;
-    s = pr < p.sk_pairs ? pr * steps / p.sk_pairs : 0;
-    s1 = pr < p.sk_pairs ? (pr + 1) * steps / p.sk_pairs : 0;
-    s_first = s / p.G;
-    q = pr;
+  __device__ __forceinline__ Work(const Params& p_, int pair) : p(p_), s(0), s1(0), q(pair) {
+    if (pair < p.sk_pairs) {
+      s = pair * (p.sk_tiles * p.G) / p.sk_pairs;
+      s1 = (pair + 1) * (p.sk_tiles * p.G) / p.sk_pairs;
+    }
   }
+  __device__ __forceinline__ int whole() const { return p.F2 * p.TT - p.sk_tiles; }   // of all pairs
   __device__ __forceinline__ bool next() {
     if (s < s1) {
       tile = s / p.G;
       g0 = s - tile * p.G;
-      g1 = p.G < g0 + (s1 - s) ? p.G : g0 + (s1 - s);
+      g1 = min(p.G, g0 + (s1 - s));
       s += g1 - g0;
       cut = g1 - g0 != p.G;
-      place(whole + tile);
+      place(whole() + tile);
       return true;
     }
-    if (q >= whole) return false;
+    if (q >= whole()) return false;
     cut = false;
     g0 = 0;
     g1 = p.G;
@@ -127,18 +152,18 @@ struct Work {
     q += p.pairs;
     return true;
   }
-  __device__ __forceinline__ void place(int64_t i) {
-    const int64_t b = i / (p.band * p.F2);
-    const int64_t r = i - b * p.band * p.F2;
-    const int64_t rows = p.TT - b * p.band < p.band ? p.TT - b * p.band : p.band;
+  __device__ __forceinline__ void place(int i) {
+    const int b = i / (p.band * p.F2);
+    const int r = i - b * p.band * p.F2;
+    const int rows = min(p.TT - b * p.band, p.band);
     f = r / rows;
     t = b * p.band + (r - f * rows);
   }
 };
 
 // The pair whose share holds step i of the cut tiles.
-__device__ __forceinline__ int64_t pair_of_step(int64_t i, const Params& p) {
-  const int64_t W = p.sk_tiles * p.G;
+__device__ __forceinline__ int pair_of_step(int i, const Params& p) {
+  const int W = p.sk_tiles * p.G;
   return ((i + 1) * p.sk_pairs + W - 1) / W - 1;
 }
 
@@ -148,14 +173,18 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
   return r;
 }
 
-// Arrives on a barrier of either block of the pair.  Block-scope release is
-// enough, and all that is ordered: tensor-memory accesses that have completed
-// (tcgen05.wait) and are fenced (tcgen05.fence::before_thread_sync).  No data
-// passes between the blocks through generic memory here.  With cluster scope
-// every arrival waited for the block's outstanding stores, and a K step took
-// 0.95 us for any T up to 128.
-__device__ __forceinline__ void arrive_cluster(uint32_t remote_bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(remote_bar) : "memory");
+// Arrives on the barrier, the first block's if one MMA serves both (k2).
+// Block-scope release is enough for it too, and all that is ordered: tensor-
+// memory accesses that have completed (tcgen05.wait) and are fenced
+// (tcgen05.fence::before_thread_sync).  No data passes between the blocks
+// through generic memory here.  With cluster scope every arrival waited for
+// the block's outstanding stores, and a K step took 0.95 us for any T up to 128.
+template <bool k2>
+__device__ __forceinline__ void arrive(uint32_t bar) {
+  if constexpr (k2)
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(map_to_rank(bar, 0)) : "memory");
+  else
+    mbar_arrive(bar);
 }
 
 // Tokens: a box of the 3D code map into this block's shared memory, its bytes
@@ -169,6 +198,18 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
       : "memory");
 }
 
+// One K half of them into both blocks' shared memory, counted on each block's
+// own barrier.
+__device__ __forceinline__ void tma_load_both(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x,
+                                              int32_t y, int32_t z, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6, %7;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "h"(static_cast<uint16_t>(3)),
+      "l"(policy)
+      : "memory");
+}
+
 __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                          uint32_t accumulate) {
   asm volatile(
@@ -179,12 +220,24 @@ __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint32_t a_tmem, uint6
       : "memory");
 }
 
-// Arrives once on `bar` in both blocks when this thread's MMAs so far completed.
-__device__ __forceinline__ void commit_pair(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-      "h"(static_cast<uint16_t>(3))
-      : "memory");
+// Arrives once on `bar`, of this block or (kBoth) of both, when this thread's
+// MMAs so far have completed.
+template <bool k2, bool kBoth>
+__device__ __forceinline__ void commit(uint32_t bar) {
+  if constexpr (k2 && kBoth)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+  else if constexpr (k2)
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  else if constexpr (kBoth)
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+  else
+    tc_commit(bar);
 }
 
 __device__ __forceinline__ void cluster_sync() {
@@ -200,40 +253,33 @@ __device__ __forceinline__ void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
-  tmem_ld16(taddr, r);
-  tmem_ld16(taddr + 16, r + 16);
-}
-
 template <int T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, const Params p) {
   using C = Cfg<T>;
   constexpr int NW = C::kWSlots;
-  constexpr int ND = C::kND;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_u32(smem);
   constexpr uint32_t x_off = NW * kWBytes;
-  Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem + x_off + kBufs * C::kXBytes);
+  Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem + x_off + C::kX * C::kXBytes);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const uint32_t rank = blockIdx.x & 1u;     // the cluster is two consecutive blocks
-  const int64_t pr = blockIdx.x >> 1;
+  const int pr = static_cast<int>(blockIdx.x >> 1);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NW; ++i) {
       mbar_init(smem_u32(&ctrl->wfull[i]), 1);
       mbar_init(smem_u32(&ctrl->wempty[i]), 4);
     }
-    for (int i = 0; i < kBufs; ++i) {
-      mbar_init(smem_u32(&ctrl->xfull[i]), 1);
-      mbar_init(smem_u32(&ctrl->a_full[i]), 8);
-      mbar_init(smem_u32(&ctrl->consumed[i]), 1);
+    for (int i = 0; i < C::kX; ++i) {
+      mbar_init(smem_u32(&ctrl->ready[i]), C::k2 ? 9 : 5);    // widening warps, and the token copies' issuer
+      mbar_init(smem_u32(&ctrl->consumed[i]), C::k2 ? 1 : 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&ctrl->d_full[i]), 1);
-      mbar_init(smem_u32(&ctrl->d_empty[i]), 16);
+      mbar_init(smem_u32(&ctrl->d_empty[i]), C::k2 ? 16 : 8);
     }
     mbar_init(smem_u32(&ctrl->mma_done), 1);
     ctrl->abort_flag = 0;
@@ -244,10 +290,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   __syncwarp();
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctrl->tmem_base)),
-                 "r"(512u)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    if constexpr (C::k2) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctrl->tmem_base)),
+                   "r"(512u)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      tmem_alloc(smem_u32(&ctrl->tmem_base), 512);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -260,7 +311,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const WaitCtx drain_ctx{p.err, &never_abort, p.limit_ns};
 
   if (warp < 4) {
-    reg_dec<32>();
+    reg_dec<C::kRegsCtl>();
     if (warp == 0 && lane == 0) {
       // -------------------------------------------------------- words
       // read once when one token tile takes them, else shared by a band
@@ -269,8 +320,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int issued = 0;
       bool ok = true;
       while (ok && w.next()) {
-        const int32_t x = static_cast<int32_t>(w.f * 256 + rank * kF);
-        for (int64_t g = w.g0; g < w.g1; ++g) {
+        const int32_t x = w.f * 256 + static_cast<int>(rank) * kF;
+        for (int g = w.g0; g < w.g1; ++g) {
           const int slot = issued % NW;
           if (!mbar_wait(smem_u32(&ctrl->wempty[slot]), (static_cast<uint32_t>(issued / NW) & 1u) ^ 1u, ctx, 60)) {
             ok = false;
@@ -278,7 +329,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           const uint32_t full = smem_u32(&ctrl->wfull[slot]);
           mbar_arrive_expect_tx(full, kWBytes);
-          tma_load_2d(sbase + slot * kWBytes, &tm_w, full, x, static_cast<int32_t>(g * 32), pol);
+          tma_load_2d(sbase + slot * kWBytes, &tm_w, full, x, g * 32, pol);
           ++issued;
         }
       }
@@ -293,74 +344,84 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int j = 0;
       bool ok = true;
       while (ok && w.next()) {
-        const int32_t row = static_cast<int32_t>(w.t * T + rank * C::kHalf);
-        for (int64_t g = w.g0; g < w.g1; ++g, ++j) {
-          const int slot = j % kBufs;
-          if (!mbar_wait(smem_u32(&ctrl->consumed[slot]), (static_cast<uint32_t>(j / kBufs) & 1u) ^ 1u, ctx, 62)) {
+        const int32_t row = w.t * T + static_cast<int>(rank) * C::kHalf;
+        for (int u = w.g0 * C::kPerStep; u < w.g1 * C::kPerStep; ++u, ++j) {
+          const int slot = j % C::kX;
+          if (!mbar_wait(smem_u32(&ctrl->consumed[slot]), (static_cast<uint32_t>(j / C::kX) & 1u) ^ 1u, ctx, 62)) {
             ok = false;
             break;
           }
-          const uint32_t full = smem_u32(&ctrl->xfull[slot]);
-          if (rank == 0) mbar_arrive_expect_tx(full, 2 * C::kXBytes);
-          tma_load_pair(sbase + x_off + slot * C::kXBytes, &tm_x, map_to_rank(full, 0), 0, row,
-                        static_cast<int32_t>(2 * g), pol);
+          const uint32_t full = smem_u32(&ctrl->ready[slot]);
+          const uint32_t dst = sbase + x_off + slot * C::kXBytes;
+          if constexpr (C::k2) {
+            if (rank == 0) mbar_arrive_expect_tx(full, 2 * C::kXBytes);
+            tma_load_pair(dst, &tm_x, map_to_rank(full, 0), 0, row, u * (C::kUnit / 64), pol);
+          } else {
+            // each 64 of K is T rows x 128 B, this block's rows its first or second half
+            mbar_arrive_expect_tx(full, C::kXBytes);
+#pragma unroll
+            for (int h = 0; h < C::kUnit / 64; ++h)
+              tma_load_both(dst + h * (T * 128u) + rank * (C::kHalf * 128u), &tm_x, full, 0, row,
+                            u * (C::kUnit / 64) + h, pol);
+          }
         }
       }
-      // the first block sees both blocks' last copies land; the second one
-      // leaves only after it (the closing cluster barrier)
-      if (rank == 0)
-        for (int i = j > kBufs ? j - kBufs : 0; i < j; ++i)
-          (void)mbar_wait(smem_u32(&ctrl->xfull[i % kBufs]), static_cast<uint32_t>(i / kBufs) & 1u, drain_ctx, 63);
+      // the last units' MMAs completed, in both blocks: their copies landed, and
+      // no arrival is on its way here when the block ends
+      if (ok)
+        for (int i = j > C::kX ? j - C::kX : 0; i < j; ++i)
+          (void)mbar_wait(smem_u32(&ctrl->consumed[i % C::kX]), static_cast<uint32_t>(i / C::kX) & 1u, drain_ctx, 63);
       if (!ok) {
         // given up: the blocks may have issued different numbers of copies, so
         // allow those in flight a millisecond to land
         const uint64_t t0 = globaltimer_ns();
         while (globaltimer_ns() - t0 < 1000000u) __nanosleep(1000);
       }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && lane == 0 && (rank == 0 || !C::k2)) {
       // ---------------------------------------------------------- MMAs
-      constexpr uint32_t idesc = idesc_f16(256, T, false);
+      constexpr uint32_t idesc = idesc_f16(C::k2 ? 256 : 128, T, false);
       Work w(p, pr);
-      int j = 0, d = 0;
+      int j = 0;
+      int d = 0;      // chunks begun
       bool ok = true;
       while (ok && w.next()) {
-        for (int64_t g = w.g0; ok && g < w.g1; g += kChunk, ++d) {
-          const int n = static_cast<int>(w.g1 - g < kChunk ? w.g1 - g : kChunk);
-          const int db = d % ND;
-          const uint32_t dcol = tmem + C::kColD + db * T;
-          if (!mbar_wait(smem_u32(&ctrl->d_empty[db]), (static_cast<uint32_t>(d / ND) & 1u) ^ 1u, ctx, 64)) {
-            ok = false;
-            break;
+        const int n = (w.g1 - w.g0) * C::kPerStep;
+        uint32_t dcol = 0;
+        for (int i = 0; i < n; ++i, ++j) {
+          const int ci = i % C::kChunk;
+          if (ci == 0) {
+            ok = mbar_wait(smem_u32(&ctrl->d_empty[d % C::kND]), (static_cast<uint32_t>(d / C::kND) & 1u) ^ 1u, ctx, 64);
+            if (!ok) break;
+            dcol = tmem + C::kColD + d % C::kND * T;
           }
-          for (int i = 0; i < n; ++i, ++j) {
-            const int slot = j % kBufs;
-            const uint32_t ph = static_cast<uint32_t>(j / kBufs) & 1u;
-            if (!mbar_wait(smem_u32(&ctrl->xfull[slot]), ph, ctx, 65) ||
-                !mbar_wait(smem_u32(&ctrl->a_full[slot]), ph, ctx, 66)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint64_t b0 = smem_desc(sbase + x_off + slot * C::kXBytes, 16u, 1024u, 2u);
+          const int slot = j % C::kX;
+          ok = mbar_wait(smem_u32(&ctrl->ready[slot]), static_cast<uint32_t>(j / C::kX) & 1u, ctx, 65);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t b0 = smem_desc(sbase + x_off + slot * C::kXBytes, 16u, 1024u, 2u);
+          const uint32_t a0 = tmem + j % kA * C::kACols;
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks) {
-              const uint32_t off = static_cast<uint32_t>(ks >> 2) * (C::kHalf * 128u) + static_cast<uint32_t>(ks & 3) * 32u;
-              mma_pair(dcol, tmem + slot * 64 + ks * 8, b0 + (off >> 4), idesc, (i > 0 || ks > 0) ? 1u : 0u);
-            }
-            commit_pair(smem_u32(&ctrl->consumed[slot]));
+          for (int ks = 0; ks < C::kUnit / 16; ++ks) {
+            const uint32_t off = static_cast<uint32_t>(ks >> 2) * (C::kRows * 128u) + static_cast<uint32_t>(ks & 3) * 32u;
+            if constexpr (C::k2)
+              mma_pair(dcol, a0 + ks * 8, b0 + (off >> 4), idesc, (ci > 0 || ks > 0) ? 1u : 0u);
+            else
+              mma_ts(dcol, a0 + ks * 8, b0 + (off >> 4), idesc, (ci > 0 || ks > 0) ? 1u : 0u);
           }
-          if (ok) commit_pair(smem_u32(&ctrl->d_full[db]));
+          if (ci == C::kChunk - 1 || i == n - 1) {
+            commit<C::k2, C::k2>(smem_u32(&ctrl->d_full[d % C::kND]));
+            ++d;
+          }
+          commit<C::k2, true>(smem_u32(&ctrl->consumed[slot]));
         }
       }
-      asm volatile(
-          "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&ctrl->mma_done))
-          : "memory");
+      commit<C::k2, false>(smem_u32(&ctrl->mma_done));
       (void)mbar_wait(smem_u32(&ctrl->mma_done), 0u, drain_ctx, 67);
     }
     __syncwarp();
   } else if (warp < 12) {
     // ---------------------------------------------------------- widening
-    reg_dec<64>();
+    reg_dec<C::kRegsConv>();
     const int ct = threadIdx.x - 128;
     const int grp = ct >> 7;
     const int r = ct & 127;
@@ -369,10 +430,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int j = 0;
     bool ok = true;
     while (ok && w.next()) {
-      for (int64_t g = w.g0; g < w.g1; ++g, ++j) {
+      for (int g = w.g0; g < w.g1; ++g, ++j) {
         if ((j & 1) != grp) continue;
         const int ws = j % NW;
-        const int ab = j % kBufs;
         ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&ctrl->wfull[ws]), static_cast<uint32_t>(j / NW) & 1u, ctx, 68));
         if (!ok) break;
         const uint32_t* src = reinterpret_cast<const uint32_t*>(smem + ws * kWBytes);
@@ -381,30 +441,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 32; ++i) word[i] = src[i * kF + r];
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ctrl->wempty[ws]));
-        // buffer ab was last used by step j - 4, this group's as well
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&ctrl->consumed[ab]),
-                                                  (static_cast<uint32_t>(j / kBufs) & 1u) ^ 1u, ctx, 69));
-        if (!ok) break;
-        tc_fence_after();
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          uint32_t v[16];
+        for (int part = 0; part < C::kPerStep; ++part) {
+          const int u = j * C::kPerStep + part;
+          // The A buffer was last used by unit u - kA.  Its barrier's next phase
+          // is of unit u - kA + kX, whose weights come after these.
+          if (u >= kA)
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&ctrl->consumed[(u - kA) % C::kX]),
+                                                   static_cast<uint32_t>((u - kA) / C::kX) & 1u, ctx, 69));
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) biased_u8x4_to_f16x4(word[8 * h + i], v[2 * i], v[2 * i + 1]);
-          tmem_st16(tmem + lane_off + ab * 64 + h * 16, v);
+          for (int h = 0; h < C::kUnit / 32; ++h) {
+            uint32_t v[16];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              biased_u8x4_to_f16x4(word[part * (C::kUnit / 4) + 8 * h + i], v[2 * i], v[2 * i + 1]);
+            tmem_st16(tmem + lane_off + u % kA * C::kACols + h * 16, v);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive<C::k2>(smem_u32(&ctrl->ready[u % C::kX]));
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_cluster(map_to_rank(smem_u32(&ctrl->a_full[ab]), 0));
+        if (!ok) break;
       }
     }
     __syncwarp();
   } else {
     // ---------------------------------------------------------- epilogue
-    reg_inc<160>();
+    reg_inc<C::kRegsEpi>();
     grid_dep_wait();   // outputs and workspace may still be in use upstream
-    constexpr int E = C::kCols;
+    constexpr int E = C::kE;
     const int et = threadIdx.x - 384;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -414,10 +482,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int d = 0;
     bool ok = true;
     while (ok && w.next()) {
-      for (int64_t g = w.g0; g < w.g1; g += kChunk, ++d) {
-        const int db = d % ND;
+#pragma unroll
+      for (int c = 0; c < E; ++c) acc[c] = 0;
+      for (int g = w.g0; g < w.g1; g += kChunkK / 128, ++d) {
+        const int db = d % C::kND;
         ok = __all_sync(0xFFFFFFFFu,
-                        mbar_wait(smem_u32(&ctrl->d_full[db]), static_cast<uint32_t>(d / ND) & 1u, ctx, 70));
+                        mbar_wait(smem_u32(&ctrl->d_full[db]), static_cast<uint32_t>(d / C::kND) & 1u, ctx, 70));
         if (!ok) break;
         tc_fence_after();
         const uint32_t dcol = tmem + lane_off + C::kColD + db * T + col0;
@@ -427,31 +497,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tmem_ld16(dcol + c, v);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int32_t x = __float2int_rn(__uint_as_float(v[i]));
-            acc[c + i] = g == w.g0 ? x : acc[c + i] + x;
-          }
+          for (int i = 0; i < 16; ++i) acc[c + i] += __float2int_rn(__uint_as_float(v[i]));
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_cluster(map_to_rank(smem_u32(&ctrl->d_empty[db]), 0));
+        if (lane == 0) arrive<C::k2>(smem_u32(&ctrl->d_empty[db]));
       }
       if (!named_bar_and(1, kEpiThreads, ok)) break;
       bool finish = true;
       if (w.cut) {
         // the contributors of this tile, and this block's place among them
-        const int64_t c0 = pair_of_step(w.tile * p.G, p);
-        const int64_t c1 = pair_of_step(w.tile * p.G + p.G - 1, p);
+        const int c0 = pair_of_step(w.tile * p.G, p);
+        const int c1 = pair_of_step(w.tile * p.G + p.G - 1, p);
         int* counter = p.counters + w.tile * 2 + rank;
-        const int others = static_cast<int>(c1 - c0);
+        const int others = c1 - c0;
+        auto slot_of = [&](int c) {   // a pair's partials: of the tile its share starts in, and of its last one
+          const int first = c * (p.sk_tiles * p.G) / p.sk_pairs / p.G;
+          return p.part + static_cast<int64_t>((c * 2 + (first == w.tile ? 0 : 1)) * 2 + static_cast<int>(rank)) * (T * kF) +
+                 col0 * kF + r;
+        };
         // if all the others have arrived, this block's sums stay in registers
         if (et == 0) ctrl->last_flag = ld_acquire_gpu(counter) == others ? 1 : 0;
         named_bar_sync(1, kEpiThreads);
         finish = ctrl->last_flag != 0;
         named_bar_sync(1, kEpiThreads);
         if (!finish) {
-          const int mine = w.tile == w.s_first ? 0 : 1;
-          int32_t* dst = p.part + ((pr * 2 + mine) * 2 + rank) * static_cast<int64_t>(T * kF) + col0 * kF + r;
+          int32_t* dst = slot_of(pr);
 #pragma unroll
           for (int c = 0; c < E; ++c) dst[c * kF] = acc[c];
           named_bar_sync(1, kEpiThreads);
@@ -461,11 +532,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           named_bar_sync(1, kEpiThreads);
         }
         if (finish) {
-          for (int64_t c = c0; c <= c1; ++c) {
+          for (int c = c0; c <= c1; ++c) {
             if (c == pr) continue;
-            const int64_t start = c * (p.sk_tiles * p.G) / p.sk_pairs;
-            const int theirs = start / p.G == w.tile ? 0 : 1;
-            const int32_t* src = p.part + ((c * 2 + theirs) * 2 + rank) * static_cast<int64_t>(T * kF) + col0 * kF + r;
+            const int32_t* src = slot_of(c);
 #pragma unroll
             for (int i = 0; i < E; i += 16) {
               int32_t v[16];
@@ -478,16 +547,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       if (finish) {
-        const int64_t n = w.f * 256 + rank * kF + r;
-        const int64_t m0 = w.t * T + col0;
+        const int64_t n = static_cast<int64_t>(w.f) * 256 + rank * kF + r;
+        const int64_t m0 = static_cast<int64_t>(w.t) * T + col0;
         if (n < p.N && m0 < p.M) {
           const float sw = __ldg(p.s_w + n);
+          const float* sa = p.s_a + m0;
           uint16_t* dst = p.y + m0 * p.N + n;
+          const int rows = static_cast<int>(p.M - m0 < E ? p.M - m0 : E);
 #pragma unroll
-          for (int c = 0; c < E; ++c) {
-            if (m0 + c < p.M)
-              dst[c * p.N] = __bfloat16_as_ushort(__float2bfloat16_rn(
-                  __fmul_rn(__fmul_rn(__int2float_rn(acc[c]), sw), __ldg(p.s_a + m0 + c))));
+          for (int c = 0; c < E; ++c, dst += p.N) {
+            if (c < rows)
+              *dst = __bfloat16_as_ushort(
+                  __float2bfloat16_rn(__fmul_rn(__fmul_rn(__int2float_rn(acc[c]), sw), __ldg(sa + c))));
           }
         }
       }
@@ -503,7 +574,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();
   if (warp == 1) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+    if constexpr (C::k2)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+    else
+      tmem_dealloc(tmem, 512);
   }
 }
 
