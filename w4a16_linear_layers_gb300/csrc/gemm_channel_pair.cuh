@@ -244,6 +244,16 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
 template <int N>
 __device__ __forceinline__ void reg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
@@ -305,7 +315,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();      // both blocks' barriers are initialised
   tc_fence_after();
   grid_dep_launch();
-  const uint32_t tmem = ctrl->tmem_base;
+  const uint32_t tmem = 0;      // the block holds all 512 columns, so they start at 0
   const WaitCtx ctx{p.err, &ctrl->abort_flag, p.limit_ns};
   int never_abort = 0;
   const WaitCtx drain_ctx{p.err, &never_abort, p.limit_ns};
@@ -377,45 +387,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint64_t t0 = globaltimer_ns();
         while (globaltimer_ns() - t0 < 1000000u) __nanosleep(1000);
       }
-    } else if (warp == 1 && lane == 0 && (rank == 0 || !C::k2)) {
+    } else if (warp == 1 && (rank == 0 || !C::k2)) {
       // ---------------------------------------------------------- MMAs
+      // The whole warp goes through the loop, on values that the compiler can
+      // see to be uniform (no branch on a lane's own wait, TMEM from column 0),
+      // and one lane issues: the MMA's operands are uniform registers, and filling
+      // them from a single lane's made an issue take 60 cycles.
       constexpr uint32_t idesc = idesc_f16(C::k2 ? 256 : 128, T, false);
+      const bool leader = elect_one();
       Work w(p, pr);
-      int j = 0;
-      int d = 0;      // chunks begun
+      int slot = 0, ab = 0, db = 0;
+      uint32_t slot_par = 0u, d_par = 1u;
       bool ok = true;
       while (ok && w.next()) {
         const int n = (w.g1 - w.g0) * C::kPerStep;
-        uint32_t dcol = 0;
-        for (int i = 0; i < n; ++i, ++j) {
+        for (int i = 0; i < n; ++i) {
           const int ci = i % C::kChunk;
-          if (ci == 0) {
-            ok = mbar_wait(smem_u32(&ctrl->d_empty[d % C::kND]), (static_cast<uint32_t>(d / C::kND) & 1u) ^ 1u, ctx, 64);
-            if (!ok) break;
-            dcol = tmem + C::kColD + d % C::kND * T;
-          }
-          const int slot = j % C::kX;
-          ok = mbar_wait(smem_u32(&ctrl->ready[slot]), static_cast<uint32_t>(j / C::kX) & 1u, ctx, 65);
+          if (ci == 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&ctrl->d_empty[db]), d_par, ctx, 64));
+          if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&ctrl->ready[slot]), slot_par, ctx, 65));
           if (!ok) break;
           tc_fence_after();
           const uint64_t b0 = smem_desc(sbase + x_off + slot * C::kXBytes, 16u, 1024u, 2u);
-          const uint32_t a0 = tmem + j % kA * C::kACols;
+          const uint32_t a0 = static_cast<uint32_t>(ab * C::kACols);
+          const uint32_t dcol = static_cast<uint32_t>(C::kColD + db * T);
+          const bool ends = ci == C::kChunk - 1 || i == n - 1;
+          if (leader) {
 #pragma unroll
-          for (int ks = 0; ks < C::kUnit / 16; ++ks) {
-            const uint32_t off = static_cast<uint32_t>(ks >> 2) * (C::kRows * 128u) + static_cast<uint32_t>(ks & 3) * 32u;
-            if constexpr (C::k2)
-              mma_pair(dcol, a0 + ks * 8, b0 + (off >> 4), idesc, (ci > 0 || ks > 0) ? 1u : 0u);
-            else
-              mma_ts(dcol, a0 + ks * 8, b0 + (off >> 4), idesc, (ci > 0 || ks > 0) ? 1u : 0u);
+            for (int ks = 0; ks < C::kUnit / 16; ++ks) {
+              const uint32_t off = static_cast<uint32_t>(ks >> 2) * (C::kRows * 128u) + static_cast<uint32_t>(ks & 3) * 32u;
+              if constexpr (C::k2)
+                mma_pair(dcol, a0 + ks * 8, b0 + (off >> 4), idesc, (ci > 0 || ks > 0) ? 1u : 0u);
+              else
+                mma_ts(dcol, a0 + ks * 8, b0 + (off >> 4), idesc, (ci > 0 || ks > 0) ? 1u : 0u);
+            }
+            commit<C::k2, true>(smem_u32(&ctrl->consumed[slot]));
+            if (ends) commit<C::k2, C::k2>(smem_u32(&ctrl->d_full[db]));
           }
-          if (ci == C::kChunk - 1 || i == n - 1) {
-            commit<C::k2, C::k2>(smem_u32(&ctrl->d_full[d % C::kND]));
-            ++d;
+          __syncwarp();
+          if (++slot == C::kX) {
+            slot = 0;
+            slot_par ^= 1u;
           }
-          commit<C::k2, true>(smem_u32(&ctrl->consumed[slot]));
+          if (++ab == kA) ab = 0;
+          if (ends && ++db == C::kND) {
+            db = 0;
+            d_par ^= 1u;
+          }
         }
       }
-      commit<C::k2, false>(smem_u32(&ctrl->mma_done));
+      if (leader) commit<C::k2, false>(smem_u32(&ctrl->mma_done));
+      __syncwarp();
       (void)mbar_wait(smem_u32(&ctrl->mma_done), 0u, drain_ctx, 67);
     }
     __syncwarp();
