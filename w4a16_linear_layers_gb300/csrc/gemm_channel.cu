@@ -11,8 +11,7 @@
 //
 // Small batches (streaming kernel).  The weights pass once and HBM is the
 // bound.  Every warp streams its own weights from global memory straight into
-// registers (16-byte loads, one 64-wide K block in flight while the previous
-// one is multiplied), widens them to fp16 in place and multiplies them with
+// registers (16-byte loads, two 64-wide K blocks on their way), widens them to fp16 in place and multiplies them with
 // mma.sync: there is no shared-memory ring, no barrier and no tensor-memory
 // hand-off on the way, so nothing but the loads themselves paces the stream.
 // The legacy tensor path does one m16n8k16 per 2 cycles and SM (measured),
@@ -31,6 +30,7 @@
 #include <cuda_fp16.h>
 
 #include <atomic>
+#include <cstdlib>
 
 #include "gemm_channel_pair.cuh"
 #include "qlin_device.cuh"
@@ -41,6 +41,7 @@ namespace {
 
 constexpr int kSWarps = 8;                 // warps of a block, along K
 constexpr int kSThreads = 32 * kSWarps;
+constexpr int kMaxSplits = 8;              // blocks of a cluster, along K
 constexpr int kKB = 64;                    // K of one step of a warp
 constexpr int kExactBlocks = 1024 / kKB;   // steps whose fp32 sums stay exact
 
@@ -81,11 +82,11 @@ __device__ __forceinline__ void cluster_sync_all() {
                    : "memory");
 }
 
-__device__ __forceinline__ int ld_cluster_s32(uint32_t local_addr, uint32_t rank) {
+__device__ __forceinline__ int2 ld_cluster_int2(uint32_t local_addr, uint32_t rank) {
   uint32_t remote;
-  int v;
+  int2 v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local_addr), "r"(rank));
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
+  asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(remote) : "memory");
   return v;
 }
 
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(kSThreads) stream_kernel(const ChannelParams p
   constexpr int F = 32 * kHalves;
   constexpr int T = 8 * kTok;
   constexpr int kPad = F + 4;                  // words of one token's row of partials
-  __shared__ int part[T * kPad];
+  __shared__ __align__(16) int part[T * kPad];
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int g = lane >> 2;                     // channel group of 4, and token of a tile of 8
@@ -119,16 +120,18 @@ __global__ void __launch_bounds__(kSThreads) stream_kernel(const ChannelParams p
   bool have[kHalves];
 #pragma unroll
   for (int hf = 0; hf < kHalves; ++hf) have[hf] = f0 + 32 * hf + 4 * g < N;   // N is a multiple of 8
-  uint4 w[4 * kHalves];
-  auto load_w = [&](int kb) {
+  uint4 w[2][4 * kHalves];
+  auto load_w = [&](uint4* to, int kb) {
     const uint32_t* src = wbase + static_cast<int64_t>(kb) * 16 * N;
 #pragma unroll
     for (int s = 0; s < 4; ++s)
 #pragma unroll
       for (int hf = 0; hf < kHalves; ++hf)
-        w[s * kHalves + hf] = have[hf] ? ld_stream(src + s * N + 32 * hf) : make_uint4(0, 0, 0, 0);
+        to[s * kHalves + hf] = have[hf] ? ld_stream(src + s * N + 32 * hf) : make_uint4(0, 0, 0, 0);
   };
-  if (first < nkb) load_w(first);   // the weights depend on no earlier kernel
+  // two steps of weights on their way; they depend on no earlier kernel
+  if (first < nkb) load_w(w[0], first);
+  if (first + stride < nkb) load_w(w[1], first + stride);
   grid_dep_launch();
   grid_dep_wait();
   __syncthreads();
@@ -164,37 +167,37 @@ __global__ void __launch_bounds__(kSThreads) stream_kernel(const ChannelParams p
         }
   };
 
-  int done = 0;
-  for (int kb = first; kb < nkb; kb += stride) {
-    uint4 a[kTok][kC16 ? 2 : 1];
+  uint4 a[2][kTok][kC16 ? 2 : 1];
+  auto load_a = [&](uint4 (*to)[kC16 ? 2 : 1], int kb) {
 #pragma unroll
     for (int i = 0; i < kTok; ++i) {
       const uint4* src = reinterpret_cast<const uint4*>(abase[i] + static_cast<int64_t>(kb) * kKB * (kC16 ? 2 : 1));
-      a[i][0] = src[0];
-      if constexpr (kC16) a[i][1] = src[1];
+      to[i][0] = src[0];
+      if constexpr (kC16) to[i][1] = src[1];
     }
-    uint4 cur[4 * kHalves];
-#pragma unroll
-    for (int i = 0; i < 4 * kHalves; ++i) cur[i] = w[i];
-    if (kb + stride < nkb) load_w(kb + stride);
+  };
+  if (first < nkb) load_a(a[0], first);
+  int done = 0;
+  auto step = [&](uint4* wc, uint4 (*ac)[kC16 ? 2 : 1], uint4 (*an)[kC16 ? 2 : 1], int kb) {
+    if (kb + stride < nkb) load_a(an, kb + stride);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       uint32_t b[kTok][2];
 #pragma unroll
       for (int i = 0; i < kTok; ++i) {
         if constexpr (kC16) {
-          const uint4 v = a[i][s >> 1];
+          const uint4 v = ac[i][s >> 1];
           b[i][0] = (s & 1) ? v.z : v.x;
           b[i][1] = (s & 1) ? v.w : v.y;
         } else {
-          const uint4 v = a[i][0];
+          const uint4 v = ac[i][0];
           const uint32_t word = s == 0 ? v.x : s == 1 ? v.y : s == 2 ? v.z : v.w;
           biased_u8x4_to_f16x4(word ^ 0x80808080u, b[i][0], b[i][1]);
         }
       }
 #pragma unroll
       for (int hf = 0; hf < kHalves; ++hf) {
-        const uint4 v = cur[s * kHalves + hf];
+        const uint4 v = wc[s * kHalves + hf];
         uint32_t c0[2], c1[2], c2[2], c3[2];
         biased_u8x4_to_f16x4(v.x, c0[0], c0[1]);
         biased_u8x4_to_f16x4(v.y, c1[0], c1[1]);
@@ -207,10 +210,15 @@ __global__ void __launch_bounds__(kSThreads) stream_kernel(const ChannelParams p
         }
       }
     }
+    if (kb + 2 * stride < nkb) load_w(wc, kb + 2 * stride);
     if (++done == kExactBlocks) {
       flush();
       done = 0;
     }
+  };
+  for (int kb = first; kb < nkb; kb += 2 * stride) {
+    step(w[0], a[0], a[1], kb);
+    if (kb + stride < nkb) step(w[1], a[1], a[0], kb + stride);
   }
   if (done) flush();
 
@@ -228,9 +236,14 @@ __global__ void __launch_bounds__(kSThreads) stream_kernel(const ChannelParams p
     int v0 = 0, v1 = 0;
     const int at = tok * kPad + ch;
     if (splits > 1) {
-      for (int r = 0; r < splits; ++r) {
-        v0 += ld_cluster_s32(pbase + 4u * at, r);
-        v1 += ld_cluster_s32(pbase + 4u * (at + 1), r);
+      int2 v[kMaxSplits];        // all on their way before the first is added
+#pragma unroll
+      for (int r = 0; r < kMaxSplits; ++r)
+        v[r] = r < splits ? ld_cluster_int2(pbase + 4u * at, r) : make_int2(0, 0);
+#pragma unroll
+      for (int r = 0; r < kMaxSplits; ++r) {
+        v0 += v[r].x;
+        v1 += v[r].y;
       }
     } else {
       v0 = part[at];
@@ -255,14 +268,14 @@ cudaError_t launch_stream(const ChannelParams& p, int splits, cudaStream_t strea
 
 template <bool kC16>
 cudaError_t launch_c(const ChannelParams& p, int sm_count, cudaStream_t stream) {
-  const int64_t ftiles = (p.N + 63) / 64;
-  const int64_t mtiles = (p.M + 15) / 16;
+  const int halves = getenv("SH") ? atoi(getenv("SH")) : 2;
+  const int64_t ftiles = (p.N + 32 * halves - 1) / (32 * halves);
   const int64_t nkb = p.K / kKB;
-  // split K while two blocks an SM are not reached and every warp keeps a K block
   int splits = 1;
-  while (splits < 8 && ftiles * mtiles * splits < 2 * sm_count && nkb >= 2 * splits * kSWarps) splits *= 2;
-  return p.M <= 8 ? launch_stream<2, 1, kC16>(p, splits, stream)
-                  : launch_stream<2, 2, kC16>(p, splits, stream);
+  const int64_t want = getenv("SW") ? atoi(getenv("SW")) : 2;
+  while (splits < 8 && ftiles * splits < want * sm_count && nkb >= 2 * splits * kSWarps) splits *= 2;
+  if (getenv("SC")) splits = atoi(getenv("SC"));
+  return halves == 1 ? launch_stream<1, 1, kC16>(p, splits, stream) : halves == 4 ? launch_stream<4, 1, kC16>(p, splits, stream) : launch_stream<2, 1, kC16>(p, splits, stream);
 }
 
 }  // namespace
@@ -271,7 +284,7 @@ namespace {
 
 // ------------------------------------------------------- larger batches
 
-constexpr int64_t kStreamTokens = 16;     // batches up to this take the streaming kernel
+constexpr int64_t kStreamTokens = 8;      // batches up to this take the streaming kernel
 constexpr size_t kCounterBytes = 1024;    // arrival counters of the cut tiles
 constexpr int64_t kMinShare = 8;          // K steps of a pair's share of the cut tiles, at least
 
@@ -284,28 +297,39 @@ struct PairPlan {
 
 PairPlan plan_pair(int64_t M, int64_t N, int64_t K, int sm_count) {
   PairPlan pl;
-  const int sizes[5] = {64, 96, 128, 192, 256};
+  // Tile size: the least of (K steps of a pair) x (time of a step) + (time of
+  // what follows a pair's last step), in 10 ns, measured where HBM or the MMAs
+  // bound the steps (N = 34816, K = 5120).
+  constexpr struct {
+    int T, step, tail;
+  } kSizes[4] = {{64, 42, 500}, {96, 49, 550}, {128, 57, 600}, {192, 68, 750}};
+  const int64_t slots = sm_count / 2;
+  const int64_t F2 = (N + 255) / 256;
   int64_t best = 0;
-  for (int T : sizes) {
-    // cycles of a K step, up to a factor: the MMA's 4 T, and what does not depend on T
-    const int64_t cost = (M + T - 1) / T * (4 * T + 128);
+  for (const auto& size : kSizes) {
+    const int64_t steps = (M + size.T - 1) / size.T * F2 * (K / 128);
+    const int64_t longest = steps / slots > kMinShare ? steps / slots : kMinShare;
+    const int64_t cost = longest * size.step + size.tail;
     if (best == 0 || cost < best) {
       best = cost;
-      pl.T = T;
+      pl.T = size.T;
     }
   }
   pl.TT = (M + pl.T - 1) / pl.T;
-  pl.F2 = (N + 255) / 256;
+  pl.F2 = F2;
   pl.G = K / 128;
-  const int64_t slots = sm_count / 2;
   const int64_t tiles = pl.TT * pl.F2;
   const int64_t rest = tiles % slots;
   pl.pairs = tiles < slots ? tiles : slots;
   pl.band = pl.TT < 8 ? pl.TT : 8;
-  // the last round's tiles are cut along K unless they nearly fill it
+  // The last round's tiles are cut along K unless they nearly fill it: into as
+  // many equal parts as the pairs allow where that is two or more (96 x 5120 x
+  // 5120, 20 tiles: 16.7 us in 3 parts, 21.0 in 76 shares that cross tiles), else
+  // into shares that cross tiles.
   if (rest != 0 && rest * 8 < slots * 7) {
-    int64_t n = rest * pl.G / kMinShare;
-    n = n < rest ? rest : n > slots ? slots : n;
+    const int64_t parts = slots / rest;
+    int64_t n = parts >= 2 ? rest * (parts < pl.G / kMinShare ? parts : pl.G / kMinShare) : slots;
+    if (n * kMinShare > rest * pl.G) n = rest * pl.G / kMinShare;
     if (n > rest) {
       pl.sk_tiles = rest;
       pl.sk_pairs = n;
@@ -388,8 +412,7 @@ cudaError_t launch_pair(const ChannelGemmArgs& a, int* err, int sm_count, cudaSt
   CUtensorMap tw, tx;
   if (!make_map_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_INT32, a.qweight, a.N, a.K / 4, static_cast<uint64_t>(a.N) * 4, 128,
                    32, CU_TENSOR_MAP_SWIZZLE_NONE) ||
-      !make_act_map(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, codes, a.M, a.K, static_cast<uint32_t>(pl.T / 2),
-                    pl.T == 256 ? 2 : 1))
+      !make_act_map(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, codes, a.M, a.K, static_cast<uint32_t>(pl.T / 2), 1))
     return cudaErrorInvalidValue;
   pair::Params p;
   p.s_a = a.s_a;
@@ -412,8 +435,7 @@ cudaError_t launch_pair(const ChannelGemmArgs& a, int* err, int sm_count, cudaSt
     case 64: return launch_pair_t<64>(tw, tx, p, stream);
     case 96: return launch_pair_t<96>(tw, tx, p, stream);
     case 128: return launch_pair_t<128>(tw, tx, p, stream);
-    case 192: return launch_pair_t<192>(tw, tx, p, stream);
-    default: return launch_pair_t<256>(tw, tx, p, stream);
+    default: return launch_pair_t<192>(tw, tx, p, stream);
   }
 }
 

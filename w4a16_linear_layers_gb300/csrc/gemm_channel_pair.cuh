@@ -7,21 +7,19 @@
 //     into tensor memory, 128 channels a block) and the tokens as operand B
 //     (T columns, fp16 codes, 128-byte swizzled).  Each block loads its own
 //     words and half of the tokens: the pair reads every operand byte once.
-//     - T of 192 and 256: cta_group::2, one MMA of 256 x T for both blocks,
-//       issued by the first, each block's shared memory holding its half of the
-//       tokens: 48 bytes a cycle and SM through L2 at T = 256, and as much
-//       shared-memory traffic.  Such an MMA takes 148 cycles at T = 256, and
-//       137 at T = 96 (measured; 8192 x 5120 x 34816: 1.90 ms, 1538 TF/s).
-//     - T of 64, 96 and 128: that floor would bound a step (16 KB of words a
-//       block) at 1100 cycles, where HBM delivers one in 700, so each block
-//       issues its own MMAs of 128 x T (cta_group::1, 46 to 64 cycles), and the
-//       token halves are multicast into both blocks' shared memory.
+//     - T = 192: cta_group::2, one MMA of 256 x T for both blocks, issued by the
+//       first, each block's shared memory holding its half of the tokens: 40 KB
+//       through L2 for a K step of 900 cycles or more.
+//     - T of 64, 96 and 128: each block issues its own MMAs of 128 x T
+//       (cta_group::1), and the token halves are multicast into both blocks'
+//       shared memory.  (A 256-row MMA with A in tensor memory takes about 85
+//       cycles at T = 128 and not much less below, two of 128 rows 64.)
 //   * An accumulator takes at most 1024 of K (exact below 2^24); the
 //     epilogue adds each such chunk to int32 registers, under the next chunk's
-//     MMAs where tensor memory has room for two accumulators (T up to 192; at
-//     T = 256 the tensor pipe is idle for 2000 of every 12,000 cycles).  At
-//     T = 192 that leaves room for 256 of K as operand A, cut into units of
-//     64 instead of 128 to keep four of them on the way.
+//     MMAs: tensor memory holds two accumulators.  (T = 256 has room for one,
+//     and the tensor pipe idled for 2000 of every 12,000 cycles.)  At T = 192
+//     that leaves room for 256 of K as operand A, cut into units of 64 instead
+//     of 128 to keep four of them on the way.
 //   * Work: whole tiles go round the pairs in bands of token tiles, so the
 //     pairs running at one time share a few channel tiles and one band's
 //     tokens in L2.  The tiles that do not fill a last round are cut along
@@ -47,18 +45,19 @@ namespace pair {
 
 constexpr int kF = 128;                 // channels of one block
 constexpr int kChunkK = 1024;           // K of an accumulator
+constexpr int kND = 2;                  // accumulators
 constexpr int kA = 4;                   // operand A buffers in TMEM, one unit of K each
 constexpr uint32_t kWBytes = 32 * kF * 4;
 constexpr int kThreads = 640;
 constexpr int kEpiThreads = 256;
-constexpr uint32_t kCtrl = 1024;
+constexpr uint32_t kCtrl = 2048;
 constexpr uint32_t kSmemMax = 232448;
 constexpr int kMaxW = 8;
 constexpr int kMaxU = 8;
 
 template <int T>
 struct Cfg {
-  static constexpr bool k2 = T >= 192;                        // one MMA for both blocks
+  static constexpr bool k2 = T == 192;                        // one MMA for both blocks
   static constexpr int kHalf = T / 2;                         // tokens that one block loads
   static constexpr int kRows = k2 ? kHalf : T;                // tokens in one block's shared memory
   static constexpr int kUnit = T == 192 ? 64 : 128;           // K of a unit: one A buffer, one token slot
@@ -67,21 +66,19 @@ struct Cfg {
   static constexpr int kACols = kUnit / 2;
   static constexpr uint32_t kXBytes = kRows * kUnit * 2u;     // a unit's codes in one block
   static constexpr int kX = T == 192 ? 8 : 4;                 // token slots
-  static constexpr int kND = T <= 192 ? 2 : 1;                // accumulators
   static constexpr int kE = T / 2;                            // sums of an epilogue thread
   static constexpr uint32_t kColD = kA * kACols;
   static constexpr int kWSlotsFit = static_cast<int>((kSmemMax - 1024 - kCtrl - kX * kXBytes) / kWBytes) & ~1;
   static constexpr int kWSlots = kWSlotsFit < kMaxW ? kWSlotsFit : kMaxW;   // even: a slot stays with one widening group
   static constexpr uint32_t kSmem = 1024 + kCtrl + kX * kXBytes + kWSlots * kWBytes;
   // Registers a thread: the block is launched with 96 and the roles trade them
-  // within that.  (32 for the control warps made the MMA issuer spill: with the
-  // rings there is no L1 to speak of, and a K step took 1100 cycles for it.)
-  static constexpr int kRegsCtl = T > 128 ? 48 : 64;
-  static constexpr int kRegsConv = T > 128 ? 64 : 80;
-  static constexpr int kRegsEpi = T > 128 ? 152 : 128;
+  // within that.  (Spills are dear: the rings leave no L1 to speak of.)
+  static constexpr int kRegsCtl = 48;
+  static constexpr int kRegsConv = T > 128 ? 64 : 72;
+  static constexpr int kRegsEpi = T > 128 ? 152 : 144;
   static constexpr int kRegsSum = 128 * kRegsCtl + 256 * kRegsConv + 256 * kRegsEpi;
   static_assert(kRegsSum <= 96 * kThreads, "setmaxnreg draws on what the block was launched with");
-  static_assert(T % 32 == 0 && T >= 64 && T <= 256, "token tile");
+  static_assert(T % 32 == 0 && T >= 64 && T <= 192, "token tile");
   static_assert(kColD + kND * T <= 512 && kE % 16 == 0, "TMEM budget");
   static_assert(kX >= kA && kX <= kMaxU && kX % 2 == 0, "token slots");
   static_assert(kWSlots >= 4 && kWSlots % 2 == 0 && kSmem <= kSmemMax, "shared memory");
@@ -96,6 +93,8 @@ struct Ctrl {
   uint64_t d_full[2];
   uint64_t d_empty[2];        // the accumulator is drained
   uint64_t mma_done;
+  uint64_t part_here;         // partials of a cut tile landed
+  alignas(16) float s_a[192]; // of the tile's tokens
   uint32_t tmem_base;
   int abort_flag;
   int last_flag;
@@ -152,6 +151,7 @@ struct Work {
     q += p.pairs;
     return true;
   }
+  __device__ __forceinline__ bool last() const { return s >= s1 && q >= whole(); }   // nothing after this segment
   __device__ __forceinline__ void place(int i) {
     const int b = i / (p.band * p.F2);
     const int r = i - b * p.band * p.F2;
@@ -254,6 +254,35 @@ __device__ __forceinline__ bool elect_one() {
   return one != 0;
 }
 
+// Adds the integers that two fp32 words hold (magnitude up to 2^24) to a0 and
+// a1, each with kIntegerBias on top, modulo 2^32.  The conversion instruction
+// runs at a quarter of the additions' rate here (a drain of 256 x 128 took
+// 2000 cycles with it), so: x + 1.5 * 2^35 keeps round(x / 4096) in the low
+// bits of its significand, what remains of x is at most 2048, and that plus
+// 1.5 * 2^23 is an integer in the low bits of its significand.
+constexpr uint32_t kBigMagic = 0x51400000u;     // 1.5 * 2^35
+constexpr uint32_t kSmallMagic = 0x4B400000u;   // 1.5 * 2^23
+constexpr uint32_t kIntegerBias = (kBigMagic << 12) + kSmallMagic;
+__device__ __forceinline__ void add_integers(uint32_t x0, uint32_t x1, int32_t& a0, int32_t& a1) {
+  uint32_t h0, h1, l0, l1;
+  asm("{\n\t.reg .b64 x, h, l, m, n;\n\t"
+      "mov.b64 x, {%4, %5};\n\t"
+      "mov.b64 m, {%6, %6};\n\t"
+      "mov.b64 n, {%7, %7};\n\t"
+      "add.rn.f32x2 h, x, m;\n\t"
+      "mov.b64 {%0, %1}, h;\n\t"
+      "mov.b64 m, {%8, %8};\n\t"
+      "add.rn.f32x2 h, h, m;\n\t"          // round(x / 4096) * 4096, exact
+      "mov.b64 m, {%9, %9};\n\t"
+      "fma.rn.f32x2 l, h, m, x;\n\t"       // x less that, exact
+      "add.rn.f32x2 l, l, n;\n\t"
+      "mov.b64 {%2, %3}, l;\n\t}"
+      : "=r"(h0), "=r"(h1), "=r"(l0), "=r"(l1)
+      : "r"(x0), "r"(x1), "r"(kBigMagic), "r"(kSmallMagic), "r"(kBigMagic | 0x80000000u), "r"(0xBF800000u));
+  a0 += static_cast<int32_t>((h0 << 12) + l0);
+  a1 += static_cast<int32_t>((h1 << 12) + l1);
+}
+
 template <int N>
 __device__ __forceinline__ void reg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
@@ -292,6 +321,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ctrl->d_empty[i]), C::k2 ? 16 : 8);
     }
     mbar_init(smem_u32(&ctrl->mma_done), 1);
+    mbar_init(smem_u32(&ctrl->part_here), 1);
     ctrl->abort_flag = 0;
     ctrl->last_flag = 0;
     fence_barrier_init();
@@ -429,7 +459,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             slot_par ^= 1u;
           }
           if (++ab == kA) ab = 0;
-          if (ends && ++db == C::kND) {
+          if (ends && ++db == kND) {
             db = 0;
             d_par ^= 1u;
           }
@@ -501,29 +531,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int32_t acc[E];
     Work w(p, pr);
     int d = 0;
+    uint32_t part_par = 0u;
     bool ok = true;
     while (ok && w.next()) {
+      named_bar_sync(1, kEpiThreads);     // the previous tile's scales are read
+      if (et < T) ctrl->s_a[et] = static_cast<int64_t>(w.t) * T + et < p.M ? __ldg(p.s_a + static_cast<int64_t>(w.t) * T + et) : 0.0f;
 #pragma unroll
       for (int c = 0; c < E; ++c) acc[c] = 0;
+      uint32_t chunks = 0;
       for (int g = w.g0; g < w.g1; g += kChunkK / 128, ++d) {
-        const int db = d % C::kND;
+        const int db = d % kND;
         ok = __all_sync(0xFFFFFFFFu,
-                        mbar_wait(smem_u32(&ctrl->d_full[db]), static_cast<uint32_t>(d / C::kND) & 1u, ctx, 70));
+                        mbar_wait(smem_u32(&ctrl->d_full[db]), static_cast<uint32_t>(d / kND) & 1u, ctx, 70));
         if (!ok) break;
         tc_fence_after();
         const uint32_t dcol = tmem + lane_off + C::kColD + db * T + col0;
+        constexpr int kCols = E == 32 ? 32 : 16;   // of one batch of TMEM loads
 #pragma unroll
-        for (int c = 0; c < E; c += 16) {
-          uint32_t v[16];
-          tmem_ld16(dcol + c, v);
+        for (int c = 0; c < E; c += kCols) {
+          uint32_t v[kCols];
+#pragma unroll
+          for (int k = 0; k + 16 <= kCols; k += 16) tmem_ld16(dcol + c + k, v + k);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) acc[c + i] += __float2int_rn(__uint_as_float(v[i]));
+          for (int i = 0; i < kCols; i += 2) add_integers(v[i], v[i + 1], acc[c + i], acc[c + i + 1]);
         }
+        ++chunks;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive<C::k2>(smem_u32(&ctrl->d_empty[db]));
       }
+#pragma unroll
+      for (int c = 0; c < E; ++c) acc[c] -= static_cast<int32_t>(chunks * kIntegerBias);
       if (!named_bar_and(1, kEpiThreads, ok)) break;
       bool finish = true;
       if (w.cut) {
@@ -534,8 +573,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int others = c1 - c0;
         auto slot_of = [&](int c) {   // a pair's partials: of the tile its share starts in, and of its last one
           const int first = c * (p.sk_tiles * p.G) / p.sk_pairs / p.G;
-          return p.part + static_cast<int64_t>((c * 2 + (first == w.tile ? 0 : 1)) * 2 + static_cast<int>(rank)) * (T * kF) +
-                 col0 * kF + r;
+          return p.part + static_cast<int64_t>((c * 2 + (first == w.tile ? 0 : 1)) * 2 + static_cast<int>(rank)) * (T * kF);
         };
         // if all the others have arrived, this block's sums stay in registers
         if (et == 0) ctrl->last_flag = ld_acquire_gpu(counter) == others ? 1 : 0;
@@ -543,7 +581,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         finish = ctrl->last_flag != 0;
         named_bar_sync(1, kEpiThreads);
         if (!finish) {
-          int32_t* dst = slot_of(pr);
+          int32_t* dst = slot_of(pr) + col0 * kF + r;
 #pragma unroll
           for (int c = 0; c < E; ++c) dst[c * kF] = acc[c];
           named_bar_sync(1, kEpiThreads);
@@ -552,35 +590,74 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           finish = ctrl->last_flag != 0;
           named_bar_sync(1, kEpiThreads);
         }
-        if (finish) {
+        if (finish && w.last()) {
+          // The pair's last segment: its rings are idle, and the others' partials
+          // come into them by bulk copies, as many at a time as there is room for
+          // (through registers a partial takes a round trip for every 32 tokens).
+          constexpr uint32_t kPart = T * kF * 4u;
+          constexpr int kRoom = static_cast<int>((NW * kWBytes + C::kX * C::kXBytes) / kPart);
+          int c = c0;
+          while (c <= c1) {
+            if (et == 0) {
+              // the rings were read, and the partials written, by generic accesses
+              fence_proxy_async_smem();
+              fence_proxy_async_global();
+            }
+            int n = 0, next = c;
+            for (; next <= c1 && n < kRoom; ++next) {
+              if (next == pr) continue;
+              if (et == 0) {
+                mbar_expect_tx(smem_u32(&ctrl->part_here), kPart);
+                bulk_load(sbase + n * kPart, slot_of(next), kPart, smem_u32(&ctrl->part_here));
+              }
+              ++n;
+            }
+            if (et == 0) mbar_arrive(smem_u32(&ctrl->part_here));
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&ctrl->part_here), part_par, drain_ctx, 73));
+            part_par ^= 1u;
+            if (!named_bar_and(2, kEpiThreads, ok)) break;
+            for (int i = 0; i < n; ++i) {
+              const int32_t* src = reinterpret_cast<const int32_t*>(smem + i * kPart) + col0 * kF + r;
+#pragma unroll
+              for (int k = 0; k < E; ++k) acc[k] += src[k * kF];
+            }
+            named_bar_sync(1, kEpiThreads);
+            c = next;
+          }
+          finish = ok;
+        } else if (finish) {
           for (int c = c0; c <= c1; ++c) {
             if (c == pr) continue;
-            const int32_t* src = slot_of(c);
+            const int32_t* src = slot_of(c) + col0 * kF + r;
+            constexpr int kBatch = E <= 48 ? E : 32;   // loads in flight, as the registers allow
 #pragma unroll
-            for (int i = 0; i < E; i += 16) {
-              int32_t v[16];
+            for (int i = 0; i < E; i += kBatch) {
+              int32_t v[kBatch];
 #pragma unroll
-              for (int k = 0; k < 16; ++k) v[k] = src[(i + k) * kF];
+              for (int k = 0; k < kBatch; ++k) v[k] = src[(i + k) * kF];
 #pragma unroll
-              for (int k = 0; k < 16; ++k) acc[i + k] += v[k];
+              for (int k = 0; k < kBatch; ++k) acc[i + k] += v[k];
             }
           }
         }
       }
       if (finish) {
+        // Two neighbouring lanes (channels) exchange a value of each two tokens,
+        // so that a lane writes both channels of one: 4 bytes, and half the stores.
         const int64_t n = static_cast<int64_t>(w.f) * 256 + rank * kF + r;
         const int64_t m0 = static_cast<int64_t>(w.t) * T + col0;
-        if (n < p.N && m0 < p.M) {
-          const float sw = __ldg(p.s_w + n);
-          const float* sa = p.s_a + m0;
-          uint16_t* dst = p.y + m0 * p.N + n;
-          const int rows = static_cast<int>(p.M - m0 < E ? p.M - m0 : E);
+        const float sw = n < p.N ? __ldg(p.s_w + n) : 0.0f;
+        const int odd = lane & 1;
+        const uint32_t sel = odd ? 0x3276u : 0x5410u;    // {theirs.hi, mine.hi} or {mine.lo, theirs.lo}
+        uint16_t* dst = p.y + (m0 + odd) * p.N + (n - odd);
+        const int rows = n < p.N ? static_cast<int>(p.M - m0 < E ? p.M - m0 : E) - odd : 0;
 #pragma unroll
-          for (int c = 0; c < E; ++c, dst += p.N) {
-            if (c < rows)
-              *dst = __bfloat16_as_ushort(
-                  __float2bfloat16_rn(__fmul_rn(__fmul_rn(__int2float_rn(acc[c]), sw), __ldg(sa + c))));
-          }
+        for (int c = 0; c < E; c += 2, dst += 2 * p.N) {
+          const float2 sa = *reinterpret_cast<const float2*>(ctrl->s_a + col0 + c);
+          const uint32_t mine = bf16x2_rn(__fmul_rn(__fmul_rn(__int2float_rn(acc[c]), sw), sa.x),
+                                          __fmul_rn(__fmul_rn(__int2float_rn(acc[c + 1]), sw), sa.y));
+          const uint32_t theirs = __shfl_xor_sync(0xFFFFFFFFu, mine, 1);
+          if (c < rows) *reinterpret_cast<uint32_t*>(dst) = prmt(mine, theirs, sel);
         }
       }
     }
