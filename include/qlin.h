@@ -285,7 +285,7 @@ qlin_status_t qlin_gemm_w8a8_gs128_noalloc(const int8_t *q_a, const float *s_a,
  *   workspace / workspace_bytes  at least
  *            qlin_gemm_w8a8_ch_workspace_bytes(M, N, K, c16) bytes on the
  *            current device, c16 being 1 for the _c16 entry and 0 for the
- *            int8 one; may be NULL where that is 0 (up to 16 rows).  It needs
+ *            int8 one; may be NULL where that is 0 (small problems).  It needs
  *            no zeroing and holds nothing between calls.  Calls that share a
  *            workspace must not overlap.
  *

@@ -11,16 +11,17 @@
 //
 // Small batches (streaming kernel).  The weights pass once and HBM is the
 // bound.  Every warp streams its own weights from global memory straight into
-// registers (16-byte loads, two 64-wide K blocks on their way), widens them to fp16 in place and multiplies them with
-// mma.sync: there is no shared-memory ring, no barrier and no tensor-memory
-// hand-off on the way, so nothing but the loads themselves paces the stream.
-// The legacy tensor path does one m16n8k16 per 2 cycles and SM (measured),
-// 256 weight bytes x 8 tokens; HBM delivers 256 bytes per 11 cycles and SM, so
-// up to 32 tokens (4 products per 256 bytes) it has room to spare.  (The int8
-// form, m16n8k32, takes 16 cycles here.)
-//   * A block's 8 warps share 64 output channels and interleave the 64-wide
-//     K blocks between them; a cluster of up to 8 blocks splits K further where
-//     the channels alone do not fill the machine.  Partials are integers:
+// registers (16-byte loads, two 64-wide K blocks on their way), widens them to
+// fp16 in place and multiplies them with mma.sync: there is no shared-memory
+// ring, no barrier and no tensor-memory hand-off on the way, so nothing but the
+// loads themselves paces the stream.  The legacy tensor path does one m16n8k16
+// per 2 cycles and SM (measured), 256 weight bytes x 8 tokens; HBM delivers 256
+// bytes per 11 cycles and SM, so for 8 tokens it has room to spare.  (The int8
+// form, m16n8k32, takes 16 cycles here.)  Measured at 8 x 5120 x 34816: 32.4 us,
+// 5.5 TB/s, 0.81 of the copy rate; 1 x 5120 x 248320: 208 us, 0.90.
+//   * A block's 8 warps share 32 or 64 output channels and interleave the 64-
+//     wide K blocks between them; a cluster of up to 8 blocks splits K further
+//     where the channels alone do not fill the machine.  Partials are integers:
 //     they meet in shared memory by atomic addition, and across the cluster
 //     through distributed shared memory, in any order with one result.
 //   * K inside a block is permuted so that a thread's 16 codes of a token are
@@ -30,7 +31,6 @@
 #include <cuda_fp16.h>
 
 #include <atomic>
-#include <cstdlib>
 
 #include "gemm_channel_pair.cuh"
 #include "qlin_device.cuh"
@@ -94,11 +94,11 @@ __device__ __forceinline__ uint16_t channel_out(int p, float sw, float sa) {
   return __bfloat16_as_ushort(__float2bfloat16_rn(__fmul_rn(__fmul_rn(__int2float_rn(p), sw), sa)));
 }
 
-// kHalves x 32 output channels and 8 kTok tokens a block.
-template <int kHalves, int kTok, bool kC16>
-__global__ void __launch_bounds__(kSThreads) stream_kernel(const ChannelParams p, int splits) {
+// kHalves x 32 output channels and 8 tokens a block.
+template <int kHalves, bool kC16>
+__global__ void __launch_bounds__(kSThreads, kHalves == 1 ? 3 : 2) stream_kernel(const ChannelParams p, int splits) {
   constexpr int F = 32 * kHalves;
-  constexpr int T = 8 * kTok;
+  constexpr int T = 8;
   constexpr int kPad = F + 4;                  // words of one token's row of partials
   __shared__ __align__(16) int part[T * kPad];
   const int warp = threadIdx.x >> 5;
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kSThreads) stream_kernel(const ChannelParams p
 #pragma unroll
   for (int hf = 0; hf < kHalves; ++hf) have[hf] = f0 + 32 * hf + 4 * g < N;   // N is a multiple of 8
   uint4 w[2][4 * kHalves];
-  auto load_w = [&](uint4* to, int kb) {
+  auto load_w = [&](uint4 (&to)[4 * kHalves], int kb) {
     const uint32_t* src = wbase + static_cast<int64_t>(kb) * 16 * N;
 #pragma unroll
     for (int s = 0; s < 4; ++s)
@@ -136,65 +136,52 @@ __global__ void __launch_bounds__(kSThreads) stream_kernel(const ChannelParams p
   grid_dep_wait();
   __syncthreads();
 
-  const char* abase[kTok];
-#pragma unroll
-  for (int i = 0; i < kTok; ++i) {
-    int64_t m = m0 + 8 * i + g;
-    if (m >= p.M) m = p.M - 1;      // computed and not written
-    abase[i] = static_cast<const char*>(p.act) + (m * K + 16 * t) * (kC16 ? 2 : 1);
-  }
+  // this thread's token (the last one again past it: computed and not written)
+  const int64_t mine = m0 + g < p.M ? m0 + g : p.M - 1;
+  const char* abase = static_cast<const char*>(p.act) + (mine * K + 16 * t) * (kC16 ? 2 : 1);
+  uint4 a[2][kC16 ? 2 : 1];
+  auto load_a = [&](uint4 (&to)[kC16 ? 2 : 1], int kb) {
+    const uint4* src = reinterpret_cast<const uint4*>(abase + static_cast<int64_t>(kb) * kKB * (kC16 ? 2 : 1));
+    to[0] = src[0];
+    if constexpr (kC16) to[1] = src[1];
+  };
+  if (first < nkb) load_a(a[0], first);
 
-  float acc[2 * kHalves][kTok][4];
+  float acc[2 * kHalves][4];
 #pragma unroll
   for (int j = 0; j < 2 * kHalves; ++j)
 #pragma unroll
-    for (int i = 0; i < kTok; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[j][i][e] = 0.0f;
-
+    for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
   auto flush = [&]() {
 #pragma unroll
     for (int j = 0; j < 2 * kHalves; ++j)
 #pragma unroll
-      for (int i = 0; i < kTok; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          // row of the 16 x 8 result: channel 4g + 2 (j & 1) + (e >> 1); column: token 2t + (e & 1)
-          const int ch = 32 * (j >> 1) + 4 * g + 2 * (j & 1) + (e >> 1);
-          const int tok = 8 * i + 2 * t + (e & 1);
-          atomicAdd(&part[tok * kPad + ch], __float2int_rn(acc[j][i][e]));
-          acc[j][i][e] = 0.0f;
-        }
+      for (int e = 0; e < 4; ++e) {
+        // row of the 16 x 8 result: channel 4g + 2 (j & 1) + (e >> 1); column: token 2t + (e & 1)
+        const int ch = 32 * (j >> 1) + 4 * g + 2 * (j & 1) + (e >> 1);
+        atomicAdd(&part[(2 * t + (e & 1)) * kPad + ch], __float2int_rn(acc[j][e]));
+        acc[j][e] = 0.0f;
+      }
   };
 
-  uint4 a[2][kTok][kC16 ? 2 : 1];
-  auto load_a = [&](uint4 (*to)[kC16 ? 2 : 1], int kb) {
-#pragma unroll
-    for (int i = 0; i < kTok; ++i) {
-      const uint4* src = reinterpret_cast<const uint4*>(abase[i] + static_cast<int64_t>(kb) * kKB * (kC16 ? 2 : 1));
-      to[i][0] = src[0];
-      if constexpr (kC16) to[i][1] = src[1];
-    }
-  };
-  if (first < nkb) load_a(a[0], first);
   int done = 0;
-  auto step = [&](uint4* wc, uint4 (*ac)[kC16 ? 2 : 1], uint4 (*an)[kC16 ? 2 : 1], int kb) {
+  auto step = [&](uint4 (&wc)[4 * kHalves], uint4 (&ac)[kC16 ? 2 : 1], uint4 (&an)[kC16 ? 2 : 1], int kb) {
+    uint32_t b[4][2];          // the token's codes, 4 of K for each product
+    if constexpr (kC16) {
+      const uint32_t c[8] = {ac[0].x, ac[0].y, ac[0].z, ac[0].w, ac[1].x, ac[1].y, ac[1].z, ac[1].w};
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        b[s][0] = c[2 * s];
+        b[s][1] = c[2 * s + 1];
+      }
+    } else {
+      const uint32_t c[4] = {ac[0].x, ac[0].y, ac[0].z, ac[0].w};
+#pragma unroll
+      for (int s = 0; s < 4; ++s) biased_u8x4_to_f16x4(c[s] ^ 0x80808080u, b[s][0], b[s][1]);
+    }
     if (kb + stride < nkb) load_a(an, kb + stride);
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      uint32_t b[kTok][2];
-#pragma unroll
-      for (int i = 0; i < kTok; ++i) {
-        if constexpr (kC16) {
-          const uint4 v = ac[i][s >> 1];
-          b[i][0] = (s & 1) ? v.z : v.x;
-          b[i][1] = (s & 1) ? v.w : v.y;
-        } else {
-          const uint4 v = ac[i][0];
-          const uint32_t word = s == 0 ? v.x : s == 1 ? v.y : s == 2 ? v.z : v.w;
-          biased_u8x4_to_f16x4(word ^ 0x80808080u, b[i][0], b[i][1]);
-        }
-      }
+    for (int s = 0; s < 4; ++s)
 #pragma unroll
       for (int hf = 0; hf < kHalves; ++hf) {
         const uint4 v = wc[s * kHalves + hf];
@@ -203,13 +190,9 @@ __global__ void __launch_bounds__(kSThreads) stream_kernel(const ChannelParams p
         biased_u8x4_to_f16x4(v.y, c1[0], c1[1]);
         biased_u8x4_to_f16x4(v.z, c2[0], c2[1]);
         biased_u8x4_to_f16x4(v.w, c3[0], c3[1]);
-#pragma unroll
-        for (int i = 0; i < kTok; ++i) {
-          mma_f16(acc[2 * hf][i], c0[0], c1[0], c0[1], c1[1], b[i][0], b[i][1]);
-          mma_f16(acc[2 * hf + 1][i], c2[0], c3[0], c2[1], c3[1], b[i][0], b[i][1]);
-        }
+        mma_f16(acc[2 * hf], c0[0], c1[0], c0[1], c1[1], b[s][0], b[s][1]);
+        mma_f16(acc[2 * hf + 1], c2[0], c3[0], c2[1], c3[1], b[s][0], b[s][1]);
       }
-    }
     if (kb + 2 * stride < nkb) load_w(wc, kb + 2 * stride);
     if (++done == kExactBlocks) {
       flush();
@@ -257,25 +240,31 @@ __global__ void __launch_bounds__(kSThreads) stream_kernel(const ChannelParams p
   if (splits > 1) cluster_sync_all();   // no block leaves while another reads its partials
 }
 
-template <int kHalves, int kTok, bool kC16>
+template <int kHalves, bool kC16>
 cudaError_t launch_stream(const ChannelParams& p, int splits, cudaStream_t stream) {
   const int64_t ftiles = (p.N + 32 * kHalves - 1) / (32 * kHalves);
-  const int64_t mtiles = (p.M + 8 * kTok - 1) / (8 * kTok);
-  return launch_cluster_pdl(stream_kernel<kHalves, kTok, kC16>,
-                            dim3(static_cast<unsigned>(ftiles * splits), static_cast<unsigned>(mtiles)),
+  return launch_cluster_pdl(stream_kernel<kHalves, kC16>,
+                            dim3(static_cast<unsigned>(ftiles * splits), static_cast<unsigned>((p.M + 7) / 8)),
                             dim3(kSThreads), 0, splits, stream, p, splits);
 }
 
 template <bool kC16>
 cudaError_t launch_c(const ChannelParams& p, int sm_count, cudaStream_t stream) {
-  const int halves = getenv("SH") ? atoi(getenv("SH")) : 2;
-  const int64_t ftiles = (p.N + 32 * halves - 1) / (32 * halves);
+  // 32 channels a block while all blocks run at one time (three an SM), K split
+  // as far as that holds and a warp's steps get fewer: at K = 5120, N = 5120 in 2
+  // parts 8.3 us (1 part 12.1, 5 parts 10.0), N = 10240 unsplit 12.8 (2 parts
+  // 16.6; 64 channels 17.2).  Blocks beyond one round of them cost more than
+  // they hide, so above that 64 channels, unsplit: N = 34816 32.6 us (32
+  // channels 38).
+  const int64_t tiles = (p.N + 31) / 32 * ((p.M + 7) / 8);
+  const int64_t slots = 3LL * sm_count;
+  if (tiles > slots) return launch_stream<2, kC16>(p, 1, stream);
   const int64_t nkb = p.K / kKB;
-  int splits = 1;
-  const int64_t want = getenv("SW") ? atoi(getenv("SW")) : 2;
-  while (splits < 8 && ftiles * splits < want * sm_count && nkb >= 2 * splits * kSWarps) splits *= 2;
-  if (getenv("SC")) splits = atoi(getenv("SC"));
-  return halves == 1 ? launch_stream<1, 1, kC16>(p, splits, stream) : halves == 4 ? launch_stream<4, 1, kC16>(p, splits, stream) : launch_stream<2, 1, kC16>(p, splits, stream);
+  int64_t most = slots / tiles;
+  if (most > kMaxSplits) most = kMaxSplits;
+  const int64_t steps = (nkb + kSWarps * most - 1) / (kSWarps * most);
+  const int64_t splits = (nkb + kSWarps * steps - 1) / (kSWarps * steps);
+  return launch_stream<1, kC16>(p, static_cast<int>(splits), stream);
 }
 
 }  // namespace
@@ -284,7 +273,16 @@ namespace {
 
 // ------------------------------------------------------- larger batches
 
-constexpr int64_t kStreamTokens = 8;      // batches up to this take the streaming kernel
+// Batches that take the streaming kernel: up to 8 tokens always, and more
+// where its pass over the weights for each 8 tokens (1.5 us and 5.2 MB a us)
+// takes less than the pairs' launch and pipeline (4.5 us and 1 us for 600 of
+// K): 16 x 5120 x 5120 11.9 us against 14.7, 32 x 5120 x 1024 6.2 against 12.3;
+// but 16 x 5120 x 10240 23.7 against 19.8, 32 x 1024 x 8192 7.9 against 6.3.
+bool streams(int64_t M, int64_t N, int64_t K) {
+  const int64_t passes = (M + 7) / 8;
+  return passes == 1 || (passes <= 64 && passes * N * K <= 15600000 + 8667 * K);
+}
+
 constexpr size_t kCounterBytes = 1024;    // arrival counters of the cut tiles
 constexpr int64_t kMinShare = 8;          // K steps of a pair's share of the cut tiles, at least
 
@@ -442,13 +440,13 @@ cudaError_t launch_pair(const ChannelGemmArgs& a, int* err, int sm_count, cudaSt
 }  // namespace
 
 size_t channel_workspace_bytes(int64_t M, int64_t N, int64_t K, bool c16, int sm_count) {
-  if (M <= kStreamTokens) return 0;
+  if (streams(M, N, K)) return 0;
   const PairPlan pl = plan_pair(M, N, K, sm_count);
   return (pl.cut ? kCounterBytes + pl.part_bytes : 0) + (c16 ? 0 : image_bytes(M, K));
 }
 
 cudaError_t launch_gemm_channel(const ChannelGemmArgs& a, int* err, int sm_count, cudaStream_t stream) {
-  if (a.M > kStreamTokens) return launch_pair(a, err, sm_count, stream);
+  if (!streams(a.M, a.N, a.K)) return launch_pair(a, err, sm_count, stream);
   const ChannelParams p{a.act, a.s_a, reinterpret_cast<const uint32_t*>(a.qweight), a.s_w, a.y, a.M, a.N, a.K};
   return a.act_c16 ? launch_c<true>(p, sm_count, stream) : launch_c<false>(p, sm_count, stream);
 }
