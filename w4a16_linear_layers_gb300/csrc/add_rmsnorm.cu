@@ -8,24 +8,26 @@
 //
 // Exactness.  h, t, z, s and q are the values that the definition gives in
 // exact arithmetic with its roundings (h, t, z to bf16; s and z / s to fp32):
-//   * x + r in fp32 rounds to the bf16 value nearest the exact sum: two bf16
-//     values whose exponents differ by 16 or less add exactly in fp32, and
-//     with a larger difference the sum is far from a bf16 halfway point;
+//   * x + r and gamma * t are one bf16 instruction each, rounded once;
 //   * the squares of bf16 values are exact in fp32 and are added with TwoSum
 //     (Knuth), the dropped parts kept in a second sum;
 //   * rstd is an unevaluated pair of fp32 values (relative error about 2^-44,
-//     by a Newton-Raphson step on rsqrtf's result): x * rstd is formed in fp32
-//     and, where that value lies within 4 fp32 ulps of a bf16 halfway point
-//     (it is within 2 of the exact one), the side is decided with the
-//     product's remainder;
-//   * codes come from the row's reciprocal scale and, next to a half-integer,
-//     from the IEEE divide.
+//     by a Newton-Raphson step on rsqrtf's result).  h * rstd is rounded to
+//     bf16 from two fp32 products, one with a slightly larger and one with a
+//     slightly smaller factor: rounding is monotonic, so where both give the same
+//     bf16 value it is the exact product's, and elsewhere (one element in
+//     8192) the side is decided with the product's remainder;
+//   * codes come from the row's reciprocal scale in the same way, and next to
+//     a half-integer from the IEEE divide.
 // No binary64 arithmetic: this part runs it at 1/64 of the fp32 rate.
 //
-// What bounds it: HBM at many rows (7 or 8 bytes an element); two block-wide
-// reductions and the launch at few.  The elementwise arithmetic runs two
-// elements to an instruction (add / mul.rn.f32x2), without which instruction
-// issue would bind before HBM.
+// What bounds it: HBM at many rows (7 or 8 bytes an element), with instruction
+// issue close behind, which the two-element instructions (f32x2, bf16x2) are
+// for (27 warp instructions for 32 elements); two block-wide reductions and
+// the launch at few.  8192 x 5120: 55.4 us with fp16 codes, 6.06 TB/s, 0.89 of
+// the copy rate (39 instructions took 62.7).  (A ring of rows filled ahead by
+// bulk copies was slower, 74 us against 62 then: many small blocks already
+// overlap one row's loads with another's reductions.)
 #include <cuda_bf16.h>
 
 #include "qlin_device.cuh"
@@ -54,8 +56,13 @@ __device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-__device__ __forceinline__ f32x2 neg2(f32x2 a) { return a ^ 0x8000000080000000ull; }
-__device__ __forceinline__ f32x2 sub2(f32x2 a, f32x2 b) { return add2(a, neg2(b)); }
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+// a - b, rounded once (a subtraction has no form for two elements)
+__device__ __forceinline__ f32x2 sub2(f32x2 a, f32x2 b) { return fma2(b, 0xBF800000BF800000ull, a); }
 
 // bf16x2 word -> its two values in fp32
 __device__ __forceinline__ f32x2 widen2(uint32_t w) {
@@ -67,14 +74,17 @@ __device__ __forceinline__ uint32_t narrow2(f32x2 v) {
   return bf16x2_rn(lo, hi);
 }
 
-// (s, c) += v, c collecting what each addition to s drops (TwoSum)
-__device__ __forceinline__ void twosum2(f32x2& s, f32x2& c, f32x2 v) {
-  const f32x2 t = add2(s, v);
-  const f32x2 bp = sub2(t, s);
-  const f32x2 ap = sub2(t, bp);
-  c = add2(c, add2(sub2(s, ap), sub2(v, bp)));
+// (s, c) += h * h, c collecting what each addition to s drops (TwoSum, with
+// the exact square inside the multiply-adds)
+__device__ __forceinline__ void add_square2(f32x2& s, f32x2& c, f32x2 h) {
+  const f32x2 t = fma2(h, h, s);
+  const f32x2 nb = sub2(s, t);                 // -(t - s)
+  const f32x2 ds = sub2(s, add2(t, nb));
+  const f32x2 dv = fma2(h, h, nb);
+  c = add2(c, add2(ds, dv));
   s = t;
 }
+// (s, c) += v
 __device__ __forceinline__ void twosum1(float& s, float& c, float v) {
   const float t = __fadd_rn(s, v);
   const float bp = __fsub_rn(t, s);
@@ -127,49 +137,58 @@ __device__ __noinline__ uint32_t norm_border(float x, Rstd rs) {
   return (base + (base & 1u)) & 0xFFFFu;
 }
 
-// Non-zero when either fp32 value of the pair may lie within 4 ulps of a bf16
-// halfway point (low 16 bits 0x7FFC .. 0x8003; a carry between the halves
-// moves the upper window by one, which stays wider than the 2 ulps needed).
-__device__ __forceinline__ uint32_t near_half2(f32x2 v) {
-  float lo, hi;
-  unpack2(v, lo, hi);
-  const uint32_t w = prmt(__float_as_uint(lo), __float_as_uint(hi), 0x5410u) + 0x00040004u;
-  const uint32_t y = (w & 0xFFF8FFF8u) ^ 0x80008000u;
-  return (y - 0x00010001u) & ~y & 0x80008000u;
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
 
-// z of one bf16x2 word of h
-__device__ __noinline__ uint32_t norm_pair_slow(uint32_t h, uint32_t g, Rstd rs) {
+// t of one bf16x2 word of h, with the products' remainders
+__device__ __noinline__ uint32_t norm_pair_slow(uint32_t h, Rstd rs) {
   const uint32_t t0 = norm_border(__uint_as_float(h << 16), rs);
   const uint32_t t1 = norm_border(__uint_as_float(h & 0xFFFF0000u), rs);
-  return narrow2(mul2(widen2(t0 | (t1 << 16)), widen2(g)));
+  return t0 | (t1 << 16);
 }
 
-__device__ __forceinline__ uint4 norm8(uint4 h, uint4 g, Rstd rs, f32x2 hi2) {
+// A factor and its bounds 1 +- 2^-22: the fp32 rounding of the factor and of a
+// product with it stay inside.
+struct Bracket {
+  f32x2 up, down;
+  __device__ __forceinline__ explicit Bracket(float f) {
+    const float u = __fmul_rn(f, 1.0f + 0x1p-22f), d = __fmul_rn(f, 1.0f - 0x1p-22f);
+    up = pack2(u, u);
+    down = pack2(d, d);
+  }
+};
+
+__device__ __forceinline__ uint4 norm8(uint4 h, uint4 g, Rstd rs, const Bracket& b) {
   const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
   const uint32_t gw[4] = {g.x, g.y, g.z, g.w};
-  uint32_t z[4];
-  uint32_t border = 0;
+  uint32_t t[4];
+  uint32_t differ = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const f32x2 t = mul2(widen2(hw[i]), hi2);
-    border |= near_half2(t);
-    // the product of two bf16 values is exact in fp32: one rounding
-    z[i] = narrow2(mul2(widen2(narrow2(t)), widen2(gw[i])));
+    const f32x2 f = widen2(hw[i]);
+    t[i] = narrow2(mul2(f, b.up));
+    differ |= t[i] ^ narrow2(mul2(f, b.down));
   }
-  if (border) {
+  if (differ) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) z[i] = norm_pair_slow(hw[i], gw[i], rs);
+    for (int i = 0; i < 4; ++i) t[i] = norm_pair_slow(hw[i], rs);
   }
-  return make_uint4(z[0], z[1], z[2], z[3]);
+  return make_uint4(mul_bf16x2(t[0], gw[0]), mul_bf16x2(t[1], gw[1]), mul_bf16x2(t[2], gw[2]), mul_bf16x2(t[3], gw[3]));
 }
 
+// magnitudes of the larger ones (signs to be ignored)
 __device__ __forceinline__ uint32_t absmax2(uint32_t m, uint32_t v) {
-  const __nv_bfloat162 a = *reinterpret_cast<const __nv_bfloat162*>(&m);
-  const uint32_t av = v & 0x7FFF7FFFu;
-  const __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162*>(&av);
-  const __nv_bfloat162 r = __hmax2(a, b);
-  return *reinterpret_cast<const uint32_t*>(&r);
+  uint32_t d;
+  asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(m), "r"(v));
+  return d;
 }
 
 constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23: t + kMagic rounds t to an integer
@@ -186,29 +205,24 @@ __device__ __noinline__ void quant8_div(uint4 z, float s, float* r) {
   for (int i = 0; i < 8; ++i) r[i] = fminf(fmaxf(r[i], -127.0f), 127.0f);
 }
 
-// Stores 8 codes.  inv = 1 / s: t = z * inv is within 2^-16 of z / s (|t| <=
-// 127), so further than 2^-15 from a half-integer t rounds as the IEEE
-// quotient does; nearer, the divide is taken.  `divide` takes it always
-// (scales whose reciprocal overflows).
+// Stores 8 codes: z / s rounded to an integer by adding kMagic, with the
+// bounds of 1 / s; where they disagree (next to a half-integer) by the divide.
+// `divide` takes it always (scales whose reciprocal overflows).
 template <bool kC16>
-__device__ __forceinline__ void quant_store8(uint4 z, float s, float inv, bool divide, void* qrow,
+__device__ __forceinline__ void quant_store8(uint4 z, float s, const Bracket& inv, bool divide, void* qrow,
                                              int64_t v) {
   const uint32_t w[4] = {z.x, z.y, z.z, z.w};
-  const f32x2 inv2 = pack2(inv, inv);
   const f32x2 magic2 = pack2(kMagic, kMagic);
   float m[8];       // r + kMagic
-  float far = 0.0f; // largest |t - r|
+  f32x2 differ = divide ? 1ull : 0ull;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const f32x2 t = mul2(widen2(w[i]), inv2);
-    const f32x2 mm = add2(t, magic2);
-    const f32x2 d = sub2(t, sub2(mm, magic2));
-    float d0, d1;
-    unpack2(d, d0, d1);
-    far = fmaxf(far, fmaxf(fabsf(d0), fabsf(d1)));
-    unpack2(mm, m[2 * i], m[2 * i + 1]);
+    const f32x2 f = widen2(w[i]);
+    const f32x2 up = fma2(f, inv.up, magic2);
+    differ |= up ^ fma2(f, inv.down, magic2);
+    unpack2(up, m[2 * i], m[2 * i + 1]);
   }
-  if (divide || far > 0.5f - 0x1p-15f) {
+  if (differ) {
     float r[8];
     quant8_div(z, s, r);
 #pragma unroll
@@ -218,7 +232,8 @@ __device__ __forceinline__ void quant_store8(uint4 z, float s, float inv, bool d
     uint32_t o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float r0 = m[2 * i] - kMagic, r1 = m[2 * i + 1] - kMagic;   // -0 becomes +0
+      float r0, r1;
+      unpack2(add2(pack2(m[2 * i], m[2 * i + 1]), pack2(-kMagic, -kMagic)), r0, r1);   // -0 has become +0
       asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[i]) : "f"(r1), "f"(r0));
     }
     reinterpret_cast<uint4*>(qrow)[v] = make_uint4(o[0], o[1], o[2], o[3]);
@@ -236,17 +251,13 @@ __device__ __forceinline__ void quant_store8(uint4 z, float s, float inv, bool d
 }
 
 __device__ __forceinline__ uint4 add8(uint4 x, uint4 r) {
-  return make_uint4(narrow2(add2(widen2(x.x), widen2(r.x))), narrow2(add2(widen2(x.y), widen2(r.y))),
-                    narrow2(add2(widen2(x.z), widen2(r.z))), narrow2(add2(widen2(x.w), widen2(r.w))));
+  return make_uint4(add_bf16x2(x.x, r.x), add_bf16x2(x.y, r.y), add_bf16x2(x.z, r.z), add_bf16x2(x.w, r.w));
 }
 
 __device__ __forceinline__ void sumsq8(uint4 h, f32x2& s, f32x2& c) {
   const uint32_t w[4] = {h.x, h.y, h.z, h.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const f32x2 f = widen2(w[i]);
-    twosum2(s, c, mul2(f, f));
-  }
+  for (int i = 0; i < 4; ++i) add_square2(s, c, widen2(w[i]));
 }
 
 struct AddNormParams {
@@ -297,7 +308,7 @@ __device__ __forceinline__ Rstd block_rstd(f32x2 s2, f32x2 c2, float2* red, cons
 }
 
 __device__ __forceinline__ float block_absmax(uint32_t m2, uint32_t* red) {
-  uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);   // non-negative bf16 bits order as integers
+  uint32_t m = max(m2 & 0x7FFFu, m2 >> 16 & 0x7FFFu);   // non-negative bf16 bits order as integers
   m = __reduce_max_sync(0xFFFFFFFFu, m);
   const int nw = blockDim.x >> 5;
   if (nw > 1) {
@@ -311,8 +322,8 @@ __device__ __forceinline__ float block_absmax(uint32_t m2, uint32_t* red) {
 
 // One block per row, kVec vectors of 8 elements a thread (blockDim * kVec >=
 // K / 8): the row stays in registers from its one read to the codes.
-template <int kVec, bool kC16>
-__global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const AddNormParams p) {
+template <int kVec, int kMaxThreads, int kMinBlocks, bool kC16>
+__global__ void __launch_bounds__(kMaxThreads, kMinBlocks) add_rmsnorm_kernel(const AddNormParams p) {
   __shared__ float2 red[32];
   __shared__ uint32_t redm[32];
   grid_dep_wait();     // x and r come from earlier kernels, which may still read h or q
@@ -350,13 +361,13 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const AddNormParams p
     sumsq8(h[i], s2, c2);
   }
   const Rstd rs = block_rstd(s2, c2, red, p);
-  const f32x2 hi2 = pack2(rs.hi, rs.hi);
+  const Bracket norm(rs.hi);
   uint32_t m2 = 0;
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
     const int v = tid + i * step;
     if (v < nvec) {
-      h[i] = norm8(h[i], __ldg(gr + v), rs, hi2);
+      h[i] = norm8(h[i], __ldg(gr + v), rs, norm);
       m2 = absmax2(absmax2(absmax2(absmax2(m2, h[i].x), h[i].y), h[i].z), h[i].w);
       if (yr) yr[v] = h[i];
     }
@@ -365,7 +376,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const AddNormParams p
   const float s = __fdiv_rn(amax, 127.0f);
   if (tid == 0) p.s[blockIdx.x] = s;
   const bool zero = amax == 0.0f;
-  const float inv = zero ? 0.0f : __frcp_rn(s);
+  const Bracket inv(zero ? 0.0f : __frcp_rn(s));
   const bool divide = !zero && !(s >= 0x1p-120f);
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
@@ -398,10 +409,10 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_long_kernel(const AddNormPar
     sumsq8(h, s2, c2);
   }
   const Rstd rs = block_rstd(s2, c2, red, p);
-  const f32x2 hi2 = pack2(rs.hi, rs.hi);
+  const Bracket norm(rs.hi);
   uint32_t m2 = 0;
   for (int64_t v = threadIdx.x; v < nvec; v += blockDim.x) {
-    const uint4 z = norm8(hr[v], __ldg(gr + v), rs, hi2);   // this thread's own store
+    const uint4 z = norm8(hr[v], __ldg(gr + v), rs, norm);   // this thread's own store
     m2 = absmax2(absmax2(absmax2(absmax2(m2, z.x), z.y), z.z), z.w);
     if (yr) yr[v] = z;
   }
@@ -409,10 +420,10 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_long_kernel(const AddNormPar
   const float s = __fdiv_rn(amax, 127.0f);
   if (threadIdx.x == 0) p.s[blockIdx.x] = s;
   const bool zero = amax == 0.0f;
-  const float inv = zero ? 0.0f : __frcp_rn(s);
+  const Bracket inv(zero ? 0.0f : __frcp_rn(s));
   const bool divide = !zero && !(s >= 0x1p-120f);
   for (int64_t v = threadIdx.x; v < nvec; v += blockDim.x)
-    quant_store8<kC16>(norm8(hr[v], __ldg(gr + v), rs, hi2), s, inv, divide, qr, v);
+    quant_store8<kC16>(norm8(hr[v], __ldg(gr + v), rs, norm), s, inv, divide, qr, v);
 }
 
 template <bool kC16>
@@ -424,14 +435,21 @@ cudaError_t launch_rows(const AddNormParams& p, int64_t M, int sm_count, cudaStr
   auto threads = [&](int vec) {
     return dim3(static_cast<unsigned>((((nvec + vec - 1) / vec) + 31) / 32 * 32));
   };
-  // One vector a thread while every row has an SM of its own (the row's
-  // latency is the call's) and the row fits 1024 threads; else four, whose
-  // blocks are small enough for several rows to share an SM.
-  if (M <= sm_count && nvec <= 1024)
-    return launch_pdl(add_rmsnorm_kernel<1, kC16>, grid, threads(1), 0, stream, p);
-  if (M <= sm_count && nvec <= 2048)
-    return launch_pdl(add_rmsnorm_kernel<2, kC16>, grid, threads(2), 0, stream, p);
-  return launch_pdl(add_rmsnorm_kernel<4, kC16>, grid, threads(4), 0, stream, p);
+  auto launch = [&](auto kernel, int vec) { return launch_pdl(kernel, grid, threads(vec), 0, stream, p); };
+  // As few vectors a thread as the row's threads allow while every row has an
+  // SM of its own (the row's latency is the call's).
+  if (M <= sm_count && nvec <= 1024) return launch(add_rmsnorm_kernel<1, 1024, 1, kC16>, 1);
+  if (M <= sm_count && nvec <= 2048) return launch(add_rmsnorm_kernel<2, 1024, 1, kC16>, 2);
+  // Two while all rows' blocks run at one time (512 x 5120: 7.6 us, with four
+  // 9.8) and for short rows (8192 x 2048: 24.9 and 26.6); else four, which
+  // share the reductions' instructions (8192 x 5120: 55.4, with two 57.6).
+  if (nvec <= 320 || (nvec <= 640 && M <= 4 * static_cast<int64_t>(sm_count)))
+    return launch(add_rmsnorm_kernel<2, 320, 4, kC16>, 2);
+  // Blocks of 288 to 576 threads within 56 registers a thread, so that two
+  // share an SM: 4096 x 17408 99.6 us, one an SM 120.7; shorter rows are faster
+  // with 64 registers.
+  if (nvec > 1152 && nvec <= 2304) return launch(add_rmsnorm_kernel<4, 576, 2, kC16>, 4);
+  return launch(add_rmsnorm_kernel<4, 1024, 1, kC16>, 4);
 }
 
 }  // namespace

@@ -399,7 +399,7 @@ def _gemm_ch(fn, c16, q_a, s_a, qweight, s_w, y, workspace, stream):
         if not workspace.is_cuda or workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace must be contiguous and on cuda:{dev}")
         nbytes = workspace.numel() * workspace.element_size()
-    else:
+    elif M > 8:            # up to 8 rows never need one
         if torch._C._cuda_getDevice() == dev:
             nbytes = load().qlin_gemm_w8a8_ch_workspace_bytes(M, N, K, c16)
         else:
