@@ -260,11 +260,96 @@ def test_channel_rows_do_not_depend_on_the_batch(gpu):
 @needs_gpu
 def test_channel_int8_minimum_code(gpu):
     """Int8 activation codes of -128 are taken as they are."""
-    q_a = np.full((4, 1024), -128, np.int8)
-    q_w = np.full((1024, 16), -128, np.int8)
-    one = np.ones(4, np.float32), np.ones(16, np.float32)
-    y = _channel_run(q_a, one[0], q_w, one[1], False)
-    assert (y.float() == 128 * 128 * 1024).all()
+    for M in (4, 70, 100, 150, 700):
+        q_a = np.full((M, 1024), -128, np.int8)
+        q_w = np.full((1024, 16), -128, np.int8)
+        y = _channel_run(q_a, np.ones(M, np.float32), q_w, np.ones(16, np.float32), False)
+        assert (y.float() == 128 * 128 * 1024).all()
+
+
+@needs_gpu
+@pytest.mark.parametrize("M,K,N", [(3000, 256, 520), (2500, 1152, 264), (700, 8320, 520), (1000, 2176, 2056)])
+def test_channel_product_of_many_tiles(gpu, M, K, N):
+    """Several token tiles a pair, bands, a last round cut along K, ragged edges."""
+    args = _channel_inputs(M, K, N, "random", 3)
+    y0, _ = ref_channel(*args)
+    for c16 in (False, True):
+        assert np.array_equal(from_dev_bits(_channel_run(*args, c16)), y0)
+
+
+# Every token tile (64, 96, 128, 192), in whole tiles, in equal parts of K and in
+# shares that cross tiles; ragged channel and token tiles.
+TILED_SHAPES = [
+    (16, 5120, 10248), (40, 2304, 8200), (64, 1280, 20488), (24, 10240, 4104), (90, 8192, 2056), (96, 2304, 8200),
+    (100, 1152, 20488), (128, 5120, 4104), (120, 17408, 1544), (130, 9344, 2056), (150, 4224, 5128),
+    (200, 17408, 1032), (192, 1152, 10248), (600, 1152, 5128), (513, 130944, 8)]
+
+
+@needs_gpu
+@pytest.mark.parametrize("M,K,N", TILED_SHAPES)
+@pytest.mark.parametrize("kind", ["random", "extreme"])
+def test_channel_product_in_tiles(gpu, M, K, N, kind):
+    assert qlin.gemm_w8a8_ch_workspace_bytes(M, N, K) > 0
+    args = _channel_inputs(M, K, N, kind, 4)
+    y0, _ = ref_channel(*args)
+    for c16 in (False, True):
+        assert np.array_equal(from_dev_bits(_channel_run(*args, c16)), y0)
+
+
+@needs_gpu
+@pytest.mark.parametrize("M,K,N", [(24, 10240, 4104), (96, 2304, 8200), (128, 5120, 4104), (700, 8320, 520)])
+def test_channel_product_in_cut_tiles_again_and_again(gpu, M, K, N):
+    """A captured call with one workspace, replayed over a dirty workspace, and
+    four streams at once with a workspace each: guard bytes stay, y is the same."""
+    args = _channel_inputs(M, K, N, "random", 6)
+    y0, _ = ref_channel(*args)
+    words, _, _ = oracle.pack_gptq(args[2], 8)
+    q, s_a, w, s_w = to_dev(args[0].astype(np.float16)), to_dev(args[1]), to_dev(words), to_dev(args[3])
+    need = qlin.gemm_w8a8_ch_workspace_bytes(M, N, K, True)
+    assert need > 0
+    want = torch.from_numpy(y0.astype(np.int16)).cuda()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    ws = [torch.full((need + 512,), 0x5A, dtype=torch.uint8, device="cuda") for _ in streams]
+    bufs = [torch.full((M * N + 512,), 7.0, dtype=torch.bfloat16, device="cuda") for _ in streams]
+    ys = [b[256:256 + M * N].view(M, N) for b in bufs]
+    torch.cuda.synchronize()
+    for i in range(12):
+        with torch.cuda.stream(streams[i % 4]):
+            ys[i % 4].zero_()
+            qlin.gemm_w8a8_ch_c16(q, s_a, w, s_w, y=ys[i % 4], workspace=ws[i % 4][256:256 + need])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        qlin.gemm_w8a8_ch_c16(q, s_a, w, s_w, y=ys[0], workspace=ws[0][256:256 + need])
+    for fill in (0xFF, 0x01):
+        ws[0][256:256 + need].fill_(fill)
+        ys[0].zero_()
+        for _ in range(3):
+            graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(ys[0].view(torch.int16), want)
+    for b, t in zip(bufs, ws):
+        assert torch.equal(b[256:256 + M * N].view(M, N).view(torch.int16), want)
+        assert (b[:256] == 7).all() and (b[256 + M * N:] == 7).all()
+        assert (t[:256] == 0x5A).all() and (t[256 + need:] == 0x5A).all()
+
+
+@needs_gpu
+def test_channel_workspace_refusals(gpu):
+    M, K, N = 300, 5120, 520
+    q = torch.zeros((M, K), dtype=torch.int8, device="cuda")
+    s, sw = torch.ones(M, device="cuda"), torch.ones(N, device="cuda")
+    w = torch.zeros((K // 4, N), dtype=torch.int32, device="cuda")
+    need = qlin.gemm_w8a8_ch_workspace_bytes(M, N, K)
+    need16 = qlin.gemm_w8a8_ch_workspace_bytes(M, N, K, True)
+    assert need == need16 + 2 * M * K and need16 > 0
+    for call, codes, n in ((qlin.gemm_w8a8_ch, q, need), (qlin.gemm_w8a8_ch_c16, q.half(), need16)):
+        with pytest.raises(qlin.QlinError) as e:
+            call(codes, s, w, sw, workspace=torch.empty(n - 16, dtype=torch.uint8, device="cuda"))
+        assert e.value.status == qlin.QLIN_ERR_WORKSPACE
+        with pytest.raises(ValueError):
+            call(codes, s, w, sw, workspace=torch.empty(n, dtype=torch.uint8))
+        assert (call(codes, s, w, sw, workspace=torch.empty(n, dtype=torch.uint8, device="cuda")) == 0).all()
 
 
 @needs_gpu
@@ -343,7 +428,11 @@ def _check_logits(x, kw, bf16, in_place=False):
 @pytest.mark.parametrize("M,V,L,B,mask", [
     (1, 8, 3, 2, True), (1, 1000, None, None, False), (2, 1000, 0, 0, True), (3, 4104, 1, 1, False),
     (5, 8200, 700, 9, True), (2, 50264, 300, 600, True), (1, 248320, 2000, 16, True), (33, 50264, 515, None, False),
-    (3, 151936, None, 40, True), (160, 2056, 64, 5, True), (400, 4096, 20, 3, True), (2, 400008, 3000, 30, True)])
+    (3, 151936, None, 40, True), (160, 2056, 64, 5, True), (400, 4096, 20, 3, True), (2, 400008, 3000, 30, True),
+    # more touched tokens than a window of counters, more generated ones than the queue, many bias rounds
+    (2, 9000, 30000, 1700, True), (330, 6000, 5000, 3, False),
+    # slices of several parts
+    (10, 700008, 900, 20, True)])
 def test_adjusted_logits(gpu, M, V, L, B, mask, bf16):
     x, kw = _logit_inputs(M, V, L, B, mask, 5)
     _check_logits(x, kw, bf16)
@@ -492,7 +581,9 @@ def test_two_streams_at_once(gpu):
         with torch.cuda.stream(streams[i % 4]):
             got.append((i % 2, qlin.gemm_w8a8_ch(*dev[i % 2])))
     explicit = qlin.gemm_w8a8_ch(*dev[1], stream=streams[0])
+    by_handle = qlin.gemm_w8a8_ch(*dev[1], stream=streams[1].cuda_stream)
     torch.cuda.synchronize()
+    assert torch.equal(explicit, by_handle)
     for k, y in got:
         assert np.array_equal(from_dev_bits(y), refs[k])
     assert np.array_equal(from_dev_bits(explicit), refs[1])
@@ -551,6 +642,13 @@ def test_refused_tensors(gpu):
         qlin.adjust_logits(logits, tokens=ints.long())
     with pytest.raises(TypeError):
         qlin.adjust_logits(logits.half())
+    for call in (qlin.adjust_logits, qlin.adjust_logits_argmax):
+        with pytest.raises(TypeError):
+            call([1.0])
+        with pytest.raises(ValueError):
+            call(logits[0])
+        with pytest.raises(ValueError):
+            call(logits[:, ::2])
     with pytest.raises(ValueError):
         qlin.adjust_logits(logits, out=torch.empty((4, 128), dtype=torch.bfloat16, device="cuda")[:, ::2])
 

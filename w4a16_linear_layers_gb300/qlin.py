@@ -439,12 +439,18 @@ def gemm_w8a8_ch_c16(q_a: torch.Tensor, s_a: torch.Tensor, qweight: torch.Tensor
 
 
 def _adjust(logits, tokens, prompt_len, total_len, repetition, presence, frequency, bias_ids, bias,
-            allowed, out, argmax, stream):
+            allowed, out, argmax, stream, greedy):
+    """The call; returns argmax if greedy, else out (allocated if not given)."""
     dev = _lead(logits, "logits", (torch.bfloat16, torch.float32), 2)
     dtype = logits.dtype
     M, V = logits.shape
     row = (M,)
     i32, f32 = torch.int32, torch.float32
+    if not greedy:
+        if out is None:
+            out = torch.empty_like(logits)
+    elif argmax is None:
+        argmax = torch.empty(row, dtype=i32, device=logits.device)
     L = B = 0
     if tokens is not None:
         _lead(tokens, "tokens", (i32,), 2)
@@ -483,6 +489,7 @@ def _adjust(logits, tokens, prompt_len, total_len, repetition, presence, frequen
     _run(fn, dev, stream, logits.data_ptr(), M, V, _opt(tokens), L, _opt(prompt_len),
          _opt(total_len), _opt(repetition), _opt(presence), _opt(frequency), _opt(bias_ids),
          _opt(bias), B, _opt(allowed), _opt(out), _opt(argmax))
+    return argmax if greedy else out
 
 
 def adjust_logits(logits: torch.Tensor, tokens=None, prompt_len=None, total_len=None,
@@ -497,11 +504,8 @@ def adjust_logits(logits: torch.Tensor, tokens=None, prompt_len=None, total_len=
     bias fp32 [M,B] (ids outside the vocabulary are skipped, the last entry of
     an id applies); allowed int32 [M, ceil(V/32)], bit 1 = allowed, least
     significant first.  Order and rounding: include/qlin.h."""
-    if out is None:
-        out = torch.empty_like(logits)
-    _adjust(logits, tokens, prompt_len, total_len, repetition, presence, frequency, bias_ids, bias,
-            allowed, out, None, stream)
-    return out
+    return _adjust(logits, tokens, prompt_len, total_len, repetition, presence, frequency, bias_ids,
+                   bias, allowed, out, None, stream, False)
 
 
 def adjust_logits_argmax(logits: torch.Tensor, tokens=None, prompt_len=None, total_len=None,
@@ -510,11 +514,8 @@ def adjust_logits_argmax(logits: torch.Tensor, tokens=None, prompt_len=None, tot
     """The greedy token of each row after adjust_logits: int32 [M], the lowest
     index on ties, -1 for a row without a value above -inf.  The adjusted
     logits are written only if out is given."""
-    if argmax is None:
-        argmax = torch.empty(logits.shape[:1], dtype=torch.int32, device=logits.device)
-    _adjust(logits, tokens, prompt_len, total_len, repetition, presence, frequency, bias_ids, bias,
-            allowed, out, argmax, stream)
-    return argmax
+    return _adjust(logits, tokens, prompt_len, total_len, repetition, presence, frequency, bias_ids,
+                   bias, allowed, out, argmax, stream, True)
 
 
 def workspace_bytes(M: int, N: int, K: int) -> int:
