@@ -289,6 +289,10 @@ qlin_status_t qlin_gemm_w8a8_gs128_noalloc(const int8_t *q_a, const float *s_a,
  *            no zeroing and holds nothing between calls.  Calls that share a
  *            workspace must not overlap.
  *
+ * Like the other GEMMs, the call may begin to read qweight while the previous
+ * kernel on its stream runs, if that is a call of this library: weights are
+ * not written by such a kernel.
+ *
  * K is at most 130,944 (QLIN_ERR_SHAPE above): sums of that many products of
  * two int8 values fit int32.
  */

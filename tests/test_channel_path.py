@@ -349,6 +349,10 @@ def test_channel_workspace_refusals(gpu):
         assert e.value.status == qlin.QLIN_ERR_WORKSPACE
         with pytest.raises(ValueError):
             call(codes, s, w, sw, workspace=torch.empty(n, dtype=torch.uint8))
+        with pytest.raises(TypeError):
+            call(codes, s, w, sw, workspace=n)
+        with pytest.raises(TypeError):
+            call(codes, s, w, sw, workspace=torch.empty(n, device="cuda"))
         assert (call(codes, s, w, sw, workspace=torch.empty(n, dtype=torch.uint8, device="cuda")) == 0).all()
 
 
@@ -587,6 +591,41 @@ def test_two_streams_at_once(gpu):
     for k, y in got:
         assert np.array_equal(from_dev_bits(y), refs[k])
     assert np.array_equal(from_dev_bits(explicit), refs[1])
+
+
+@needs_gpu
+@pytest.mark.parametrize("by_handle", [False, True], ids=["stream", "handle"])
+def test_a_named_stream_leaves_freed_memory_of_the_current_one(gpu, by_handle):
+    """The current stream holds work on a tensor that was freed: what a call on
+    another stream allocates must not be its memory."""
+    M, K, N = 64, 5120, 5128
+    shape = (M, K)
+    x = torch.ones(shape, dtype=torch.bfloat16, device="cuda")
+    g = torch.ones(K, dtype=torch.bfloat16, device="cuda")
+    codes = torch.ones(shape, dtype=torch.float16, device="cuda")
+    w, s_w = torch.zeros((K // 4, N), dtype=torch.int32, device="cuda"), torch.ones(N, device="cuda")
+    s_a = torch.ones(M, device="cuda")
+    logits = torch.zeros((M, N), dtype=torch.bfloat16, device="cuda")
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if by_handle else side
+    need = qlin.gemm_w8a8_ch_workspace_bytes(M, N, K, True)
+    assert need > 0
+    calls = [(lambda: qlin.add_rmsnorm_act_quant_c16(x, x, g, 1e-6, stream=stream), (M * K * 2,)),
+             (lambda: qlin.gemm_w8a8_ch_c16(codes, s_a, w, s_w, stream=stream), (M * N * 2, need)),
+             (lambda: qlin.adjust_logits(logits, repetition=s_a, stream=stream), (M * N * 2,))]
+    for call, sizes in calls:
+        call()
+        torch.cuda.synchronize()
+        held = [torch.full((n,), 0x35, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(2)]
+        kept = [torch.empty_like(t) for t in held]
+        torch.cuda._sleep(50_000_000)
+        for k, t in zip(kept, held):
+            k.copy_(t)
+        del held, t
+        call()
+        torch.cuda.synchronize()
+        for k in kept:
+            assert (k == 0x35).all()
 
 
 @needs_gpu

@@ -267,10 +267,6 @@ cudaError_t launch_c(const ChannelParams& p, int sm_count, cudaStream_t stream) 
   return launch_stream<1, kC16>(p, static_cast<int>(splits), stream);
 }
 
-}  // namespace
-
-namespace {
-
 // ------------------------------------------------------- larger batches
 
 // Batches that take the streaming kernel: up to 8 tokens always, and more

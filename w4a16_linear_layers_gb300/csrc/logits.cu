@@ -181,6 +181,7 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
+
 template <bool kF32, bool kRules, bool kMasked>
 __global__ void __launch_bounds__(kLThreads, kRules ? 2 : 3) adjust_logits_kernel(const LogitParams p) {
   constexpr int kAhead = kF32 ? 2 : 4;       // vectors in flight a thread

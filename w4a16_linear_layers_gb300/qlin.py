@@ -303,13 +303,9 @@ def _lead(t, name, dtypes, ndim) -> int:
     return t.get_device()
 
 
-def _run(fn, index, stream, *args):
-    """fn(*args, stream) with device `index` current, on `stream` (default: the
-    device's current stream)."""
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(index)
-    else:
-        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+def _run(fn, index, *args):
+    """fn(*args, stream) with device `index` current, on its current stream."""
+    handle = torch._C._cuda_getCurrentRawStream(index)
     if torch._C._cuda_getDevice() == index:
         status = fn(*args, handle)
     else:
@@ -319,6 +315,28 @@ def _run(fn, index, stream, *args):
         _check(status)
 
 
+def _on(stream, index, call, *args):
+    """call(*args) with `stream` (a torch stream, or a raw handle) current.
+
+    What the call allocates belongs to that stream: memory of the caller's
+    current stream may be what was freed there with work on it still to come,
+    which this stream does not wait for.  Tensors that it returns are the
+    caller's too: their memory also waits for the stream current here when they
+    are freed."""
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch.cuda.ExternalStream(handle, device=torch.device("cuda", index))
+    if stream.device_index != index:
+        raise ValueError(f"stream must be of cuda:{index}, got {stream.device}")
+    caller = torch.cuda.current_stream(index)
+    with torch.cuda.stream(stream):
+        result = call(*args)
+    if caller != stream:
+        for t in result if isinstance(result, tuple) else (result,):
+            t.record_stream(caller)
+    return result
+
+
 def _opt(t):
     return None if t is None else t.data_ptr()
 
@@ -326,6 +344,9 @@ def _opt(t):
 def _add_rmsnorm_act_quant(fn, code_dtype, x, residual, gamma, eps, residual_out, q, s_a, y, stream):
     bf16 = torch.bfloat16
     dev = _lead(x, "x", (bf16,), 2)
+    if stream is not None:
+        return _on(stream, dev, _add_rmsnorm_act_quant, fn, code_dtype, x, residual, gamma, eps,
+                   residual_out, q, s_a, y, None)
     shape = x.shape
     M, K = shape
     if not _is(residual, bf16, shape, dev):
@@ -346,7 +367,7 @@ def _add_rmsnorm_act_quant(fn, code_dtype, x, residual, gamma, eps, residual_out
         _refuse(s_a, "s_a", torch.float32, (M,), dev)
     if y is not None and not _is(y, bf16, shape, dev):
         _refuse(y, "y", bf16, shape, dev)
-    _run(fn, dev, stream, x.data_ptr(), residual.data_ptr(), gamma.data_ptr(), eps, M, K,
+    _run(fn, dev, x.data_ptr(), residual.data_ptr(), gamma.data_ptr(), eps, M, K,
          residual_out.data_ptr(), q.data_ptr(), s_a.data_ptr(), None if y is None else y.data_ptr())
     return q, s_a, residual_out
 
@@ -372,14 +393,17 @@ def gemm_w8a8_ch_workspace_bytes(M: int, N: int, K: int, c16: bool = False) -> i
     return int(load().qlin_gemm_w8a8_ch_workspace_bytes(int(M), int(N), int(K), int(c16)))
 
 
-def _ch_inputs(code_dtype, q_a, s_a, qweight, s_w, y):
+def _gemm_ch(fn, c16, q_a, s_a, qweight, s_w, y, workspace, stream):
+    code_dtype = torch.float16 if c16 else torch.int8
     dev = _lead(q_a, "q_a", (code_dtype,), 2)
+    if stream is not None:
+        return _on(stream, dev, _gemm_ch, fn, c16, q_a, s_a, qweight, s_w, y, workspace, None)
     _lead(qweight, "qweight", (torch.int32,), 2)
     M, K = q_a.shape
     N = qweight.shape[1]
-    if not _is(qweight, torch.int32, (K // 4, N), dev) or K % 4:
-        if K % 4:
-            raise ValueError("K must be a multiple of 128")
+    if K % 4:
+        raise ValueError("K must be a multiple of 128")
+    if not _is(qweight, torch.int32, (K // 4, N), dev):
         _refuse(qweight, "qweight", torch.int32, (K // 4, N), dev)
     if not _is(s_a, torch.float32, (M,), dev):
         _refuse(s_a, "s_a", torch.float32, (M,), dev)
@@ -389,16 +413,12 @@ def _ch_inputs(code_dtype, q_a, s_a, qweight, s_w, y):
         y = torch.empty((M, N), dtype=torch.bfloat16, device=q_a.device)
     elif not _is(y, torch.bfloat16, (M, N), dev):
         _refuse(y, "y", torch.bfloat16, (M, N), dev)
-    return dev, M, N, K, y
-
-
-def _gemm_ch(fn, c16, q_a, s_a, qweight, s_w, y, workspace, stream):
-    dev, M, N, K, y = _ch_inputs(torch.float16 if c16 else torch.int8, q_a, s_a, qweight, s_w, y)
     nbytes = 0
     if workspace is not None:
-        if not workspace.is_cuda or workspace.get_device() != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be contiguous and on cuda:{dev}")
-        nbytes = workspace.numel() * workspace.element_size()
+        nbytes = workspace.shape[0] if isinstance(workspace, torch.Tensor) and workspace.dim() == 1 else -1
+        if not _is(workspace, torch.uint8, (nbytes,), dev):
+            _lead(workspace, "workspace", (torch.uint8,), 1)
+            _refuse(workspace, "workspace", torch.uint8, (nbytes,), dev)
     elif M > 8:            # up to 8 rows never need one
         if torch._C._cuda_getDevice() == dev:
             nbytes = load().qlin_gemm_w8a8_ch_workspace_bytes(M, N, K, c16)
@@ -409,12 +429,7 @@ def _gemm_ch(fn, c16, q_a, s_a, qweight, s_w, y, workspace, stream):
             # its own for every call: calls on several streams, or replayed
             # graphs, do not meet in it
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=q_a.device)
-            if stream is not None:
-                # freed with this call, while `stream` may still use it
-                workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
-                                        torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream),
-                                                                  device=q_a.device))
-    _run(fn, dev, stream, q_a.data_ptr(), s_a.data_ptr(), qweight.data_ptr(), s_w.data_ptr(), M, N, K,
+    _run(fn, dev, q_a.data_ptr(), s_a.data_ptr(), qweight.data_ptr(), s_w.data_ptr(), M, N, K,
          y.data_ptr(), _opt(workspace), nbytes)
     return y
 
@@ -442,6 +457,9 @@ def _adjust(logits, tokens, prompt_len, total_len, repetition, presence, frequen
             allowed, out, argmax, stream, greedy):
     """The call; returns argmax if greedy, else out (allocated if not given)."""
     dev = _lead(logits, "logits", (torch.bfloat16, torch.float32), 2)
+    if stream is not None:
+        return _on(stream, dev, _adjust, logits, tokens, prompt_len, total_len, repetition, presence,
+                   frequency, bias_ids, bias, allowed, out, argmax, None, greedy)
     dtype = logits.dtype
     M, V = logits.shape
     row = (M,)
@@ -486,7 +504,7 @@ def _adjust(logits, tokens, prompt_len, total_len, repetition, presence, frequen
         _refuse(argmax, "argmax", i32, row, dev)
     lib = load()
     fn = lib.qlin_adjust_logits_bf16 if dtype is torch.bfloat16 else lib.qlin_adjust_logits_f32
-    _run(fn, dev, stream, logits.data_ptr(), M, V, _opt(tokens), L, _opt(prompt_len),
+    _run(fn, dev, logits.data_ptr(), M, V, _opt(tokens), L, _opt(prompt_len),
          _opt(total_len), _opt(repetition), _opt(presence), _opt(frequency), _opt(bias_ids),
          _opt(bias), B, _opt(allowed), _opt(out), _opt(argmax))
     return argmax if greedy else out
