@@ -4,7 +4,9 @@ Each .cu file under csrc/ is compiled to an object in parallel, then linked
 into ``w4a16_linear_layers_gb300/_build/libqlin.so``.  The library links the
 CUDA runtime statically and reaches the driver's tensor-map encoder through
 the runtime's entry-point query, so it does not link against PyTorch or
-libcuda.  Usage: ``python -m w4a16_linear_layers_gb300.build [--force]``.
+libcuda.  csrc/torch_calls.cpp, the Python extension of the calls that are
+short on the device, becomes ``_build/qlin_torch.so`` beside it, with the host
+compiler and PyTorch's headers.  Usage: ``python -m w4a16_linear_layers_gb300.build [--force]``.
 """
 from __future__ import annotations
 
@@ -12,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +22,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libqlin.so")
+CALLS_PATH = os.path.join(BUILD_DIR, "qlin_torch.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -45,10 +49,29 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(CALLS_PATH):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(CALLS_PATH))
     return all(os.path.getmtime(d) <= t for d in _deps())
+
+
+def _build_calls() -> None:
+    import torch
+
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    headers = [sysconfig.get_paths()["include"], os.path.join(base, "include"),
+               os.path.join(base, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
+    tmp = CALLS_PATH + f".{os.getpid()}.tmp"
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden", "-I", INCLUDE]
+    for path in headers:
+        cmd += ["-isystem", path]
+    cmd += [os.path.join(CSRC, "torch_calls.cpp"), "-o", tmp, "-L", os.path.join(base, "lib"),
+            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for torch_calls.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS_PATH)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
@@ -71,8 +94,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
             print(r.stdout + r.stderr, flush=True)
         return obj
 
-    with ThreadPoolExecutor(max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with ThreadPoolExecutor(max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        calls = ex.submit(_build_calls)
         objs = list(ex.map(compile_one, srcs))
+        calls.result()
     tmp = LIB_PATH + f".{os.getpid()}.tmp"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

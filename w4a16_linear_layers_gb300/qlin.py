@@ -1,6 +1,7 @@
-"""Python binding of libqlin (ctypes).  Argument marshalling only: every step
-of the computation runs in the library's CUDA kernels; PyTorch supplies device
-memory and the current stream.
+"""Python binding of libqlin (ctypes, and a Python extension for the calls that
+are short on the device).  Argument marshalling only: every step of the
+computation runs in the library's CUDA kernels; PyTorch supplies device memory
+and the current stream.
 
 Names follow the C ABI (include/qlin.h) without the ``qlin_`` prefix.  Tensors
 must be CUDA tensors, contiguous, of the dtypes listed per call; outputs are
@@ -11,6 +12,8 @@ allocated with ``torch.empty`` when not given.  A non-zero status raises
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
@@ -265,64 +268,44 @@ def silu_mul_act_quant_c16(gate_up: torch.Tensor, q=None, s_a=None, y=None, stre
                                y, stream)
 
 
-# The calls below launch on their tensors' device, whichever device is current.
-# A small batch's kernel takes less time than Python needs to call it, so they
-# check each argument once, with the cheapest attribute reads, and skip the
-# tensors they allocated themselves.
+# The calls below go through the extension that csrc/torch_calls.cpp describes.
+# They launch on their tensors' device, whichever device is current.
 
-def _is(t, dtype, shape, index) -> bool:
-    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-            and t.get_device() == index and t.is_contiguous())
+_torch_calls = None
 
 
-def _refuse(t, name, dtype, shape, index):
-    """Raises what is wrong with an argument that _is turned down."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    if t.get_device() != index:
-        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
-    raise ValueError(f"{name} must be contiguous")
+def _calls():
+    """The extension, loaded and given libqlin's entry points."""
+    global _torch_calls
+    lib = load()
+    with _lock:
+        if _torch_calls is None:
+            path = _build.CALLS_PATH
+            if not os.path.exists(path):
+                raise QlinError(QLIN_ERR_CUDA, f"{path} is not built; run "
+                                "`python -m w4a16_linear_layers_gb300.build` (or __graft_entry__.build())")
+            loader = importlib.machinery.ExtensionFileLoader("qlin_torch", path)
+            module = importlib.util.module_from_spec(importlib.util.spec_from_loader("qlin_torch", loader))
+            loader.exec_module(module)
+            names = ("qlin_add_rmsnorm_act_quant_i8", "qlin_add_rmsnorm_act_quant_c16", "qlin_gemm_w8a8_ch",
+                     "qlin_gemm_w8a8_ch_c16", "qlin_gemm_w8a8_ch_workspace_bytes", "qlin_adjust_logits_bf16",
+                     "qlin_adjust_logits_f32")
+            module.setup(_check, *(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names))
+            _torch_calls = module
+    return _torch_calls
 
 
-def _lead(t, name, dtypes, ndim) -> int:
-    """The argument that the others' shapes follow from; returns its device's index."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    if t.dim() != ndim:
-        raise ValueError(f"{name} must have {ndim} dimensions, got {t.dim()}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.get_device()
-
-
-def _run(fn, index, *args):
-    """fn(*args, stream) with device `index` current, on its current stream."""
-    handle = torch._C._cuda_getCurrentRawStream(index)
-    if torch._C._cuda_getDevice() == index:
-        status = fn(*args, handle)
-    else:
-        with torch.cuda.device(index):
-            status = fn(*args, handle)
-    if status != QLIN_OK:
-        _check(status)
-
-
-def _on(stream, index, call, *args):
-    """call(*args) with `stream` (a torch stream, or a raw handle) current.
+def _on(stream, lead, call, *args):
+    """call(*args) with `stream` (a torch stream, or a raw handle, of lead's device) current.
 
     What the call allocates belongs to that stream: memory of the caller's
     current stream may be what was freed there with work on it still to come,
     which this stream does not wait for.  Tensors that it returns are the
     caller's too: their memory also waits for the stream current here when they
     are freed."""
+    if not isinstance(lead, torch.Tensor) or not lead.is_cuda:
+        return call(*args)      # which refuses it
+    index = lead.get_device()
     if not isinstance(stream, torch.cuda.Stream):
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
         stream = torch.cuda.ExternalStream(handle, device=torch.device("cuda", index))
@@ -337,101 +320,29 @@ def _on(stream, index, call, *args):
     return result
 
 
-def _opt(t):
-    return None if t is None else t.data_ptr()
-
-
-def _add_rmsnorm_act_quant(fn, code_dtype, x, residual, gamma, eps, residual_out, q, s_a, y, stream):
-    bf16 = torch.bfloat16
-    dev = _lead(x, "x", (bf16,), 2)
-    if stream is not None:
-        return _on(stream, dev, _add_rmsnorm_act_quant, fn, code_dtype, x, residual, gamma, eps,
-                   residual_out, q, s_a, y, None)
-    shape = x.shape
-    M, K = shape
-    if not _is(residual, bf16, shape, dev):
-        _refuse(residual, "residual", bf16, shape, dev)
-    if not _is(gamma, bf16, (K,), dev):
-        _refuse(gamma, "gamma", bf16, (K,), dev)
-    if residual_out is None:
-        residual_out = torch.empty_like(residual)
-    elif not _is(residual_out, bf16, shape, dev):
-        _refuse(residual_out, "residual_out", bf16, shape, dev)
-    if q is None:
-        q = torch.empty(shape, dtype=code_dtype, device=x.device)
-    elif not _is(q, code_dtype, shape, dev):
-        _refuse(q, "q", code_dtype, shape, dev)
-    if s_a is None:
-        s_a = torch.empty((M,), dtype=torch.float32, device=x.device)
-    elif not _is(s_a, torch.float32, (M,), dev):
-        _refuse(s_a, "s_a", torch.float32, (M,), dev)
-    if y is not None and not _is(y, bf16, shape, dev):
-        _refuse(y, "y", bf16, shape, dev)
-    _run(fn, dev, x.data_ptr(), residual.data_ptr(), gamma.data_ptr(), eps, M, K,
-         residual_out.data_ptr(), q.data_ptr(), s_a.data_ptr(), None if y is None else y.data_ptr())
-    return q, s_a, residual_out
-
-
 def add_rmsnorm_act_quant_i8(x: torch.Tensor, residual: torch.Tensor, gamma: torch.Tensor,
                              eps: float, residual_out=None, q=None, s_a=None, y=None, stream=None):
     """h = x + residual (bf16 [M,K]), RMSNorm of h with weight gamma bf16 [K],
     then per-token INT8 act-quant -> (q int8 [M,K], s_a fp32 [M], h).  h is
     written to residual_out, which may be x or residual (in place).  If y (bf16
     [M,K]) is given the norm's bf16 output is written there too."""
-    return _add_rmsnorm_act_quant(load().qlin_add_rmsnorm_act_quant_i8, torch.int8, x, residual,
-                                  gamma, eps, residual_out, q, s_a, y, stream)
+    call = (_torch_calls or _calls()).add_rmsnorm
+    if stream is not None:
+        return _on(stream, x, call, False, x, residual, gamma, eps, residual_out, q, s_a, y)
+    return call(False, x, residual, gamma, eps, residual_out, q, s_a, y)
 
 
 def add_rmsnorm_act_quant_c16(x: torch.Tensor, residual: torch.Tensor, gamma: torch.Tensor,
                               eps: float, residual_out=None, q=None, s_a=None, y=None, stream=None):
     """add_rmsnorm_act_quant_i8 with the codes as fp16 (q fp16 [M,K])."""
-    return _add_rmsnorm_act_quant(load().qlin_add_rmsnorm_act_quant_c16, torch.float16, x, residual,
-                                  gamma, eps, residual_out, q, s_a, y, stream)
+    call = (_torch_calls or _calls()).add_rmsnorm
+    if stream is not None:
+        return _on(stream, x, call, True, x, residual, gamma, eps, residual_out, q, s_a, y)
+    return call(True, x, residual, gamma, eps, residual_out, q, s_a, y)
 
 
 def gemm_w8a8_ch_workspace_bytes(M: int, N: int, K: int, c16: bool = False) -> int:
     return int(load().qlin_gemm_w8a8_ch_workspace_bytes(int(M), int(N), int(K), int(c16)))
-
-
-def _gemm_ch(fn, c16, q_a, s_a, qweight, s_w, y, workspace, stream):
-    code_dtype = torch.float16 if c16 else torch.int8
-    dev = _lead(q_a, "q_a", (code_dtype,), 2)
-    if stream is not None:
-        return _on(stream, dev, _gemm_ch, fn, c16, q_a, s_a, qweight, s_w, y, workspace, None)
-    _lead(qweight, "qweight", (torch.int32,), 2)
-    M, K = q_a.shape
-    N = qweight.shape[1]
-    if K % 4:
-        raise ValueError("K must be a multiple of 128")
-    if not _is(qweight, torch.int32, (K // 4, N), dev):
-        _refuse(qweight, "qweight", torch.int32, (K // 4, N), dev)
-    if not _is(s_a, torch.float32, (M,), dev):
-        _refuse(s_a, "s_a", torch.float32, (M,), dev)
-    if not _is(s_w, torch.float32, (N,), dev):
-        _refuse(s_w, "s_w", torch.float32, (N,), dev)
-    if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=q_a.device)
-    elif not _is(y, torch.bfloat16, (M, N), dev):
-        _refuse(y, "y", torch.bfloat16, (M, N), dev)
-    nbytes = 0
-    if workspace is not None:
-        nbytes = workspace.shape[0] if isinstance(workspace, torch.Tensor) and workspace.dim() == 1 else -1
-        if not _is(workspace, torch.uint8, (nbytes,), dev):
-            _lead(workspace, "workspace", (torch.uint8,), 1)
-            _refuse(workspace, "workspace", torch.uint8, (nbytes,), dev)
-    elif M > 8:            # up to 8 rows never need one
-        if torch._C._cuda_getDevice() == dev:
-            nbytes = load().qlin_gemm_w8a8_ch_workspace_bytes(M, N, K, c16)
-        else:
-            with torch.cuda.device(dev):
-                nbytes = load().qlin_gemm_w8a8_ch_workspace_bytes(M, N, K, c16)
-        if nbytes:
-            # its own for every call: calls on several streams, or replayed
-            # graphs, do not meet in it
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q_a.device)
-    _run(fn, dev, q_a.data_ptr(), s_a.data_ptr(), qweight.data_ptr(), s_w.data_ptr(), M, N, K,
-         y.data_ptr(), _opt(workspace), nbytes)
-    return y
 
 
 def gemm_w8a8_ch(q_a: torch.Tensor, s_a: torch.Tensor, qweight: torch.Tensor, s_w: torch.Tensor,
@@ -441,7 +352,10 @@ def gemm_w8a8_ch(q_a: torch.Tensor, s_a: torch.Tensor, qweight: torch.Tensor, s_
     s_w fp32 [N] (one scale per output channel) -> y bf16 [M,N].  workspace: a
     uint8 tensor of gemm_w8a8_ch_workspace_bytes(M, N, K) bytes; allocated for
     the call when not given and needed."""
-    return _gemm_ch(load().qlin_gemm_w8a8_ch, 0, q_a, s_a, qweight, s_w, y, workspace, stream)
+    call = (_torch_calls or _calls()).gemm_ch
+    if stream is not None:
+        return _on(stream, q_a, call, False, q_a, s_a, qweight, s_w, y, workspace)
+    return call(False, q_a, s_a, qweight, s_w, y, workspace)
 
 
 def gemm_w8a8_ch_c16(q_a: torch.Tensor, s_a: torch.Tensor, qweight: torch.Tensor,
@@ -450,64 +364,10 @@ def gemm_w8a8_ch_c16(q_a: torch.Tensor, s_a: torch.Tensor, qweight: torch.Tensor
     """gemm_w8a8_ch with the activation codes as fp16 (q_a fp16 [M,K], the
     output of the *_c16 producers); its workspace has
     gemm_w8a8_ch_workspace_bytes(M, N, K, True) bytes."""
-    return _gemm_ch(load().qlin_gemm_w8a8_ch_c16, 1, q_a, s_a, qweight, s_w, y, workspace, stream)
-
-
-def _adjust(logits, tokens, prompt_len, total_len, repetition, presence, frequency, bias_ids, bias,
-            allowed, out, argmax, stream, greedy):
-    """The call; returns argmax if greedy, else out (allocated if not given)."""
-    dev = _lead(logits, "logits", (torch.bfloat16, torch.float32), 2)
+    call = (_torch_calls or _calls()).gemm_ch
     if stream is not None:
-        return _on(stream, dev, _adjust, logits, tokens, prompt_len, total_len, repetition, presence,
-                   frequency, bias_ids, bias, allowed, out, argmax, None, greedy)
-    dtype = logits.dtype
-    M, V = logits.shape
-    row = (M,)
-    i32, f32 = torch.int32, torch.float32
-    if not greedy:
-        if out is None:
-            out = torch.empty_like(logits)
-    elif argmax is None:
-        argmax = torch.empty(row, dtype=i32, device=logits.device)
-    L = B = 0
-    if tokens is not None:
-        _lead(tokens, "tokens", (i32,), 2)
-        L = tokens.shape[1]
-        if not _is(tokens, i32, (M, L), dev):
-            _refuse(tokens, "tokens", i32, (M, L), dev)
-        if prompt_len is not None and not _is(prompt_len, i32, row, dev):
-            _refuse(prompt_len, "prompt_len", i32, row, dev)
-        if total_len is not None and not _is(total_len, i32, row, dev):
-            _refuse(total_len, "total_len", i32, row, dev)
-    elif prompt_len is not None or total_len is not None:
-        raise ValueError("prompt_len and total_len need tokens")
-    if bias_ids is not None and bias is not None:
-        _lead(bias_ids, "bias_ids", (i32,), 2)
-        B = bias_ids.shape[1]
-        if not _is(bias_ids, i32, (M, B), dev):
-            _refuse(bias_ids, "bias_ids", i32, (M, B), dev)
-        if not _is(bias, f32, (M, B), dev):
-            _refuse(bias, "bias", f32, (M, B), dev)
-    elif bias_ids is not None or bias is not None:
-        raise ValueError("bias_ids and bias go together")
-    if repetition is not None and not _is(repetition, f32, row, dev):
-        _refuse(repetition, "repetition", f32, row, dev)
-    if presence is not None and not _is(presence, f32, row, dev):
-        _refuse(presence, "presence", f32, row, dev)
-    if frequency is not None and not _is(frequency, f32, row, dev):
-        _refuse(frequency, "frequency", f32, row, dev)
-    if allowed is not None and not _is(allowed, i32, (M, (V + 31) // 32), dev):
-        _refuse(allowed, "allowed", i32, (M, (V + 31) // 32), dev)
-    if out is not None and not _is(out, dtype, (M, V), dev):
-        _refuse(out, "out", dtype, (M, V), dev)
-    if argmax is not None and not _is(argmax, i32, row, dev):
-        _refuse(argmax, "argmax", i32, row, dev)
-    lib = load()
-    fn = lib.qlin_adjust_logits_bf16 if dtype is torch.bfloat16 else lib.qlin_adjust_logits_f32
-    _run(fn, dev, logits.data_ptr(), M, V, _opt(tokens), L, _opt(prompt_len),
-         _opt(total_len), _opt(repetition), _opt(presence), _opt(frequency), _opt(bias_ids),
-         _opt(bias), B, _opt(allowed), _opt(out), _opt(argmax))
-    return argmax if greedy else out
+        return _on(stream, q_a, call, True, q_a, s_a, qweight, s_w, y, workspace)
+    return call(True, q_a, s_a, qweight, s_w, y, workspace)
 
 
 def adjust_logits(logits: torch.Tensor, tokens=None, prompt_len=None, total_len=None,
@@ -522,8 +382,12 @@ def adjust_logits(logits: torch.Tensor, tokens=None, prompt_len=None, total_len=
     bias fp32 [M,B] (ids outside the vocabulary are skipped, the last entry of
     an id applies); allowed int32 [M, ceil(V/32)], bit 1 = allowed, least
     significant first.  Order and rounding: include/qlin.h."""
-    return _adjust(logits, tokens, prompt_len, total_len, repetition, presence, frequency, bias_ids,
-                   bias, allowed, out, None, stream, False)
+    call = (_torch_calls or _calls()).adjust_logits
+    if stream is not None:
+        return _on(stream, logits, call, False, logits, tokens, prompt_len, total_len, repetition, presence,
+                   frequency, bias_ids, bias, allowed, out, None)
+    return call(False, logits, tokens, prompt_len, total_len, repetition, presence, frequency, bias_ids, bias,
+                allowed, out, None)
 
 
 def adjust_logits_argmax(logits: torch.Tensor, tokens=None, prompt_len=None, total_len=None,
@@ -532,8 +396,12 @@ def adjust_logits_argmax(logits: torch.Tensor, tokens=None, prompt_len=None, tot
     """The greedy token of each row after adjust_logits: int32 [M], the lowest
     index on ties, -1 for a row without a value above -inf.  The adjusted
     logits are written only if out is given."""
-    return _adjust(logits, tokens, prompt_len, total_len, repetition, presence, frequency, bias_ids,
-                   bias, allowed, out, argmax, stream, True)
+    call = (_torch_calls or _calls()).adjust_logits
+    if stream is not None:
+        return _on(stream, logits, call, True, logits, tokens, prompt_len, total_len, repetition, presence,
+                   frequency, bias_ids, bias, allowed, out, argmax)
+    return call(True, logits, tokens, prompt_len, total_len, repetition, presence, frequency, bias_ids, bias,
+                allowed, out, argmax)
 
 
 def workspace_bytes(M: int, N: int, K: int) -> int:
