@@ -130,7 +130,9 @@ def _norm_inputs(M, K, seed=0):
 @pytest.mark.parametrize("M,K,eps", [
     (1, 128, 1e-6), (1, 5120, 1e-6), (3, 5120, 1e-5), (8, 8192, 1e-6), (5, 8320, 1e-6), (7, 17408, 1e-6),
     (2, 25600, 1e-6), (2, 32768, 1e-6), (3, 33024, 1e-6), (160, 640, 1e-6), (153, 4096, 1e-6),
-    (300, 1280, 1e-6), (200, 5120, 0.0), (400, 128, 1e-3)])
+    (300, 1280, 1e-6), (200, 5120, 0.0), (400, 128, 1e-3),
+    # rows in four, two blocks and one
+    (38, 8320, 1e-6), (39, 8320, 1e-6), (60, 17408, 0.0), (152, 18432, 1e-6), (20, 18560, 1e-6), (19, 32768, 1e-6), (154, 12288, 1e-6)])
 def test_add_rmsnorm_equals_the_oracle_chain(gpu, M, K, eps):
     xb, rb, gb = _norm_inputs(M, K)
     if eps == 0.0:
@@ -150,7 +152,7 @@ def test_add_rmsnorm_equals_the_oracle_chain(gpu, M, K, eps):
 
 
 @needs_gpu
-@pytest.mark.parametrize("M,K", [(2, 640), (170, 5120), (1, 33024)])
+@pytest.mark.parametrize("M,K", [(2, 640), (170, 5120), (1, 33024), (6, 17408), (40, 9088)])
 @pytest.mark.parametrize("into", ["x", "residual"])
 def test_add_rmsnorm_in_place(gpu, M, K, into):
     xb, rb, gb = _norm_inputs(M, K, 1)

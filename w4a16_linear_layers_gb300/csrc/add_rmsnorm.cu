@@ -272,9 +272,27 @@ struct AddNormParams {
   float eps, ki, kl;   // 1 / K = ki + kl
 };
 
+__device__ __forceinline__ uint32_t map_block(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void row_sync() {   // all threads of the row's blocks
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The block's place among the kParts of its row.
+template <int kParts>
+__device__ __forceinline__ int block_of_row() {
+  return static_cast<int>(blockIdx.x % kParts);
+}
+
 // The sums of squares of the block's threads -> rstd, in every thread.  Each
 // warp's pair goes through shared memory and every warp adds all of them in
 // the same order, so all threads hold the same rstd after one barrier.
+// The kParts blocks of a row, a cluster, send them to one another, with a
+// cluster barrier in the block's place.
+template <int kParts>
 __device__ __forceinline__ Rstd block_rstd(f32x2 s2, f32x2 c2, float2* red, const AddNormParams& p) {
   float s, s1, c, c1;
   unpack2(s2, s, s1);
@@ -288,14 +306,28 @@ __device__ __forceinline__ Rstd block_rstd(f32x2 s2, f32x2 c2, float2* red, cons
     c = __fadd_rn(c, co);
     twosum1(s, c, so);
   }
-  const int nw = blockDim.x >> 5;
-  if (nw > 1) {
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(s, c);
+  const int lane = threadIdx.x & 31;
+  int nw = blockDim.x >> 5;
+  if constexpr (kParts > 1) {
+    if (lane < kParts)
+      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(
+                       map_block(smem_u32(red + block_of_row<kParts>() * nw + (threadIdx.x >> 5)), lane)),
+                   "f"(s), "f"(c)
+                   : "memory");
+    row_sync();
+    nw *= kParts;
+  } else if (nw > 1) {
+    if (lane == 0) red[threadIdx.x >> 5] = make_float2(s, c);
     __syncthreads();
-    const int lane = threadIdx.x & 31;
+  }
+  if (nw > 1) {
     const float2 mine = lane < nw ? red[lane] : make_float2(0.0f, 0.0f);
     s = mine.x;
     c = mine.y;
+    for (int i = lane + 32; kParts > 1 && i < nw; i += 32) {
+      c = __fadd_rn(c, red[i].y);
+      twosum1(s, c, red[i].x);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       const float so = __shfl_xor_sync(0xFFFFFFFFu, s, o);
@@ -307,29 +339,48 @@ __device__ __forceinline__ Rstd block_rstd(f32x2 s2, f32x2 c2, float2* red, cons
   return row_rstd(s, c, p.ki, p.kl, p.eps);
 }
 
+template <int kParts>
 __device__ __forceinline__ float block_absmax(uint32_t m2, uint32_t* red) {
   uint32_t m = max(m2 & 0x7FFFu, m2 >> 16 & 0x7FFFu);   // non-negative bf16 bits order as integers
   m = __reduce_max_sync(0xFFFFFFFFu, m);
-  const int nw = blockDim.x >> 5;
-  if (nw > 1) {
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+  const int lane = threadIdx.x & 31;
+  int nw = blockDim.x >> 5;
+  if constexpr (kParts > 1) {
+    if (lane < kParts)
+      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(
+                       map_block(smem_u32(red + block_of_row<kParts>() * nw + (threadIdx.x >> 5)), lane)),
+                   "r"(m)
+                   : "memory");
+    row_sync();
+    nw *= kParts;
+  } else if (nw > 1) {
+    if (lane == 0) red[threadIdx.x >> 5] = m;
     __syncthreads();
-    const int lane = threadIdx.x & 31;
-    m = __reduce_max_sync(0xFFFFFFFFu, lane < nw ? red[lane] : 0u);
+  }
+  if (nw > 1) {
+    m = lane < nw ? red[lane] : 0u;
+    for (int i = lane + 32; kParts > 1 && i < nw; i += 32) m = max(m, red[i]);
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
   }
   return __uint_as_float(m << 16);
 }
 
-// One block per row, kVec vectors of 8 elements a thread (blockDim * kVec >=
-// K / 8): the row stays in registers from its one read to the codes.
-template <int kVec, int kMaxThreads, int kMinBlocks, bool kC16>
+// kParts blocks (a cluster) per row, kVec vectors of 8 elements a thread
+// (kParts * blockDim * kVec >= K / 8): the row stays in registers from its one
+// read to the codes.
+template <int kVec, int kParts, int kMaxThreads, int kMinBlocks, bool kC16>
 __global__ void __launch_bounds__(kMaxThreads, kMinBlocks) add_rmsnorm_kernel(const AddNormParams p) {
-  __shared__ float2 red[32];
-  __shared__ uint32_t redm[32];
+  __shared__ float2 red[32 * kParts];
+  __shared__ uint32_t redm[32 * kParts];
+  if constexpr (kParts > 1) {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  }
   grid_dep_wait();     // x and r come from earlier kernels, which may still read h or q
   grid_dep_launch();
   const int nvec = static_cast<int>(p.K / 8);
-  const int64_t base = static_cast<int64_t>(blockIdx.x) * p.K;
+  const int64_t row = blockIdx.x / kParts;
+  const int64_t base = row * p.K;
   // h may be x or r itself: plain loads, every element read before its thread writes it
   const uint4* xr = reinterpret_cast<const uint4*>(p.x + base);
   const uint4* rr = reinterpret_cast<const uint4*>(p.r + base);
@@ -338,8 +389,8 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks) add_rmsnorm_kernel(co
   uint4* yr = p.y ? reinterpret_cast<uint4*>(p.y + base) : nullptr;
   void* qr = kC16 ? static_cast<void*>(static_cast<uint16_t*>(p.q) + base)
                   : static_cast<void*>(static_cast<int8_t*>(p.q) + base);
-  const int tid = threadIdx.x;
-  const int step = blockDim.x;
+  const int step = blockDim.x * kParts;
+  const int tid = block_of_row<kParts>() * blockDim.x + threadIdx.x;   // among the row's threads
 
   uint4 h[kVec];
   {
@@ -360,7 +411,11 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks) add_rmsnorm_kernel(co
     if (v < nvec) hr[v] = h[i];
     sumsq8(h[i], s2, c2);
   }
-  const Rstd rs = block_rstd(s2, c2, red, p);
+  if constexpr (kParts > 1) {   // the row's blocks have all started: their shared memory can be written
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+  const Rstd rs = block_rstd<kParts>(s2, c2, red, p);
   const Bracket norm(rs.hi);
   uint32_t m2 = 0;
 #pragma unroll
@@ -372,9 +427,9 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks) add_rmsnorm_kernel(co
       if (yr) yr[v] = h[i];
     }
   }
-  const float amax = block_absmax(m2, redm);
+  const float amax = block_absmax<kParts>(m2, redm);
   const float s = __fdiv_rn(amax, 127.0f);
-  if (tid == 0) p.s[blockIdx.x] = s;
+  if (tid == 0) p.s[row] = s;
   const bool zero = amax == 0.0f;
   const Bracket inv(zero ? 0.0f : __frcp_rn(s));
   const bool divide = !zero && !(s >= 0x1p-120f);
@@ -408,7 +463,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_long_kernel(const AddNormPar
     hr[v] = h;
     sumsq8(h, s2, c2);
   }
-  const Rstd rs = block_rstd(s2, c2, red, p);
+  const Rstd rs = block_rstd<1>(s2, c2, red, p);
   const Bracket norm(rs.hi);
   uint32_t m2 = 0;
   for (int64_t v = threadIdx.x; v < nvec; v += blockDim.x) {
@@ -416,7 +471,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_long_kernel(const AddNormPar
     m2 = absmax2(absmax2(absmax2(absmax2(m2, z.x), z.y), z.z), z.w);
     if (yr) yr[v] = z;
   }
-  const float amax = block_absmax(m2, redm);
+  const float amax = block_absmax<1>(m2, redm);
   const float s = __fdiv_rn(amax, 127.0f);
   if (threadIdx.x == 0) p.s[blockIdx.x] = s;
   const bool zero = amax == 0.0f;
@@ -432,24 +487,36 @@ cudaError_t launch_rows(const AddNormParams& p, int64_t M, int sm_count, cudaStr
   const dim3 grid(static_cast<unsigned>(M));
   if (nvec > 4096)
     return launch_pdl(add_rmsnorm_long_kernel<kC16>, grid, dim3(1024), 0, stream, p);
-  auto threads = [&](int vec) {
+  auto threads = [&](int vec) {   // of a block with nvec / vec of them, in whole warps
     return dim3(static_cast<unsigned>((((nvec + vec - 1) / vec) + 31) / 32 * 32));
   };
   auto launch = [&](auto kernel, int vec) { return launch_pdl(kernel, grid, threads(vec), 0, stream, p); };
-  // As few vectors a thread as the row's threads allow while every row has an
-  // SM of its own (the row's latency is the call's).
-  if (M <= sm_count && nvec <= 1024) return launch(add_rmsnorm_kernel<1, 1024, 1, kC16>, 1);
-  if (M <= sm_count && nvec <= 2048) return launch(add_rmsnorm_kernel<2, 1024, 1, kC16>, 2);
+  auto launch_parts = [&](auto kernel, int vec, int parts) {
+    return launch_cluster_pdl(kernel, dim3(static_cast<unsigned>(M * parts)), threads(vec * parts), 0, parts, stream,
+                              p);
+  };
+  // As few vectors a thread as the row's threads allow while all rows run at
+  // one time (the row's latency is the call's), those of long rows in several
+  // blocks: 8 x 17408 3.7 us in four blocks a row and 5.9 in one, 152 x 17408 8.6
+  // in two and 10.2 in one.  In four while half the SMs, or for blocks of which
+  // two fit one all of them, take the clusters (38 x 17408 5.5 us, in one block
+  // 7.9; 38 x 32768 10.1 and 9.3); in two above 16384 (152 x 12288 7.4 us, in one
+  // block 6.9) and up to 18432.
+  if (M <= sm_count && nvec <= 1024) return launch(add_rmsnorm_kernel<1, 1, 1024, 1, kC16>, 1);
+  if (M * 8 <= sm_count || (M * 4 <= sm_count && nvec <= 2304))
+    return launch_parts(add_rmsnorm_kernel<1, 4, 1024, 1, kC16>, 1, 4);
+  if (M <= sm_count && nvec <= 2048) return launch(add_rmsnorm_kernel<2, 1, 1024, 1, kC16>, 2);
+  if (M <= sm_count && nvec <= 2304) return launch_parts(add_rmsnorm_kernel<2, 2, 576, 2, kC16>, 2, 2);
   // Two while all rows' blocks run at one time (512 x 5120: 7.6 us, with four
   // 9.8) and for short rows (8192 x 2048: 24.9 and 26.6); else four, which
   // share the reductions' instructions (8192 x 5120: 55.4, with two 57.6).
   if (nvec <= 320 || (nvec <= 640 && M <= 4 * static_cast<int64_t>(sm_count)))
-    return launch(add_rmsnorm_kernel<2, 320, 4, kC16>, 2);
+    return launch(add_rmsnorm_kernel<2, 1, 320, 4, kC16>, 2);
   // Blocks of 288 to 576 threads within 56 registers a thread, so that two
   // share an SM: 4096 x 17408 99.6 us, one an SM 120.7; shorter rows are faster
   // with 64 registers.
-  if (nvec > 1152 && nvec <= 2304) return launch(add_rmsnorm_kernel<4, 576, 2, kC16>, 4);
-  return launch(add_rmsnorm_kernel<4, 1024, 1, kC16>, 4);
+  if (nvec > 1152 && nvec <= 2304) return launch(add_rmsnorm_kernel<4, 1, 576, 2, kC16>, 4);
+  return launch(add_rmsnorm_kernel<4, 1, 1024, 1, kC16>, 4);
 }
 
 }  // namespace
