@@ -67,7 +67,7 @@ def _build_calls() -> None:
     for path in headers:
         cmd += ["-isystem", path]
     cmd += [os.path.join(CSRC, "torch_calls.cpp"), "-o", tmp, "-L", os.path.join(base, "lib"),
-            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for torch_calls.cpp:\n{r.stdout}\n{r.stderr}")

@@ -12,7 +12,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -117,7 +117,7 @@ const Tensor* lead(PyObject* o, const char* name, std::initializer_list<ScalarTy
 }
 
 Tensor fresh(at::IntArrayRef shape, ScalarType type, const Tensor& like) {
-  return at::empty(shape, at::TensorOptions().dtype(type).device(like.device()));
+  return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
 }
 
 // An output: the one given, else a new one; false with an error raised.
