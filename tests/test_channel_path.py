@@ -435,8 +435,8 @@ def _check_logits(x, kw, bf16, in_place=False):
     (1, 8, 3, 2, True), (1, 1000, None, None, False), (2, 1000, 0, 0, True), (3, 4104, 1, 1, False),
     (5, 8200, 700, 9, True), (2, 50264, 300, 600, True), (1, 248320, 2000, 16, True), (33, 50264, 515, None, False),
     (3, 151936, None, 40, True), (160, 2056, 64, 5, True), (400, 4096, 20, 3, True), (2, 400008, 3000, 30, True),
-    # more touched tokens than a window of counters, more generated ones than the queue, many bias rounds
-    (2, 9000, 30000, 1700, True), (330, 6000, 5000, 3, False),
+    # more touched tokens than the table takes: windows of them; many bias entries
+    (2, 9000, 30000, 1700, True), (330, 6000, 5000, 3, False), (1, 4096, 20000, 9000, True), (3, 40000, 60000, 0, False),
     # slices of several parts
     (10, 700008, 900, 20, True)])
 def test_adjusted_logits(gpu, M, V, L, B, mask, bf16):

@@ -14,22 +14,18 @@
 // chain of steps below.  A row's vocabulary is cut between the blocks of a
 // cluster.  Without penalties and biases a block streams its slice through
 // registers.  With them it brings the slice into shared memory by one bulk
-// copy, and while that is on its way
-//   1. looks through the history (4 bytes a token, from L2), sets a bit for
-//      each token of its own slice and notes it in a queue;
-//   2. counts the generated ones of the queue.  A token's counter is its rank
-//      among the set bits, so the counters take 8 KB, where a counter for each
-//      token of the slice would take as much as the slice itself;
-// then, in shared memory,
-//   3. adjusts the touched tokens from their list, every thread with one, and
-//      the biased ones from their entries, of those with one id the last;
-//   4. masks, compares and writes out the slice.
-// 96 rows of 248,320 bf16 logits with 8192 tokens of history each: 40 us,
-// against 15 us of traffic; 17 us without rules.  (Streaming through registers
-// with the touched tokens adjusted in global memory afterwards took 43 to 66
-// us, in several forms: the steps wait for one another, and the scattered
-// 2-byte accesses cost as much as the stream.)
-// Integer counts and a maximum do not depend on the order of the atomics.  The
+// copy, and while that is on its way looks through the history (4 bytes a
+// token, from L2) and the bias ids for tokens of its own slice: each is entered
+// once in a hash table, with how often it was generated and the last bias entry
+// that names it.  Then, in shared memory, every entry's logit is adjusted, and
+// the slice is masked, compared and written out.
+// 96 rows of 248,320 bf16 logits with 8192 tokens of history each: 35.5 us,
+// against 15 us of traffic (two and a half rounds of blocks, of whose 9.5 us the
+// history takes 3 and the way out 2.5; 17 us without rules); one row with 2000
+// tokens 5.1 us.  (Counters by each token's rank among bits set in a bit map,
+// and lists built from it, took 40.1 and 6.0 us; streaming through registers with
+// the touched tokens adjusted in global memory afterwards 43 to 66.)
+// Counts and maxima of integers do not depend on the order of the atomics.  The
 // blocks' best values meet in the first one's shared memory, so there is no
 // workspace.
 #include <cuda_bf16.h>
@@ -45,18 +41,10 @@ namespace {
 constexpr int kLThreads = 512;
 constexpr int kLWarps = kLThreads / 32;
 constexpr int kMaxSplits = 16;
-constexpr int kSliceBytes = 81920;  // of the logits that a block holds in shared memory at a time, at most
-constexpr int kWindow = 2048;       // touched tokens counted at a time
-constexpr int kQueue = 2048;        // queued tokens of the history
-
-// A bit a token, in shared memory.
-struct Bits {
-  uint32_t* w;
-  __device__ __forceinline__ void set(uint32_t i) const { atomicOr(w + (i >> 5), 1u << (i & 31u)); }
-  __device__ __forceinline__ void unset(uint32_t i) const { atomicAnd(w + (i >> 5), ~(1u << (i & 31u))); }
-  __device__ __forceinline__ bool get(uint32_t i) const { return w[i >> 5] >> (i & 31u) & 1u; }
-  __device__ __forceinline__ uint32_t vec(int j) const { return reinterpret_cast<const uint8_t*>(w)[j]; }   // 8 tokens
-};
+constexpr int kSliceBytes = 65536;  // of the logits that a block holds in shared memory at a time, at most
+constexpr int kMaxSlots = 4096;     // of the hash table: with the slice, two blocks an SM
+constexpr int kProbes = 32;         // slots that an entry is tried in
+constexpr uint32_t kFree = 0xFFFFFFFFu;
 
 struct LogitParams {
   const void* logits;
@@ -75,7 +63,8 @@ struct LogitParams {
   void* out;
   int32_t* argmax;
   int64_t slice;         // tokens of one block, a multiple of 8
-  int part;              // tokens counted at a time, a multiple of 8
+  int part;              // tokens held at a time, a multiple of 8
+  int slots;             // of the table, a power of two of at least kLThreads
   int splits;            // blocks of a row = cluster size
   int* err;
 };
@@ -162,18 +151,15 @@ struct Vec8 {
   }
 };
 
-// Shared memory of the rules, after the slice: the bits of tokens in the
-// history and of biased ones, the rank of each bit word's first bit, a window's
-// counters and list, the queue, and a round's bias ids.
-__host__ __device__ inline int bits_bytes(int part) { return (part / 8 + 15) / 16 * 16; }
-__host__ __device__ inline int rank_bytes(int part) { return (part / 16 + 2 + 15) / 16 * 16; }
-__host__ __device__ inline int rule_bytes(int part, int elem) {
-  return part * elem + 2 * bits_bytes(part) + rank_bytes(part) + kWindow * 4 + kWindow * 2 + kQueue * 4 + kLThreads * 4;
-}
+// Shared memory of the rules: the slice, then the table: the tokens, their
+// occurrences (2 for each generated one, 1 for all in the prompt) and the last
+// bias entries.
+__host__ __device__ inline int rule_bytes(int part, int elem, int slots) { return part * elem + slots * 12; }
 
+// (fence_barrier_init has published the barrier, all that this announces)
 __device__ __forceinline__ void cluster_arrive() {
   __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
@@ -182,26 +168,26 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
   return r;
 }
 
+// Brings thread tid's share of [p, p + bytes) into L2, the line of p + 128 tid.
+__device__ __forceinline__ void prefetch_share(const void* p, int64_t bytes, int tid) {
+  const int64_t at = 128 * static_cast<int64_t>(tid);
+  if (at < bytes) asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(p) + at));
+}
+
 template <bool kF32, bool kRules, bool kMasked>
 __global__ void __launch_bounds__(kLThreads, kRules ? 2 : 3) adjust_logits_kernel(const LogitParams p) {
   constexpr int kAhead = kF32 ? 2 : 4;       // vectors in flight a thread
   constexpr int kE = kF32 ? 2 : 1;           // uint4 of a vector
   extern __shared__ uint4 smem4[];
   uint8_t* const smem = reinterpret_cast<uint8_t*>(smem4);
-  uint8_t* const bits = smem + p.part * (kF32 ? 4 : 2);   // the slice's logits come first
-  const Bits seen{reinterpret_cast<uint32_t*>(bits)};
-  const Bits biased{reinterpret_cast<uint32_t*>(bits + bits_bytes(p.part))};
-  uint16_t* const ranks = reinterpret_cast<uint16_t*>(bits + 2 * bits_bytes(p.part));
-  uint32_t* const counts = reinterpret_cast<uint32_t*>(bits + 2 * bits_bytes(p.part) + rank_bytes(p.part));
-  uint16_t* const list = reinterpret_cast<uint16_t*>(counts + kWindow);
-  uint32_t* const queue = reinterpret_cast<uint32_t*>(list + kWindow);
-  int32_t* const ids = reinterpret_cast<int32_t*>(queue + kQueue);
+  uint32_t* const key = reinterpret_cast<uint32_t*>(smem + p.part * (kF32 ? 4 : 2));   // the slice's logits come first
+  uint32_t* const occurs = key + p.slots;
+  int32_t* const entry = reinterpret_cast<int32_t*>(occurs + p.slots);
   __shared__ Best red[kLWarps];
   __shared__ Best others[kMaxSplits];        // rank 0: the other blocks' best values
   __shared__ uint64_t others_here, slice_here;
-  __shared__ int queued;
   __shared__ int abort_flag;
-  __shared__ int warp_sums[kLWarps];
+  __shared__ int too_full;
   const int tid = threadIdx.x;
   const int lane = tid & 31;
   const int64_t m = blockIdx.x / p.splits;
@@ -214,7 +200,7 @@ __global__ void __launch_bounds__(kLThreads, kRules ? 2 : 3) adjust_logits_kerne
   const uint8_t* mask = kMasked ? p.allowed + m * p.mask_stride : nullptr;
   if (tid == 0) {
     abort_flag = 0;
-    queued = 0;
+    too_full = 0;
     mbar_init(smem_u32(&others_here), 1);
     mbar_init(smem_u32(&slice_here), 1);
     fence_barrier_init();
@@ -227,11 +213,23 @@ __global__ void __launch_bounds__(kLThreads, kRules ? 2 : 3) adjust_logits_kerne
     mbar_arrive_expect_tx(bar, n * (kF32 ? 4 : 2));
     bulk_load(smem_u32(smem), row_in + v0 * (kF32 ? 4 : 2), n * (kF32 ? 4 : 2), bar);
   };
-  auto zero_bits = [&]() {
-    for (int i = tid; i < 2 * bits_bytes(p.part) / 16; i += kLThreads)
-      reinterpret_cast<uint4*>(bits)[i] = make_uint4(0, 0, 0, 0);
+  auto clear_table = [&]() {
+    for (int i = tid; i < p.slots / 4; i += kLThreads) {
+      reinterpret_cast<uint4*>(key)[i] = make_uint4(kFree, kFree, kFree, kFree);
+      reinterpret_cast<uint4*>(occurs)[i] = make_uint4(0, 0, 0, 0);
+      reinterpret_cast<uint4*>(entry)[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
+    }
   };
-  if constexpr (kRules) zero_bits();
+  // What small inputs the block reads comes into L2 while an earlier kernel
+  // still runs (their values are read after it).
+  if (kMasked && s0 < V) prefetch_share(mask + s0 / 8, (s1 - s0) / 8, tid);
+  if constexpr (kRules) {
+    if (p.B > 0) {
+      prefetch_share(p.bias_ids + m * p.B, 4LL * p.B, tid);
+      prefetch_share(p.bias + m * p.B, 4LL * p.B, tid);
+    }
+    clear_table();
+  }
   grid_dep_launch();
   grid_dep_wait();
   int total = 0, prompt = 0;
@@ -258,10 +256,10 @@ __global__ void __launch_bounds__(kLThreads, kRules ? 2 : 3) adjust_logits_kerne
 
     if constexpr (kRules) {
       if (parts_done > 0) {
-        __syncthreads();   // the previous part's slice and bits are read
-        zero_bits();
+        __syncthreads();   // the previous part's slice and table are read
+        clear_table();
         if (tid == 0) {
-          queued = 0;
+          too_full = 0;
           fence_proxy_async_smem();
         }
       }
@@ -287,50 +285,6 @@ __global__ void __launch_bounds__(kLThreads, kRules ? 2 : 3) adjust_logits_kerne
       auto bias_place = [&](int j) {   // of entry j, n or more where it is not in the part
         return static_cast<uint32_t>(__ldg(p.bias_ids + m * p.B + j)) - static_cast<uint32_t>(v0);
       };
-      history([&](uint32_t at, bool made) {
-        seen.set(at);
-        if (made) {
-          const int slot = atomicAdd(&queued, 1);
-          if (slot < kQueue) queue[slot] = at;
-        }
-      });
-      for (int i = tid; i < p.B; i += kLThreads) {
-        const uint32_t at = bias_place(i);
-        if (at < n) biased.set(at);
-      }
-      __syncthreads();
-      // ranks: each thread's run of bit words, summed across the block
-      const int words = (static_cast<int>(n) + 31) / 32;
-      const int run = (words + kLThreads - 1) / kLThreads;
-      int sum = 0;
-      for (int k = 0; k < run; ++k)
-        if (run * tid + k < words) sum += __popc(seen.w[run * tid + k]);
-      int incl = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-        if (lane >= o) incl += up;
-      }
-      if (lane == 31) warp_sums[tid >> 5] = incl;
-      __syncthreads();
-      int base = incl - sum;
-      int touched = 0;
-#pragma unroll
-      for (int w = 0; w < kLWarps; ++w) {
-        const int t = warp_sums[w];
-        touched += t;
-        if (w < (tid >> 5)) base += t;
-      }
-      for (int k = 0; k < run; ++k) {
-        const int i = run * tid + k;
-        if (i < words) {
-          ranks[i] = static_cast<uint16_t>(base);
-          base += __popc(seen.w[i]);
-        }
-      }
-      auto rank_of = [&](uint32_t at) {
-        return ranks[at >> 5] + __popc(seen.w[at >> 5] & ((1u << (at & 31u)) - 1u));
-      };
       auto logit = [&](uint32_t at) {
         return kF32 ? reinterpret_cast<const float*>(smem)[at]
                     : __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(smem)[at]) << 16);
@@ -339,59 +293,62 @@ __global__ void __launch_bounds__(kLThreads, kRules ? 2 : 3) adjust_logits_kerne
         if constexpr (kF32) reinterpret_cast<float*>(smem)[at] = x;
         else reinterpret_cast<uint16_t*>(smem)[at] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
       };
-      // windows of the touched tokens' ranks: one, unless the history touches
-      // more than 2048 of the part's tokens
-      for (int w0 = 0; w0 == 0 || w0 < touched; w0 += kWindow) {
-        __syncthreads();   // ranks are written; the previous window is read
-        for (int i = tid; i < kWindow / 4; i += kLThreads) reinterpret_cast<uint4*>(counts)[i] = make_uint4(0, 0, 0, 0);
-        for (int i = tid; i < words; i += kLThreads) {
-          int r = static_cast<int>(ranks[i]) - w0;
-          for (uint32_t left = seen.w[i]; left != 0u; left &= left - 1u, ++r)
-            if (r >= 0 && r < kWindow) list[r] = static_cast<uint16_t>(32 * i + __ffs(left) - 1);
+      // The table takes the tokens at lo .. lo + span of the part: all of them
+      // at first, hashed; if they are too many for it, as many as it has slots
+      // at a time, each in its own.
+      uint32_t lo = 0, span = n;
+      const int shift = 32 - __ffs(p.slots) + 1;
+      bool hashed = true;
+      auto slot_of = [&](uint32_t at) {
+        uint32_t slot = hashed ? (at * 0x9E3779B1u) >> shift : at - lo;   // 2^32 / golden ratio
+        for (int i = 0; i < kProbes; ++i) {
+          const uint32_t was = atomicCAS(key + slot, kFree, at);
+          if (was == kFree || was == at) return static_cast<int>(slot);
+          slot = (slot + 1u) & static_cast<uint32_t>(p.slots - 1);
         }
+        too_full = 1;
+        return -1;
+      };
+      const uint32_t first_bias = tid < p.B ? bias_place(tid) : n;   // on its way beside the history
+      for (;;) {
+        history([&](uint32_t at, bool made) {
+          if (at - lo >= span) return;
+          const int slot = slot_of(at);
+          if (slot < 0) return;
+          if (made) atomicAdd(occurs + slot, 2u);
+          else atomicOr(occurs + slot, 1u);
+        });
+        for (int i = tid; i < p.B; i += kLThreads) {
+          const uint32_t at = i == tid ? first_bias : bias_place(i);
+          if (at >= n || at - lo >= span) continue;
+          const int slot = slot_of(at);
+          if (slot >= 0) atomicMax(entry + slot, i);
+        }
+        if (lo == 0 && span == n && !mbar_wait(smem_u32(&slice_here), parts_done & 1, ctx, 81)) abort_flag = 1;
         __syncthreads();
-        auto count = [&](uint32_t at) {
-          const uint32_t r = static_cast<uint32_t>(rank_of(at) - w0);
-          if (r < static_cast<uint32_t>(kWindow)) atomicAdd(counts + r, 1u);
-        };
-        if (queued <= kQueue) {
-          for (int i = tid; i < queued; i += kLThreads) count(queue[i]);
-        } else {   // more than the queue holds
-          history([&](uint32_t at, bool made) {
-            if (made) count(at);
-          });
-        }
-        if (w0 == 0 && !mbar_wait(smem_u32(&slice_here), parts_done & 1, ctx, 81)) abort_flag = 1;
-        __syncthreads();
-        for (int i = tid; i < touched - w0 && i < kWindow; i += kLThreads) {
-          const uint32_t at = list[i];
-          if (!biased.get(at)) put(at, penalized(logit(at), counts[i], true, rules));
-        }
-        // Biased tokens, from the last entries to the first: an entry applies
-        // unless a later one of its round has its id, or an earlier round
-        // (later entries) has unset the bit.
-        for (int c1 = p.B; c1 > 0; c1 -= kLThreads) {
-          const int j = c1 - kLThreads + tid;
-          const int first = c1 < kLThreads ? kLThreads - c1 : 0;   // threads below it have no entry
-          __syncthreads();   // bits unset by, and ids of, the round before
-          const uint32_t at = j >= 0 ? bias_place(j) : 0xFFFFFFFFu;
-          ids[tid] = static_cast<int32_t>(at);
-          bool open = at < n && biased.get(at);
-          uint32_t r = 0;
-          const bool hist = open && seen.get(at);
-          if (hist) r = static_cast<uint32_t>(rank_of(at) - w0);
-          open = open && (hist ? r < static_cast<uint32_t>(kWindow) : w0 == 0);
-          __syncthreads();
-          if (open)
-            for (int k = max(tid + 1, first); k < kLThreads; ++k)
-              if (ids[k] == static_cast<int32_t>(at)) open = false;
-          __syncthreads();
-          if (open) {
-            biased.unset(at);
-            const float x = hist ? penalized(logit(at), counts[r], true, rules) : logit(at);
-            put(at, __fadd_rn(x, __ldg(p.bias + m * p.B + j)));
+        const bool again = hashed && too_full != 0;
+        if (!again) {
+          uint32_t mine = 0;   // this thread's slots that hold a token
+#pragma unroll
+          for (int k = 0; k < kMaxSlots / kLThreads; ++k)
+            if (k * kLThreads < p.slots && key[k * kLThreads + tid] != kFree) mine |= 1u << k;
+          for (; mine != 0u; mine &= mine - 1u) {
+            const int slot = (__ffs(mine) - 1) * kLThreads + tid;
+            const uint32_t at = key[slot];
+            const uint32_t n_seen = occurs[slot];
+            const int j = entry[slot];
+            float x = penalized(logit(at), n_seen >> 1, n_seen != 0u, rules);
+            if (j >= 0) x = __fadd_rn(x, __ldg(p.bias + m * p.B + j));
+            put(at, x);
           }
+          if (hashed || lo + span >= n) break;
+          lo += span;
         }
+        hashed = false;
+        span = min(static_cast<uint32_t>(p.slots), n - lo);
+        __syncthreads();   // the table is read
+        clear_table();
+        __syncthreads();
       }
       __syncthreads();
       if (abort_flag) break;   // the slice did not arrive; the error word says so
@@ -470,13 +427,13 @@ cudaError_t launch_kind(const LogitParams& p, int64_t M, cudaStream_t stream) {
   const uint64_t bit = 1ull << (dev & 63);
   if (!(ready.load(std::memory_order_acquire) & bit)) {
     if (kRules) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           rule_bytes(kSliceBytes / (kF32 ? 4 : 2), kF32 ? 4 : 2));
+                                           rule_bytes(kSliceBytes / (kF32 ? 4 : 2), kF32 ? 4 : 2, kMaxSlots));
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_release);
   }
   return launch_cluster_pdl(kernel, dim3(static_cast<unsigned>(M * p.splits)), dim3(kLThreads),
-                            kRules ? rule_bytes(p.part, kF32 ? 4 : 2) : 0, p.splits, stream, p);
+                            kRules ? rule_bytes(p.part, kF32 ? 4 : 2, p.slots) : 0, p.splits, stream, p);
 }
 
 template <bool kF32>
@@ -494,7 +451,7 @@ cudaError_t launch_adjust_logits(const LogitArgs& a, int* err, int sm_count, cud
   const bool penalties = a.repetition != nullptr || a.presence != nullptr || a.frequency != nullptr;
   LogitParams p{a.logits, a.V, penalties ? static_cast<int>(a.L) : 0, static_cast<int>(a.B), a.tokens, a.prompt_len,
                 a.total_len, a.repetition, a.presence, a.frequency, a.bias_ids, a.bias,
-                reinterpret_cast<const uint8_t*>(a.allowed), (a.V + 31) / 32 * 4, a.out, a.argmax, 0, 0, 1, err};
+                reinterpret_cast<const uint8_t*>(a.allowed), (a.V + 31) / 32 * 4, a.out, a.argmax, 0, 0, kLThreads, 1, err};
   const bool rules = p.L > 0 || p.B > 0;
   const int64_t most = rules ? kSliceBytes / (a.f32 ? 4 : 2) : a.V;
   // Clusters of 16 find room late once a few of them are about (33 rows of
@@ -505,6 +462,8 @@ cudaError_t launch_adjust_logits(const LogitArgs& a, int* err, int sm_count, cud
     p.splits *= 2;
   p.slice = ((a.V + p.splits - 1) / p.splits + 7) / 8 * 8;
   p.part = static_cast<int>(p.slice < most ? p.slice : most);
+  // twice the entries where it can have that
+  while (p.slots < kMaxSlots && p.slots < 2 * (static_cast<int64_t>(p.L) + p.B)) p.slots *= 2;
   return a.f32 ? launch_type<true>(p, a.M, stream) : launch_type<false>(p, a.M, stream);
 }
 
