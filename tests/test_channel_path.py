@@ -225,6 +225,7 @@ CHANNEL_SHAPES = [
     (1, 128, 8), (1, 5120, 1024), (3, 384, 40), (7, 256, 200), (8, 640, 64), (8, 1152, 136), (9, 128, 72),
     (16, 1280, 1000), (17, 512, 264), (31, 2176, 328), (33, 1024, 128), (40, 1152, 264), (63, 384, 512),
     (64, 5120, 256), (65, 2048, 520), (96, 17408, 264), (97, 256, 8), (128, 1024, 136), (129, 640, 1288),
+    (9, 5120, 5120), (20, 17408, 1032), (130, 5120, 1032), (33, 1152, 3208), (513, 130944, 8), (1030, 128, 8),
     (200, 3200, 392), (255, 128, 256), (257, 2304, 264), (300, 5120, 520), (513, 1152, 776), (1030, 256, 264)]
 
 
@@ -284,7 +285,9 @@ def test_channel_product_of_many_tiles(gpu, M, K, N):
 TILED_SHAPES = [
     (16, 5120, 10248), (40, 2304, 8200), (64, 1280, 20488), (24, 10240, 4104), (90, 8192, 2056), (96, 2304, 8200),
     (100, 1152, 20488), (128, 5120, 4104), (120, 17408, 1544), (130, 9344, 2056), (150, 4224, 5128),
-    (200, 17408, 1032), (192, 1152, 10248), (600, 1152, 5128), (513, 130944, 8)]
+    (200, 17408, 1032), (192, 1152, 10248), (600, 1152, 5128), (700, 130944, 8),
+    # few codes
+    (9, 5120, 20488), (12, 5120, 12296), (40, 1536, 20488), (57, 1152, 20488)]
 
 
 @needs_gpu

@@ -94,11 +94,13 @@ __device__ __forceinline__ uint16_t channel_out(int p, float sw, float sa) {
   return __bfloat16_as_ushort(__float2bfloat16_rn(__fmul_rn(__fmul_rn(__int2float_rn(p), sw), sa)));
 }
 
-// kHalves x 32 output channels and 8 tokens a block.
-template <int kHalves, bool kC16>
-__global__ void __launch_bounds__(kSThreads, kHalves == 1 ? 3 : 2) stream_kernel(const ChannelParams p, int splits) {
+// kHalves x 32 output channels and kTiles x 8 tokens a block.
+template <int kHalves, int kTiles, bool kC16>
+__global__ void __launch_bounds__(kSThreads, kHalves * kTiles == 1 ? 3 : 2)
+    stream_kernel(const ChannelParams p, int splits) {
   constexpr int F = 32 * kHalves;
-  constexpr int T = 8;
+  constexpr int T = 8 * kTiles;
+  constexpr int kCodes = kC16 ? 2 : 1;         // uint4 of 16 codes
   constexpr int kPad = F + 4;                  // words of one token's row of partials
   __shared__ __align__(16) int part[T * kPad];
   const int warp = threadIdx.x >> 5;
@@ -136,48 +138,64 @@ __global__ void __launch_bounds__(kSThreads, kHalves == 1 ? 3 : 2) stream_kernel
   grid_dep_wait();
   __syncthreads();
 
-  // this thread's token (the last one again past it: computed and not written)
-  const int64_t mine = m0 + g < p.M ? m0 + g : p.M - 1;
-  const char* abase = static_cast<const char*>(p.act) + (mine * K + 16 * t) * (kC16 ? 2 : 1);
-  uint4 a[2][kC16 ? 2 : 1];
-  auto load_a = [&](uint4 (&to)[kC16 ? 2 : 1], int kb) {
-    const uint4* src = reinterpret_cast<const uint4*>(abase + static_cast<int64_t>(kb) * kKB * (kC16 ? 2 : 1));
-    to[0] = src[0];
-    if constexpr (kC16) to[1] = src[1];
+  // this thread's tokens, one of each tile of 8 (the last one again past it:
+  // computed and not written)
+  const char* abase[kTiles];
+#pragma unroll
+  for (int i = 0; i < kTiles; ++i) {
+    const int64_t mine = m0 + 8 * i + g < p.M ? m0 + 8 * i + g : p.M - 1;
+    abase[i] = static_cast<const char*>(p.act) + (mine * K + 16 * t) * (kC16 ? 2 : 1);
+  }
+  uint4 a[2][kTiles * kCodes];
+  auto load_a = [&](uint4 (&to)[kTiles * kCodes], int kb) {
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) {
+      const uint4* src = reinterpret_cast<const uint4*>(abase[i] + static_cast<int64_t>(kb) * kKB * (kC16 ? 2 : 1));
+#pragma unroll
+      for (int c = 0; c < kCodes; ++c) to[i * kCodes + c] = src[c];
+    }
   };
   if (first < nkb) load_a(a[0], first);
 
-  float acc[2 * kHalves][4];
+  float acc[kTiles][2 * kHalves][4];
 #pragma unroll
-  for (int j = 0; j < 2 * kHalves; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
-  auto flush = [&]() {
+  for (int i = 0; i < kTiles; ++i)
 #pragma unroll
     for (int j = 0; j < 2 * kHalves; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        // row of the 16 x 8 result: channel 4g + 2 (j & 1) + (e >> 1); column: token 2t + (e & 1)
-        const int ch = 32 * (j >> 1) + 4 * g + 2 * (j & 1) + (e >> 1);
-        atomicAdd(&part[(2 * t + (e & 1)) * kPad + ch], __float2int_rn(acc[j][e]));
-        acc[j][e] = 0.0f;
-      }
+      for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.0f;
+  auto flush = [&]() {
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+      for (int j = 0; j < 2 * kHalves; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          // row of the 16 x 8 result: channel 4g + 2 (j & 1) + (e >> 1); column: token 2t + (e & 1)
+          const int ch = 32 * (j >> 1) + 4 * g + 2 * (j & 1) + (e >> 1);
+          atomicAdd(&part[(8 * i + 2 * t + (e & 1)) * kPad + ch], __float2int_rn(acc[i][j][e]));
+          acc[i][j][e] = 0.0f;
+        }
   };
 
   int done = 0;
-  auto step = [&](uint4 (&wc)[4 * kHalves], uint4 (&ac)[kC16 ? 2 : 1], uint4 (&an)[kC16 ? 2 : 1], int kb) {
-    uint32_t b[4][2];          // the token's codes, 4 of K for each product
-    if constexpr (kC16) {
-      const uint32_t c[8] = {ac[0].x, ac[0].y, ac[0].z, ac[0].w, ac[1].x, ac[1].y, ac[1].z, ac[1].w};
+  auto step = [&](uint4 (&wc)[4 * kHalves], uint4 (&ac)[kTiles * kCodes], uint4 (&an)[kTiles * kCodes], int kb) {
+    uint32_t b[kTiles][4][2];          // the tokens' codes, 4 of K for each product
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        b[s][0] = c[2 * s];
-        b[s][1] = c[2 * s + 1];
+    for (int i = 0; i < kTiles; ++i) {
+      if constexpr (kC16) {
+        const uint4 lo = ac[2 * i], hi = ac[2 * i + 1];
+        const uint32_t c[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          b[i][s][0] = c[2 * s];
+          b[i][s][1] = c[2 * s + 1];
+        }
+      } else {
+        const uint32_t c[4] = {ac[i].x, ac[i].y, ac[i].z, ac[i].w};
+#pragma unroll
+        for (int s = 0; s < 4; ++s) biased_u8x4_to_f16x4(c[s] ^ 0x80808080u, b[i][s][0], b[i][s][1]);
       }
-    } else {
-      const uint32_t c[4] = {ac[0].x, ac[0].y, ac[0].z, ac[0].w};
-#pragma unroll
-      for (int s = 0; s < 4; ++s) biased_u8x4_to_f16x4(c[s] ^ 0x80808080u, b[s][0], b[s][1]);
     }
     if (kb + stride < nkb) load_a(an, kb + stride);
 #pragma unroll
@@ -190,8 +208,11 @@ __global__ void __launch_bounds__(kSThreads, kHalves == 1 ? 3 : 2) stream_kernel
         biased_u8x4_to_f16x4(v.y, c1[0], c1[1]);
         biased_u8x4_to_f16x4(v.z, c2[0], c2[1]);
         biased_u8x4_to_f16x4(v.w, c3[0], c3[1]);
-        mma_f16(acc[2 * hf], c0[0], c1[0], c0[1], c1[1], b[s][0], b[s][1]);
-        mma_f16(acc[2 * hf + 1], c2[0], c3[0], c2[1], c3[1], b[s][0], b[s][1]);
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) {
+          mma_f16(acc[i][2 * hf], c0[0], c1[0], c0[1], c1[1], b[i][s][0], b[i][s][1]);
+          mma_f16(acc[i][2 * hf + 1], c2[0], c3[0], c2[1], c3[1], b[i][s][0], b[i][s][1]);
+        }
       }
     if (kb + 2 * stride < nkb) load_w(wc, kb + 2 * stride);
     if (++done == kExactBlocks) {
@@ -240,44 +261,50 @@ __global__ void __launch_bounds__(kSThreads, kHalves == 1 ? 3 : 2) stream_kernel
   if (splits > 1) cluster_sync_all();   // no block leaves while another reads its partials
 }
 
-template <int kHalves, bool kC16>
+template <int kHalves, int kTiles, bool kC16>
 cudaError_t launch_stream(const ChannelParams& p, int splits, cudaStream_t stream) {
   const int64_t ftiles = (p.N + 32 * kHalves - 1) / (32 * kHalves);
-  return launch_cluster_pdl(stream_kernel<kHalves, kC16>,
-                            dim3(static_cast<unsigned>(ftiles * splits), static_cast<unsigned>((p.M + 7) / 8)),
+  const int64_t ttiles = (p.M + 8 * kTiles - 1) / (8 * kTiles);
+  return launch_cluster_pdl(stream_kernel<kHalves, kTiles, kC16>,
+                            dim3(static_cast<unsigned>(ftiles * splits), static_cast<unsigned>(ttiles)),
                             dim3(kSThreads), 0, splits, stream, p, splits);
 }
 
+// Blocks that share K: as many as run at one time with the tiles' others, while
+// a warp's steps get fewer.
+struct StreamSplit {
+  int64_t splits, steps;
+};
+StreamSplit split_stream(int64_t tiles, int64_t slots, int64_t K) {
+  const int64_t nkb = K / kKB;
+  int64_t most = slots / tiles;
+  most = most < 1 ? 1 : most > kMaxSplits ? kMaxSplits : most;
+  const int64_t steps = (nkb + kSWarps * most - 1) / (kSWarps * most);
+  return {(nkb + kSWarps * steps - 1) / (kSWarps * steps), steps};
+}
+
+// 16 tokens a block: two blocks an SM (three of 85 registers a thread spill:
+// 16 x 5120 x 1024 6.2 us instead of 4.1).
+int64_t stream16_tiles(int64_t M, int64_t N) { return (N + 31) / 32 * ((M + 15) / 16); }
+
 template <bool kC16>
 cudaError_t launch_c(const ChannelParams& p, int sm_count, cudaStream_t stream) {
-  // 32 channels a block while all blocks run at one time (three an SM), K split
-  // as far as that holds and a warp's steps get fewer: at K = 5120, N = 5120 in 2
-  // parts 8.3 us (1 part 12.1, 5 parts 10.0), N = 10240 unsplit 12.8 (2 parts
-  // 16.6; 64 channels 17.2).  Blocks beyond one round of them cost more than
-  // they hide, so above that 64 channels, unsplit: N = 34816 32.6 us (32
-  // channels 38).
-  const int64_t tiles = (p.N + 31) / 32 * ((p.M + 7) / 8);
+  if (p.M > 8) {
+    const StreamSplit s = split_stream(stream16_tiles(p.M, p.N), 2LL * sm_count, p.K);
+    return launch_stream<1, 2, kC16>(p, static_cast<int>(s.splits), stream);
+  }
+  // 32 channels a block while all blocks run at one time (three an SM): at K =
+  // 5120, N = 5120 in 2 parts of K 8.3 us (1 part 12.1, 5 parts 10.0), N = 10240
+  // unsplit 12.8 (2 parts 16.6; 64 channels 17.2).  Blocks beyond one round of
+  // them cost more than they hide, so above that 64 channels, unsplit: N = 34816
+  // 32.6 us (32 channels 38).
+  const int64_t tiles = (p.N + 31) / 32;
   const int64_t slots = 3LL * sm_count;
-  if (tiles > slots) return launch_stream<2, kC16>(p, 1, stream);
-  const int64_t nkb = p.K / kKB;
-  int64_t most = slots / tiles;
-  if (most > kMaxSplits) most = kMaxSplits;
-  const int64_t steps = (nkb + kSWarps * most - 1) / (kSWarps * most);
-  const int64_t splits = (nkb + kSWarps * steps - 1) / (kSWarps * steps);
-  return launch_stream<1, kC16>(p, static_cast<int>(splits), stream);
+  if (tiles > slots) return launch_stream<2, 1, kC16>(p, 1, stream);
+  return launch_stream<1, 1, kC16>(p, static_cast<int>(split_stream(tiles, slots, p.K).splits), stream);
 }
 
 // ------------------------------------------------------- larger batches
-
-// Batches that take the streaming kernel: up to 8 tokens always, and more
-// where its pass over the weights for each 8 tokens (1.5 us and 5.2 MB a us)
-// takes less than the pairs' launch and pipeline (4.5 us and 1 us for 600 of
-// K): 16 x 5120 x 5120 11.9 us against 14.7, 32 x 5120 x 1024 6.2 against 12.3;
-// but 16 x 5120 x 10240 23.7 against 19.8, 32 x 1024 x 8192 7.9 against 6.3.
-bool streams(int64_t M, int64_t N, int64_t K) {
-  const int64_t passes = (M + 7) / 8;
-  return passes == 1 || (passes <= 64 && passes * N * K <= 15600000 + 8667 * K);
-}
 
 constexpr size_t kCounterBytes = 1024;    // arrival counters of the cut tiles
 constexpr int64_t kMinShare = 8;          // K steps of a pair's share of the cut tiles, at least
@@ -335,23 +362,64 @@ PairPlan plan_pair(int64_t M, int64_t N, int64_t K, int sm_count) {
   return pl;
 }
 
-size_t image_bytes(int64_t M, int64_t K) { return static_cast<size_t>(M) * static_cast<size_t>(K) * 2; }
+// Batches that take the streaming kernel: up to 8 tokens always, and more where
+// its blocks of 16 all run at one time and are done first.  A step of their warps
+// takes 0.95 us, mostly latency; a K step of a pair 0.37 us at least, and cut
+// tiles meet again after 5 us and half a one for every part.  Measured: 16 x 5120 x
+// 5120 10.9 us against 14.6 in pairs, 128 x 5120 x 1024 9.7 and 12.2, 64 x 17408 x
+// 1024 17.4 and 19.5, 16 x 1152 x 8192 4.0 and 6.7; but 16 x 17408 x 5120 33.6 and
+// 26.6, 96 x 17408 x 1024 30.6 and 22.9, 16 x 5120 x 10240 23.2 and 20.1.
+bool streams(int64_t M, int64_t N, int64_t K, int sm_count) {
+  if (M <= 8) return true;
+  const int64_t tiles = stream16_tiles(M, N);
+  if (tiles > 2LL * sm_count) return false;
+  const int64_t stream = 180 + 95 * split_stream(tiles, 2LL * sm_count, K).steps;
+  const PairPlan pl = plan_pair(M, N, K, sm_count);
+  const int64_t steps = (pl.TT * pl.F2 * pl.G + pl.pairs - 1) / pl.pairs;
+  const int64_t parts = pl.cut ? (pl.sk_pairs + pl.sk_tiles - 1) / pl.sk_tiles : 0;
+  return stream < 330 + 37 * steps + (pl.cut ? 480 + 45 * parts : 0);
+}
 
-// Before the pair kernel: the counters to zero and, for int8 codes, their
-// exact fp16 image (16 codes a thread).
-__global__ void __launch_bounds__(256) pair_prepare_kernel(int* counters, const int8_t* __restrict__ q,
+// The pair kernel reads fp16 codes: int8 ones from an image in the workspace,
+// and some small fp16 ones.  Loads through a tensor map of up to 128 KB were slow
+// (12 x 5120 x 34816, 120 KB of codes: 55 us; 13 rows 38; about 0.2 us a K step), so
+// such an image lies in front of memory that makes the map's K 1024 halves of
+// 128 B; the kernel loads none past the codes' own, but what a map describes has
+// to be there.  fp16 codes get it where the preparing kernel runs in any case or
+// the K steps make up for it (24 x 1152 x 8192, 9 steps: 6.7 us without, 9.0 with).
+constexpr int64_t kSmallCodes = 65536;
+constexpr int64_t kMapHalves = 1024;
+bool small_codes(int64_t M, int64_t K) { return M * K <= kSmallCodes; }
+bool has_image(const PairPlan& pl, int64_t M, int64_t K, bool c16) {
+  return !c16 || (small_codes(M, K) && (pl.cut || pl.TT * pl.F2 * pl.G >= 16 * pl.pairs));
+}
+size_t image_bytes(int64_t M, int64_t K) {
+  const int64_t own = M * K * 2;
+  return static_cast<size_t>(small_codes(M, K) ? (M - 1) * K * 2 + kMapHalves * 128 : own);
+}
+static_assert(kMapHalves * 64 >= kSmallCodes, "a row of small codes is no longer than the map's");
+
+// Before the pair kernel: the counters to zero and the codes' fp16 image (16
+// codes a thread).
+template <bool kC16>
+__global__ void __launch_bounds__(256) pair_prepare_kernel(int* counters, const void* __restrict__ q,
                                                            uint16_t* __restrict__ image, int64_t n16) {
   grid_dep_wait();    // the workspace may still be in use, and the codes come from the previous kernel
   grid_dep_launch();
   if (blockIdx.x == 0 && counters != nullptr) counters[threadIdx.x] = 0;
   for (int64_t i = blockIdx.x * static_cast<int64_t>(256) + threadIdx.x; i < n16;
        i += static_cast<int64_t>(gridDim.x) * 256) {
-    const uint4 raw = __ldg(reinterpret_cast<const uint4*>(q) + i);
     uint4 lo, hi;
-    biased_u8x4_to_f16x4(raw.x ^ 0x80808080u, lo.x, lo.y);
-    biased_u8x4_to_f16x4(raw.y ^ 0x80808080u, lo.z, lo.w);
-    biased_u8x4_to_f16x4(raw.z ^ 0x80808080u, hi.x, hi.y);
-    biased_u8x4_to_f16x4(raw.w ^ 0x80808080u, hi.z, hi.w);
+    if constexpr (kC16) {
+      lo = __ldg(static_cast<const uint4*>(q) + 2 * i);
+      hi = __ldg(static_cast<const uint4*>(q) + 2 * i + 1);
+    } else {
+      const uint4 raw = __ldg(static_cast<const uint4*>(q) + i);
+      biased_u8x4_to_f16x4(raw.x ^ 0x80808080u, lo.x, lo.y);
+      biased_u8x4_to_f16x4(raw.y ^ 0x80808080u, lo.z, lo.w);
+      biased_u8x4_to_f16x4(raw.z ^ 0x80808080u, hi.x, hi.y);
+      biased_u8x4_to_f16x4(raw.w ^ 0x80808080u, hi.z, hi.w);
+    }
     reinterpret_cast<uint4*>(image)[2 * i] = lo;
     reinterpret_cast<uint4*>(image)[2 * i + 1] = hi;
   }
@@ -393,20 +461,23 @@ cudaError_t launch_pair(const ChannelGemmArgs& a, int* err, int sm_count, cudaSt
     counters = reinterpret_cast<int*>(ws);
     at = kCounterBytes + pl.part_bytes;
   }
-  if (pl.cut || !a.act_c16) {
-    const int64_t n16 = a.act_c16 ? 0 : a.M * a.K / 16;
-    uint16_t* image = a.act_c16 ? nullptr : reinterpret_cast<uint16_t*>(ws + at);
+  const bool with_image = has_image(pl, a.M, a.K, a.act_c16);
+  if (pl.cut || with_image) {
+    const int64_t n16 = with_image ? a.M * a.K / 16 : 0;
+    uint16_t* image = with_image ? reinterpret_cast<uint16_t*>(ws + at) : nullptr;
     int64_t blocks = (n16 + 255) / 256;
     blocks = blocks < 1 ? 1 : blocks > 4096 ? 4096 : blocks;
-    const cudaError_t e = launch_pdl(pair_prepare_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream,
-                                     counters, static_cast<const int8_t*>(a.act), image, n16);
+    const cudaError_t e = launch_pdl(a.act_c16 ? pair_prepare_kernel<true> : pair_prepare_kernel<false>,
+                                     dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, counters, a.act,
+                                     image, n16);
     if (e != cudaSuccess) return e;
-    if (!a.act_c16) codes = image;
+    if (with_image) codes = image;
   }
   CUtensorMap tw, tx;
   if (!make_map_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_INT32, a.qweight, a.N, a.K / 4, static_cast<uint64_t>(a.N) * 4, 128,
                    32, CU_TENSOR_MAP_SWIZZLE_NONE) ||
-      !make_act_map(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, codes, a.M, a.K, static_cast<uint32_t>(pl.T / 2), 1))
+      !make_act_map(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, codes, a.M, a.K, static_cast<uint32_t>(pl.T / 2), 1,
+                    with_image && small_codes(a.M, a.K) ? kMapHalves : 0))
     return cudaErrorInvalidValue;
   pair::Params p;
   p.s_a = a.s_a;
@@ -436,13 +507,13 @@ cudaError_t launch_pair(const ChannelGemmArgs& a, int* err, int sm_count, cudaSt
 }  // namespace
 
 size_t channel_workspace_bytes(int64_t M, int64_t N, int64_t K, bool c16, int sm_count) {
-  if (streams(M, N, K)) return 0;
+  if (streams(M, N, K, sm_count)) return 0;
   const PairPlan pl = plan_pair(M, N, K, sm_count);
-  return (pl.cut ? kCounterBytes + pl.part_bytes : 0) + (c16 ? 0 : image_bytes(M, K));
+  return (pl.cut ? kCounterBytes + pl.part_bytes : 0) + (has_image(pl, M, K, c16) ? image_bytes(M, K) : 0);
 }
 
 cudaError_t launch_gemm_channel(const ChannelGemmArgs& a, int* err, int sm_count, cudaStream_t stream) {
-  if (!streams(a.M, a.N, a.K)) return launch_pair(a, err, sm_count, stream);
+  if (!streams(a.M, a.N, a.K, sm_count)) return launch_pair(a, err, sm_count, stream);
   const ChannelParams p{a.act, a.s_a, reinterpret_cast<const uint32_t*>(a.qweight), a.s_w, a.y, a.M, a.N, a.K};
   return a.act_c16 ? launch_c<true>(p, sm_count, stream) : launch_c<false>(p, sm_count, stream);
 }
