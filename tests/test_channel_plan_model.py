@@ -9,29 +9,41 @@ import random
 
 import pytest
 
-SIZES = [(64, 42, 500), (96, 49, 550), (128, 57, 600), (192, 68, 750)]
+SIZES = [(64, 38, 330), (96, 43, 400), (128, 47, 450), (192, 56, 560)]
 MIN_SHARE = 8
 COUNTERS = 256
+ROOM = {2: 36, 3: 23, 4: 15}     # clusters of so many pairs on 152 SMs
 
 
-def plan(M, N, K, sm_count):
-    slots, F2, G = sm_count // 2, -(-N // 256), K // 128
-
-    def cost(size):
-        return max(-(-M // size[0]) * F2 * G // slots, MIN_SHARE) * size[1] + size[2]
-    T = min(SIZES, key=cost)[0]
-    TT = -(-M // T)
+def plan_tiles(size, M, N, K, sm_count):
+    T, step, base = size
+    slots, F2, TT, G = sm_count // 2, -(-N // 256), -(-M // T), K // 128
     tiles = TT * F2
-    rest = tiles % slots
-    p = dict(T=T, TT=TT, F2=F2, G=G, pairs=min(tiles, slots), band=min(TT, 8), sk_tiles=0, sk_pairs=1, parts=0)
+    rounds, rest = divmod(tiles, slots)
+    p = dict(T=T, TT=TT, F2=F2, G=G, pairs=min(tiles, slots), band=min(TT, 8), sk_tiles=0, sk_pairs=1, parts=0,
+             cluster=1)
+    last, meet = G if rest else 0, 0
     if rest and rest * 8 < slots * 7:
-        parts = slots // rest
-        n = rest * min(parts, G // MIN_SHARE) if parts >= 2 else slots
+        most = slots // rest
+        n = rest * min(most, G // MIN_SHARE) if most >= 2 else slots
         if n * MIN_SHARE > rest * G:
             n = rest * G // MIN_SHARE
         if n > rest:
-            p.update(sk_tiles=rest, sk_pairs=n, parts=n * 4, pairs=max(p["pairs"], n))
+            share_meet = 150 if rounds else 480 + 45 * -(-n // rest)
+            if step * -(-rest * G // n) + share_meet < step * last:
+                p.update(sk_tiles=rest, sk_pairs=n, parts=n * 4, pairs=max(p["pairs"], n))
+                last, meet = -(-rest * G // n), share_meet
+    for c, room in ROOM.items():
+        steps = -(-G // c)
+        if c * MIN_SHARE <= G and tiles * 152 <= room * sm_count and step * steps + 200 < step * last + meet:
+            p.update(cluster=c, sk_tiles=tiles, sk_pairs=tiles * c, pairs=tiles * c, parts=0)
+            last, meet = steps, 200
+    p["cost"] = base + step * (rounds * G + last) + meet
     return p
+
+
+def plan(M, N, K, sm_count):
+    return min((plan_tiles(size, M, N, K, sm_count) for size in SIZES), key=lambda p: p["cost"])
 
 
 def segments(p, pair):
@@ -68,12 +80,19 @@ def check(M, N, K, sm_count=152):
                 seen.add((tile, g))
             if shared is not None:
                 cut += 1
+                if p["cluster"] > 1:     # its one segment, of the cluster's tile
+                    assert shared == pair // p["cluster"] and cut == 1
+                    continue
                 first = pair * W // n // G
                 slot = pair * 2 + (0 if first == shared else 1)
                 assert 0 <= slot * 2 + 1 < p["parts"]
                 contributors.setdefault(shared, []).append((pair, slot))
         assert cut <= 2
     assert len(seen) == tiles * G
+
+    if p["cluster"] > 1:
+        assert all(len(segments(p, pair)) == 1 for pair in range(p["pairs"]))
+        return p
 
     def pair_of_step(i):
         return ((i + 1) * n + W - 1) // W - 1

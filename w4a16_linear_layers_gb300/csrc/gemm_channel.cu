@@ -312,72 +312,98 @@ constexpr int64_t kMinShare = 8;          // K steps of a pair's share of the cu
 struct PairPlan {
   int T = 0;
   int64_t TT = 0, F2 = 0, G = 0, pairs = 0, band = 0, sk_tiles = 0, sk_pairs = 0;
-  bool cut = false;         // some tile is shared between pairs
+  int64_t parts = 1;        // pairs of a cluster: they share a tile
+  bool cut = false;         // some tile is shared between other pairs
   size_t part_bytes = 0;    // int32 partials of the shared tiles
+  int64_t cost = 0;         // estimated time, in 10 ns
 };
 
-PairPlan plan_pair(int64_t M, int64_t N, int64_t K, int sm_count) {
+// A tile size: the time of a K step and of what is around a pair's steps, in 10
+// ns, measured at N from 5120 to 34816.  Parts of a tile that meet in a cluster
+// take 2 us; through the workspace 5 us and half a one for each part, of which
+// 1.5 are left where whole tiles follow.
+struct PairSize {
+  int T, step, base;
+};
+constexpr PairSize kPairSizes[4] = {{64, 38, 330}, {96, 43, 400}, {128, 47, 450}, {192, 56, 560}};
+
+PairPlan plan_tiles(const PairSize& size, int64_t M, int64_t N, int64_t K, int sm_count) {
   PairPlan pl;
-  // Tile size: the least of (K steps of a pair) x (time of a step) + (time of
-  // what follows a pair's last step), in 10 ns, measured where HBM or the MMAs
-  // bound the steps (N = 34816, K = 5120).
-  constexpr struct {
-    int T, step, tail;
-  } kSizes[4] = {{64, 42, 500}, {96, 49, 550}, {128, 57, 600}, {192, 68, 750}};
   const int64_t slots = sm_count / 2;
-  const int64_t F2 = (N + 255) / 256;
-  int64_t best = 0;
-  for (const auto& size : kSizes) {
-    const int64_t steps = (M + size.T - 1) / size.T * F2 * (K / 128);
-    const int64_t longest = steps / slots > kMinShare ? steps / slots : kMinShare;
-    const int64_t cost = longest * size.step + size.tail;
-    if (best == 0 || cost < best) {
-      best = cost;
-      pl.T = size.T;
-    }
-  }
-  pl.TT = (M + pl.T - 1) / pl.T;
-  pl.F2 = F2;
+  pl.T = size.T;
+  pl.TT = (M + size.T - 1) / size.T;
+  pl.F2 = (N + 255) / 256;
   pl.G = K / 128;
+  pl.band = pl.TT < 8 ? pl.TT : 8;
   const int64_t tiles = pl.TT * pl.F2;
   const int64_t rest = tiles % slots;
+  const int64_t rounds = tiles / slots;
   pl.pairs = tiles < slots ? tiles : slots;
-  pl.band = pl.TT < 8 ? pl.TT : 8;
+  int64_t last = rest == 0 ? 0 : pl.G;    // steps of the last round
+  int64_t meet = 0;
   // The last round's tiles are cut along K unless they nearly fill it: into as
-  // many equal parts as the pairs allow where that is two or more (96 x 5120 x
-  // 5120, 20 tiles: 16.7 us in 3 parts, 21.0 in 76 shares that cross tiles), else
-  // into shares that cross tiles.
+  // many equal parts as the pairs allow where that is two or more, else into
+  // shares that cross tiles.
+  int64_t n = 0, shares = 0, share_meet = 0;
   if (rest != 0 && rest * 8 < slots * 7) {
-    const int64_t parts = slots / rest;
-    int64_t n = parts >= 2 ? rest * (parts < pl.G / kMinShare ? parts : pl.G / kMinShare) : slots;
+    const int64_t most = slots / rest;
+    n = most >= 2 ? rest * (most < pl.G / kMinShare ? most : pl.G / kMinShare) : slots;
     if (n * kMinShare > rest * pl.G) n = rest * pl.G / kMinShare;
     if (n > rest) {
-      pl.sk_tiles = rest;
-      pl.sk_pairs = n;
-      pl.cut = true;
-      pl.part_bytes = static_cast<size_t>(n) * 4 * pl.T * 128 * sizeof(int32_t);
-      if (pl.pairs < n) pl.pairs = n;
+      shares = (rest * pl.G + n - 1) / n;
+      share_meet = rounds > 0 ? 150 : 480 + 45 * ((n + rest - 1) / rest);
+      if (size.step * shares + share_meet < size.step * last) {
+        pl.sk_tiles = rest;
+        pl.sk_pairs = n;
+        pl.cut = true;
+        pl.part_bytes = static_cast<size_t>(n) * 4 * pl.T * 128 * sizeof(int32_t);
+        if (pl.pairs < n) pl.pairs = n;
+        last = shares;
+        meet = share_meet;
+      }
     }
   }
+  // Few tiles: the pairs of a cluster share one, and meet in shared memory (64 x
+  // 5120 x 5120 11.2 us, through the workspace 15.2; 512 x 5120 x 1024 13.2 and
+  // 17.3; 64 x 2048 x 4096 7.2 and 11.5).  With one block an SM there is room for
+  // 36, 23 and 15 clusters of two, three and four pairs on 152 SMs.
+  constexpr int kRoom[pair::kMaxParts + 1] = {0, 0, 36, 23, 15};
+  for (int c = 2; c <= pair::kMaxParts && c * kMinShare <= pl.G; ++c) {
+    const int64_t steps = (pl.G + c - 1) / c;
+    if (tiles * 152 <= static_cast<int64_t>(kRoom[c]) * sm_count && size.step * steps + 200 < size.step * last + meet) {
+      pl.parts = c;
+      pl.cut = false;
+      pl.part_bytes = 0;
+      pl.sk_tiles = tiles;
+      pl.sk_pairs = pl.pairs = tiles * c;
+      last = steps;
+      meet = 200;
+    }
+  }
+  pl.cost = size.base + size.step * (rounds * pl.G + last) + meet;
   return pl;
+}
+
+PairPlan plan_pair(int64_t M, int64_t N, int64_t K, int sm_count) {
+  PairPlan best;
+  for (const PairSize& size : kPairSizes) {
+    const PairPlan pl = plan_tiles(size, M, N, K, sm_count);
+    if (best.T == 0 || pl.cost < best.cost) best = pl;
+  }
+  return best;
 }
 
 // Batches that take the streaming kernel: up to 8 tokens always, and more where
 // its blocks of 16 all run at one time and are done first.  A step of their warps
-// takes 0.95 us, mostly latency; a K step of a pair 0.37 us at least, and cut
-// tiles meet again after 5 us and half a one for every part.  Measured: 16 x 5120 x
-// 5120 10.9 us against 14.6 in pairs, 128 x 5120 x 1024 9.7 and 12.2, 64 x 17408 x
-// 1024 17.4 and 19.5, 16 x 1152 x 8192 4.0 and 6.7; but 16 x 17408 x 5120 33.6 and
-// 26.6, 96 x 17408 x 1024 30.6 and 22.9, 16 x 5120 x 10240 23.2 and 20.1.
+// takes 0.88 us, mostly latency.  Measured: 16 x 17408 x 1024 7.9 us against 19.3 in
+// pairs, 64 x 5120 x 1024 6.8 and 12.2 (both through the workspace), 16 x 1152 x
+// 8192 4.0 and 6.7; but 128 x 5120 x 1024 9.7 and 8.6, 64 x 17408 x 1024 17.5 and
+// 16.8, 16 x 17408 x 5120 33.6 and 22.7, 16 x 5120 x 10240 23.2 and 20.1.
 bool streams(int64_t M, int64_t N, int64_t K, int sm_count) {
   if (M <= 8) return true;
   const int64_t tiles = stream16_tiles(M, N);
   if (tiles > 2LL * sm_count) return false;
-  const int64_t stream = 180 + 95 * split_stream(tiles, 2LL * sm_count, K).steps;
-  const PairPlan pl = plan_pair(M, N, K, sm_count);
-  const int64_t steps = (pl.TT * pl.F2 * pl.G + pl.pairs - 1) / pl.pairs;
-  const int64_t parts = pl.cut ? (pl.sk_pairs + pl.sk_tiles - 1) / pl.sk_tiles : 0;
-  return stream < 330 + 37 * steps + (pl.cut ? 480 + 45 * parts : 0);
+  return 180 + 88 * split_stream(tiles, 2LL * sm_count, K).steps < plan_pair(M, N, K, sm_count).cost;
 }
 
 // The pair kernel reads fp16 codes: int8 ones from an image in the workspace,
@@ -446,8 +472,8 @@ cudaError_t launch_pair_t(const CUtensorMap& tw, const CUtensorMap& tx, const pa
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_release);
   }
-  return launch_pdl(pair::pair_kernel<T>, dim3(static_cast<unsigned>(2 * p.pairs)), dim3(pair::kThreads),
-                    pair::Cfg<T>::kSmem, stream, tw, tx, p);
+  return launch_cluster_pdl(pair::pair_kernel<T>, dim3(static_cast<unsigned>(2 * p.pairs)), dim3(pair::kThreads),
+                            pair::Cfg<T>::kSmem, 2 * p.parts, stream, tw, tx, p);
 }
 
 cudaError_t launch_pair(const ChannelGemmArgs& a, int* err, int sm_count, cudaStream_t stream) {
@@ -492,6 +518,7 @@ cudaError_t launch_pair(const ChannelGemmArgs& a, int* err, int sm_count, cudaSt
   p.pairs = static_cast<int>(pl.pairs);
   p.sk_tiles = static_cast<int>(pl.sk_tiles);
   p.sk_pairs = pl.sk_pairs > 0 ? static_cast<int>(pl.sk_pairs) : 1;
+  p.parts = static_cast<int>(pl.parts);
   p.counters = counters;
   p.part = pl.cut ? reinterpret_cast<int32_t*>(ws + kCounterBytes) : nullptr;
   p.err = err;

@@ -27,6 +27,9 @@
 //     its int32 partial of such a tile, and the last one to arrive on the
 //     tile's counter adds the others' to its own.  Integer sums: the result
 //     does not depend on who is last.
+//   * Few tiles: the two to four pairs of a cluster share a tile, each with its
+//     part of K.  Their sums meet in shared memory, where each block finishes
+//     its share of the tokens: no workspace, no counters, 2 us instead of 6.
 //   * Roles of a block's 20 warps: 0 streams words and 2 tokens by TMA, 1
 //     issues the MMAs, 4-11 widen weights (two
 //     groups taking alternate steps), 12-19 drain and write.
@@ -54,6 +57,7 @@ constexpr uint32_t kCtrl = 2048;
 constexpr uint32_t kSmemMax = 232448;
 constexpr int kMaxW = 8;
 constexpr int kMaxU = 8;
+constexpr int kMaxParts = 4;            // pairs of a cluster
 
 template <int T>
 struct Cfg {
@@ -112,6 +116,7 @@ struct Params {
   int pairs;
   int sk_tiles;       // tiles cut along K: the last ones of the order
   int sk_pairs;       // pairs that share them
+  int parts;          // pairs of a cluster, which then are those that share a tile
   int* counters;      // [sk_tiles][2]
   int32_t* part;      // [pairs][2][2][T][128]
   int* err;
@@ -180,9 +185,9 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
 // through generic memory here.  With cluster scope every arrival waited for
 // the block's outstanding stores, and a K step took 0.95 us for any T up to 128.
 template <bool k2>
-__device__ __forceinline__ void arrive(uint32_t bar) {
+__device__ __forceinline__ void arrive(uint32_t bar, uint32_t first) {
   if constexpr (k2)
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(map_to_rank(bar, 0)) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(map_to_rank(bar, first)) : "memory");
   else
     mbar_arrive(bar);
 }
@@ -201,12 +206,11 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
 // One K half of them into both blocks' shared memory, counted on each block's
 // own barrier.
 __device__ __forceinline__ void tma_load_both(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x,
-                                              int32_t y, int32_t z, uint64_t policy) {
+                                              int32_t y, int32_t z, uint64_t policy, uint16_t both) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
       ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6, %7;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "h"(static_cast<uint16_t>(3)),
-      "l"(policy)
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "h"(both), "l"(policy)
       : "memory");
 }
 
@@ -223,18 +227,18 @@ __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint32_t a_tmem, uint6
 // Arrives once on `bar`, of this block or (kBoth) of both, when this thread's
 // MMAs so far have completed.
 template <bool k2, bool kBoth>
-__device__ __forceinline__ void commit(uint32_t bar) {
+__device__ __forceinline__ void commit(uint32_t bar, uint16_t both) {
   if constexpr (k2 && kBoth)
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"(static_cast<uint16_t>(3))
+        "h"(both)
         : "memory");
   else if constexpr (k2)
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
   else if constexpr (kBoth)
     asm volatile(
         "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"(static_cast<uint16_t>(3))
+        "h"(both)
         : "memory");
   else
     tc_commit(bar);
@@ -242,6 +246,21 @@ __device__ __forceinline__ void commit(uint32_t bar) {
 
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank_of_block() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ int4 ld_cluster_int4(uint32_t addr) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -293,7 +312,7 @@ __device__ __forceinline__ void reg_inc() {
 }
 
 template <int T>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, const Params p) {
   using C = Cfg<T>;
   constexpr int NW = C::kWSlots;
@@ -304,7 +323,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem + x_off + C::kX * C::kXBytes);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const uint32_t rank = blockIdx.x & 1u;     // the cluster is two consecutive blocks
+  const uint32_t rank = blockIdx.x & 1u;     // in the pair, two consecutive blocks
+  const uint32_t first = cluster_rank_of_block() & ~1u;      // the pair's place in its cluster
+  const uint16_t both = static_cast<uint16_t>(3u << first);  // its blocks
   const int pr = static_cast<int>(blockIdx.x >> 1);
 
   if (threadIdx.x == 0) {
@@ -395,14 +416,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t dst = sbase + x_off + slot * C::kXBytes;
           if constexpr (C::k2) {
             if (rank == 0) mbar_arrive_expect_tx(full, 2 * C::kXBytes);
-            tma_load_pair(dst, &tm_x, map_to_rank(full, 0), 0, row, u * (C::kUnit / 64), pol);
+            tma_load_pair(dst, &tm_x, map_to_rank(full, first), 0, row, u * (C::kUnit / 64), pol);
           } else {
             // each 64 of K is T rows x 128 B, this block's rows its first or second half
             mbar_arrive_expect_tx(full, C::kXBytes);
 #pragma unroll
             for (int h = 0; h < C::kUnit / 64; ++h)
               tma_load_both(dst + h * (T * 128u) + rank * (C::kHalf * 128u), &tm_x, full, 0, row,
-                            u * (C::kUnit / 64) + h, pol);
+                            u * (C::kUnit / 64) + h, pol, both);
           }
         }
       }
@@ -450,8 +471,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               else
                 mma_ts(dcol, a0 + ks * 8, b0 + (off >> 4), idesc, (ci > 0 || ks > 0) ? 1u : 0u);
             }
-            commit<C::k2, true>(smem_u32(&ctrl->consumed[slot]));
-            if (ends) commit<C::k2, C::k2>(smem_u32(&ctrl->d_full[db]));
+            commit<C::k2, true>(smem_u32(&ctrl->consumed[slot]), both);
+            if (ends) commit<C::k2, C::k2>(smem_u32(&ctrl->d_full[db]), both);
           }
           __syncwarp();
           if (++slot == C::kX) {
@@ -465,7 +486,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (leader) commit<C::k2, false>(smem_u32(&ctrl->mma_done));
+      if (leader) commit<C::k2, false>(smem_u32(&ctrl->mma_done), both);
       __syncwarp();
       (void)mbar_wait(smem_u32(&ctrl->mma_done), 0u, drain_ctx, 67);
     }
@@ -513,7 +534,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) arrive<C::k2>(smem_u32(&ctrl->ready[u % C::kX]));
+          if (lane == 0) arrive<C::k2>(smem_u32(&ctrl->ready[u % C::kX]), first);
         }
         if (!ok) break;
       }
@@ -532,7 +553,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     Work w(p, pr);
     int d = 0;
     uint32_t part_par = 0u;
-    bool ok = true;
+    bool ok = true, summed = false;
     while (ok && w.next()) {
       named_bar_sync(1, kEpiThreads);     // the previous tile's scales are read
       if (et < T) ctrl->s_a[et] = static_cast<int64_t>(w.t) * T + et < p.M ? __ldg(p.s_a + static_cast<int64_t>(w.t) * T + et) : 0.0f;
@@ -559,11 +580,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ++chunks;
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive<C::k2>(smem_u32(&ctrl->d_empty[db]));
+        if (lane == 0) arrive<C::k2>(smem_u32(&ctrl->d_empty[db]), first);
       }
 #pragma unroll
       for (int c = 0; c < E; ++c) acc[c] -= static_cast<int32_t>(chunks * kIntegerBias);
       if (!named_bar_and(1, kEpiThreads, ok)) break;
+      if (p.parts > 1) {
+        summed = true;
+        break;
+      }
       bool finish = true;
       if (w.cut) {
         // the contributors of this tile, and this block's place among them
@@ -661,8 +686,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
     }
+    if (p.parts > 1) {
+      // The cluster's pairs hold sums of one tile, each over its part of K.
+      // Each block leaves its own in shared memory, in its idle rings, and
+      // finishes its share of the tokens.
+      int32_t* mine = reinterpret_cast<int32_t*>(smem);
+      if (summed) {
+#pragma unroll
+        for (int c = 0; c < E; ++c) mine[(col0 + c) * kF + r] = acc[c];
+      }
+      __syncwarp();
+      cluster_sync();
+      if (summed) {
+        const int share = (T + p.parts - 1) / p.parts;
+        const int tok0 = static_cast<int>(first >> 1) * share;
+        const int64_t rows = p.M - static_cast<int64_t>(w.t) * T;    // of the tile
+        const int tok1 = static_cast<int>(min(static_cast<int64_t>(min(T, tok0 + share)), rows));
+        const int64_t n = static_cast<int64_t>(w.f) * 256 + rank * kF + 4 * lane;
+        const float4 sw = n < p.N ? __ldg(reinterpret_cast<const float4*>(p.s_w + n)) : make_float4(0, 0, 0, 0);
+        constexpr int kAhead = 3;     // tokens of a warp on their way
+        for (int t0 = tok0 + warp - 12; t0 < tok1; t0 += 8 * kAhead) {
+          int4 v[kAhead][kMaxParts];
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+            for (int i = 0; i < kMaxParts; ++i)
+              v[k][i] = t0 + 8 * k < tok1 && i < p.parts
+                            ? ld_cluster_int4(map_to_rank(sbase + ((t0 + 8 * k) * kF + 4 * lane) * 4, 2 * i + rank))
+                            : make_int4(0, 0, 0, 0);
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) {
+            const int t = t0 + 8 * k;
+            if (t >= tok1 || n >= p.N) continue;
+            int4 sum = v[k][0];
+#pragma unroll
+            for (int i = 1; i < kMaxParts; ++i) {
+              sum.x += v[k][i].x;
+              sum.y += v[k][i].y;
+              sum.z += v[k][i].z;
+              sum.w += v[k][i].w;
+            }
+            const float sa = ctrl->s_a[t];
+            uint2 out;
+            out.x = bf16x2_rn(__fmul_rn(__fmul_rn(__int2float_rn(sum.x), sw.x), sa),
+                              __fmul_rn(__fmul_rn(__int2float_rn(sum.y), sw.y), sa));
+            out.y = bf16x2_rn(__fmul_rn(__fmul_rn(__int2float_rn(sum.z), sw.z), sa),
+                              __fmul_rn(__fmul_rn(__int2float_rn(sum.w), sw.w), sa));
+            *reinterpret_cast<uint2*>(p.y + (static_cast<int64_t>(w.t) * T + t) * p.N + n) = out;
+          }
+        }
+      }
+    }
     __syncwarp();
   }
+  if (p.parts > 1 && warp < 12) cluster_sync();   // the epilogue's, above
 
   // ------------------------------------------------------------- teardown
   // The cluster barrier keeps each block's shared and tensor memory until the
