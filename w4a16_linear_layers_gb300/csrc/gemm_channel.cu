@@ -430,8 +430,8 @@ static_assert(kMapHalves * 64 >= kSmallCodes, "a row of small codes is no longer
 template <bool kC16>
 __global__ void __launch_bounds__(256) pair_prepare_kernel(int* counters, const void* __restrict__ q,
                                                            uint16_t* __restrict__ image, int64_t n16) {
+  grid_dep_launch();  // the pairs' blocks may take the SMs that come free, and load words
   grid_dep_wait();    // the workspace may still be in use, and the codes come from the previous kernel
-  grid_dep_launch();
   if (blockIdx.x == 0 && counters != nullptr) counters[threadIdx.x] = 0;
   for (int64_t i = blockIdx.x * static_cast<int64_t>(256) + threadIdx.x; i < n16;
        i += static_cast<int64_t>(gridDim.x) * 256) {
