@@ -31,6 +31,7 @@
 #include <cuda_fp16.h>
 
 #include <atomic>
+#include <mutex>
 
 #include "gemm_channel_pair.cuh"
 #include "qlin_device.cuh"
@@ -270,17 +271,73 @@ cudaError_t launch_stream(const ChannelParams& p, int splits, cudaStream_t strea
                             dim3(kSThreads), 0, splits, stream, p, splits);
 }
 
-// Blocks that share K: as many as run at one time with the tiles' others, while
-// a warp's steps get fewer.
-struct StreamSplit {
-  int64_t splits, steps;
+// Clusters that run at one time on a device, by their size: GPCs of different
+// sizes each take whole ones (152 SMs take 36, 23 and 15 clusters of 4, 6 and 8
+// blocks that fill an SM).
+struct Room {
+  int sm_count = 0;
+  int pairs[pair::kMaxParts + 1] = {};     // of so many pairs
+  int narrow[kMaxSplits + 1] = {};         // of the streaming kernel's blocks: 32 channels, 8 tokens
+  int wide[kMaxSplits + 1] = {};           // 64 channels, 8 tokens
+  int tokens16[kMaxSplits + 1] = {};       // 32 channels, 16 tokens
 };
-StreamSplit split_stream(int64_t tiles, int64_t slots, int64_t K) {
+
+template <typename Kernel>
+int clusters_at_once(Kernel kernel, int threads, size_t smem, int size, int blocks_per_sm, int sm_count) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(size));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(size);
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0) return n;
+  (void)cudaGetLastError();
+  return blocks_per_sm * sm_count / size;
+}
+
+// Of the current device.
+const Room& room_of_device(int sm_count) {
+  static Room rooms[64];
+  static std::once_flag once[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) dev = 0;
+  dev &= 63;
+  std::call_once(once[dev], [&] {
+    Room& r = rooms[dev];
+    r.sm_count = sm_count;
+    (void)cudaFuncSetAttribute(pair::pair_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(pair::Cfg<128>::kSmem));
+    for (int c = 1; c <= pair::kMaxParts; ++c)
+      r.pairs[c] = clusters_at_once(pair::pair_kernel<128>, pair::kThreads, pair::Cfg<128>::kSmem, 2 * c, 1, sm_count);
+    for (int c = 1; c <= kMaxSplits; ++c) {
+      r.narrow[c] = clusters_at_once(stream_kernel<1, 1, false>, kSThreads, 0, c, 3, sm_count);
+      r.wide[c] = clusters_at_once(stream_kernel<2, 1, false>, kSThreads, 0, c, 2, sm_count);
+      r.tokens16[c] = clusters_at_once(stream_kernel<1, 2, false>, kSThreads, 0, c, 2, sm_count);
+    }
+  });
+  return rooms[dev];
+}
+
+// Blocks that share K: as many as run at one time for all tiles, while a warp's
+// steps get fewer.
+struct StreamSplit {
+  int splits;
+  int64_t steps;
+};
+StreamSplit split_stream(int64_t tiles, const int* room, int64_t K) {
   const int64_t nkb = K / kKB;
-  int64_t most = slots / tiles;
-  most = most < 1 ? 1 : most > kMaxSplits ? kMaxSplits : most;
-  const int64_t steps = (nkb + kSWarps * most - 1) / (kSWarps * most);
-  return {(nkb + kSWarps * steps - 1) / (kSWarps * steps), steps};
+  StreamSplit best{1, (nkb + kSWarps - 1) / kSWarps};
+  for (int c = 2; c <= kMaxSplits; ++c) {
+    const int64_t steps = (nkb + kSWarps * c - 1) / (kSWarps * c);
+    if (tiles <= room[c] && steps < best.steps) best = {c, steps};
+  }
+  return best;
 }
 
 // 16 tokens a block: two blocks an SM (three of 85 registers a thread spill:
@@ -288,20 +345,21 @@ StreamSplit split_stream(int64_t tiles, int64_t slots, int64_t K) {
 int64_t stream16_tiles(int64_t M, int64_t N) { return (N + 31) / 32 * ((M + 15) / 16); }
 
 template <bool kC16>
-cudaError_t launch_c(const ChannelParams& p, int sm_count, cudaStream_t stream) {
-  if (p.M > 8) {
-    const StreamSplit s = split_stream(stream16_tiles(p.M, p.N), 2LL * sm_count, p.K);
-    return launch_stream<1, 2, kC16>(p, static_cast<int>(s.splits), stream);
-  }
-  // 32 channels a block while all blocks run at one time (three an SM): at K =
-  // 5120, N = 5120 in 2 parts of K 8.3 us (1 part 12.1, 5 parts 10.0), N = 10240
-  // unsplit 12.8 (2 parts 16.6; 64 channels 17.2).  Blocks beyond one round of
-  // them cost more than they hide, so above that 64 channels, unsplit: N = 34816
-  // 32.6 us (32 channels 38).
-  const int64_t tiles = (p.N + 31) / 32;
-  const int64_t slots = 3LL * sm_count;
-  if (tiles > slots) return launch_stream<2, 1, kC16>(p, 1, stream);
-  return launch_stream<1, 1, kC16>(p, static_cast<int>(split_stream(tiles, slots, p.K).splits), stream);
+cudaError_t launch_c(const ChannelParams& p, const Room& room, cudaStream_t stream) {
+  if (p.M > 8)
+    return launch_stream<1, 2, kC16>(p, split_stream(stream16_tiles(p.M, p.N), room.tokens16, p.K).splits, stream);
+  // A step of a warp takes about 1.2 us, of 64 channels 1.5, mostly latency: the
+  // fewer steps the better, while all blocks run at one time.  8 x 5120 x 5120 7.9
+  // us (32 channels in 2 parts of K; unsplit 11.4, in 3 parts of 64 8.3), 8 x 17408
+  // x 5120 18.7 (64 channels in 3 parts; 32 in 2 21.3), 8 x 17408 x 8192 26.7 (64 in
+  // 2; 32 unsplit 38.6), 8 x 5120 x 10240 12.3 (32 unsplit; 64 14.4).  More tiles
+  // of 32 than run at one time: N = 34816 32.6 us in 64, 38 in 32.
+  const int64_t tiles = (p.N + 31) / 32, tiles2 = (p.N + 63) / 64;
+  const StreamSplit narrow = split_stream(tiles, room.narrow, p.K);
+  const StreamSplit wide = split_stream(tiles2, room.wide, p.K);
+  if (tiles > room.narrow[1] || (tiles2 <= room.wide[1] && 152 * wide.steps < 120 * narrow.steps))
+    return launch_stream<2, 1, kC16>(p, wide.splits, stream);
+  return launch_stream<1, 1, kC16>(p, narrow.splits, stream);
 }
 
 // ------------------------------------------------------- larger batches
@@ -327,9 +385,9 @@ struct PairSize {
 };
 constexpr PairSize kPairSizes[4] = {{64, 38, 330}, {96, 43, 400}, {128, 47, 450}, {192, 56, 560}};
 
-PairPlan plan_tiles(const PairSize& size, int64_t M, int64_t N, int64_t K, int sm_count) {
+PairPlan plan_tiles(const PairSize& size, int64_t M, int64_t N, int64_t K, const Room& room) {
   PairPlan pl;
-  const int64_t slots = sm_count / 2;
+  const int64_t slots = room.sm_count / 2;
   pl.T = size.T;
   pl.TT = (M + size.T - 1) / size.T;
   pl.F2 = (N + 255) / 256;
@@ -365,12 +423,10 @@ PairPlan plan_tiles(const PairSize& size, int64_t M, int64_t N, int64_t K, int s
   }
   // Few tiles: the pairs of a cluster share one, and meet in shared memory (64 x
   // 5120 x 5120 11.2 us, through the workspace 15.2; 512 x 5120 x 1024 13.2 and
-  // 17.3; 64 x 2048 x 4096 7.2 and 11.5).  With one block an SM there is room for
-  // 36, 23 and 15 clusters of two, three and four pairs on 152 SMs.
-  constexpr int kRoom[pair::kMaxParts + 1] = {0, 0, 36, 23, 15};
+  // 17.3; 64 x 2048 x 4096 7.2 and 11.5).
   for (int c = 2; c <= pair::kMaxParts && c * kMinShare <= pl.G; ++c) {
     const int64_t steps = (pl.G + c - 1) / c;
-    if (tiles * 152 <= static_cast<int64_t>(kRoom[c]) * sm_count && size.step * steps + 200 < size.step * last + meet) {
+    if (tiles <= room.pairs[c] && size.step * steps + 200 < size.step * last + meet) {
       pl.parts = c;
       pl.cut = false;
       pl.part_bytes = 0;
@@ -384,10 +440,10 @@ PairPlan plan_tiles(const PairSize& size, int64_t M, int64_t N, int64_t K, int s
   return pl;
 }
 
-PairPlan plan_pair(int64_t M, int64_t N, int64_t K, int sm_count) {
+PairPlan plan_pair(int64_t M, int64_t N, int64_t K, const Room& room) {
   PairPlan best;
   for (const PairSize& size : kPairSizes) {
-    const PairPlan pl = plan_tiles(size, M, N, K, sm_count);
+    const PairPlan pl = plan_tiles(size, M, N, K, room);
     if (best.T == 0 || pl.cost < best.cost) best = pl;
   }
   return best;
@@ -399,11 +455,11 @@ PairPlan plan_pair(int64_t M, int64_t N, int64_t K, int sm_count) {
 // pairs, 64 x 5120 x 1024 6.8 and 12.2 (both through the workspace), 16 x 1152 x
 // 8192 4.0 and 6.7; but 128 x 5120 x 1024 9.7 and 8.6, 64 x 17408 x 1024 17.5 and
 // 16.8, 16 x 17408 x 5120 33.6 and 22.7, 16 x 5120 x 10240 23.2 and 20.1.
-bool streams(int64_t M, int64_t N, int64_t K, int sm_count) {
+bool streams(int64_t M, int64_t N, int64_t K, const Room& room) {
   if (M <= 8) return true;
   const int64_t tiles = stream16_tiles(M, N);
-  if (tiles > 2LL * sm_count) return false;
-  return 180 + 88 * split_stream(tiles, 2LL * sm_count, K).steps < plan_pair(M, N, K, sm_count).cost;
+  if (tiles > room.tokens16[1]) return false;
+  return 180 + 88 * split_stream(tiles, room.tokens16, K).steps < plan_pair(M, N, K, room).cost;
 }
 
 // The pair kernel reads fp16 codes: int8 ones from an image in the workspace,
@@ -476,8 +532,8 @@ cudaError_t launch_pair_t(const CUtensorMap& tw, const CUtensorMap& tx, const pa
                             pair::Cfg<T>::kSmem, 2 * p.parts, stream, tw, tx, p);
 }
 
-cudaError_t launch_pair(const ChannelGemmArgs& a, int* err, int sm_count, cudaStream_t stream) {
-  const PairPlan pl = plan_pair(a.M, a.N, a.K, sm_count);
+cudaError_t launch_pair(const ChannelGemmArgs& a, int* err, const Room& room, cudaStream_t stream) {
+  const PairPlan pl = plan_pair(a.M, a.N, a.K, room);
   if (pl.TT * pl.F2 > (1LL << 30)) return cudaErrorInvalidValue;   // y would not fit any memory
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   const void* codes = a.act;
@@ -534,15 +590,17 @@ cudaError_t launch_pair(const ChannelGemmArgs& a, int* err, int sm_count, cudaSt
 }  // namespace
 
 size_t channel_workspace_bytes(int64_t M, int64_t N, int64_t K, bool c16, int sm_count) {
-  if (streams(M, N, K, sm_count)) return 0;
-  const PairPlan pl = plan_pair(M, N, K, sm_count);
+  const Room& room = room_of_device(sm_count);
+  if (streams(M, N, K, room)) return 0;
+  const PairPlan pl = plan_pair(M, N, K, room);
   return (pl.cut ? kCounterBytes + pl.part_bytes : 0) + (has_image(pl, M, K, c16) ? image_bytes(M, K) : 0);
 }
 
 cudaError_t launch_gemm_channel(const ChannelGemmArgs& a, int* err, int sm_count, cudaStream_t stream) {
-  if (!streams(a.M, a.N, a.K, sm_count)) return launch_pair(a, err, sm_count, stream);
+  const Room& room = room_of_device(sm_count);
+  if (!streams(a.M, a.N, a.K, room)) return launch_pair(a, err, room, stream);
   const ChannelParams p{a.act, a.s_a, reinterpret_cast<const uint32_t*>(a.qweight), a.s_w, a.y, a.M, a.N, a.K};
-  return a.act_c16 ? launch_c<true>(p, sm_count, stream) : launch_c<false>(p, sm_count, stream);
+  return a.act_c16 ? launch_c<true>(p, room, stream) : launch_c<false>(p, room, stream);
 }
 
 }  // namespace qlin
