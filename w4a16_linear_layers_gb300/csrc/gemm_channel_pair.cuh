@@ -557,6 +557,50 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && w.next()) {
       named_bar_sync(1, kEpiThreads);     // the previous tile's scales are read
       if (et < T) ctrl->s_a[et] = static_cast<int64_t>(w.t) * T + et < p.M ? __ldg(p.s_a + static_cast<int64_t>(w.t) * T + et) : 0.0f;
+      // Two neighbouring lanes (channels) exchange a value of each two tokens,
+      // so that a lane writes both channels of one: 4 bytes, and half the stores.
+      const int odd = lane & 1;
+      auto write2 = [&](int c, float p0, float p1, float sw, uint16_t* dst, int rows) {   // the sums of tokens c and c + 1
+        const float2 sa = *reinterpret_cast<const float2*>(ctrl->s_a + col0 + c);
+        const uint32_t mine = bf16x2_rn(__fmul_rn(__fmul_rn(p0, sw), sa.x), __fmul_rn(__fmul_rn(p1, sw), sa.y));
+        const uint32_t theirs = __shfl_xor_sync(0xFFFFFFFFu, mine, 1);
+        // {theirs.hi, mine.hi} or {mine.lo, theirs.lo}
+        if (c < rows) *reinterpret_cast<uint32_t*>(dst) = prmt(mine, theirs, odd ? 0x3276u : 0x5410u);
+      };
+      auto output = [&](int& rows, float& sw) {   // of token `odd`; rows: that this lane writes
+        const int64_t n = static_cast<int64_t>(w.f) * 256 + rank * kF + r;
+        sw = n < p.N ? __ldg(p.s_w + n) : 0.0f;
+        const int64_t m0 = static_cast<int64_t>(w.t) * T + col0;
+        rows = n < p.N ? static_cast<int>(p.M - m0 < E ? p.M - m0 : E) - odd : 0;
+        return p.y + (m0 + odd) * p.N + (n - odd);
+      };
+      if (!w.cut && w.g1 - w.g0 <= kChunkK / 128) {
+        // One accumulator holds the whole sum, exact in fp32 as it is.
+        const int db = d % kND;
+        int rows;
+        float sw;
+        uint16_t* dst = output(rows, sw);
+        ok = __all_sync(0xFFFFFFFFu,
+                        mbar_wait(smem_u32(&ctrl->d_full[db]), static_cast<uint32_t>(d / kND) & 1u, ctx, 70));
+        if (!named_bar_and(1, kEpiThreads, ok)) break;
+        tc_fence_after();
+        const uint32_t dcol = tmem + lane_off + C::kColD + db * T + col0;
+        uint32_t v[2][16];
+        tmem_ld16(dcol, v[0]);
+#pragma unroll
+        for (int c = 0; c < E; c += 16) {
+          tmem_wait_ld();
+          if (c + 16 < E) tmem_ld16(dcol + c + 16, v[(c / 16 + 1) & 1]);
+#pragma unroll
+          for (int i = 0; i < 16; i += 2, dst += 2 * p.N)
+            write2(c + i, __uint_as_float(v[c / 16 & 1][i]), __uint_as_float(v[c / 16 & 1][i + 1]), sw, dst, rows);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive<C::k2>(smem_u32(&ctrl->d_empty[db]), first);
+        ++d;
+        continue;
+      }
 #pragma unroll
       for (int c = 0; c < E; ++c) acc[c] = 0;
       uint32_t chunks = 0;
@@ -667,23 +711,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (finish) {
-        // Two neighbouring lanes (channels) exchange a value of each two tokens,
-        // so that a lane writes both channels of one: 4 bytes, and half the stores.
-        const int64_t n = static_cast<int64_t>(w.f) * 256 + rank * kF + r;
-        const int64_t m0 = static_cast<int64_t>(w.t) * T + col0;
-        const float sw = n < p.N ? __ldg(p.s_w + n) : 0.0f;
-        const int odd = lane & 1;
-        const uint32_t sel = odd ? 0x3276u : 0x5410u;    // {theirs.hi, mine.hi} or {mine.lo, theirs.lo}
-        uint16_t* dst = p.y + (m0 + odd) * p.N + (n - odd);
-        const int rows = n < p.N ? static_cast<int>(p.M - m0 < E ? p.M - m0 : E) - odd : 0;
+        int rows;
+        float sw;
+        uint16_t* dst = output(rows, sw);
 #pragma unroll
-        for (int c = 0; c < E; c += 2, dst += 2 * p.N) {
-          const float2 sa = *reinterpret_cast<const float2*>(ctrl->s_a + col0 + c);
-          const uint32_t mine = bf16x2_rn(__fmul_rn(__fmul_rn(__int2float_rn(acc[c]), sw), sa.x),
-                                          __fmul_rn(__fmul_rn(__int2float_rn(acc[c + 1]), sw), sa.y));
-          const uint32_t theirs = __shfl_xor_sync(0xFFFFFFFFu, mine, 1);
-          if (c < rows) *reinterpret_cast<uint32_t*>(dst) = prmt(mine, theirs, sel);
-        }
+        for (int c = 0; c < E; c += 2, dst += 2 * p.N)
+          write2(c, __int2float_rn(acc[c]), __int2float_rn(acc[c + 1]), sw, dst, rows);
       }
     }
     if (p.parts > 1) {
