@@ -286,7 +286,7 @@ TILED_SHAPES = [
     (16, 5120, 10248), (40, 2304, 8200), (64, 1280, 20488), (24, 10240, 4104), (90, 8192, 2056), (96, 2304, 8200),
     (100, 1152, 20488), (128, 5120, 4104), (120, 17408, 1544), (130, 9344, 2056), (150, 4224, 5128),
     (200, 17408, 1032), (192, 1152, 10248), (600, 1152, 5128), (300, 65536, 264),
-    (24, 5120, 10248), (96, 5120, 10248), (96, 3200, 20488), (160, 5120, 10248), (128, 5120, 12296), (700, 8320, 2568),
+    (24, 5120, 10248), (96, 5120, 10248), (96, 3200, 20488), (160, 10240, 10248), (128, 10240, 10248), (700, 8320, 2568),
     # few codes
     (9, 5120, 20488), (12, 5120, 12296), (40, 1536, 20488), (57, 1152, 20488)]
 
@@ -303,7 +303,7 @@ def test_channel_product_in_tiles(gpu, M, K, N, kind):
 
 
 @needs_gpu
-@pytest.mark.parametrize("M,K,N", [(24, 5120, 10248), (96, 5120, 10248), (128, 5120, 12296), (700, 8320, 2568)])
+@pytest.mark.parametrize("M,K,N", [(24, 10240, 10248), (96, 10240, 10248), (128, 10240, 10248), (700, 8320, 2568)])
 def test_channel_product_in_cut_tiles_again_and_again(gpu, M, K, N):
     """A captured call with one workspace, replayed over a dirty workspace, and
     four streams at once with a workspace each: guard bytes stay, y is the same."""
@@ -342,7 +342,7 @@ def test_channel_product_in_cut_tiles_again_and_again(gpu, M, K, N):
 
 @needs_gpu
 def test_channel_workspace_refusals(gpu):
-    M, K, N = 24, 5120, 10248
+    M, K, N = 24, 10240, 10248
     q = torch.zeros((M, K), dtype=torch.int8, device="cuda")
     s, sw = torch.ones(M, device="cuda"), torch.ones(N, device="cuda")
     w = torch.zeros((K // 4, N), dtype=torch.int32, device="cuda")
@@ -604,7 +604,7 @@ def test_two_streams_at_once(gpu):
 def test_a_named_stream_leaves_freed_memory_of_the_current_one(gpu, by_handle):
     """The current stream holds work on a tensor that was freed: what a call on
     another stream allocates must not be its memory."""
-    M, K, N = 64, 5120, 10248
+    M, K, N = 64, 10240, 10248
     shape = (M, K)
     x = torch.ones(shape, dtype=torch.bfloat16, device="cuda")
     g = torch.ones(K, dtype=torch.bfloat16, device="cuda")

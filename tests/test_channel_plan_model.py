@@ -29,7 +29,7 @@ def plan_tiles(size, M, N, K, sm_count):
         if n * MIN_SHARE > rest * G:
             n = rest * G // MIN_SHARE
         if n > rest:
-            share_meet = 150 if rounds else 480 + 45 * -(-n // rest)
+            share_meet = 150 if rounds else 480 + 45 * -(-n // rest) * T // 64
             if step * -(-rest * G // n) + share_meet < step * last:
                 p.update(sk_tiles=rest, sk_pairs=n, parts=n * 4, pairs=max(p["pairs"], n))
                 last, meet = -(-rest * G // n), share_meet

@@ -378,8 +378,8 @@ struct PairPlan {
 
 // A tile size: the time of a K step and of what is around a pair's steps, in 10
 // ns, measured at N from 5120 to 34816.  Parts of a tile that meet in a cluster
-// take 2 us; through the workspace 5 us and half a one for each part, of which
-// 1.5 are left where whole tiles follow.
+// take 2 us; through the workspace 5 us and half a one for 64 tokens of each
+// part, of which 1.5 are left where whole tiles follow.
 struct PairSize {
   int T, step, base;
 };
@@ -409,7 +409,7 @@ PairPlan plan_tiles(const PairSize& size, int64_t M, int64_t N, int64_t K, const
     if (n * kMinShare > rest * pl.G) n = rest * pl.G / kMinShare;
     if (n > rest) {
       shares = (rest * pl.G + n - 1) / n;
-      share_meet = rounds > 0 ? 150 : 480 + 45 * ((n + rest - 1) / rest);
+      share_meet = rounds > 0 ? 150 : 480 + 45 * ((n + rest - 1) / rest) * size.T / 64;
       if (size.step * shares + share_meet < size.step * last) {
         pl.sk_tiles = rest;
         pl.sk_pairs = n;
