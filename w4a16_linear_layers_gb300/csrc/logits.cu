@@ -31,6 +31,7 @@
 #include <cuda_bf16.h>
 
 #include <atomic>
+#include <mutex>
 
 #include "qlin_device.cuh"
 #include "qlin_internal.h"
@@ -418,7 +419,7 @@ __global__ void __launch_bounds__(kLThreads, kRules ? 2 : 3) adjust_logits_kerne
 }
 
 template <bool kF32, bool kRules, bool kMasked>
-cudaError_t launch_kind(const LogitParams& p, int64_t M, cudaStream_t stream) {
+cudaError_t prepare_kind() {
   const auto kernel = adjust_logits_kernel<kF32, kRules, kMasked>;
   static std::atomic<uint64_t> ready{0};
   int dev = 0;
@@ -432,6 +433,46 @@ cudaError_t launch_kind(const LogitParams& p, int64_t M, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_release);
   }
+  return cudaSuccess;
+}
+
+// Rows that run at one time on the current device in clusters of 16 blocks.
+template <bool kF32>
+int rows_in_16(int sm_count) {
+  static int rows[64];
+  static std::once_flag once[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) dev = 0;
+  dev &= 63;
+  std::call_once(once[dev], [&] {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kMaxSplits);
+    cfg.blockDim = dim3(kLThreads);
+    cfg.dynamicSmemBytes = rule_bytes(kSliceBytes / (kF32 ? 4 : 2), kF32 ? 4 : 2, kMaxSlots);
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = kMaxSplits;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (prepare_kind<kF32, true, true>() == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&n, adjust_logits_kernel<kF32, true, true>, &cfg) == cudaSuccess) {
+      rows[dev] = n;
+    } else {
+      (void)cudaGetLastError();
+      rows[dev] = sm_count / 2 / kMaxSplits;
+    }
+  });
+  return rows[dev];
+}
+
+template <bool kF32, bool kRules, bool kMasked>
+cudaError_t launch_kind(const LogitParams& p, int64_t M, cudaStream_t stream) {
+  const auto kernel = adjust_logits_kernel<kF32, kRules, kMasked>;
+  const cudaError_t e = prepare_kind<kF32, kRules, kMasked>();
+  if (e != cudaSuccess) return e;
   return launch_cluster_pdl(kernel, dim3(static_cast<unsigned>(M * p.splits)), dim3(kLThreads),
                             kRules ? rule_bytes(p.part, kF32 ? 4 : 2, p.slots) : 0, p.splits, stream, p);
 }
@@ -454,10 +495,11 @@ cudaError_t launch_adjust_logits(const LogitArgs& a, int* err, int sm_count, cud
                 reinterpret_cast<const uint8_t*>(a.allowed), (a.V + 31) / 32 * 4, a.out, a.argmax, 0, 0, kLThreads, 1, err};
   const bool rules = p.L > 0 || p.B > 0;
   const int64_t most = rules ? kSliceBytes / (a.f32 ? 4 : 2) : a.V;
-  // Clusters of 16 find room late once a few of them are about (33 rows of
-  // 50,264 fp32 logits: 12.6 us against 5.6 with 8); at one row they are the
-  // faster ones (248,320 bf16 logits: 6.0 us against 7.1).
-  const int cap = a.M * kMaxSplits <= sm_count / 2 ? kMaxSplits : 8;
+  // In clusters of 16 while all rows run at one time (14 on 152 SMs): 7 rows of
+  // 248,320 fp32 logits 7.4 us, with 8 blocks a row 12.8; 14 rows 10.9 and 16.1.
+  // Beyond that they cost a second round: 33 rows of 50,264 12.6 and 5.6.
+  const int in_16 = a.f32 ? rows_in_16<true>(sm_count) : rows_in_16<false>(sm_count);
+  const int cap = a.M <= in_16 ? kMaxSplits : 8;
   while (p.splits < cap && (a.M * p.splits < 2 * sm_count || a.V > most * p.splits) && a.V >= 4096 * p.splits)
     p.splits *= 2;
   p.slice = ((a.V + p.splits - 1) / p.splits + 7) / 8 * 8;
