@@ -634,6 +634,68 @@ def test_a_named_stream_leaves_freed_memory_of_the_current_one(gpu, by_handle):
             assert (k == 0x35).all()
 
 
+# --------------------------------------------- offsets of more than 32 bits
+
+def _channel_sampled(q_a, s_a, w, s_w, y, rows, cols):
+    codes = torch.stack([(w[:, cols] >> (8 * i)) & 255 for i in range(4)], 1).reshape(-1, len(cols)) - 128
+    P = q_a[rows].double() @ codes.double()
+    want = ((P.float() * s_w[cols]) * s_a[rows, None]).bfloat16()
+    assert torch.equal(y[rows][:, cols], want)
+
+
+@needs_gpu
+@pytest.mark.parametrize("M,K,N", [(9000, 128, 248320), (9000, 1280, 248320), (5, 130944, 65544), (16, 130944, 65544)])
+def test_channel_product_past_32_bits(gpu, M, K, N):
+    """Outputs, and weights, whose last elements lie past 2^31."""
+    assert max(M * N, K // 4 * N) > 2 ** 31 - 2 ** 26
+    g = torch.Generator("cuda").manual_seed(M + K)
+    q = torch.randint(-127, 128, (M, K), generator=g, device="cuda", dtype=torch.int8)
+    w = torch.empty((K // 4, N), dtype=torch.int32, device="cuda").random_(-2 ** 31, 2 ** 31 - 1, generator=g)
+    s_a, s_w = torch.rand(M, generator=g, device="cuda"), torch.rand(N, generator=g, device="cuda")
+    y = qlin.gemm_w8a8_ch(q, s_a, w, s_w)
+    rows = torch.tensor(sorted({0, M // 2, M - 2, M - 1}), device="cuda")
+    cols = torch.cat([torch.arange(0, 40), torch.randint(0, N, (200,)), torch.arange(N - 40, N)]).cuda()
+    _channel_sampled(q, s_a, w, s_w, y, rows, cols)
+
+
+@needs_gpu
+def test_add_rmsnorm_past_32_bits(gpu):
+    M, K = 125000, 17408
+    g = torch.Generator("cuda").manual_seed(5)
+    x = torch.randn((M, K), generator=g, device="cuda", dtype=torch.bfloat16)
+    r = torch.randn((M, K), generator=g, device="cuda", dtype=torch.bfloat16)
+    gamma = torch.rand(K, generator=g, device="cuda").bfloat16()
+    q, s, h = qlin.add_rmsnorm_act_quant_i8(x, r, gamma, 1e-6)
+    rows = torch.tensor([0, 123361, M - 1], device="cuda")     # 123361 * 17408 passes 2^31
+    q0, s0, _, h0 = ref_add_rmsnorm(from_dev_bits(x[rows]), from_dev_bits(r[rows]), from_dev_bits(gamma), 1e-6)
+    assert np.array_equal(from_dev_bits(h[rows]), h0) and np.array_equal(q[rows].cpu().numpy(), q0)
+    assert np.array_equal(s[rows].cpu().numpy(), s0)
+
+
+@needs_gpu
+@pytest.mark.parametrize("rules", [False, True])
+def test_adjusted_logits_past_32_bits(gpu, rules):
+    M, V, L = 8800, 248320, 40
+    g = torch.Generator("cuda").manual_seed(6)
+    x = torch.randn((M, V), generator=g, device="cuda", dtype=torch.bfloat16)
+    allowed = torch.empty((M, V // 32), dtype=torch.int32, device="cuda").random_(-2 ** 31, 2 ** 31 - 1, generator=g)
+    kw = {"allowed": allowed}
+    if rules:
+        kw["tokens"] = torch.randint(0, V, (M, L), generator=g, device="cuda", dtype=torch.int32)
+        kw["repetition"] = 1.0 + torch.rand(M, generator=g, device="cuda")
+        kw["frequency"] = torch.rand(M, generator=g, device="cuda")
+    out = torch.empty_like(x)
+    best = qlin.adjust_logits_argmax(x, **kw, out=out)
+    rows = torch.tensor([0, 8648, M - 1], device="cuda")       # 8648 * 248320 passes 2^31
+    few = {"allowed": allowed[rows].cpu().numpy()}
+    if rules:
+        few.update(tokens=kw["tokens"][rows].cpu().numpy(), rep=kw["repetition"][rows].cpu().numpy(),
+                   freq=kw["frequency"][rows].cpu().numpy())
+    o0, _, arg0 = ref_logits(x[rows].float().cpu().numpy(), True, **few)
+    assert np.array_equal(out[rows].float().cpu().numpy(), o0)
+    assert np.array_equal(best[rows].cpu().numpy(), arg0)
+
+
 @needs_gpu
 def test_empty_batches(gpu):
     x = torch.empty((0, 256), dtype=torch.bfloat16, device="cuda")
