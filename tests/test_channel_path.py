@@ -16,6 +16,8 @@ fp32 steps.  Each is also held to an unrounded binary64 evaluation:
     logits' type: |o - o64| <= 5 * 2^-24 S + e |o64|, e = 2^-8 (bf16) or 0."""
 import ctypes
 
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -632,6 +634,50 @@ def test_a_named_stream_leaves_freed_memory_of_the_current_one(gpu, by_handle):
         torch.cuda.synchronize()
         for k in kept:
             assert (k == 0x35).all()
+
+
+@needs_gpu
+def test_threads_and_a_replay_beside_eager_calls(gpu):
+    """Four threads on streams of their own, and a captured step replayed while
+    another stream runs the same step eagerly: no two calls meet."""
+    M, K, N = 64, 5120, 10248
+    g = torch.Generator("cuda").manual_seed(9)
+    x = torch.randn((M, K), generator=g, device="cuda").bfloat16()
+    gamma = torch.ones(K, dtype=torch.bfloat16, device="cuda")
+    w = torch.empty((K // 4, N), dtype=torch.int32, device="cuda").random_(-2 ** 31, 2 ** 31 - 1, generator=g)
+    s_w = torch.rand(N, generator=g, device="cuda")
+    tokens = torch.randint(0, N, (M, 20), generator=g, device="cuda", dtype=torch.int32)
+    rep = torch.full((M,), 1.5, device="cuda")
+
+    def step():
+        q, s, _ = qlin.add_rmsnorm_act_quant_c16(x, x, gamma, 1e-6)
+        y = qlin.gemm_w8a8_ch_c16(q, s, w, s_w)
+        return y, qlin.adjust_logits_argmax(y, tokens=tokens, repetition=rep)
+
+    want = step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        replayed = step()
+    torch.cuda.synchronize()
+    got = [None] * 4
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(20):
+                got[i] = step()
+        stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for _ in range(20):
+        graph.replay()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for y, token in [replayed, *got]:
+        assert torch.equal(y, want[0]) and torch.equal(token, want[1])
 
 
 # --------------------------------------------- offsets of more than 32 bits
