@@ -9,36 +9,37 @@ import random
 
 import pytest
 
-SIZES = [(64, 38, 330), (96, 43, 400), (128, 47, 450), (192, 56, 560)]
+SIZES = [(64, 38, 170, 330), (96, 43, 210, 400), (128, 47, 250, 450), (192, 56, 320, 560)]
 MIN_SHARE = 8
 COUNTERS = 256
 ROOM = {2: 36, 3: 23, 4: 15}     # clusters of so many pairs on 152 SMs
 
 
 def plan_tiles(size, M, N, K, sm_count):
-    T, step, base = size
+    T, step, out, base = size
     slots, F2, TT, G = sm_count // 2, -(-N // 256), -(-M // T), K // 128
     tiles = TT * F2
     rounds, rest = divmod(tiles, slots)
     p = dict(T=T, TT=TT, F2=F2, G=G, pairs=min(tiles, slots), band=min(TT, 8), sk_tiles=0, sk_pairs=1, parts=0,
              cluster=1)
-    last, meet = G if rest else 0, 0
+    whole = max(step * G, out)
+    last = whole if rest else 0
     if rest and rest * 8 < slots * 7:
         most = slots // rest
         n = rest * min(most, G // MIN_SHARE) if most >= 2 else slots
         if n * MIN_SHARE > rest * G:
             n = rest * G // MIN_SHARE
         if n > rest:
-            share_meet = 150 if rounds else 480 + 45 * -(-n // rest) * T // 64
-            if step * -(-rest * G // n) + share_meet < step * last:
+            cut = step * -(-rest * G // n) + (150 if rounds else 480 + 45 * -(-n // rest) * T // 64)
+            if cut < last:
                 p.update(sk_tiles=rest, sk_pairs=n, parts=n * 4, pairs=max(p["pairs"], n))
-                last, meet = -(-rest * G // n), share_meet
+                last = cut
     for c, room in ROOM.items():
-        steps = -(-G // c)
-        if c * MIN_SHARE <= G and tiles * 152 <= room * sm_count and step * steps + 200 < step * last + meet:
+        shared = step * -(-G // c) + 200
+        if c * MIN_SHARE <= G and tiles * 152 <= room * sm_count and shared < last:
             p.update(cluster=c, sk_tiles=tiles, sk_pairs=tiles * c, pairs=tiles * c, parts=0)
-            last, meet = steps, 200
-    p["cost"] = base + step * (rounds * G + last) + meet
+            last = shared
+    p["cost"] = base + whole * rounds + last
     return p
 
 

@@ -376,14 +376,15 @@ struct PairPlan {
   int64_t cost = 0;         // estimated time, in 10 ns
 };
 
-// A tile size: the time of a K step and of what is around a pair's steps, in 10
-// ns, measured at N from 5120 to 34816.  Parts of a tile that meet in a cluster
+// A tile size: the time of a K step, of a tile's way out (where its steps take
+// less) and of what is around a pair's tiles, in 10 ns, measured at N from 5120 to
+// 219520.  Parts of a tile that meet in a cluster
 // take 2 us; through the workspace 5 us and half a one for 64 tokens of each
 // part, of which 1.5 are left where whole tiles follow.
 struct PairSize {
-  int T, step, base;
+  int T, step, out, base;
 };
-constexpr PairSize kPairSizes[4] = {{64, 38, 330}, {96, 43, 400}, {128, 47, 450}, {192, 56, 560}};
+constexpr PairSize kPairSizes[4] = {{64, 38, 170, 330}, {96, 43, 210, 400}, {128, 47, 250, 450}, {192, 56, 320, 560}};
 
 PairPlan plan_tiles(const PairSize& size, int64_t M, int64_t N, int64_t K, const Room& room) {
   PairPlan pl;
@@ -397,27 +398,25 @@ PairPlan plan_tiles(const PairSize& size, int64_t M, int64_t N, int64_t K, const
   const int64_t rest = tiles % slots;
   const int64_t rounds = tiles / slots;
   pl.pairs = tiles < slots ? tiles : slots;
-  int64_t last = rest == 0 ? 0 : pl.G;    // steps of the last round
-  int64_t meet = 0;
+  const int64_t whole = size.step * pl.G > size.out ? size.step * pl.G : size.out;
+  int64_t last = rest == 0 ? 0 : whole;   // time of the last round
   // The last round's tiles are cut along K unless they nearly fill it: into as
   // many equal parts as the pairs allow where that is two or more, else into
   // shares that cross tiles.
-  int64_t n = 0, shares = 0, share_meet = 0;
   if (rest != 0 && rest * 8 < slots * 7) {
     const int64_t most = slots / rest;
-    n = most >= 2 ? rest * (most < pl.G / kMinShare ? most : pl.G / kMinShare) : slots;
+    int64_t n = most >= 2 ? rest * (most < pl.G / kMinShare ? most : pl.G / kMinShare) : slots;
     if (n * kMinShare > rest * pl.G) n = rest * pl.G / kMinShare;
     if (n > rest) {
-      shares = (rest * pl.G + n - 1) / n;
-      share_meet = rounds > 0 ? 150 : 480 + 45 * ((n + rest - 1) / rest) * size.T / 64;
-      if (size.step * shares + share_meet < size.step * last) {
+      const int64_t meet = rounds > 0 ? 150 : 480 + 45 * ((n + rest - 1) / rest) * size.T / 64;
+      const int64_t cut = size.step * ((rest * pl.G + n - 1) / n) + meet;
+      if (cut < last) {
         pl.sk_tiles = rest;
         pl.sk_pairs = n;
         pl.cut = true;
         pl.part_bytes = static_cast<size_t>(n) * 4 * pl.T * 128 * sizeof(int32_t);
         if (pl.pairs < n) pl.pairs = n;
-        last = shares;
-        meet = share_meet;
+        last = cut;
       }
     }
   }
@@ -425,18 +424,17 @@ PairPlan plan_tiles(const PairSize& size, int64_t M, int64_t N, int64_t K, const
   // 5120 x 5120 11.2 us, through the workspace 15.2; 512 x 5120 x 1024 13.2 and
   // 17.3; 64 x 2048 x 4096 7.2 and 11.5).
   for (int c = 2; c <= pair::kMaxParts && c * kMinShare <= pl.G; ++c) {
-    const int64_t steps = (pl.G + c - 1) / c;
-    if (tiles <= room.pairs[c] && size.step * steps + 200 < size.step * last + meet) {
+    const int64_t shared = size.step * ((pl.G + c - 1) / c) + 200;
+    if (tiles <= room.pairs[c] && shared < last) {
       pl.parts = c;
       pl.cut = false;
       pl.part_bytes = 0;
       pl.sk_tiles = tiles;
       pl.sk_pairs = pl.pairs = tiles * c;
-      last = steps;
-      meet = 200;
+      last = shared;
     }
   }
-  pl.cost = size.base + size.step * (rounds * pl.G + last) + meet;
+  pl.cost = size.base + whole * rounds + last;
   return pl;
 }
 
