@@ -378,9 +378,9 @@ struct PairPlan {
 
 // A tile size: the time of a K step, of a tile's way out (where its steps take
 // less) and of what is around a pair's tiles, in 10 ns, measured at N from 5120 to
-// 219520.  Parts of a tile that meet in a cluster
-// take 2 us; through the workspace 5 us and half a one for 64 tokens of each
-// part, of which 1.5 are left where whole tiles follow.
+// 219520.  Parts of a tile that meet in a cluster take 2 us; through the workspace
+// 5 us and half a one for 64 tokens of each part, of which 1.5 are left where
+// whole tiles follow.
 struct PairSize {
   int T, step, out, base;
 };

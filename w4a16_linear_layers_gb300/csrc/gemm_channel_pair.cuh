@@ -562,7 +562,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true, summed = false;
     while (ok && w.next()) {
       named_bar_sync(1, kEpiThreads);     // the previous tile's scales are read
-      if (et < T) ctrl->s_a[et] = static_cast<int64_t>(w.t) * T + et < p.M ? __ldg(p.s_a + static_cast<int64_t>(w.t) * T + et) : 0.0f;
+      if (et < T) {
+        const int64_t m = static_cast<int64_t>(w.t) * T + et;
+        ctrl->s_a[et] = m < p.M ? __ldg(p.s_a + m) : 0.0f;
+      }
       // Two neighbouring lanes (channels) exchange a value of each two tokens,
       // so that a lane writes both channels of one: 4 bytes, and half the stores.
       const int odd = lane & 1;
