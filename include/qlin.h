@@ -27,8 +27,10 @@
  *
  * Conventions shared by every call
  * --------------------------------
- *  - Pointers are DEVICE pointers owned by the caller; the library never
- *    allocates, frees or retains them.  All matrices are dense row-major.
+ *  - Pointers are DEVICE pointers owned by the caller, into the memory of the
+ *    device that is current in the call (not a peer's or the host's); the
+ *    library never allocates, frees or retains them.  All matrices are dense
+ *    row-major.
  *  - bf16 and fp16 values are passed as their 16-bit patterns (uint16_t).
  *  - Every call is asynchronous on `stream` (a cudaStream_t; NULL = the legacy
  *    default stream) and returns a qlin_status_t at launch time.  Errors found

@@ -6,14 +6,12 @@
 //   * The MMA runs with the weights as operand A (widened by threads straight
 //     into tensor memory, 128 channels a block) and the tokens as operand B
 //     (T columns, fp16 codes, 128-byte swizzled).  Each block loads its own
-//     words and half of the tokens: the pair reads every operand byte once.
-//     - T = 192: cta_group::2, one MMA of 256 x T for both blocks, issued by the
-//       first, each block's shared memory holding its half of the tokens: 40 KB
-//       through L2 for a K step of 900 cycles or more.
-//     - T of 64, 96 and 128: each block issues its own MMAs of 128 x T
-//       (cta_group::1), and the token halves are multicast into both blocks'
-//       shared memory.  (A 256-row MMA with A in tensor memory takes about 85
-//       cycles at T = 128 and not much less below, two of 128 rows 64.)
+//     words and half of the tokens, and one cta_group::2 MMA of 256 x T, issued
+//     by the first block, reads both halves where they lie: the pair reads every
+//     operand byte once, and an SM takes in 16 KB of words and T x 128 B of codes
+//     a K step.  (MMAs of 128 x T of each block's own need all T tokens in both:
+//     96 x 5120 x 248320 209 us in this form, 236 with every block loading them
+//     all; 128 x 5120 x 5120 12.7 and 13.7.)
 //   * An accumulator takes at most 1024 of K (exact below 2^24); the
 //     epilogue adds each such chunk to int32 registers, under the next chunk's
 //     MMAs: tensor memory holds two accumulators.  (T = 256 has room for one,
@@ -67,14 +65,12 @@ constexpr int kMaxParts = 4;            // pairs of a cluster
 
 template <int T>
 struct Cfg {
-  static constexpr bool k2 = T == 192;                        // one MMA for both blocks
   static constexpr int kHalf = T / 2;                         // tokens that one block loads
-  static constexpr int kRows = k2 ? kHalf : T;                // tokens in one block's shared memory
   static constexpr int kUnit = T == 192 ? 64 : 128;           // K of a unit: one A buffer, one token slot
   static constexpr int kPerStep = 128 / kUnit;                // units of a K step
   static constexpr int kChunk = kChunkK / kUnit;              // units of an accumulator
   static constexpr int kACols = kUnit / 2;
-  static constexpr uint32_t kXBytes = kRows * kUnit * 2u;     // a unit's codes in one block
+  static constexpr uint32_t kXBytes = kHalf * kUnit * 2u;     // a unit's codes in one block
   static constexpr int kX = T == 192 ? 8 : 4;                 // token slots
   static constexpr int kE = T / 2;                            // sums of an epilogue thread
   static constexpr uint32_t kColD = kA * kACols;
@@ -96,10 +92,10 @@ struct Cfg {
 
 struct Ctrl {
   uint64_t wfull[kMaxW], wempty[kMaxW];
-  // of a unit; with one MMA for both blocks, the first block's `ready` and
-  // d_empty count both
+  // of a unit; the first block's `ready` and d_empty count both blocks, the
+  // second's are not used
   uint64_t ready[kMaxU];      // its weights are in TMEM and its codes landed
-  uint64_t consumed[kMaxU];   // the MMAs that read them completed (both blocks')
+  uint64_t consumed[kMaxU];   // the MMAs that read them completed
   uint64_t d_full[2];
   uint64_t d_empty[2];        // the accumulator is drained
   uint64_t mma_done;
@@ -184,18 +180,14 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
   return r;
 }
 
-// Arrives on the barrier, the first block's if one MMA serves both (k2).
+// Arrives on the first block's barrier at this offset.
 // Block-scope release is enough for it too, and all that is ordered: tensor-
 // memory accesses that have completed (tcgen05.wait) and are fenced
 // (tcgen05.fence::before_thread_sync).  No data passes between the blocks
 // through generic memory here.  With cluster scope every arrival waited for
 // the block's outstanding stores, and a K step took 0.95 us for any T up to 128.
-template <bool k2>
 __device__ __forceinline__ void arrive(uint32_t bar, uint32_t first) {
-  if constexpr (k2)
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(map_to_rank(bar, first)) : "memory");
-  else
-    mbar_arrive(bar);
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(map_to_rank(bar, first)) : "memory");
 }
 
 // Tokens: a box of the 3D code map into this block's shared memory, its bytes
@@ -206,17 +198,6 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
       ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(policy)
-      : "memory");
-}
-
-// One K half of them into both blocks' shared memory, counted on each block's
-// own barrier.
-__device__ __forceinline__ void tma_load_both(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x,
-                                              int32_t y, int32_t z, uint64_t policy, uint16_t both) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-      ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6, %7;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "h"(both), "l"(policy)
       : "memory");
 }
 
@@ -232,22 +213,15 @@ __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint32_t a_tmem, uint6
 
 // Arrives once on `bar`, of this block or (kBoth) of both, when this thread's
 // MMAs so far have completed.
-template <bool k2, bool kBoth>
+template <bool kBoth>
 __device__ __forceinline__ void commit(uint32_t bar, uint16_t both) {
-  if constexpr (k2 && kBoth)
+  if constexpr (kBoth)
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
         "h"(both)
         : "memory");
-  else if constexpr (k2)
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-  else if constexpr (kBoth)
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"(both)
-        : "memory");
   else
-    tc_commit(bar);
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ void cluster_sync() {
@@ -340,12 +314,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ctrl->wempty[i]), 4);
     }
     for (int i = 0; i < C::kX; ++i) {
-      mbar_init(smem_u32(&ctrl->ready[i]), C::k2 ? 9 : 5);    // widening warps, and the token copies' issuer
-      mbar_init(smem_u32(&ctrl->consumed[i]), C::k2 ? 1 : 2);
+      mbar_init(smem_u32(&ctrl->ready[i]), 9);      // both blocks' widening warps, and the token copies' issuer
+      mbar_init(smem_u32(&ctrl->consumed[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&ctrl->d_full[i]), 1);
-      mbar_init(smem_u32(&ctrl->d_empty[i]), C::k2 ? 16 : 8);
+      mbar_init(smem_u32(&ctrl->d_empty[i]), 16);
     }
     mbar_init(smem_u32(&ctrl->mma_done), 1);
     mbar_init(smem_u32(&ctrl->part_here), 1);
@@ -357,15 +331,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncwarp();
   if (warp == 1) {
-    if constexpr (C::k2) {
-      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctrl->tmem_base)),
-                   "r"(512u)
-                   : "memory");
-      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-    } else {
-      tmem_alloc(smem_u32(&ctrl->tmem_base), 512);
-      tmem_relinquish();
-    }
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctrl->tmem_base)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
@@ -420,21 +389,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const uint32_t full = smem_u32(&ctrl->ready[slot]);
           const uint32_t dst = sbase + x_off + slot * C::kXBytes;
-          if constexpr (C::k2) {
-            if (rank == 0) mbar_arrive_expect_tx(full, 2 * C::kXBytes);
-            tma_load_pair(dst, &tm_x, map_to_rank(full, first), 0, row, u * (C::kUnit / 64), pol);
-          } else {
-            // each 64 of K is T rows x 128 B, this block's rows its first or second half
-            mbar_arrive_expect_tx(full, C::kXBytes);
+          if (rank == 0) mbar_arrive_expect_tx(full, 2 * C::kXBytes);
 #pragma unroll
-            for (int h = 0; h < C::kUnit / 64; ++h)
-              tma_load_both(dst + h * (T * 128u) + rank * (C::kHalf * 128u), &tm_x, full, 0, row,
-                            u * (C::kUnit / 64) + h, pol, both);
-          }
+          for (int h = 0; h < C::kUnit / 64; ++h)    // each 64 of K is kHalf rows x 128 B
+            tma_load_pair(dst + h * (C::kHalf * 128u), &tm_x, map_to_rank(full, first), 0, row,
+                          u * (C::kUnit / 64) + h, pol);
         }
       }
-      // the last units' MMAs completed, in both blocks: their copies landed, and
-      // no arrival is on its way here when the block ends
+      // the last units' MMAs completed: both blocks' copies landed, and no
+      // arrival is on its way here when the block ends
       if (ok)
         for (int i = j > C::kX ? j - C::kX : 0; i < j; ++i)
           (void)mbar_wait(smem_u32(&ctrl->consumed[i % C::kX]), static_cast<uint32_t>(i / C::kX) & 1u, drain_ctx, 63);
@@ -444,13 +407,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t t0 = globaltimer_ns();
         while (globaltimer_ns() - t0 < 1000000u) __nanosleep(1000);
       }
-    } else if (warp == 1 && (rank == 0 || !C::k2)) {
+    } else if (warp == 1 && rank == 0) {
       // ---------------------------------------------------------- MMAs
       // The whole warp goes through the loop, on values that the compiler can
       // see to be uniform (no branch on a lane's own wait, TMEM from column 0),
       // and one lane issues: the MMA's operands are uniform registers, and filling
       // them from a single lane's made an issue take 60 cycles.
-      constexpr uint32_t idesc = idesc_f16(C::k2 ? 256 : 128, T, false);
+      constexpr uint32_t idesc = idesc_f16(256, T, false);
       const bool leader = elect_one();
       Work w(p, pr);
       int slot = 0, ab = 0, db = 0;
@@ -471,14 +434,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (leader) {
 #pragma unroll
             for (int ks = 0; ks < C::kUnit / 16; ++ks) {
-              const uint32_t off = static_cast<uint32_t>(ks >> 2) * (C::kRows * 128u) + static_cast<uint32_t>(ks & 3) * 32u;
-              if constexpr (C::k2)
-                mma_pair(dcol, a0 + ks * 8, b0 + (off >> 4), idesc, (ci > 0 || ks > 0) ? 1u : 0u);
-              else
-                mma_ts(dcol, a0 + ks * 8, b0 + (off >> 4), idesc, (ci > 0 || ks > 0) ? 1u : 0u);
+              const uint32_t off = static_cast<uint32_t>(ks >> 2) * (C::kHalf * 128u) + static_cast<uint32_t>(ks & 3) * 32u;
+              mma_pair(dcol, a0 + ks * 8, b0 + (off >> 4), idesc, (ci > 0 || ks > 0) ? 1u : 0u);
             }
-            commit<C::k2, true>(smem_u32(&ctrl->consumed[slot]), both);
-            if (ends) commit<C::k2, C::k2>(smem_u32(&ctrl->d_full[db]), both);
+            commit<true>(smem_u32(&ctrl->consumed[slot]), both);
+            if (ends) commit<true>(smem_u32(&ctrl->d_full[db]), both);
           }
           __syncwarp();
           if (++slot == C::kX) {
@@ -492,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (leader) commit<C::k2, false>(smem_u32(&ctrl->mma_done), both);
+      if (leader) commit<false>(smem_u32(&ctrl->mma_done), both);
       __syncwarp();
       (void)mbar_wait(smem_u32(&ctrl->mma_done), 0u, drain_ctx, 67);
     }
@@ -540,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) arrive<C::k2>(smem_u32(&ctrl->ready[u % C::kX]), first);
+          if (lane == 0) arrive(smem_u32(&ctrl->ready[u % C::kX]), first);
         }
         if (!ok) break;
       }
@@ -607,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive<C::k2>(smem_u32(&ctrl->d_empty[db]), first);
+        if (lane == 0) arrive(smem_u32(&ctrl->d_empty[db]), first);
         ++d;
         continue;
       }
@@ -634,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++chunks;
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive<C::k2>(smem_u32(&ctrl->d_empty[db]), first);
+        if (lane == 0) arrive(smem_u32(&ctrl->d_empty[db]), first);
       }
 #pragma unroll
       for (int c = 0; c < E; ++c) acc[c] -= static_cast<int32_t>(chunks * kIntegerBias);
@@ -792,10 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync();
   if (warp == 1) {
     tc_fence_after();
-    if constexpr (C::k2)
-      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
-    else
-      tmem_dealloc(tmem, 512);
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
   }
 }
 
