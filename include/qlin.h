@@ -46,6 +46,13 @@
  *    may then be NULL.
  *  - Alignment: every pointer must be 16-byte aligned (the kernels move data
  *    with TMA and 16-byte vector accesses), unless a call states otherwise.
+ *  - The GEMMs may begin to read their weights (qweight or tiles) while the
+ *    kernel in front of them on the stream still runs: it must not be one that
+ *    writes them.  qlin_pack_gptq, qlin_ingest_nk and qlin_pack_tiles leave
+ *    their output complete for a GEMM directly behind them.  Where another
+ *    library's kernel wrote the weights, an act-quant call in between is
+ *    enough, or any kernel launched in the ordinary way (without programmatic
+ *    serialization).
  *  - The calls run only on an sm_103 GPU (GB300); elsewhere they return
  *    QLIN_ERR_DEVICE.
  */
@@ -290,10 +297,6 @@ qlin_status_t qlin_gemm_w8a8_gs128_noalloc(const int8_t *q_a, const float *s_a,
  *            int8 one; may be NULL where that is 0 (small problems).  It needs
  *            no zeroing and holds nothing between calls.  Calls that share a
  *            workspace must not overlap.
- *
- * Like the other GEMMs, the call may begin to read qweight while the previous
- * kernel on its stream runs, if that is a call of this library: weights are
- * not written by such a kernel.
  *
  * K is at most 130,944 (QLIN_ERR_SHAPE above): sums of that many products of
  * two int8 values fit int32.

@@ -40,6 +40,19 @@ __global__ void fill_kernel(int32_t* __restrict__ dst, int64_t count, uint32_t v
     dst[i] = static_cast<int32_t>(value);
 }
 
+// Behind a kernel that writes weights.  The GEMMs are launched with programmatic
+// serialization and read weights before they wait for the previous kernel.
+// Launched without it, this one starts when the weights are complete and
+// visible, and a GEMM behind it when it has ended.
+__global__ void weights_written_kernel() {}
+
+cudaError_t weights_written(cudaStream_t stream) {
+  const cudaError_t e = cudaGetLastError();   // of the launch in front
+  if (e != cudaSuccess) return e;
+  weights_written_kernel<<<1, 1, 0, stream>>>();
+  return cudaGetLastError();
+}
+
 // One thread waits on a barrier that nothing completes; the bounded wait runs
 // out, records kDevTimeout and the kernel returns normally.
 __global__ void wait_timeout_kernel(int64_t limit_ns, int* err) {
@@ -122,8 +135,8 @@ cudaError_t launch_ingest_nk(const int32_t* packed_nk, const uint16_t* scales_ng
                              int64_t N, int bits, int32_t* qweight, uint16_t* scales,
                              cudaStream_t stream) {
   cudaError_t e = transpose<int32_t>(packed_nk, N, K * bits / 32, qweight, stream);
-  if (e != cudaSuccess) return e;
-  return transpose<uint16_t>(scales_ng, N, K / kGroup, scales, stream);
+  if (e == cudaSuccess) e = transpose<uint16_t>(scales_ng, N, K / kGroup, scales, stream);
+  return e == cudaSuccess ? weights_written(stream) : e;
 }
 
 cudaError_t launch_pack(const int8_t* q, int64_t K, int64_t N, int bits, int32_t* qweight,
@@ -134,7 +147,7 @@ cudaError_t launch_pack(const int8_t* q, int64_t K, int64_t N, int bits, int32_t
     pack_kernel<8><<<grid_for(words, 256), 256, 0, stream>>>(q, N, words, qweight, err);
   else
     pack_kernel<4><<<grid_for(words, 256), 256, 0, stream>>>(q, N, words, qweight, err);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = weights_written(stream);
   if (e != cudaSuccess || qzeros == nullptr) return e;
   const int64_t zwords = (K / kGroup) * (N / per);
   const uint32_t zword = bits == 8 ? 0x80808080u : 0x88888888u;
@@ -152,7 +165,7 @@ cudaError_t launch_pack_tiles(const int32_t* qweight, int64_t K, int64_t N, int 
   const int wpg = kGroup * bits / 32;
   const int64_t total = static_cast<int64_t>(tiles_bytes(K, N, bits) / 4);
   tiles_kernel<<<grid_for(total, 256), 256, 0, stream>>>(qweight, N, K / kGroup, wpg, total, tiles);
-  return cudaGetLastError();
+  return weights_written(stream);
 }
 
 cudaError_t launch_wait_timeout(int64_t limit_ns, int* err, cudaStream_t stream) {
