@@ -308,7 +308,10 @@ def _on(stream, lead, call, *args):
     index = lead.get_device()
     if not isinstance(stream, torch.cuda.Stream):
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        stream = torch.cuda.ExternalStream(handle, device=torch.device("cuda", index))
+        # ExternalStream takes the default stream's handle, 0, for none given, and
+        # makes a stream of its own
+        stream = (torch.cuda.ExternalStream(handle, device=torch.device("cuda", index)) if handle
+                  else torch.cuda.default_stream(index))
     if stream.device_index != index:
         raise ValueError(f"stream must be of cuda:{index}, got {stream.device}")
     caller = torch.cuda.current_stream(index)
