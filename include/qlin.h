@@ -182,9 +182,10 @@ qlin_status_t qlin_silu_mul_act_quant_c16(const uint16_t *gate_up, int64_t M, in
  *   q, s_a, y     as for the RMSNorm producer (y, z itself, may be NULL)
  *
  * A row of h that is all zero gives z = 0, q = 0 and s_a = 0, also with
- * eps = 0.  Non-finite sums, rows whose mean of h^2 is not a normal fp32
- * number with eps = 0, and sums of h^2 of 2^127 and more are outside the
- * contract.  Errors as for the RMSNorm producer.
+ * eps = 0.  Outside the contract: non-finite sums and gamma, sums of h^2
+ * beyond fp32's range, and rows, other than zero ones, whose mean of h^2 plus
+ * eps is below 2^-100.  Where |t| is below 2^-126 (subnormal in bf16) it may be one step of
+ * 2^-133 off.  Errors as for the RMSNorm producer.
  */
 qlin_status_t qlin_add_rmsnorm_act_quant_i8(const uint16_t *x, const uint16_t *residual,
                                             const uint16_t *gamma, float eps, int64_t M,

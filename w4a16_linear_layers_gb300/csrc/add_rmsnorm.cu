@@ -97,14 +97,20 @@ struct Rstd {
   float hi, lo;
 };
 
-// 1 / sqrt((s + c) / K + eps) as hi + lo; inv_k = 1 / K as ki + kl.  y0 is
-// rsqrtf's approximation; with r = 1 - v y0^2 (formed exactly to about 2^-45),
+// 1 / sqrt((s + c) / K + eps) as hi + lo; 1 / K as ki + kl.  y0 is rsqrtf's
+// approximation; with r = 1 - v y0^2 (formed exactly to about 2^-45),
 // 1 / sqrt(v) = y0 (1 - r)^(-1/2) = y0 + y0 (r / 2 + 3 r^2 / 8 + ...).
+// v above 2^60 or below 2^-60 is brought nearer to 1 by a power of 4: from 2^105
+// and 2^-104 on the products' remainders would be subnormal, and rounded.
 // A row of zeros with eps = 0 gives 0.
 __device__ __forceinline__ Rstd row_rstd(float s, float c, float ki, float kl, float eps) {
+  const float about = __fmaf_rn(s, ki, eps);
+  const float back = about > 0x1p60f ? 0x1p-50f : about < 0x1p-60f ? 0x1p50f : 1.0f;
+  const float scale = __fmul_rn(back, back);
+  s = __fmul_rn(s, scale);
   float vh = __fmul_rn(s, ki);
-  float vl = __fadd_rn(__fmaf_rn(s, ki, -vh), __fmaf_rn(s, kl, __fmul_rn(c, ki)));
-  twosum1(vh, vl, eps);
+  float vl = __fadd_rn(__fmaf_rn(s, ki, -vh), __fmaf_rn(s, kl, __fmul_rn(__fmul_rn(c, scale), ki)));
+  twosum1(vh, vl, __fmul_rn(eps, scale));
   const float t = __fadd_rn(vh, vl);
   vl = __fsub_rn(vl, __fsub_rn(t, vh));
   vh = t;
@@ -117,7 +123,7 @@ __device__ __forceinline__ Rstd row_rstd(float s, float c, float ki, float kl, f
   const float r = __fsub_rn(__fsub_rn(1.0f, p), pe);
   const float corr = __fmul_rn(y0, __fmul_rn(r, __fmaf_rn(0.375f, r, 0.5f)));
   const float hi = __fadd_rn(y0, corr);
-  return Rstd{hi, __fsub_rn(corr, __fsub_rn(hi, y0))};
+  return Rstd{__fmul_rn(hi, back), __fmul_rn(__fsub_rn(corr, __fsub_rn(hi, y0)), back)};
 }
 
 // bf16 bits of x * (hi + lo), rounded once: p + e is the product with its
