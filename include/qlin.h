@@ -182,9 +182,11 @@ qlin_status_t qlin_silu_mul_act_quant_c16(const uint16_t *gate_up, int64_t M, in
  *   q, s_a, y     as for the RMSNorm producer (y, z itself, may be NULL)
  *
  * A row of h that is all zero gives z = 0, q = 0 and s_a = 0, also with
- * eps = 0.  Outside the contract: non-finite sums and gamma, sums of h^2
- * beyond fp32's range, and rows, other than zero ones, whose mean of h^2 plus
- * eps is below 2^-100.  Where |t| is below 2^-126 (subnormal in bf16) it may be one step of
+ * eps = 0.  A row that holds a NaN or an infinity, or whose sum of h^2 is
+ * beyond fp32's range, gives z = NaN and s_a = NaN, so that a linear after it
+ * gives NaN too; its codes mean nothing.  Outside the contract: rows, other
+ * than zero ones, whose mean of h^2 plus eps is below 2^-100, and non-finite
+ * gamma.  Where |t| is below 2^-126 (subnormal in bf16) it may be one step of
  * 2^-133 off.  Errors as for the RMSNorm producer.
  */
 qlin_status_t qlin_add_rmsnorm_act_quant_i8(const uint16_t *x, const uint16_t *residual,

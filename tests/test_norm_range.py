@@ -1,5 +1,5 @@
 """Residual addition + RMSNorm + act-quant at the ends of its range: rows of very
-large and very small values.
+large and very small values, and rows that hold no finite result.
 
 The references are exact where the definition is: the sum is one bf16 rounding,
 and the oracle forms the norm in binary64 (relative error of its 1 / sqrt about
@@ -88,3 +88,59 @@ def test_products_next_to_the_middle_at_the_largest_sums():
         _, _, z0 = oracle.rmsnorm_act_quant_i8(hb, gb, 0.0)
         _, _, _, y = run(hb, zero, gb, 0.0)
         assert np.array_equal(from_dev_bits(y), z0)
+
+
+BAD = ["nan", "inf", "both infinities", "the sum overflows bf16", "the squares overflow", "large and nan"]
+
+
+@pytest.mark.parametrize("M,K", [(8, 256), (300, 640), (12, 17408), (9, 33024)])
+@pytest.mark.parametrize("c16", [False, True], ids=["i8", "c16"])
+def test_rows_without_a_finite_result_are_nan(M, K, c16):
+    """Not zeros: the product after them is NaN too, and the other rows are as ever."""
+    rng = np.random.default_rng(K)
+    x, r = rng.standard_normal((M, K)), rng.standard_normal((M, K))
+    xb, rb = bits(x), bits(r)
+    at = {name: i + 1 for i, name in enumerate(BAD)}
+    nan, inf = 0x7FC0, 0x7F80
+    xb[at["nan"], K // 3] = nan
+    rb[at["inf"], 5] = inf
+    xb[at["both infinities"], [0, K - 1]] = inf
+    rb[at["both infinities"], K - 1] = inf | 0x8000
+    xb[at["the sum overflows bf16"], K // 2] = rb[at["the sum overflows bf16"], K // 2] = 0x7F7F
+    xb[at["the squares overflow"], :] = bits(2.0 ** 62)
+    rb[at["the squares overflow"], :] = bits(2.0 ** 62)
+    xb[at["large and nan"], :] = bits(2.0 ** 62)
+    xb[at["large and nan"], K - 2] = nan | 0x8000
+    gb = bits(1.0 + 0.1 * rng.standard_normal(K))
+    bad = np.zeros(M, bool)
+    bad[list(at.values())] = True
+    q, s, h, y = run(xb, rb, gb, 1e-6, c16)
+    assert torch.isnan(s).cpu().numpy().tolist() == bad.tolist()
+    assert torch.isnan(y).all(1).cpu().numpy().tolist() == bad.tolist()
+    fine = ~bad
+    hb = bits(synth.bf16_values(xb[fine]).astype(np.float64) + synth.bf16_values(rb[fine]).astype(np.float64))
+    q0, s0, z0 = oracle.rmsnorm_act_quant_i8(hb, gb, 1e-6)
+    assert np.array_equal(from_dev_bits(h)[fine], hb) and np.array_equal(from_dev_bits(y)[fine], z0)
+    assert np.array_equal(s.cpu().numpy()[fine], s0)
+    assert np.array_equal(q.float().cpu().numpy()[fine], q0.astype(np.float32))
+    # the product: few channels (streamed) and many (in tiles)
+    for N in (64, 20488) if K == 640 else (64,):
+        w = torch.randint(-2 ** 31, 2 ** 31, (K // 4, N), device="cuda").to(torch.int32)
+        s_w = torch.ones(N, device="cuda")
+        out = (qlin.gemm_w8a8_ch_c16 if c16 else qlin.gemm_w8a8_ch)(q, s, w, s_w)
+        assert torch.isnan(out).all(1).cpu().numpy().tolist() == bad.tolist()
+        assert not torch.isnan(out[torch.from_numpy(fine).cuda()]).any()
+
+
+def test_a_bad_row_written_in_place():
+    K = 640
+    xb, rb = bits(np.ones((4, K))), bits(np.full((4, K), 2.0))
+    xb[2, 7] = 0x7FC0
+    x, r, g = (to_dev_bits(a, torch.bfloat16) for a in (xb, rb, bits(np.ones(K))))
+    _, s, h = qlin.add_rmsnorm_act_quant_i8(x, r, g, 1e-6, residual_out=r)
+    assert h.data_ptr() == r.data_ptr()
+    assert torch.isnan(s).tolist() == [False, False, True, False]
+    assert torch.isnan(r).sum() == 1 and torch.isnan(r[2, 7])
+    keep = torch.ones_like(r, dtype=torch.bool)
+    keep[2, 7] = False
+    assert (r[keep] == 3).all()

@@ -102,7 +102,8 @@ struct Rstd {
 // 1 / sqrt(v) = y0 (1 - r)^(-1/2) = y0 + y0 (r / 2 + 3 r^2 / 8 + ...).
 // v above 2^60 or below 2^-60 is brought nearer to 1 by a power of 4: from 2^105
 // and 2^-104 on the products' remainders would be subnormal, and rounded.
-// A row of zeros with eps = 0 gives 0.
+// A row of zeros with eps = 0 gives 0; a sum that is not finite gives NaN (its
+// c is NaN, from the difference of two infinities).
 __device__ __forceinline__ Rstd row_rstd(float s, float c, float ki, float kl, float eps) {
   const float about = __fmaf_rn(s, ki, eps);
   const float back = about > 0x1p60f ? 0x1p-50f : about < 0x1p-60f ? 0x1p50f : 1.0f;
@@ -114,7 +115,7 @@ __device__ __forceinline__ Rstd row_rstd(float s, float c, float ki, float kl, f
   const float t = __fadd_rn(vh, vl);
   vl = __fsub_rn(vl, __fsub_rn(t, vh));
   vh = t;
-  if (!(vh > 0.0f)) return Rstd{0.0f, 0.0f};
+  if (vh == 0.0f) return Rstd{0.0f, 0.0f};
   const float y0 = rsqrtf(vh);
   const float a = __fmul_rn(y0, y0);
   const float ae = __fmaf_rn(y0, y0, -a);
@@ -190,7 +191,7 @@ __device__ __forceinline__ uint4 norm8(uint4 h, uint4 g, Rstd rs, const Bracket&
   return make_uint4(mul_bf16x2(t[0], gw[0]), mul_bf16x2(t[1], gw[1]), mul_bf16x2(t[2], gw[2]), mul_bf16x2(t[3], gw[3]));
 }
 
-// magnitudes of the larger ones (signs to be ignored)
+// magnitudes of the larger ones (signs to be ignored); of a NaN and a number the number
 __device__ __forceinline__ uint32_t absmax2(uint32_t m, uint32_t v) {
   uint32_t d;
   asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(m), "r"(v));
@@ -371,6 +372,11 @@ __device__ __forceinline__ float block_absmax(uint32_t m2, uint32_t* red) {
   return __uint_as_float(m << 16);
 }
 
+// NaN where the row has no finite norm: its z are all NaN, which the maximum leaves out.
+__device__ __forceinline__ float row_scale(float amax, Rstd rs) {
+  return rs.hi == rs.hi ? __fdiv_rn(amax, 127.0f) : __int_as_float(0x7FFFFFFF);
+}
+
 // kParts blocks (a cluster) per row, kVec vectors of 8 elements a thread
 // (kParts * blockDim * kVec >= K / 8): the row stays in registers from its one
 // read to the codes.
@@ -434,9 +440,9 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks) add_rmsnorm_kernel(co
     }
   }
   const float amax = block_absmax<kParts>(m2, redm);
-  const float s = __fdiv_rn(amax, 127.0f);
+  const float s = row_scale(amax, rs);
   if (tid == 0) p.s[row] = s;
-  const bool zero = amax == 0.0f;
+  const bool zero = s == 0.0f;
   const Bracket inv(zero ? 0.0f : __frcp_rn(s));
   const bool divide = !zero && !(s >= 0x1p-120f);
 #pragma unroll
@@ -478,9 +484,9 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_long_kernel(const AddNormPar
     if (yr) yr[v] = z;
   }
   const float amax = block_absmax<1>(m2, redm);
-  const float s = __fdiv_rn(amax, 127.0f);
+  const float s = row_scale(amax, rs);
   if (threadIdx.x == 0) p.s[blockIdx.x] = s;
-  const bool zero = amax == 0.0f;
+  const bool zero = s == 0.0f;
   const Bracket inv(zero ? 0.0f : __frcp_rn(s));
   const bool divide = !zero && !(s >= 0x1p-120f);
   for (int64_t v = threadIdx.x; v < nvec; v += blockDim.x)
