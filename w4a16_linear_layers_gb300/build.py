@@ -6,10 +6,15 @@ CUDA runtime statically and reaches the driver's tensor-map encoder through
 the runtime's entry-point query, so it does not link against PyTorch or
 libcuda.  csrc/torch_calls.cpp, the Python extension of the calls that are
 short on the device, becomes ``_build/qlin_torch.so`` beside it, with the host
-compiler and PyTorch's headers.  Usage: ``python -m w4a16_linear_layers_gb300.build [--force]``.
+compiler and PyTorch's headers, and ``qlin_torch.stamp`` says which PyTorch and
+Python it is for.  The library does not wait for it: it is there without
+PyTorch, and where the extension cannot be built.  Usage:
+``python -m w4a16_linear_layers_gb300.build [--force]``.
 """
 from __future__ import annotations
 
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -23,6 +28,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libqlin.so")
 CALLS_PATH = os.path.join(BUILD_DIR, "qlin_torch.so")
+CALLS_SOURCE = os.path.join(CSRC, "torch_calls.cpp")
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -41,24 +47,43 @@ def _sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
-def _deps():
+def _newer(path: str, deps) -> bool:
+    """path is there and none of deps changed after it."""
+    return os.path.exists(path) and all(os.path.getmtime(d) <= os.path.getmtime(path) for d in deps)
+
+
+def _library_up_to_date() -> bool:
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    deps.append(os.path.join(INCLUDE, "qlin.h"))
-    deps.append(os.path.abspath(__file__))
-    return deps
+    deps = [d for d in deps if d != CALLS_SOURCE]
+    return _newer(LIB_PATH, deps + [os.path.join(INCLUDE, "qlin.h"), os.path.abspath(__file__)])
+
+
+def calls_stamp() -> str | None:
+    """What the extension is built for; None where there is no PyTorch."""
+    if importlib.util.find_spec("torch") is None:
+        return None
+    return f"torch {importlib.metadata.version('torch')}, python {sysconfig.get_config_var('SOABI')}"
+
+
+def calls_built_for() -> str | None:
+    try:
+        with open(os.path.splitext(CALLS_PATH)[0] + ".stamp") as f:
+            return f.read()
+    except OSError:
+        return None
+
+
+def _calls_up_to_date() -> bool:
+    return (calls_built_for() == calls_stamp()
+            and _newer(CALLS_PATH, [CALLS_SOURCE, os.path.join(INCLUDE, "qlin.h"), os.path.abspath(__file__)]))
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(CALLS_PATH):
-        return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(CALLS_PATH))
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return _library_up_to_date() and (calls_stamp() is None or _calls_up_to_date())
 
 
 def _build_calls() -> None:
-    import torch
-
-    base = os.path.dirname(torch.__file__)
+    base = os.path.dirname(importlib.util.find_spec("torch").origin)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     headers = [sysconfig.get_paths()["include"], os.path.join(base, "include"),
                os.path.join(base, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
@@ -66,18 +91,21 @@ def _build_calls() -> None:
     cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden", "-I", INCLUDE]
     for path in headers:
         cmd += ["-isystem", path]
-    cmd += [os.path.join(CSRC, "torch_calls.cpp"), "-o", tmp, "-L", os.path.join(base, "lib"),
+    cmd += [CALLS_SOURCE, "-o", tmp, "-L", os.path.join(base, "lib"),
             "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for torch_calls.cpp:\n{r.stdout}\n{r.stderr}")
+    stamp = os.path.splitext(CALLS_PATH)[0] + ".stamp"
+    if os.path.exists(stamp):      # none while the extension changes
+        os.remove(stamp)
     os.replace(tmp, CALLS_PATH)
+    with open(stamp + f".{os.getpid()}.tmp", "w") as f:
+        f.write(calls_stamp())
+    os.replace(stamp + f".{os.getpid()}.tmp", stamp)
 
 
-def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
-    if not force and up_to_date():
-        return LIB_PATH
-    os.makedirs(BUILD_DIR, exist_ok=True)
+def _build_library(verbose: bool, extra_flags) -> None:
     cc = nvcc()
     flags = NVCC_FLAGS + list(extra_flags or [])
     srcs = _sources()
@@ -94,16 +122,27 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
             print(r.stdout + r.stderr, flush=True)
         return obj
 
-    with ThreadPoolExecutor(max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
-        calls = ex.submit(_build_calls)
+    with ThreadPoolExecutor(max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
         objs = list(ex.map(compile_one, srcs))
-        calls.result()
     tmp = LIB_PATH + f".{os.getpid()}.tmp"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+
+
+def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
+    """The library, then what is left of the extension: an error of the latter
+    is raised when the former is in place."""
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    with ThreadPoolExecutor(1) as ex:      # beside the library
+        calls = (ex.submit(_build_calls) if calls_stamp() is not None and (force or not _calls_up_to_date())
+                 else None)
+        if force or not _library_up_to_date():
+            _build_library(verbose, extra_flags)
+    if calls is not None and calls.exception() is not None:
+        raise RuntimeError(f"{LIB_PATH} is built, its Python extension is not") from calls.exception()
     return LIB_PATH
 
 

@@ -281,9 +281,10 @@ def _calls():
     with _lock:
         if _torch_calls is None:
             path = _build.CALLS_PATH
-            if not os.path.exists(path):
-                raise QlinError(QLIN_ERR_CUDA, f"{path} is not built; run "
-                                "`python -m w4a16_linear_layers_gb300.build` (or __graft_entry__.build())")
+            built, here = _build.calls_built_for(), _build.calls_stamp()
+            if not os.path.exists(path) or built != here:
+                raise QlinError(QLIN_ERR_CUDA, f"{path} is not built for {here}" + (f" (but for {built})" if built else "")
+                                + "; run `python -m w4a16_linear_layers_gb300.build` (or __graft_entry__.build())")
             loader = importlib.machinery.ExtensionFileLoader("qlin_torch", path)
             module = importlib.util.module_from_spec(importlib.util.spec_from_loader("qlin_torch", loader))
             loader.exec_module(module)
