@@ -44,6 +44,7 @@
 
 #include <cuda_bf16.h>
 
+#include "channel_plan.h"
 #include "qlin_device.cuh"
 #include "qlin_internal.h"
 
@@ -61,7 +62,6 @@ constexpr uint32_t kCtrl = 2048;
 constexpr uint32_t kSmemMax = 232448;
 constexpr int kMaxW = 8;
 constexpr int kMaxU = 8;
-constexpr int kMaxParts = 4;            // pairs of a cluster
 
 template <int T>
 struct Cfg {
