@@ -278,8 +278,8 @@ __device__ __forceinline__ void add_integers(uint32_t x0, uint32_t x1, int32_t& 
       "mov.b64 {%2, %3}, l;\n\t}"
       : "=r"(h0), "=r"(h1), "=r"(l0), "=r"(l1)
       : "r"(x0), "r"(x1), "r"(kBigMagic), "r"(kSmallMagic), "r"(kBigMagic | 0x80000000u), "r"(0xBF800000u));
-  a0 += static_cast<int32_t>((h0 << 12) + l0);
-  a1 += static_cast<int32_t>((h1 << 12) + l1);
+  a0 = static_cast<int32_t>(static_cast<uint32_t>(a0) + (h0 << 12) + l0);
+  a1 = static_cast<int32_t>(static_cast<uint32_t>(a1) + (h1 << 12) + l1);
 }
 
 template <int N>
@@ -597,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) arrive(smem_u32(&ctrl->d_empty[db]), first);
       }
 #pragma unroll
-      for (int c = 0; c < E; ++c) acc[c] -= static_cast<int32_t>(chunks * kIntegerBias);
+      for (int c = 0; c < E; ++c) acc[c] = static_cast<int32_t>(static_cast<uint32_t>(acc[c]) - chunks * kIntegerBias);
       if (!named_bar_and(1, kEpiThreads, ok)) break;
       if (p.parts > 1) {
         summed = true;
