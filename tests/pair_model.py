@@ -156,13 +156,17 @@ def _roles(c, segments):
             if (j & 1) != group:
                 continue
             yield ("wait", f"wfull{b}.{j % nw}", (j // nw) & 1)
-            yield ("read", f"W{b}.{j % nw}")
-            yield ("arrive", f"wempty{b}.{j % nw}")
+            if c.get("early_release"):
+                yield ("arrive", f"wempty{b}.{j % nw}")
             for u in range(j * per, (j + 1) * per):
                 if u >= KA and not c.get("no_consumed"):
                     yield ("wait", f"consumed{b}.{(u - KA) % kx}", ((u - KA) // kx) & 1)
+                # the words may be loaded as late as here
+                yield ("read", f"W{b}.{j % nw}")
                 yield ("write", f"A{b}.{u % KA}")
                 yield ("arrive", f"ready{u % kx}")
+            if not c.get("early_release"):
+                yield ("arrive", f"wempty{b}.{j % nw}")
 
     def epilogue(b, w):
         chunk = 0

@@ -36,8 +36,8 @@ def test_no_deadlock_or_hazard_with_all_warps(T):
 
 
 @pytest.mark.parametrize("T", [64, 192])
-@pytest.mark.parametrize("change", ["no_consumed", "no_dempty", "commit_to_one"])
-def test_a_missing_wait_or_commit_is_seen(T, change):
+@pytest.mark.parametrize("change", ["no_consumed", "no_dempty", "commit_to_one", "early_release"])
+def test_a_missing_wait_or_commit_or_an_early_release_is_seen(T, change):
     assert failures(T, 30, segments=[[40], [3, 17, 17]], **{change: True}) != {}
 
 

@@ -477,8 +477,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t word[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) word[i] = src[i * kF + r];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ctrl->wempty[ws]));
 #pragma unroll
         for (int part = 0; part < C::kPerStep; ++part) {
           const int u = j * C::kPerStep + part;
@@ -500,7 +498,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) arrive(smem_u32(&ctrl->ready[u % C::kX]), first);
+          if (lane == 0) {
+            arrive(smem_u32(&ctrl->ready[u % C::kX]), first);
+            // The slot is free when the words are in tensor memory, not before: an
+            // arrival ahead of that does not keep the compiler from loading the last
+            // words behind it, where they can be those of a later step.
+            if (part == C::kPerStep - 1) mbar_arrive(smem_u32(&ctrl->wempty[ws]));
+          }
         }
         if (!ok) break;
       }
