@@ -161,29 +161,13 @@ inline bool streams(int64_t M, int64_t N, int64_t K, const Room& room) {
   return 180 + 88 * split_stream(tiles, room.tokens16, K).steps < plan_pair(M, N, K, room).cost;
 }
 
-// The pair kernel reads fp16 codes: int8 ones from an image in the workspace,
-// and some small fp16 ones.  Loads through a tensor map of up to 128 KB were slow
-// (12 x 5120 x 34816, 120 KB of codes: 55 us; 13 rows 38; about 0.2 us a K step), so
-// such an image lies in front of memory that makes the map's K 1024 halves of
-// 128 B; the kernel loads none past the codes' own, but what a map describes has
-// to be there.  fp16 codes get it where the preparing kernel runs in any case or
-// the K steps make up for it (24 x 1152 x 8192, 9 steps: 6.7 us without, 9.0 with).
-constexpr int64_t kSmallCodes = 65536;
-constexpr int64_t kMapHalves = 1024;
-inline bool small_codes(int64_t M, int64_t K) { return M * K <= kSmallCodes; }
-inline bool has_image(const PairPlan& pl, int64_t M, int64_t K, bool c16) {
-  return !c16 || (small_codes(M, K) && (pl.cut || pl.TT * pl.F2 * pl.G >= 16 * pl.pairs));
-}
-inline size_t image_bytes(int64_t M, int64_t K) {
-  const int64_t own = M * K * 2;
-  return static_cast<size_t>(small_codes(M, K) ? (M - 1) * K * 2 + kMapHalves * 128 : own);
-}
-static_assert(kMapHalves * 64 >= kSmallCodes, "a row of small codes is no longer than the map's");
+// The pair kernel reads fp16 codes: int8 ones from an image in the workspace.
+inline size_t image_bytes(int64_t M, int64_t K) { return static_cast<size_t>(M) * K * 2; }
 
 inline size_t plan_workspace_bytes(int64_t M, int64_t N, int64_t K, bool c16, const Room& room) {
   if (streams(M, N, K, room)) return 0;
   const PairPlan pl = plan_pair(M, N, K, room);
-  return (pl.cut ? kCounterBytes + pl.part_bytes : 0) + (has_image(pl, M, K, c16) ? image_bytes(M, K) : 0);
+  return (pl.cut ? kCounterBytes + pl.part_bytes : 0) + (c16 ? 0 : image_bytes(M, K));
 }
 
 }  // namespace qlin

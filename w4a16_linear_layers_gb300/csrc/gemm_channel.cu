@@ -321,27 +321,21 @@ cudaError_t launch_c(const ChannelParams& p, const Room& room, cudaStream_t stre
 
 // ------------------------------------------------------- larger batches
 
-// Before the pair kernel: the counters to zero and the codes' fp16 image (16
-// codes a thread).
-template <bool kC16>
-__global__ void __launch_bounds__(256) pair_prepare_kernel(int* counters, const void* __restrict__ q,
+// Before the pair kernel: the counters to zero and int8 codes as fp16 (16 a
+// thread).
+__global__ void __launch_bounds__(256) pair_prepare_kernel(int* counters, const int8_t* __restrict__ q,
                                                            uint16_t* __restrict__ image, int64_t n16) {
   grid_dep_launch();  // the pairs' blocks may take the SMs that come free, and load words
   grid_dep_wait();    // the workspace may still be in use, and the codes come from the previous kernel
   if (blockIdx.x == 0 && counters != nullptr) counters[threadIdx.x] = 0;
   for (int64_t i = blockIdx.x * static_cast<int64_t>(256) + threadIdx.x; i < n16;
        i += static_cast<int64_t>(gridDim.x) * 256) {
+    const uint4 raw = __ldg(reinterpret_cast<const uint4*>(q) + i);
     uint4 lo, hi;
-    if constexpr (kC16) {
-      lo = __ldg(static_cast<const uint4*>(q) + 2 * i);
-      hi = __ldg(static_cast<const uint4*>(q) + 2 * i + 1);
-    } else {
-      const uint4 raw = __ldg(static_cast<const uint4*>(q) + i);
-      biased_u8x4_to_f16x4(raw.x ^ 0x80808080u, lo.x, lo.y);
-      biased_u8x4_to_f16x4(raw.y ^ 0x80808080u, lo.z, lo.w);
-      biased_u8x4_to_f16x4(raw.z ^ 0x80808080u, hi.x, hi.y);
-      biased_u8x4_to_f16x4(raw.w ^ 0x80808080u, hi.z, hi.w);
-    }
+    biased_u8x4_to_f16x4(raw.x ^ 0x80808080u, lo.x, lo.y);
+    biased_u8x4_to_f16x4(raw.y ^ 0x80808080u, lo.z, lo.w);
+    biased_u8x4_to_f16x4(raw.z ^ 0x80808080u, hi.x, hi.y);
+    biased_u8x4_to_f16x4(raw.w ^ 0x80808080u, hi.z, hi.w);
     reinterpret_cast<uint4*>(image)[2 * i] = lo;
     reinterpret_cast<uint4*>(image)[2 * i + 1] = hi;
   }
@@ -383,23 +377,21 @@ cudaError_t launch_pair(const ChannelGemmArgs& a, int* err, const Room& room, cu
     counters = reinterpret_cast<int*>(ws);
     at = kCounterBytes + pl.part_bytes;
   }
-  const bool with_image = has_image(pl, a.M, a.K, a.act_c16);
-  if (pl.cut || with_image) {
-    const int64_t n16 = with_image ? a.M * a.K / 16 : 0;
-    uint16_t* image = with_image ? reinterpret_cast<uint16_t*>(ws + at) : nullptr;
+  if (pl.cut || !a.act_c16) {
+    const int8_t* q = a.act_c16 ? nullptr : static_cast<const int8_t*>(a.act);
+    const int64_t n16 = a.act_c16 ? 0 : a.M * a.K / 16;
+    uint16_t* image = a.act_c16 ? nullptr : reinterpret_cast<uint16_t*>(ws + at);
     int64_t blocks = (n16 + 255) / 256;
     blocks = blocks < 1 ? 1 : blocks > 4096 ? 4096 : blocks;
-    const cudaError_t e = launch_pdl(a.act_c16 ? pair_prepare_kernel<true> : pair_prepare_kernel<false>,
-                                     dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, counters, a.act,
-                                     image, n16);
+    const cudaError_t e = launch_pdl(pair_prepare_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream,
+                                     counters, q, image, n16);
     if (e != cudaSuccess) return e;
-    if (with_image) codes = image;
+    if (!a.act_c16) codes = image;
   }
   CUtensorMap tw, tx;
   if (!make_map_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_INT32, a.qweight, a.N, a.K / 4, static_cast<uint64_t>(a.N) * 4, 128,
                    32, CU_TENSOR_MAP_SWIZZLE_NONE) ||
-      !make_act_map(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, codes, a.M, a.K, static_cast<uint32_t>(pl.T / 2), 1,
-                    with_image && small_codes(a.M, a.K) ? kMapHalves : 0))
+      !make_act_map(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, codes, a.M, a.K, static_cast<uint32_t>(pl.T / 2), 1))
     return cudaErrorInvalidValue;
   pair::Params p;
   p.s_a = a.s_a;

@@ -24,7 +24,7 @@ const DeviceInfo* current_device();
 // make_act_map: 16-bit codes or activations [M, K] as boxes of `halves`
 // 64-wide K halves x T rows; make_map_2d: a plain row-major matrix.
 bool make_act_map(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t M,
-                  uint64_t K, uint32_t T, uint32_t halves, uint64_t min_halves = 0);
+                  uint64_t K, uint32_t T, uint32_t halves);
 bool make_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t inner,
                  uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
                  CUtensorMapSwizzle swz);

@@ -30,14 +30,12 @@ EncodeFn encode_fn() {
 
 // 16-bit activations [M][K] seen as a 3D tensor {64 (k inside a half group),
 // M (rows, stride K*2 bytes), K/64 (half groups, stride 128 bytes)}; a box
-// {64, T, 2g} is g 128-wide K groups as 2g swizzled T x 128 B tiles.  The map
-// has at least min_halves half groups, for a kernel that loads none past K / 64:
-// the memory up to there behind the last row has to exist.
+// {64, T, 2g} is g 128-wide K groups as 2g swizzled T x 128 B tiles.
 bool make_act_map(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t M,
-                  uint64_t K, uint32_t T, uint32_t halves, uint64_t min_halves) {
+                  uint64_t K, uint32_t T, uint32_t halves) {
   EncodeFn fn = encode_fn();
   if (!fn) return false;
-  const cuuint64_t dims[3] = {64, M, K / 64 > min_halves ? K / 64 : min_halves};
+  const cuuint64_t dims[3] = {64, M, K / 64};
   const cuuint64_t strides[2] = {K * 2, 128};
   const cuuint32_t box[3] = {64, T, halves};
   const cuuint32_t estr[3] = {1, 1, 1};
