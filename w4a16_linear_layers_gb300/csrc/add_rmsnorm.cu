@@ -24,8 +24,8 @@
 // What bounds it: HBM at many rows (7 or 8 bytes an element), with instruction
 // issue close behind, which the two-element instructions (f32x2, bf16x2) are
 // for (27 warp instructions for 32 elements); two block-wide reductions and
-// the launch at few.  8192 x 5120: 55.4 us with fp16 codes, 6.06 TB/s, 0.89 of
-// the copy rate (39 instructions took 62.7).  (A ring of rows filled ahead by
+// the launch at few.  8192 x 5120: 55.1 us with fp16 codes, 6.09 TB/s, 0.90 of
+// the copy rate (39 instructions took 62.7); 50.9 with int8 codes, 5.77 TB/s.  (A ring of rows filled ahead by
 // bulk copies was slower, 74 us against 62 then: many small blocks already
 // overlap one row's loads with another's reductions.)
 #include <cuda_bf16.h>

@@ -79,7 +79,8 @@ struct PairPlan {
 
 // A tile size: the time of a K step, of a tile's way out (where its steps take
 // less) and of what is around a pair's tiles, in 10 ns, measured at N from 5120 to
-// 219520.  Parts of a tile that meet in a cluster take 2 us; through the workspace
+// 219520; a step takes 37, 40, 44 and 56 now, and less where few tiles share HBM.
+// Parts of a tile that meet in a cluster take 2 us; through the workspace
 // 5 us and half a one for 64 tokens of each part, of which 1.5 are left where
 // whole tiles follow.
 struct PairSize {
@@ -122,8 +123,8 @@ inline PairPlan plan_tiles(const PairSize& size, int64_t M, int64_t N, int64_t K
     }
   }
   // Few tiles: the pairs of a cluster share one, and meet in shared memory (64 x
-  // 5120 x 5120 11.2 us, through the workspace 15.2; 512 x 5120 x 1024 13.2 and
-  // 17.3; 64 x 2048 x 4096 7.2 and 11.5).
+  // 5120 x 5120 10.9 us, without 12.5; 512 x 5120 x 1024 12.8 and 14.4; 64 x 2048 x
+  // 4096 6.9 and 8.7).
   for (int c = 2; c <= kMaxParts && c * kMinShare <= pl.G; ++c) {
     const int64_t shared = size.step * ((pl.G + c - 1) / c) + 200;
     if (tiles <= room.pairs[c] && shared < last) {
@@ -150,10 +151,11 @@ inline PairPlan plan_pair(int64_t M, int64_t N, int64_t K, const Room& room) {
 
 // Batches that take the streaming kernel: up to 8 tokens always, and more where
 // its blocks of 16 all run at one time and are done first.  A step of their warps
-// takes 0.88 us, mostly latency.  Measured: 16 x 17408 x 1024 7.9 us against 19.3 in
-// pairs, 64 x 5120 x 1024 6.8 and 12.2 (both through the workspace), 16 x 1152 x
-// 8192 4.0 and 6.7; but 128 x 5120 x 1024 9.7 and 8.6, 64 x 17408 x 1024 17.5 and
-// 16.8, 16 x 17408 x 5120 33.6 and 22.7, 16 x 5120 x 10240 23.2 and 20.1.
+// takes 0.88 us, mostly latency.  Measured: 16 x 17408 x 1024 7.9 us against 15.1 in
+// pairs, 64 x 5120 x 1024 6.9 and 7.5, 16 x 1152 x 8192 3.8 and 6.5; but 128 x 5120
+// x 1024 9.7 and 8.3, 16 x 17408 x 5120 33.6 and 21.2, 16 x 5120 x 10240 23.2 and
+// 16.9.  The estimate errs by what steps of few tiles take less: 64 x 17408 x 1024
+// streams in 17.4 us and takes 15.6 in pairs.
 inline bool streams(int64_t M, int64_t N, int64_t K, const Room& room) {
   if (M <= 8) return true;
   const int64_t tiles = stream16_tiles(M, N);

@@ -17,7 +17,7 @@
 // loads themselves paces the stream.  The legacy tensor path does one m16n8k16
 // per 2 cycles and SM (measured), 256 weight bytes x 8 tokens; HBM delivers 256
 // bytes per 11 cycles and SM, so for 8 tokens it has room to spare.  (The int8
-// form, m16n8k32, takes 16 cycles here.)  Measured at 8 x 5120 x 34816: 32.2 us,
+// form, m16n8k32, takes 16 cycles here.)  Measured at 8 x 5120 x 34816: 32.4 us,
 // 5.5 TB/s, 0.81 of the copy rate; 1 x 5120 x 248320: 208 us, 0.90.
 //   * A block's 8 warps share 32 or 64 output channels and interleave the 64-
 //     wide K blocks between them; a cluster of up to 8 blocks splits K further
