@@ -39,7 +39,7 @@ def test_handle_0_is_the_default_stream(make):
     is current, and NULL in the C interface."""
     assert torch.cuda.default_stream().cuda_stream == 0
     side = torch.cuda.Stream()
-    assert stream_of(make(0)) == 0
+    assert stream_of(make(0)) == 0 and stream_of(make(1)) == 0       # 1: cudaStreamLegacy
     with torch.cuda.stream(side):
         assert stream_of(make(0)) == 0
         assert stream_of(torch.cuda.default_stream()) == 0

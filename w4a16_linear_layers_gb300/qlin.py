@@ -309,10 +309,11 @@ def _on(stream, lead, call, *args):
     index = lead.get_device()
     if not isinstance(stream, torch.cuda.Stream):
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        # ExternalStream takes the default stream's handle, 0, for none given, and
-        # makes a stream of its own
-        stream = (torch.cuda.ExternalStream(handle, device=torch.device("cuda", index)) if handle
-                  else torch.cuda.default_stream(index))
+        # The default stream's handle is 0 (or 1, cudaStreamLegacy).  ExternalStream
+        # takes 0 for none given and makes a stream of its own, and 1 for one of
+        # PyTorch's own numbers.
+        stream = (torch.cuda.default_stream(index) if handle in (0, 1)
+                  else torch.cuda.ExternalStream(handle, device=torch.device("cuda", index)))
     if stream.device_index != index:
         raise ValueError(f"stream must be of cuda:{index}, got {stream.device}")
     caller = torch.cuda.current_stream(index)
