@@ -80,6 +80,15 @@ def test_an_extension_for_something_else_is_not_loaded(monkeypatch):
         qlin._calls()
 
 
+def test_a_pytorch_that_is_not_installed(monkeypatch):
+    """One that is only in the path has no metadata."""
+    def none(name):
+        raise qbuild.importlib.metadata.PackageNotFoundError(name)
+    monkeypatch.setattr(qbuild.importlib.metadata, "version", none)
+    import torch
+    assert torch.__version__ in qbuild.calls_stamp()
+
+
 def test_the_extension_loads():
     qbuild.build()
     assert qbuild.calls_built_for() == qbuild.calls_stamp()

@@ -62,7 +62,13 @@ def calls_stamp() -> str | None:
     """What the extension is built for; None where there is no PyTorch."""
     if importlib.util.find_spec("torch") is None:
         return None
-    return f"torch {importlib.metadata.version('torch')}, python {sysconfig.get_config_var('SOABI')}"
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:     # in the path, not installed
+        import torch
+
+        version = torch.__version__
+    return f"torch {version}, python {sysconfig.get_config_var('SOABI')}"
 
 
 def calls_built_for() -> str | None:
