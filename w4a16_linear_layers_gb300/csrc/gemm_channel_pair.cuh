@@ -33,7 +33,7 @@
 //     12-19 drain and write.
 //
 // What bounds it: at thousands of tokens the MMAs under the power limit (8192 x
-// 5120 x 34816 1.69 to 1.81 ms, 1610 to 1730 TF/s); at 64 to a few hundred, HBM and
+// 5120 x 34816 1.58 to 1.81 ms, 1610 to 1850 TF/s); at 64 to a few hundred, HBM and
 // the words and codes on their way from L2 to the SMs, 10 to 12 TB/s (64 x 5120 x
 // 248320 194 us, 6.7 TB/s of HBM; 96 tokens 209, 6.3); with little of K the way out
 // of tensor memory (836 x 256 x 95952 80 us).
