@@ -16,7 +16,10 @@
  *   7. a W8A8 GEMM with one scale per token and one per output channel over
  *      the same GPTQ words,
  *   8. the residual addition fused with RMSNorm and 1, and the logits after
- *      the vocabulary head adjusted by penalties, biases and grammar masks.
+ *      the vocabulary head adjusted by penalties, biases and grammar masks,
+ *   9. what stands between a layer's fused q/k/v linear and its o linear: the
+ *      new tokens' heads normalised, rotated and quantized into a paged INT8
+ *      key/value cache, the cache read back, and attention over it.
  *
  * Format (all calls): GPTQ qweight / qzeros / scales, no g_idx,
  * desc_act = false, symmetric, groups of exactly 128 contiguous K
@@ -489,6 +492,147 @@ qlin_status_t qlin_adjust_logits_f32(const float *logits, int64_t M, int64_t V,
                                      float *out, int32_t *argmax, qlin_stream_t stream);
 
 /*
+ * A paged INT8 key/value cache: one fp32 scale per token, key/value head and
+ * 128-wide group, heads being 128 wide.
+ *
+ * Passages: "Flint-DFlash2-GPTQ-INT8-PTQR" card, serving recipe (INT8 block
+ * KV cache in 128-wide groups) and "Qwen3.8-27B-DFlash2-W4A16-g128-sym-GPTQ"
+ * card, property table (32 query heads and 8 key/value heads of dimension 128,
+ * sliding window 2048, bidirectional within a drafted block).
+ *
+ * The cache holds `pages` pages of `page_size` tokens (a multiple of 16, at
+ * most 65536), each as one block of 4224 bytes for every 16 tokens of a head:
+ *   uint8 [pages, kv_heads, page_size / 16, 4224],  a block being
+ *     bytes    0 .. 2047  K codes: token r's at 128 r, each stored as code + 128
+ *     bytes 2048 .. 4095  V codes, the same
+ *     bytes 4096 .. 4159  K scales fp32 [16]
+ *     bytes 4160 .. 4223  V scales fp32 [16]
+ *   with the four 32-byte quarters of a token's codes permuted: components
+ *   32 j .. 32 j + 31 of token r stand at quarter j ^ (r / 4) (the order in
+ *   which the attention reads shared memory without bank conflicts).
+ * Its base is 128-byte aligned.  qlin_kv_cache_bytes gives its size, 0 for
+ * sizes outside the rules.
+ *
+ * A sequence's tokens are numbered from 0; token j of sequence b is in page
+ * block_table[b, j / page_size], at its place j % page_size.  Arguments that the
+ * calls below share:
+ *   B, T          sequences, and rows of each sequence in the batch: row b T + t
+ *                 belongs to sequence b (B T <= 2^31 - 1)
+ *   block_table   int32 [B, max_pages]; max_pages >= 1, max_pages * page_size
+ *                 <= 2^30.  Entries outside [0, pages) hold no tokens: what is
+ *                 written there is dropped, what is read there is 0 and is not
+ *                 attended to.  Entries past a sequence's length are not read.
+ *   total_len     int32 [B]  tokens of each sequence with its new ones; taken
+ *                 as the nearer end where outside [0, max_pages * page_size]
+ *   new_len       int32 [B] or NULL (T of each): new tokens, the last ones of
+ *                 the sequence, in rows t < new_len[b]; lengths outside
+ *                 [0, min(T, total_len[b])] are taken as the nearer end.  Rows
+ *                 from new_len[b] on are padding: nothing is read from them,
+ *                 and their outputs are left as they were.
+ * Row b T + t is thus token total_len[b] - new_len[b] + t.  int32, uint8 and
+ * fp32 arrays are 4-byte aligned except where stated, all else 16-byte.  Where
+ * B or T is 0 the calls do nothing.
+ */
+size_t qlin_kv_cache_bytes(int64_t pages, int64_t kv_heads, int64_t page_size);
+
+/*
+ * The new tokens' heads out of the fused q/k/v linear: query and key heads
+ * normalised and rotated, keys and values quantized into the cache.
+ *
+ * Passages: the cards above, and the "DFlash2 decoding" recipe page (fused
+ * Q/K norm and rotation).  The code is that of qlin_act_quant_i8 for a row of
+ * 128, but its quotient is decided exactly.
+ *
+ * Each row of qkv holds q_heads query, kv_heads key and kv_heads value heads
+ * of 128.  For a head x of a row, with nothing rounded in between:
+ *   u = gamma * x,  rho = 1 / sqrt(mean x^2 + eps)   (query and key heads, where
+ *   the gamma is given; else u = x, rho = 1),
+ *   y = u rotated: for i < R/2, with c and s of pair i,
+ *       y[i] = u[i] c - u[i + R/2] s,  y[i + R/2] = u[i + R/2] c + u[i] s,
+ *       and y = u from component R on                (query and key heads),
+ *   query:       q = bf16(y * rho),
+ *   key, value:  a = max |y|,  code = the integer nearest to 127 y / a (the
+ *                even one of two),  scale = fp32(a * rho / 127).
+ * q and the scales come from fp32 arithmetic (scales within 2^-20 of their
+ * value), the codes are exact.  A head of zeros gives codes and scale 0.  A key
+ * or value head with a NaN or an infinity, or whose sums leave fp32's range,
+ * gives scale NaN (its codes mean nothing), a query head NaN.  Outside the
+ * contract: heads, other than zero ones, whose mean of x^2 plus eps is below
+ * 2^-100 under a norm, and non-finite gamma, cos or sin.
+ *
+ *   qkv           bf16 [B T, (q_heads + 2 kv_heads) * 128];  q_heads >= 0
+ *   q_gamma, k_gamma  bf16 [128] or NULL each;  eps >= 0, finite
+ *   cos_sin       fp32 [P, R], 16-byte aligned: for each position R/2 cosines,
+ *                 then R/2 sines; R a multiple of 16, at most 128.  NULL with
+ *                 P = R = 0: no rotation.
+ *   positions     int32 [A, B T]: the position of each row along each of A axes
+ *                 (time, height, width, ...), or NULL with A = 0: the token's
+ *                 number.  Positions outside [0, P) are taken as the nearer end.
+ *   axes          uint8 [R/2]: the axis of pair i, values of A and above taken
+ *                 as A - 1.  May be NULL where A <= 1.  A <= 255
+ *   q             bf16 [B T, q_heads * 128]  output; NULL where q_heads is 0.
+ *                 May not overlap qkv.
+ * The rows' places in the cache have to differ; where two rows of one call have
+ * the same one, its bytes are some of the one's and some of the other's.
+ */
+qlin_status_t qlin_kv_write_i8(const uint16_t *qkv, int64_t B, int64_t T, int64_t q_heads,
+                               int64_t kv_heads, const uint16_t *q_gamma, const uint16_t *k_gamma,
+                               float eps, const float *cos_sin, int64_t P, int64_t R,
+                               const int32_t *positions, int64_t A, const uint8_t *axes,
+                               void *cache, int64_t pages, int64_t page_size,
+                               const int32_t *block_table, int64_t max_pages,
+                               const int32_t *total_len, const int32_t *new_len, uint16_t *q,
+                               qlin_stream_t stream);
+
+/*
+ * Keys and values taken out of the cache: bf16(code * scale), the product
+ * rounded to fp32 first.
+ *
+ *   start  int32 [B] or NULL (0): the first token taken, outside
+ *          [0, total_len[b]] the nearer end
+ *   k, v   bf16 [B, L, kv_heads, 128]  outputs: row i is token start[b] + i,
+ *          zeros from the sequence's end on; either may be NULL (not both)
+ */
+qlin_status_t qlin_kv_read_bf16(const void *cache, int64_t pages, int64_t page_size,
+                                int64_t kv_heads, const int32_t *block_table, int64_t B,
+                                int64_t max_pages, const int32_t *total_len, const int32_t *start,
+                                int64_t L, uint16_t *k, uint16_t *v, qlin_stream_t stream);
+
+/*
+ * Attention of the new tokens over the cache (which already holds them): the
+ * producer of the o projection's input.  For query head h of row b T + t, at
+ * token i, with key/value head h / (q_heads / kv_heads):
+ *   x_j = scale * q . K_j,   K_j = code * scale of the cache,
+ *   x_j <- softcap * tanh(x_j / softcap)              where softcap > 0,
+ *   out = bf16( sum_j exp(x_j) V_j / sum_j exp(x_j) )
+ * over the tokens j < total_len[b] that it sees: j <= i if causal, and
+ * |i - j| < window where window > 0.  A row that sees none gives zeros.
+ *
+ * fp32 accumulation; each exp(x_j) times its V scale is rounded to fp16
+ * relative to the row's largest.  Cache bytes at places that no row sees have
+ * no effect, whatever they hold.  Non-finite scales at seen tokens give
+ * non-finite outputs for the rows that see them.  The result does not depend
+ * on timing, but in its last bits on the batch, which decides how sequences
+ * are cut.
+ *
+ *   q        bf16 [B T, q_heads * 128]  (rotated, qlin_kv_write_i8)
+ *   q_heads  a positive multiple of kv_heads, at most 65535
+ *   scale    finite;  softcap >= 0, finite;  window >= 0 (0: none)
+ *   out      bf16 [B T, q_heads * 128]
+ *   workspace / workspace_bytes  at least qlin_paged_attn_workspace_bytes(B, T,
+ *            q_heads, kv_heads) bytes on the current device.  It needs no
+ *            zeroing and holds nothing between calls.  Calls that share a
+ *            workspace must not overlap.
+ */
+size_t qlin_paged_attn_workspace_bytes(int64_t B, int64_t T, int64_t q_heads, int64_t kv_heads);
+qlin_status_t qlin_paged_attn_i8(const uint16_t *q, int64_t B, int64_t T, int64_t q_heads,
+                                 int64_t kv_heads, const void *cache, int64_t pages,
+                                 int64_t page_size, const int32_t *block_table, int64_t max_pages,
+                                 const int32_t *total_len, const int32_t *new_len, float scale,
+                                 float softcap, int64_t window, int causal, uint16_t *out,
+                                 void *workspace, size_t workspace_bytes, qlin_stream_t stream);
+
+/*
  * GPTQ packer (offline step; not on the timed path).
  *
  * Passages: "Flint-DFlash2-GPTQ-INT8-PTQR" card, parameter table (GPTQ
@@ -588,8 +732,10 @@ const char *qlin_status_string(qlin_status_t status);
  * qlin_silu_mul_act_quant_c16, qlin_gemm_w8a8_gs128_c16); the workspace of
  * batches of up to 32 tokens grows by M * K bytes.  Later additions that
  * change no earlier call keep 1.3: qlin_add_rmsnorm_act_quant_{i8,c16},
- * qlin_gemm_w8a8_ch{,_c16} with its workspace size, and
- * qlin_adjust_logits_{bf16,f32}. */
+ * qlin_gemm_w8a8_ch{,_c16} with its workspace size,
+ * qlin_adjust_logits_{bf16,f32}, and the paged cache: qlin_kv_cache_bytes,
+ * qlin_kv_write_i8, qlin_kv_read_bf16 and qlin_paged_attn_i8 with its
+ * workspace size. */
 int qlin_version(void);
 
 #ifdef __cplusplus

@@ -30,49 +30,12 @@
 // overlap one row's loads with another's reductions.)
 #include <cuda_bf16.h>
 
+#include "f32x2.cuh"
 #include "qlin_device.cuh"
 #include "qlin_internal.h"
 
 namespace qlin {
 namespace {
-
-using f32x2 = unsigned long long;   // two fp32 values, the lower-indexed one low
-
-__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
-  f32x2 d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-  return d;
-}
-__device__ __forceinline__ void unpack2(f32x2 v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
-  f32x2 d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-  f32x2 d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-// a - b, rounded once (a subtraction has no form for two elements)
-__device__ __forceinline__ f32x2 sub2(f32x2 a, f32x2 b) { return fma2(b, 0xBF800000BF800000ull, a); }
-
-// bf16x2 word -> its two values in fp32
-__device__ __forceinline__ f32x2 widen2(uint32_t w) {
-  return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-}
-__device__ __forceinline__ uint32_t narrow2(f32x2 v) {
-  float lo, hi;
-  unpack2(v, lo, hi);
-  return bf16x2_rn(lo, hi);
-}
 
 // (s, c) += h * h, c collecting what each addition to s drops (TwoSum, with
 // the exact square inside the multiply-adds)

@@ -1,0 +1,42 @@
+// kv_cache.cuh -- the paged INT8 key/value cache as its kernels see it: the
+// block of 16 tokens, where a code stands in it, and a sequence's new tokens.
+#pragma once
+
+#include <cstdint>
+
+#include "qlin_device.cuh"
+#include "qlin_internal.h"
+
+namespace qlin {
+
+constexpr int kHeadDim = 128;
+constexpr int kVCodes = 2048;    // offsets in a block
+constexpr int kKScales = 4096;
+constexpr int kVScales = 4160;
+
+// Offset, in a token's 128 codes, of component d (its 32-byte quarter moved).
+__device__ __forceinline__ int code_place(int r, int d) { return ((((d >> 5) ^ (r >> 2)) & 3) << 5) + (d & 31); }
+
+// A sequence's tokens in the cache, and how many of them are new.
+struct SeqLen {
+  int len, fresh;
+};
+__device__ __forceinline__ SeqLen seq_len(const CacheArgs& c, int64_t b, int64_t T) {
+  SeqLen s;
+  s.len = min(max(__ldg(c.total_len + b), 0), static_cast<int>(c.max_pages * c.page_size));
+  const int most = static_cast<int>(T < s.len ? T : s.len);
+  s.fresh = c.new_len == nullptr ? most : min(max(__ldg(c.new_len + b), 0), most);
+  return s;
+}
+
+// Block of 16 that holds tokens 16 n .. 16 n + 15 of sequence b, head h;
+// nullptr where its page is none.
+__device__ __forceinline__ uint8_t* cache_block(const CacheArgs& c, int64_t b, int h, int n) {
+  const int per_page = static_cast<int>(c.page_size) >> 4;
+  const int in_table = n / per_page;
+  const int page = __ldg(c.block_table + b * c.max_pages + in_table);
+  if (page < 0 || page >= c.pages) return nullptr;
+  return c.cache + ((page * c.kv_heads + h) * per_page + (n - in_table * per_page)) * static_cast<int64_t>(kCacheBlock);
+}
+
+}  // namespace qlin

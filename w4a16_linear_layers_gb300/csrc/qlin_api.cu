@@ -253,6 +253,92 @@ qlin_status_t run_silu_mul_quant(const uint16_t* gate_up, int64_t M, int64_t I, 
       launch_silu_mul_quant(gate_up, M, I, q, c16, s_a, y, d->err_word, d->sm_count, stream));
 }
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+constexpr int64_t kMaxPageSize = 65536;
+constexpr int64_t kMaxHeads = 65535;
+constexpr int64_t kMaxTokens = 1LL << 30;   // of a sequence
+
+bool cache_shape(int64_t pages, int64_t kv_heads, int64_t page_size) {
+  return pages >= 1 && pages <= kMaxDim && kv_heads >= 1 && kv_heads <= kMaxHeads && page_size >= 16 &&
+         page_size <= kMaxPageSize && page_size % 16 == 0;
+}
+
+bool batch_shape(int64_t B, int64_t T) { return B >= 0 && T >= 0 && B <= kMaxDim && T <= kMaxDim && B * T <= kMaxDim; }
+
+// NULL pointers, shapes and alignment of what the calls on the cache share.
+// An empty batch needs no pointers sized by it.
+qlin_status_t check_cache(const CacheArgs& c, bool rows) {
+  if (rows && (c.cache == nullptr || c.block_table == nullptr || c.total_len == nullptr)) return QLIN_ERR_NULL;
+  if (!cache_shape(c.pages, c.kv_heads, c.page_size) || c.max_pages < 1 || c.max_pages > kMaxTokens / c.page_size)
+    return QLIN_ERR_SHAPE;
+  if ((reinterpret_cast<uintptr_t>(c.cache) & 127u) != 0 || !aligned4(c.block_table) || !aligned4(c.total_len) ||
+      !aligned4(c.new_len))
+    return QLIN_ERR_ALIGN;
+  return QLIN_OK;
+}
+
+qlin_status_t run_kv_write(const KvWriteArgs& a, cudaStream_t stream) {
+  const bool rows = a.c.B != 0 && a.T != 0;
+  if ((rows && (a.qkv == nullptr || (a.q_heads > 0 && a.q == nullptr))) ||
+      (a.R != 0 && a.cos_sin == nullptr) || (a.R == 0 && a.cos_sin != nullptr) ||
+      (rows && a.A != 0 && a.positions == nullptr) || (a.A > 1 && a.R != 0 && a.axes == nullptr))
+    return QLIN_ERR_NULL;
+  if (!batch_shape(a.c.B, a.T) || a.q_heads < 0 || a.q_heads > kMaxHeads || !(a.eps >= 0.0f) || !std::isfinite(a.eps) ||
+      a.R < 0 || a.R > 128 || a.R % 16 != 0 || a.P < 0 || a.P > kMaxDim || (a.R != 0 && a.P == 0) || a.A < 0 || a.A > 255)
+    return QLIN_ERR_SHAPE;
+  const qlin_status_t cache = check_cache(a.c, rows);
+  if (cache != QLIN_OK) return cache;
+  if (!aligned16(a.qkv) || !aligned16(a.q) || !aligned16(a.q_gamma) || !aligned16(a.k_gamma) ||
+      !aligned16(a.cos_sin) || !aligned4(a.positions) || !aligned4(a.axes))
+    return QLIN_ERR_ALIGN;
+  const DeviceInfo* d = nullptr;
+  const qlin_status_t st = device_or_error(&d);
+  if (st != QLIN_OK) return st;
+  if (!rows) return QLIN_OK;
+  return from_cuda(launch_kv_write(a, d->sm_count, stream));
+}
+
+qlin_status_t run_kv_read(const CacheArgs& c, const int32_t* start, int64_t L, uint16_t* k, uint16_t* v,
+                          cudaStream_t stream) {
+  const bool rows = c.B != 0 && L != 0;
+  if (rows && k == nullptr && v == nullptr) return QLIN_ERR_NULL;
+  if (c.B < 0 || c.B > kMaxDim || L < 0 || L > kMaxTokens) return QLIN_ERR_SHAPE;
+  const qlin_status_t cache = check_cache(c, rows);
+  if (cache != QLIN_OK) return cache;
+  if (!aligned4(start) || !aligned16(k) || !aligned16(v)) return QLIN_ERR_ALIGN;
+  const DeviceInfo* d = nullptr;
+  const qlin_status_t st = device_or_error(&d);
+  if (st != QLIN_OK) return st;
+  if (!rows) return QLIN_OK;
+  return from_cuda(launch_kv_read(c, start, L, k, v, stream));
+}
+
+qlin_status_t attn_shape(int64_t B, int64_t T, int64_t q_heads, int64_t kv_heads) {
+  if (!batch_shape(B, T) || kv_heads < 1 || kv_heads > kMaxHeads || q_heads < 1 || q_heads > kMaxHeads ||
+      q_heads % kv_heads != 0)
+    return QLIN_ERR_SHAPE;
+  return QLIN_OK;
+}
+
+qlin_status_t run_paged_attn(const PagedAttnArgs& a, size_t workspace_bytes, cudaStream_t stream) {
+  const bool rows = a.c.B != 0 && a.T != 0;
+  if (rows && (a.q == nullptr || a.out == nullptr)) return QLIN_ERR_NULL;
+  qlin_status_t st = attn_shape(a.c.B, a.T, a.q_heads, a.c.kv_heads);
+  if (st != QLIN_OK) return st;
+  if (!std::isfinite(a.scale) || !(a.softcap >= 0.0f) || !std::isfinite(a.softcap) || a.window < 0) return QLIN_ERR_SHAPE;
+  st = check_cache(a.c, rows);
+  if (st != QLIN_OK) return st;
+  if (!aligned16(a.q) || !aligned16(a.out) || !aligned16(a.workspace)) return QLIN_ERR_ALIGN;
+  const DeviceInfo* d = nullptr;
+  st = device_or_error(&d);
+  if (st != QLIN_OK) return st;
+  if (!rows) return QLIN_OK;
+  const size_t need = paged_attn_workspace_bytes(a.c.B, a.T, a.q_heads, a.c.kv_heads, d->sm_count);
+  if (need != 0 && (a.workspace == nullptr || workspace_bytes < need)) return QLIN_ERR_WORKSPACE;
+  return from_cuda(launch_paged_attn(a, d->err_word, d->sm_count, stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -480,6 +566,51 @@ qlin_status_t qlin_adjust_logits_f32(const float* logits, int64_t M, int64_t V,
   return run_adjust_logits(LogitArgs{logits, true, M, V, tokens, L, prompt_len, total_len, repetition,
                                      presence, frequency, bias_ids, bias, B, allowed, out, argmax},
                            reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t qlin_kv_cache_bytes(int64_t pages, int64_t kv_heads, int64_t page_size) {
+  if (!cache_shape(pages, kv_heads, page_size)) return 0;
+  // in 64 bits: at most 2^31 * 2^16 * 2^12 * 2^13 would not fit, such a cache does not either
+  const unsigned __int128 n = static_cast<unsigned __int128>(pages) * kv_heads * (page_size / 16) * kCacheBlock;
+  return n > static_cast<unsigned __int128>(INT64_MAX) ? 0 : static_cast<size_t>(n);
+}
+
+qlin_status_t qlin_kv_write_i8(const uint16_t* qkv, int64_t B, int64_t T, int64_t q_heads, int64_t kv_heads,
+                               const uint16_t* q_gamma, const uint16_t* k_gamma, float eps, const float* cos_sin,
+                               int64_t P, int64_t R, const int32_t* positions, int64_t A, const uint8_t* axes,
+                               void* cache, int64_t pages, int64_t page_size, const int32_t* block_table,
+                               int64_t max_pages, const int32_t* total_len, const int32_t* new_len, uint16_t* q,
+                               qlin_stream_t stream) {
+  return run_kv_write(KvWriteArgs{CacheArgs{static_cast<uint8_t*>(cache), pages, kv_heads, page_size, block_table, B,
+                                            max_pages, total_len, new_len},
+                                  qkv, T, q_heads, q_gamma, k_gamma, eps, cos_sin, P, R, positions, A, axes, q},
+                      reinterpret_cast<cudaStream_t>(stream));
+}
+
+qlin_status_t qlin_kv_read_bf16(const void* cache, int64_t pages, int64_t page_size, int64_t kv_heads,
+                                const int32_t* block_table, int64_t B, int64_t max_pages, const int32_t* total_len,
+                                const int32_t* start, int64_t L, uint16_t* k, uint16_t* v, qlin_stream_t stream) {
+  return run_kv_read(CacheArgs{static_cast<uint8_t*>(const_cast<void*>(cache)), pages, kv_heads, page_size, block_table,
+                               B, max_pages, total_len, nullptr},
+                     start, L, k, v, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t qlin_paged_attn_workspace_bytes(int64_t B, int64_t T, int64_t q_heads, int64_t kv_heads) {
+  if (attn_shape(B, T, q_heads, kv_heads) != QLIN_OK || B == 0 || T == 0) return 0;
+  const DeviceInfo* d = current_device();
+  if (d == nullptr || !d->supported) return 0;
+  return paged_attn_workspace_bytes(B, T, q_heads, kv_heads, d->sm_count);
+}
+
+qlin_status_t qlin_paged_attn_i8(const uint16_t* q, int64_t B, int64_t T, int64_t q_heads, int64_t kv_heads,
+                                 const void* cache, int64_t pages, int64_t page_size, const int32_t* block_table,
+                                 int64_t max_pages, const int32_t* total_len, const int32_t* new_len, float scale,
+                                 float softcap, int64_t window, int causal, uint16_t* out, void* workspace,
+                                 size_t workspace_bytes, qlin_stream_t stream) {
+  return run_paged_attn(PagedAttnArgs{CacheArgs{static_cast<uint8_t*>(const_cast<void*>(cache)), pages, kv_heads, page_size,
+                                                block_table, B, max_pages, total_len, new_len},
+                                      q, T, q_heads, scale, softcap, window, causal != 0, out, workspace},
+                        workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t qlin_workspace_bytes(int64_t M, int64_t N, int64_t K) {

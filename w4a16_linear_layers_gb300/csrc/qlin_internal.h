@@ -86,6 +86,50 @@ struct LogitArgs {
 };
 cudaError_t launch_adjust_logits(const LogitArgs& a, int* err, int sm_count, cudaStream_t stream);
 
+// The paged INT8 key/value cache and where its sequences' tokens are.
+constexpr int kCacheBlock = 4224;   // bytes of 16 tokens of a head
+struct CacheArgs {
+  uint8_t* cache;
+  int64_t pages, kv_heads, page_size;
+  const int32_t* block_table;   // [B, max_pages]
+  int64_t B, max_pages;
+  const int32_t* total_len;     // [B]
+  const int32_t* new_len;       // [B] or nullptr
+};
+
+struct KvWriteArgs {
+  CacheArgs c;
+  const uint16_t* qkv;          // [B T, q_heads + 2 kv_heads, 128]
+  int64_t T, q_heads;
+  const uint16_t* q_gamma;      // [128] or nullptr
+  const uint16_t* k_gamma;
+  float eps;
+  const float* cos_sin;         // [P, R] or nullptr
+  int64_t P, R;
+  const int32_t* positions;     // [A, B T] or nullptr
+  int64_t A;
+  const uint8_t* axes;          // [R / 2] or nullptr
+  uint16_t* q;                  // [B T, q_heads, 128]
+};
+cudaError_t launch_kv_write(const KvWriteArgs& a, int sm_count, cudaStream_t stream);
+
+// k, v: bf16 [B, L, kv_heads, 128], either may be nullptr
+cudaError_t launch_kv_read(const CacheArgs& c, const int32_t* start, int64_t L, uint16_t* k, uint16_t* v,
+                           cudaStream_t stream);
+
+struct PagedAttnArgs {
+  CacheArgs c;
+  const uint16_t* q;            // [B T, q_heads, 128]
+  int64_t T, q_heads;
+  float scale, softcap;
+  int64_t window;
+  bool causal;
+  uint16_t* out;                // as q
+  void* workspace;
+};
+size_t paged_attn_workspace_bytes(int64_t B, int64_t T, int64_t q_heads, int64_t kv_heads, int sm_count);
+cudaError_t launch_paged_attn(const PagedAttnArgs& a, int* err, int sm_count, cudaStream_t stream);
+
 cudaError_t launch_pack(const int8_t* q, int64_t K, int64_t N, int bits, int32_t* qweight,
                         int32_t* qzeros, int* err, cudaStream_t stream);
 

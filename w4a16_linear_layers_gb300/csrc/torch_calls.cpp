@@ -31,6 +31,10 @@ decltype(&qlin_gemm_w8a8_ch_c16) gemm_c16;
 decltype(&qlin_gemm_w8a8_ch_workspace_bytes) gemm_workspace;
 decltype(&qlin_adjust_logits_bf16) logits_bf16;
 decltype(&qlin_adjust_logits_f32) logits_f32;
+decltype(&qlin_kv_write_i8) write_i8;
+decltype(&qlin_kv_read_bf16) read_bf16;
+decltype(&qlin_paged_attn_i8) attn_i8;
+decltype(&qlin_paged_attn_workspace_bytes) attn_workspace;
 PyObject* raise_status;   // raises the error of a status
 
 using at::ScalarType;
@@ -68,11 +72,13 @@ void refuse(PyObject* o, const char* name, ScalarType type, at::IntArrayRef shap
   } else if (t.sizes() != shape) {
     PyObject* got = PyObject_GetAttrString(o, "shape");
     if (got == nullptr) return;
+    auto n = [&](size_t i) { return static_cast<long long>(shape[i]); };
     if (shape.size() == 1)
-      PyErr_Format(PyExc_ValueError, "%s must have shape [%lld], got %S", name, static_cast<long long>(shape[0]), got);
+      PyErr_Format(PyExc_ValueError, "%s must have shape [%lld], got %S", name, n(0), got);
+    else if (shape.size() == 2)
+      PyErr_Format(PyExc_ValueError, "%s must have shape [%lld, %lld], got %S", name, n(0), n(1), got);
     else
-      PyErr_Format(PyExc_ValueError, "%s must have shape [%lld, %lld], got %S", name, static_cast<long long>(shape[0]),
-                   static_cast<long long>(shape[1]), got);
+      PyErr_Format(PyExc_ValueError, "%s must have shape [%lld, %lld, %lld, %lld], got %S", name, n(0), n(1), n(2), n(3), got);
     Py_DECREF(got);
   } else if (!t.is_cuda() || t.get_device() != index) {
     PyErr_Format(PyExc_ValueError, "%s must be on cuda:%d, got %s", name, index, t.device().str().c_str());
@@ -335,11 +341,215 @@ PyObject* adjust_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+constexpr int64_t kCacheBlock = 4224;   // bytes of 16 tokens of a head
+
+// What the calls on a paged cache share: the cache and its sequences.
+struct Cache {
+  void* data;
+  int64_t pages, kv_heads, page_size, B, max_pages;
+  const int32_t *table, *total, *fresh;
+};
+
+// false with an error raised
+bool cache_of(Cache& c, PyObject* cache, PyObject* table, PyObject* total, PyObject* fresh, int index) {
+  const Tensor* t = lead(cache, "cache", {ScalarType::Byte}, 4);
+  if (t == nullptr) return false;
+  c.pages = t->size(0);
+  c.kv_heads = t->size(1);
+  c.page_size = 16 * t->size(2);
+  if (tensor(cache, "cache", ScalarType::Byte, {c.pages, c.kv_heads, t->size(2), kCacheBlock}, index) == nullptr) return false;
+  c.data = out<void>(*t);
+  const Tensor* pages = lead(table, "block_table", {ScalarType::Int}, 2);
+  if (pages == nullptr || tensor(table, "block_table", ScalarType::Int, pages->sizes(), index) == nullptr) return false;
+  c.B = pages->size(0);
+  c.max_pages = pages->size(1);
+  c.table = in<int32_t>(*pages);
+  const Tensor* n = tensor(total, "total_len", ScalarType::Int, {c.B}, index);
+  if (n == nullptr) return false;
+  c.total = in<int32_t>(*n);
+  c.fresh = nullptr;
+  if (!is_none(fresh)) {
+    n = tensor(fresh, "new_len", ScalarType::Int, {c.B}, index);
+    if (n == nullptr) return false;
+    c.fresh = in<int32_t>(*n);
+  }
+  return true;
+}
+
+bool whole(PyObject* o, int64_t& to) {
+  to = PyLong_AsLongLong(o);
+  return to != -1 || !PyErr_Occurred();
+}
+
+bool real(PyObject* o, float& to) {
+  const double d = PyFloat_AsDouble(o);
+  to = static_cast<float>(d);
+  return d != -1.0 || !PyErr_Occurred();
+}
+
+// Rows of each sequence: M / B.
+bool rows_of(int64_t M, int64_t B, const char* name, int64_t& T) {
+  T = B == 0 ? 0 : M / B;
+  if (M == B * T) return true;
+  PyErr_Format(PyExc_ValueError, "%s must have a multiple of %lld rows, got %lld", name, static_cast<long long>(B),
+               static_cast<long long>(M));
+  return false;
+}
+
+// (qkv, cache, block_table, total_len, q_heads, new_len, q_gamma, k_gamma, eps, cos_sin, positions, axes, q) -> q
+PyObject* kv_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!count(n, 13)) return nullptr;
+  const Tensor* x = lead(a[0], "qkv", {ScalarType::BFloat16}, 2);
+  if (x == nullptr) return nullptr;
+  const int64_t M = x->size(0);
+  const int index = x->get_device();
+  Cache c;
+  int64_t T, q_heads, P = 0, R = 0, A = 0;
+  float eps;
+  if (!cache_of(c, a[1], a[2], a[3], a[5], index) || !rows_of(M, c.B, "qkv", T) || !whole(a[4], q_heads) || !real(a[8], eps))
+    return nullptr;
+  if (q_heads < 0 || x->size(1) != (q_heads + 2 * c.kv_heads) * 128) {
+    PyErr_Format(PyExc_ValueError, "qkv must have (q_heads + 2 * %lld) * 128 columns, got %lld", static_cast<long long>(c.kv_heads),
+                 static_cast<long long>(x->size(1)));
+    return nullptr;
+  }
+  const Tensor *q_gamma = nullptr, *k_gamma = nullptr, *table = nullptr, *positions = nullptr, *axes = nullptr;
+  if (!is_none(a[6]) && (q_gamma = tensor(a[6], "q_gamma", ScalarType::BFloat16, {128}, index)) == nullptr) return nullptr;
+  if (!is_none(a[7]) && (k_gamma = tensor(a[7], "k_gamma", ScalarType::BFloat16, {128}, index)) == nullptr) return nullptr;
+  if (!is_none(a[9])) {
+    table = lead(a[9], "cos_sin", {ScalarType::Float}, 2);
+    if (table == nullptr || tensor(a[9], "cos_sin", ScalarType::Float, table->sizes(), index) == nullptr) return nullptr;
+    P = table->size(0);
+    R = table->size(1);
+    if (P == 0 || R == 0) {
+      PyErr_SetString(PyExc_ValueError, "cos_sin must not be empty");
+      return nullptr;
+    }
+  } else if (!is_none(a[10]) || !is_none(a[11])) {
+    PyErr_SetString(PyExc_ValueError, "positions and axes need cos_sin");
+    return nullptr;
+  }
+  if (!is_none(a[10])) {
+    positions = lead(a[10], "positions", {ScalarType::Int}, 2);
+    if (positions == nullptr) return nullptr;
+    A = positions->size(0);
+    if (A == 0) {
+      PyErr_SetString(PyExc_ValueError, "positions must have an axis");
+      return nullptr;
+    }
+    if (tensor(a[10], "positions", ScalarType::Int, {A, M}, index) == nullptr) return nullptr;
+  }
+  if (!is_none(a[11])) {
+    axes = tensor(a[11], "axes", ScalarType::Byte, {R / 2}, index);
+    if (axes == nullptr) return nullptr;
+  } else if (A > 1) {
+    PyErr_SetString(PyExc_ValueError, "positions of several axes need axes");
+    return nullptr;
+  }
+  Tensor q;
+  if (!output(q, a[12], "q", ScalarType::BFloat16, {M, q_heads * 128}, *x)) return nullptr;
+  const c10::cuda::CUDAGuard guard(x->device());
+  const qlin_status_t status = call(
+      write_i8, in<uint16_t>(*x), c.B, T, q_heads, c.kv_heads, q_gamma == nullptr ? nullptr : in<uint16_t>(*q_gamma),
+      k_gamma == nullptr ? nullptr : in<uint16_t>(*k_gamma), eps, table == nullptr ? nullptr : in<float>(*table), P, R,
+      positions == nullptr ? nullptr : in<int32_t>(*positions), A, axes == nullptr ? nullptr : in<uint8_t>(*axes), c.data,
+      c.pages, c.page_size, c.table, c.max_pages, c.total, c.fresh, q_heads == 0 ? nullptr : out<uint16_t>(q), stream_of(*x));
+  if (!done(status)) return nullptr;
+  return THPVariable_Wrap(q);
+  END_HANDLE_TH_ERRORS
+}
+
+// (cache, block_table, total_len, length, start, k, v) -> (k, v)
+PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!count(n, 7)) return nullptr;
+  const Tensor* cache = lead(a[0], "cache", {ScalarType::Byte}, 4);
+  if (cache == nullptr) return nullptr;
+  const int index = cache->get_device();
+  Cache c;
+  int64_t L;
+  if (!cache_of(c, a[0], a[1], a[2], Py_None, index) || !whole(a[3], L)) return nullptr;
+  if (L < 0) {
+    PyErr_SetString(PyExc_ValueError, "length must not be negative");
+    return nullptr;
+  }
+  const Tensor* start = nullptr;
+  if (!is_none(a[4]) && (start = tensor(a[4], "start", ScalarType::Int, {c.B}, index)) == nullptr) return nullptr;
+  Tensor k, v;
+  if (!output(k, a[5], "k", ScalarType::BFloat16, {c.B, L, c.kv_heads, 128}, *cache) ||
+      !output(v, a[6], "v", ScalarType::BFloat16, {c.B, L, c.kv_heads, 128}, *cache))
+    return nullptr;
+  const c10::cuda::CUDAGuard guard(cache->device());
+  const qlin_status_t status =
+      call(read_bf16, static_cast<const void*>(c.data), c.pages, c.page_size, c.kv_heads, c.table, c.B, c.max_pages, c.total,
+           start == nullptr ? nullptr : in<int32_t>(*start), L, out<uint16_t>(k), out<uint16_t>(v), stream_of(*cache));
+  if (!done(status)) return nullptr;
+  PyObject* result = PyTuple_New(2);
+  if (result == nullptr) return nullptr;
+  const Tensor* const parts[2] = {&k, &v};
+  for (int i = 0; i < 2; ++i) {
+    PyObject* const part = THPVariable_Wrap(*parts[i]);
+    if (part == nullptr) {
+      Py_DECREF(result);
+      return nullptr;
+    }
+    PyTuple_SET_ITEM(result, i, part);
+  }
+  return result;
+  END_HANDLE_TH_ERRORS
+}
+
+// (q, cache, block_table, total_len, new_len, scale, softcap, window, causal, out, workspace) -> out
+PyObject* paged_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!count(n, 11)) return nullptr;
+  const Tensor* q = lead(a[0], "q", {ScalarType::BFloat16}, 2);
+  if (q == nullptr) return nullptr;
+  const int64_t M = q->size(0), width = q->size(1);
+  const int index = q->get_device();
+  Cache c;
+  int64_t T, window;
+  float scale = 0.08838834764831845f, softcap;   // 1 / sqrt(128)
+  if (!cache_of(c, a[1], a[2], a[3], a[4], index) || !rows_of(M, c.B, "q", T) || (!is_none(a[5]) && !real(a[5], scale)) ||
+      !real(a[6], softcap) || !whole(a[7], window))
+    return nullptr;
+  const int causal = PyObject_IsTrue(a[8]);
+  if (causal < 0) return nullptr;
+  if (width == 0 || c.kv_heads == 0 || width % (128 * c.kv_heads) != 0) {
+    PyErr_Format(PyExc_ValueError, "q must have a multiple of %lld * 128 columns, got %lld", static_cast<long long>(c.kv_heads),
+                 static_cast<long long>(width));
+    return nullptr;
+  }
+  const int64_t q_heads = width / 128;
+  Tensor to, workspace;
+  if (!output(to, a[9], "out", ScalarType::BFloat16, {M, width}, *q)) return nullptr;
+  const c10::cuda::CUDAGuard guard(q->device());
+  if (!is_none(a[10])) {
+    const Tensor* given = lead(a[10], "workspace", {ScalarType::Byte}, 1);
+    if (given == nullptr || tensor(a[10], "workspace", ScalarType::Byte, given->sizes(), index) == nullptr) return nullptr;
+    workspace = *given;
+  } else {
+    // its own for every call: calls on several streams, or replayed graphs, do
+    // not meet in it
+    const int64_t bytes = static_cast<int64_t>(attn_workspace(c.B, T, q_heads, c.kv_heads));
+    if (bytes > 0) workspace = fresh({bytes}, ScalarType::Byte, *q);
+  }
+  const qlin_status_t status =
+      call(attn_i8, in<uint16_t>(*q), c.B, T, q_heads, c.kv_heads, static_cast<const void*>(c.data), c.pages, c.page_size,
+           c.table, c.max_pages, c.total, c.fresh, scale, softcap, window, causal, out<uint16_t>(to),
+           workspace.defined() ? out<void>(workspace) : nullptr,
+           workspace.defined() ? static_cast<size_t>(workspace.size(0)) : size_t{0}, stream_of(*q));
+  if (!done(status)) return nullptr;
+  return THPVariable_Wrap(to);
+  END_HANDLE_TH_ERRORS
+}
+
 // (raise_status, addresses of the entry points in the order below)
 PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!count(n, 8)) return nullptr;
-  void* at[7];
-  for (int i = 0; i < 7; ++i) {
+  if (!count(n, 12)) return nullptr;
+  void* at[11];
+  for (int i = 0; i < 11; ++i) {
     at[i] = PyLong_AsVoidPtr(a[1 + i]);
     if (at[i] == nullptr) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "a null address");
@@ -353,6 +563,10 @@ PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
   gemm_workspace = reinterpret_cast<decltype(gemm_workspace)>(at[4]);
   logits_bf16 = reinterpret_cast<decltype(logits_bf16)>(at[5]);
   logits_f32 = reinterpret_cast<decltype(logits_f32)>(at[6]);
+  write_i8 = reinterpret_cast<decltype(write_i8)>(at[7]);
+  read_bf16 = reinterpret_cast<decltype(read_bf16)>(at[8]);
+  attn_i8 = reinterpret_cast<decltype(attn_i8)>(at[9]);
+  attn_workspace = reinterpret_cast<decltype(attn_workspace)>(at[10]);
   Py_INCREF(a[0]);
   raise_status = a[0];
   Py_RETURN_NONE;
@@ -366,6 +580,9 @@ PyMethodDef methods[] = {{"setup", fast(setup), METH_FASTCALL, nullptr},
                          {"add_rmsnorm", fast(add_rmsnorm), METH_FASTCALL, nullptr},
                          {"gemm_ch", fast(gemm_ch), METH_FASTCALL, nullptr},
                          {"adjust_logits", fast(adjust_logits), METH_FASTCALL, nullptr},
+                         {"kv_write", fast(kv_write), METH_FASTCALL, nullptr},
+                         {"kv_read", fast(kv_read), METH_FASTCALL, nullptr},
+                         {"paged_attn", fast(paged_attn), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "qlin_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -58,6 +58,11 @@ EXPORTS = (
     "qlin_gemm_w4a16_g128_argmax",
     "qlin_adjust_logits_bf16",
     "qlin_adjust_logits_f32",
+    "qlin_kv_cache_bytes",
+    "qlin_kv_write_i8",
+    "qlin_kv_read_bf16",
+    "qlin_paged_attn_i8",
+    "qlin_paged_attn_workspace_bytes",
     "qlin_pack_gptq",
     "qlin_ingest_nk",
     "qlin_workspace_bytes",
@@ -110,6 +115,13 @@ def load():
             "qlin_gemm_w8a8_ch_workspace_bytes": ([I64, I64, I64, I], SZ),
             "qlin_adjust_logits_bf16": ([P, I64, I64, P, I64, P, P, P, P, P, P, P, I64, P, P, P, P], I),
             "qlin_adjust_logits_f32": ([P, I64, I64, P, I64, P, P, P, P, P, P, P, I64, P, P, P, P], I),
+            "qlin_kv_cache_bytes": ([I64, I64, I64], SZ),
+            "qlin_kv_write_i8": ([P, I64, I64, I64, I64, P, P, ctypes.c_float, P, I64, I64, P, I64, P, P, I64, I64, P,
+                                  I64, P, P, P, P], I),
+            "qlin_kv_read_bf16": ([P, I64, I64, I64, P, I64, I64, P, P, I64, P, P, P], I),
+            "qlin_paged_attn_i8": ([P, I64, I64, I64, I64, P, I64, I64, P, I64, P, P, ctypes.c_float, ctypes.c_float,
+                                    I64, I, P, P, SZ, P], I),
+            "qlin_paged_attn_workspace_bytes": ([I64, I64, I64, I64], SZ),
             "qlin_gemm_w8a8_gs128": ([P, P, P, P, I64, I64, I64, P, P, SZ, P], I),
             "qlin_gemm_w8a8_gs128_c16": ([P, P, P, P, I64, I64, I64, P, P, SZ, P], I),
             "qlin_gemm_w8a8_gs128_noalloc": ([P, P, P, P, I64, I64, I64, P, P], I),
@@ -290,7 +302,8 @@ def _calls():
             loader.exec_module(module)
             names = ("qlin_add_rmsnorm_act_quant_i8", "qlin_add_rmsnorm_act_quant_c16", "qlin_gemm_w8a8_ch",
                      "qlin_gemm_w8a8_ch_c16", "qlin_gemm_w8a8_ch_workspace_bytes", "qlin_adjust_logits_bf16",
-                     "qlin_adjust_logits_f32")
+                     "qlin_adjust_logits_f32", "qlin_kv_write_i8", "qlin_kv_read_bf16", "qlin_paged_attn_i8",
+                     "qlin_paged_attn_workspace_bytes")
             module.setup(_check, *(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names))
             _torch_calls = module
     return _torch_calls
@@ -407,6 +420,75 @@ def adjust_logits_argmax(logits: torch.Tensor, tokens=None, prompt_len=None, tot
                    frequency, bias_ids, bias, allowed, out, argmax)
     return call(True, logits, tokens, prompt_len, total_len, repetition, presence, frequency, bias_ids, bias,
                 allowed, out, argmax)
+
+
+def kv_cache_bytes(pages: int, kv_heads: int, page_size: int) -> int:
+    """Bytes of a paged INT8 key/value cache; 0 for sizes outside the rules."""
+    return int(load().qlin_kv_cache_bytes(int(pages), int(kv_heads), int(page_size)))
+
+
+def kv_cache(pages: int, kv_heads: int, page_size: int, device=None) -> torch.Tensor:
+    """An empty paged INT8 key/value cache: uint8 [pages, kv_heads, page_size / 16, 4224]
+    in the layout of include/qlin.h, page_size a multiple of 16."""
+    if kv_cache_bytes(pages, kv_heads, page_size) == 0:
+        raise ValueError("pages and kv_heads must be positive, page_size a multiple of 16 up to 65536")
+    return torch.zeros((pages, kv_heads, page_size // 16, 4224), dtype=torch.uint8,
+                       device=device if device is not None else "cuda")
+
+
+def kv_write_i8(qkv: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, total_len: torch.Tensor,
+                q_heads: int, new_len=None, q_gamma=None, k_gamma=None, eps: float = 1e-6, cos_sin=None,
+                positions=None, axes=None, q=None, stream=None) -> torch.Tensor:
+    """The new tokens' heads out of the fused q/k/v linear's output qkv bf16
+    [B*T, (q_heads + 2 * kv_heads) * 128]: keys and values quantized into the
+    cache (kv_cache), queries -> q bf16 [B*T, q_heads * 128].
+
+    Row b*T + t is token total_len[b] - new_len[b] + t of sequence b (total_len
+    int32 [B] counts the new tokens; new_len int32 [B], default T; rows from
+    new_len[b] on are padding and left as they were), on page block_table[b,
+    token / page_size] (int32 [B, max_pages]).  q_gamma and k_gamma bf16 [128]:
+    RMSNorm of each query and key head.  cos_sin fp32 [P, R], R/2 cosines and R/2
+    sines a position: rotation of the first R components, at the token's number
+    or at positions int32 [A, B*T], pair i's along axis axes[i] (uint8 [R/2])."""
+    call = (_torch_calls or _calls()).kv_write
+    if stream is not None:
+        return _on(stream, qkv, call, qkv, cache, block_table, total_len, q_heads, new_len, q_gamma, k_gamma, eps,
+                   cos_sin, positions, axes, q)
+    return call(qkv, cache, block_table, total_len, q_heads, new_len, q_gamma, k_gamma, eps, cos_sin, positions, axes, q)
+
+
+def kv_read_bf16(cache: torch.Tensor, block_table: torch.Tensor, total_len: torch.Tensor, length: int,
+                 start=None, k=None, v=None, stream=None):
+    """Tokens start[b] .. start[b] + length - 1 (start int32 [B], default 0) of
+    each sequence out of the cache -> (k, v) bf16 [B, length, kv_heads, 128],
+    zeros past total_len[b]."""
+    call = (_torch_calls or _calls()).kv_read
+    if stream is not None:
+        return _on(stream, cache, call, cache, block_table, total_len, length, start, k, v)
+    return call(cache, block_table, total_len, length, start, k, v)
+
+
+def paged_attn_workspace_bytes(B: int, T: int, q_heads: int, kv_heads: int) -> int:
+    return int(load().qlin_paged_attn_workspace_bytes(int(B), int(T), int(q_heads), int(kv_heads)))
+
+
+def paged_attn_i8(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, total_len: torch.Tensor,
+                  new_len=None, scale=None, softcap: float = 0.0, window: int = 0, causal: bool = True, out=None,
+                  workspace=None, stream=None) -> torch.Tensor:
+    """Attention of the new tokens' queries q bf16 [B*T, q_heads * 128] over the
+    cache, which holds their own keys and values already (kv_write_i8; rows and
+    lengths as there) -> out bf16 [B*T, q_heads * 128].
+
+    scale: default 1 / sqrt(128).  softcap > 0: scores capped to softcap *
+    tanh(score / softcap).  A token sees those up to itself (causal) or all,
+    with window > 0 those less than window away.  workspace: a uint8 tensor of
+    paged_attn_workspace_bytes(B, T, q_heads, kv_heads) bytes; allocated for the
+    call when not given."""
+    call = (_torch_calls or _calls()).paged_attn
+    if stream is not None:
+        return _on(stream, q, call, q, cache, block_table, total_len, new_len, scale, softcap, window, causal, out,
+                   workspace)
+    return call(q, cache, block_table, total_len, new_len, scale, softcap, window, causal, out, workspace)
 
 
 def workspace_bytes(M: int, N: int, K: int) -> int:
