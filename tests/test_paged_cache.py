@@ -21,11 +21,11 @@ Tolerances, from the definitions of include/qlin.h:
     its value; the weight's rounding to fp16 2^-11 of it; numerator and
     denominator each carry that, and sums of n terms in fp32, 4 sqrt(n) 2^-23
     of A (Higham and Mary, as in tests/helpers.py); a row's largest weight is
-    2^10 or more in fp16's units, so the weights below its normal range (2^-14),
-    off by half a step of 2^-24, are off by at most 2^-35 of the largest, times a
-    code of at most 127 by 2^-35 of the largest |V|; then bf16's rounding:
+    2^3 or more in fp16's units, so the weights below its normal range (2^-14),
+    off by half a step of 2^-24, are off by at most 2^-28 of the largest, times a
+    code of at most 127 by 2^-28 of the largest |V|; then bf16's rounding:
     |o - o64| <= 2^-8 |o64| + (2^-11 + 2 (2^-16 X + 2^-20) + 4 sqrt(n) 2^-23) A
-                 + n 2^-35 max|V|, all but the first term times 1.05."""
+                 + n 2^-28 max|V|, all but the first term times 1.05."""
 import ctypes
 import threading
 
@@ -316,7 +316,7 @@ def test_read_one_of_the_two(gpu, lib):
 
 def tolerance(o64, A, X, big, n):
     return 2.0 ** -8 * np.abs(o64) + 1.05 * ((2.0 ** -11 + 2 * (2.0 ** -16 * X + 2.0 ** -20) + 4 * np.sqrt(n) * 2.0 ** -23) * A
-                                             + n * 2.0 ** -35 * big)
+                                             + n * 2.0 ** -28 * big)
 
 
 class Attn:

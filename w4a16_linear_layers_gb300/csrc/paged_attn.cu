@@ -26,7 +26,7 @@
 // codes as operand A.  The warps' sums meet when the piece is done.
 //
 // The reference m is raised only where a weight would pass 2^15, and then to put
-// the row's largest at 2^11: no exchange between lanes elsewhere (a tile of 128
+// the row's largest at 2^4: no exchange between lanes elsewhere (a tile of 128
 // tokens that the block's warps shared, with a running maximum exchanged through
 // shared memory and the components of the output divided between them, took 118
 // us for 12 x 8 rows of 32 heads over 8192 tokens).
@@ -36,8 +36,8 @@
 // and the rows, mostly 4 to 32, fill a fraction of its tile.
 //
 // Precision.  Codes are exact in fp16, and so is q up to 2^-39 of its row's
-// largest component.  Weights have fp16's 11 bits down to 2^-24 of the row's
-// largest, and are at most 2^-35 of it off below that.  Scores, sums and
+// largest component.  Weights have fp16's 11 bits down to 2^-17 of the row's
+// largest, and are at most 2^-28 of it off below that.  Scores, sums and
 // outputs are fp32.
 #include <cuda_fp16.h>
 
@@ -55,6 +55,11 @@ constexpr int kMeetStride = 36;     // floats of a row's 32 components where the
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr float kNone = -1e30f;     // reference of a row that has seen nothing
+// Logarithms of the weights that a row's reference may let through, and of its
+// largest where it is set: 11 apart, so that few blocks set one (4 apart, a third
+// of the blocks of 32 rows did).
+constexpr float kMostWeight = 15.0f;
+constexpr float kNewWeight = 4.0f;
 
 template <int NR>
 struct Shape {
@@ -282,6 +287,19 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NR>::kPerSm) attn_kernel(c
   int ahead_i = warp;                // of the piece
   const uint8_t* ahead_from = nullptr;
   bool ahead_more = true;
+  const int per_page = static_cast<int>(a.c.page_size) >> 4;
+  const int page_step = kAttnWarps / per_page, in_page_step = kAttnWarps % per_page;
+  const int64_t head_bytes = static_cast<int64_t>(per_page) * kCacheBlock, page_bytes = head_bytes * a.c.kv_heads;
+  const int32_t* table = nullptr;    // of the sequence, at the block's page
+  int in_page = 0;
+  const uint8_t* head_at = nullptr;  // of page 0
+  auto enter = [&]() {               // the piece's first block
+    const int n = ahead.span.first + ahead.off + warp, page = n / per_page;
+    in_page = n - page * per_page;
+    table = a.c.block_table + ahead.b * a.c.max_pages + page;
+    head_at = a.c.cache + ahead.seg / p.row_tiles * head_bytes;
+    ahead_i = warp;
+  };
   auto look = [&]() {                // the next block's address: read long before it is needed
     while (ahead_i >= ahead.piece()) {
       ahead.next(a);
@@ -289,10 +307,17 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NR>::kPerSm) attn_kernel(c
         ahead_more = false;
         return;
       }
-      ahead_i = warp;
+      enter();
     }
-    ahead_from = cache_block(a.c, ahead.b, ahead.seg / p.row_tiles, ahead.span.first + ahead.off + ahead_i);
+    const int page = __ldg(table);
+    ahead_from = page >= 0 && page < a.c.pages ? head_at + page * page_bytes + in_page * kCacheBlock : nullptr;
     ahead_i += kAttnWarps;
+    table += page_step;
+    in_page += in_page_step;
+    if (in_page >= per_page) {
+      in_page -= per_page;
+      ++table;
+    }
   };
   uint32_t there = 0;                // bit i: the block in slot i is on a page
   auto fetch = [&](int slot) {
@@ -305,6 +330,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NR>::kPerSm) attn_kernel(c
     }
     look();
   };
+  enter();
   look();
 #pragma unroll
   for (int i = 0; i < kSlots; ++i) fetch(i);
@@ -416,73 +442,70 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NR>::kPerSm) attn_kernel(c
         const float lv0 = log2_above(vs0), lv1 = log2_above(vs1);
         const int j0 = 16 * (walk.span.first + walk.off + i);     // first token of the block
         const bool all_seen = j0 >= seen_from && j0 + 16 <= seen_to;
-        // scores times log2(e): x[r][c] * kk of tokens tok + 2 c and rows 8 r + 2 q, + 1
+        // scores times log2(e), of tokens tok + 2 c and rows 8 r + 2 q, + 1
         f32x2 x[NR][2];
-        const f32x2 kk[2] = {both(kCap ? 1.0f : ks0), both(kCap ? 1.0f : ks1)};
-        uint32_t hidden = 0;        // bit 4 r + 2 c + row
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            x[r][c] = mul2(pack2(s[r][2 * c], s[r][2 * c + 1]), factor[r]);
+            x[r][c] = mul2(mul2(pack2(s[r][2 * c], s[r][2 * c + 1]), factor[r]), both(c == 0 ? ks0 : ks1));
             if constexpr (kCap) {
               // tanh(y) = 1 - 2 / (1 + e^2y), with an error of about 2^-23
               float v[2];
-              unpack2(mul2(x[r][c], both(c == 0 ? ks0 : ks1)), v[0], v[1]);
+              unpack2(x[r][c], v[0], v[1]);
 #pragma unroll
               for (int k = 0; k < 2; ++k)
                 v[k] = a.softcap * kLog2e * (1.0f - __fdividef(2.0f, 1.0f + ex2(v[k] * (2.0f * kLog2e / a.softcap))));
               x[r][c] = pack2(v[0], v[1]);
             }
           }
-          if (!all_seen) {
+        }
+        if (!all_seen) {
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
             const int2 lo = *reinterpret_cast<const int2*>(lows + 8 * r + 2 * q), hi = *reinterpret_cast<const int2*>(highs + 8 * r + 2 * q);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const int j = j0 + tok + 2 * c;
-              hidden |= (j < lo.x || j >= hi.x ? 1u : 0u) << (4 * r + 2 * c);
-              hidden |= (j < lo.y || j >= hi.y ? 2u : 0u) << (4 * r + 2 * c);
+              float v0, v1;
+              unpack2(x[r][c], v0, v1);
+              x[r][c] = pack2(j >= lo.x && j < hi.x ? v0 : -INFINITY, j >= lo.y && j < hi.y ? v1 : -INFINITY);
             }
           }
         }
-        // the four numbers f of row group r, -inf where hidden
-        auto seen = [&](int r, f32x2 f0, f32x2 f1, float (&v)[4]) {
-          unpack2(f0, v[0], v[1]);
-          unpack2(f1, v[2], v[3]);
-          if (!all_seen) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (hidden >> (4 * r + k) & 1u) v[k] = -INFINITY;
-          }
-        };
-        auto weight_log = [&](int r, int c) { return sub2(fma2(x[r][c], kk[c], top[r]), low[r]); };
-        float far = -INFINITY;      // the largest weight's logarithm
+        auto under = [&](int r, int c) { return sub2(add2(x[r][c], top[r]), low[r]); };   // less the reference
+        float far[2] = {-INFINITY, -INFINITY};
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-          float w[4];
-          seen(r, add2(weight_log(r, 0), both(lv0)), add2(weight_log(r, 1), both(lv1)), w);
-          far = fmaxf(far, fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3])));
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float v0, v1;
+            unpack2(under(r, c), v0, v1);
+            far[c] = fmaxf(far[c], fmaxf(v0, v1));
+          }
         }
-        if (__any_sync(kAll, far > 15.0f)) {
+        if (__any_sync(kAll, fmaxf(far[0] + lv0, far[1] + lv1) > kMostWeight)) {
           // references of the rows concerned up, what stands under them down
 #pragma unroll
           for (int r = 0; r < NR; ++r) {
-            float w[4], m[2], c[2], next[2], keep[2];
-            seen(r, add2(weight_log(r, 0), both(lv0)), add2(weight_log(r, 1), both(lv1)), w);
-            const bool up[2] = {max_over_g(fmaxf(w[0], w[2])) > 15.0f, max_over_g(fmaxf(w[1], w[3])) > 15.0f};
-            seen(r, mul2(x[r][0], kk[0]), mul2(x[r][1], kk[1]), w);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) next[k] = -max_over_g(fmaxf(w[k], w[2 + k]));
-            // (a product rounds further off than the small number's size where scores are large: formed as weight_log does)
-            const f32x2 n2 = pack2(next[0], next[1]);
-            seen(r, add2(fma2(x[r][0], kk[0], n2), both(lv0)), add2(fma2(x[r][1], kk[1], n2), both(lv1)), w);
+            float w[4], m[2], c[2], keep[2];
+            bool up[2];
+            unpack2(add2(under(r, 0), both(lv0)), w[0], w[1]);
+            unpack2(add2(under(r, 1), both(lv1)), w[2], w[3]);
+            up[0] = fmaxf(w[0], w[2]) > kMostWeight;
+            up[1] = fmaxf(w[1], w[3]) > kMostWeight;
+            if (!__any_sync(kAll, up[0] || up[1])) continue;
+            unpack2(x[r][0], w[0], w[1]);
+            unpack2(x[r][1], w[2], w[3]);
             unpack2(top[r], m[0], m[1]);
             unpack2(low[r], c[0], c[1]);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const float over = max_over_g(fmaxf(w[k], w[2 + k])) - 11.0f;
-              keep[k] = up[k] ? ex2((next[k] - m[k]) + (c[k] - over)) : 1.0f;
-              m[k] = up[k] ? next[k] : m[k];
+              up[k] = max_over_g(up[k] ? 1.0f : 0.0f) > 0.0f;
+              const float next = max_over_g(fmaxf(w[k], w[2 + k]));
+              const float over = max_over_g(fmaxf(w[k] - next + lv0, w[2 + k] - next + lv1)) - kNewWeight;
+              keep[k] = up[k] ? ex2((-m[k] - next) + (c[k] - over)) : 1.0f;
+              m[k] = up[k] ? -next : m[k];
               c[k] = up[k] ? over : c[k];
             }
             top[r] = pack2(m[0], m[1]);
@@ -500,18 +523,32 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NR>::kPerSm) attn_kernel(c
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
           float w[4];
-          seen(r, weight_log(r, 0), weight_log(r, 1), w);
+          unpack2(under(r, 0), w[0], w[1]);
+          unpack2(under(r, 1), w[2], w[3]);
 #pragma unroll
           for (int k = 0; k < 4; ++k) w[k] = ex2(w[k]);
-          sum[r] = add2(sum[r], add2(pack2(w[0], w[1]), pack2(w[2], w[3])));
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            w[k] *= k < 2 ? vs0 : vs1;
-            if (!all_seen && (hidden >> (4 * r + k) & 1u)) w[k] = 0.0f;      // whatever the scale holds
-          }
+          const f32x2 p0 = pack2(w[0], w[1]), p1 = pack2(w[2], w[3]);
+          sum[r] = add2(sum[r], add2(p0, p1));
+          unpack2(mul2(p0, both(vs0)), w[0], w[1]);
+          unpack2(mul2(p1, both(vs1)), w[2], w[3]);
           const __half2 w0 = __floats2half2_rn(w[0], w[1]), w1 = __floats2half2_rn(w[2], w[3]);
-          b0[r] = transpose(*reinterpret_cast<const uint32_t*>(&w0));
-          b1[r] = transpose(*reinterpret_cast<const uint32_t*>(&w1));
+          b0[r] = *reinterpret_cast<const uint32_t*>(&w0);
+          b1[r] = *reinterpret_cast<const uint32_t*>(&w1);
+        }
+        if (!all_seen) {      // hidden weights 0, whatever the scale holds
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            float v[4];
+            unpack2(x[r][0], v[0], v[1]);
+            unpack2(x[r][1], v[2], v[3]);
+            b0[r] &= (v[0] == -INFINITY ? 0u : 0xFFFFu) | (v[1] == -INFINITY ? 0u : 0xFFFF0000u);
+            b1[r] &= (v[2] == -INFINITY ? 0u : 0xFFFFu) | (v[3] == -INFINITY ? 0u : 0xFFFF0000u);
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          b0[r] = transpose(b0[r]);
+          b1[r] = transpose(b1[r]);
         }
         // ---- outputs: components 16 g + 4 w + 0 .. 3, tokens by q
         const uint8_t* const v = blk + kVCodes;
