@@ -285,7 +285,8 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NR>::kPerSm) attn_kernel(c
   // ---- copies: this warp's blocks, through all pieces, ahead of their use
   Walk ahead = walk;
   int ahead_i = warp;                // of the piece
-  const uint8_t* ahead_from = nullptr;
+  int ahead_page = -1, ahead_in_page = 0;
+  const uint8_t* ahead_head = nullptr;
   bool ahead_more = true;
   const int per_page = static_cast<int>(a.c.page_size) >> 4;
   const int page_step = kAttnWarps / per_page, in_page_step = kAttnWarps % per_page;
@@ -300,7 +301,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NR>::kPerSm) attn_kernel(c
     head_at = a.c.cache + ahead.seg / p.row_tiles * head_bytes;
     ahead_i = warp;
   };
-  auto look = [&]() {                // the next block's address: read long before it is needed
+  auto look = [&]() {                // the next block's page: read long before it is needed
     while (ahead_i >= ahead.piece()) {
       ahead.next(a);
       if (ahead.left == 0) {
@@ -309,8 +310,9 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NR>::kPerSm) attn_kernel(c
       }
       enter();
     }
-    const int page = __ldg(table);
-    ahead_from = page >= 0 && page < a.c.pages ? head_at + page * page_bytes + in_page * kCacheBlock : nullptr;
+    ahead_page = __ldg(table);       // (looked at in fetch: nothing waits for it here)
+    ahead_in_page = in_page;
+    ahead_head = head_at;
     ahead_i += kAttnWarps;
     table += page_step;
     in_page += in_page_step;
@@ -322,11 +324,12 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<NR>::kPerSm) attn_kernel(c
   uint32_t there = 0;                // bit i: the block in slot i is on a page
   auto fetch = [&](int slot) {
     if (!ahead_more) return;
-    there = (there & ~(1u << slot)) | (ahead_from != nullptr ? 1u << slot : 0u);
+    const bool real = ahead_page >= 0 && ahead_page < a.c.pages;
+    there = (there & ~(1u << slot)) | (real ? 1u << slot : 0u);
     if (lane == 0) {
       const uint32_t bar = full_at + 8 * slot;
-      mbar_arrive_expect_tx(bar, ahead_from != nullptr ? kCacheBlock : 0);
-      if (ahead_from != nullptr) bulk_load(ring_at + slot * kCacheBlock, ahead_from, kCacheBlock, bar);
+      mbar_arrive_expect_tx(bar, real ? kCacheBlock : 0);
+      if (real) bulk_load(ring_at + slot * kCacheBlock, ahead_head + ahead_page * page_bytes + ahead_in_page * kCacheBlock, kCacheBlock, bar);
     }
     look();
   };
