@@ -510,8 +510,8 @@ qlin_status_t qlin_adjust_logits_f32(const float *logits, int64_t M, int64_t V,
  *   with the four 32-byte quarters of a token's codes permuted: components
  *   32 j .. 32 j + 31 of token r stand at quarter j ^ (r / 4) (the order in
  *   which the attention reads shared memory without bank conflicts).
- * Its base is 128-byte aligned.  qlin_kv_cache_bytes gives its size, 0 for
- * sizes outside the rules.
+ * Its base is 128-byte aligned, its blocks at most 2^31 - 1.  qlin_kv_cache_bytes
+ * gives its size, 0 for sizes outside the rules.
  *
  * A sequence's tokens are numbered from 0; token j of sequence b is in page
  * block_table[b, j / page_size], at its place j % page_size.  Arguments that the

@@ -15,21 +15,22 @@
 // whatever the sequences' lengths.  The parts of a segment that shares cut meet
 // in a second kernel; segments inside one are finished at once.
 //
-// A warp takes every eighth block of 16 tokens of its thread block's piece, on
-// its own: it brings the 4224 bytes into its slots in shared memory by one bulk
-// copy each, two or three ahead, and nothing in the loop waits for another warp.
-// Scores are formed transposed, tokens x rows: the codes are operand A (m16 = the
-// tokens), widened to fp16 on the way, and q, as fp16 times a power of two of
-// its row, operand B (n8 = rows).  So 1 to 8 rows cost half of what rows as operand
-// A would.  The weights, as fp16, are transposed between the lanes (movmatrix) and
-// are operand B again of the output, formed as components x rows, with the value
-// codes as operand A.  The warps' sums meet when the piece is done.
+// A thread block goes through its share 128 tokens at a time.  Scores are formed
+// transposed, tokens x rows, warp w those of the tile's block w: the key codes are
+// operand A (m16 = the block's tokens), widened to fp16 on the way, and q, as fp16
+// times a power of two of its row, operand B (n8 = rows).  So 1 to 8 rows cost half of
+// what rows as operand A would, and no code is widened twice.  The weights go as
+// fp16 through shared memory, and the outputs are formed transposed too, components
+// x rows, with the value codes as operand A: warp w takes the 32 components w % 4
+// from the half w / 4 of the tile.  Each warp brings its block of the tiles to
+// come by bulk copies: keys into a slot of its own, free when its scores are done,
+// values where all read them, free behind the next tile's barrier.
 //
-// The reference m is raised only where a weight would pass 2^15, and then to put
-// the row's largest at 2^4: no exchange between lanes elsewhere (a tile of 128
-// tokens that the block's warps shared, with a running maximum exchanged through
-// shared memory and the components of the output divided between them, took 118
-// us for 12 x 8 rows of 32 heads over 8192 tokens).
+// One barrier a tile: the reference m is raised only where a weight would pass
+// 2^15, and then to put the row's largest at 2^4, so that weights are formed and
+// written as if it held, and the barrier that they need anyway says whether it
+// did.  (With a running maximum exchanged before, two barriers and copies
+// through one producer warp a tile took twice the time.)
 //
 // mma.sync, not tcgen05: its operands come from registers, where the codes are
 // widened; tcgen05's would have to be written to shared or tensor memory first,
@@ -51,6 +52,7 @@ constexpr int kAttnWarps = 8;
 constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kTileBlocks = 8;      // of 16 tokens, of a tile
 constexpr int kTile = 16 * kTileBlocks;
+constexpr int kScaleBytes = kCacheBlock - kKScales;    // of a block
 constexpr int kMinShare = kTileBlocks;
 constexpr int kQStride = 272;       // bytes of a row of q: rows 16 bytes apart mod 128
 constexpr int kPStride = 288;       // bytes of a row of weights: rows 32 bytes apart mod 128
@@ -61,41 +63,29 @@ constexpr float kNone = -1e30f;     // reference of a row that has seen nothing
 // largest where it is set: 11 apart, so that few tiles set one (4 apart, a third
 // of the tiles of 32 rows did).
 constexpr float kMostWeight = 15.0f;
-constexpr float kNewWeight = 4.0f;
+constexpr float kLiftWeight = 4.0f;
+constexpr float kNewWeight = 0.0f;
 
 template <int NR>
 struct Shape {
   static constexpr int kRows = 8 * NR;
-  static constexpr int kParts = NR == 4 ? 2 : 1;         // row parts, shared out among the warps for the scores
-  static constexpr int kGroups = NR / kParts;            // 8-row groups of a part
-  static constexpr int kTokenWarps = kAttnWarps / kParts;
   static constexpr int kStages = NR == 1 ? 3 : 2;
-  // shared memory, in order
-  static constexpr int kRing = kStages * kTileBlocks * kCacheBlock;
-  static constexpr int kQ = kRing;
-  static constexpr int kP = kQ + kRows * kQStride;
-  static constexpr int kO = kP + 2 * kRows * kPStride;   // fp32 [rows][128]
-  static constexpr int kPair = kO + kRows * 512;         // float2 [token warps][rows]: references; sums
-  static constexpr int kRef = kPair + kTokenWarps * kRows * 8;    // float2 [rows]
-  static constexpr int kKeep = kRef + kRows * 8;         // fp32 [rows]
+  // shared memory, in order: [stages][warps] keys, the same of scales (K, V), of values
+  static constexpr int kScaleRing = kStages * kTileBlocks * kVCodes;
+  static constexpr int kVRing = kScaleRing + kStages * kTileBlocks * kScaleBytes;
+  static constexpr int kQ = kVRing + kStages * kTileBlocks * kVCodes;
+  static constexpr int kP = kQ + kRows * kQStride;       // weights of two tiles
+  static constexpr int kO = kP;                          // fp32 [rows][128], when a piece is done
+  static_assert(512 <= 2 * kPStride, "outputs stand where the weights did");
+  static constexpr int kPair = kP + 2 * kRows * kPStride;      // float2 [warps][rows]: references; sums
+  static constexpr int kRef = kPair + kAttnWarps * kRows * 8;     // float4 [rows / 2]: two rows' references
+  static constexpr int kKeep = kRef + kRows * 8;         // fp32 [rows]: what a raised reference leaves of the sums
   static constexpr int kFactor = kKeep + kRows * 4;      // fp32 [rows]
-  static constexpr int kLow = kFactor + kRows * 4;       // int32 [rows]: first token seen
+  static constexpr int kTo = kFactor + kRows * 4;        // int32 [rows]: the row's head of the sequence's outputs, -1: none
+  static constexpr int kLow = kTo + kRows * 4;           // int32 [rows]: first token seen
   static constexpr int kHigh = kLow + kRows * 4;         // and the one behind the last
   static constexpr int kBytes = kHigh + kRows * 4;
 };
-
-// What a stage of the ring holds.
-struct alignas(16) Tile {
-  int j0;              // first token
-  int blocks;          // of 16 tokens
-  uint32_t there;      // bit i: block i is on a page
-  uint32_t flags;
-  int64_t b;
-  int seg;
-  int len, fresh;      // of the sequence
-  int cut;             // the piece starts inside its segment
-};
-enum : uint32_t { kFirst = 1, kLast = 2, kWhole = 4, kFinal = 8 };   // of a piece; the piece is a segment; of the share
 
 // A row's reference m + c and the sum under it, of a part of its tokens.
 struct alignas(16) Share {
@@ -130,8 +120,14 @@ __device__ __forceinline__ Span span_of(const PagedAttnArgs& a, const SeqLen& s)
 
 // Blocks of 16 that each of `grid` thread blocks takes.
 __device__ __forceinline__ int64_t share_of(int64_t total, int grid) {
-  const int64_t share = (total + grid - 1) / grid;
+  // (a 32-bit division unless it takes more: a tenth of the instructions)
+  const int64_t share = total < 1LL << 31 ? static_cast<uint32_t>(total + grid - 1) / static_cast<uint32_t>(grid) : (total + grid - 1) / grid;
   return share < kMinShare ? kMinShare : share;
+}
+
+// The share that block `at` is in.
+__device__ __forceinline__ int share_at(int64_t at, int64_t share) {
+  return (at | share) < 1LL << 31 ? static_cast<int>(at) / static_cast<int>(share) : static_cast<int>(at / share);
 }
 
 // A walk through a share: its pieces (parts of segments), in order.
@@ -166,6 +162,17 @@ struct Walk {
   }
 };
 
+// A piece that the copies have come to, for when its tiles are gone through.
+struct alignas(16) Piece {
+  int64_t b;
+  int seg, len, fresh;
+  int cut;             // its first block of the segment
+  int n;               // blocks of 16
+  int j0;              // first token
+  bool whole, final;   // it is a segment; the last one of the share
+};
+constexpr int kPieces = 8;      // the copies look up to kStages + 1 pieces ahead
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -196,24 +203,24 @@ __device__ __forceinline__ float log2_above(float v) {
 template <int NR, bool kCap>
 __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams p) {
   using S = Shape<NR>;
-  constexpr int kStages = S::kStages, kGroups = S::kGroups, kOwn = S::kParts;   // kOwn: blocks of a tile that a warp scores
+  constexpr int kStages = S::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint64_t full[kStages];     // the stage's blocks are there
-  __shared__ uint64_t told[kStages];     // its Tile is written
-  __shared__ Tile tiles[kStages];
-  __shared__ int abort_flag, told_abort;
+  __shared__ uint64_t full_k[kAttnWarps][kStages], full_v[kStages];      // a warp's keys and scales, all values are there
+  __shared__ Walk aheads[kAttnWarps];       // of each warp's copies
+  __shared__ Piece pieces[kAttnWarps][kPieces];
+  __shared__ Walk start;
+  __shared__ int abort_flag;
   __shared__ int64_t warp_sums[kAttnWarps];
-  __shared__ Walk ahead;             // of the copies
   __shared__ int64_t before_b;
   const PagedAttnArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int segs = p.row_tiles * static_cast<int>(a.c.kv_heads);
 
   if (tid == 0) {
-    abort_flag = told_abort = 0;
+    abort_flag = 0;
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_u32(&full[i]), 1);
-      mbar_init(smem_u32(&told[i]), 1);
+      for (int w = 0; w < kAttnWarps; ++w) mbar_init(smem_u32(&full_k[w][i]), 1);
+      mbar_init(smem_u32(&full_v[i]), kAttnWarps);
     }
     fence_barrier_init();
   }
@@ -225,13 +232,14 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
   auto chunk = [&](int64_t b0, int& n, int64_t& incl, int64_t& all) {
     const int64_t b = b0 + tid;
     n = b < a.c.B ? span_of(a, seq_len(a.c, b, a.T)).count : 0;
-    incl = n;
+    uint32_t in_warp = static_cast<uint32_t>(n);      // 32 spans of 2^26 blocks at most
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(kAll, incl, o);
-      if (lane >= o) incl += v;
+      const uint32_t v = __shfl_up_sync(kAll, in_warp, o);
+      if (lane >= o) in_warp += v;
     }
-    if (lane == 31) warp_sums[warp] = incl;
+    if (lane == 31) warp_sums[warp] = in_warp;
+    incl = in_warp;
     __syncthreads();
     all = 0;
 #pragma unroll
@@ -262,12 +270,13 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
     if (b0 > 0) chunk(b0, n0, incl, all);
     const int64_t from = (before + incl - n0) * segs;
     if (n0 > 0 && from <= at && at < from + static_cast<int64_t>(n0) * segs) {
-      ahead.b = b0 + tid;
-      ahead.segs = segs;
-      ahead.seg = static_cast<int>((at - from) / n0);
-      ahead.off = static_cast<int>((at - from) % n0);
-      ahead.left = total - at < share ? total - at : share;
-      ahead.load(a);
+      start.b = b0 + tid;
+      start.segs = segs;
+      const int64_t in_b = at - from;
+      start.seg = in_b < 1LL << 31 ? static_cast<int>(in_b) / n0 : static_cast<int>(in_b / n0);
+      start.off = static_cast<int>(in_b - static_cast<int64_t>(start.seg) * n0);
+      start.left = total - at < share ? total - at : share;
+      start.load(a);
       before_b = from;
     }
     before += all;
@@ -275,195 +284,224 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
   }
   __syncthreads();
 
+  if (tid == 0) {
+    // the first boundary inside a segment announces it
+    const int64_t s0 = before_b + static_cast<int64_t>(start.seg) * start.span.count;
+    const int64_t first = share_at(s0, share), last = share_at(s0 + start.span.count - 1, share);
+    const bool cut = start.off > 0 && first == blockIdx.x - 1;
+    *reinterpret_cast<int4*>(p.cuts + 4 * blockIdx.x) =
+        make_int4(cut ? start.seg : -1, static_cast<int>(first), static_cast<int>(last), static_cast<int>(start.b));
+  }
+
   // A copy that does not come ends the work, not the walk through the tiles, in
-  // which the warps keep meeting: they go on with tiles told to be empty.
+  // which the warps keep meeting.
   const WaitCtx ctx{p.err, &abort_flag, kWaitLimitNs};
-  const WaitCtx told_ctx{p.err, &told_abort, 8 * kWaitLimitNs};
   bool ok = true;
 
-  // ---- copies: warp 0's lanes bring the blocks of a tile, one each.  The next
-  // tile's pages are read a tile ahead of their use.
-  int ahead_i = 0;                   // of the piece
-  int ahead_page = 0;
-  bool ahead_more = true;
+  // ---- copies: this warp's block of each tile, the next tile's page read a tile
+  // before it is used
+  Walk& ahead = aheads[warp];
   const int per_page = static_cast<int>(a.c.page_size) >> 4;
-  auto look = [&]() {
-    const int i = ahead_i + lane;
-    if (lane < kTileBlocks && i < ahead.piece())
-      ahead_page = __ldg(a.c.block_table + ahead.b * a.c.max_pages + (ahead.span.first + ahead.off + i) / per_page);
-  };
-  auto fetch = [&](int stage) {      // warp 0
-    if (!ahead_more) return;
-    const int n = ahead.piece(), left = n - ahead_i;
-    const int first = ahead.span.first + ahead.off + ahead_i;
-    const bool real = ok && lane < kTileBlocks && lane < left && ahead_page >= 0 && ahead_page < a.c.pages;
-    const uint32_t there = __ballot_sync(kAll, real);
-    const bool last = left <= kTileBlocks, final = last && ahead.left == n;
-    if (lane == 0) {
-      Tile& t = tiles[stage];
-      t.j0 = 16 * first;
-      t.blocks = left < kTileBlocks ? left : kTileBlocks;
-      t.there = there;
-      t.flags = (ahead_i == 0 ? kFirst : 0u) | (last ? kLast : 0u) | (n == ahead.span.count ? kWhole : 0u) | (final ? kFinal : 0u);
-      t.b = ahead.b;
-      t.seg = ahead.seg;
-      t.len = ahead.seq.len;
-      t.fresh = ahead.seq.fresh;
-      t.cut = ahead.off;
-      if (ok) mbar_arrive_expect_tx(smem_u32(&full[stage]), __popc(there) * kCacheBlock);
-      mbar_arrive(smem_u32(&told[stage]));
-    }
-    __syncwarp();
-    if (real) {
-      const int in_page = (first + lane) % per_page;
-      bulk_load(smem_u32(smem) + (stage * kTileBlocks + lane) * kCacheBlock,
-                a.c.cache + ((ahead_page * a.c.kv_heads + ahead.seg / p.row_tiles) * per_page + in_page) * kCacheBlock, kCacheBlock,
-                smem_u32(&full[stage]));
-    }
-    ahead_i += kTileBlocks;
-    ahead_more = !final;
-    if (last && !final) {
-      __syncwarp();
-      if (lane == 0) ahead.next(a);
-      ahead_i = 0;
-      __syncwarp();
-    }
-    if (ahead_more) look();
-  };
-  if (warp == 0) {
-    if (lane == 0) {
-      // the first boundary inside a segment announces it
-      const int64_t s0 = before_b + static_cast<int64_t>(ahead.seg) * ahead.span.count;
-      const int64_t first = s0 / share, last = (s0 + ahead.span.count - 1) / share;
-      const bool cut = ahead.off > 0 && first == blockIdx.x - 1;
-      *reinterpret_cast<int4*>(p.cuts + 4 * blockIdx.x) =
-          make_int4(cut ? ahead.seg : -1, static_cast<int>(first), static_cast<int>(last), static_cast<int>(ahead.b));
-    }
-    __syncwarp();
+  const int page_step = kTileBlocks / per_page, in_page_step = kTileBlocks % per_page;
+  const uint32_t page_blocks = static_cast<uint32_t>(per_page * static_cast<int>(a.c.kv_heads));
+  int next_i = 0, next_n = 0;        // the tile's first block of the piece, the piece's blocks
+  const int32_t* table = nullptr;    // at the block's page
+  int page = -1, in_page = 0, put = 0;
+  uint32_t head_at = 0;              // block of the cache: the head's first of page 0
+  // blocks of the tiles whose keys were sent, not their values: two at most
+  constexpr uint32_t kNoBlock = 0xFFFFFFFFu;
+  uint32_t values[2] = {kNoBlock, kNoBlock};
+  int waiting = 0;
+  bool more = true;
+  uint32_t sent_pages = 0;           // bit s: the block in stage s is on a page
+  auto look = [&]() { page = next_i + warp < next_n ? __ldg(table) : -1; };
+  auto enter = [&]() {               // ahead's piece
+    next_i = 0;
+    next_n = ahead.piece();
+    const int n = ahead.span.first + ahead.off, mine = n + warp, of_table = mine / per_page;
+    in_page = mine - of_table * per_page;
+    table = a.c.block_table + ahead.b * a.c.max_pages + of_table;
+    head_at = static_cast<uint32_t>(ahead.seg / p.row_tiles * per_page);
+    if (lane == 0)
+      pieces[warp][put] = Piece{ahead.b, ahead.seg, ahead.seq.len, ahead.seq.fresh, ahead.off, next_n, 16 * n, next_n == ahead.span.count,
+                                next_n == ahead.left};
+    put = (put + 1) % kPieces;
     look();
-    for (int i = 0; i < kStages; ++i) fetch(i);
+  };
+  auto send_keys = [&](int stage) {  // and scales
+    if (!more) return;
+    const bool real = page >= 0 && page < a.c.pages;
+    const uint32_t block = head_at + static_cast<uint32_t>(page) * page_blocks + static_cast<uint32_t>(in_page);
+    if (ok && lane == 0) {
+      const uint32_t bar = smem_u32(&full_k[warp][stage]);
+      mbar_arrive_expect_tx(bar, real ? kVCodes + kScaleBytes : 0);
+      if (real) {
+        const uint8_t* const from = a.c.cache + static_cast<int64_t>(block) * kCacheBlock;
+        bulk_load(smem_u32(smem) + (stage * kTileBlocks + warp) * kVCodes, from, kVCodes, bar);
+        bulk_load(smem_u32(smem) + S::kScaleRing + (stage * kTileBlocks + warp) * kScaleBytes, from + kKScales, kScaleBytes, bar);
+      }
+    }
+    sent_pages = (sent_pages & ~(1u << stage)) | (real ? 1u << stage : 0u);
+    (waiting == 0 ? values[0] : values[1]) = real ? block : kNoBlock;
+    ++waiting;
+    next_i += kTileBlocks;
+    if (next_i < next_n) {
+      table += page_step;
+      in_page += in_page_step;
+      if (in_page >= per_page) {
+        in_page -= per_page;
+        ++table;
+      }
+      look();
+    } else {
+      more = ahead.left > next_n;
+      __syncwarp();
+      if (more) {
+        if (lane == 0) ahead.next(a);
+        __syncwarp();
+        enter();
+      }
+    }
+  };
+  auto send_values = [&](int stage) {
+    if (waiting == 0) return;
+    if (ok && lane == 0) {
+      const uint32_t bar = smem_u32(&full_v[stage]);
+      mbar_arrive_expect_tx(bar, values[0] != kNoBlock ? kVCodes : 0);
+      if (values[0] != kNoBlock)
+        bulk_load(smem_u32(smem) + S::kVRing + (stage * kTileBlocks + warp) * kVCodes,
+                  a.c.cache + static_cast<int64_t>(values[0]) * kCacheBlock + kVCodes, kVCodes, bar);
+    }
+    values[0] = values[1];
+    --waiting;
+  };
+  if (lane == 0) ahead = start;
+  __syncwarp();
+  enter();
+#pragma unroll
+  for (int i = 0; i < kStages; ++i) {
+    send_keys(i);
+    if (i < kStages - 1) send_values(i);
   }
-  __syncthreads();
 
   const int g = lane >> 2, q = lane & 3;
-  // Scores: tokens tok and tok + 1 of the blocks own .. own + kOwn - 1 of a tile,
-  // rows 8 (group0 + r) + 2 q and the next one.  The tokens are such that 8
-  // lanes' reads of keys (g = 2 u and 2 u + 1, 4 chunks each) meet in no bank.
+  // Scores: tokens tok and tok + 1 of the warp's block, rows 8 r + 2 q and the
+  // next one.  The tokens are such that 8 lanes' reads of keys (g = 2 u and
+  // 2 u + 1, 4 chunks each) meet in no bank.
   const int tok = 2 * (g >> 1) + 8 * (g & 1);
   const int k_turn = 2 * ((tok >> 2) & 3);
-  const int own = warp / S::kParts * kOwn;
-  const int group0 = warp % S::kParts * kGroups;
   // Outputs: components 32 quarter + 4 g .. + 3 of all rows, from four blocks of a tile.
   const int quarter = warp & 3, half = warp >> 2;
   uint8_t* const qs = smem + S::kQ;
   uint8_t* const ps = smem + S::kP;
   float* const os = reinterpret_cast<float*>(smem + S::kO);
   float2* const pairs = reinterpret_cast<float2*>(smem + S::kPair);
-  float2* const refs = reinterpret_cast<float2*>(smem + S::kRef);
+  float4* const refs = reinterpret_cast<float4*>(smem + S::kRef);
   float* const keeps = reinterpret_cast<float*>(smem + S::kKeep);
+  int* const tos = reinterpret_cast<int*>(smem + S::kTo);
   float* const factors = reinterpret_cast<float*>(smem + S::kFactor);
   int* const lows = reinterpret_cast<int*>(smem + S::kLow);
   int* const highs = reinterpret_cast<int*>(smem + S::kHigh);
   const int rows = static_cast<int>(a.T) * p.G;
 
-  // Of the rows that a lane scores.  The reference is a score (top, its negative)
-  // plus a small number (low), so that large scores do not swallow the logarithm
-  // of the value scale in it.
-  f32x2 factor[kGroups], top[kGroups], low[kGroups], sum[kGroups];
-  uint4 qb[kGroups][4];              // q as operand B: components 16 (q + 4 (c / 2)) + 8 (c % 2) .. + 7
+  // A row's reference is a score (its negative is held) plus a small number, so
+  // that large scores do not swallow the logarithm of the value scale in it.
+  f32x2 sum[NR];
+  constexpr int kHeld = NR <= 2 ? NR : 0;      // groups whose q stays in registers
+  uint4 qb[kHeld > 0 ? kHeld : 1][4];
+  auto q_part = [&](int r, int c) {            // operand B: components 16 (q + 4 (c / 2)) + 8 (c % 2) .. + 7
+    return *reinterpret_cast<const uint4*>(qs + (8 * r + g) * kQStride + 32 * (q + 4 * (c >> 1)) + 16 * (c & 1));
+  };
   float o[2][NR][4];
   int seen_from = 0, seen_to = 0;    // tokens that all rows see
 
-  int stage = 0, phase = 0, turn = 0;
-  for (int refill = -1;; refill = stage, phase ^= stage == kStages - 1, stage = stage == kStages - 1 ? 0 : stage + 1) {
-    // (the tile behind this one is told while some warps are still here, so its
-    // Tile may not be looked at before)
-    (void)mbar_wait(smem_u32(&told[stage]), phase, told_ctx, 90);
-    const Tile& tile = tiles[stage];
-    const uint32_t flags = tile.flags;
-    if (flags & kFirst) {
+  int stage = 0, phase = 0, turn = 0, get = 0;
+  int i = 0, n = 0, j0 = 0;          // the tile's first block of the piece, the piece's blocks, the tile's first token
+  for (;;) {
+    const Piece& piece = pieces[warp][get];
+    if (i >= n) {
       // q of the piece's rows, what they see
-      const int fresh = tile.fresh, len = tile.len, h = tile.seg / p.row_tiles;
-      const int row0 = (tile.seg - h * p.row_tiles) * S::kRows;
-      const uint16_t* const from = a.q + (tile.b * a.T * a.q_heads + h * p.G) * kHeadDim;
+      __syncwarp();
+      i = 0;
+      n = piece.n;
+      j0 = piece.j0;
+      // lane by row: its place, and what it sees
+      const int h = piece.seg / p.row_tiles, row = (piece.seg - h * p.row_tiles) * S::kRows + lane, t = row / p.G;
+      const bool real = lane < S::kRows && row < rows && t < piece.fresh;
+      const int to = real ? t * static_cast<int>(a.q_heads) + h * p.G + (row - t * p.G) : -1;
+      const int len = piece.len, token = len - piece.fresh + t;
+      const int64_t w = a.window > 0 ? a.window : 1LL << 40;
+      const int low = real && token - w + 1 > 0 ? static_cast<int>(token - w + 1) : 0;
+      const int high = !real ? 0 : a.causal ? token + 1 : token + w < len ? static_cast<int>(token + w) : len;
+      seen_from = __reduce_max_sync(kAll, low);
+      seen_to = __reduce_min_sync(kAll, real ? high : len);
+      if (warp == 0 && lane < S::kRows) {
+        tos[lane] = to;
+        lows[lane] = low;
+        highs[lane] = high;
+        reinterpret_cast<float2*>(refs)[lane] = (lane & 1) ? make_float2(0.0f, 0.0f) : make_float2(-kNone, -kNone);
+      }
+      const uint16_t* const from = a.q + piece.b * a.T * a.q_heads * kHeadDim;
       uint2 x[NR];
 #pragma unroll
       for (int k = 0; k < NR; ++k) {
-        const int row = row0 + warp + kAttnWarps * k, t = row / p.G;
-        x[k] = make_uint2(0, 0);
-        if (row < rows && t < fresh)
-          x[k] = __ldg(reinterpret_cast<const uint2*>(from + (t * a.q_heads + (row - t * p.G)) * kHeadDim) + lane);
+        const int at = __shfl_sync(kAll, to, warp + kAttnWarps * k);
+        x[k] = at >= 0 ? __ldg(reinterpret_cast<const uint2*>(from + static_cast<int64_t>(at) * kHeadDim) + lane) : make_uint2(0, 0);
       }
 #pragma unroll
       for (int k = 0; k < NR; ++k) {
-        const int r = warp + kAttnWarps * k, row = row0 + r, t = row / p.G;
+        const int r = warp + kAttnWarps * k;
         const float f[4] = {__uint_as_float(x[k].x << 16), __uint_as_float(x[k].x & 0xFFFF0000u), __uint_as_float(x[k].y << 16),
                             __uint_as_float(x[k].y & 0xFFFF0000u)};
-        float most = fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3])));
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, d));
+        // the largest exponent (of finite numbers' bits the order is that of the numbers)
+        const uint32_t most = __reduce_max_sync(kAll, max(max(x[k].x << 16 & 0x7F800000u, x[k].x & 0x7F800000u),
+                                                          max(x[k].y << 16 & 0x7F800000u, x[k].y & 0x7F800000u)));
         // into [2^14, 2^15)
-        const int e = min(max(static_cast<int>(__float_as_uint(most) >> 23), 27), 254);
+        const int e = min(max(static_cast<int>(most >> 23), 27), 254);
         const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 + 127 - e) << 23);
         const __half2 lo = __floats2half2_rn(f[0] * up, f[1] * up), hi = __floats2half2_rn(f[2] * up, f[3] * up);
         *reinterpret_cast<uint2*>(qs + r * kQStride + 8 * lane) =
             make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-        if (lane == 0) {
-          factors[r] = a.scale * __uint_as_float(static_cast<uint32_t>(e - 14) << 23) * (kCap ? 1.0f : kLog2e);
-          const int i = len - fresh + t;
-          const int64_t w = a.window > 0 ? a.window : 1LL << 40;
-          lows[r] = i - w + 1 > 0 ? static_cast<int>(i - w + 1) : 0;
-          highs[r] = a.causal ? i + 1 : i + w < len ? static_cast<int>(i + w) : len;
-          if (row >= rows || t >= fresh) highs[r] = 0;
-        }
+        if (lane == 0) factors[r] = a.scale * __uint_as_float(static_cast<uint32_t>(e - 14) << 23) * (kCap ? 1.0f : kLog2e);
       }
       __syncthreads();
-      const int last_row = min(min(S::kRows, rows - row0), fresh * p.G - row0) - 1;   // < 0: none
-      seen_from = last_row < 0 ? 0 : lows[last_row];
-      seen_to = last_row < 0 ? 0 : highs[0];
 #pragma unroll
-      for (int r = 0; r < kGroups; ++r) {
-        const int row = 8 * (group0 + r);
+      for (int r = 0; r < kHeld; ++r) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          qb[r][c] = *reinterpret_cast<const uint4*>(qs + (row + g) * kQStride + 32 * (q + 4 * (c >> 1)) + 16 * (c & 1));
-        const float2 f = *reinterpret_cast<const float2*>(factors + row + 2 * q);
-        factor[r] = pack2(f.x, f.y);
-        top[r] = both(-kNone);
-        low[r] = sum[r] = both(0.0f);
+        for (int c = 0; c < 4; ++c) qb[r][c] = q_part(r, c);
       }
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
+        sum[r] = both(0.0f);
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[0][r][c] = o[1][r][c] = 0.0f;
       }
     }
 
-    ok = __all_sync(kAll, ok && mbar_wait(smem_u32(&full[stage]), phase, ctx, 91));
-    const int j0 = tile.j0;
-    // All rows see all of the tile's 128 tokens.  Elsewhere what a row does not see
-    // gets no weight: blocks that are not there are gone through all the same, as
-    // whatever finite codes stand in their place.
-    const uint32_t there = ok ? tile.there : 0u;
-    const bool all_seen = there == 0xFFu && j0 >= seen_from && j0 + kTile <= seen_to;
-    const uint8_t* const ring = smem + stage * kTileBlocks * kCacheBlock;
+    ok = __all_sync(kAll, ok && mbar_wait(smem_u32(&full_k[warp][stage]), phase, ctx, 91));
+    // Whether all rows see all of the warp's block.  Elsewhere what a row does not
+    // see gets no weight; a block that is not there is gone through all the same, as
+    // whatever finite codes stand in its place.
+    const bool here = ok && i + warp < n && (sent_pages >> stage & 1u);
+    const int j = j0 + 16 * warp;
+    const bool all_seen = here && j >= seen_from && j + 16 <= seen_to;
 
     // ---- scores times log2(e)
-    f32x2 x[kOwn][kGroups][2];
-    float2 vs[kOwn];
+    f32x2 x[NR][2];
+    float2 vs;
+    {
+      const uint8_t* const keys = smem + (stage * kTileBlocks + warp) * kVCodes;
+      const uint8_t* const scales = smem + S::kScaleRing + (stage * kTileBlocks + warp) * kScaleBytes;
+      float s[NR][4];
 #pragma unroll
-    for (int n = 0; n < kOwn; ++n) {
-      const uint8_t* const blk = ring + (own + n) * kCacheBlock;
-      float s[kGroups][4];
-#pragma unroll
-      for (int r = 0; r < kGroups; ++r) {
+      for (int r = 0; r < NR; ++r) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) s[r][c] = 0.0f;
       }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const uint4 ka = *reinterpret_cast<const uint4*>(blk + tok * kHeadDim + 16 * ((q + 4 * c) ^ k_turn));
-        const uint4 kb = *reinterpret_cast<const uint4*>(blk + (tok + 1) * kHeadDim + 16 * ((q + 4 * c) ^ k_turn));
+        const uint4 ka = *reinterpret_cast<const uint4*>(keys + tok * kHeadDim + 16 * ((q + 4 * c) ^ k_turn));
+        const uint4 kb = *reinterpret_cast<const uint4*>(keys + (tok + 1) * kHeadDim + 16 * ((q + 4 * c) ^ k_turn));
         uint32_t fa[4][4];
         biased_u8x4_to_f16x4(ka.x, fa[0][0], fa[0][2]);
         biased_u8x4_to_f16x4(kb.x, fa[0][1], fa[0][3]);
@@ -474,184 +512,149 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
         biased_u8x4_to_f16x4(ka.w, fa[3][0], fa[3][2]);
         biased_u8x4_to_f16x4(kb.w, fa[3][1], fa[3][3]);
 #pragma unroll
-        for (int r = 0; r < kGroups; ++r) {
-          mma(s[r], fa[0], qb[r][2 * c].x, qb[r][2 * c].y);
-          mma(s[r], fa[1], qb[r][2 * c].z, qb[r][2 * c].w);
-          mma(s[r], fa[2], qb[r][2 * c + 1].x, qb[r][2 * c + 1].y);
-          mma(s[r], fa[3], qb[r][2 * c + 1].z, qb[r][2 * c + 1].w);
+        for (int r = 0; r < NR; ++r) {
+          const uint4 b0 = r < kHeld ? qb[r < kHeld ? r : 0][2 * c] : q_part(r, 2 * c);
+          const uint4 b1 = r < kHeld ? qb[r < kHeld ? r : 0][2 * c + 1] : q_part(r, 2 * c + 1);
+          mma(s[r], fa[0], b0.x, b0.y);
+          mma(s[r], fa[1], b0.z, b0.w);
+          mma(s[r], fa[2], b1.x, b1.y);
+          mma(s[r], fa[3], b1.z, b1.w);
         }
       }
-      const float2 ks = *reinterpret_cast<const float2*>(blk + kKScales + 4 * tok);
-      vs[n] = *reinterpret_cast<const float2*>(blk + kVScales + 4 * tok);
+      const float2 ks = *reinterpret_cast<const float2*>(scales + 4 * tok);
+      vs = *reinterpret_cast<const float2*>(scales + 64 + 4 * tok);
 #pragma unroll
-      for (int r = 0; r < kGroups; ++r) {
+      for (int r = 0; r < NR; ++r) {
+        const float2 f = *reinterpret_cast<const float2*>(factors + 8 * r + 2 * q);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          x[n][r][c] = mul2(mul2(pack2(s[r][2 * c], s[r][2 * c + 1]), factor[r]), both(c == 0 ? ks.x : ks.y));
+          x[r][c] = mul2(mul2(pack2(s[r][2 * c], s[r][2 * c + 1]), pack2(f.x, f.y)), both(c == 0 ? ks.x : ks.y));
           if constexpr (kCap) {
             // tanh(y) = 1 - 2 / (1 + e^2y), with an error of about 2^-23
             float v[2];
-            unpack2(x[n][r][c], v[0], v[1]);
+            unpack2(x[r][c], v[0], v[1]);
 #pragma unroll
             for (int k = 0; k < 2; ++k)
               v[k] = a.softcap * kLog2e * (1.0f - __fdividef(2.0f, 1.0f + ex2(v[k] * (2.0f * kLog2e / a.softcap))));
-            x[n][r][c] = pack2(v[0], v[1]);
+            x[r][c] = pack2(v[0], v[1]);
           }
         }
       }
     }
     if (!all_seen) {
+      if (!here) vs = make_float2(0.0f, 0.0f);
 #pragma unroll
-      for (int n = 0; n < kOwn; ++n) {
-        const bool here = (there >> (own + n)) & 1u;
-        const int j = j0 + 16 * (own + n) + tok;
-        if (!here) vs[n] = make_float2(0.0f, 0.0f);
+      for (int r = 0; r < NR; ++r) {
+        const int2 lo = *reinterpret_cast<const int2*>(lows + 8 * r + 2 * q), hi = *reinterpret_cast<const int2*>(highs + 8 * r + 2 * q);
 #pragma unroll
-        for (int r = 0; r < kGroups; ++r) {
-          const int2 lo = *reinterpret_cast<const int2*>(lows + 8 * (group0 + r) + 2 * q);
-          const int2 hi = *reinterpret_cast<const int2*>(highs + 8 * (group0 + r) + 2 * q);
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float v0, v1;
-            unpack2(x[n][r][c], v0, v1);
-            x[n][r][c] = pack2(here && j + c >= lo.x && j + c < hi.x ? v0 : -INFINITY, here && j + c >= lo.y && j + c < hi.y ? v1 : -INFINITY);
-          }
+        for (int c = 0; c < 2; ++c) {
+          const int at = j + tok + c;
+          float v0, v1;
+          unpack2(x[r][c], v0, v1);
+          x[r][c] = pack2(here && at >= lo.x && at < hi.x ? v0 : -INFINITY, here && at >= lo.y && at < hi.y ? v1 : -INFINITY);
         }
       }
     }
+    // the keys are read: the next ones into their slot
+    fence_proxy_async_smem();
+    __syncwarp();
+    send_keys(stage);
 
     // ---- weights, as if the references held
     uint8_t* const weights = ps + turn * (S::kRows * kPStride);
-    f32x2 more[kGroups];
-    auto weigh = [&]() {
-      float far = -INFINITY;
+    const float lv[2] = {log2_above(vs.x), log2_above(vs.y)};
+    f32x2 part[NR];
+    for (bool again = false;; again = true) {
+      float most[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int r = 0; r < kGroups; ++r) more[r] = both(0.0f);
+      for (int r = 0; r < NR; ++r) {
+        const ulonglong2 ref = *reinterpret_cast<const ulonglong2*>(refs + 4 * r + q);
+        float w[4];
+        unpack2(sub2(add2(x[r][0], ref.x), ref.y), w[0], w[1]);
+        unpack2(sub2(add2(x[r][1], ref.x), ref.y), w[2], w[3]);
+        most[0] = fmaxf(most[0], fmaxf(w[0], w[1]));
+        most[1] = fmaxf(most[1], fmaxf(w[2], w[3]));
 #pragma unroll
-      for (int n = 0; n < kOwn; ++n) {
-        float most[2] = {-INFINITY, -INFINITY};
+        for (int k = 0; k < 4; ++k) w[k] = ex2(w[k]);
+        const f32x2 p0 = pack2(w[0], w[1]), p1 = pack2(w[2], w[3]);
+        part[r] = add2(p0, p1);
+        unpack2(mul2(p0, both(vs.x)), w[0], w[1]);
+        unpack2(mul2(p1, both(vs.y)), w[2], w[3]);
+        if (!all_seen) {      // hidden weights 0, whatever the scale holds
+          float v[4];
+          unpack2(x[r][0], v[0], v[1]);
+          unpack2(x[r][1], v[2], v[3]);
 #pragma unroll
-        for (int r = 0; r < kGroups; ++r) {
-          float w[4];
-          unpack2(sub2(add2(x[n][r][0], top[r]), low[r]), w[0], w[1]);
-          unpack2(sub2(add2(x[n][r][1], top[r]), low[r]), w[2], w[3]);
-          most[0] = fmaxf(most[0], fmaxf(w[0], w[1]));
-          most[1] = fmaxf(most[1], fmaxf(w[2], w[3]));
-#pragma unroll
-          for (int k = 0; k < 4; ++k) w[k] = ex2(w[k]);
-          const f32x2 p0 = pack2(w[0], w[1]), p1 = pack2(w[2], w[3]);
-          more[r] = add2(more[r], add2(p0, p1));
-          unpack2(mul2(p0, both(vs[n].x)), w[0], w[1]);
-          unpack2(mul2(p1, both(vs[n].y)), w[2], w[3]);
-          if (!all_seen) {      // hidden weights 0, whatever the scale holds
-            float v[4];
-            unpack2(x[n][r][0], v[0], v[1]);
-            unpack2(x[n][r][1], v[2], v[3]);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] = v[k] == -INFINITY ? 0.0f : w[k];
-          }
-          uint8_t* const to = weights + (8 * (group0 + r) + 2 * q) * kPStride + 2 * (16 * (own + n) + tok);
-          *reinterpret_cast<__half2*>(to) = __floats2half2_rn(w[0], w[2]);
-          *reinterpret_cast<__half2*>(to + kPStride) = __floats2half2_rn(w[1], w[3]);
+          for (int k = 0; k < 4; ++k) w[k] = v[k] == -INFINITY ? 0.0f : w[k];
         }
-        far = fmaxf(far, fmaxf(most[0] + log2_above(vs[n].x), most[1] + log2_above(vs[n].y)));
+        uint8_t* const to = weights + (8 * r + 2 * q) * kPStride + 2 * (16 * warp + tok);
+        *reinterpret_cast<__half2*>(to) = __floats2half2_rn(w[0], w[2]);
+        *reinterpret_cast<__half2*>(to + kPStride) = __floats2half2_rn(w[1], w[3]);
       }
-      return far;
-    };
-    // (behind this barrier all warps are done with the tile before this one, so its stage is free)
-    const bool raise = __syncthreads_or(weigh() > kMostWeight) != 0;
-    if (warp == 0 && refill >= 0) {
+      // (behind this barrier all warps are done with the values of the tile before this one)
+      const bool raise = __syncthreads_or(fmaxf(most[0] + lv[0], most[1] + lv[1]) > kMostWeight) != 0;
+      if (again) break;
       fence_proxy_async_smem();
-      fetch(refill);
-    }
-    if (raise) {
+      send_values(stage == 0 ? kStages - 1 : stage - 1);
+      if (!raise) break;
       // References of the rows concerned up, what stands under them down.  Each
-      // warp's largest score and, over that, weight of a row; then the warps'.
+      // warp's largest score and, over that, weight of a row; then the warps',
+      // lane by row.
 #pragma unroll
-      for (int r = 0; r < kGroups; ++r) {
-        float most[2] = {-INFINITY, -INFINITY}, over[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-        for (int n = 0; n < kOwn; ++n) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float v[2];
-            unpack2(x[n][r][c], v[0], v[1]);
-            most[0] = fmaxf(most[0], v[0]);
-            most[1] = fmaxf(most[1], v[1]);
-          }
-        }
+      for (int r = 0; r < NR; ++r) {
+        float v[4];
+        unpack2(x[r][0], v[0], v[1]);
+        unpack2(x[r][1], v[2], v[3]);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          most[k] = max_over_g(most[k]);
-          if (most[k] == -INFINITY) most[k] = kNone;
-        }
-#pragma unroll
-        for (int n = 0; n < kOwn; ++n) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float v[2];
-            unpack2(x[n][r][c], v[0], v[1]);
-            const float lv = log2_above(c == 0 ? vs[n].x : vs[n].y);
-            over[0] = fmaxf(over[0], v[0] - most[0] + lv);
-            over[1] = fmaxf(over[1], v[1] - most[1] + lv);
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          over[k] = max_over_g(over[k]);
-          if (g == 0) pairs[warp / S::kParts * S::kRows + 8 * (group0 + r) + 2 * q + k] = make_float2(most[k], over[k]);
+          float top = max_over_g(fmaxf(v[k], v[2 + k]));
+          if (top == -INFINITY) top = kNone;
+          const float over = max_over_g(fmaxf(v[k] - top + lv[0], v[2 + k] - top + lv[1]));
+          if (g == 0) pairs[warp * S::kRows + 8 * r + 2 * q + k] = make_float2(top, over);
         }
       }
       __syncthreads();
+      if (warp == 0 && lane < S::kRows) {
+        float2 of[kAttnWarps];
+        float top = kNone, over = -INFINITY;
 #pragma unroll
-      for (int r = 0; r < kGroups; ++r) {
-        float m[2], c[2], keep[2];
-        unpack2(top[r], m[0], m[1]);
-        unpack2(low[r], c[0], c[1]);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int row = 8 * (group0 + r) + 2 * q + k;
-          float2 of[S::kTokenWarps];
-          float most = kNone, over = -INFINITY;
-#pragma unroll
-          for (int w = 0; w < S::kTokenWarps; ++w) {
-            of[w] = pairs[w * S::kRows + row];
-            most = fmaxf(most, of[w].x);
-          }
-#pragma unroll
-          for (int w = 0; w < S::kTokenWarps; ++w) over = fmaxf(over, (of[w].x - most) + of[w].y);
-          const bool up = (most + m[k]) + (over - c[k]) > kMostWeight;
-          over -= kNewWeight;
-          keep[k] = up ? ex2((c[k] - over) - (most + m[k])) : 1.0f;
-          if (up) {
-            m[k] = -most;
-            c[k] = over;
-          }
-          if (warp < S::kParts && g == 0) keeps[row] = keep[k];
+        for (int w = 0; w < kAttnWarps; ++w) {
+          of[w] = pairs[w * S::kRows + lane];
+          top = fmaxf(top, of[w].x);
         }
-        top[r] = pack2(m[0], m[1]);
-        low[r] = pack2(c[0], c[1]);
-        sum[r] = mul2(sum[r], pack2(keep[0], keep[1]));
+#pragma unroll
+        for (int w = 0; w < kAttnWarps; ++w) over = fmaxf(over, (of[w].x - top) + of[w].y);
+        float* const ref = reinterpret_cast<float*>(refs + (lane >> 1)) + (lane & 1);
+        const float m = ref[0], c = ref[2];
+        const bool up = (top + m) + (over - c) > kLiftWeight;
+        over -= kNewWeight;
+        keeps[lane] = up ? ex2((c - over) - (top + m)) : 1.0f;
+        if (up) {
+          ref[0] = -top;
+          ref[2] = over;
+        }
       }
-      (void)weigh();
       __syncthreads();
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
-        const float2 k = *reinterpret_cast<const float2*>(keeps + 8 * r + 2 * q);
+        const float2 keep = *reinterpret_cast<const float2*>(keeps + 8 * r + 2 * q);
+        sum[r] = mul2(sum[r], pack2(keep.x, keep.y));
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          o[0][r][c] *= (c & 1) ? k.y : k.x;
-          o[1][r][c] *= (c & 1) ? k.y : k.x;
+        for (int k = 0; k < 4; ++k) {
+          o[0][r][k] *= (k & 1) ? keep.y : keep.x;
+          o[1][r][k] *= (k & 1) ? keep.y : keep.x;
         }
       }
     }
 #pragma unroll
-    for (int r = 0; r < kGroups; ++r) sum[r] = add2(sum[r], more[r]);
+    for (int r = 0; r < NR; ++r) sum[r] = add2(sum[r], part[r]);
     // ---- outputs
+    ok = __all_sync(kAll, ok && mbar_wait(smem_u32(&full_v[stage]), phase, ctx, 92));
+    const uint8_t* const tile_values = smem + S::kVRing + stage * kTileBlocks * kVCodes;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int in_tile = 4 * half + k;
-      const uint8_t* const v = ring + in_tile * kCacheBlock + kVCodes + 4 * q * kHeadDim + 32 * (quarter ^ q) + 4 * g;
+      const uint8_t* const v = tile_values + in_tile * kVCodes + 4 * q * kHeadDim + 32 * (quarter ^ q) + 4 * g;
       uint32_t w[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) w[e] = *reinterpret_cast<const uint32_t*>(v + e * kHeadDim);
@@ -668,24 +671,23 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
       }
     }
     turn ^= 1;
+    i += kTileBlocks;
+    j0 += kTile;
 
-    if (flags & kLast) {
+    if (i >= n) {
       // ---- the piece is done: sums over the warps, outputs of the two halves
 #pragma unroll
-      for (int r = 0; r < kGroups; ++r) {
-        float l[2], m[2], c[2];
+      for (int r = 0; r < NR; ++r) {
+        float l[2];
         unpack2(sum[r], l[0], l[1]);
-        unpack2(top[r], m[0], m[1]);
-        unpack2(low[r], c[0], c[1]);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-#pragma unroll
-          for (int d = 4; d <= 16; d <<= 1) l[k] += __shfl_xor_sync(kAll, l[k], d);
-          const int row = 8 * (group0 + r) + 2 * q + k;
-          if (g == 0) pairs[warp / S::kParts * S::kRows + row].x = l[k];
-          if (g == 0 && warp < S::kParts) refs[row] = make_float2(-m[k], c[k]);
+        for (int d = 4; d <= 16; d <<= 1) {
+          l[0] += __shfl_xor_sync(kAll, l[0], d);
+          l[1] += __shfl_xor_sync(kAll, l[1], d);
         }
+        if (g == 0) *reinterpret_cast<float4*>(pairs + warp * S::kRows + 8 * r + 2 * q) = make_float4(l[0], 0.0f, l[1], 0.0f);
       }
+      __syncthreads();      // the weights are read
       if (half == 1) {
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
@@ -697,43 +699,48 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
       }
       __syncthreads();
       if (half == 0) {
-        const int h = tile.seg / p.row_tiles, row0 = (tile.seg - h * p.row_tiles) * S::kRows, fresh = tile.fresh;
-        const int64_t part = (2LL * blockIdx.x + (tile.cut > 0 ? 0 : 1)) * S::kRows;
+        const bool whole = piece.whole;
+        float l = 0.0f;       // lane by row
+        if (lane < S::kRows) {
+#pragma unroll
+          for (int w = 0; w < kAttnWarps; ++w) l += pairs[w * S::kRows + lane].x;
+        }
+        const int64_t part = (2LL * blockIdx.x + (piece.cut > 0 ? 0 : 1)) * S::kRows;
+        if (!whole && warp == 0 && lane < S::kRows) {
+          const float* const ref = reinterpret_cast<const float*>(refs + (lane >> 1)) + (lane & 1);
+          p.part_share[part + lane] = Share{-ref[0], ref[2], l, 0.0f};
+        }
+        const float back = !whole ? 1.0f : l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);      // 0: no token seen
+        uint16_t* const out = a.out + piece.b * a.T * a.q_heads * kHeadDim + 32 * quarter + 4 * g;
+        float* const part_o = p.part_o + part * kHeadDim + 32 * quarter + 4 * g;
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const int in_tile = 8 * r + 2 * q + c, row = row0 + in_tile, t = row / p.G;
-            if (row >= rows || t >= fresh) continue;
-            float l = 0.0f;
-#pragma unroll
-            for (int w = 0; w < S::kTokenWarps; ++w) l += pairs[w * S::kRows + in_tile].x;
-            float4 v = *reinterpret_cast<const float4*>(os + in_tile * kHeadDim + 32 * quarter + 4 * g);
-            v = make_float4(o[0][r][c] + v.x, o[0][r][2 + c] + v.y, o[1][r][c] + v.z, o[1][r][2 + c] + v.w);
-            const int d = 32 * quarter + 4 * g;
-            if (flags & kWhole) {
-              const float back = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);      // 0: no token seen
-              *reinterpret_cast<uint2*>(a.out + ((tile.b * a.T + t) * a.q_heads + h * p.G + (row - t * p.G)) * kHeadDim + d) =
-                  make_uint2(bf16x2_rn(v.x * back, v.y * back), bf16x2_rn(v.z * back, v.w * back));
-            } else {
-              *reinterpret_cast<float4*>(p.part_o + (part + in_tile) * kHeadDim + d) = v;
-              if (d == 0) p.part_share[part + in_tile] = Share{refs[in_tile].x, refs[in_tile].y, l, 0.0f};
-            }
+            const int in_tile = 8 * r + 2 * q + c, to = tos[in_tile];
+            const float f = __shfl_sync(kAll, back, in_tile);
+            const float4 v = *reinterpret_cast<const float4*>(os + in_tile * kHeadDim + 32 * quarter + 4 * g);
+            const float4 sums = make_float4((o[0][r][c] + v.x) * f, (o[0][r][2 + c] + v.y) * f, (o[1][r][c] + v.z) * f,
+                                            (o[1][r][2 + c] + v.w) * f);
+            if (to >= 0 && whole)
+              *reinterpret_cast<uint2*>(out + static_cast<int64_t>(to) * kHeadDim) =
+                  make_uint2(bf16x2_rn(sums.x, sums.y), bf16x2_rn(sums.z, sums.w));
+            if (to >= 0 && !whole) *reinterpret_cast<float4*>(part_o + in_tile * kHeadDim) = sums;
           }
         }
       }
-      if (flags & kFinal) break;
+      if (piece.final) break;
+      get = (get + 1) % kPieces;
+      __syncthreads();      // the rows' places are read
+    }
+    if (++stage == kStages) {
+      stage = 0;
+      phase ^= 1;
     }
   }
-  if (!ok) {      // the copies land before the block ends
-    int never = 0;
-    const WaitCtx drain{p.err, &never, kWaitLimitNs};
-    for (int i = 0; i < kStages; ++i) {
-      (void)mbar_wait(smem_u32(&full[stage]), phase, drain, 92);
-      if (--stage < 0) {
-        stage = kStages - 1;
-        phase ^= 1;
-      }
+  if (!ok) {      // what copies are still on their way land before the block ends
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < kWaitLimitNs / 100) {
     }
   }
 }
@@ -821,8 +828,8 @@ __global__ void __launch_bounds__(128) join_segments_kernel(const AttnParams p, 
   if (n == 0 || row >= static_cast<int>(a.T) * p.G || t >= seq.fresh) return;
   const int64_t share = share_of(total * segs, grid);
   const int64_t s0 = before * segs + static_cast<int64_t>(seg) * n;
-  const int64_t first = s0 / share;
-  const int parts = static_cast<int>((s0 + n - 1) / share - first) + 1;
+  const int first = share_at(s0, share);
+  const int parts = share_at(s0 + n - 1, share) - first + 1;
   if (parts == 1) return;       // written already
   Joined j;
   j.add_parts(p, first, parts, warp, 4, tile_rows, in_tile, lane);

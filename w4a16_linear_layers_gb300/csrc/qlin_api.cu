@@ -261,7 +261,7 @@ constexpr int64_t kMaxTokens = 1LL << 30;   // of a sequence
 
 bool cache_shape(int64_t pages, int64_t kv_heads, int64_t page_size) {
   return pages >= 1 && pages <= kMaxDim && kv_heads >= 1 && kv_heads <= kMaxHeads && page_size >= 16 &&
-         page_size <= kMaxPageSize && page_size % 16 == 0;
+         page_size <= kMaxPageSize && page_size % 16 == 0 && kv_heads * (page_size / 16) <= kMaxDim / pages;
 }
 
 bool batch_shape(int64_t B, int64_t T) { return B >= 0 && T >= 0 && B <= kMaxDim && T <= kMaxDim && B * T <= kMaxDim; }
@@ -570,9 +570,7 @@ qlin_status_t qlin_adjust_logits_f32(const float* logits, int64_t M, int64_t V,
 
 size_t qlin_kv_cache_bytes(int64_t pages, int64_t kv_heads, int64_t page_size) {
   if (!cache_shape(pages, kv_heads, page_size)) return 0;
-  // in 64 bits: at most 2^31 * 2^16 * 2^12 * 2^13 would not fit, such a cache does not either
-  const unsigned __int128 n = static_cast<unsigned __int128>(pages) * kv_heads * (page_size / 16) * kCacheBlock;
-  return n > static_cast<unsigned __int128>(INT64_MAX) ? 0 : static_cast<size_t>(n);
+  return static_cast<size_t>(pages * kv_heads * (page_size / 16)) * kCacheBlock;
 }
 
 qlin_status_t qlin_kv_write_i8(const uint16_t* qkv, int64_t B, int64_t T, int64_t q_heads, int64_t kv_heads,
