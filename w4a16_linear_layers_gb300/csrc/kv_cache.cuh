@@ -17,15 +17,16 @@ constexpr int kVScales = 4160;
 // Offset, in a token's 128 codes, of component d (its 32-byte quarter moved).
 __device__ __forceinline__ int code_place(int r, int d) { return ((((d >> 5) ^ (r >> 2)) & 3) << 5) + (d & 31); }
 
-// A sequence's tokens in the cache, and how many of them are new.
+// A sequence's tokens in the cache, and how many of them are new.  (Read from L2:
+// the kernel that joins the attention's parts reads them before its wait.)
 struct SeqLen {
   int len, fresh;
 };
 __device__ __forceinline__ SeqLen seq_len(const CacheArgs& c, int64_t b, int64_t T) {
   SeqLen s;
-  s.len = min(max(__ldg(c.total_len + b), 0), static_cast<int>(c.max_pages * c.page_size));
+  s.len = min(max(__ldcg(c.total_len + b), 0), static_cast<int>(c.max_pages * c.page_size));
   const int most = static_cast<int>(T < s.len ? T : s.len);
-  s.fresh = c.new_len == nullptr ? most : min(max(__ldg(c.new_len + b), 0), most);
+  s.fresh = c.new_len == nullptr ? most : min(max(__ldcg(c.new_len + b), 0), most);
   return s;
 }
 

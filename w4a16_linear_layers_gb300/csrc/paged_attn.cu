@@ -98,6 +98,7 @@ struct AttnParams {
   PagedAttnArgs a;
   int G;               // query heads of a key/value head
   int row_tiles;       // of a sequence's T * G rows
+  bool whole_parts;    // few segments: no share holds parts of two
   int* err;
   // workspace: where the cut segments are, then their parts
   int32_t* cuts;       // [grid][4]: segment, its first and last share, sequence; segment -1: none
@@ -129,6 +130,60 @@ __device__ __forceinline__ int64_t share_of(int64_t total, int grid) {
 __device__ __forceinline__ int share_at(int64_t at, int64_t share) {
   return (at | share) < 1LL << 31 ? static_cast<int>(at) / static_cast<int>(share) : static_cast<int>(at / share);
 }
+
+// Few segments, an eighth of the thread blocks or less (64 sequences at most):
+// each gets thread blocks of its own, shares of equal size but its last.
+// Segments of n_s blocks cut into ceil(n_s / share) parts are fewer parts than
+// sum n_s / share + segments, so share = sum n_s / (grid - segments) is enough.
+// (A piece's beginning and end take 2 to 3 us.)  Each warp finds this by itself.
+struct Parts {
+  int64_t share;
+  int n[2], parts[2], before[2];      // of sequences lane and lane + 32; parts of the ones before
+
+  __device__ __forceinline__ Parts(const AttnParams& p, int grid, int lane) {
+    const int segs = p.row_tiles * static_cast<int>(p.a.c.kv_heads);
+    const int B = static_cast<int>(p.a.c.B);
+    int64_t total = 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      n[k] = lane + 32 * k < B ? span_of(p.a, seq_len(p.a.c, lane + 32 * k, p.a.T)).count : 0;
+      total += n[k];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
+    share = share_of(total * segs, grid - B * segs);
+    int all = 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      parts[k] = n[k] == 0 ? 0 : share_at(n[k] - 1, share) + 1;
+      int incl = parts[k];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(kAll, incl, o);
+        if (lane >= o) incl += v;
+      }
+      before[k] = all + incl - parts[k];
+      all += __shfl_sync(kAll, incl, 31);
+    }
+  }
+  // The sequence, segment and part of thread block c; false: none
+  __device__ __forceinline__ bool find(int c, int segs, int lane, int64_t& b, int& seg, int& part) const {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int in_b = c - before[k] * segs;
+      const uint32_t who = __ballot_sync(kAll, in_b >= 0 && in_b < parts[k] * segs);
+      if (who != 0) {
+        const int src = __ffs(who) - 1;
+        const int of_b = __shfl_sync(kAll, parts[k], src), at = __shfl_sync(kAll, in_b, src);
+        b = src + 32 * k;
+        seg = at / of_b;
+        part = at - seg * of_b;
+        return true;
+      }
+    }
+    return false;
+  }
+};
 
 // A walk through a share: its pieces (parts of segments), in order.
 struct Walk {
@@ -211,7 +266,6 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
   __shared__ Walk start;
   __shared__ int abort_flag;
   __shared__ int64_t warp_sums[kAttnWarps];
-  __shared__ int64_t before_b;
   const PagedAttnArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int segs = p.row_tiles * static_cast<int>(a.c.kv_heads);
@@ -224,73 +278,86 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
     }
     fence_barrier_init();
   }
-  grid_dep_launch();
   grid_dep_wait();
+  grid_dep_launch();      // (the joining kernel may read what this one's predecessors wrote at once)
 
-  // ---- this block's share.  Blocks of 16 of 256 sequences at a time: their
-  // running sum, which places the share, and what they are in all.
-  auto chunk = [&](int64_t b0, int& n, int64_t& incl, int64_t& all) {
-    const int64_t b = b0 + tid;
-    n = b < a.c.B ? span_of(a, seq_len(a.c, b, a.T)).count : 0;
-    uint32_t in_warp = static_cast<uint32_t>(n);      // 32 spans of 2^26 blocks at most
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t v = __shfl_up_sync(kAll, in_warp, o);
-      if (lane >= o) in_warp += v;
-    }
-    if (lane == 31) warp_sums[warp] = in_warp;
-    incl = in_warp;
-    __syncthreads();
-    all = 0;
-#pragma unroll
-    for (int w = 0; w < kAttnWarps; ++w) {
-      if (w < warp) incl += warp_sums[w];
-      all += warp_sums[w];
-    }
-    __syncthreads();
-  };
-  int n0;
-  int64_t incl, all;
-  chunk(0, n0, incl, all);
-  int64_t total = all;
-  for (int64_t b0 = kAttnThreads; b0 < a.c.B; b0 += kAttnThreads) {
-    int n;
-    int64_t i, s;
-    chunk(b0, n, i, s);
-    total += s;
-  }
-  total *= segs;
-  const int64_t share = share_of(total, gridDim.x);
-  const int64_t at = blockIdx.x * share;
-  if (at >= total) {
-    if (tid == 0) p.cuts[4 * blockIdx.x] = -1;
-    return;
-  }
-  for (int64_t b0 = 0, before = 0;; b0 += kAttnThreads) {
-    if (b0 > 0) chunk(b0, n0, incl, all);
-    const int64_t from = (before + incl - n0) * segs;
-    if (n0 > 0 && from <= at && at < from + static_cast<int64_t>(n0) * segs) {
-      start.b = b0 + tid;
+  // ---- this block's share
+  if (p.whole_parts) {
+    const Parts parts(p, gridDim.x, lane);
+    int64_t b;
+    int seg, part;
+    if (!parts.find(blockIdx.x, segs, lane, b, seg, part)) return;
+    if (tid == 0) {
+      start.b = b;
       start.segs = segs;
-      const int64_t in_b = at - from;
-      start.seg = in_b < 1LL << 31 ? static_cast<int>(in_b) / n0 : static_cast<int>(in_b / n0);
-      start.off = static_cast<int>(in_b - static_cast<int64_t>(start.seg) * n0);
-      start.left = total - at < share ? total - at : share;
+      start.seg = seg;
+      start.off = part * parts.share;
       start.load(a);
-      before_b = from;
+      const int rest = start.span.count - start.off;
+      start.left = rest < parts.share ? rest : parts.share;
     }
-    before += all;
-    if (before * segs > at) break;
-  }
-  __syncthreads();
-
-  if (tid == 0) {
-    // the first boundary inside a segment announces it
-    const int64_t s0 = before_b + static_cast<int64_t>(start.seg) * start.span.count;
-    const int64_t first = share_at(s0, share), last = share_at(s0 + start.span.count - 1, share);
-    const bool cut = start.off > 0 && first == blockIdx.x - 1;
-    *reinterpret_cast<int4*>(p.cuts + 4 * blockIdx.x) =
-        make_int4(cut ? start.seg : -1, static_cast<int>(first), static_cast<int>(last), static_cast<int>(start.b));
+    __syncthreads();
+  } else {
+    // Blocks of 16 of 256 sequences at a time: their running sum, which places
+    // the share, and what they are in all.
+    auto chunk = [&](int64_t b0, int& n, int64_t& incl, int64_t& all) {
+      const int64_t b = b0 + tid;
+      n = b < a.c.B ? span_of(a, seq_len(a.c, b, a.T)).count : 0;
+      uint32_t in_warp = static_cast<uint32_t>(n);      // 32 spans of 2^26 blocks at most
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(kAll, in_warp, o);
+        if (lane >= o) in_warp += v;
+      }
+      if (lane == 31) warp_sums[warp] = in_warp;
+      incl = in_warp;
+      __syncthreads();
+      all = 0;
+#pragma unroll
+      for (int w = 0; w < kAttnWarps; ++w) {
+        if (w < warp) incl += warp_sums[w];
+        all += warp_sums[w];
+      }
+      __syncthreads();
+    };
+    int n0;
+    int64_t incl, all;
+    chunk(0, n0, incl, all);
+    int64_t total = all;
+    for (int64_t b0 = kAttnThreads; b0 < a.c.B; b0 += kAttnThreads) {
+      int n;
+      int64_t i, s;
+      chunk(b0, n, i, s);
+      total += s;
+    }
+    total *= segs;
+    const int64_t share = share_of(total, gridDim.x);
+    const int64_t at = blockIdx.x * share;
+    if (at >= total) {
+      if (tid == 0) p.cuts[4 * blockIdx.x] = -1;
+      return;
+    }
+    for (int64_t b0 = 0, before = 0;; b0 += kAttnThreads) {
+      if (b0 > 0) chunk(b0, n0, incl, all);
+      const int64_t from = (before + incl - n0) * segs;
+      if (n0 > 0 && from <= at && at < from + static_cast<int64_t>(n0) * segs) {
+        start.b = b0 + tid;
+        start.segs = segs;
+        const int64_t in_b = at - from;
+        start.seg = in_b < 1LL << 31 ? static_cast<int>(in_b) / n0 : static_cast<int>(in_b / n0);
+        start.off = static_cast<int>(in_b - static_cast<int64_t>(start.seg) * n0);
+        start.left = total - at < share ? total - at : share;
+        start.load(a);
+        // the first boundary inside a segment announces it
+        const int64_t s0 = from + static_cast<int64_t>(start.seg) * n0;
+        const int first = share_at(s0, share), last = share_at(s0 + n0 - 1, share);
+        *reinterpret_cast<int4*>(p.cuts + 4 * blockIdx.x) =
+            make_int4(start.off > 0 && first == static_cast<int>(blockIdx.x) - 1 ? start.seg : -1, first, last, static_cast<int>(start.b));
+      }
+      before += all;
+      if (before * segs > at) break;
+    }
+    __syncthreads();
   }
 
   // A copy that does not come ends the work, not the walk through the tiles, in
@@ -419,7 +486,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
   int i = 0, n = 0, j0 = 0;          // the tile's first block of the piece, the piece's blocks, the tile's first token
   for (;;) {
     const Piece& piece = pieces[warp][get];
-    if (i >= n) {
+    const bool first = i >= n;
+    if (first) {
       // q of the piece's rows, what they see
       __syncwarp();
       i = 0;
@@ -564,39 +632,45 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
     uint8_t* const weights = ps + turn * (S::kRows * kPStride);
     const float lv[2] = {log2_above(vs.x), log2_above(vs.y)};
     f32x2 part[NR];
-    for (bool again = false;; again = true) {
-      float most[2] = {-INFINITY, -INFINITY};
+    bool sent = false;
+    for (bool raised = false;; raised = true) {
+      // (a piece's first tile has no references yet)
+      if (raised || !first) {
+        float most[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        const ulonglong2 ref = *reinterpret_cast<const ulonglong2*>(refs + 4 * r + q);
-        float w[4];
-        unpack2(sub2(add2(x[r][0], ref.x), ref.y), w[0], w[1]);
-        unpack2(sub2(add2(x[r][1], ref.x), ref.y), w[2], w[3]);
-        most[0] = fmaxf(most[0], fmaxf(w[0], w[1]));
-        most[1] = fmaxf(most[1], fmaxf(w[2], w[3]));
+        for (int r = 0; r < NR; ++r) {
+          const ulonglong2 ref = *reinterpret_cast<const ulonglong2*>(refs + 4 * r + q);
+          float w[4];
+          unpack2(sub2(add2(x[r][0], ref.x), ref.y), w[0], w[1]);
+          unpack2(sub2(add2(x[r][1], ref.x), ref.y), w[2], w[3]);
+          most[0] = fmaxf(most[0], fmaxf(w[0], w[1]));
+          most[1] = fmaxf(most[1], fmaxf(w[2], w[3]));
 #pragma unroll
-        for (int k = 0; k < 4; ++k) w[k] = ex2(w[k]);
-        const f32x2 p0 = pack2(w[0], w[1]), p1 = pack2(w[2], w[3]);
-        part[r] = add2(p0, p1);
-        unpack2(mul2(p0, both(vs.x)), w[0], w[1]);
-        unpack2(mul2(p1, both(vs.y)), w[2], w[3]);
-        if (!all_seen) {      // hidden weights 0, whatever the scale holds
-          float v[4];
-          unpack2(x[r][0], v[0], v[1]);
-          unpack2(x[r][1], v[2], v[3]);
+          for (int k = 0; k < 4; ++k) w[k] = ex2(w[k]);
+          const f32x2 p0 = pack2(w[0], w[1]), p1 = pack2(w[2], w[3]);
+          part[r] = add2(p0, p1);
+          unpack2(mul2(p0, both(vs.x)), w[0], w[1]);
+          unpack2(mul2(p1, both(vs.y)), w[2], w[3]);
+          if (!all_seen) {      // hidden weights 0, whatever the scale holds
+            float v[4];
+            unpack2(x[r][0], v[0], v[1]);
+            unpack2(x[r][1], v[2], v[3]);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) w[k] = v[k] == -INFINITY ? 0.0f : w[k];
+            for (int k = 0; k < 4; ++k) w[k] = v[k] == -INFINITY ? 0.0f : w[k];
+          }
+          uint8_t* const to = weights + (8 * r + 2 * q) * kPStride + 2 * (16 * warp + tok);
+          *reinterpret_cast<__half2*>(to) = __floats2half2_rn(w[0], w[2]);
+          *reinterpret_cast<__half2*>(to + kPStride) = __floats2half2_rn(w[1], w[3]);
         }
-        uint8_t* const to = weights + (8 * r + 2 * q) * kPStride + 2 * (16 * warp + tok);
-        *reinterpret_cast<__half2*>(to) = __floats2half2_rn(w[0], w[2]);
-        *reinterpret_cast<__half2*>(to + kPStride) = __floats2half2_rn(w[1], w[3]);
+        // (behind this barrier all warps are done with the values of the tile before this one)
+        const bool raise = __syncthreads_or(fmaxf(most[0] + lv[0], most[1] + lv[1]) > kMostWeight) != 0;
+        if (!sent) {
+          fence_proxy_async_smem();
+          send_values(stage == 0 ? kStages - 1 : stage - 1);
+          sent = true;
+        }
+        if (raised || !raise) break;
       }
-      // (behind this barrier all warps are done with the values of the tile before this one)
-      const bool raise = __syncthreads_or(fmaxf(most[0] + lv[0], most[1] + lv[1]) > kMostWeight) != 0;
-      if (again) break;
-      fence_proxy_async_smem();
-      send_values(stage == 0 ? kStages - 1 : stage - 1);
-      if (!raise) break;
       // References of the rows concerned up, what stands under them down.  Each
       // warp's largest score and, over that, weight of a row; then the warps',
       // lane by row.
@@ -614,6 +688,11 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
         }
       }
       __syncthreads();
+      if (!sent) {      // a first tile's: the barrier was this one
+        fence_proxy_async_smem();
+        send_values(stage == 0 ? kStages - 1 : stage - 1);
+        sent = true;
+      }
       if (warp == 0 && lane < S::kRows) {
         float2 of[kAttnWarps];
         float top = kNone, over = -INFINITY;
@@ -760,7 +839,7 @@ struct Joined {
   // parts k, k + step, .. of those that shares first .. first + parts - 1 left
   __device__ __forceinline__ void add_parts(const AttnParams& p, int64_t first, int parts, int k, int step, int tile_rows, int in_tile,
                                             int lane) {
-    constexpr int kAhead = 4;
+    constexpr int kAhead = 5;
     for (; k < parts; k += kAhead * step) {
       float4 part[kAhead], v[kAhead];
 #pragma unroll
@@ -786,8 +865,8 @@ struct Joined {
 // The parts of the cut segment that share x announces: a warp takes a row at a time.
 __global__ void __launch_bounds__(256) join_cuts_kernel(const AttnParams p, int tile_rows) {
   const int lane = threadIdx.x & 31;
-  grid_dep_launch();
   grid_dep_wait();
+  grid_dep_launch();
   const int4 cut = __ldg(reinterpret_cast<const int4*>(p.cuts + 4 * (blockIdx.x + 1)));
   if (cut.x < 0) return;
   const int fresh = seq_len(p.a.c, cut.w, p.a.T).fresh;
@@ -800,45 +879,34 @@ __global__ void __launch_bounds__(256) join_cuts_kernel(const AttnParams p, int 
   }
 }
 
-// The same where there are few segments, of many parts each: a block takes row y
-// of segment x, and finds its parts from the lengths.
-__global__ void __launch_bounds__(128) join_segments_kernel(const AttnParams p, int tile_rows, int grid) {
-  __shared__ float4 acc[4][32];
-  __shared__ Share of[4];
+// The same where there are few segments, of up to grid / segments parts each: a
+// block takes row y of segment x, its warps parts.
+constexpr int kJoinWarps = 8;
+__global__ void __launch_bounds__(32 * kJoinWarps) join_segments_kernel(const AttnParams p, int tile_rows, int grid) {
+  __shared__ float4 acc[kJoinWarps][32];
+  __shared__ Share of[kJoinWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const PagedAttnArgs& a = p.a;
-  grid_dep_launch();
-  grid_dep_wait();
+  // The lengths are older than the kernel in front, which starts this one when
+  // its own predecessors are done.
+  const Parts parts(p, grid, lane);
   const int segs = p.row_tiles * static_cast<int>(a.c.kv_heads);
   const int b = blockIdx.x / segs, seg = blockIdx.x % segs, in_tile = blockIdx.y;
-  int64_t total = 0, before = 0;
-  for (int i = lane; i < static_cast<int>(a.c.B); i += 32) {
-    const int n = span_of(a, seq_len(a.c, i, a.T)).count;
-    total += n;
-    if (i < b) before += n;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    total += __shfl_xor_sync(kAll, total, o);
-    before += __shfl_xor_sync(kAll, before, o);
-  }
-  const SeqLen seq = seq_len(a.c, b, a.T);
-  const int n = span_of(a, seq).count;
+  const int n = __shfl_sync(kAll, b < 32 ? parts.parts[0] : parts.parts[1], b & 31);
+  const int first = __shfl_sync(kAll, b < 32 ? parts.before[0] : parts.before[1], b & 31) * segs + seg * n;
   const int row = seg % p.row_tiles * tile_rows + in_tile, t = row / p.G;
-  if (n == 0 || row >= static_cast<int>(a.T) * p.G || t >= seq.fresh) return;
-  const int64_t share = share_of(total * segs, grid);
-  const int64_t s0 = before * segs + static_cast<int64_t>(seg) * n;
-  const int first = share_at(s0, share);
-  const int parts = share_at(s0 + n - 1, share) - first + 1;
-  if (parts == 1) return;       // written already
+  const bool none = n <= 1 || row >= static_cast<int>(a.T) * p.G || t >= seq_len(a.c, b, a.T).fresh;      // one part: written already
+  grid_dep_wait();
+  grid_dep_launch();
+  if (none) return;
   Joined j;
-  j.add_parts(p, first, parts, warp, 4, tile_rows, in_tile, lane);
+  j.add_parts(p, first, n, warp, kJoinWarps, tile_rows, in_tile, lane);
   acc[warp][lane] = j.o;
   if (lane == 0) of[warp] = j.all;
   __syncthreads();
   if (warp != 0) return;
 #pragma unroll
-  for (int w = 1; w < 4; ++w) j.add(of[w], acc[w][lane]);
+  for (int w = 1; w < kJoinWarps; ++w) j.add(of[w], acc[w][lane]);
   j.store(p, b, seg, row, t, lane);
 }
 
@@ -854,11 +922,10 @@ cudaError_t launch_groups(const AttnParams& p, int grid, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kAttnThreads), Shape<NR>::kBytes, stream, p);
   if (e != cudaSuccess) return e;
-  const int64_t segments = p.a.c.B * p.row_tiles * p.a.c.kv_heads;
-  if (8 * segments <= grid) {   // of eight parts and more
-    const int64_t rows = p.a.T * p.G;
+  if (p.whole_parts) {
+    const int64_t rows = p.a.T * p.G, segments = p.a.c.B * p.row_tiles * p.a.c.kv_heads;
     return launch_pdl(join_segments_kernel, dim3(static_cast<unsigned>(segments), static_cast<unsigned>(rows < 8 * NR ? rows : 8 * NR)),
-                      dim3(128), 0, stream, p, 8 * NR, grid);
+                      dim3(32 * kJoinWarps), 0, stream, p, 8 * NR, grid);
   }
   return launch_pdl(join_cuts_kernel, dim3(static_cast<unsigned>(grid - 1)), dim3(256), 0, stream, p, 8 * NR);
 }
@@ -886,6 +953,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, int* err, int sm_count, cu
   p.row_tiles = static_cast<int>(tiles);
   p.err = err;
   const int grid = 2 * sm_count;
+  p.whole_parts = 8 * a.c.B * tiles * a.c.kv_heads <= grid;
   uint8_t* const ws = static_cast<uint8_t*>(a.workspace);
   p.cuts = reinterpret_cast<int32_t*>(ws);
   p.part_o = reinterpret_cast<float*>(ws + static_cast<size_t>(grid) * 16);
