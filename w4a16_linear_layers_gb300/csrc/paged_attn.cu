@@ -98,7 +98,7 @@ struct AttnParams {
   PagedAttnArgs a;
   int G;               // query heads of a key/value head
   int row_tiles;       // of a sequence's T * G rows
-  bool whole_parts;    // few segments: no share holds parts of two
+  bool planned;        // Plan is used
   int* err;
   // workspace: where the cut segments are, then their parts
   int32_t* cuts;       // [grid][4]: segment, its first and last share, sequence; segment -1: none
@@ -131,57 +131,69 @@ __device__ __forceinline__ int share_at(int64_t at, int64_t share) {
   return (at | share) < 1LL << 31 ? static_cast<int>(at) / static_cast<int>(share) : static_cast<int>(at / share);
 }
 
-// Few segments, an eighth of the thread blocks or less (64 sequences at most):
-// each gets thread blocks of its own, shares of equal size but its last.
-// Segments of n_s blocks cut into ceil(n_s / share) parts are fewer parts than
-// sum n_s / share + segments, so share = sum n_s / (grid - segments) is enough.
-// (A piece's beginning and end take 2 to 3 us.)  Each warp finds this by itself.
-struct Parts {
-  int64_t share;
-  int n[2], parts[2], before[2];      // of sequences lane and lane + 32; parts of the ones before
+// Segments that can be of eight parts and more each.
+__host__ __device__ inline bool few_segments(int64_t segments, int64_t grid) { return 8 * segments <= grid; }
 
-  __device__ __forceinline__ Parts(const AttnParams& p, int grid, int lane) {
-    const int segs = p.row_tiles * static_cast<int>(p.a.c.kv_heads);
-    const int B = static_cast<int>(p.a.c.B);
-    int64_t total = 0;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      n[k] = lane + 32 * k < B ? span_of(p.a, seq_len(p.a.c, lane + 32 * k, p.a.T)).count : 0;
-      total += n[k];
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
-    share = share_of(total * segs, grid - B * segs);
-    int all = 0;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      parts[k] = n[k] == 0 ? 0 : share_at(n[k] - 1, share) + 1;
-      int incl = parts[k];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(kAll, incl, o);
-        if (lane >= o) incl += v;
+// How the work of up to 32 sequences, less than 2^31 blocks, is shared out; each
+// warp finds it by itself, lane by sequence.  Either every thread block takes
+// `share` blocks of the list, or (own) segments are cut into parts of their own: a
+// thread block that holds parts of two begins and ends two pieces, 1 to 3 us more
+// than the others.  Then the share is the smallest for which the parts,
+// ceil(n_s / share) of a segment of n_s blocks, are no more than the thread blocks.
+// That is done where it is at most kPieceBlocks over the even one (12 x 8 rows: at
+// 2 over 41 32.4 us, 35.6 with even shares; at 15 over 126 71.5 and 67.5), and where
+// segments are few (then it is less than grid / (grid - segments) times the even
+// one, and the parts are joined by segment).
+constexpr int kPieceBlocks = 5;
+struct Plan {
+  int share, blocks;       // of a thread block, of all
+  bool own;
+  int parts;               // of the lane's sequence's segments; blocks where not own
+  int before;              // of the sequences before, for one segment
+
+  __device__ __forceinline__ Plan(const AttnParams& p, int grid, int lane) {
+    const int B = static_cast<int>(p.a.c.B), segs = p.row_tiles * static_cast<int>(p.a.c.kv_heads);
+    const int n = lane < B ? span_of(p.a, seq_len(p.a.c, lane, p.a.T)).count : 0;
+    blocks = __reduce_add_sync(kAll, n) * segs;
+    const int even = max((blocks + grid - 1) / grid, kMinShare);
+    const bool few = few_segments(B * segs, grid);
+    share = even;
+    own = false;
+    if (B * segs <= grid) {
+      // as many parts of each: enough, and hardly more where lengths are alike
+      const int each = grid / (B * segs);
+      int lo = even, hi = max((__reduce_max_sync(kAll, n) + each - 1) / each, even);
+      if (hi <= lo + 2) lo = hi;
+      if (!few && hi > lo + kPieceBlocks) hi = lo + kPieceBlocks + 1;      // not taken
+      while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (__reduce_add_sync(kAll, (n + mid - 1) / mid) * segs <= grid) hi = mid;
+        else lo = mid + 1;
       }
-      before[k] = all + incl - parts[k];
-      all += __shfl_sync(kAll, incl, 31);
+      own = few || lo <= even + kPieceBlocks;
+      if (own) share = lo;
     }
+    parts = own ? (n + share - 1) / share : n;
+    int incl = parts;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(kAll, incl, o);
+      if (lane >= o) incl += v;
+    }
+    before = incl - parts;
   }
-  // The sequence, segment and part of thread block c; false: none
-  __device__ __forceinline__ bool find(int c, int segs, int lane, int64_t& b, int& seg, int& part) const {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int in_b = c - before[k] * segs;
-      const uint32_t who = __ballot_sync(kAll, in_b >= 0 && in_b < parts[k] * segs);
-      if (who != 0) {
-        const int src = __ffs(who) - 1;
-        const int of_b = __shfl_sync(kAll, parts[k], src), at = __shfl_sync(kAll, in_b, src);
-        b = src + 32 * k;
-        seg = at / of_b;
-        part = at - seg * of_b;
-        return true;
-      }
-    }
-    return false;
+  // Where thread block c begins: sequence, segment, part (own) or block of it, and
+  // of how many; false: nowhere
+  __device__ __forceinline__ bool find(int c, int segs, int& b, int& seg, int& at, int& of) const {
+    const int in_b = (own ? c : c * share) - before * segs;
+    const uint32_t who = __ballot_sync(kAll, in_b >= 0 && in_b < parts * segs);
+    if (who == 0) return false;
+    b = __ffs(who) - 1;
+    const int in = __shfl_sync(kAll, in_b, b);
+    of = __shfl_sync(kAll, parts, b);
+    seg = in / of;
+    at = in - seg * of;
+    return true;
   }
 };
 
@@ -282,20 +294,33 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
   grid_dep_launch();      // (the joining kernel may read what this one's predecessors wrote at once)
 
   // ---- this block's share
-  if (p.whole_parts) {
-    const Parts parts(p, gridDim.x, lane);
-    int64_t b;
-    int seg, part;
-    if (!parts.find(blockIdx.x, segs, lane, b, seg, part)) return;
+  if (p.planned) {
+    const Plan plan(p, gridDim.x, lane);
+    const int c = blockIdx.x;
+    int b = 0, seg = 0, piece_at = 0, of = 1;
+    const bool mine = plan.find(c, segs, b, seg, piece_at, of);
     if (tid == 0) {
-      start.b = b;
-      start.segs = segs;
-      start.seg = seg;
-      start.off = part * parts.share;
-      start.load(a);
-      const int rest = start.span.count - start.off;
-      start.left = rest < parts.share ? rest : parts.share;
+      // the first boundary inside a segment announces it
+      int4 cut = make_int4(-1, 0, 0, b);
+      if (mine) {
+        start.b = b;
+        start.segs = segs;
+        start.seg = seg;
+        start.load(a);
+        if (plan.own) {
+          start.off = piece_at * plan.share;
+          start.left = min(start.span.count - start.off, plan.share);
+          if (piece_at == 1) cut = make_int4(seg, c - 1, c - 2 + of, b);
+        } else {
+          const int from = c * plan.share, s0 = from - piece_at, first = s0 / plan.share;
+          start.off = piece_at;
+          start.left = min(plan.blocks - from, plan.share);
+          if (piece_at > 0 && first == c - 1) cut = make_int4(seg, first, (s0 + of - 1) / plan.share, b);
+        }
+      }
+      *reinterpret_cast<int4*>(p.cuts + 4 * c) = cut;
     }
+    if (!mine) return;
     __syncthreads();
   } else {
     // Blocks of 16 of 256 sequences at a time: their running sum, which places
@@ -879,8 +904,8 @@ __global__ void __launch_bounds__(256) join_cuts_kernel(const AttnParams p, int 
   }
 }
 
-// The same where there are few segments, of up to grid / segments parts each: a
-// block takes row y of segment x, its warps parts.
+// The same where there are few segments, of eight parts and more: a block takes
+// row y of segment x, its warps parts.
 constexpr int kJoinWarps = 8;
 __global__ void __launch_bounds__(32 * kJoinWarps) join_segments_kernel(const AttnParams p, int tile_rows, int grid) {
   __shared__ float4 acc[kJoinWarps][32];
@@ -889,11 +914,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_segments_kernel(const At
   const PagedAttnArgs& a = p.a;
   // The lengths are older than the kernel in front, which starts this one when
   // its own predecessors are done.
-  const Parts parts(p, grid, lane);
+  const Plan plan(p, grid, lane);
   const int segs = p.row_tiles * static_cast<int>(a.c.kv_heads);
   const int b = blockIdx.x / segs, seg = blockIdx.x % segs, in_tile = blockIdx.y;
-  const int n = __shfl_sync(kAll, b < 32 ? parts.parts[0] : parts.parts[1], b & 31);
-  const int first = __shfl_sync(kAll, b < 32 ? parts.before[0] : parts.before[1], b & 31) * segs + seg * n;
+  const int n = __shfl_sync(kAll, plan.parts, b), first = __shfl_sync(kAll, plan.before, b) * segs + seg * n;
   const int row = seg % p.row_tiles * tile_rows + in_tile, t = row / p.G;
   const bool none = n <= 1 || row >= static_cast<int>(a.T) * p.G || t >= seq_len(a.c, b, a.T).fresh;      // one part: written already
   grid_dep_wait();
@@ -922,11 +946,10 @@ cudaError_t launch_groups(const AttnParams& p, int grid, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kAttnThreads), Shape<NR>::kBytes, stream, p);
   if (e != cudaSuccess) return e;
-  if (p.whole_parts) {
-    const int64_t rows = p.a.T * p.G, segments = p.a.c.B * p.row_tiles * p.a.c.kv_heads;
+  const int64_t rows = p.a.T * p.G, segments = p.a.c.B * p.row_tiles * p.a.c.kv_heads;
+  if (p.planned && few_segments(segments, grid))
     return launch_pdl(join_segments_kernel, dim3(static_cast<unsigned>(segments), static_cast<unsigned>(rows < 8 * NR ? rows : 8 * NR)),
                       dim3(32 * kJoinWarps), 0, stream, p, 8 * NR, grid);
-  }
   return launch_pdl(join_cuts_kernel, dim3(static_cast<unsigned>(grid - 1)), dim3(256), 0, stream, p, 8 * NR);
 }
 
@@ -953,7 +976,8 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, int* err, int sm_count, cu
   p.row_tiles = static_cast<int>(tiles);
   p.err = err;
   const int grid = 2 * sm_count;
-  p.whole_parts = 8 * a.c.B * tiles * a.c.kv_heads <= grid;
+  const int64_t segments = a.c.B * tiles * a.c.kv_heads, longest = a.c.max_pages * (a.c.page_size / 16);
+  p.planned = a.c.B <= 32 && segments <= ((1LL << 31) - 1 - 2 * kTile * grid) / longest;
   uint8_t* const ws = static_cast<uint8_t*>(a.workspace);
   p.cuts = reinterpret_cast<int32_t*>(ws);
   p.part_o = reinterpret_cast<float*>(ws + static_cast<size_t>(grid) * 16);
