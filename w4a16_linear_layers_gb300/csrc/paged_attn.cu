@@ -238,7 +238,7 @@ struct alignas(16) Piece {
   int j0;              // first token
   bool whole, final;   // it is a segment; the last one of the share
 };
-constexpr int kPieces = 8;      // the copies look up to kStages + 1 pieces ahead
+constexpr int kPieces = 16;     // more than the copies look ahead
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -272,10 +272,11 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
   using S = Shape<NR>;
   constexpr int kStages = S::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint64_t full_k[kAttnWarps][kStages], full_v[kStages];      // a warp's keys and scales, all values are there
+  __shared__ uint64_t full_k[kStages], full_v[kStages];      // keys and scales, values are there
   __shared__ Walk aheads[kAttnWarps];       // of each warp's copies
-  __shared__ Piece pieces[kAttnWarps][kPieces];
+  __shared__ Piece pieces[kPieces];
   __shared__ Walk start;
+  __shared__ uint16_t on_page[4];      // [stages]: bit i: block i is on a page
   __shared__ int abort_flag;
   __shared__ int64_t warp_sums[kAttnWarps];
   const PagedAttnArgs& a = p.a;
@@ -285,8 +286,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
   if (tid == 0) {
     abort_flag = 0;
     for (int i = 0; i < kStages; ++i) {
-      for (int w = 0; w < kAttnWarps; ++w) mbar_init(smem_u32(&full_k[w][i]), 1);
-      mbar_init(smem_u32(&full_v[i]), kAttnWarps);
+      mbar_init(smem_u32(&full_k[i]), 2);
+      mbar_init(smem_u32(&full_v[i]), 2);
     }
     fence_barrier_init();
   }
@@ -390,91 +391,84 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
   const WaitCtx ctx{p.err, &abort_flag, kWaitLimitNs};
   bool ok = true;
 
-  // ---- copies: this warp's block of each tile, the next tile's page read a tile
-  // before it is used
+  // ---- copies.  At tile t, warps 2 (t % 4) and the next one send the keys and
+  // scales of tile t + kStages, whose stage the barrier of tile t freed, four blocks
+  // each by four lanes, and at tile t + 1 its values.  A warp looks at its next
+  // tile's pages at once, four tiles before it sends them.
   Walk& ahead = aheads[warp];
   const int per_page = static_cast<int>(a.c.page_size) >> 4;
-  const int page_step = kTileBlocks / per_page, in_page_step = kTileBlocks % per_page;
   const uint32_t page_blocks = static_cast<uint32_t>(per_page * static_cast<int>(a.c.kv_heads));
-  int next_i = 0, next_n = 0;        // the tile's first block of the piece, the piece's blocks
-  const int32_t* table = nullptr;    // at the block's page
-  int page = -1, in_page = 0, put = 0;
-  uint32_t head_at = 0;              // block of the cache: the head's first of page 0
-  // blocks of the tiles whose keys were sent, not their values: two at most
   constexpr uint32_t kNoBlock = 0xFFFFFFFFu;
-  uint32_t values[2] = {kNoBlock, kNoBlock};
-  int waiting = 0;
-  bool more = true;
-  uint32_t sent_pages = 0;           // bit s: the block in stage s is on a page
-  auto look = [&]() { page = next_i + warp < next_n ? __ldg(table) : -1; };
-  auto enter = [&]() {               // ahead's piece
-    next_i = 0;
-    next_n = ahead.piece();
-    const int n = ahead.span.first + ahead.off, mine = n + warp, of_table = mine / per_page;
-    in_page = mine - of_table * per_page;
-    table = a.c.block_table + ahead.b * a.c.max_pages + of_table;
-    head_at = static_cast<uint32_t>(ahead.seg / p.row_tiles * per_page);
-    if (lane == 0)
-      pieces[warp][put] = Piece{ahead.b, ahead.seg, ahead.seq.len, ahead.seq.fresh, ahead.off, next_n, 16 * n, next_n == ahead.span.count,
-                                next_n == ahead.left};
-    put = (put + 1) % kPieces;
-    look();
-  };
-  auto send_keys = [&](int stage) {  // and scales
-    if (!more) return;
-    const bool real = page >= 0 && page < a.c.pages;
-    const uint32_t block = head_at + static_cast<uint32_t>(page) * page_blocks + static_cast<uint32_t>(in_page);
-    if (ok && lane == 0) {
-      const uint32_t bar = smem_u32(&full_k[warp][stage]);
-      mbar_arrive_expect_tx(bar, real ? kVCodes + kScaleBytes : 0);
-      if (real) {
-        const uint8_t* const from = a.c.cache + static_cast<int64_t>(block) * kCacheBlock;
-        bulk_load(smem_u32(smem) + (stage * kTileBlocks + warp) * kVCodes, from, kVCodes, bar);
-        bulk_load(smem_u32(smem) + S::kScaleRing + (stage * kTileBlocks + warp) * kScaleBytes, from + kKScales, kScaleBytes, bar);
-      }
-    }
-    sent_pages = (sent_pages & ~(1u << stage)) | (real ? 1u << stage : 0u);
-    (waiting == 0 ? values[0] : values[1]) = real ? block : kNoBlock;
-    ++waiting;
-    next_i += kTileBlocks;
-    if (next_i < next_n) {
-      table += page_step;
-      in_page += in_page_step;
-      if (in_page >= per_page) {
-        in_page -= per_page;
-        ++table;
-      }
-      look();
-    } else {
-      more = ahead.left > next_n;
+  const int sent_block = 4 * (warp & 1) + (lane & 3);      // of a tile
+  int next_tile = 0, pieces_seen = 0;      // the warp's next tile of the piece; pieces before it
+  int page = -1;                           // of the lane's block
+  uint32_t block = kNoBlock;               // of the cache: the lane's of the tile whose values are next
+  bool more = true, values_due = false;
+  auto skip = [&](int tiles) {             // on to the warp's next tile
+    next_tile += tiles;
+    for (;;) {
+      const int n = ahead.piece(), of_piece = (n + kTileBlocks - 1) / kTileBlocks;
+      if (next_tile < of_piece) break;
+      next_tile -= of_piece;
+      ++pieces_seen;
+      more = ahead.left > n;
+      if (!more) return;
       __syncwarp();
-      if (more) {
-        if (lane == 0) ahead.next(a);
-        __syncwarp();
-        enter();
-      }
+      if (lane == 0) ahead.next(a);
+      __syncwarp();
     }
+    const int n = ahead.piece(), first = ahead.span.first + ahead.off;
+    if (next_tile == 0 && lane == 0)
+      pieces[pieces_seen % kPieces] = Piece{ahead.b, ahead.seg, ahead.seq.len, ahead.seq.fresh, ahead.off, n, 16 * first,
+                                            n == ahead.span.count, n == ahead.left};
+    const int i = next_tile * kTileBlocks + sent_block;
+    const int of_table = (first + i) / per_page;
+    page = i < n ? __ldg(a.c.block_table + ahead.b * a.c.max_pages + of_table) : -1;
+    block = static_cast<uint32_t>(ahead.seg / p.row_tiles * per_page + (first + i - of_table * per_page));      // but for its page
+  };
+  auto send_keys = [&](int stage) {        // and scales
+    if (!more) return;
+    const bool real = ok && page >= 0 && page < a.c.pages;
+    block = real ? block + static_cast<uint32_t>(page) * page_blocks : kNoBlock;
+    const uint32_t there = __ballot_sync(kAll, real) & 0xFu;
+    const uint32_t bar = smem_u32(&full_k[stage]);
+    if (lane == 0) {
+      reinterpret_cast<uint8_t*>(on_page)[2 * stage + (warp & 1)] = static_cast<uint8_t>(there);
+      if (ok) mbar_arrive_expect_tx(bar, __popc(there) * (kVCodes + kScaleBytes));
+    }
+    __syncwarp();
+    if (real && lane < 4) {
+      const uint8_t* const from = a.c.cache + static_cast<int64_t>(block) * kCacheBlock;
+      bulk_load(smem_u32(smem) + (stage * kTileBlocks + sent_block) * kVCodes, from, kVCodes, bar);
+      bulk_load(smem_u32(smem) + S::kScaleRing + (stage * kTileBlocks + sent_block) * kScaleBytes, from + kKScales, kScaleBytes, bar);
+    }
+    values_due = true;
   };
   auto send_values = [&](int stage) {
-    if (waiting == 0) return;
-    if (ok && lane == 0) {
-      const uint32_t bar = smem_u32(&full_v[stage]);
-      mbar_arrive_expect_tx(bar, values[0] != kNoBlock ? kVCodes : 0);
-      if (values[0] != kNoBlock)
-        bulk_load(smem_u32(smem) + S::kVRing + (stage * kTileBlocks + warp) * kVCodes,
-                  a.c.cache + static_cast<int64_t>(values[0]) * kCacheBlock + kVCodes, kVCodes, bar);
-    }
-    values[0] = values[1];
-    --waiting;
+    if (!values_due) return;
+    const uint32_t bar = smem_u32(&full_v[stage]);
+    const bool real = block != kNoBlock && lane < 4;
+    const uint32_t there = __ballot_sync(kAll, real);
+    if (ok && lane == 0) mbar_arrive_expect_tx(bar, __popc(there) * kVCodes);
+    __syncwarp();
+    if (ok && real)
+      bulk_load(smem_u32(smem) + S::kVRing + (stage * kTileBlocks + sent_block) * kVCodes,
+                a.c.cache + static_cast<int64_t>(block) * kCacheBlock + kVCodes, kVCodes, bar);
+    values_due = false;
+    skip(4);
   };
   if (lane == 0) ahead = start;
   __syncwarp();
-  enter();
-#pragma unroll
-  for (int i = 0; i < kStages; ++i) {
-    send_keys(i);
-    if (i < kStages - 1) send_values(i);
+  {
+    const int mine = ((warp >> 1) + kStages) & 3;      // the warp's first tile
+    skip(mine);
+    if (mine < kStages) {
+      send_keys(mine);
+      if (mine < kStages - 1) send_values(mine);
+    }
   }
+  int to_send = (4 - (warp >> 1)) & 3;     // 0: keys at this tile, 1: values
+  __syncthreads();                         // the first piece is there
 
   const int g = lane >> 2, q = lane & 3;
   // Scores: tokens tok and tok + 1 of the warp's block, rows 8 r + 2 q and the
@@ -510,11 +504,10 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
   int stage = 0, phase = 0, turn = 0, get = 0;
   int i = 0, n = 0, j0 = 0;          // the tile's first block of the piece, the piece's blocks, the tile's first token
   for (;;) {
-    const Piece& piece = pieces[warp][get];
+    const Piece& piece = pieces[get];
     const bool first = i >= n;
     if (first) {
       // q of the piece's rows, what they see
-      __syncwarp();
       i = 0;
       n = piece.n;
       j0 = piece.j0;
@@ -571,11 +564,11 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
       }
     }
 
-    ok = __all_sync(kAll, ok && mbar_wait(smem_u32(&full_k[warp][stage]), phase, ctx, 91));
+    ok = ok && mbar_wait(smem_u32(&full_k[stage]), phase, ctx, 91);
     // Whether all rows see all of the warp's block.  Elsewhere what a row does not
     // see gets no weight; a block that is not there is gone through all the same, as
     // whatever finite codes stand in its place.
-    const bool here = ok && i + warp < n && (sent_pages >> stage & 1u);
+    const bool here = ok && (reinterpret_cast<const uint8_t*>(on_page)[2 * stage + (warp >> 2)] >> (warp & 3) & 1u);
     const int j = j0 + 16 * warp;
     const bool all_seen = here && j >= seen_from && j + 16 <= seen_to;
 
@@ -648,16 +641,20 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
         }
       }
     }
-    // the keys are read: the next ones into their slot
-    fence_proxy_async_smem();
-    __syncwarp();
-    send_keys(stage);
-
     // ---- weights, as if the references held
     uint8_t* const weights = ps + turn * (S::kRows * kPStride);
     const float lv[2] = {log2_above(vs.x), log2_above(vs.y)};
     f32x2 part[NR];
     bool sent = false;
+    auto send = [&]() {
+      sent = true;
+      if (to_send <= 1) {
+        fence_proxy_async_smem();
+        if (to_send == 0) send_keys(stage);
+        else send_values(stage == 0 ? kStages - 1 : stage - 1);
+      }
+      to_send = (to_send + 1) & 3;
+    };
     for (bool raised = false;; raised = true) {
       // (a piece's first tile has no references yet)
       if (raised || !first) {
@@ -687,13 +684,9 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
           *reinterpret_cast<__half2*>(to) = __floats2half2_rn(w[0], w[2]);
           *reinterpret_cast<__half2*>(to + kPStride) = __floats2half2_rn(w[1], w[3]);
         }
-        // (behind this barrier all warps are done with the values of the tile before this one)
+        // (behind this barrier all warps are done with this tile's keys and the values of the one before)
         const bool raise = __syncthreads_or(fmaxf(most[0] + lv[0], most[1] + lv[1]) > kMostWeight) != 0;
-        if (!sent) {
-          fence_proxy_async_smem();
-          send_values(stage == 0 ? kStages - 1 : stage - 1);
-          sent = true;
-        }
+        if (!sent) send();
         if (raised || !raise) break;
       }
       // References of the rows concerned up, what stands under them down.  Each
@@ -713,11 +706,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
         }
       }
       __syncthreads();
-      if (!sent) {      // a first tile's: the barrier was this one
-        fence_proxy_async_smem();
-        send_values(stage == 0 ? kStages - 1 : stage - 1);
-        sent = true;
-      }
+      if (!sent) send();      // a first tile's: the barrier was this one
       if (warp == 0 && lane < S::kRows) {
         float2 of[kAttnWarps];
         float top = kNone, over = -INFINITY;
@@ -753,7 +742,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
 #pragma unroll
     for (int r = 0; r < NR; ++r) sum[r] = add2(sum[r], part[r]);
     // ---- outputs
-    ok = __all_sync(kAll, ok && mbar_wait(smem_u32(&full_v[stage]), phase, ctx, 92));
+    ok = ok && mbar_wait(smem_u32(&full_v[stage]), phase, ctx, 92);
     const uint8_t* const tile_values = smem + S::kVRing + stage * kTileBlocks * kVCodes;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
