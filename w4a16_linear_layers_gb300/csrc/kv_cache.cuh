@@ -22,12 +22,17 @@ __device__ __forceinline__ int code_place(int r, int d) { return ((((d >> 5) ^ (
 struct SeqLen {
   int len, fresh;
 };
-__device__ __forceinline__ SeqLen seq_len(const CacheArgs& c, int64_t b, int64_t T) {
+__device__ __forceinline__ SeqLen seq_of(const CacheArgs& c, int64_t T, int total, int fresh) {
   SeqLen s;
-  s.len = min(max(__ldcg(c.total_len + b), 0), static_cast<int>(c.max_pages * c.page_size));
-  const int most = static_cast<int>(T < s.len ? T : s.len);
-  s.fresh = c.new_len == nullptr ? most : min(max(__ldcg(c.new_len + b), 0), most);
+  s.len = min(max(total, 0), static_cast<int>(c.max_pages * c.page_size));
+  s.fresh = min(max(fresh, 0), static_cast<int>(T < s.len ? T : s.len));
   return s;
+}
+__device__ __forceinline__ int fresh_of(const CacheArgs& c, int64_t b) {
+  return c.new_len == nullptr ? 0x7FFFFFFF : __ldcg(c.new_len + b);
+}
+__device__ __forceinline__ SeqLen seq_len(const CacheArgs& c, int64_t b, int64_t T) {
+  return seq_of(c, T, __ldcg(c.total_len + b), fresh_of(c, b));
 }
 
 // Block of 16 that holds tokens 16 n .. 16 n + 15 of sequence b, head h;

@@ -52,7 +52,6 @@ constexpr int kAttnWarps = 8;
 constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kTileBlocks = 8;      // of 16 tokens, of a tile
 constexpr int kTile = 16 * kTileBlocks;
-constexpr int kScaleBytes = kCacheBlock - kKScales;    // of a block
 constexpr int kMinShare = kTileBlocks;
 constexpr int kQStride = 272;       // bytes of a row of q: rows 16 bytes apart mod 128
 constexpr int kPStride = 288;       // bytes of a row of weights: rows 32 bytes apart mod 128
@@ -69,11 +68,10 @@ constexpr float kNewWeight = 0.0f;
 template <int NR>
 struct Shape {
   static constexpr int kRows = 8 * NR;
-  static constexpr int kStages = NR == 1 ? 3 : 2;
-  // shared memory, in order: [stages][warps] keys, the same of scales (K, V), of values
-  static constexpr int kScaleRing = kStages * kTileBlocks * kVCodes;
-  static constexpr int kVRing = kScaleRing + kStages * kTileBlocks * kScaleBytes;
-  static constexpr int kQ = kVRing + kStages * kTileBlocks * kVCodes;
+  // blocks in the ring: what two thread blocks an SM have room for
+  static constexpr int kSlots = NR == 1 ? 24 : NR == 2 ? 22 : 17;
+  // shared memory, in order
+  static constexpr int kQ = kSlots * kCacheBlock;
   static constexpr int kP = kQ + kRows * kQStride;       // weights of two tiles
   static constexpr int kO = kP;                          // fp32 [rows][128], when a piece is done
   static_assert(512 <= 2 * kPStride, "outputs stand where the weights did");
@@ -81,10 +79,12 @@ struct Shape {
   static constexpr int kRef = kPair + kAttnWarps * kRows * 8;     // float4 [rows / 2]: two rows' references
   static constexpr int kKeep = kRef + kRows * 8;         // fp32 [rows]: what a raised reference leaves of the sums
   static constexpr int kFactor = kKeep + kRows * 4;      // fp32 [rows]
+  // of two pieces:
   static constexpr int kTo = kFactor + kRows * 4;        // int32 [rows]: the row's head of the sequence's outputs, -1: none
-  static constexpr int kLow = kTo + kRows * 4;           // int32 [rows]: first token seen
-  static constexpr int kHigh = kLow + kRows * 4;         // and the one behind the last
-  static constexpr int kBytes = kHigh + kRows * 4;
+  static constexpr int kLow = kTo + 2 * kRows * 4;       // int32 [rows]: first token seen
+  static constexpr int kHigh = kLow + 2 * kRows * 4;     // and the one behind the last
+  static constexpr int kRaw = kHigh + 2 * kRows * 4;     // bf16 [rows][128]: q of the piece to come
+  static constexpr int kBytes = kRaw + kRows * kHeadDim * 2;
 };
 
 // A row's reference m + c and the sum under it, of a part of its tokens.
@@ -214,7 +214,8 @@ struct Walk {
     const int rest = span.count - off;
     return left < rest ? static_cast<int>(left) : rest;
   }
-  __device__ __forceinline__ void next(const PagedAttnArgs& a) {
+  // total and fresh: total_len and new_len of the sequence behind b, read long before
+  __device__ __forceinline__ void next(const PagedAttnArgs& a, int& total, int& fresh) {
     const int n = piece();
     left -= n;
     off += n;
@@ -222,10 +223,20 @@ struct Walk {
     off = 0;
     if (++seg < segs) return;
     seg = 0;
-    do {
+    ++b;
+    seq = seq_of(a.c, a.T, total, fresh);
+    span = span_of(a, seq);
+    while (span.count == 0) {      // more blocks are to come, so there is one
       ++b;
       load(a);
-    } while (span.count == 0);      // more blocks are to come, so there is one
+    }
+    look_behind(a, total, fresh);
+  }
+  __device__ __forceinline__ void look_behind(const PagedAttnArgs& a, int& total, int& fresh) const {
+    if (b + 1 < a.c.B) {
+      total = __ldcg(a.c.total_len + b + 1);
+      fresh = fresh_of(a.c, b + 1);
+    }
   }
 };
 
@@ -238,7 +249,8 @@ struct alignas(16) Piece {
   int j0;              // first token
   bool whole, final;   // it is a segment; the last one of the share
 };
-constexpr int kPieces = 16;     // more than the copies look ahead
+constexpr int kPieces = 8;      // more than the copies look ahead
+constexpr int kTilesAhead = 4;  // and tiles, this one among them
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -270,13 +282,12 @@ __device__ __forceinline__ float log2_above(float v) {
 template <int NR, bool kCap>
 __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams p) {
   using S = Shape<NR>;
-  constexpr int kStages = S::kStages;
+  constexpr int kSlots = S::kSlots;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint64_t full_k[kStages], full_v[kStages];      // keys and scales, values are there
+  __shared__ uint64_t full[kTilesAhead];    // a tile's blocks are there
   __shared__ Walk aheads[kAttnWarps];       // of each warp's copies
   __shared__ Piece pieces[kPieces];
   __shared__ Walk start;
-  __shared__ uint16_t on_page[4];      // [stages]: bit i: block i is on a page
   __shared__ int abort_flag;
   __shared__ int64_t warp_sums[kAttnWarps];
   const PagedAttnArgs& a = p.a;
@@ -285,10 +296,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
 
   if (tid == 0) {
     abort_flag = 0;
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_u32(&full_k[i]), 2);
-      mbar_init(smem_u32(&full_v[i]), 2);
-    }
+    for (int i = 0; i < kTilesAhead; ++i) mbar_init(smem_u32(&full[i]), kAttnWarps);
     fence_barrier_init();
   }
   grid_dep_wait();
@@ -391,85 +399,100 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
   const WaitCtx ctx{p.err, &abort_flag, kWaitLimitNs};
   bool ok = true;
 
-  // ---- copies.  At tile t, warps 2 (t % 4) and the next one send the keys and
-  // scales of tile t + kStages, whose stage the barrier of tile t freed, four blocks
-  // each by four lanes, and at tile t + 1 its values.  A warp looks at its next
-  // tile's pages at once, four tiles before it sends them.
+  // ---- copies: this warp's block of each tile, one bulk copy (whose issue takes
+  // its thread 200 cycles), into the ring as soon as the block that it displaces is
+  // of a tile that is done.  The next page is read when the one before is sent.
   Walk& ahead = aheads[warp];
   const int per_page = static_cast<int>(a.c.page_size) >> 4;
+  const int page_step = kTileBlocks / per_page, in_page_step = kTileBlocks % per_page;
   const uint32_t page_blocks = static_cast<uint32_t>(per_page * static_cast<int>(a.c.kv_heads));
-  constexpr uint32_t kNoBlock = 0xFFFFFFFFu;
-  const int sent_block = 4 * (warp & 1) + (lane & 3);      // of a tile
-  int next_tile = 0, pieces_seen = 0;      // the warp's next tile of the piece; pieces before it
-  int page = -1;                           // of the lane's block
-  uint32_t block = kNoBlock;               // of the cache: the lane's of the tile whose values are next
-  bool more = true, values_due = false;
-  auto skip = [&](int tiles) {             // on to the warp's next tile
-    next_tile += tiles;
-    for (;;) {
-      const int n = ahead.piece(), of_piece = (n + kTileBlocks - 1) / kTileBlocks;
-      if (next_tile < of_piece) break;
-      next_tile -= of_piece;
-      ++pieces_seen;
-      more = ahead.left > n;
-      if (!more) return;
+  int next_i = 0, next_n = 0;        // the tile's first block of the piece, the piece's blocks
+  const int32_t* table = nullptr;    // at the block's page
+  int page = -1, in_page = 0, put = 0;
+  uint32_t head_at = 0;              // block of the cache: the head's first of page 0
+  bool more = true;
+  uint32_t on_page = 0;              // bit t % kTilesAhead: the warp's block of tile t is on a page
+  int to_send = 0, send_slot = warp; // the tile whose block is next, and where it goes
+  int behind_total = 0, behind_fresh = 0;  // lane 0: see Walk
+  auto look = [&]() { page = next_i + warp < next_n ? __ldg(table) : -1; };
+  auto enter = [&]() {               // ahead's piece (each warp writes the same)
+    next_i = 0;
+    next_n = ahead.piece();
+    const int n = ahead.span.first + ahead.off, mine = n + warp, of_table = mine / per_page;
+    in_page = mine - of_table * per_page;
+    table = a.c.block_table + ahead.b * a.c.max_pages + of_table;
+    head_at = static_cast<uint32_t>(ahead.seg / p.row_tiles * per_page);
+    if (lane == 0)
+      pieces[put] = Piece{ahead.b, ahead.seg, ahead.seq.len, ahead.seq.fresh, ahead.off, next_n, 16 * n, next_n == ahead.span.count,
+                          next_n == ahead.left};
+    put = (put + 1) % kPieces;
+    look();
+  };
+  // tile: the one whose predecessors are done
+  auto send = [&](int tile) {
+    if (!more || kTileBlocks * to_send + warp >= kTileBlocks * tile + kSlots) return;
+    const bool real = page >= 0 && page < a.c.pages;
+    const int of = to_send % kTilesAhead;
+    if (ok && lane == 0) {
+      const uint32_t bar = smem_u32(&full[of]);
+      mbar_arrive_expect_tx(bar, real ? kCacheBlock : 0);
+      if (real)
+        bulk_load(smem_u32(smem) + send_slot * kCacheBlock,
+                  a.c.cache + static_cast<int64_t>(head_at + static_cast<uint32_t>(page) * page_blocks + static_cast<uint32_t>(in_page)) * kCacheBlock,
+                  kCacheBlock, bar);
+    }
+    on_page = (on_page & ~(1u << of)) | (real ? 1u << of : 0u);
+    ++to_send;
+    send_slot += kTileBlocks;
+    if (send_slot >= kSlots) send_slot -= kSlots;
+    next_i += kTileBlocks;
+    if (next_i < next_n) {
+      table += page_step;
+      in_page += in_page_step;
+      if (in_page >= per_page) {
+        in_page -= per_page;
+        ++table;
+      }
+      look();
+    } else {
+      more = ahead.left > next_n;
       __syncwarp();
-      if (lane == 0) ahead.next(a);
-      __syncwarp();
+      if (more) {
+        if (lane == 0) ahead.next(a, behind_total, behind_fresh);
+        __syncwarp();
+        enter();
+      }
     }
-    const int n = ahead.piece(), first = ahead.span.first + ahead.off;
-    if (next_tile == 0 && lane == 0)
-      pieces[pieces_seen % kPieces] = Piece{ahead.b, ahead.seg, ahead.seq.len, ahead.seq.fresh, ahead.off, n, 16 * first,
-                                            n == ahead.span.count, n == ahead.left};
-    const int i = next_tile * kTileBlocks + sent_block;
-    const int of_table = (first + i) / per_page;
-    page = i < n ? __ldg(a.c.block_table + ahead.b * a.c.max_pages + of_table) : -1;
-    block = static_cast<uint32_t>(ahead.seg / p.row_tiles * per_page + (first + i - of_table * per_page));      // but for its page
   };
-  auto send_keys = [&](int stage) {        // and scales
-    if (!more) return;
-    const bool real = ok && page >= 0 && page < a.c.pages;
-    block = real ? block + static_cast<uint32_t>(page) * page_blocks : kNoBlock;
-    const uint32_t there = __ballot_sync(kAll, real) & 0xFu;
-    const uint32_t bar = smem_u32(&full_k[stage]);
-    if (lane == 0) {
-      reinterpret_cast<uint8_t*>(on_page)[2 * stage + (warp & 1)] = static_cast<uint8_t>(there);
-      if (ok) mbar_arrive_expect_tx(bar, __popc(there) * (kVCodes + kScaleBytes));
-    }
-    __syncwarp();
-    if (real && lane < 4) {
-      const uint8_t* const from = a.c.cache + static_cast<int64_t>(block) * kCacheBlock;
-      bulk_load(smem_u32(smem) + (stage * kTileBlocks + sent_block) * kVCodes, from, kVCodes, bar);
-      bulk_load(smem_u32(smem) + S::kScaleRing + (stage * kTileBlocks + sent_block) * kScaleBytes, from + kKScales, kScaleBytes, bar);
-    }
-    values_due = true;
-  };
-  auto send_values = [&](int stage) {
-    if (!values_due) return;
-    const uint32_t bar = smem_u32(&full_v[stage]);
-    const bool real = block != kNoBlock && lane < 4;
-    const uint32_t there = __ballot_sync(kAll, real);
-    if (ok && lane == 0) mbar_arrive_expect_tx(bar, __popc(there) * kVCodes);
-    __syncwarp();
-    if (ok && real)
-      bulk_load(smem_u32(smem) + S::kVRing + (stage * kTileBlocks + sent_block) * kVCodes,
-                a.c.cache + static_cast<int64_t>(block) * kCacheBlock + kVCodes, kVCodes, bar);
-    values_due = false;
-    skip(4);
-  };
-  if (lane == 0) ahead = start;
-  __syncwarp();
-  {
-    const int mine = ((warp >> 1) + kStages) & 3;      // the warp's first tile
-    skip(mine);
-    if (mine < kStages) {
-      send_keys(mine);
-      if (mine < kStages - 1) send_values(mine);
-    }
+  if (lane == 0) {
+    ahead = start;
+    start.look_behind(a, behind_total, behind_fresh);
   }
-  int to_send = (4 - (warp >> 1)) & 3;     // 0: keys at this tile, 1: values
-  __syncthreads();                         // the first piece is there
-
+  __syncwarp();
+  enter();
+  for (int i = 0; kTileBlocks * i + warp < kSlots; ++i) send(0);
+  // ---- q of the piece to come, each warp's rows, brought while the piece before
+  // it ends
+  const int rows = static_cast<int>(a.T) * p.G;
+  uint8_t* const raw = smem + S::kRaw;
+  // lane by row: its head of the sequence's outputs, -1: none
+  auto place = [&](int seg, int fresh) {
+    const int h = seg / p.row_tiles, row = (seg - h * p.row_tiles) * S::kRows + lane, t = row / p.G;
+    return lane < S::kRows && row < rows && t < fresh ? t * static_cast<int>(a.q_heads) + h * p.G + (row - t * p.G) : -1;
+  };
+  auto bring_q = [&](int64_t b, int to) {
+    const uint16_t* const from = a.q + b * a.T * a.q_heads * kHeadDim + 8 * (lane & 15);
+#pragma unroll
+    for (int k = 0; k < NR; k += 2) {      // half a warp a row
+      const int r = warp + kAttnWarps * (k + (NR > 1 ? lane >> 4 : 0));
+      const int at = __shfl_sync(kAll, to, r);
+      if (at >= 0 && (NR > 1 || lane < 16))
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(raw + r * kHeadDim * 2 + 16 * (lane & 15))),
+                     "l"(from + static_cast<int64_t>(at) * kHeadDim)
+                     : "memory");
+    }
+  };
+  bring_q(start.b, place(start.seg, start.seq.fresh));
   const int g = lane >> 2, q = lane & 3;
   // Scores: tokens tok and tok + 1 of the warp's block, rows 8 r + 2 q and the
   // next one.  The tokens are such that 8 lanes' reads of keys (g = 2 u and
@@ -488,7 +511,6 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
   float* const factors = reinterpret_cast<float*>(smem + S::kFactor);
   int* const lows = reinterpret_cast<int*>(smem + S::kLow);
   int* const highs = reinterpret_cast<int*>(smem + S::kHigh);
-  const int rows = static_cast<int>(a.T) * p.G;
 
   // A row's reference is a score (its negative is held) plus a small number, so
   // that large scores do not swallow the logarithm of the value scale in it.
@@ -501,38 +523,39 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
   float o[2][NR][4];
   int seen_from = 0, seen_to = 0;    // tokens that all rows see
 
-  int stage = 0, phase = 0, turn = 0, get = 0;
+  int tile = 0, slot = 0, turn = 0, get = 0, odd = 0;      // slot: of the tile's first block
   int i = 0, n = 0, j0 = 0;          // the tile's first block of the piece, the piece's blocks, the tile's first token
   for (;;) {
     const Piece& piece = pieces[get];
     const bool first = i >= n;
     if (first) {
+      __syncwarp();
       // q of the piece's rows, what they see
       i = 0;
       n = piece.n;
       j0 = piece.j0;
       // lane by row: its place, and what it sees
-      const int h = piece.seg / p.row_tiles, row = (piece.seg - h * p.row_tiles) * S::kRows + lane, t = row / p.G;
-      const bool real = lane < S::kRows && row < rows && t < piece.fresh;
-      const int to = real ? t * static_cast<int>(a.q_heads) + h * p.G + (row - t * p.G) : -1;
-      const int len = piece.len, token = len - piece.fresh + t;
+      odd ^= 1;
+      const int to = place(piece.seg, piece.fresh);
+      const bool real = to >= 0;
+      const int len = piece.len, token = len - piece.fresh + (real ? to / static_cast<int>(a.q_heads) : 0);
       const int64_t w = a.window > 0 ? a.window : 1LL << 40;
       const int low = real && token - w + 1 > 0 ? static_cast<int>(token - w + 1) : 0;
       const int high = !real ? 0 : a.causal ? token + 1 : token + w < len ? static_cast<int>(token + w) : len;
       seen_from = __reduce_max_sync(kAll, low);
       seen_to = __reduce_min_sync(kAll, real ? high : len);
       if (warp == 0 && lane < S::kRows) {
-        tos[lane] = to;
-        lows[lane] = low;
-        highs[lane] = high;
-        reinterpret_cast<float2*>(refs)[lane] = (lane & 1) ? make_float2(0.0f, 0.0f) : make_float2(-kNone, -kNone);
+        tos[odd * S::kRows + lane] = to;
+        lows[odd * S::kRows + lane] = low;
+        highs[odd * S::kRows + lane] = high;
       }
-      const uint16_t* const from = a.q + piece.b * a.T * a.q_heads * kHeadDim;
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
       uint2 x[NR];
 #pragma unroll
       for (int k = 0; k < NR; ++k) {
-        const int at = __shfl_sync(kAll, to, warp + kAttnWarps * k);
-        x[k] = at >= 0 ? __ldg(reinterpret_cast<const uint2*>(from + static_cast<int64_t>(at) * kHeadDim) + lane) : make_uint2(0, 0);
+        const int r = warp + kAttnWarps * k;
+        x[k] = __shfl_sync(kAll, to, r) >= 0 ? *reinterpret_cast<const uint2*>(raw + r * kHeadDim * 2 + 8 * lane) : make_uint2(0, 0);
       }
 #pragma unroll
       for (int k = 0; k < NR; ++k) {
@@ -564,11 +587,17 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
       }
     }
 
-    ok = ok && mbar_wait(smem_u32(&full_k[stage]), phase, ctx, 91);
+    if (i + kTileBlocks >= n && !piece.final) {
+      __syncwarp();
+      const Piece& behind = pieces[(get + 1) % kPieces];
+      bring_q(behind.b, place(behind.seg, behind.fresh));
+    }
+
+    ok = ok && mbar_wait(smem_u32(&full[tile % kTilesAhead]), tile / kTilesAhead & 1, ctx, 91);
     // Whether all rows see all of the warp's block.  Elsewhere what a row does not
     // see gets no weight; a block that is not there is gone through all the same, as
     // whatever finite codes stand in its place.
-    const bool here = ok && (reinterpret_cast<const uint8_t*>(on_page)[2 * stage + (warp >> 2)] >> (warp & 3) & 1u);
+    const bool here = ok && (on_page >> (tile % kTilesAhead) & 1u);
     const int j = j0 + 16 * warp;
     const bool all_seen = here && j >= seen_from && j + 16 <= seen_to;
 
@@ -576,8 +605,9 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
     f32x2 x[NR][2];
     float2 vs;
     {
-      const uint8_t* const keys = smem + (stage * kTileBlocks + warp) * kVCodes;
-      const uint8_t* const scales = smem + S::kScaleRing + (stage * kTileBlocks + warp) * kScaleBytes;
+      const int mine = slot + warp;
+      const uint8_t* const keys = smem + (mine >= kSlots ? mine - kSlots : mine) * kCacheBlock;
+      const uint8_t* const scales = keys + kKScales;
       float s[NR][4];
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
@@ -631,7 +661,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
       if (!here) vs = make_float2(0.0f, 0.0f);
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
-        const int2 lo = *reinterpret_cast<const int2*>(lows + 8 * r + 2 * q), hi = *reinterpret_cast<const int2*>(highs + 8 * r + 2 * q);
+        const int2 lo = *reinterpret_cast<const int2*>(lows + odd * S::kRows + 8 * r + 2 * q);
+        const int2 hi = *reinterpret_cast<const int2*>(highs + odd * S::kRows + 8 * r + 2 * q);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int at = j + tok + c;
@@ -645,16 +676,6 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
     uint8_t* const weights = ps + turn * (S::kRows * kPStride);
     const float lv[2] = {log2_above(vs.x), log2_above(vs.y)};
     f32x2 part[NR];
-    bool sent = false;
-    auto send = [&]() {
-      sent = true;
-      if (to_send <= 1) {
-        fence_proxy_async_smem();
-        if (to_send == 0) send_keys(stage);
-        else send_values(stage == 0 ? kStages - 1 : stage - 1);
-      }
-      to_send = (to_send + 1) & 3;
-    };
     for (bool raised = false;; raised = true) {
       // (a piece's first tile has no references yet)
       if (raised || !first) {
@@ -684,9 +705,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
           *reinterpret_cast<__half2*>(to) = __floats2half2_rn(w[0], w[2]);
           *reinterpret_cast<__half2*>(to + kPStride) = __floats2half2_rn(w[1], w[3]);
         }
-        // (behind this barrier all warps are done with this tile's keys and the values of the one before)
+        // (behind this barrier all warps are done with the tile before this one)
         const bool raise = __syncthreads_or(fmaxf(most[0] + lv[0], most[1] + lv[1]) > kMostWeight) != 0;
-        if (!sent) send();
         if (raised || !raise) break;
       }
       // References of the rows concerned up, what stands under them down.  Each
@@ -706,24 +726,33 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
         }
       }
       __syncthreads();
-      if (!sent) send();      // a first tile's: the barrier was this one
-      if (warp == 0 && lane < S::kRows) {
+      float most = kNone, over = -INFINITY;
+      if (lane < S::kRows) {
         float2 of[kAttnWarps];
-        float top = kNone, over = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kAttnWarps; ++w) {
           of[w] = pairs[w * S::kRows + lane];
-          top = fmaxf(top, of[w].x);
+          most = fmaxf(most, of[w].x);
         }
 #pragma unroll
-        for (int w = 0; w < kAttnWarps; ++w) over = fmaxf(over, (of[w].x - top) + of[w].y);
-        float* const ref = reinterpret_cast<float*>(refs + (lane >> 1)) + (lane & 1);
-        const float m = ref[0], c = ref[2];
-        const bool up = (top + m) + (over - c) > kLiftWeight;
+        for (int w = 0; w < kAttnWarps; ++w) over = fmaxf(over, (of[w].x - most) + of[w].y);
         over -= kNewWeight;
-        keeps[lane] = up ? ex2((c - over) - (top + m)) : 1.0f;
+      }
+      float* const ref = reinterpret_cast<float*>(refs + (lane >> 1)) + (lane & 1);
+      if (first) {      // (each warp writes the same; nothing stands under it)
+        if (lane < S::kRows) {
+          ref[0] = -most;
+          ref[2] = over == -INFINITY ? 0.0f : over;
+        }
+        __syncwarp();
+        continue;
+      }
+      if (warp == 0 && lane < S::kRows) {
+        const float m = ref[0], c = ref[2];
+        const bool up = (most + m) + (over + kNewWeight - c) > kLiftWeight;
+        keeps[lane] = up ? ex2((c - over) - (most + m)) : 1.0f;
         if (up) {
-          ref[0] = -top;
+          ref[0] = -most;
           ref[2] = over;
         }
       }
@@ -739,15 +768,15 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
         }
       }
     }
+    fence_proxy_async_smem();
+    send(tile);
 #pragma unroll
     for (int r = 0; r < NR; ++r) sum[r] = add2(sum[r], part[r]);
     // ---- outputs
-    ok = ok && mbar_wait(smem_u32(&full_v[stage]), phase, ctx, 92);
-    const uint8_t* const tile_values = smem + S::kVRing + stage * kTileBlocks * kVCodes;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int in_tile = 4 * half + k;
-      const uint8_t* const v = tile_values + in_tile * kVCodes + 4 * q * kHeadDim + 32 * (quarter ^ q) + 4 * g;
+      const int in_tile = 4 * half + k, of = slot + in_tile;
+      const uint8_t* const v = smem + (of >= kSlots ? of - kSlots : of) * kCacheBlock + kVCodes + 4 * q * kHeadDim + 32 * (quarter ^ q) + 4 * g;
       uint32_t w[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) w[e] = *reinterpret_cast<const uint32_t*>(v + e * kHeadDim);
@@ -810,7 +839,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
         for (int r = 0; r < NR; ++r) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const int in_tile = 8 * r + 2 * q + c, to = tos[in_tile];
+            const int in_tile = 8 * r + 2 * q + c, to = tos[odd * S::kRows + in_tile];
             const float f = __shfl_sync(kAll, back, in_tile);
             const float4 v = *reinterpret_cast<const float4*>(os + in_tile * kHeadDim + 32 * quarter + 4 * g);
             const float4 sums = make_float4((o[0][r][c] + v.x) * f, (o[0][r][2 + c] + v.y) * f, (o[1][r][c] + v.z) * f,
@@ -824,12 +853,10 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
       }
       if (piece.final) break;
       get = (get + 1) % kPieces;
-      __syncthreads();      // the rows' places are read
     }
-    if (++stage == kStages) {
-      stage = 0;
-      phase ^= 1;
-    }
+    ++tile;
+    slot += kTileBlocks;
+    if (slot >= kSlots) slot -= kSlots;
   }
   if (!ok) {      // what copies are still on their way land before the block ends
     const uint64_t t0 = globaltimer_ns();
