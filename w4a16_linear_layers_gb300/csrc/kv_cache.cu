@@ -9,17 +9,20 @@
 // scales.  rho is a factor of the whole head, so codes do not depend on it.
 //
 // Codes are those of exact arithmetic.  The fp32 quotient t = y (127 / a) is
-// less than 2^-13 off (y by 2.42 half steps of a, as the products of a rotation
-// are at most sqrt(2) a, a by as much, 127 / a by one, the product by one:
-// 127 * 6.9 * 2^-24 = 2^-14.2).  Where t is further than that from a
-// half-integer, its rounding is the exact one's; elsewhere (one element in
-// 4096, and every x = a / 2 of a value head) y and a are formed again as
-// unevaluated pairs of fp32 values (two-product and two-sum, error about 2^-46)
-// and 254 |y| is compared with the odd multiple of a.
+// less than 2^-14 off (y by 2.42 half steps of a, as the products of a rotation
+// are at most sqrt(2) a, a by as much, 127 / a by three: 127 * 7.84 * 2^-24 =
+// 2^-14.04).  Where t is further than that from a half-integer, its rounding is
+// the exact one's; for the rest (one element in 8192) y and a are formed again
+// as unevaluated pairs of fp32 values (two-product and two-sum, error about
+// 2^-46) and 254 |y| is compared with the odd multiple of a.  A head that is
+// neither normalised nor rotated is bf16: there a half-integer is met exactly
+// (every x = a / 2) or missed by 2^-17 of t, and t from 127 / a as a pair of
+// fp32 values rounds as the exact one does.
 //
-// A half warp holds a head, 8 components a lane, so that a rotation's partner
-// is R/16 lanes away and reductions take four shuffles; a warp goes through
-// heads of one row two at a time, with the rotation's factors in registers.
+// A quarter warp holds a head, 16 components a lane in two vectors of 8, which
+// are each other's partners in the rotation: nothing passes between lanes but
+// three steps of a reduction.  A warp goes through heads of one row four at a
+// time, the next four on their way, with the rotation's factors in registers.
 #include "f32x2.cuh"
 #include "kv_cache.cuh"
 
@@ -29,27 +32,28 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
+constexpr float kSure = 0.5f - 0x1p-14f;   // quotients this near their codes round as the exact ones
 
-// the larger of |a| and b; NaN where either is
-__device__ __forceinline__ float max_abs(float a, float b) {
+// the largest of |a|, |b| and |c|; NaN where one is
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
   float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(fabsf(a)), "f"(b));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 
-// reductions over a head's 16 lanes
+// reductions over a head's 8 lanes
 __device__ __forceinline__ float head_sum(float v) {
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
   return v;
 }
 __device__ __forceinline__ float head_max(float v) {
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) v = max_abs(__shfl_xor_sync(kAll, v, o), v);
+  for (int o = 4; o > 0; o >>= 1) v = max_abs(__shfl_xor_sync(kAll, v, o), v, v);
   return v;
 }
 
-// a lane's 8 components, two at a time
+// 8 components, two at a time
 struct Part {
   f32x2 v[4];
   __device__ __forceinline__ void fill(float x) {
@@ -70,61 +74,50 @@ struct Part {
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], pack2(x, x));
   }
-  __device__ __forceinline__ float square_sum() const {
-    f32x2 s = mul2(v[0], v[0]);
-#pragma unroll
-    for (int i = 1; i < 4; ++i) s = fma2(v[i], v[i], s);
-    float lo, hi;
-    unpack2(s, lo, hi);
-    return lo + hi;
-  }
   __device__ __forceinline__ float top() const {
-    float m = 0.0f;
+    float f[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float lo, hi;
-      unpack2(v[i], lo, hi);
-      m = max_abs(lo, max_abs(hi, m));
-    }
-    return m;
-  }
-  __device__ __forceinline__ float get(int e) const {
-    float lo, hi;
-    unpack2(v[e >> 1], lo, hi);
-    return (e & 1) ? hi : lo;
+    for (int i = 0; i < 4; ++i) unpack2(v[i], f[2 * i], f[2 * i + 1]);
+    return max_abs(max_abs(f[0], f[1], f[2]), max_abs(f[3], f[4], f[5]), max_abs(f[6], f[7], f[7]));
   }
 };
 
-// Factors of a lane's components in the rotation: y = u * own + partner * other.
+// A lane's two vectors of a head's 16: with the first R/2 components turned
+// against the next R/2, lanes below R/16 hold partners, the others neighbours
+// of the rest.
+struct Place {
+  int at[2];            // vectors of 8 components
+  bool turned;
+  __device__ __forceinline__ Place(int R, int lane) {
+    const int l = lane & 7, half = R >> 4;
+    turned = l < half;
+    at[0] = turned ? l : 2 * l;
+    at[1] = turned ? l + half : 2 * l + 1;
+  }
+};
+
+// cosines and sines of a lane's first vector: y0 = u0 c - u1 s, y1 = u1 c + u0 s
 struct Turn {
-  Part own, other;
-  __device__ __forceinline__ Part apply(const Part& u, const Part& partner) const {
-    Part y;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) y.v[i] = fma2(partner.v[i], other.v[i], mul2(u.v[i], own.v[i]));
-    return y;
-  }
+  Part c, s;
 };
 
-__device__ __forceinline__ Turn load_turn(const KvWriteArgs& a, int64_t row, int pos, int i) {
+__device__ __forceinline__ Turn load_turn(const KvWriteArgs& a, int64_t row, int pos, const Place& place) {
   Turn t;
-  t.own.fill(1.0f);
-  t.other.fill(0.0f);
-  const int R = static_cast<int>(a.R);
-  if (8 * i >= R) return t;
-  const int half = R / 2;
-  const bool second = 8 * i >= half;
-  const int pair0 = second ? 8 * i - half : 8 * i;
+  t.c.fill(1.0f);
+  t.s.fill(0.0f);
+  if (!place.turned) return t;
+  const int R = static_cast<int>(a.R), half = R / 2;
+  const int pair0 = 8 * place.at[0];
   const int last = static_cast<int>(a.P) - 1;
-  float c[8], s[8];
   if (a.A <= 1 || a.positions == nullptr) {
     const int at = min(max(a.positions == nullptr ? pos : __ldg(a.positions + row), 0), last);
     const float4* const p = reinterpret_cast<const float4*>(a.cos_sin + static_cast<int64_t>(at) * R + pair0);
     const float4 c0 = __ldg(p), c1 = __ldg(p + 1), s0 = __ldg(p + half / 4), s1 = __ldg(p + half / 4 + 1);
-    c[0] = c0.x, c[1] = c0.y, c[2] = c0.z, c[3] = c0.w, c[4] = c1.x, c[5] = c1.y, c[6] = c1.z, c[7] = c1.w;
-    s[0] = s0.x, s[1] = s0.y, s[2] = s0.z, s[3] = s0.w, s[4] = s1.x, s[5] = s1.y, s[6] = s1.z, s[7] = s1.w;
+    t.c.v[0] = pack2(c0.x, c0.y), t.c.v[1] = pack2(c0.z, c0.w), t.c.v[2] = pack2(c1.x, c1.y), t.c.v[3] = pack2(c1.z, c1.w);
+    t.s.v[0] = pack2(s0.x, s0.y), t.s.v[1] = pack2(s0.z, s0.w), t.s.v[2] = pack2(s1.x, s1.y), t.s.v[3] = pack2(s1.z, s1.w);
   } else {
     const int64_t rows = a.c.B * a.T;
+    float c[8], s[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int axis = min(static_cast<int>(__ldg(a.axes + pair0 + e)), static_cast<int>(a.A) - 1);
@@ -133,13 +126,45 @@ __device__ __forceinline__ Turn load_turn(const KvWriteArgs& a, int64_t row, int
       c[e] = __ldg(p);
       s[e] = __ldg(p + half);
     }
-  }
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    t.own.v[e] = pack2(c[2 * e], c[2 * e + 1]);
-    t.other.v[e] = second ? pack2(s[2 * e], s[2 * e + 1]) : pack2(-s[2 * e], -s[2 * e + 1]);
+    for (int e = 0; e < 4; ++e) {
+      t.c.v[e] = pack2(c[2 * e], c[2 * e + 1]);
+      t.s.v[e] = pack2(s[2 * e], s[2 * e + 1]);
+    }
   }
   return t;
+}
+
+__device__ __forceinline__ void load_gain(const uint16_t* gamma, const Place& place, Part gain[2]) {
+#pragma unroll
+  for (int w = 0; w < 2; ++w) gain[w].widen(__ldg(reinterpret_cast<const uint4*>(gamma) + place.at[w]));
+}
+
+// u0 c - u1 s and u1 c + u0 s
+__device__ __forceinline__ void turn_heads(const Part u[2], const Turn& t, Part y[2]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float u_lo, u_hi, s_lo, s_hi, q_lo, q_hi;
+    unpack2(u[1].v[i], u_lo, u_hi);
+    unpack2(t.s.v[i], s_lo, s_hi);
+    unpack2(mul2(u[0].v[i], t.c.v[i]), q_lo, q_hi);
+    const f32x2 second = fma2(u[0].v[i], t.s.v[i], mul2(u[1].v[i], t.c.v[i]));
+    y[0].v[i] = pack2(__fmaf_rn(-u_lo, s_lo, q_lo), __fmaf_rn(-u_hi, s_hi, q_hi));   // (only these have a sign for free)
+    y[1].v[i] = second;
+  }
+}
+
+// four low bytes
+__device__ __forceinline__ uint32_t low_bytes(const float m[4]) {
+  return prmt(prmt(__float_as_uint(m[0]), __float_as_uint(m[1]), 0x0040u), prmt(__float_as_uint(m[2]), __float_as_uint(m[3]), 0x0040u),
+              0x5410u);
+}
+
+// 1 / x, two half steps off at most for what is above 2^-100
+__device__ __forceinline__ float rcp(float x) {
+  float d;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(x));
+  return d;
 }
 
 struct Pair {
@@ -157,183 +182,236 @@ __device__ __forceinline__ Pair exact_turn(float u, float c, float p, float s) {
   return {hi, __fsub_rn(l, __fsub_rn(hi, h))};
 }
 
-// The 8 codes of a lane, decided exactly (all lanes of the warp take part).
-__device__ void exact_codes(const Part& u, const Part& partner, const Turn& turn, int code[8]) {
-  Pair y[8];
-  float top = 0.0f;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    y[e] = exact_turn(u.get(e), turn.own.get(e), partner.get(e), turn.other.get(e));
-    if (y[e].hi < 0.0f) y[e].lo = -y[e].lo;      // of |y| from here on
-    top = fmaxf(top, fabsf(y[e].hi));
+__device__ __forceinline__ float bf16_at(const uint16_t* p) { return __uint_as_float(static_cast<uint32_t>(__ldg(p)) << 16); }
+
+// Component e of a lane's 16 of the head at x, times `scaled`, as an
+// unevaluated pair; formed again from memory, as few are asked for.
+__device__ __forceinline__ Pair exact_component(const KvWriteArgs& a, uint32_t row, int pos, const uint16_t* x, const uint16_t* gamma,
+                                                bool turned, const Place& place, int e, float scaled) {
+  const int i = e & 7, d0 = 8 * place.at[0] + i, d1 = 8 * place.at[1] + i;
+  // (the scaling first: a subnormal product would lose bits)
+  float u0 = bf16_at(x + d0) * scaled, u1 = bf16_at(x + d1) * scaled;
+  if (gamma != nullptr) u0 *= bf16_at(gamma + d0), u1 *= bf16_at(gamma + d1);
+  if (!turned) return {e < 8 ? u0 : u1, 0.0f};
+  const int R = static_cast<int>(a.R);
+  int at = pos;
+  if (a.positions != nullptr) {
+    const int axis = a.A <= 1 ? 0 : min(static_cast<int>(__ldg(a.axes + d0)), static_cast<int>(a.A) - 1);
+    at = __ldg(a.positions + axis * (a.c.B * a.T) + row);
   }
-  top = head_max(top);
-  float low = -INFINITY;
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (fabsf(y[e].hi) == top) low = fmaxf(low, y[e].lo);
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) low = fmaxf(low, __shfl_xor_sync(kAll, low, o));
-  const float r = __fdiv_rn(127.0f, top);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float h = fabsf(y[e].hi);
-    const float t = __fmul_rn(h, r);
-    const float below = floorf(t);
-    float n = rintf(t);
-    if (fabsf(t - below - 0.5f) < 0x1p-12f) {
-      const float odd = __fmaf_rn(2.0f, below, 1.0f);
-      const float p = __fmul_rn(254.0f, h), pe = __fmaf_rn(254.0f, h, -p);
-      const float q = __fmul_rn(odd, top), qe = __fmaf_rn(odd, top, -q);
-      const float d = __fadd_rn(__fsub_rn(p, q), __fadd_rn(__fsub_rn(pe, qe), __fsub_rn(__fmul_rn(254.0f, y[e].lo), __fmul_rn(odd, low))));
-      n = d > 0.0f ? below + 1.0f : d < 0.0f ? below : 2.0f * rintf(0.5f * (below + 0.5f));
-    }
-    code[e] = static_cast<int>(y[e].hi < 0.0f ? -n : n);
-  }
+  at = min(max(at, 0), static_cast<int>(a.P) - 1);
+  const float* const p = a.cos_sin + static_cast<int64_t>(at) * R + d0;
+  const float c = __ldg(p), s = __ldg(p + R / 2);
+  return e < 8 ? exact_turn(u0, c, u1, -s) : exact_turn(u1, c, u0, s);
 }
 
-// One unit of a warp: `per` pairs of heads of a row, of the row's `chunks` such.
-// Query, key and value heads are paired among themselves.
-__global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvWriteArgs a, int chunks, int per) {
+// One unit of a warp: `per` groups of four heads of a row, of the row's `chunks`
+// such.  Query, key and value heads are grouped among themselves.
+__global__ void __launch_bounds__(kThreads, 5) kv_write_kernel(const __grid_constant__ KvWriteArgs a, uint32_t chunks, int per) {
   const int lane = threadIdx.x & 31;
-  const int i = lane & 15;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
   grid_dep_launch();
   grid_dep_wait();
-  const int64_t row = unit / chunks;
+  const uint32_t row = unit / chunks;
   if (row >= a.c.B * a.T) return;
-  const int64_t b = row / a.T;
-  const int t = static_cast<int>(row - b * a.T);
+  const uint32_t b = row / static_cast<uint32_t>(a.T);
+  const int t = static_cast<int>(row - b * static_cast<uint32_t>(a.T));
   const int q_heads = static_cast<int>(a.q_heads), kv_heads = static_cast<int>(a.c.kv_heads);
-  const int q_pairs = (q_heads + 1) / 2, kv_pairs = (kv_heads + 1) / 2;
+  const int q_groups = (q_heads + 3) / 4, kv_groups = (kv_heads + 3) / 4;
   const SeqLen seq = seq_len(a.c, b, a.T);
   if (t >= seq.fresh) return;
   const int pos = seq.len - seq.fresh + t;
   const int first = static_cast<int>(unit - row * chunks) * per;
-  const int last = min(first + per, q_pairs + 2 * kv_pairs);
-  const uint16_t* const in = a.qkv + row * (q_heads + 2 * kv_heads) * kHeadDim + 8 * i;
+  const int last = min(first + per, q_groups + 2 * kv_groups);
+  const Place place(static_cast<int>(a.R), lane);
+  const uint16_t* const in = a.qkv + static_cast<int64_t>(row) * (q_heads + 2 * kv_heads) * kHeadDim;
 
-  // where a pair's head of this half warp is: its kind, number and place in the row
+  // where a group's head of this quarter warp is: its kind, number and place in the row
   struct Head {
-    int kind, at;
+    int kind, at, row_head;
     bool there;
   };
-  auto head_of = [&](int pair) {
+  auto head_of = [&](int group) {
     Head h;
-    h.kind = pair < q_pairs ? 0 : pair < q_pairs + kv_pairs ? 1 : 2;
-    h.at = 2 * (pair - (h.kind == 0 ? 0 : h.kind == 1 ? q_pairs : q_pairs + kv_pairs)) + (lane >> 4);
+    h.kind = group < q_groups ? 0 : group < q_groups + kv_groups ? 1 : 2;
+    h.at = 4 * (group - (h.kind == 0 ? 0 : h.kind == 1 ? q_groups : q_groups + kv_groups)) + (lane >> 3);
     h.there = h.at < (h.kind == 0 ? q_heads : kv_heads);
+    h.row_head = h.at + (h.kind == 0 ? 0 : h.kind == 1 ? q_heads : q_heads + kv_heads);
     return h;
   };
-  auto load = [&](const Head& h) {
-    if (!h.there) return make_uint4(0, 0, 0, 0);
-    return __ldg(reinterpret_cast<const uint4*>(in + (h.at + (h.kind == 0 ? 0 : h.kind == 1 ? q_heads : q_heads + kv_heads)) * kHeadDim));
+  auto load = [&](const Head& h, uint4 x[2]) {
+    const uint4* const p = reinterpret_cast<const uint4*>(in + h.row_head * kHeadDim);
+#pragma unroll
+    for (int w = 0; w < 2; ++w) x[w] = h.there ? __ldg(p + place.at[w]) : make_uint4(0, 0, 0, 0);
   };
 
   Head head = head_of(first);
-  uint4 next = load(head);
+  uint4 next[2];
+  load(head, next);
   uint8_t* block = nullptr;       // of head 0
-  if (last > q_pairs) block = cache_block(a.c, b, 0, pos >> 4);
+  if (last > q_groups) block = cache_block(a.c, b, 0, pos >> 4);
   const int64_t head_step = (a.c.page_size >> 4) * kCacheBlock;
   const bool turned = a.R != 0;
-  const Turn turn = load_turn(a, row, pos, i);
-  const int step = static_cast<int>(a.R) >> 4;
-  const int partner_lane = i < step ? lane + step : i < 2 * step ? lane - step : lane;
-  Part gain, partner_gain;
+  Turn turn;
+  if (turned) turn = load_turn(a, row, pos, place);
+  Part gain[2];
   int gained = -1;                // the kind that the gains are of
 
-  for (int pair = first; pair < last; ++pair) {
+  for (int group = first; group < last; ++group) {
     const Head h = head;
-    const uint4 x = next;
-    if (pair + 1 < last) {
-      head = head_of(pair + 1);
-      next = load(head);
+    const uint4 x0 = next[0], x1 = next[1];
+    if (group + 1 < last) {
+      head = head_of(group + 1);
+      load(head, next);
     }
     const uint16_t* const gamma = h.kind == 0 ? a.q_gamma : h.kind == 1 ? a.k_gamma : nullptr;
     if (gamma != nullptr && gained != h.kind) {
       gained = h.kind;
-      gain.widen(__ldg(reinterpret_cast<const uint4*>(gamma) + i));
-      partner_gain.widen(__ldg(reinterpret_cast<const uint4*>(gamma) + (partner_lane & 15)));
+      load_gain(gamma, place, gain);
     }
-    Part u;
-    u.widen(x);
+    Part y[2];
+    y[0].widen(x0);
+    y[1].widen(x1);
     float rho = 1.0f;
     if (gamma != nullptr) {
-      const float sum = head_sum(u.square_sum());
+      f32x2 two = mul2(y[0].v[0], y[0].v[0]);
+#pragma unroll
+      for (int e = 1; e < 8; ++e) two = fma2(y[e >> 2].v[e & 3], y[e >> 2].v[e & 3], two);
+      float lo, hi;
+      unpack2(two, lo, hi);
+      const float sum = head_sum(lo + hi);
       // a head of zeros stays one with eps = 0; a sum past fp32's range gives NaN
-      rho = sum == 0.0f ? 0.0f : sum < INFINITY ? __frsqrt_rn(__fmaf_rn(sum, 1.0f / kHeadDim, a.eps)) : NAN;
-      u.times(gain);
+      rho = sum == 0.0f ? 0.0f : sum < INFINITY ? rsqrtf(__fmaf_rn(sum, 1.0f / kHeadDim, a.eps)) : NAN;
+      y[0].times(gain[0]);
+      y[1].times(gain[1]);
     }
-    Part partner = u;
-    Part y = u;
     if (turned && h.kind != 2) {
-      uint4 w;
-      w.x = __shfl_sync(kAll, x.x, partner_lane);
-      w.y = __shfl_sync(kAll, x.y, partner_lane);
-      w.z = __shfl_sync(kAll, x.z, partner_lane);
-      w.w = __shfl_sync(kAll, x.w, partner_lane);
-      partner.widen(w);
-      if (gamma != nullptr) partner.times(partner_gain);
-      y = turn.apply(u, partner);
+      const Part u[2] = {y[0], y[1]};
+      turn_heads(u, turn, y);
     }
     if (h.kind == 0) {
-      if (gamma != nullptr) y.times(rho);
-      if (h.there)
-        *reinterpret_cast<uint4*>(a.q + (row * q_heads + h.at) * kHeadDim + 8 * i) =
-            make_uint4(narrow2(y.v[0]), narrow2(y.v[1]), narrow2(y.v[2]), narrow2(y.v[3]));
+      if (gamma != nullptr) {
+        y[0].times(rho);
+        y[1].times(rho);
+      }
+      if (h.there) {
+        uint4* const to = reinterpret_cast<uint4*>(a.q + (static_cast<int64_t>(row) * q_heads + h.at) * kHeadDim);
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+          to[place.at[w]] = make_uint4(narrow2(y[w].v[0]), narrow2(y[w].v[1]), narrow2(y[w].v[2]), narrow2(y[w].v[3]));
+      }
       continue;
     }
 
-    float top = head_max(y.top());
-    float scaled = 1.0f;
-    if (__any_sync(kAll, (top > 0.0f && top < 0x1p-60f) || (top > 0x1p100f && top < INFINITY))) {
-      // where 127 / a or the pairs' remainders would leave fp32's range
-      scaled = top < 0x1p-60f ? 0x1p60f : top > 0x1p100f ? 0x1p-30f : 1.0f;
-      u.times(scaled);
-      partner.times(scaled);
-      y = u;
-      if (turned && h.kind != 2) y = turn.apply(u, partner);
-      top = head_max(y.top());
-    }
+    float top = head_max(max_abs(y[0].top(), y[1].top(), 0.0f));
     const bool good = top > 0.0f && top < INFINITY;
-    const float r = good ? __fdiv_rn(127.0f, top) : 0.0f;
-    const f32x2 r2 = pack2(r, r);
+    const float inverse = rcp(top);
+    const float r = good ? 127.0f * inverse : 0.0f;
     constexpr float kMagic = 12582912.0f + 128.0f;   // its low byte becomes code + 128
-    const f32x2 magic = pack2(kMagic, kMagic);
-    uint32_t m[8];
-    float far = 0.0f;
+    const f32x2 magic = pack2(kMagic, kMagic), minus = pack2(-1.0f, -1.0f), r2 = pack2(r, r);
+    uint32_t codes[4];
+    const bool out_of_range = good && (top < 0x1p-60f || top > 0x1p100f);
+    float far = 0.0f;               // the largest distance of a quotient from its code
+    if (gamma == nullptr && !(turned && h.kind == 1)) {
+      const float rest = good ? __fmul_rn(__fmaf_rn(-top, r, 127.0f), inverse) : 0.0f;
+      const f32x2 rest2 = pack2(rest, rest);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const f32x2 n = fma2(y.v[e], r2, magic);
-      const f32x2 back = sub2(n, magic);
-      const f32x2 d = fma2(y.v[e], r2, mul2(back, pack2(-1.0f, -1.0f)));
-      float lo, hi;
-      unpack2(d, lo, hi);
-      far = fmaxf(far, fmaxf(fabsf(lo), fabsf(hi)));
-      unpack2(n, lo, hi);
-      m[2 * e] = __float_as_uint(lo);
-      m[2 * e + 1] = __float_as_uint(hi);
+      for (int w = 0; w < 4; ++w) {
+        float m[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const f32x2 v = y[w >> 1].v[2 * (w & 1) + i];
+          unpack2(add2(fma2(v, r2, mul2(v, rest2)), magic), m[2 * i], m[2 * i + 1]);
+        }
+        codes[w] = low_bytes(m);
+      }
+    } else {
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        float m[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const f32x2 v = y[w >> 1].v[2 * (w & 1) + i];
+          const f32x2 n = fma2(v, r2, magic);
+          // v r - (n - magic), rounded once: the sum in brackets is exact
+          const f32x2 d = fma2(v, r2, fma2(n, minus, magic));
+          float lo, hi;
+          unpack2(d, lo, hi);
+          far = max_abs(far, lo, hi);
+          unpack2(n, m[2 * i], m[2 * i + 1]);
+        }
+        codes[w] = low_bytes(m);
+      }
     }
-    if (__any_sync(kAll, good && far > 0.5f - 0x1p-13f)) {
-      Turn none;
-      none.own.fill(1.0f);
-      none.other.fill(0.0f);
-      int code[8];
-      exact_codes(u, partner, turned && h.kind != 2 ? turn : none, code);
-      if (good) {
+    float back = 1.0f;
+    if (__any_sync(kAll, good && (far > kSure || out_of_range))) {
+      // Elements to decide (bits 0..15), and those that may be the largest: all of
+      // a head where 127 / a or the pairs' remainders would leave fp32's range.
+      const float scaled = !out_of_range ? 1.0f : top < 1.0f ? 0x1p60f : 0x1p-30f;
+      uint32_t unsure = 0, tops = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m[e] = static_cast<uint32_t>(code[e] + 128);
+      for (int e = 0; e < 16; ++e) {
+        float lo, hi;
+        unpack2(y[e >> 3].v[(e & 7) >> 1], lo, hi);
+        const float v = fabsf((e & 1) ? hi : lo);
+        const float n = __fmaf_rn(v, r, kMagic);
+        if (out_of_range || fabsf(__fmaf_rn(v, r, kMagic - n)) > kSure) unsure |= 1u << e;
+        if (out_of_range || v >= top * (1.0f - 0x1p-20f)) tops |= 1u << e;
+      }
+      const float head_far = head_max(far);
+      if (!good || !(head_far > kSure || out_of_range)) unsure = tops = 0;
+      const uint16_t* const x = in + h.row_head * kHeadDim;
+      const bool rotated = place.turned && h.kind == 1;
+      Pair most{0.0f, -INFINITY};   // of the head, as a pair
+      for (; __any_sync(kAll, tops != 0); tops &= tops - 1) {
+        if (tops == 0) continue;
+        Pair v = exact_component(a, row, pos, x, gamma, rotated, place, __ffs(tops) - 1, scaled);
+        if (v.hi < 0.0f) v.lo = -v.lo, v.hi = -v.hi;
+        if (v.hi > most.hi || (v.hi == most.hi && v.lo > most.lo)) most = v;
+      }
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) {
+        const Pair v{__shfl_xor_sync(kAll, most.hi, o), __shfl_xor_sync(kAll, most.lo, o)};
+        if (v.hi > most.hi || (v.hi == most.hi && v.lo > most.lo)) most = v;
+      }
+      const float per_top = __fdiv_rn(127.0f, most.hi);
+      for (; __any_sync(kAll, unsure != 0); unsure &= unsure - 1) {
+        if (unsure == 0) continue;
+        const int e = __ffs(unsure) - 1;
+        Pair v = exact_component(a, row, pos, x, gamma, rotated, place, e, scaled);
+        const bool negative = v.hi < 0.0f;
+        if (negative) v.lo = -v.lo, v.hi = -v.hi;
+        const float t = __fmul_rn(v.hi, per_top);
+        const float below = floorf(t);
+        float n = rintf(t);
+        if (fabsf(t - below - 0.5f) < 0x1p-12f) {
+          const float odd = __fmaf_rn(2.0f, below, 1.0f);
+          const float p = __fmul_rn(254.0f, v.hi), pe = __fmaf_rn(254.0f, v.hi, -p);
+          const float q = __fmul_rn(odd, most.hi), qe = __fmaf_rn(odd, most.hi, -q);
+          const float d = __fadd_rn(__fsub_rn(p, q), __fadd_rn(__fsub_rn(pe, qe), __fsub_rn(__fmul_rn(254.0f, v.lo), __fmul_rn(odd, most.lo))));
+          n = d > 0.0f ? below + 1.0f : d < 0.0f ? below : 2.0f * rintf(0.5f * (below + 0.5f));
+        }
+        const uint32_t code = static_cast<uint32_t>(static_cast<int>(negative ? -n : n) + 128);
+        const int shift = 8 * (e & 3);
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+          if (e >> 2 == w) codes[w] = (codes[w] & ~(0xFFu << shift)) | code << shift;
+      }
+      if (out_of_range) {
+        top = most.hi;
+        back = 1.0f / scaled;
       }
     }
     if (!h.there || block == nullptr) continue;
     uint8_t* const to = block + h.at * head_step;
-    const int place = pos & 15;
-    const uint32_t lo = prmt(prmt(m[0], m[1], 0x0040u), prmt(m[2], m[3], 0x0040u), 0x5410u);
-    const uint32_t hi = prmt(prmt(m[4], m[5], 0x0040u), prmt(m[6], m[7], 0x0040u), 0x5410u);
-    *reinterpret_cast<uint2*>(to + (h.kind == 1 ? 0 : kVCodes) + place * kHeadDim + code_place(place, 8 * i)) = make_uint2(lo, hi);
-    if (i == 0) {
-      const float s = __fdiv_rn(__fmul_rn(top, rho), 127.0f) * (1.0f / scaled);
-      reinterpret_cast<float*>(to + (h.kind == 1 ? kKScales : kVScales))[place] =
+    const int place_of = pos & 15;
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+      *reinterpret_cast<uint2*>(to + (h.kind == 1 ? 0 : kVCodes) + place_of * kHeadDim + code_place(place_of, 8 * place.at[w])) =
+          make_uint2(codes[2 * w], codes[2 * w + 1]);
+    if ((lane & 7) == 0) {
+      const float s = __fmul_rn(__fmul_rn(top, rho), 1.0f / 127.0f) * back;
+      reinterpret_cast<float*>(to + (h.kind == 1 ? kKScales : kVScales))[place_of] =
           top == 0.0f ? 0.0f : good && s < INFINITY ? s : NAN;
     }
   }
@@ -406,15 +484,16 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const CacheArgs c, co
 
 cudaError_t launch_kv_write(const KvWriteArgs& a, int sm_count, cudaStream_t stream) {
   const int64_t rows = a.c.B * a.T;
-  const int64_t pairs = (a.q_heads + 1) / 2 + 2 * ((a.c.kv_heads + 1) / 2);
-  // A warp takes one pair of heads until that fills the SMs' warps, then more
+  const int64_t groups = (a.q_heads + 3) / 4 + 2 * ((a.c.kv_heads + 3) / 4);
+  // A warp takes one group of heads until that fills the SMs' warps, then more
   // of a row, which share the rotation's factors.
-  int per = 1;
-  while (per < 8 && rows * ((pairs + per - 1) / per) > 2LL * 48 * sm_count) per *= 2;
-  const int64_t chunks = (pairs + per - 1) / per;
+  int64_t per = 1;
+  while (per < 16 && rows * ((groups + per - 1) / per) > 2LL * 24 * sm_count) per *= 2;
+  const int64_t chunks = (groups + per - 1) / per;
   const int64_t blocks = (rows * chunks + kWarps - 1) / kWarps;
-  if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
-  return launch_pdl(kv_write_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, a, static_cast<int>(chunks), per);
+  if (blocks > 0xFFFFFFFFLL / kWarps || blocks > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
+  return launch_pdl(kv_write_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, a, static_cast<uint32_t>(chunks),
+                    static_cast<int>(per));
 }
 
 cudaError_t launch_kv_read(const CacheArgs& c, const int32_t* start, int64_t L, uint16_t* k, uint16_t* v,
