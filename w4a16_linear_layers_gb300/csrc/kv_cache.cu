@@ -23,6 +23,17 @@
 // are each other's partners in the rotation: nothing passes between lanes but
 // three steps of a reduction.  A warp goes through heads of one row four at a
 // time, the next four on their way, with the rotation's factors in registers.
+//
+// Long calls are bound by memory: 8192 rows of 32 + 16 heads take 40.6 us, 4.6 TB/s
+// of what has to move (32768 rows 5.4), and 36.8 us where nothing is normalised
+// or turned.  With a half warp a head, partners R/16 lanes away and whole heads
+// decided again where one code was near a half-integer it took 98.6.  Warps that
+// stay and take rows in turn took 42 to 46 us, two or three groups ahead 46 to 48;
+// 16 warps an SM 46, 24 with spilled registers 46 to 49.  Short calls are a chain
+// of three loads (length, angles, the rest) and take 3.9 us, 1.7 of them above an
+// empty launch.
+#include <type_traits>
+
 #include "f32x2.cuh"
 #include "kv_cache.cuh"
 
@@ -205,216 +216,225 @@ __device__ __forceinline__ Pair exact_component(const KvWriteArgs& a, uint32_t r
   return e < 8 ? exact_turn(u0, c, u1, -s) : exact_turn(u1, c, u0, s);
 }
 
-// One unit of a warp: `per` groups of four heads of a row, of the row's `chunks`
+// A unit of a warp is `per` groups of four heads of a row, of the row's `chunks`
 // such.  Query, key and value heads are grouped among themselves.
-__global__ void __launch_bounds__(kThreads, 5) kv_write_kernel(const __grid_constant__ KvWriteArgs a, uint32_t chunks, int per) {
+struct Split {
+  uint32_t per, chunks, q_groups, kv_groups;
+};
+
+__global__ void __launch_bounds__(kThreads, 5) kv_write_kernel(const __grid_constant__ KvWriteArgs a, const Split split) {
   const int lane = threadIdx.x & 31;
   const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
   grid_dep_launch();
   grid_dep_wait();
-  const uint32_t row = unit / chunks;
+  const uint32_t row = unit / split.chunks;
   if (row >= a.c.B * a.T) return;
+  const int q_heads = static_cast<int>(a.q_heads), kv_heads = static_cast<int>(a.c.kv_heads);
+  const int q_groups = split.q_groups, k_end = q_groups + split.kv_groups, groups = k_end + split.kv_groups;
+  const int first = static_cast<int>((unit - row * split.chunks) * split.per);
+  const int last = min(first + static_cast<int>(split.per), groups);
+  const Place place(static_cast<int>(a.R), lane);
+
+  // this quarter warp's head of the group whose components come next
+  int at;                         // its number among the heads of its kind
+  const uint16_t* x;
+  uint4 next[2];
+  auto load = [&](int heads) {
+#pragma unroll
+    for (int w = 0; w < 2; ++w) next[w] = at < heads ? __ldg(reinterpret_cast<const uint4*>(x) + place.at[w]) : make_uint4(0, 0, 0, 0);
+  };
+  auto enter = [&](int group) {
+    const bool query = group < q_groups, value = group >= k_end;
+    at = 4 * (group - (query ? 0 : value ? k_end : q_groups)) + (lane >> 3);
+    x = a.qkv + (static_cast<int64_t>(row) * (q_heads + 2 * kv_heads) + at + (query ? 0 : value ? q_heads + kv_heads : q_heads)) * kHeadDim;
+    load(query ? q_heads : kv_heads);
+  };
+
+  enter(first);                   // (of rows of padding too: they are in the buffer)
   const uint32_t b = row / static_cast<uint32_t>(a.T);
   const int t = static_cast<int>(row - b * static_cast<uint32_t>(a.T));
-  const int q_heads = static_cast<int>(a.q_heads), kv_heads = static_cast<int>(a.c.kv_heads);
-  const int q_groups = (q_heads + 3) / 4, kv_groups = (kv_heads + 3) / 4;
   const SeqLen seq = seq_len(a.c, b, a.T);
   if (t >= seq.fresh) return;
   const int pos = seq.len - seq.fresh + t;
-  const int first = static_cast<int>(unit - row * chunks) * per;
-  const int last = min(first + per, q_groups + 2 * kv_groups);
-  const Place place(static_cast<int>(a.R), lane);
-  const uint16_t* const in = a.qkv + static_cast<int64_t>(row) * (q_heads + 2 * kv_heads) * kHeadDim;
-
-  // where a group's head of this quarter warp is: its kind, number and place in the row
-  struct Head {
-    int kind, at, row_head;
-    bool there;
-  };
-  auto head_of = [&](int group) {
-    Head h;
-    h.kind = group < q_groups ? 0 : group < q_groups + kv_groups ? 1 : 2;
-    h.at = 4 * (group - (h.kind == 0 ? 0 : h.kind == 1 ? q_groups : q_groups + kv_groups)) + (lane >> 3);
-    h.there = h.at < (h.kind == 0 ? q_heads : kv_heads);
-    h.row_head = h.at + (h.kind == 0 ? 0 : h.kind == 1 ? q_heads : q_heads + kv_heads);
-    return h;
-  };
-  auto load = [&](const Head& h, uint4 x[2]) {
-    const uint4* const p = reinterpret_cast<const uint4*>(in + h.row_head * kHeadDim);
-#pragma unroll
-    for (int w = 0; w < 2; ++w) x[w] = h.there ? __ldg(p + place.at[w]) : make_uint4(0, 0, 0, 0);
-  };
-
-  Head head = head_of(first);
-  uint4 next[2];
-  load(head, next);
-  uint8_t* block = nullptr;       // of head 0
-  if (last > q_groups) block = cache_block(a.c, b, 0, pos >> 4);
-  const int64_t head_step = (a.c.page_size >> 4) * kCacheBlock;
   const bool turned = a.R != 0;
   Turn turn;
   if (turned) turn = load_turn(a, row, pos, place);
-  Part gain[2];
-  int gained = -1;                // the kind that the gains are of
+  const int place_of = pos & 15;
+  const int64_t head_step = (a.c.page_size >> 4) * kCacheBlock;
+  uint8_t* block = nullptr;       // of head 0
+  if (last > q_groups) block = cache_block(a.c, b, 0, pos >> 4);
 
-  for (int group = first; group < last; ++group) {
-    const Head h = head;
-    const uint4 x0 = next[0], x1 = next[1];
-    if (group + 1 < last) {
-      head = head_of(group + 1);
-      load(head, next);
-    }
-    const uint16_t* const gamma = h.kind == 0 ? a.q_gamma : h.kind == 1 ? a.k_gamma : nullptr;
-    if (gamma != nullptr && gained != h.kind) {
-      gained = h.kind;
-      load_gain(gamma, place, gain);
-    }
-    Part y[2];
-    y[0].widen(x0);
-    y[1].widen(x1);
-    float rho = 1.0f;
-    if (gamma != nullptr) {
-      f32x2 two = mul2(y[0].v[0], y[0].v[0]);
-#pragma unroll
-      for (int e = 1; e < 8; ++e) two = fma2(y[e >> 2].v[e & 3], y[e >> 2].v[e & 3], two);
-      float lo, hi;
-      unpack2(two, lo, hi);
-      const float sum = head_sum(lo + hi);
-      // a head of zeros stays one with eps = 0; a sum past fp32's range gives NaN
-      rho = sum == 0.0f ? 0.0f : sum < INFINITY ? rsqrtf(__fmaf_rn(sum, 1.0f / kHeadDim, a.eps)) : NAN;
-      y[0].times(gain[0]);
-      y[1].times(gain[1]);
-    }
-    if (turned && h.kind != 2) {
-      const Part u[2] = {y[0], y[1]};
-      turn_heads(u, turn, y);
-    }
-    if (h.kind == 0) {
-      if (gamma != nullptr) {
-        y[0].times(rho);
-        y[1].times(rho);
+  auto run = [&](auto kind_of) {
+    constexpr int kKind = decltype(kind_of)::value;
+    const int from = max(first, kKind == 0 ? 0 : kKind == 1 ? q_groups : k_end);
+    const int end = min(last, kKind == 0 ? q_groups : kKind == 1 ? k_end : groups);
+    if (from >= end) return;
+    const uint16_t* const gamma = kKind == 0 ? a.q_gamma : kKind == 1 ? a.k_gamma : nullptr;
+    Part gain[2];
+    if (gamma != nullptr) load_gain(gamma, place, gain);
+    // the head's place in q or in the cache (where that has one)
+    const bool placed = kKind == 0 || block != nullptr;
+    uint8_t* to = kKind == 0 ? reinterpret_cast<uint8_t*>(a.q + (static_cast<int64_t>(row) * q_heads + at) * kHeadDim)
+                             : (placed ? block : a.c.cache) + at * head_step + place_of * kHeadDim + (kKind == 1 ? 0 : kVCodes);
+    const int64_t step = kKind == 0 ? 4 * kHeadDim * 2 : 4 * head_step;
+    const int to_place[2] = {kKind == 0 ? 16 * place.at[0] : code_place(place_of, 8 * place.at[0]),
+                             kKind == 0 ? 16 * place.at[1] : code_place(place_of, 8 * place.at[1])};
+    const int heads = kKind == 0 ? q_heads : kv_heads;
+    for (int group = from; group < end; ++group, to += step) {
+      const uint4 x0 = next[0], x1 = next[1];
+      const bool there = at < heads;
+      const uint16_t* const head = x;
+      if (group + 1 < end) {
+        at += 4;
+        x += 4 * kHeadDim;
+        load(heads);
+      } else if (kKind < 2 && end < last) {
+        enter(end);
       }
-      if (h.there) {
-        uint4* const to = reinterpret_cast<uint4*>(a.q + (static_cast<int64_t>(row) * q_heads + h.at) * kHeadDim);
+      Part y[2];
+      y[0].widen(x0);
+      y[1].widen(x1);
+      float rho = 1.0f;
+      if (gamma != nullptr) {
+        f32x2 two = mul2(y[0].v[0], y[0].v[0]);
+#pragma unroll
+        for (int e = 1; e < 8; ++e) two = fma2(y[e >> 2].v[e & 3], y[e >> 2].v[e & 3], two);
+        float lo, hi;
+        unpack2(two, lo, hi);
+        const float sum = head_sum(lo + hi);
+        // a head of zeros stays one with eps = 0; a sum past fp32's range gives NaN
+        rho = sum == 0.0f ? 0.0f : sum < INFINITY ? rsqrtf(__fmaf_rn(sum, 1.0f / kHeadDim, a.eps)) : NAN;
+        y[0].times(gain[0]);
+        y[1].times(gain[1]);
+      }
+      if (turned && kKind != 2) {
+        const Part u[2] = {y[0], y[1]};
+        turn_heads(u, turn, y);
+      }
+      if constexpr (kKind == 0) {
+        if (gamma != nullptr) {
+          y[0].times(rho);
+          y[1].times(rho);
+        }
 #pragma unroll
         for (int w = 0; w < 2; ++w)
-          to[place.at[w]] = make_uint4(narrow2(y[w].v[0]), narrow2(y[w].v[1]), narrow2(y[w].v[2]), narrow2(y[w].v[3]));
+          if (there)
+            *reinterpret_cast<uint4*>(to + to_place[w]) =
+                make_uint4(narrow2(y[w].v[0]), narrow2(y[w].v[1]), narrow2(y[w].v[2]), narrow2(y[w].v[3]));
+        continue;
       }
-      continue;
-    }
-
-    float top = head_max(max_abs(y[0].top(), y[1].top(), 0.0f));
-    const bool good = top > 0.0f && top < INFINITY;
-    const float inverse = rcp(top);
-    const float r = good ? 127.0f * inverse : 0.0f;
-    constexpr float kMagic = 12582912.0f + 128.0f;   // its low byte becomes code + 128
-    const f32x2 magic = pack2(kMagic, kMagic), minus = pack2(-1.0f, -1.0f), r2 = pack2(r, r);
-    uint32_t codes[4];
-    const bool out_of_range = good && (top < 0x1p-60f || top > 0x1p100f);
-    float far = 0.0f;               // the largest distance of a quotient from its code
-    if (gamma == nullptr && !(turned && h.kind == 1)) {
-      const float rest = good ? __fmul_rn(__fmaf_rn(-top, r, 127.0f), inverse) : 0.0f;
-      const f32x2 rest2 = pack2(rest, rest);
+      float top = head_max(max_abs(y[0].top(), y[1].top(), 0.0f));
+      const bool good = top > 0.0f && top < INFINITY;
+      const float inverse = rcp(top);
+      const float r = good ? 127.0f * inverse : 0.0f;
+      constexpr float kMagic = 12582912.0f + 128.0f;   // its low byte becomes code + 128
+      const f32x2 magic = pack2(kMagic, kMagic), minus = pack2(-1.0f, -1.0f), r2 = pack2(r, r);
+      uint32_t codes[4];
+      const bool out_of_range = good && (top < 0x1p-60f || top > 0x1p100f);
+      float far = 0.0f;               // the largest distance of a quotient from its code
+      if (gamma == nullptr && !(turned && kKind == 1)) {
+        const float rest = good ? __fmul_rn(__fmaf_rn(-top, r, 127.0f), inverse) : 0.0f;
+        const f32x2 rest2 = pack2(rest, rest);
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        float m[4];
+        for (int w = 0; w < 4; ++w) {
+          float m[4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const f32x2 v = y[w >> 1].v[2 * (w & 1) + i];
-          unpack2(add2(fma2(v, r2, mul2(v, rest2)), magic), m[2 * i], m[2 * i + 1]);
+          for (int i = 0; i < 2; ++i) {
+            const f32x2 v = y[w >> 1].v[2 * (w & 1) + i];
+            unpack2(add2(fma2(v, r2, mul2(v, rest2)), magic), m[2 * i], m[2 * i + 1]);
+          }
+          codes[w] = low_bytes(m);
         }
-        codes[w] = low_bytes(m);
+      } else {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          float m[4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const f32x2 v = y[w >> 1].v[2 * (w & 1) + i];
+            const f32x2 n = fma2(v, r2, magic);
+            // v r - (n - magic), rounded once: the sum in brackets is exact
+            const f32x2 d = fma2(v, r2, fma2(n, minus, magic));
+            float lo, hi;
+            unpack2(d, lo, hi);
+            far = max_abs(far, lo, hi);
+            unpack2(n, m[2 * i], m[2 * i + 1]);
+          }
+          codes[w] = low_bytes(m);
+        }
       }
-    } else {
+      float back = 1.0f;
+      if (__any_sync(kAll, good && (far > kSure || out_of_range))) {
+        // Elements to decide (bits 0..15), and those that may be the largest: all of
+        // a head where 127 / a or the pairs' remainders would leave fp32's range.
+        const float scaled = !out_of_range ? 1.0f : top < 1.0f ? 0x1p60f : 0x1p-30f;
+        uint32_t unsure = 0, tops = 0;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        float m[4];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const f32x2 v = y[w >> 1].v[2 * (w & 1) + i];
-          const f32x2 n = fma2(v, r2, magic);
-          // v r - (n - magic), rounded once: the sum in brackets is exact
-          const f32x2 d = fma2(v, r2, fma2(n, minus, magic));
+        for (int e = 0; e < 16; ++e) {
           float lo, hi;
-          unpack2(d, lo, hi);
-          far = max_abs(far, lo, hi);
-          unpack2(n, m[2 * i], m[2 * i + 1]);
+          unpack2(y[e >> 3].v[(e & 7) >> 1], lo, hi);
+          const float v = fabsf((e & 1) ? hi : lo);
+          const float n = __fmaf_rn(v, r, kMagic);
+          if (out_of_range || fabsf(__fmaf_rn(v, r, kMagic - n)) > kSure) unsure |= 1u << e;
+          if (out_of_range || v >= top * (1.0f - 0x1p-20f)) tops |= 1u << e;
         }
-        codes[w] = low_bytes(m);
-      }
-    }
-    float back = 1.0f;
-    if (__any_sync(kAll, good && (far > kSure || out_of_range))) {
-      // Elements to decide (bits 0..15), and those that may be the largest: all of
-      // a head where 127 / a or the pairs' remainders would leave fp32's range.
-      const float scaled = !out_of_range ? 1.0f : top < 1.0f ? 0x1p60f : 0x1p-30f;
-      uint32_t unsure = 0, tops = 0;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        float lo, hi;
-        unpack2(y[e >> 3].v[(e & 7) >> 1], lo, hi);
-        const float v = fabsf((e & 1) ? hi : lo);
-        const float n = __fmaf_rn(v, r, kMagic);
-        if (out_of_range || fabsf(__fmaf_rn(v, r, kMagic - n)) > kSure) unsure |= 1u << e;
-        if (out_of_range || v >= top * (1.0f - 0x1p-20f)) tops |= 1u << e;
-      }
-      const float head_far = head_max(far);
-      if (!good || !(head_far > kSure || out_of_range)) unsure = tops = 0;
-      const uint16_t* const x = in + h.row_head * kHeadDim;
-      const bool rotated = place.turned && h.kind == 1;
-      Pair most{0.0f, -INFINITY};   // of the head, as a pair
-      for (; __any_sync(kAll, tops != 0); tops &= tops - 1) {
-        if (tops == 0) continue;
-        Pair v = exact_component(a, row, pos, x, gamma, rotated, place, __ffs(tops) - 1, scaled);
-        if (v.hi < 0.0f) v.lo = -v.lo, v.hi = -v.hi;
-        if (v.hi > most.hi || (v.hi == most.hi && v.lo > most.lo)) most = v;
-      }
-#pragma unroll
-      for (int o = 4; o > 0; o >>= 1) {
-        const Pair v{__shfl_xor_sync(kAll, most.hi, o), __shfl_xor_sync(kAll, most.lo, o)};
-        if (v.hi > most.hi || (v.hi == most.hi && v.lo > most.lo)) most = v;
-      }
-      const float per_top = __fdiv_rn(127.0f, most.hi);
-      for (; __any_sync(kAll, unsure != 0); unsure &= unsure - 1) {
-        if (unsure == 0) continue;
-        const int e = __ffs(unsure) - 1;
-        Pair v = exact_component(a, row, pos, x, gamma, rotated, place, e, scaled);
-        const bool negative = v.hi < 0.0f;
-        if (negative) v.lo = -v.lo, v.hi = -v.hi;
-        const float t = __fmul_rn(v.hi, per_top);
-        const float below = floorf(t);
-        float n = rintf(t);
-        if (fabsf(t - below - 0.5f) < 0x1p-12f) {
-          const float odd = __fmaf_rn(2.0f, below, 1.0f);
-          const float p = __fmul_rn(254.0f, v.hi), pe = __fmaf_rn(254.0f, v.hi, -p);
-          const float q = __fmul_rn(odd, most.hi), qe = __fmaf_rn(odd, most.hi, -q);
-          const float d = __fadd_rn(__fsub_rn(p, q), __fadd_rn(__fsub_rn(pe, qe), __fsub_rn(__fmul_rn(254.0f, v.lo), __fmul_rn(odd, most.lo))));
-          n = d > 0.0f ? below + 1.0f : d < 0.0f ? below : 2.0f * rintf(0.5f * (below + 0.5f));
+        const float head_far = head_max(far);
+        if (!good || !(head_far > kSure || out_of_range)) unsure = tops = 0;
+        const bool rotated = place.turned && kKind == 1;
+        Pair most{0.0f, -INFINITY};   // of the head, as a pair
+        for (; __any_sync(kAll, tops != 0); tops &= tops - 1) {
+          if (tops == 0) continue;
+          Pair v = exact_component(a, row, pos, head, gamma, rotated, place, __ffs(tops) - 1, scaled);
+          if (v.hi < 0.0f) v.lo = -v.lo, v.hi = -v.hi;
+          if (v.hi > most.hi || (v.hi == most.hi && v.lo > most.lo)) most = v;
         }
-        const uint32_t code = static_cast<uint32_t>(static_cast<int>(negative ? -n : n) + 128);
-        const int shift = 8 * (e & 3);
 #pragma unroll
-        for (int w = 0; w < 4; ++w)
-          if (e >> 2 == w) codes[w] = (codes[w] & ~(0xFFu << shift)) | code << shift;
-      }
-      if (out_of_range) {
-        top = most.hi;
-        back = 1.0f / scaled;
-      }
-    }
-    if (!h.there || block == nullptr) continue;
-    uint8_t* const to = block + h.at * head_step;
-    const int place_of = pos & 15;
+        for (int o = 4; o > 0; o >>= 1) {
+          const Pair v{__shfl_xor_sync(kAll, most.hi, o), __shfl_xor_sync(kAll, most.lo, o)};
+          if (v.hi > most.hi || (v.hi == most.hi && v.lo > most.lo)) most = v;
+        }
+        const float per_top = __fdiv_rn(127.0f, most.hi);
+        for (; __any_sync(kAll, unsure != 0); unsure &= unsure - 1) {
+          if (unsure == 0) continue;
+          const int e = __ffs(unsure) - 1;
+          Pair v = exact_component(a, row, pos, head, gamma, rotated, place, e, scaled);
+          const bool negative = v.hi < 0.0f;
+          if (negative) v.lo = -v.lo, v.hi = -v.hi;
+          const float t = __fmul_rn(v.hi, per_top);
+          const float below = floorf(t);
+          float n = rintf(t);
+          if (fabsf(t - below - 0.5f) < 0x1p-12f) {
+            const float odd = __fmaf_rn(2.0f, below, 1.0f);
+            const float p = __fmul_rn(254.0f, v.hi), pe = __fmaf_rn(254.0f, v.hi, -p);
+            const float q = __fmul_rn(odd, most.hi), qe = __fmaf_rn(odd, most.hi, -q);
+            const float d = __fadd_rn(__fsub_rn(p, q), __fadd_rn(__fsub_rn(pe, qe), __fsub_rn(__fmul_rn(254.0f, v.lo), __fmul_rn(odd, most.lo))));
+            n = d > 0.0f ? below + 1.0f : d < 0.0f ? below : 2.0f * rintf(0.5f * (below + 0.5f));
+          }
+          const uint32_t code = static_cast<uint32_t>(static_cast<int>(negative ? -n : n) + 128);
+          const int shift = 8 * (e & 3);
 #pragma unroll
-    for (int w = 0; w < 2; ++w)
-      *reinterpret_cast<uint2*>(to + (h.kind == 1 ? 0 : kVCodes) + place_of * kHeadDim + code_place(place_of, 8 * place.at[w])) =
-          make_uint2(codes[2 * w], codes[2 * w + 1]);
-    if ((lane & 7) == 0) {
-      const float s = __fmul_rn(__fmul_rn(top, rho), 1.0f / 127.0f) * back;
-      reinterpret_cast<float*>(to + (h.kind == 1 ? kKScales : kVScales))[place_of] =
-          top == 0.0f ? 0.0f : good && s < INFINITY ? s : NAN;
-    }
-  }
+          for (int w = 0; w < 4; ++w)
+            if (e >> 2 == w) codes[w] = (codes[w] & ~(0xFFu << shift)) | code << shift;
+        }
+        if (out_of_range) {
+          top = most.hi;
+          back = 1.0f / scaled;
+        }
+      }
+      if (!there || !placed) continue;
+#pragma unroll
+      for (int w = 0; w < 2; ++w) *reinterpret_cast<uint2*>(to + to_place[w]) = make_uint2(codes[2 * w], codes[2 * w + 1]);
+      if ((lane & 7) == 0) {
+        const float s = __fmul_rn(__fmul_rn(top, rho), 1.0f / 127.0f) * back;
+        // from the token's codes to its scale
+        const int to_scale = (kKind == 1 ? kKScales : kVScales - kVCodes) + place_of * (4 - kHeadDim);
+        *reinterpret_cast<float*>(to + to_scale) = top == 0.0f ? 0.0f : good && s < INFINITY ? s : NAN;
+      }
+      }
+    };
+  run(std::integral_constant<int, 0>());
+  run(std::integral_constant<int, 1>());
+  run(std::integral_constant<int, 2>());
 }
 
 // A warp takes one block of 16 tokens of a head: 4 vectors of codes a lane and
@@ -484,16 +504,18 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const CacheArgs c, co
 
 cudaError_t launch_kv_write(const KvWriteArgs& a, int sm_count, cudaStream_t stream) {
   const int64_t rows = a.c.B * a.T;
-  const int64_t groups = (a.q_heads + 3) / 4 + 2 * ((a.c.kv_heads + 3) / 4);
-  // A warp takes one group of heads until that fills the SMs' warps, then more
-  // of a row, which share the rotation's factors.
+  const int64_t q_groups = (a.q_heads + 3) / 4, kv_groups = (a.c.kv_heads + 3) / 4, groups = q_groups + 2 * kv_groups;
+  // A warp takes one group of heads until that fills the SMs' warps twice or so,
+  // then more of a row, which share the rotation's factors (8192 rows of 12
+  // groups: 40.6 us a row a warp, 49 in fours, 58 in twos; 1545 ragged rows of 9
+  // groups: 8.5 us in fours, 12.5 in twos).
   int64_t per = 1;
   while (per < 16 && rows * ((groups + per - 1) / per) > 2LL * 24 * sm_count) per *= 2;
   const int64_t chunks = (groups + per - 1) / per;
   const int64_t blocks = (rows * chunks + kWarps - 1) / kWarps;
-  if (blocks > 0xFFFFFFFFLL / kWarps || blocks > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
-  return launch_pdl(kv_write_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, a, static_cast<uint32_t>(chunks),
-                    static_cast<int>(per));
+  if (blocks > 0xFFFFFFFFLL / kWarps || blocks > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;   // (of more than 10^12 bytes)
+  const Split split{static_cast<uint32_t>(per), static_cast<uint32_t>(chunks), static_cast<uint32_t>(q_groups), static_cast<uint32_t>(kv_groups)};
+  return launch_pdl(kv_write_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, a, split);
 }
 
 cudaError_t launch_kv_read(const CacheArgs& c, const int32_t* start, int64_t L, uint16_t* k, uint16_t* v,
