@@ -146,6 +146,7 @@ __host__ __device__ inline bool few_segments(int64_t segments, int64_t grid) { r
 // one, and the parts are joined by segment).
 constexpr int kPieceBlocks = 5;
 struct Plan {
+  SeqLen seq;              // the lane's
   int share, blocks;       // of a thread block, of all
   bool own;
   int parts;               // of the lane's sequence's segments; blocks where not own
@@ -153,7 +154,8 @@ struct Plan {
 
   __device__ __forceinline__ Plan(const AttnParams& p, int grid, int lane) {
     const int B = static_cast<int>(p.a.c.B), segs = p.row_tiles * static_cast<int>(p.a.c.kv_heads);
-    const int n = lane < B ? span_of(p.a, seq_len(p.a.c, lane, p.a.T)).count : 0;
+    seq = lane < B ? seq_len(p.a.c, lane, p.a.T) : SeqLen{0, 0};
+    const int n = span_of(p.a, seq).count;
     blocks = __reduce_add_sync(kAll, n) * segs;
     const int even = max((blocks + grid - 1) / grid, kMinShare);
     const bool few = few_segments(B * segs, grid);
@@ -308,6 +310,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
     const int c = blockIdx.x;
     int b = 0, seg = 0, piece_at = 0, of = 1;
     const bool mine = plan.find(c, segs, b, seg, piece_at, of);
+    const SeqLen seq{__shfl_sync(kAll, plan.seq.len, b), __shfl_sync(kAll, plan.seq.fresh, b)};
     if (tid == 0) {
       // the first boundary inside a segment announces it
       int4 cut = make_int4(-1, 0, 0, b);
@@ -315,7 +318,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
         start.b = b;
         start.segs = segs;
         start.seg = seg;
-        start.load(a);
+        start.seq = seq;
+        start.span = span_of(a, seq);
         if (plan.own) {
           start.off = piece_at * plan.share;
           start.left = min(start.span.count - start.off, plan.share);
@@ -334,9 +338,11 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
   } else {
     // Blocks of 16 of 256 sequences at a time: their running sum, which places
     // the share, and what they are in all.
+    SeqLen seq{0, 0};      // the thread's
     auto chunk = [&](int64_t b0, int& n, int64_t& incl, int64_t& all) {
       const int64_t b = b0 + tid;
-      n = b < a.c.B ? span_of(a, seq_len(a.c, b, a.T)).count : 0;
+      seq = b < a.c.B ? seq_len(a.c, b, a.T) : SeqLen{0, 0};
+      n = span_of(a, seq).count;
       uint32_t in_warp = static_cast<uint32_t>(n);      // 32 spans of 2^26 blocks at most
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -372,7 +378,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
       return;
     }
     for (int64_t b0 = 0, before = 0;; b0 += kAttnThreads) {
-      if (b0 > 0) chunk(b0, n0, incl, all);
+      if (a.c.B > kAttnThreads) chunk(b0, n0, incl, all);
       const int64_t from = (before + incl - n0) * segs;
       if (n0 > 0 && from <= at && at < from + static_cast<int64_t>(n0) * segs) {
         start.b = b0 + tid;
@@ -381,7 +387,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
         start.seg = in_b < 1LL << 31 ? static_cast<int>(in_b) / n0 : static_cast<int>(in_b / n0);
         start.off = static_cast<int>(in_b - static_cast<int64_t>(start.seg) * n0);
         start.left = total - at < share ? total - at : share;
-        start.load(a);
+        start.seq = seq;
+        start.span = span_of(a, seq);
         // the first boundary inside a segment announces it
         const int64_t s0 = from + static_cast<int64_t>(start.seg) * n0;
         const int first = share_at(s0, share), last = share_at(s0 + n0 - 1, share);
@@ -399,6 +406,29 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
   const WaitCtx ctx{p.err, &abort_flag, kWaitLimitNs};
   bool ok = true;
 
+  // ---- q of the piece to come, each warp's rows, brought while the piece before
+  // it ends
+  const int rows = static_cast<int>(a.T) * p.G;
+  uint8_t* const raw = smem + S::kRaw;
+  // lane by row: its head of the sequence's outputs, -1: none, and its new token
+  int token_of = 0;
+  auto place = [&](int seg, int fresh, int& t) {
+    const int h = p.row_tiles == 1 ? seg : seg / p.row_tiles, row = (seg - h * p.row_tiles) * S::kRows + lane;
+    t = row / p.G;
+    return lane < S::kRows && row < rows && t < fresh ? t * static_cast<int>(a.q_heads) + h * p.G + (row - t * p.G) : -1;
+  };
+  auto bring_q = [&](int64_t b, int to) {
+    const uint16_t* const from = a.q + b * a.T * a.q_heads * kHeadDim + 8 * (lane & 15);
+#pragma unroll
+    for (int k = 0; k < NR; k += 2) {      // half a warp a row
+      const int r = warp + kAttnWarps * (k + (NR > 1 ? lane >> 4 : 0));
+      const int at = __shfl_sync(kAll, to, r);
+      if (at >= 0 && (NR > 1 || lane < 16))
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(raw + r * kHeadDim * 2 + 16 * (lane & 15))),
+                     "l"(from + static_cast<int64_t>(at) * kHeadDim)
+                     : "memory");
+    }
+  };
   // ---- copies: this warp's block of each tile, one bulk copy (whose issue takes
   // its thread 200 cycles), into the ring as soon as the block that it displaces is
   // of a tile that is done.  The next page is read when the one before is sent.
@@ -421,7 +451,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
     const int n = ahead.span.first + ahead.off, mine = n + warp, of_table = mine / per_page;
     in_page = mine - of_table * per_page;
     table = a.c.block_table + ahead.b * a.c.max_pages + of_table;
-    head_at = static_cast<uint32_t>(ahead.seg / p.row_tiles * per_page);
+    head_at = static_cast<uint32_t>((p.row_tiles == 1 ? ahead.seg : ahead.seg / p.row_tiles) * per_page);
     if (lane == 0)
       pieces[put] = Piece{ahead.b, ahead.seg, ahead.seq.len, ahead.seq.fresh, ahead.off, next_n, 16 * n, next_n == ahead.span.count,
                           next_n == ahead.left};
@@ -470,29 +500,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
   }
   __syncwarp();
   enter();
+  bring_q(start.b, place(start.seg, start.seq.fresh, token_of));
   for (int i = 0; kTileBlocks * i + warp < kSlots; ++i) send(0);
-  // ---- q of the piece to come, each warp's rows, brought while the piece before
-  // it ends
-  const int rows = static_cast<int>(a.T) * p.G;
-  uint8_t* const raw = smem + S::kRaw;
-  // lane by row: its head of the sequence's outputs, -1: none
-  auto place = [&](int seg, int fresh) {
-    const int h = seg / p.row_tiles, row = (seg - h * p.row_tiles) * S::kRows + lane, t = row / p.G;
-    return lane < S::kRows && row < rows && t < fresh ? t * static_cast<int>(a.q_heads) + h * p.G + (row - t * p.G) : -1;
-  };
-  auto bring_q = [&](int64_t b, int to) {
-    const uint16_t* const from = a.q + b * a.T * a.q_heads * kHeadDim + 8 * (lane & 15);
-#pragma unroll
-    for (int k = 0; k < NR; k += 2) {      // half a warp a row
-      const int r = warp + kAttnWarps * (k + (NR > 1 ? lane >> 4 : 0));
-      const int at = __shfl_sync(kAll, to, r);
-      if (at >= 0 && (NR > 1 || lane < 16))
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(raw + r * kHeadDim * 2 + 16 * (lane & 15))),
-                     "l"(from + static_cast<int64_t>(at) * kHeadDim)
-                     : "memory");
-    }
-  };
-  bring_q(start.b, place(start.seg, start.seq.fresh));
   const int g = lane >> 2, q = lane & 3;
   // Scores: tokens tok and tok + 1 of the warp's block, rows 8 r + 2 q and the
   // next one.  The tokens are such that 8 lanes' reads of keys (g = 2 u and
@@ -536,9 +545,9 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
       j0 = piece.j0;
       // lane by row: its place, and what it sees
       odd ^= 1;
-      const int to = place(piece.seg, piece.fresh);
+      const int to = place(piece.seg, piece.fresh, token_of);
       const bool real = to >= 0;
-      const int len = piece.len, token = len - piece.fresh + (real ? to / static_cast<int>(a.q_heads) : 0);
+      const int len = piece.len, token = len - piece.fresh + token_of;
       const int64_t w = a.window > 0 ? a.window : 1LL << 40;
       const int low = real && token - w + 1 > 0 ? static_cast<int>(token - w + 1) : 0;
       const int high = !real ? 0 : a.causal ? token + 1 : token + w < len ? static_cast<int>(token + w) : len;
@@ -590,7 +599,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
     if (i + kTileBlocks >= n && !piece.final) {
       __syncwarp();
       const Piece& behind = pieces[(get + 1) % kPieces];
-      bring_q(behind.b, place(behind.seg, behind.fresh));
+      bring_q(behind.b, place(behind.seg, behind.fresh, token_of));
     }
 
     ok = ok && mbar_wait(smem_u32(&full[tile % kTilesAhead]), tile / kTilesAhead & 1, ctx, 91);
