@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
   const int rows = static_cast<int>(a.T) * p.G;
   uint8_t* const raw = smem + S::kRaw;
   // lane by row: its head of the sequence's outputs, -1: none, and its new token
-  int token_of = 0;
+  int to_next = 0, token_next = 0;
   auto place = [&](int seg, int fresh, int& t) {
     const int h = p.row_tiles == 1 ? seg : seg / p.row_tiles, row = (seg - h * p.row_tiles) * S::kRows + lane;
     t = row / p.G;
@@ -434,41 +434,44 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
   // of a tile that is done.  The next page is read when the one before is sent.
   Walk& ahead = aheads[warp];
   const int per_page = static_cast<int>(a.c.page_size) >> 4;
-  const int page_step = kTileBlocks / per_page, in_page_step = kTileBlocks % per_page;
-  const uint32_t page_blocks = static_cast<uint32_t>(per_page * static_cast<int>(a.c.kv_heads));
+  const int page_blocks = per_page * static_cast<int>(a.c.kv_heads);
   int next_i = 0, next_n = 0;        // the tile's first block of the piece, the piece's blocks
-  const int32_t* table = nullptr;    // at the block's page
-  int page = -1, in_page = 0, put = 0;
-  uint32_t head_at = 0;              // block of the cache: the head's first of page 0
+  int first = 0, head_at = 0;        // the piece's first block of the sequence; the head's first block of a page
+  int page = -1, in_head = 0;        // lane by tile: the block's page, its place in the cache but for that
+  int put = 0;
   bool more = true;
   uint32_t on_page = 0;              // bit t % kTilesAhead: the warp's block of tile t is on a page
   int to_send = 0, send_slot = warp; // the tile whose block is next, and where it goes
   int behind_total = 0, behind_fresh = 0;  // lane 0: see Walk
-  auto look = [&]() { page = next_i + warp < next_n ? __ldg(table) : -1; };
+  auto look = [&]() {                // at the pages of 32 tiles
+    const int i = next_i + kTileBlocks * lane + warp;
+    const int n = first + i, of_table = n / per_page;
+    in_head = head_at + n - of_table * per_page;
+    page = i < next_n ? __ldg(a.c.block_table + ahead.b * a.c.max_pages + of_table) : -1;
+  };
   auto enter = [&]() {               // ahead's piece (each warp writes the same)
     next_i = 0;
     next_n = ahead.piece();
-    const int n = ahead.span.first + ahead.off, mine = n + warp, of_table = mine / per_page;
-    in_page = mine - of_table * per_page;
-    table = a.c.block_table + ahead.b * a.c.max_pages + of_table;
-    head_at = static_cast<uint32_t>((p.row_tiles == 1 ? ahead.seg : ahead.seg / p.row_tiles) * per_page);
+    first = ahead.span.first + ahead.off;
+    head_at = (p.row_tiles == 1 ? ahead.seg : ahead.seg / p.row_tiles) * per_page;
+    look();
     if (lane == 0)
-      pieces[put] = Piece{ahead.b, ahead.seg, ahead.seq.len, ahead.seq.fresh, ahead.off, next_n, 16 * n, next_n == ahead.span.count,
+      pieces[put] = Piece{ahead.b, ahead.seg, ahead.seq.len, ahead.seq.fresh, ahead.off, next_n, 16 * first, next_n == ahead.span.count,
                           next_n == ahead.left};
     put = (put + 1) % kPieces;
-    look();
   };
   // tile: the one whose predecessors are done
   auto send = [&](int tile) {
     if (!more || kTileBlocks * to_send + warp >= kTileBlocks * tile + kSlots) return;
-    const bool real = page >= 0 && page < a.c.pages;
+    const int from = next_i / kTileBlocks % 32;
+    const int on = __shfl_sync(kAll, page, from), in = __shfl_sync(kAll, in_head, from);
+    const bool real = on >= 0 && on < a.c.pages;
     const int of = to_send % kTilesAhead;
     if (ok && lane == 0) {
       const uint32_t bar = smem_u32(&full[of]);
       mbar_arrive_expect_tx(bar, real ? kCacheBlock : 0);
       if (real)
-        bulk_load(smem_u32(smem) + send_slot * kCacheBlock,
-                  a.c.cache + static_cast<int64_t>(head_at + static_cast<uint32_t>(page) * page_blocks + static_cast<uint32_t>(in_page)) * kCacheBlock,
+        bulk_load(smem_u32(smem) + send_slot * kCacheBlock, a.c.cache + (static_cast<int64_t>(on) * page_blocks + in) * kCacheBlock,
                   kCacheBlock, bar);
     }
     on_page = (on_page & ~(1u << of)) | (real ? 1u << of : 0u);
@@ -477,13 +480,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
     if (send_slot >= kSlots) send_slot -= kSlots;
     next_i += kTileBlocks;
     if (next_i < next_n) {
-      table += page_step;
-      in_page += in_page_step;
-      if (in_page >= per_page) {
-        in_page -= per_page;
-        ++table;
-      }
-      look();
+      if (from == 31) look();
     } else {
       more = ahead.left > next_n;
       __syncwarp();
@@ -500,7 +497,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
   }
   __syncwarp();
   enter();
-  bring_q(start.b, place(start.seg, start.seq.fresh, token_of));
+  to_next = place(start.seg, start.seq.fresh, token_next);
+  bring_q(start.b, to_next);
   for (int i = 0; kTileBlocks * i + warp < kSlots; ++i) send(0);
   const int g = lane >> 2, q = lane & 3;
   // Scores: tokens tok and tok + 1 of the warp's block, rows 8 r + 2 q and the
@@ -536,8 +534,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
   int i = 0, n = 0, j0 = 0;          // the tile's first block of the piece, the piece's blocks, the tile's first token
   for (;;) {
     const Piece& piece = pieces[get];
-    const bool first = i >= n;
-    if (first) {
+    const bool begins = i >= n;
+    if (begins) {
       __syncwarp();
       // q of the piece's rows, what they see
       i = 0;
@@ -545,9 +543,9 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
       j0 = piece.j0;
       // lane by row: its place, and what it sees
       odd ^= 1;
-      const int to = place(piece.seg, piece.fresh, token_of);
+      const int to = to_next;
       const bool real = to >= 0;
-      const int len = piece.len, token = len - piece.fresh + token_of;
+      const int len = piece.len, token = len - piece.fresh + token_next;
       const int64_t w = a.window > 0 ? a.window : 1LL << 40;
       const int low = real && token - w + 1 > 0 ? static_cast<int>(token - w + 1) : 0;
       const int high = !real ? 0 : a.causal ? token + 1 : token + w < len ? static_cast<int>(token + w) : len;
@@ -599,7 +597,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
     if (i + kTileBlocks >= n && !piece.final) {
       __syncwarp();
       const Piece& behind = pieces[(get + 1) % kPieces];
-      bring_q(behind.b, place(behind.seg, behind.fresh, token_of));
+      to_next = place(behind.seg, behind.fresh, token_next);
+      bring_q(behind.b, to_next);
     }
 
     ok = ok && mbar_wait(smem_u32(&full[tile % kTilesAhead]), tile / kTilesAhead & 1, ctx, 91);
@@ -687,7 +686,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
     f32x2 part[NR];
     for (bool raised = false;; raised = true) {
       // (a piece's first tile has no references yet)
-      if (raised || !first) {
+      if (raised || !begins) {
         float most[2] = {-INFINITY, -INFINITY};
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
@@ -748,7 +747,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
         over -= kNewWeight;
       }
       float* const ref = reinterpret_cast<float*>(refs + (lane >> 1)) + (lane & 1);
-      if (first) {      // (each warp writes the same; nothing stands under it)
+      if (begins) {      // (each warp writes the same; nothing stands under it)
         if (lane < S::kRows) {
           ref[0] = -most;
           ref[2] = over == -INFINITY ? 0.0f : over;
