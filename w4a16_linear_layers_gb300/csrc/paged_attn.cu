@@ -98,7 +98,9 @@ struct AttnParams {
   PagedAttnArgs a;
   int G;               // query heads of a key/value head
   int row_tiles;       // of a sequence's T * G rows
-  bool planned;        // Plan is used
+  bool planned;        // Plan is used; then
+  int each;            // thread blocks of a segment, 0: fewer than segments
+  uint64_t per_grid;   // 2^40 / grid, rounded up
   int* err;
   // workspace: where the cut segments are, then their parts
   int32_t* cuts;       // [grid][4]: segment, its first and last share, sequence; segment -1: none
@@ -157,13 +159,14 @@ struct Plan {
     seq = lane < B ? seq_len(p.a.c, lane, p.a.T) : SeqLen{0, 0};
     const int n = span_of(p.a, seq).count;
     blocks = __reduce_add_sync(kAll, n) * segs;
-    const int even = max((blocks + grid - 1) / grid, kMinShare);
+    // (exact: blocks are less than 2^31, and grid times that less than 2^40)
+    const int even = max(static_cast<int>(static_cast<uint32_t>(blocks + grid - 1) * p.per_grid >> 40), kMinShare);
     const bool few = few_segments(B * segs, grid);
     share = even;
     own = false;
-    if (B * segs <= grid) {
+    if (p.each > 0) {
+      const int each = p.each;
       // as many parts of each: enough, and hardly more where lengths are alike
-      const int each = grid / (B * segs);
       int lo = even, hi = max((__reduce_max_sync(kAll, n) + each - 1) / each, even);
       if (hi <= lo + 2) lo = hi;
       if (!few && hi > lo + kPieceBlocks) hi = lo + kPieceBlocks + 1;      // not taken
@@ -301,40 +304,38 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
     for (int i = 0; i < kTilesAhead; ++i) mbar_init(smem_u32(&full[i]), kAttnWarps);
     fence_barrier_init();
   }
+  __syncthreads();
   grid_dep_wait();
   grid_dep_launch();      // (the joining kernel may read what this one's predecessors wrote at once)
 
   // ---- this block's share
+  Walk walk;
+  walk.segs = segs;
   if (p.planned) {
     const Plan plan(p, gridDim.x, lane);
     const int c = blockIdx.x;
     int b = 0, seg = 0, piece_at = 0, of = 1;
     const bool mine = plan.find(c, segs, b, seg, piece_at, of);
-    const SeqLen seq{__shfl_sync(kAll, plan.seq.len, b), __shfl_sync(kAll, plan.seq.fresh, b)};
-    if (tid == 0) {
-      // the first boundary inside a segment announces it
-      int4 cut = make_int4(-1, 0, 0, b);
-      if (mine) {
-        start.b = b;
-        start.segs = segs;
-        start.seg = seg;
-        start.seq = seq;
-        start.span = span_of(a, seq);
-        if (plan.own) {
-          start.off = piece_at * plan.share;
-          start.left = min(start.span.count - start.off, plan.share);
-          if (piece_at == 1) cut = make_int4(seg, c - 1, c - 2 + of, b);
-        } else {
-          const int from = c * plan.share, s0 = from - piece_at, first = s0 / plan.share;
-          start.off = piece_at;
-          start.left = min(plan.blocks - from, plan.share);
-          if (piece_at > 0 && first == c - 1) cut = make_int4(seg, first, (s0 + of - 1) / plan.share, b);
-        }
+    // the first boundary inside a segment announces it
+    int4 cut = make_int4(-1, 0, 0, b);
+    if (mine) {
+      walk.b = b;
+      walk.seg = seg;
+      walk.seq = SeqLen{__shfl_sync(kAll, plan.seq.len, b), __shfl_sync(kAll, plan.seq.fresh, b)};
+      walk.span = span_of(a, walk.seq);
+      if (plan.own) {
+        walk.off = piece_at * plan.share;
+        walk.left = min(walk.span.count - walk.off, plan.share);
+        if (piece_at == 1) cut = make_int4(seg, c - 1, c - 2 + of, b);
+      } else {
+        const int from = c * plan.share;
+        walk.off = piece_at;
+        walk.left = min(plan.blocks - from, plan.share);
+        if (piece_at > 0 && piece_at <= plan.share) cut = make_int4(seg, c - 1, (from - piece_at + of - 1) / plan.share, b);
       }
-      *reinterpret_cast<int4*>(p.cuts + 4 * c) = cut;
     }
+    if (tid == 0) *reinterpret_cast<int4*>(p.cuts + 4 * c) = cut;
     if (!mine) return;
-    __syncthreads();
   } else {
     // Blocks of 16 of 256 sequences at a time: their running sum, which places
     // the share, and what they are in all.
@@ -399,6 +400,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
       if (before * segs > at) break;
     }
     __syncthreads();
+    walk = start;
   }
 
   // A copy that does not come ends the work, not the walk through the tiles, in
@@ -492,13 +494,13 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
     }
   };
   if (lane == 0) {
-    ahead = start;
-    start.look_behind(a, behind_total, behind_fresh);
+    ahead = walk;
+    walk.look_behind(a, behind_total, behind_fresh);
   }
   __syncwarp();
   enter();
-  to_next = place(start.seg, start.seq.fresh, token_next);
-  bring_q(start.b, to_next);
+  to_next = place(walk.seg, walk.seq.fresh, token_next);
+  bring_q(walk.b, to_next);
   for (int i = 0; kTileBlocks * i + warp < kSlots; ++i) send(0);
   const int g = lane >> 2, q = lane & 3;
   // Scores: tokens tok and tok + 1 of the warp's block, rows 8 r + 2 q and the
@@ -1002,6 +1004,8 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, int* err, int sm_count, cu
   const int grid = 2 * sm_count;
   const int64_t segments = a.c.B * tiles * a.c.kv_heads, longest = a.c.max_pages * (a.c.page_size / 16);
   p.planned = a.c.B <= 32 && segments <= ((1LL << 31) - 1 - 2 * kTile * grid) / longest;
+  p.each = static_cast<int>(grid / segments);
+  p.per_grid = ((1ULL << 40) + grid - 1) / grid;
   uint8_t* const ws = static_cast<uint8_t*>(a.workspace);
   p.cuts = reinterpret_cast<int32_t*>(ws);
   p.part_o = reinterpret_cast<float*>(ws + static_cast<size_t>(grid) * 16);
