@@ -609,7 +609,8 @@ qlin_status_t qlin_kv_read_bf16(const void *cache, int64_t pages, int64_t page_s
  * |i - j| < window where window > 0.  A row that sees none gives zeros.
  *
  * fp32 accumulation; each exp(x_j) times its V scale is rounded to fp16
- * relative to the row's largest.  Cache bytes at places that no row sees have
+ * relative to the row's largest (V scales below 2^-90 to that: values that
+ * small are off by up to 2^-107 each).  Cache bytes at places that no row sees have
  * no effect, whatever they hold.  Non-finite scales at seen tokens give
  * non-finite outputs for the rows that see them.  The result does not depend
  * on timing, but in its last bits on the batch, which decides how sequences

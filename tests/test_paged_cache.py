@@ -7,9 +7,10 @@ Tolerances, from the definitions of include/qlin.h:
     occur by chance.
   * scales: a * rho / 127 in fp32: y two products and a sum (2.42 half steps of
     a, the products of a rotation being at most sqrt(2) a), the mean of 128
-    squares under rho (half of at most 12 half steps), its root, two more
-    operations: below 12 half steps of 2^-24, held to 2^-20; subnormal ones
-    are half a step of 2^-149 off besides.
+    squares plus eps under rho (half of at most 13 half steps), its root (two
+    ulps: 4), two products (2, and 1/127 in fp32 is 2^-28 off): below 15 half
+    steps of 2^-24, held to 2^-20; subnormal ones are half a step of 2^-149 off
+    besides.
   * q: the same sums, whose terms' magnitudes S = |u c| + |u' s| (times rho)
     carry them, then the rounding to bf16 (2^-8 of the value):
     |q - q64| <= 2^-8 |q64| + 2^-20 S + 2^-134 (half a step of subnormal bf16).
@@ -21,11 +22,13 @@ Tolerances, from the definitions of include/qlin.h:
     its value; the weight's rounding to fp16 2^-11 of it; numerator and
     denominator each carry that, and sums of n terms in fp32, 4 sqrt(n) 2^-23
     of A (Higham and Mary, as in tests/helpers.py); a row's largest weight is
-    2^3 or more in fp16's units, so the weights below its normal range (2^-14),
-    off by half a step of 2^-24, are off by at most 2^-28 of the largest, times a
-    code of at most 127 by 2^-28 of the largest |V|; then bf16's rounding:
+    2^-1 or more in fp16's units (its reference puts a power of two above it at
+    2^0), so the weights below its normal range (2^-14), off by half a step of
+    2^-24, are off by at most 2^-24 of the largest, times a code of at most 127
+    by 2^-24 of the largest |V|, n of them by n of that at most and, as roundings
+    of either sign, by 4 sqrt(n) of it; then bf16's rounding:
     |o - o64| <= 2^-8 |o64| + (2^-11 + 2 (2^-16 X + 2^-20) + 4 sqrt(n) 2^-23) A
-                 + n 2^-28 max|V|, all but the first term times 1.05."""
+                 + min(n, 4 sqrt(n)) 2^-24 max|V|, all but the first term times 1.05."""
 import ctypes
 import threading
 
@@ -159,6 +162,17 @@ def test_write(gpu, B, T, Hq, Hkv, page, R, A, norm):
     total = T + rng.integers(0, 41, B)
     batch = Batch(B + T + R, B, T, Hq, Hkv, page, per, total, R=R, A=A, norm=norm)
     assert batch.check(batch.run()) == B * T
+
+
+@needs_gpu
+@pytest.mark.parametrize("T,Hq,Hkv,R,norm", [
+    # heads as they come, many ties, heads of a kind that leave lanes without one
+    (200, 3, 5, 0, False), (90, 2, 6, 0, True), (60, 5, 3, 16, False),
+    # a warp through several groups of a row: of one kind, of two, of all three
+    (1300, 7, 5, 128, True), (2600, 9, 1, 64, True), (5200, 6, 2, 0, False)])
+def test_write_long(gpu, T, Hq, Hkv, R, norm):
+    batch = Batch(T, 1, T, Hq, Hkv, 64, -(-T // 64), [T], R=R, norm=norm)
+    assert batch.check(batch.run()) == T
 
 
 @needs_gpu
@@ -316,7 +330,7 @@ def test_read_one_of_the_two(gpu, lib):
 
 def tolerance(o64, A, X, big, n):
     return 2.0 ** -8 * np.abs(o64) + 1.05 * ((2.0 ** -11 + 2 * (2.0 ** -16 * X + 2.0 ** -20) + 4 * np.sqrt(n) * 2.0 ** -23) * A
-                                             + n * 2.0 ** -28 * big)
+                                             + min(n, 4 * np.sqrt(n)) * 2.0 ** -24 * big)
 
 
 class Attn:
@@ -454,6 +468,20 @@ def test_attention_long_context(gpu):
 
 
 @needs_gpu
+@pytest.mark.parametrize("seed,B,T,Hq,Hkv,longest", [
+    # few segments, each cut into parts; as many as thread blocks; more
+    (1, 1, 1, 4, 1, 9000), (2, 2, 3, 8, 2, 5000), (3, 7, 8, 16, 4, 900), (4, 31, 2, 16, 8, 700), (5, 32, 1, 6, 6, 1500),
+    # a sequence more than a warp has lanes
+    (6, 33, 1, 6, 6, 1500), (7, 33, 5, 4, 2, 600), (8, 40, 1, 8, 8, 200), (9, 12, 8, 8, 2, 2500)])
+def test_attention_however_the_work_is_shared_out(gpu, seed, B, T, Hq, Hkv, longest):
+    """Lengths alike, of all sizes, and one long among short ones."""
+    rng = np.random.default_rng(100 + seed)
+    for total in (np.full(B, longest // 3), rng.integers(0, longest + 1, B), np.where(np.arange(B) == B // 2, longest, 20)):
+        a = Attn(110 + seed, B, T, Hq, Hkv, 16, -(-longest // 16), total, window=int(rng.integers(0, 2)) * 333)
+        a.check(a.run())
+
+
+@needs_gpu
 def test_attention_many_sequences(gpu):
     """More sequences than threads of a block, most of them short."""
     rng = np.random.default_rng(60)
@@ -564,6 +592,54 @@ def test_step_in_a_graph_beside_eager_calls(gpu):
             assert torch.equal(x, y), n
         for x, y in zip(other, want_b):
             assert torch.equal(x, y)
+
+
+def attn_of(state):
+    """The state behind its step's write, with the queries."""
+    q = qlin.kv_write_i8(state["qkv"], state["cache"], state["table"], state["total"], state["Hq"], cos_sin=state["turn"])
+    return {**state, "q": q}
+
+
+@needs_gpu
+def test_two_captured_steps_in_one_workspace(gpu):
+    """Replayed one behind the other, in either order."""
+    room = torch.empty(qlin.paged_attn_workspace_bytes(3, 2, 8, 2), dtype=torch.uint8, device="cuda")
+    outs, graphs = [], []
+    states = [attn_of(step_state(3)), attn_of(step_state(4))]
+    for s in states:
+        out = torch.empty_like(s["q"])
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            qlin.paged_attn_i8(s["q"], s["cache"], s["table"], s["total"], out=out, workspace=room)
+        outs.append(out)
+        graphs.append(graph)
+    alone = []
+    for i in (0, 1):
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        alone.append(outs[i].clone())
+    assert not torch.equal(alone[0], alone[1])
+    for order in ((0, 1), (1, 0), (0, 0, 1), (1, 1, 0, 1)):
+        for out in outs:
+            out.zero_()
+        for i in order:
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], alone[0]) and torch.equal(outs[1], alone[1])
+
+
+@needs_gpu
+def test_calls_on_the_null_stream_by_its_handle(gpu):
+    s = attn_of(step_state(5))
+    want = qlin.paged_attn_i8(s["q"], s["cache"], s["table"], s["total"])
+    k, v = qlin.kv_read_bf16(s["cache"], s["table"], s["total"], 30)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        got = qlin.paged_attn_i8(s["q"], s["cache"], s["table"], s["total"], stream=0)
+        k0, v0 = qlin.kv_read_bf16(s["cache"], s["table"], s["total"], 30, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(k0, k) and torch.equal(v0, v)
 
 
 @needs_gpu

@@ -23,23 +23,36 @@
 // fp16 through shared memory, and the outputs are formed transposed too, components
 // x rows, with the value codes as operand A: warp w takes the 32 components w % 4
 // from the half w / 4 of the tile.  Each warp brings its block of the tiles to
-// come by bulk copies: keys into a slot of its own, free when its scores are done,
-// values where all read them, free behind the next tile's barrier.
+// come, one bulk copy a block, into a ring of blocks, where a place is free behind
+// the barrier of the tile after.
 //
 // One barrier a tile: the reference m is raised only where a weight would pass
-// 2^15, and then to put the row's largest at 2^4, so that weights are formed and
+// 2^15, and then to put the row's largest at 2^0, so that weights are formed and
 // written as if it held, and the barrier that they need anyway says whether it
 // did.  (With a running maximum exchanged before, two barriers and copies
 // through one producer warp a tile took twice the time.)
+//
+// Where the time goes (two thread blocks an SM): with 32 rows a tile of 128 tokens
+// takes one of them 4700 cycles, 1300 for scores, 700 weights, 300 the barrier, 600
+// the copies' issue, 1100 outputs; the tensor pipe is 36% busy, shared memory 57%
+// (q read again by each warp), issue 53%: the chain through a tile bounds it, not one
+// of them (12 x 8 tokens at 8192: 64.7 us, 2.5 TB/s).  With 8 rows a tile takes 2200
+// to 3400 and the copies keep up (96 x 1 at 4096: 106.5 us, 5.9 TB/s; 1 x 131072:
+// 48.5 us, 5.7 TB/s).  Beginning a share takes 4 us (lengths, the plan, a page, the
+// first blocks: five loads one behind the other), ending a piece 0.6: what short
+// calls are made of (1 x 515: 6.6 us).
 //
 // mma.sync, not tcgen05: its operands come from registers, where the codes are
 // widened; tcgen05's would have to be written to shared or tensor memory first,
 // and the rows, mostly 4 to 32, fill a fraction of its tile.
 //
 // Precision.  Codes are exact in fp16, and so is q up to 2^-39 of its row's
-// largest component.  Weights have fp16's 11 bits down to 2^-17 of the row's
-// largest, and are at most 2^-28 of it off below that.  Scores, sums and
-// outputs are fp32.
+// largest component.  The largest weight of what a row has seen stands between
+// 2^-1 (its logarithm is of a power of two above the value scale) and 2^15, so weights
+// have fp16's 11 bits down to 2^-13 of it, and are at most 2^-24 of it off below
+// that.  Scores, sums and outputs are fp32.
+#include <atomic>
+
 #include <cuda_fp16.h>
 
 #include "f32x2.cuh"
@@ -58,9 +71,10 @@ constexpr int kPStride = 288;       // bytes of a row of weights: rows 32 bytes 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr float kNone = -1e30f;     // reference of a row that has seen nothing
-// Logarithms of the weights that a row's reference may let through, and of its
-// largest where it is set: 11 apart, so that few tiles set one (4 apart, a third
-// of the tiles of 32 rows did).
+// Logarithms of the weights that a row's reference may let through, of one that a
+// reference set in passing is lifted at, and of a row's largest where one is set: 15
+// apart, so that few tiles set one (of 27 tiles of 32 rows one in ten; 11 apart one in
+// four, 4 apart one in three).
 constexpr float kMostWeight = 15.0f;
 constexpr float kLiftWeight = 4.0f;
 constexpr float kNewWeight = 0.0f;
@@ -898,8 +912,8 @@ struct Joined {
         const int at = k + i * step;
         if (at >= parts) break;
         const int64_t slot = at == 0 ? 2 * first + 1 : 2 * (first + at);
-        part[i] = __ldg(reinterpret_cast<const float4*>(p.part_share + slot * tile_rows + in_tile));
-        v[i] = __ldg(reinterpret_cast<const float4*>(p.part_o + (slot * tile_rows + in_tile) * kHeadDim) + lane);
+        part[i] = __ldcg(reinterpret_cast<const float4*>(p.part_share + slot * tile_rows + in_tile));
+        v[i] = __ldcg(reinterpret_cast<const float4*>(p.part_o + (slot * tile_rows + in_tile) * kHeadDim) + lane);
       }
 #pragma unroll
       for (int i = 0; i < kAhead; ++i)
@@ -918,7 +932,7 @@ __global__ void __launch_bounds__(256) join_cuts_kernel(const AttnParams p, int 
   const int lane = threadIdx.x & 31;
   grid_dep_wait();
   grid_dep_launch();
-  const int4 cut = __ldg(reinterpret_cast<const int4*>(p.cuts + 4 * (blockIdx.x + 1)));
+  const int4 cut = __ldcg(reinterpret_cast<const int4*>(p.cuts + 4 * (blockIdx.x + 1)));
   if (cut.x < 0) return;
   const int fresh = seq_len(p.a.c, cut.w, p.a.T).fresh;
   for (int in_tile = threadIdx.x >> 5; in_tile < tile_rows; in_tile += 8) {
@@ -967,9 +981,16 @@ int row_groups(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 template <int NR, bool kCap>
 cudaError_t launch_groups(const AttnParams& p, int grid, cudaStream_t stream) {
   const auto kernel = attn_kernel<NR, kCap>;
-  // per call: a device's first costs nothing more, and no state is kept
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<NR>::kBytes);
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(ready.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<NR>::kBytes);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_release);
+  }
   e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kAttnThreads), Shape<NR>::kBytes, stream, p);
   if (e != cudaSuccess) return e;
   const int64_t rows = p.a.T * p.G, segments = p.a.c.B * p.row_tiles * p.a.c.kv_heads;
