@@ -24,14 +24,14 @@
 // three steps of a reduction.  A warp goes through heads of one row four at a
 // time, the next four on their way, with the rotation's factors in registers.
 //
-// Long calls are bound by memory: 8192 rows of 32 + 16 heads take 40.6 us, 4.6 TB/s
-// of what has to move (32768 rows 5.4), and 36.8 us where nothing is normalised
-// or turned.  With a half warp a head, partners R/16 lanes away and whole heads
+// Long calls are bound by memory: 8192 rows of 32 + 16 heads take 39.7 us, 4.7 TB/s
+// of what has to move, and 36.4 us where nothing is normalised or turned.  With a half warp a head, partners R/16 lanes away and whole heads
 // decided again where one code was near a half-integer it took 98.6.  Warps that
 // stay and take rows in turn took 42 to 46 us, two or three groups ahead 46 to 48;
 // 16 warps an SM 46, 24 with spilled registers 46 to 49.  Short calls are a chain
-// of three loads (length, angles, the rest) and take 3.9 us, 1.7 of them above an
-// empty launch.
+// of loads (length, angles or page, the head) and take 3.75 us, 1.6 of them above
+// an empty launch.
+#include <algorithm>
 #include <type_traits>
 
 #include "f32x2.cuh"
@@ -40,8 +40,12 @@
 namespace qlin {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kWarps = kThreads / 32;
+// Warps have nothing to do with one another, and small blocks start and end by
+// themselves: writes in blocks of one warp (12 x 8 rows 4.2 us, 4.6 in blocks of two or
+// four; 8192 rows 39.7, 40.3, 40.5), reads of two (515 tokens 2.85 us, 3.1 in four;
+// 12 x 8192 in blocks of one 93.1, of two 90.6).
+constexpr int kReadWarps = 2;
+constexpr int64_t kWritesAtOnce = 20;     // blocks of a write on an SM, which is what 96 registers allow
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr float kSure = 0.5f - 0x1p-14f;   // quotients this near their codes round as the exact ones
 
@@ -222,9 +226,9 @@ struct Split {
   uint32_t per, chunks, q_groups, kv_groups;
 };
 
-__global__ void __launch_bounds__(kThreads, 5) kv_write_kernel(const __grid_constant__ KvWriteArgs a, const Split split) {
-  const int lane = threadIdx.x & 31;
-  const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
+__global__ void __launch_bounds__(32, kWritesAtOnce) kv_write_kernel(const __grid_constant__ KvWriteArgs a, const Split split) {
+  const int lane = threadIdx.x;
+  const uint32_t unit = blockIdx.x;
   grid_dep_launch();
   grid_dep_wait();
   const uint32_t row = unit / split.chunks;
@@ -439,10 +443,10 @@ __global__ void __launch_bounds__(kThreads, 5) kv_write_kernel(const __grid_cons
 
 // A warp takes one block of 16 tokens of a head: 4 vectors of codes a lane and
 // tensor, all in flight at once.
-__global__ void __launch_bounds__(kThreads) kv_read_kernel(const CacheArgs c, const int32_t* start, int64_t L, int spans,
+__global__ void __launch_bounds__(32 * kReadWarps) kv_read_kernel(const CacheArgs c, const int32_t* start, int64_t L, int spans,
                                                            uint16_t* k, uint16_t* v) {
   const int lane = threadIdx.x & 31;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kReadWarps + (threadIdx.x >> 5);
   grid_dep_launch();
   grid_dep_wait();
   const int kv_heads = static_cast<int>(c.kv_heads);
@@ -505,26 +509,26 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const CacheArgs c, co
 cudaError_t launch_kv_write(const KvWriteArgs& a, int sm_count, cudaStream_t stream) {
   const int64_t rows = a.c.B * a.T;
   const int64_t q_groups = (a.q_heads + 3) / 4, kv_groups = (a.c.kv_heads + 3) / 4, groups = q_groups + 2 * kv_groups;
-  // A warp takes one group of heads until that fills the SMs' warps twice or so,
-  // then more of a row, which share the rotation's factors (8192 rows of 12
-  // groups: 40.6 us a row a warp, 49 in fours, 58 in twos; 1545 ragged rows of 9
-  // groups: 8.5 us in fours, 12.5 in twos).
-  int64_t per = 1;
-  while (per < 16 && rows * ((groups + per - 1) / per) > 2LL * 24 * sm_count) per *= 2;
+  // Rows are cut into as many parts as run at one time, whose groups share the
+  // rotation's factors (1545 ragged rows of 9 groups of three axes: whole 7.5 us, in
+  // parts for two rounds 8.8, for three 10.3; 700 rows of 12 groups: in four 6.0, in
+  // eight 7.3).
+  const int64_t parts = std::min(std::max<int64_t>(kWritesAtOnce * sm_count / rows, 1), groups);
+  const int64_t per = (groups + parts - 1) / parts;
   const int64_t chunks = (groups + per - 1) / per;
-  const int64_t blocks = (rows * chunks + kWarps - 1) / kWarps;
-  if (blocks > 0xFFFFFFFFLL / kWarps || blocks > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;   // (of more than 10^12 bytes)
+  const int64_t blocks = rows * chunks;
+  if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;   // (of more than 5 * 10^11 bytes)
   const Split split{static_cast<uint32_t>(per), static_cast<uint32_t>(chunks), static_cast<uint32_t>(q_groups), static_cast<uint32_t>(kv_groups)};
-  return launch_pdl(kv_write_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, a, split);
+  return launch_pdl(kv_write_kernel, dim3(static_cast<unsigned>(blocks)), dim3(32), 0, stream, a, split);
 }
 
 cudaError_t launch_kv_read(const CacheArgs& c, const int32_t* start, int64_t L, uint16_t* k, uint16_t* v,
                            cudaStream_t stream) {
   // blocks of 16 that L tokens from any start on may touch
   const int64_t spans = start == nullptr ? (L + 15) / 16 : (L + 30) / 16;
-  const int64_t blocks = (c.B * spans * c.kv_heads + kWarps - 1) / kWarps;
+  const int64_t blocks = (c.B * spans * c.kv_heads + kReadWarps - 1) / kReadWarps;
   if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
-  return launch_pdl(kv_read_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, c, start, L,
+  return launch_pdl(kv_read_kernel, dim3(static_cast<unsigned>(blocks)), dim3(32 * kReadWarps), 0, stream, c, start, L,
                     static_cast<int>(spans), k, v);
 }
 
