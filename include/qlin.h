@@ -619,7 +619,7 @@ qlin_status_t qlin_kv_read_bf16(const void *cache, int64_t pages, int64_t page_s
  *   q        bf16 [B T, q_heads * 128]  (rotated, qlin_kv_write_i8)
  *   q_heads  a positive multiple of kv_heads, at most 65535
  *   scale    finite;  softcap >= 0, finite;  window >= 0 (0: none)
- *   out      bf16 [B T, q_heads * 128]
+ *   out      bf16 [B T, q_heads * 128].  May not overlap q.
  *   workspace / workspace_bytes  at least qlin_paged_attn_workspace_bytes(B, T,
  *            q_heads, kv_heads) bytes on the current device.  It needs no
  *            zeroing and holds nothing between calls.  Calls that share a

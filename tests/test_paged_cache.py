@@ -381,7 +381,9 @@ class Attn:
     (3, 1, 4, 1, 16, [300, 12, 140], {"window": 131}), (2, 4, 4, 2, 16, [400, 20], {"window": 100, "causal": False}),
     (1, 1, 4, 1, 16, [200], {"window": 2 ** 40}),
     # scores
-    (2, 2, 4, 2, 16, [90, 200], {"softcap": 5.0}), (1, 8, 8, 2, 16, [200], {"softcap": 30.0, "causal": False, "window": 60}),
+    (2, 2, 4, 2, 16, [90, 200], {"softcap": 5.0}), (1, 3, 6, 2, 16, [150], {"softcap": 1e5}), (1, 2, 4, 2, 16, [150], {"softcap": 0.01}),
+    (1, 2, 4, 2, 16, [150], {"softcap": 2.0 ** -140}), (1, 2, 4, 2, 16, [150], {"softcap": 3e38}),
+    (1, 2, 4, 2, 16, [150], {"window": 2 ** 63 - 1, "causal": False}), (1, 8, 8, 2, 16, [200], {"softcap": 30.0, "causal": False, "window": 60}),
     (1, 1, 4, 1, 16, [200], {"scale": 0.0}), (1, 1, 4, 1, 16, [200], {"scale": -0.3})])
 def test_attention(gpu, B, T, Hq, Hkv, page, total, kw):
     per = -(-max(total) // page) + 1

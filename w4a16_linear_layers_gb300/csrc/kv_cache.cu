@@ -526,8 +526,8 @@ cudaError_t launch_kv_read(const CacheArgs& c, const int32_t* start, int64_t L, 
                            cudaStream_t stream) {
   // blocks of 16 that L tokens from any start on may touch
   const int64_t spans = start == nullptr ? (L + 15) / 16 : (L + 30) / 16;
+  if (c.B > 0x7FFFFFFFLL / (spans * c.kv_heads)) return cudaErrorInvalidConfiguration;    // (outputs of 2^43 bytes)
   const int64_t blocks = (c.B * spans * c.kv_heads + kReadWarps - 1) / kReadWarps;
-  if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
   return launch_pdl(kv_read_kernel, dim3(static_cast<unsigned>(blocks)), dim3(32 * kReadWarps), 0, stream, c, start, L,
                     static_cast<int>(spans), k, v);
 }
