@@ -64,8 +64,6 @@
 namespace qlin {
 namespace {
 
-constexpr int kAttnWarps = 8;
-constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kTileBlocks = 8;      // of 16 tokens, of a tile
 constexpr int kTile = 16 * kTileBlocks;
 constexpr int kMinShare = kTileBlocks;
@@ -85,15 +83,19 @@ constexpr float kNewWeight = 0.0f;
 template <int NR>
 struct Shape {
   static constexpr int kRows = 8 * NR;
+  static constexpr int kWarps = NR == 4 ? 4 : 8;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kOf = kTileBlocks / kWarps;      // blocks of a tile that a warp scores
+  static constexpr int kRowsOf = kRows / kWarps;        // rows whose q it brings
   // blocks in the ring: what two thread blocks an SM have room for
-  static constexpr int kSlots = NR == 1 ? 24 : NR == 2 ? 22 : 17;
+  static constexpr int kSlots = NR == 1 ? 24 : NR == 2 ? 22 : 16;
   // shared memory, in order
   static constexpr int kQ = kSlots * kCacheBlock;
   static constexpr int kP = kQ + kRows * kQStride;       // weights of two tiles
   static constexpr int kO = kP;                          // fp32 [rows][128], when a piece is done
   static_assert(512 <= 2 * kPStride, "outputs stand where the weights did");
   static constexpr int kPair = kP + 2 * kRows * kPStride;      // float2 [warps][rows]: references; sums
-  static constexpr int kRef = kPair + kAttnWarps * kRows * 8;     // float4 [rows / 2]: two rows' references
+  static constexpr int kRef = kPair + kWarps * kRows * 8;     // float4 [rows / 2]: two rows' references
   static constexpr int kKeep = kRef + kRows * 8;         // fp32 [rows]: what a raised reference leaves of the sums
   static constexpr int kFactor = kKeep + kRows * 4;      // fp32 [rows]
   // of two pieces:
@@ -333,23 +335,23 @@ __device__ __forceinline__ float log2_above(float v) {
 }
 
 template <int NR, bool kCap>
-__global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(Shape<NR>::kThreads, 2) attn_kernel(const AttnParams p) {
   using S = Shape<NR>;
-  constexpr int kSlots = S::kSlots;
+  constexpr int kSlots = S::kSlots, kWarps = S::kWarps, kThreads = S::kThreads, kOf = S::kOf, kRowsOf = S::kRowsOf;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kTilesAhead];    // a tile's blocks are there
-  __shared__ Walk aheads[kAttnWarps];       // of each warp's copies
+  __shared__ Walk aheads[kWarps];       // of each warp's copies
   __shared__ Piece pieces[kPieces];
   __shared__ Walk start;
   __shared__ int abort_flag;
-  __shared__ int64_t warp_sums[kAttnWarps];
+  __shared__ int64_t warp_sums[kWarps];
   const PagedAttnArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int segs = p.row_tiles * static_cast<int>(a.c.kv_heads);
 
   if (tid == 0) {
     abort_flag = 0;
-    for (int i = 0; i < kTilesAhead; ++i) mbar_init(smem_u32(&full[i]), kAttnWarps);
+    for (int i = 0; i < kTilesAhead; ++i) mbar_init(smem_u32(&full[i]), kTileBlocks);
     fence_barrier_init();
   }
   __syncthreads();
@@ -403,7 +405,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
       __syncthreads();
       all = 0;
 #pragma unroll
-      for (int w = 0; w < kAttnWarps; ++w) {
+      for (int w = 0; w < kWarps; ++w) {
         if (w < warp) incl += warp_sums[w];
         all += warp_sums[w];
       }
@@ -413,7 +415,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
     int64_t incl, all;
     chunk(0, n0, incl, all);
     int64_t total = all;
-    for (int64_t b0 = kAttnThreads; b0 < a.c.B; b0 += kAttnThreads) {
+    for (int64_t b0 = kThreads; b0 < a.c.B; b0 += kThreads) {
       int n;
       int64_t i, s;
       chunk(b0, n, i, s);
@@ -426,8 +428,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
       if (tid == 0) p.cuts[4 * blockIdx.x] = -1;
       return;
     }
-    for (int64_t b0 = 0, before = 0;; b0 += kAttnThreads) {
-      if (a.c.B > kAttnThreads) chunk(b0, n0, incl, all);
+    for (int64_t b0 = 0, before = 0;; b0 += kThreads) {
+      if (a.c.B > kThreads) chunk(b0, n0, incl, all);
       const int64_t from = (before + incl - n0) * segs;
       if (n0 > 0 && from <= at && at < from + static_cast<int64_t>(n0) * segs) {
         start.b = b0 + tid;
@@ -470,10 +472,10 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
   auto bring_q = [&](int64_t b, int to) {
     const uint16_t* const from = a.q + b * a.T * a.q_heads * kHeadDim + 8 * (lane & 15);
 #pragma unroll
-    for (int k = 0; k < NR; k += 2) {      // half a warp a row
-      const int r = warp + kAttnWarps * (k + (NR > 1 ? lane >> 4 : 0));
+    for (int k = 0; k < kRowsOf; k += 2) {      // half a warp a row
+      const int r = warp + kWarps * (k + (kRowsOf > 1 ? lane >> 4 : 0));
       const int at = __shfl_sync(kAll, to, r);
-      if (at >= 0 && (NR > 1 || lane < 16))
+      if (at >= 0 && (kRowsOf > 1 || lane < 16))
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(raw + r * kHeadDim * 2 + 16 * (lane & 15))),
                      "l"(from + static_cast<int64_t>(at) * kHeadDim)
                      : "memory");
@@ -487,17 +489,20 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
   const int page_blocks = per_page * static_cast<int>(a.c.kv_heads);
   int next_i = 0, next_n = 0;        // the tile's first block of the piece, the piece's blocks
   int first = 0, head_at = 0;        // the piece's first block of the sequence; the head's first block of a page
-  int page = -1, in_head = 0;        // lane by tile: the block's page, its place in the cache but for that
+  int page[kOf], in_head[kOf];       // lane by tile: the blocks' pages, their places in the cache but for that
   int put = 0;
   bool more = true;
-  uint32_t on_page = 0;              // bit t % kTilesAhead: the warp's block of tile t is on a page
+  uint32_t on_page = 0;              // bits t % kTilesAhead, kOf each: the warp's blocks of tile t are on a page
   int to_send = 0, send_slot = warp; // the tile whose block is next, and where it goes
   int behind_total = 0, behind_fresh = 0;  // lane 0: see Walk
   auto look = [&]() {                // at the pages of 32 tiles
-    const int i = next_i + kTileBlocks * lane + warp;
-    const int n = first + i, of_table = n / per_page;
-    in_head = head_at + n - of_table * per_page;
-    page = i < next_n ? __ldg(a.c.block_table + ahead.b * a.c.max_pages + of_table) : -1;
+#pragma unroll
+    for (int k = 0; k < kOf; ++k) {
+      const int i = next_i + kTileBlocks * lane + warp + kWarps * k;
+      const int n = first + i, of_table = n / per_page;
+      in_head[k] = head_at + n - of_table * per_page;
+      page[k] = i < next_n ? __ldg(a.c.block_table + ahead.b * a.c.max_pages + of_table) : -1;
+    }
   };
   auto enter = [&]() {               // ahead's piece (each warp writes the same)
     next_i = 0;
@@ -512,19 +517,24 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
   };
   // tile: the one whose predecessors are done
   auto send = [&](int tile) {
-    if (!more || kTileBlocks * to_send + warp >= kTileBlocks * tile + kSlots) return;
+    if (!more || kTileBlocks * to_send + (kOf > 1 ? kTileBlocks - 1 : warp) >= kTileBlocks * tile + kSlots) return;
     const int from = next_i / kTileBlocks % 32;
-    const int on = __shfl_sync(kAll, page, from), in = __shfl_sync(kAll, in_head, from);
-    const bool real = on >= 0 && on < a.c.pages;
     const int of = to_send % kTilesAhead;
-    if (ok && lane == 0) {
-      const uint32_t bar = smem_u32(&full[of]);
-      mbar_arrive_expect_tx(bar, real ? kCacheBlock : 0);
-      if (real)
-        bulk_load(smem_u32(smem) + send_slot * kCacheBlock, a.c.cache + (static_cast<int64_t>(on) * page_blocks + in) * kCacheBlock,
-                  kCacheBlock, bar);
+#pragma unroll
+    for (int k = 0; k < kOf; ++k) {
+      const int on = __shfl_sync(kAll, page[k], from), in = __shfl_sync(kAll, in_head[k], from);
+      const bool real = on >= 0 && on < a.c.pages;
+      if (ok && lane == 0) {
+        const uint32_t bar = smem_u32(&full[of]);
+        const int slot = send_slot + kWarps * k;
+        mbar_arrive_expect_tx(bar, real ? kCacheBlock : 0);
+        if (real)
+          bulk_load(smem_u32(smem) + slot * kCacheBlock, a.c.cache + (static_cast<int64_t>(on) * page_blocks + in) * kCacheBlock,
+                    kCacheBlock, bar);
+      }
+      const uint32_t bit = 1u << (of * kOf + k);
+      on_page = (on_page & ~bit) | (real ? bit : 0u);
     }
-    on_page = (on_page & ~(1u << of)) | (real ? 1u << of : 0u);
     ++to_send;
     send_slot += kTileBlocks;
     if (send_slot >= kSlots) send_slot -= kSlots;
@@ -549,7 +559,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
   enter();
   to_next = place(walk.seg, walk.seq.fresh, token_next);
   bring_q(walk.b, to_next);
-  for (int i = 0; kTileBlocks * i + warp < kSlots; ++i) send(0);
+  for (int i = 0; kTileBlocks * i < kSlots; ++i) send(0);
   const int g = lane >> 2, q = lane & 3;
   // Scores: tokens tok and tok + 1 of the warp's block, rows 8 r + 2 q and the
   // next one.  The tokens are such that 8 lanes' reads of keys (g = 2 u and
@@ -572,7 +582,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
   // A row's reference is a score (its negative is held) plus a small number, so
   // that large scores do not swallow the logarithm of the value scale in it.
   f32x2 sum[NR];
-  constexpr int kHeld = NR <= 2 ? NR : 0;      // groups whose q stays in registers
+  constexpr int kHeld = NR <= 2 || kOf > 1 ? NR : 0;      // groups whose q stays in registers
   uint4 qb[kHeld > 0 ? kHeld : 1][4];
   auto q_part = [&](int r, int c) {            // operand B: components 16 (q + 4 (c / 2)) + 8 (c % 2) .. + 7
     return *reinterpret_cast<const uint4*>(qs + (8 * r + g) * kQStride + 32 * (q + 4 * (c >> 1)) + 16 * (c & 1));
@@ -608,15 +618,15 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
       __syncwarp();
-      uint2 x[NR];
+      uint2 x[kRowsOf];
 #pragma unroll
-      for (int k = 0; k < NR; ++k) {
-        const int r = warp + kAttnWarps * k;
+      for (int k = 0; k < kRowsOf; ++k) {
+        const int r = warp + kWarps * k;
         x[k] = __shfl_sync(kAll, to, r) >= 0 ? *reinterpret_cast<const uint2*>(raw + r * kHeadDim * 2 + 8 * lane) : make_uint2(0, 0);
       }
 #pragma unroll
-      for (int k = 0; k < NR; ++k) {
-        const int r = warp + kAttnWarps * k;
+      for (int k = 0; k < kRowsOf; ++k) {
+        const int r = warp + kWarps * k;
         const float f[4] = {__uint_as_float(x[k].x << 16), __uint_as_float(x[k].x & 0xFFFF0000u), __uint_as_float(x[k].y << 16),
                             __uint_as_float(x[k].y & 0xFFFF0000u)};
         // the largest exponent (of finite numbers' bits the order is that of the numbers)
@@ -655,113 +665,144 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
     // Whether all rows see all of the warp's block.  Elsewhere what a row does not
     // see gets no weight; a block that is not there is gone through all the same, as
     // whatever finite codes stand in its place.
-    const bool here = ok && (on_page >> (tile % kTilesAhead) & 1u);
-    const int j = j0 + 16 * warp;
-    const bool all_seen = here && j >= seen_from && j + 16 <= seen_to;
+    bool here[kOf], all_seen = true;
+#pragma unroll
+    for (int k = 0; k < kOf; ++k) {
+      here[k] = ok && (on_page >> (tile % kTilesAhead * kOf + k) & 1u);
+      const int j = j0 + 16 * (warp + kWarps * k);
+      all_seen = all_seen && here[k] && j >= seen_from && j + 16 <= seen_to;
+    }
 
     // ---- scores times log2(e)
-    f32x2 x[NR][2];
-    float2 vs;
+    f32x2 x[kOf][NR][2];
+    float2 vs[kOf];
     {
-      const int mine = slot + warp;
-      const uint8_t* const keys = smem + (mine >= kSlots ? mine - kSlots : mine) * kCacheBlock;
-      const uint8_t* const scales = keys + kKScales;
-      float s[NR][4];
+      const uint8_t* keys[kOf];
+      float s[kOf][NR][4];
 #pragma unroll
-      for (int r = 0; r < NR; ++r) {
+      for (int k = 0; k < kOf; ++k) {
+        const int mine = slot + warp + kWarps * k;
+        keys[k] = smem + (mine >= kSlots ? mine - kSlots : mine) * kCacheBlock;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) s[r][c] = 0.0f;
+        for (int r = 0; r < NR; ++r) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[k][r][c] = 0.0f;
+        }
       }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const uint4 ka = *reinterpret_cast<const uint4*>(keys + tok * kHeadDim + 16 * ((q + 4 * c) ^ k_turn));
-        const uint4 kb = *reinterpret_cast<const uint4*>(keys + (tok + 1) * kHeadDim + 16 * ((q + 4 * c) ^ k_turn));
-        uint32_t fa[4][4];
-        biased_u8x4_to_f16x4(ka.x, fa[0][0], fa[0][2]);
-        biased_u8x4_to_f16x4(kb.x, fa[0][1], fa[0][3]);
-        biased_u8x4_to_f16x4(ka.y, fa[1][0], fa[1][2]);
-        biased_u8x4_to_f16x4(kb.y, fa[1][1], fa[1][3]);
-        biased_u8x4_to_f16x4(ka.z, fa[2][0], fa[2][2]);
-        biased_u8x4_to_f16x4(kb.z, fa[2][1], fa[2][3]);
-        biased_u8x4_to_f16x4(ka.w, fa[3][0], fa[3][2]);
-        biased_u8x4_to_f16x4(kb.w, fa[3][1], fa[3][3]);
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          const uint4 b0 = r < kHeld ? qb[r < kHeld ? r : 0][2 * c] : q_part(r, 2 * c);
-          const uint4 b1 = r < kHeld ? qb[r < kHeld ? r : 0][2 * c + 1] : q_part(r, 2 * c + 1);
-          mma(s[r], fa[0], b0.x, b0.y);
-          mma(s[r], fa[1], b0.z, b0.w);
-          mma(s[r], fa[2], b1.x, b1.y);
-          mma(s[r], fa[3], b1.z, b1.w);
+        for (int k = 0; k < kOf; ++k) {
+          const uint4 ka = *reinterpret_cast<const uint4*>(keys[k] + tok * kHeadDim + 16 * ((q + 4 * c) ^ k_turn));
+          const uint4 kb = *reinterpret_cast<const uint4*>(keys[k] + (tok + 1) * kHeadDim + 16 * ((q + 4 * c) ^ k_turn));
+          uint32_t fa[4][4];
+          biased_u8x4_to_f16x4(ka.x, fa[0][0], fa[0][2]);
+          biased_u8x4_to_f16x4(kb.x, fa[0][1], fa[0][3]);
+          biased_u8x4_to_f16x4(ka.y, fa[1][0], fa[1][2]);
+          biased_u8x4_to_f16x4(kb.y, fa[1][1], fa[1][3]);
+          biased_u8x4_to_f16x4(ka.z, fa[2][0], fa[2][2]);
+          biased_u8x4_to_f16x4(kb.z, fa[2][1], fa[2][3]);
+          biased_u8x4_to_f16x4(ka.w, fa[3][0], fa[3][2]);
+          biased_u8x4_to_f16x4(kb.w, fa[3][1], fa[3][3]);
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            const uint4 b0 = r < kHeld ? qb[r < kHeld ? r : 0][2 * c] : q_part(r, 2 * c);
+            const uint4 b1 = r < kHeld ? qb[r < kHeld ? r : 0][2 * c + 1] : q_part(r, 2 * c + 1);
+            mma(s[k][r], fa[0], b0.x, b0.y);
+            mma(s[k][r], fa[1], b0.z, b0.w);
+            mma(s[k][r], fa[2], b1.x, b1.y);
+            mma(s[k][r], fa[3], b1.z, b1.w);
+          }
         }
       }
-      const float2 ks = *reinterpret_cast<const float2*>(scales + 4 * tok);
-      vs = *reinterpret_cast<const float2*>(scales + 64 + 4 * tok);
+      float2 ks[kOf];
+#pragma unroll
+      for (int k = 0; k < kOf; ++k) {
+        ks[k] = *reinterpret_cast<const float2*>(keys[k] + kKScales + 4 * tok);
+        vs[k] = *reinterpret_cast<const float2*>(keys[k] + kVScales + 4 * tok);
+      }
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
         const float2 f = *reinterpret_cast<const float2*>(factors + 8 * r + 2 * q);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) x[r][c] = mul2(mul2(pack2(s[r][2 * c], s[r][2 * c + 1]), pack2(f.x, f.y)), both(c == 0 ? ks.x : ks.y));
-        if constexpr (kCap) {
-          float v[4];
-          unpack2(x[r][0], v[0], v[1]);
-          unpack2(x[r][1], v[2], v[3]);
-          cap_scores(v, p.cap, p.per_cap);
-          x[r][0] = pack2(v[0], v[1]);
-          x[r][1] = pack2(v[2], v[3]);
+        for (int k = 0; k < kOf; ++k) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            x[k][r][c] = mul2(mul2(pack2(s[k][r][2 * c], s[k][r][2 * c + 1]), pack2(f.x, f.y)), both(c == 0 ? ks[k].x : ks[k].y));
+          if constexpr (kCap) {
+            float v[4];
+            unpack2(x[k][r][0], v[0], v[1]);
+            unpack2(x[k][r][1], v[2], v[3]);
+            cap_scores(v, p.cap, p.per_cap);
+            x[k][r][0] = pack2(v[0], v[1]);
+            x[k][r][1] = pack2(v[2], v[3]);
+          }
         }
       }
     }
     if (!all_seen) {
-      if (!here) vs = make_float2(0.0f, 0.0f);
 #pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        const int2 lo = *reinterpret_cast<const int2*>(lows + odd * S::kRows + 8 * r + 2 * q);
-        const int2 hi = *reinterpret_cast<const int2*>(highs + odd * S::kRows + 8 * r + 2 * q);
+      for (int k = 0; k < kOf; ++k) {
+        if (!here[k]) vs[k] = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int at = j + tok + c;
-          float v0, v1;
-          unpack2(x[r][c], v0, v1);
-          x[r][c] = pack2(here && at >= lo.x && at < hi.x ? v0 : -INFINITY, here && at >= lo.y && at < hi.y ? v1 : -INFINITY);
+        for (int r = 0; r < NR; ++r) {
+          const int2 lo = *reinterpret_cast<const int2*>(lows + odd * S::kRows + 8 * r + 2 * q);
+          const int2 hi = *reinterpret_cast<const int2*>(highs + odd * S::kRows + 8 * r + 2 * q);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int at = j0 + 16 * (warp + kWarps * k) + tok + c;
+            float v0, v1;
+            unpack2(x[k][r][c], v0, v1);
+            x[k][r][c] = pack2(here[k] && at >= lo.x && at < hi.x ? v0 : -INFINITY, here[k] && at >= lo.y && at < hi.y ? v1 : -INFINITY);
+          }
         }
       }
     }
     // ---- weights, as if the references held
     uint8_t* const weights = ps + turn * (S::kRows * kPStride);
-    const float lv[2] = {log2_above(vs.x), log2_above(vs.y)};
+    float lv[kOf][2];
+#pragma unroll
+    for (int k = 0; k < kOf; ++k) lv[k][0] = log2_above(vs[k].x), lv[k][1] = log2_above(vs[k].y);
     f32x2 part[NR];
     for (bool raised = false;; raised = true) {
       // (a piece's first tile has no references yet)
       if (raised || !begins) {
-        float most[2] = {-INFINITY, -INFINITY};
+        float over = -INFINITY;
+        float most[kOf][2];
+#pragma unroll
+        for (int k = 0; k < kOf; ++k) most[k][0] = most[k][1] = -INFINITY;
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
           const ulonglong2 ref = *reinterpret_cast<const ulonglong2*>(refs + 4 * r + q);
-          float w[4];
-          unpack2(sub2(add2(x[r][0], ref.x), ref.y), w[0], w[1]);
-          unpack2(sub2(add2(x[r][1], ref.x), ref.y), w[2], w[3]);
-          most[0] = fmaxf(most[0], fmaxf(w[0], w[1]));
-          most[1] = fmaxf(most[1], fmaxf(w[2], w[3]));
 #pragma unroll
-          for (int k = 0; k < 4; ++k) w[k] = ex2(w[k]);
-          const f32x2 p0 = pack2(w[0], w[1]), p1 = pack2(w[2], w[3]);
-          part[r] = add2(p0, p1);
-          unpack2(mul2(p0, both(vs.x)), w[0], w[1]);
-          unpack2(mul2(p1, both(vs.y)), w[2], w[3]);
-          if (!all_seen) {      // hidden weights 0, whatever the scale holds
-            float v[4];
-            unpack2(x[r][0], v[0], v[1]);
-            unpack2(x[r][1], v[2], v[3]);
+          for (int k = 0; k < kOf; ++k) {
+            float w[4];
+            unpack2(sub2(add2(x[k][r][0], ref.x), ref.y), w[0], w[1]);
+            unpack2(sub2(add2(x[k][r][1], ref.x), ref.y), w[2], w[3]);
+            most[k][0] = fmaxf(most[k][0], fmaxf(w[0], w[1]));
+            most[k][1] = fmaxf(most[k][1], fmaxf(w[2], w[3]));
 #pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] = v[k] == -INFINITY ? 0.0f : w[k];
+            for (int e = 0; e < 4; ++e) w[e] = ex2(w[e]);
+            const f32x2 p0 = pack2(w[0], w[1]), p1 = pack2(w[2], w[3]);
+            part[r] = k == 0 ? add2(p0, p1) : add2(part[r], add2(p0, p1));
+            unpack2(mul2(p0, both(vs[k].x)), w[0], w[1]);
+            unpack2(mul2(p1, both(vs[k].y)), w[2], w[3]);
+            if (!all_seen) {      // hidden weights 0, whatever the scale holds
+              float v[4];
+              unpack2(x[k][r][0], v[0], v[1]);
+              unpack2(x[k][r][1], v[2], v[3]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) w[e] = v[e] == -INFINITY ? 0.0f : w[e];
+            }
+            uint8_t* const to = weights + (8 * r + 2 * q) * kPStride + 2 * (16 * (warp + kWarps * k) + tok);
+            *reinterpret_cast<__half2*>(to) = __floats2half2_rn(w[0], w[2]);
+            *reinterpret_cast<__half2*>(to + kPStride) = __floats2half2_rn(w[1], w[3]);
           }
-          uint8_t* const to = weights + (8 * r + 2 * q) * kPStride + 2 * (16 * warp + tok);
-          *reinterpret_cast<__half2*>(to) = __floats2half2_rn(w[0], w[2]);
-          *reinterpret_cast<__half2*>(to + kPStride) = __floats2half2_rn(w[1], w[3]);
         }
+#pragma unroll
+        for (int k = 0; k < kOf; ++k) over = fmaxf(over, fmaxf(most[k][0] + lv[k][0], most[k][1] + lv[k][1]));
         // (behind this barrier all warps are done with the tile before this one)
-        const bool raise = __syncthreads_or(fmaxf(most[0] + lv[0], most[1] + lv[1]) > kMostWeight) != 0;
+        const bool raise = __syncthreads_or(over > kMostWeight) != 0;
         if (raised || !raise) break;
       }
       // References of the rows concerned up, what stands under them down.  Each
@@ -769,28 +810,33 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
       // lane by row.
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
-        float v[4];
-        unpack2(x[r][0], v[0], v[1]);
-        unpack2(x[r][1], v[2], v[3]);
+        float v[kOf][4];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float top = max_over_g(fmaxf(v[k], v[2 + k]));
+        for (int k = 0; k < kOf; ++k) unpack2(x[k][r][0], v[k][0], v[k][1]), unpack2(x[k][r][1], v[k][2], v[k][3]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float top = -INFINITY, over = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < kOf; ++k) top = fmaxf(top, fmaxf(v[k][e], v[k][2 + e]));
+          top = max_over_g(top);
           if (top == -INFINITY) top = kNone;
-          const float over = max_over_g(fmaxf(v[k] - top + lv[0], v[2 + k] - top + lv[1]));
-          if (g == 0) pairs[warp * S::kRows + 8 * r + 2 * q + k] = make_float2(top, over);
+#pragma unroll
+          for (int k = 0; k < kOf; ++k) over = fmaxf(over, fmaxf(v[k][e] - top + lv[k][0], v[k][2 + e] - top + lv[k][1]));
+          over = max_over_g(over);
+          if (g == 0) pairs[warp * S::kRows + 8 * r + 2 * q + e] = make_float2(top, over);
         }
       }
       __syncthreads();
       float most = kNone, over = -INFINITY;
       if (lane < S::kRows) {
-        float2 of[kAttnWarps];
+        float2 of[kWarps];
 #pragma unroll
-        for (int w = 0; w < kAttnWarps; ++w) {
+        for (int w = 0; w < kWarps; ++w) {
           of[w] = pairs[w * S::kRows + lane];
           most = fmaxf(most, of[w].x);
         }
 #pragma unroll
-        for (int w = 0; w < kAttnWarps; ++w) over = fmaxf(over, (of[w].x - most) + of[w].y);
+        for (int w = 0; w < kWarps; ++w) over = fmaxf(over, (of[w].x - most) + of[w].y);
         over -= kNewWeight;
       }
       float* const ref = reinterpret_cast<float*>(refs + (lane >> 1)) + (lane & 1);
@@ -829,7 +875,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
     for (int r = 0; r < NR; ++r) sum[r] = add2(sum[r], part[r]);
     // ---- outputs
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 4 * kOf; ++k) {
       const int in_tile = 4 * half + k, of = slot + in_tile;
       const uint8_t* const v = smem + (of >= kSlots ? of - kSlots : of) * kCacheBlock + kVCodes + 4 * q * kHeadDim + 32 * (quarter ^ q) + 4 * g;
       uint32_t w[4];
@@ -865,7 +911,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
         if (g == 0) *reinterpret_cast<float4*>(pairs + warp * S::kRows + 8 * r + 2 * q) = make_float4(l[0], 0.0f, l[1], 0.0f);
       }
       __syncthreads();      // the weights are read
-      if (half == 1) {
+      if (kOf == 1 && half == 1) {
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
 #pragma unroll
@@ -874,13 +920,13 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
                 make_float4(o[0][r][c], o[0][r][2 + c], o[1][r][c], o[1][r][2 + c]);
         }
       }
-      __syncthreads();
+      if (kOf == 1) __syncthreads();
       if (half == 0) {
         const bool whole = piece.whole;
         float l = 0.0f;       // lane by row
         if (lane < S::kRows) {
 #pragma unroll
-          for (int w = 0; w < kAttnWarps; ++w) l += pairs[w * S::kRows + lane].x;
+          for (int w = 0; w < kWarps; ++w) l += pairs[w * S::kRows + lane].x;
         }
         const int64_t part = (2LL * blockIdx.x + (piece.cut > 0 ? 0 : 1)) * S::kRows;
         if (!whole && warp == 0 && lane < S::kRows) {
@@ -896,7 +942,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
           for (int c = 0; c < 2; ++c) {
             const int in_tile = 8 * r + 2 * q + c, to = tos[odd * S::kRows + in_tile];
             const float f = __shfl_sync(kAll, back, in_tile);
-            const float4 v = *reinterpret_cast<const float4*>(os + in_tile * kHeadDim + 32 * quarter + 4 * g);
+            const float4 v = kOf == 1 ? *reinterpret_cast<const float4*>(os + in_tile * kHeadDim + 32 * quarter + 4 * g) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             const float4 sums = make_float4((o[0][r][c] + v.x) * f, (o[0][r][2 + c] + v.y) * f, (o[1][r][c] + v.z) * f,
                                             (o[1][r][2 + c] + v.w) * f);
             if (to >= 0 && whole)
@@ -1022,7 +1068,7 @@ cudaError_t launch_groups(const AttnParams& p, int grid, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_release);
   }
-  e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kAttnThreads), Shape<NR>::kBytes, stream, p);
+  e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(Shape<NR>::kThreads), Shape<NR>::kBytes, stream, p);
   if (e != cudaSuccess) return e;
   const int64_t rows = p.a.T * p.G, segments = p.a.c.B * p.row_tiles * p.a.c.kv_heads;
   if (p.planned && few_segments(segments, grid))
