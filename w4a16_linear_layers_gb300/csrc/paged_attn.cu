@@ -16,15 +16,19 @@
 // in a second kernel; segments inside one are finished at once.
 //
 // A thread block goes through its share 128 tokens at a time.  Scores are formed
-// transposed, tokens x rows, warp w those of the tile's block w: the key codes are
-// operand A (m16 = the block's tokens), widened to fp16 on the way, and q, as fp16
-// times a power of two of its row, operand B (n8 = rows).  So 1 to 8 rows cost half of
-// what rows as operand A would, and no code is widened twice.  The weights go as
-// fp16 through shared memory, and the outputs are formed transposed too, components
-// x rows, with the value codes as operand A: warp w takes the 32 components w % 4
-// from the half w / 4 of the tile.  Each warp brings its block of the tiles to
-// come, one bulk copy a block, into a ring of blocks, where a place is free behind
-// the barrier of the tile after.
+// transposed, tokens x rows, warp w of four those of the tile's blocks w and w + 4:
+// the key codes are operand A (m16 = a block's tokens), widened to fp16 on the way,
+// and q, as fp16 times a power of two of its row, operand B (n8 = rows), in registers
+// for a whole piece.  So 1 to 8 rows cost half of what rows as operand A would, and no
+// code is widened twice.  The weights go as fp16 through shared memory, and the outputs
+// are formed transposed too, components x rows, with the value codes as operand A: warp
+// w takes 32 components.  Each warp brings its blocks of the tiles to come, one bulk
+// copy a block, into a ring of tiles, where one is free behind the barrier of the tile
+// after.
+//
+// Four warps of 255 registers and not eight of 128: with q of 32 rows read from
+// shared memory by eight warps a tile, that was busy 57% of the time (12 x 8 tokens at
+// 8192 65.0 us, four warps 58.8; 96 x 1 at 512 30.0 and 28.3).
 //
 // One barrier a tile: the reference m is raised only where a weight would pass
 // 2^15, and then to put the row's largest at 2^0, so that weights are formed and
@@ -64,7 +68,10 @@
 namespace qlin {
 namespace {
 
+constexpr int kAttnWarps = 4;
+constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kTileBlocks = 8;      // of 16 tokens, of a tile
+constexpr int kOf = kTileBlocks / kAttnWarps;     // of them that a warp scores: w, w + 4
 constexpr int kTile = 16 * kTileBlocks;
 constexpr int kMinShare = kTileBlocks;
 constexpr int kQStride = 272;       // bytes of a row of q: rows 16 bytes apart mod 128
@@ -83,19 +90,15 @@ constexpr float kNewWeight = 0.0f;
 template <int NR>
 struct Shape {
   static constexpr int kRows = 8 * NR;
-  static constexpr int kWarps = NR == 4 ? 4 : 8;
-  static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kOf = kTileBlocks / kWarps;      // blocks of a tile that a warp scores
-  static constexpr int kRowsOf = kRows / kWarps;        // rows whose q it brings
+  static constexpr int kRowsOf = kRows / kAttnWarps;    // whose q a warp brings
   // blocks in the ring: what two thread blocks an SM have room for
-  static constexpr int kSlots = NR == 1 ? 24 : NR == 2 ? 22 : 16;
+  static constexpr int kSlots = NR == 1 ? 24 : 16;
+  static_assert(kSlots % kTileBlocks == 0, "whole tiles");
   // shared memory, in order
   static constexpr int kQ = kSlots * kCacheBlock;
   static constexpr int kP = kQ + kRows * kQStride;       // weights of two tiles
-  static constexpr int kO = kP;                          // fp32 [rows][128], when a piece is done
-  static_assert(512 <= 2 * kPStride, "outputs stand where the weights did");
   static constexpr int kPair = kP + 2 * kRows * kPStride;      // float2 [warps][rows]: references; sums
-  static constexpr int kRef = kPair + kWarps * kRows * 8;     // float4 [rows / 2]: two rows' references
+  static constexpr int kRef = kPair + kAttnWarps * kRows * 8;     // float4 [rows / 2]: two rows' references
   static constexpr int kKeep = kRef + kRows * 8;         // fp32 [rows]: what a raised reference leaves of the sums
   static constexpr int kFactor = kKeep + kRows * 4;      // fp32 [rows]
   // of two pieces:
@@ -335,16 +338,16 @@ __device__ __forceinline__ float log2_above(float v) {
 }
 
 template <int NR, bool kCap>
-__global__ void __launch_bounds__(Shape<NR>::kThreads, 2) attn_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams p) {
   using S = Shape<NR>;
-  constexpr int kSlots = S::kSlots, kWarps = S::kWarps, kThreads = S::kThreads, kOf = S::kOf, kRowsOf = S::kRowsOf;
+  constexpr int kSlots = S::kSlots, kRowsOf = S::kRowsOf;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kTilesAhead];    // a tile's blocks are there
-  __shared__ Walk aheads[kWarps];       // of each warp's copies
+  __shared__ Walk aheads[kAttnWarps];       // of each warp's copies
   __shared__ Piece pieces[kPieces];
   __shared__ Walk start;
   __shared__ int abort_flag;
-  __shared__ int64_t warp_sums[kWarps];
+  __shared__ int64_t warp_sums[kAttnWarps];
   const PagedAttnArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int segs = p.row_tiles * static_cast<int>(a.c.kv_heads);
@@ -405,7 +408,7 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, 2) attn_kernel(const Attn
       __syncthreads();
       all = 0;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
+      for (int w = 0; w < kAttnWarps; ++w) {
         if (w < warp) incl += warp_sums[w];
         all += warp_sums[w];
       }
@@ -415,7 +418,7 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, 2) attn_kernel(const Attn
     int64_t incl, all;
     chunk(0, n0, incl, all);
     int64_t total = all;
-    for (int64_t b0 = kThreads; b0 < a.c.B; b0 += kThreads) {
+    for (int64_t b0 = kAttnThreads; b0 < a.c.B; b0 += kAttnThreads) {
       int n;
       int64_t i, s;
       chunk(b0, n, i, s);
@@ -428,8 +431,8 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, 2) attn_kernel(const Attn
       if (tid == 0) p.cuts[4 * blockIdx.x] = -1;
       return;
     }
-    for (int64_t b0 = 0, before = 0;; b0 += kThreads) {
-      if (a.c.B > kThreads) chunk(b0, n0, incl, all);
+    for (int64_t b0 = 0, before = 0;; b0 += kAttnThreads) {
+      if (a.c.B > kAttnThreads) chunk(b0, n0, incl, all);
       const int64_t from = (before + incl - n0) * segs;
       if (n0 > 0 && from <= at && at < from + static_cast<int64_t>(n0) * segs) {
         start.b = b0 + tid;
@@ -473,9 +476,9 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, 2) attn_kernel(const Attn
     const uint16_t* const from = a.q + b * a.T * a.q_heads * kHeadDim + 8 * (lane & 15);
 #pragma unroll
     for (int k = 0; k < kRowsOf; k += 2) {      // half a warp a row
-      const int r = warp + kWarps * (k + (kRowsOf > 1 ? lane >> 4 : 0));
+      const int r = warp + kAttnWarps * (k + (lane >> 4));
       const int at = __shfl_sync(kAll, to, r);
-      if (at >= 0 && (kRowsOf > 1 || lane < 16))
+      if (at >= 0)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(raw + r * kHeadDim * 2 + 16 * (lane & 15))),
                      "l"(from + static_cast<int64_t>(at) * kHeadDim)
                      : "memory");
@@ -498,7 +501,7 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, 2) attn_kernel(const Attn
   auto look = [&]() {                // at the pages of 32 tiles
 #pragma unroll
     for (int k = 0; k < kOf; ++k) {
-      const int i = next_i + kTileBlocks * lane + warp + kWarps * k;
+      const int i = next_i + kTileBlocks * lane + warp + kAttnWarps * k;
       const int n = first + i, of_table = n / per_page;
       in_head[k] = head_at + n - of_table * per_page;
       page[k] = i < next_n ? __ldg(a.c.block_table + ahead.b * a.c.max_pages + of_table) : -1;
@@ -517,7 +520,7 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, 2) attn_kernel(const Attn
   };
   // tile: the one whose predecessors are done
   auto send = [&](int tile) {
-    if (!more || kTileBlocks * to_send + (kOf > 1 ? kTileBlocks - 1 : warp) >= kTileBlocks * tile + kSlots) return;
+    if (!more || kTileBlocks * to_send >= kTileBlocks * tile + kSlots) return;
     const int from = next_i / kTileBlocks % 32;
     const int of = to_send % kTilesAhead;
 #pragma unroll
@@ -526,7 +529,7 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, 2) attn_kernel(const Attn
       const bool real = on >= 0 && on < a.c.pages;
       if (ok && lane == 0) {
         const uint32_t bar = smem_u32(&full[of]);
-        const int slot = send_slot + kWarps * k;
+        const int slot = send_slot + kAttnWarps * k;
         mbar_arrive_expect_tx(bar, real ? kCacheBlock : 0);
         if (real)
           bulk_load(smem_u32(smem) + slot * kCacheBlock, a.c.cache + (static_cast<int64_t>(on) * page_blocks + in) * kCacheBlock,
@@ -566,11 +569,9 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, 2) attn_kernel(const Attn
   // 2 u + 1, 4 chunks each) meet in no bank.
   const int tok = 2 * (g >> 1) + 8 * (g & 1);
   const int k_turn = 2 * ((tok >> 2) & 3);
-  // Outputs: components 32 quarter + 4 g .. + 3 of all rows, from four blocks of a tile.
-  const int quarter = warp & 3, half = warp >> 2;
+  // Outputs: components 32 warp + 4 g .. + 3 of all rows.
   uint8_t* const qs = smem + S::kQ;
   uint8_t* const ps = smem + S::kP;
-  float* const os = reinterpret_cast<float*>(smem + S::kO);
   float2* const pairs = reinterpret_cast<float2*>(smem + S::kPair);
   float4* const refs = reinterpret_cast<float4*>(smem + S::kRef);
   float* const keeps = reinterpret_cast<float*>(smem + S::kKeep);
@@ -582,8 +583,7 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, 2) attn_kernel(const Attn
   // A row's reference is a score (its negative is held) plus a small number, so
   // that large scores do not swallow the logarithm of the value scale in it.
   f32x2 sum[NR];
-  constexpr int kHeld = NR <= 2 || kOf > 1 ? NR : 0;      // groups whose q stays in registers
-  uint4 qb[kHeld > 0 ? kHeld : 1][4];
+  uint4 qb[NR][4];
   auto q_part = [&](int r, int c) {            // operand B: components 16 (q + 4 (c / 2)) + 8 (c % 2) .. + 7
     return *reinterpret_cast<const uint4*>(qs + (8 * r + g) * kQStride + 32 * (q + 4 * (c >> 1)) + 16 * (c & 1));
   };
@@ -621,12 +621,12 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, 2) attn_kernel(const Attn
       uint2 x[kRowsOf];
 #pragma unroll
       for (int k = 0; k < kRowsOf; ++k) {
-        const int r = warp + kWarps * k;
+        const int r = warp + kAttnWarps * k;
         x[k] = __shfl_sync(kAll, to, r) >= 0 ? *reinterpret_cast<const uint2*>(raw + r * kHeadDim * 2 + 8 * lane) : make_uint2(0, 0);
       }
 #pragma unroll
       for (int k = 0; k < kRowsOf; ++k) {
-        const int r = warp + kWarps * k;
+        const int r = warp + kAttnWarps * k;
         const float f[4] = {__uint_as_float(x[k].x << 16), __uint_as_float(x[k].x & 0xFFFF0000u), __uint_as_float(x[k].y << 16),
                             __uint_as_float(x[k].y & 0xFFFF0000u)};
         // the largest exponent (of finite numbers' bits the order is that of the numbers)
@@ -642,7 +642,7 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, 2) attn_kernel(const Attn
       }
       __syncthreads();
 #pragma unroll
-      for (int r = 0; r < kHeld; ++r) {
+      for (int r = 0; r < NR; ++r) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) qb[r][c] = q_part(r, c);
       }
@@ -669,7 +669,7 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, 2) attn_kernel(const Attn
 #pragma unroll
     for (int k = 0; k < kOf; ++k) {
       here[k] = ok && (on_page >> (tile % kTilesAhead * kOf + k) & 1u);
-      const int j = j0 + 16 * (warp + kWarps * k);
+      const int j = j0 + 16 * (warp + kAttnWarps * k);
       all_seen = all_seen && here[k] && j >= seen_from && j + 16 <= seen_to;
     }
 
@@ -681,8 +681,7 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, 2) attn_kernel(const Attn
       float s[kOf][NR][4];
 #pragma unroll
       for (int k = 0; k < kOf; ++k) {
-        const int mine = slot + warp + kWarps * k;
-        keys[k] = smem + (mine >= kSlots ? mine - kSlots : mine) * kCacheBlock;
+        keys[k] = smem + (slot + warp + kAttnWarps * k) * kCacheBlock;
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
 #pragma unroll
@@ -706,8 +705,7 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, 2) attn_kernel(const Attn
           biased_u8x4_to_f16x4(kb.w, fa[3][1], fa[3][3]);
 #pragma unroll
           for (int r = 0; r < NR; ++r) {
-            const uint4 b0 = r < kHeld ? qb[r < kHeld ? r : 0][2 * c] : q_part(r, 2 * c);
-            const uint4 b1 = r < kHeld ? qb[r < kHeld ? r : 0][2 * c + 1] : q_part(r, 2 * c + 1);
+            const uint4 b0 = qb[r][2 * c], b1 = qb[r][2 * c + 1];
             mma(s[k][r], fa[0], b0.x, b0.y);
             mma(s[k][r], fa[1], b0.z, b0.w);
             mma(s[k][r], fa[2], b1.x, b1.y);
@@ -750,7 +748,7 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, 2) attn_kernel(const Attn
           const int2 hi = *reinterpret_cast<const int2*>(highs + odd * S::kRows + 8 * r + 2 * q);
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const int at = j0 + 16 * (warp + kWarps * k) + tok + c;
+            const int at = j0 + 16 * (warp + kAttnWarps * k) + tok + c;
             float v0, v1;
             unpack2(x[k][r][c], v0, v1);
             x[k][r][c] = pack2(here[k] && at >= lo.x && at < hi.x ? v0 : -INFINITY, here[k] && at >= lo.y && at < hi.y ? v1 : -INFINITY);
@@ -794,7 +792,7 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, 2) attn_kernel(const Attn
 #pragma unroll
               for (int e = 0; e < 4; ++e) w[e] = v[e] == -INFINITY ? 0.0f : w[e];
             }
-            uint8_t* const to = weights + (8 * r + 2 * q) * kPStride + 2 * (16 * (warp + kWarps * k) + tok);
+            uint8_t* const to = weights + (8 * r + 2 * q) * kPStride + 2 * (16 * (warp + kAttnWarps * k) + tok);
             *reinterpret_cast<__half2*>(to) = __floats2half2_rn(w[0], w[2]);
             *reinterpret_cast<__half2*>(to + kPStride) = __floats2half2_rn(w[1], w[3]);
           }
@@ -829,14 +827,14 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, 2) attn_kernel(const Attn
       __syncthreads();
       float most = kNone, over = -INFINITY;
       if (lane < S::kRows) {
-        float2 of[kWarps];
+        float2 of[kAttnWarps];
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < kAttnWarps; ++w) {
           of[w] = pairs[w * S::kRows + lane];
           most = fmaxf(most, of[w].x);
         }
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) over = fmaxf(over, (of[w].x - most) + of[w].y);
+        for (int w = 0; w < kAttnWarps; ++w) over = fmaxf(over, (of[w].x - most) + of[w].y);
         over -= kNewWeight;
       }
       float* const ref = reinterpret_cast<float*>(refs + (lane >> 1)) + (lane & 1);
@@ -875,9 +873,8 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, 2) attn_kernel(const Attn
     for (int r = 0; r < NR; ++r) sum[r] = add2(sum[r], part[r]);
     // ---- outputs
 #pragma unroll
-    for (int k = 0; k < 4 * kOf; ++k) {
-      const int in_tile = 4 * half + k, of = slot + in_tile;
-      const uint8_t* const v = smem + (of >= kSlots ? of - kSlots : of) * kCacheBlock + kVCodes + 4 * q * kHeadDim + 32 * (quarter ^ q) + 4 * g;
+    for (int k = 0; k < kTileBlocks; ++k) {
+      const uint8_t* const v = smem + (slot + k) * kCacheBlock + kVCodes + 4 * q * kHeadDim + 32 * (warp ^ q) + 4 * g;
       uint32_t w[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) w[e] = *reinterpret_cast<const uint32_t*>(v + e * kHeadDim);
@@ -888,7 +885,7 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, 2) attn_kernel(const Attn
       biased_u8x4_to_f16x4(prmt(w[2], w[3], 0x7362u), fa[1][2], fa[1][3]);
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
-        const uint2 b = *reinterpret_cast<const uint2*>(weights + (8 * r + g) * kPStride + 32 * in_tile + 8 * q);
+        const uint2 b = *reinterpret_cast<const uint2*>(weights + (8 * r + g) * kPStride + 32 * k + 8 * q);
         mma(o[0][r], fa[0], b.x, b.y);
         mma(o[1][r], fa[1], b.x, b.y);
       }
@@ -898,7 +895,7 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, 2) attn_kernel(const Attn
     j0 += kTile;
 
     if (i >= n) {
-      // ---- the piece is done: sums over the warps, outputs of the two halves
+      // ---- the piece is done: sums over the warps, outputs
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
         float l[2];
@@ -910,46 +907,32 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, 2) attn_kernel(const Attn
         }
         if (g == 0) *reinterpret_cast<float4*>(pairs + warp * S::kRows + 8 * r + 2 * q) = make_float4(l[0], 0.0f, l[1], 0.0f);
       }
-      __syncthreads();      // the weights are read
-      if (kOf == 1 && half == 1) {
+      __syncthreads();
+      const bool whole = piece.whole;
+      float l = 0.0f;       // lane by row
+      if (lane < S::kRows) {
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-            *reinterpret_cast<float4*>(os + (8 * r + 2 * q + c) * kHeadDim + 32 * quarter + 4 * g) =
-                make_float4(o[0][r][c], o[0][r][2 + c], o[1][r][c], o[1][r][2 + c]);
-        }
+        for (int w = 0; w < kAttnWarps; ++w) l += pairs[w * S::kRows + lane].x;
       }
-      if (kOf == 1) __syncthreads();
-      if (half == 0) {
-        const bool whole = piece.whole;
-        float l = 0.0f;       // lane by row
-        if (lane < S::kRows) {
+      const int64_t part = (2LL * blockIdx.x + (piece.cut > 0 ? 0 : 1)) * S::kRows;
+      if (!whole && warp == 0 && lane < S::kRows) {
+        const float* const ref = reinterpret_cast<const float*>(refs + (lane >> 1)) + (lane & 1);
+        p.part_share[part + lane] = Share{-ref[0], ref[2], l, 0.0f};
+      }
+      const float back = !whole ? 1.0f : l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);      // 0: no token seen
+      uint16_t* const out = a.out + piece.b * a.T * a.q_heads * kHeadDim + 32 * warp + 4 * g;
+      float* const part_o = p.part_o + part * kHeadDim + 32 * warp + 4 * g;
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) l += pairs[w * S::kRows + lane].x;
-        }
-        const int64_t part = (2LL * blockIdx.x + (piece.cut > 0 ? 0 : 1)) * S::kRows;
-        if (!whole && warp == 0 && lane < S::kRows) {
-          const float* const ref = reinterpret_cast<const float*>(refs + (lane >> 1)) + (lane & 1);
-          p.part_share[part + lane] = Share{-ref[0], ref[2], l, 0.0f};
-        }
-        const float back = !whole ? 1.0f : l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);      // 0: no token seen
-        uint16_t* const out = a.out + piece.b * a.T * a.q_heads * kHeadDim + 32 * quarter + 4 * g;
-        float* const part_o = p.part_o + part * kHeadDim + 32 * quarter + 4 * g;
+      for (int r = 0; r < NR; ++r) {
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int in_tile = 8 * r + 2 * q + c, to = tos[odd * S::kRows + in_tile];
-            const float f = __shfl_sync(kAll, back, in_tile);
-            const float4 v = kOf == 1 ? *reinterpret_cast<const float4*>(os + in_tile * kHeadDim + 32 * quarter + 4 * g) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            const float4 sums = make_float4((o[0][r][c] + v.x) * f, (o[0][r][2 + c] + v.y) * f, (o[1][r][c] + v.z) * f,
-                                            (o[1][r][2 + c] + v.w) * f);
-            if (to >= 0 && whole)
-              *reinterpret_cast<uint2*>(out + static_cast<int64_t>(to) * kHeadDim) =
-                  make_uint2(bf16x2_rn(sums.x, sums.y), bf16x2_rn(sums.z, sums.w));
-            if (to >= 0 && !whole) *reinterpret_cast<float4*>(part_o + in_tile * kHeadDim) = sums;
-          }
+        for (int c = 0; c < 2; ++c) {
+          const int in_tile = 8 * r + 2 * q + c, to = tos[odd * S::kRows + in_tile];
+          const float f = __shfl_sync(kAll, back, in_tile);
+          const float4 sums = make_float4(o[0][r][c] * f, o[0][r][2 + c] * f, o[1][r][c] * f, o[1][r][2 + c] * f);
+          if (to >= 0 && whole)
+            *reinterpret_cast<uint2*>(out + static_cast<int64_t>(to) * kHeadDim) =
+                make_uint2(bf16x2_rn(sums.x, sums.y), bf16x2_rn(sums.z, sums.w));
+          if (to >= 0 && !whole) *reinterpret_cast<float4*>(part_o + in_tile * kHeadDim) = sums;
         }
       }
       if (piece.final) break;
@@ -1068,7 +1051,7 @@ cudaError_t launch_groups(const AttnParams& p, int grid, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_release);
   }
-  e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(Shape<NR>::kThreads), Shape<NR>::kBytes, stream, p);
+  e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kAttnThreads), Shape<NR>::kBytes, stream, p);
   if (e != cudaSuccess) return e;
   const int64_t rows = p.a.T * p.G, segments = p.a.c.B * p.row_tiles * p.a.c.kv_heads;
   if (p.planned && few_segments(segments, grid))
