@@ -374,7 +374,8 @@ class Attn:
     (1, 1, 14, 2, 64, [200], {}),
     # drafted blocks: rows of 8 to 128 a key/value head
     (2, 8, 4, 1, 16, [8, 140], {}), (2, 8, 16, 4, 16, [40, 300], {}), (1, 3, 30, 6, 48, [1000], {}), (2, 8, 8, 1, 16, [90, 9], {}),
-    (1, 16, 8, 1, 16, [200], {}), (1, 9, 7, 1, 16, [70], {}), (1, 33, 2, 1, 16, [100], {}), (1, 1, 65, 1, 16, [50], {}),
+    (2, 5, 4, 1, 16, [300, 20], {}), (3, 3, 16, 2, 16, [150, 3, 70], {}), (1, 10, 8, 2, 16, [280], {"causal": False}),
+    (2, 9, 8, 1, 16, [200, 33], {"window": 70}), (1, 16, 8, 1, 16, [200], {}), (1, 9, 7, 1, 16, [70], {}), (1, 33, 2, 1, 16, [100], {}), (1, 1, 65, 1, 16, [50], {}),
     # masks
     (2, 8, 4, 1, 16, [8, 300], {"causal": False}), (2, 8, 4, 2, 16, [20, 300], {"window": 1}), (2, 8, 4, 2, 16, [20, 300], {"window": 5}),
     (2, 8, 4, 2, 16, [20, 300], {"window": 5, "causal": False}), (2, 1, 4, 1, 16, [300, 299], {"window": 128}),

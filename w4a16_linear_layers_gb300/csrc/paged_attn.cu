@@ -37,14 +37,13 @@
 // through one producer warp a tile took twice the time.)
 //
 // Where the time goes (two thread blocks an SM): with 32 rows a tile of 128 tokens
-// takes one of them 4700 cycles, 1300 for scores, 700 weights, 300 the barrier, 600
-// the copies' issue, 1100 outputs; the tensor pipe is 36% busy, shared memory 57%
-// (q read again by each warp), issue 53%: the chain through a tile bounds it, not one
-// of them (12 x 8 tokens at 8192: 64.7 us, 2.5 TB/s).  With 8 rows a tile takes 2200
-// to 3400 and the copies keep up (96 x 1 at 4096: 106.5 us, 5.9 TB/s; 1 x 131072:
-// 48.5 us, 5.7 TB/s).  Beginning a share takes 4 us (lengths, the plan, a page, the
-// first blocks: five loads one behind the other), ending a piece 0.6: what short
-// calls are made of (1 x 515: 6.6 us).
+// takes one of them 4600 cycles, 1300 for scores, 700 weights, 300 the barrier, 700
+// the copies' issue, 1200 outputs; the tensor pipe is 45% busy, and the chain through a
+// tile bounds it (12 x 8 tokens at 8192: 57.9 us, 2.8 TB/s; 8 rows less take 7 us less).
+// With 8 rows a tile takes 2200 to 3000 and the copies keep up (96 x 1 at 4096:
+// 104.6 us, 6.0 TB/s; 1 x 131072: 47.5 us, 5.8 TB/s).  Beginning a share takes 4 us
+// (lengths, the plan, a page, the first blocks: loads one behind the other), ending a
+// piece 0.4: what short calls are made of (1 x 515: 6.4 us).
 //
 // mma.sync, not tcgen05: its operands come from registers, where the codes are
 // widened; tcgen05's would have to be written to shared or tensor memory first,
@@ -1034,9 +1033,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_segments_kernel(const At
   j.store(p, b, seg, row, t, lane);
 }
 
-// 8-row groups of a tile for `rows` rows: as few as hold them, four at most.
-int row_groups(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
-
+// 8-row groups of a tile for `rows` rows: as few tiles of 32 rows as hold them, and as
+// small ones (each reads the segment's blocks again).  12 sequences at 8192: 24 rows
+// 50.9 us, 56.5 in a tile of 32; 40 rows in two of 24 81.4, in two of 32 93.3.
+int row_groups(int64_t rows) {
+  const int64_t tiles = (rows + 31) / 32;
+  return static_cast<int>(((rows + tiles - 1) / tiles + 7) / 8);
+}
 
 template <int NR, bool kCap>
 cudaError_t launch_groups(const AttnParams& p, int grid, cudaStream_t stream) {
@@ -1098,6 +1101,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, int* err, int sm_count, cu
   switch (groups) {
     case 1: return launch_cap<1>(p, grid, stream);
     case 2: return launch_cap<2>(p, grid, stream);
+    case 3: return launch_cap<3>(p, grid, stream);
     default: return launch_cap<4>(p, grid, stream);
   }
 }
