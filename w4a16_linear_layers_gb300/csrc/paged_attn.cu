@@ -161,12 +161,12 @@ __host__ __device__ inline bool few_segments(int64_t segments, int64_t grid) { r
 // How the work of up to 32 sequences, less than 2^31 blocks, is shared out; each
 // warp finds it by itself, lane by sequence.  Either every thread block takes
 // `share` blocks of the list, or (own) segments are cut into parts of their own: a
-// thread block that holds parts of two begins and ends two pieces, 1 to 3 us more
+// thread block that holds parts of two begins and ends two pieces, 1 to 2 us more
 // than the others.  Then the share is the smallest for which the parts,
 // ceil(n_s / share) of a segment of n_s blocks, are no more than the thread blocks.
-// That is done where it is at most kPieceBlocks over the even one (12 x 8 rows: at
-// 2 over 41 32.4 us, 35.6 with even shares; at 15 over 126 71.5 and 67.5), and where
-// segments are few (then it is less than grid / (grid - segments) times the even
+// That is done where it is at most kPieceBlocks over the even one (12 x 8 rows in a
+// window of 2048, 2 over 41: 28.3 us, 30.8 with even shares; of 1000 tokens 21.0 and
+// 23.2; at 8192, 15 over 126, 58.1 and 58.0), and where segments are few (then it is less than grid / (grid - segments) times the even
 // one, and the parts are joined by segment).
 constexpr int kPieceBlocks = 5;
 struct Plan {
