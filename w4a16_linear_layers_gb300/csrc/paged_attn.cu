@@ -121,7 +121,10 @@ struct AttnParams {
   int row_tiles;       // of a sequence's T * G rows
   bool planned;        // Plan is used; then
   int each;            // thread blocks of a segment, 0: fewer than segments
-  uint64_t per_grid;   // 2^40 / grid, rounded up
+  // Quotients by these come from products (a division is a chain of 20 instructions,
+  // and a share's beginning one of such chains): 2^40, 2^36, 2^40 and 2^38 over each,
+  // rounded up
+  uint64_t per_grid, per_each, per_group, per_page;
   float cap, per_cap;  // of scores times log2(e); 1 / softcap
   int* err;
   // workspace: where the cut segments are, then their parts
@@ -129,6 +132,16 @@ struct AttnParams {
   Share* part_share;   // [2 grid][rows]
   float* part_o;       // [2 grid][rows][128]
 };
+
+// x / d with m = 2^s / d rounded up: exact where x (d - 1) is below 2^s and x m below 2^64.
+__device__ __forceinline__ int over(int x, uint64_t m, int s) { return static_cast<int>(static_cast<uint32_t>(x) * m >> s); }
+
+// x / d where that is below 2^16 (fp32's quotient is then less than one off)
+__device__ __forceinline__ int few_times(int x, int d) {
+  const int q = static_cast<int>(__fdividef(static_cast<float>(x), static_cast<float>(d)));
+  const int rest = x - q * d;
+  return rest < 0 ? q - 1 : rest >= d ? q + 1 : q;
+}
 
 // Blocks of 16 of a sequence that its new rows see, and the first of them.
 struct Span {
@@ -144,15 +157,14 @@ __device__ __forceinline__ Span span_of(const PagedAttnArgs& a, const SeqLen& s)
 }
 
 // Blocks of 16 that each of `grid` thread blocks takes.
-__device__ __forceinline__ int64_t share_of(int64_t total, int grid) {
-  // (a 32-bit division unless it takes more: a tenth of the instructions)
-  const int64_t share = total < 1LL << 31 ? static_cast<uint32_t>(total + grid - 1) / static_cast<uint32_t>(grid) : (total + grid - 1) / grid;
+__device__ __forceinline__ int64_t share_of(const AttnParams& p, int64_t total, int grid) {
+  const int64_t share = total < 1LL << 30 ? over(static_cast<int>(total) + grid - 1, p.per_grid, 40) : (total + grid - 1) / grid;
   return share < kMinShare ? kMinShare : share;
 }
 
-// The share that block `at` is in.
+// The share that block `at` is in (of fewer than 2^16).
 __device__ __forceinline__ int share_at(int64_t at, int64_t share) {
-  return (at | share) < 1LL << 31 ? static_cast<int>(at) / static_cast<int>(share) : static_cast<int>(at / share);
+  return at < 1LL << 30 ? few_times(static_cast<int>(at), static_cast<int>(share)) : static_cast<int>(at / share);
 }
 
 // Segments that can be of eight parts and more each.
@@ -182,25 +194,24 @@ struct Plan {
     const int n = span_of(p.a, seq).count;
     blocks = __reduce_add_sync(kAll, n) * segs;
     // (exact: blocks are less than 2^31, and grid times that less than 2^40)
-    const int even = max(static_cast<int>(static_cast<uint32_t>(blocks + grid - 1) * p.per_grid >> 40), kMinShare);
+    const int even = max(over(blocks + grid - 1, p.per_grid, 40), kMinShare);
     const bool few = few_segments(B * segs, grid);
     share = even;
     own = false;
     if (p.each > 0) {
-      const int each = p.each;
       // as many parts of each: enough, and hardly more where lengths are alike
-      int lo = even, hi = max((__reduce_max_sync(kAll, n) + each - 1) / each, even);
+      int lo = even, hi = max(over(__reduce_max_sync(kAll, n) + p.each - 1, p.per_each, 36), even);
       if (hi <= lo + 2) lo = hi;
       if (!few && hi > lo + kPieceBlocks) hi = lo + kPieceBlocks + 1;      // not taken
       while (lo < hi) {
         const int mid = (lo + hi) / 2;
-        if (__reduce_add_sync(kAll, (n + mid - 1) / mid) * segs <= grid) hi = mid;
+        if (__reduce_add_sync(kAll, few_times(n + mid - 1, mid)) * segs <= grid) hi = mid;
         else lo = mid + 1;
       }
       own = few || lo <= even + kPieceBlocks;
       if (own) share = lo;
     }
-    parts = own ? (n + share - 1) / share : n;
+    parts = own ? few_times(n + share - 1, share) : n;      // (shares are n / grid and more)
     int incl = parts;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -218,7 +229,7 @@ struct Plan {
     b = __ffs(who) - 1;
     const int in = __shfl_sync(kAll, in_b, b);
     of = __shfl_sync(kAll, parts, b);
-    seg = in / of;
+    seg = segs < 1 << 16 ? few_times(in, of) : in / of;
     at = in - seg * of;
     return true;
   }
@@ -383,7 +394,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
         const int from = c * plan.share;
         walk.off = piece_at;
         walk.left = min(plan.blocks - from, plan.share);
-        if (piece_at > 0 && piece_at <= plan.share) cut = make_int4(seg, c - 1, (from - piece_at + of - 1) / plan.share, b);
+        if (piece_at > 0 && piece_at <= plan.share) cut = make_int4(seg, c - 1, few_times(from - piece_at + of - 1, plan.share), b);
       }
     }
     if (tid == 0) *reinterpret_cast<int4*>(p.cuts + 4 * c) = cut;
@@ -424,7 +435,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
       total += s;
     }
     total *= segs;
-    const int64_t share = share_of(total, gridDim.x);
+    const int64_t share = share_of(p, total, gridDim.x);
     const int64_t at = blockIdx.x * share;
     if (at >= total) {
       if (tid == 0) p.cuts[4 * blockIdx.x] = -1;
@@ -437,7 +448,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
         start.b = b0 + tid;
         start.segs = segs;
         const int64_t in_b = at - from;
-        start.seg = in_b < 1LL << 31 ? static_cast<int>(in_b) / n0 : static_cast<int>(in_b / n0);
+        start.seg = in_b < 1LL << 30 && segs < 1 << 16 ? few_times(static_cast<int>(in_b), n0) : static_cast<int>(in_b / n0);
         start.off = static_cast<int>(in_b - static_cast<int64_t>(start.seg) * n0);
         start.left = total - at < share ? total - at : share;
         start.seq = seq;
@@ -468,7 +479,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
   int to_next = 0, token_next = 0;
   auto place = [&](int seg, int fresh, int& t) {
     const int h = p.row_tiles == 1 ? seg : seg / p.row_tiles, row = (seg - h * p.row_tiles) * S::kRows + lane;
-    t = row / p.G;
+    t = rows < 1 << 24 ? over(row, p.per_group, 40) : row / p.G;
     return lane < S::kRows && row < rows && t < fresh ? t * static_cast<int>(a.q_heads) + h * p.G + (row - t * p.G) : -1;
   };
   auto bring_q = [&](int64_t b, int to) {
@@ -501,7 +512,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
 #pragma unroll
     for (int k = 0; k < kOf; ++k) {
       const int i = next_i + kTileBlocks * lane + warp + kAttnWarps * k;
-      const int n = first + i, of_table = n / per_page;
+      const int n = first + i, of_table = over(n, p.per_page, 38);
       in_head[k] = head_at + n - of_table * per_page;
       page[k] = i < next_n ? __ldg(a.c.block_table + ahead.b * a.c.max_pages + of_table) : -1;
     }
@@ -1094,6 +1105,10 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, int* err, int sm_count, cu
   p.planned = a.c.B <= 32 && segments <= ((1LL << 31) - 1 - 2 * kTile * grid) / longest;
   p.each = static_cast<int>(grid / segments);
   p.per_grid = ((1ULL << 40) + grid - 1) / grid;
+  if (p.each > 0) p.per_each = ((1ULL << 36) + p.each - 1) / p.each;      // (of less than 2^27)
+  p.per_group = ((1ULL << 40) + p.G - 1) / p.G;
+  const uint64_t in_page = static_cast<uint64_t>(a.c.page_size / 16);
+  p.per_page = ((1ULL << 38) + in_page - 1) / in_page;      // (2^12 blocks at most, of 2^26)
   uint8_t* const ws = static_cast<uint8_t*>(a.workspace);
   p.cuts = reinterpret_cast<int32_t*>(ws);
   p.part_o = reinterpret_cast<float*>(ws + static_cast<size_t>(grid) * 16);
