@@ -90,7 +90,12 @@ template <int NR>
 struct Shape {
   static constexpr int kRows = 8 * NR;
   static constexpr int kRowsOf = kRows / kAttnWarps;    // whose q a warp brings
-  // blocks in the ring: what two thread blocks an SM have room for
+  // Blocks in the ring: whole tiles, as many as two thread blocks an SM have room
+  // for.  A tile's blocks leave when its predecessor is done, so with 8 rows, whose
+  // tiles are short, three tiles and not two (96 x 1 at 4096 104 us, 134).  Three thread
+  // blocks of two tiles each would take short contexts (96 x 1 at 512 24.6 us for 27.5)
+  // further than long ones back (12 x 1 at 8192 35.6 for 34.3, 1 x 8192 10.4 for 8.9), but
+  // lengths are not known where a grid is chosen.
   static constexpr int kSlots = NR == 1 ? 24 : 16;
   static_assert(kSlots % kTileBlocks == 0, "whole tiles");
   // shared memory, in order
