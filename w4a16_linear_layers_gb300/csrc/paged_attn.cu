@@ -73,7 +73,6 @@ constexpr int kTileBlocks = 8;      // of 16 tokens, of a tile
 constexpr int kOf = kTileBlocks / kAttnWarps;     // of them that a warp scores: w, w + 4
 constexpr int kTile = 16 * kTileBlocks;
 constexpr int kMinShare = kTileBlocks;
-constexpr int kQStride = 272;       // bytes of a row of q: rows 16 bytes apart mod 128
 constexpr int kPStride = 288;       // bytes of a row of weights: rows 32 bytes apart mod 128
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
@@ -91,16 +90,17 @@ struct Shape {
   static constexpr int kRows = 8 * NR;
   static constexpr int kRowsOf = kRows / kAttnWarps;    // whose q a warp brings
   // Blocks in the ring: whole tiles, as many as two thread blocks an SM have room
-  // for.  A tile's blocks leave when its predecessor is done, so with 8 rows, whose
-  // tiles are short, three tiles and not two (96 x 1 at 4096 104 us, 134).  Three thread
+  // for.  A tile's blocks are sent when the one two (three) before is done, which with
+  // few rows, whose tiles are short, is late in a ring of two tiles (96 x 1 at 4096 134 us,
+  // 104 in three; 12 x 4 at 8192 44.4 and 40.7).  Three thread
   // blocks of two tiles each would take short contexts (96 x 1 at 512 24.6 us for 27.5)
   // further than long ones back (12 x 1 at 8192 35.6 for 34.3, 1 x 8192 10.4 for 8.9), but
   // lengths are not known where a grid is chosen.
-  static constexpr int kSlots = NR == 1 ? 24 : 16;
+  static constexpr int kSlots = NR <= 2 ? 24 : 16;
   static_assert(kSlots % kTileBlocks == 0, "whole tiles");
   // shared memory, in order
-  static constexpr int kQ = kSlots * kCacheBlock;
-  static constexpr int kP = kQ + kRows * kQStride;       // weights of two tiles
+  // weights of two tiles; and, where a piece begins, its q, in the place of its first tile's
+  static constexpr int kP = kSlots * kCacheBlock;
   static constexpr int kPair = kP + 2 * kRows * kPStride;      // float2 [warps][rows]: references; sums
   static constexpr int kRef = kPair + kAttnWarps * kRows * 8;     // float4 [rows / 2]: two rows' references
   static constexpr int kKeep = kRef + kRows * 8;         // fp32 [rows]: what a raised reference leaves of the sums
@@ -109,8 +109,7 @@ struct Shape {
   static constexpr int kTo = kFactor + kRows * 4;        // int32 [rows]: the row's head of the sequence's outputs, -1: none
   static constexpr int kLow = kTo + 2 * kRows * 4;       // int32 [rows]: first token seen
   static constexpr int kHigh = kLow + 2 * kRows * 4;     // and the one behind the last
-  static constexpr int kRaw = kHigh + 2 * kRows * 4;     // bf16 [rows][128]: q of the piece to come
-  static constexpr int kBytes = kRaw + kRows * kHeadDim * 2;
+  static constexpr int kBytes = kHigh + 2 * kRows * 4;
 };
 
 // A row's reference m + c and the sum under it, of a part of its tokens.
@@ -479,7 +478,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
   // ---- q of the piece to come, each warp's rows, brought while the piece before
   // it ends
   const int rows = static_cast<int>(a.T) * p.G;
-  uint8_t* const raw = smem + S::kRaw;
+  uint8_t* const ps = smem + S::kP;
+  auto q_at = [&](int turn, int r) { return ps + (turn * S::kRows + r) * kPStride; };      // bf16, then fp16
   // lane by row: its head of the sequence's outputs, -1: none, and its new token
   int to_next = 0, token_next = 0;
   auto place = [&](int seg, int fresh, int& t) {
@@ -487,14 +487,14 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
     t = rows < 1 << 24 ? over(row, p.per_group, 40) : row / p.G;
     return lane < S::kRows && row < rows && t < fresh ? t * static_cast<int>(a.q_heads) + h * p.G + (row - t * p.G) : -1;
   };
-  auto bring_q = [&](int64_t b, int to) {
+  auto bring_q = [&](int64_t b, int to, int turn) {
     const uint16_t* const from = a.q + b * a.T * a.q_heads * kHeadDim + 8 * (lane & 15);
 #pragma unroll
     for (int k = 0; k < kRowsOf; k += 2) {      // half a warp a row
       const int r = warp + kAttnWarps * (k + (lane >> 4));
       const int at = __shfl_sync(kAll, to, r);
       if (at >= 0)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(raw + r * kHeadDim * 2 + 16 * (lane & 15))),
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(q_at(turn, r) + 16 * (lane & 15))),
                      "l"(from + static_cast<int64_t>(at) * kHeadDim)
                      : "memory");
     }
@@ -576,7 +576,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
   __syncwarp();
   enter();
   to_next = place(walk.seg, walk.seq.fresh, token_next);
-  bring_q(walk.b, to_next);
+  bring_q(walk.b, to_next, 0);
   for (int i = 0; kTileBlocks * i < kSlots; ++i) send(0);
   const int g = lane >> 2, q = lane & 3;
   // Scores: tokens tok and tok + 1 of the warp's block, rows 8 r + 2 q and the
@@ -585,8 +585,6 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
   const int tok = 2 * (g >> 1) + 8 * (g & 1);
   const int k_turn = 2 * ((tok >> 2) & 3);
   // Outputs: components 32 warp + 4 g .. + 3 of all rows.
-  uint8_t* const qs = smem + S::kQ;
-  uint8_t* const ps = smem + S::kP;
   float2* const pairs = reinterpret_cast<float2*>(smem + S::kPair);
   float4* const refs = reinterpret_cast<float4*>(smem + S::kRef);
   float* const keeps = reinterpret_cast<float*>(smem + S::kKeep);
@@ -599,8 +597,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
   // that large scores do not swallow the logarithm of the value scale in it.
   f32x2 sum[NR];
   uint4 qb[NR][4];
-  auto q_part = [&](int r, int c) {            // operand B: components 16 (q + 4 (c / 2)) + 8 (c % 2) .. + 7
-    return *reinterpret_cast<const uint4*>(qs + (8 * r + g) * kQStride + 32 * (q + 4 * (c >> 1)) + 16 * (c & 1));
+  auto q_part = [&](int turn, int r, int c) {  // operand B: components 16 (q + 4 (c / 2)) + 8 (c % 2) .. + 7
+    return *reinterpret_cast<const uint4*>(q_at(turn, 8 * r + g) + 32 * (q + 4 * (c >> 1)) + 16 * (c & 1));
   };
   float o[2][NR][4];
   int seen_from = 0, seen_to = 0;    // tokens that all rows see
@@ -637,7 +635,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
 #pragma unroll
       for (int k = 0; k < kRowsOf; ++k) {
         const int r = warp + kAttnWarps * k;
-        x[k] = __shfl_sync(kAll, to, r) >= 0 ? *reinterpret_cast<const uint2*>(raw + r * kHeadDim * 2 + 8 * lane) : make_uint2(0, 0);
+        x[k] = __shfl_sync(kAll, to, r) >= 0 ? *reinterpret_cast<const uint2*>(q_at(turn, r) + 8 * lane) : make_uint2(0, 0);
       }
 #pragma unroll
       for (int k = 0; k < kRowsOf; ++k) {
@@ -651,7 +649,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
         const int e = min(max(static_cast<int>(most >> 23), 27), 254);
         const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 + 127 - e) << 23);
         const __half2 lo = __floats2half2_rn(f[0] * up, f[1] * up), hi = __floats2half2_rn(f[2] * up, f[3] * up);
-        *reinterpret_cast<uint2*>(qs + r * kQStride + 8 * lane) =
+        *reinterpret_cast<uint2*>(q_at(turn, r) + 8 * lane) =
             make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
         if (lane == 0) factors[r] = a.scale * __uint_as_float(static_cast<uint32_t>(e - 14) << 23) * (kCap ? 1.0f : kLog2e);
       }
@@ -659,7 +657,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) qb[r][c] = q_part(r, c);
+        for (int c = 0; c < 4; ++c) qb[r][c] = q_part(turn, r, c);
       }
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
@@ -667,13 +665,6 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[0][r][c] = o[1][r][c] = 0.0f;
       }
-    }
-
-    if (i + kTileBlocks >= n && !piece.final) {
-      __syncwarp();
-      const Piece& behind = pieces[(get + 1) % kPieces];
-      to_next = place(behind.seg, behind.fresh, token_next);
-      bring_q(behind.b, to_next);
     }
 
     ok = ok && mbar_wait(smem_u32(&full[tile % kTilesAhead]), tile / kTilesAhead & 1, ctx, 91);
@@ -881,6 +872,13 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
           o[1][r][k] *= (k & 1) ? keep.y : keep.x;
         }
       }
+    }
+    // (the tile before this one is done with its weights)
+    if (i + kTileBlocks >= n && !piece.final) {
+      __syncwarp();
+      const Piece& behind = pieces[(get + 1) % kPieces];
+      to_next = place(behind.seg, behind.fresh, token_next);
+      bring_q(behind.b, to_next, turn ^ 1);
     }
     fence_proxy_async_smem();
     send(tile);
