@@ -521,7 +521,7 @@ qlin_status_t qlin_adjust_logits_f32(const float *logits, int64_t M, int64_t V,
  *   block_table   int32 [B, max_pages]; max_pages >= 1, max_pages * page_size
  *                 <= 2^30.  Entries outside [0, pages) hold no tokens: what is
  *                 written there is dropped, what is read there is 0 and is not
- *                 attended to.  Entries past a sequence's length are not read.
+ *                 attended to.  Entries past a sequence's length are not used.
  *   total_len     int32 [B]  tokens of each sequence with its new ones; taken
  *                 as the nearer end where outside [0, max_pages * page_size]
  *   new_len       int32 [B] or NULL (T of each): new tokens, the last ones of

@@ -29,7 +29,7 @@
 // decided again where one code was near a half-integer it took 98.6.  Warps that
 // stay and take rows in turn took 42 to 46 us, two or three groups ahead 46 to 48;
 // 16 warps an SM 46, 24 with spilled registers 46 to 49.  Short calls are a chain
-// of loads (length, angles or page, the head) and take 3.75 us, 1.6 of them above
+// of loads (length, angles or page, the head) and take 3.6 us, 1.5 of them above
 // an empty launch.
 #include <algorithm>
 #include <type_traits>
@@ -42,7 +42,7 @@ namespace {
 
 // Warps have nothing to do with one another, and small blocks start and end by
 // themselves: writes in blocks of one warp (12 x 8 rows 4.2 us, 4.6 in blocks of two or
-// four; 8192 rows 39.7, 40.3, 40.5), reads of two (515 tokens 2.85 us, 3.1 in four;
+// four; 8192 rows 39.7, 40.3, 40.5), reads of two (515 tokens 2.5 us, 2.8 in four;
 // 12 x 8192 in blocks of one 93.1, of two 90.6).
 constexpr int kReadWarps = 2;
 constexpr int64_t kWritesAtOnce = 20;     // blocks of a write on an SM, which is what 96 registers allow
@@ -220,22 +220,20 @@ __device__ __forceinline__ Pair exact_component(const KvWriteArgs& a, uint32_t r
   return e < 8 ? exact_turn(u0, c, u1, -s) : exact_turn(u1, c, u0, s);
 }
 
-// A unit of a warp is `per` groups of four heads of a row, of the row's `chunks`
-// such.  Query, key and value heads are grouped among themselves.
+// A unit of a warp is `per` groups of four heads of row x, the y-th such.  Query,
+// key and value heads are grouped among themselves.
 struct Split {
-  uint32_t per, chunks, q_groups, kv_groups;
+  uint32_t per, q_groups, kv_groups;
 };
 
 __global__ void __launch_bounds__(32, kWritesAtOnce) kv_write_kernel(const __grid_constant__ KvWriteArgs a, const Split split) {
   const int lane = threadIdx.x;
-  const uint32_t unit = blockIdx.x;
+  const uint32_t row = blockIdx.x;
   grid_dep_launch();
   grid_dep_wait();
-  const uint32_t row = unit / split.chunks;
-  if (row >= a.c.B * a.T) return;
   const int q_heads = static_cast<int>(a.q_heads), kv_heads = static_cast<int>(a.c.kv_heads);
   const int q_groups = split.q_groups, k_end = q_groups + split.kv_groups, groups = k_end + split.kv_groups;
-  const int first = static_cast<int>((unit - row * split.chunks) * split.per);
+  const int first = static_cast<int>(blockIdx.y * split.per);
   const int last = min(first + static_cast<int>(split.per), groups);
   const Place place(static_cast<int>(a.R), lane);
 
@@ -255,7 +253,7 @@ __global__ void __launch_bounds__(32, kWritesAtOnce) kv_write_kernel(const __gri
   };
 
   enter(first);                   // (of rows of padding too: they are in the buffer)
-  const uint32_t b = row / static_cast<uint32_t>(a.T);
+  const uint32_t b = a.T == 1 ? row : row / static_cast<uint32_t>(a.T);
   const int t = static_cast<int>(row - b * static_cast<uint32_t>(a.T));
   const SeqLen seq = seq_len(a.c, b, a.T);
   if (t >= seq.fresh) return;
@@ -443,22 +441,37 @@ __global__ void __launch_bounds__(32, kWritesAtOnce) kv_write_kernel(const __gri
 
 // A warp takes one block of 16 tokens of a head: 4 vectors of codes a lane and
 // tensor, all in flight at once.
-__global__ void __launch_bounds__(32 * kReadWarps) kv_read_kernel(const CacheArgs c, const int32_t* start, int64_t L, int spans,
+__global__ void __launch_bounds__(32 * kReadWarps) kv_read_kernel(const CacheArgs c, const int32_t* start, int64_t L, uint32_t spans,
                                                            uint16_t* k, uint16_t* v) {
   const int lane = threadIdx.x & 31;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kReadWarps + (threadIdx.x >> 5);
+  const uint32_t unit = blockIdx.x * kReadWarps + (threadIdx.x >> 5);
   grid_dep_launch();
   grid_dep_wait();
-  const int kv_heads = static_cast<int>(c.kv_heads);
-  const int64_t span = unit / kv_heads;
+  const uint32_t kv_heads = static_cast<uint32_t>(c.kv_heads);
+  const uint32_t span = unit / kv_heads;
   const int h = static_cast<int>(unit - span * kv_heads);
-  const int64_t b = span / spans;
+  const uint32_t b = span / spans;
   if (b >= c.B) return;
-  const int len = seq_len(c, b, 1).len;
-  const int first = start == nullptr ? 0 : min(max(__ldg(start + b), 0), len);
-  const int n = first / 16 + static_cast<int>(span - b * spans);
-  const int tok0 = 16 * n;
-  const uint8_t* const block = tok0 < len ? cache_block(c, b, h, n) : nullptr;
+  // Lengths, starts and, where no start shifts it, the page are on their way together
+  // (an entry past the sequence's length is not used).
+  const int total = __ldcg(c.total_len + b), from = start == nullptr ? 0 : __ldg(start + b);
+  const int per_page = static_cast<int>(c.page_size) >> 4;
+  const int32_t* const table = c.block_table + b * c.max_pages;
+  int n = static_cast<int>(span - b * spans);
+  int of_table = per_page == 1 ? n : n / per_page;
+  int page = start == nullptr && of_table < c.max_pages ? __ldg(table + of_table) : -1;
+  const int len = seq_of(c, 1, total, 0).len;
+  const int first = min(max(from, 0), len);
+  if (start != nullptr) {
+    n += first >> 4;
+    of_table = per_page == 1 ? n : n / per_page;
+    if (16LL * n < len) page = __ldg(table + of_table);
+  }
+  const int64_t tok0 = 16LL * n;
+  const uint8_t* const block =
+      tok0 < len && page >= 0 && page < c.pages
+          ? c.cache + ((static_cast<int64_t>(page) * kv_heads + h) * per_page + (n - of_table * per_page)) * kCacheBlock
+          : nullptr;
   const int chunk = lane & 7;
   uint4 code[2][4];
   float scale[2][4];
@@ -482,7 +495,7 @@ __global__ void __launch_bounds__(32 * kReadWarps) kv_read_kernel(const CacheArg
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int r = 4 * j + (lane >> 3);
-      const int64_t at = static_cast<int64_t>(tok0) + r - first;
+      const int64_t at = tok0 + r - first;
       if (at < 0 || at >= L) continue;
       const bool there = block != nullptr && tok0 + r < len;
       const uint32_t words[4] = {code[w][j].x, code[w][j].y, code[w][j].z, code[w][j].w};
@@ -516,10 +529,8 @@ cudaError_t launch_kv_write(const KvWriteArgs& a, int sm_count, cudaStream_t str
   const int64_t parts = std::min(std::max<int64_t>(kWritesAtOnce * sm_count / rows, 1), groups);
   const int64_t per = (groups + parts - 1) / parts;
   const int64_t chunks = (groups + per - 1) / per;
-  const int64_t blocks = rows * chunks;
-  if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;   // (of more than 5 * 10^11 bytes)
-  const Split split{static_cast<uint32_t>(per), static_cast<uint32_t>(chunks), static_cast<uint32_t>(q_groups), static_cast<uint32_t>(kv_groups)};
-  return launch_pdl(kv_write_kernel, dim3(static_cast<unsigned>(blocks)), dim3(32), 0, stream, a, split);
+  const Split split{static_cast<uint32_t>(per), static_cast<uint32_t>(q_groups), static_cast<uint32_t>(kv_groups)};
+  return launch_pdl(kv_write_kernel, dim3(static_cast<unsigned>(rows), static_cast<unsigned>(chunks)), dim3(32), 0, stream, a, split);
 }
 
 cudaError_t launch_kv_read(const CacheArgs& c, const int32_t* start, int64_t L, uint16_t* k, uint16_t* v,
@@ -529,7 +540,7 @@ cudaError_t launch_kv_read(const CacheArgs& c, const int32_t* start, int64_t L, 
   if (c.B > 0x7FFFFFFFLL / (spans * c.kv_heads)) return cudaErrorInvalidConfiguration;    // (outputs of 2^43 bytes)
   const int64_t blocks = (c.B * spans * c.kv_heads + kReadWarps - 1) / kReadWarps;
   return launch_pdl(kv_read_kernel, dim3(static_cast<unsigned>(blocks)), dim3(32 * kReadWarps), 0, stream, c, start, L,
-                    static_cast<int>(spans), k, v);
+                    static_cast<uint32_t>(spans), k, v);
 }
 
 }  // namespace qlin

@@ -39,7 +39,7 @@ __device__ __forceinline__ SeqLen seq_len(const CacheArgs& c, int64_t b, int64_t
 // nullptr where its page is none.
 __device__ __forceinline__ uint8_t* cache_block(const CacheArgs& c, int64_t b, int h, int n) {
   const int per_page = static_cast<int>(c.page_size) >> 4;
-  const int in_table = n / per_page;
+  const int in_table = per_page == 1 ? n : n / per_page;
   const int page = __ldg(c.block_table + b * c.max_pages + in_table);
   if (page < 0 || page >= c.pages) return nullptr;
   return c.cache + ((page * c.kv_heads + h) * per_page + (n - in_table * per_page)) * static_cast<int64_t>(kCacheBlock);
