@@ -371,7 +371,7 @@ class Attn:
     (2, 1, 32, 8, 16, [515, 300], {}), (1, 1, 32, 8, 32, [2500], {}), (5, 1, 6, 6, 48, [1, 700, 2, 333, 48], {}),
     # groups of 1 to 16 query heads, odd ones too
     (2, 1, 3, 1, 16, [100, 40], {}), (2, 1, 5, 1, 16, [100, 40], {}), (1, 1, 9, 1, 16, [200], {}), (1, 1, 16, 1, 16, [333], {}),
-    (1, 1, 14, 2, 64, [200], {}),
+    (1, 1, 14, 2, 64, [200], {}), (2, 1, 300, 1, 16, [40, 3], {}), (1, 2, 130, 2, 32, [60], {"window": 20}),
     # drafted blocks: rows of 8 to 128 a key/value head
     (2, 8, 4, 1, 16, [8, 140], {}), (2, 8, 16, 4, 16, [40, 300], {}), (1, 3, 30, 6, 48, [1000], {}), (2, 8, 8, 1, 16, [90, 9], {}),
     (2, 5, 4, 1, 16, [300, 20], {}), (3, 3, 16, 2, 16, [150, 3, 70], {}), (1, 10, 8, 2, 16, [280], {"causal": False}),

@@ -38,10 +38,10 @@
 //
 // Where the time goes (two thread blocks an SM): with 32 rows a tile of 128 tokens
 // takes one of them 4600 cycles, 1300 for scores, 700 weights, 300 the barrier, 700
-// the copies' issue, 1200 outputs; the tensor pipe is 45% busy, and the chain through a
-// tile bounds it (12 x 8 tokens at 8192: 57.9 us, 2.8 TB/s; 8 rows less take 7 us less).
-// With 8 rows a tile takes 2200 to 3000 and the copies keep up (96 x 1 at 4096:
-// 104.6 us, 6.0 TB/s; 1 x 131072: 47.5 us, 5.8 TB/s).  Beginning a share takes 4 us
+// the copies' issue, 1200 outputs; the tensor pipe is 37% busy over the call, and the
+// chain through a tile bounds it (12 x 8 tokens at 8192: 57.8 us, 2.8 TB/s; of 6 50.9, of
+// 4 40.7).  With 8 rows a tile takes 2200 to 3000 and the copies keep up (96 x 1 at
+// 4096: 104.2 us, 6.0 TB/s; 1 x 131072: 47.3 us, 5.9 TB/s).  Beginning a share takes 4 us
 // (lengths, the plan, a page, the first blocks: loads one behind the other), ending a
 // piece 0.4: what short calls are made of (1 x 515: 6.4 us).
 //
@@ -499,9 +499,9 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
                      : "memory");
     }
   };
-  // ---- copies: this warp's block of each tile, one bulk copy (whose issue takes
-  // its thread 200 cycles), into the ring as soon as the block that it displaces is
-  // of a tile that is done.  The next page is read when the one before is sent.
+  // ---- copies: this warp's blocks of each tile, one bulk copy each (whose issue
+  // takes its thread 200 cycles), into the ring as soon as the tile that they displace
+  // is done.  The pages of 32 tiles are read at once, lane by tile.
   Walk& ahead = aheads[warp];
   const int per_page = static_cast<int>(a.c.page_size) >> 4;
   const int page_blocks = per_page * static_cast<int>(a.c.kv_heads);
