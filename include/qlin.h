@@ -613,8 +613,8 @@ qlin_status_t qlin_kv_read_bf16(const void *cache, int64_t pages, int64_t page_s
  * small are off by up to 2^-107 each).  Cache bytes at places that no row sees have
  * no effect, whatever they hold.  Non-finite scales at seen tokens give
  * non-finite outputs for the rows that see them.  The result does not depend
- * on timing, but in its last bits on the batch, which decides how sequences
- * are cut.
+ * on timing, but in its last bits on the batch and max_pages, which decide how
+ * sequences are cut.
  *
  *   q        bf16 [B T, q_heads * 128]  (rotated, qlin_kv_write_i8)
  *   q_heads  a positive multiple of kv_heads, at most 65535

@@ -482,6 +482,9 @@ def test_attention_however_the_work_is_shared_out(gpu, seed, B, T, Hq, Hkv, long
     for total in (np.full(B, longest // 3), rng.integers(0, longest + 1, B), np.where(np.arange(B) == B // 2, longest, 20)):
         a = Attn(110 + seed, B, T, Hq, Hkv, 16, -(-longest // 16), total, window=int(rng.integers(0, 2)) * 333)
         a.check(a.run())
+        # tables with room for much longer sequences
+        a.table = np.concatenate([a.table, np.full((B, 16000), -1, np.int32)], 1)
+        a.check(a.run())
 
 
 @needs_gpu

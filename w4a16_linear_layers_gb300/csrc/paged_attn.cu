@@ -85,18 +85,15 @@ constexpr float kMostWeight = 15.0f;
 constexpr float kLiftWeight = 4.0f;
 constexpr float kNewWeight = 0.0f;
 
-template <int NR>
+template <int NR, int kPerSm>
 struct Shape {
   static constexpr int kRows = 8 * NR;
   static constexpr int kRowsOf = kRows / kAttnWarps;    // whose q a warp brings
-  // Blocks in the ring: whole tiles, as many as two thread blocks an SM have room
+  // Blocks in the ring: whole tiles, as many as the thread blocks of an SM have room
   // for.  A tile's blocks are sent when the one two (three) before is done, which with
   // few rows, whose tiles are short, is late in a ring of two tiles (96 x 1 at 4096 134 us,
-  // 104 in three; 12 x 4 at 8192 44.4 and 40.7).  Three thread
-  // blocks of two tiles each would take short contexts (96 x 1 at 512 24.6 us for 27.5)
-  // further than long ones back (12 x 1 at 8192 35.6 for 34.3, 1 x 8192 10.4 for 8.9), but
-  // lengths are not known where a grid is chosen.
-  static constexpr int kSlots = NR <= 2 ? 24 : 16;
+  // 104 in three; 12 x 4 at 8192 44.4 and 40.7).
+  static constexpr int kSlots = kPerSm == 2 && NR <= 2 ? 24 : 16;
   static_assert(kSlots % kTileBlocks == 0, "whole tiles");
   // shared memory, in order
   // weights of two tiles; and, where a piece begins, its q, in the place of its first tile's
@@ -351,9 +348,9 @@ __device__ __forceinline__ float log2_above(float v) {
   return static_cast<float>(max(static_cast<int>(__float_as_uint(v) >> 23 & 255u) - 126, -90));
 }
 
-template <int NR, bool kCap>
-__global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams p) {
-  using S = Shape<NR>;
+template <int NR, bool kCap, int kPerSm>
+__global__ void __launch_bounds__(kAttnThreads, kPerSm) attn_kernel(const AttnParams p) {
+  using S = Shape<NR, kPerSm>;
   constexpr int kSlots = S::kSlots, kRowsOf = S::kRowsOf;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kTilesAhead];    // a tile's blocks are there
@@ -1055,20 +1052,36 @@ int row_groups(int64_t rows) {
   return static_cast<int>(((rows + tiles - 1) / tiles + 7) / 8);
 }
 
-template <int NR, bool kCap>
+// Whether three thread blocks an SM, with rings of two tiles, do better with 8 rows than
+// two with rings of three: where pieces are short, so that their beginnings and ends
+// overlap, as far as the host can tell from what tables have room for and the window.
+// `blocks` a segment and `share` a thread block (of two an SM), us with three and two:
+//   32 and 81 (96 x 1 at 512) 24.8 and 27.7;  63 and 159 (96 x 1 at 1000) 36.9 and 39.0;
+//   13 and 87 (256 x 1 at 200) 33.6 and 39.6;  129 and 41 (12 x 1 in a window of 2048)
+//   14.5 and 15.2;  63 and 10 (6 x 1 at 1000) 7.4 and 10.0;  250 and 53 (8 x 1 at 4000)
+//   15.2 and 15.6;  125 and 316 (96 x 1 at 2000) 59.9 and 59.5;  512 and 162 (12 x 1 at 8192)
+//   35.6 and 34.2.
+// Few segments are joined from fewer parts (1 x 8192 10.4 and 8.9).
+bool short_contexts(int64_t segments, int64_t blocks, int64_t grid) {
+  if (few_segments(segments, grid) || blocks >= 400) return false;
+  const int64_t share = segments < grid * 400 ? segments * blocks / grid : 400;
+  return blocks + 2 * share < 400;
+}
+
+template <int NR, bool kCap, int kPerSm>
 cudaError_t launch_groups(const AttnParams& p, int grid, cudaStream_t stream) {
-  const auto kernel = attn_kernel<NR, kCap>;
+  const auto kernel = attn_kernel<NR, kCap, kPerSm>;
   static std::atomic<uint64_t> ready{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(ready.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<NR>::kBytes);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<NR, kPerSm>::kBytes);
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_release);
   }
-  e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kAttnThreads), Shape<NR>::kBytes, stream, p);
+  e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kAttnThreads), Shape<NR, kPerSm>::kBytes, stream, p);
   if (e != cudaSuccess) return e;
   const int64_t rows = p.a.T * p.G, segments = p.a.c.B * p.row_tiles * p.a.c.kv_heads;
   if (p.planned && few_segments(segments, grid))
@@ -1077,17 +1090,18 @@ cudaError_t launch_groups(const AttnParams& p, int grid, cudaStream_t stream) {
   return launch_pdl(join_cuts_kernel, dim3(static_cast<unsigned>(grid - 1)), dim3(256), 0, stream, p, 8 * NR);
 }
 
-template <int NR>
+template <int NR, int kPerSm>
 cudaError_t launch_cap(const AttnParams& p, int grid, cudaStream_t stream) {
   // (a cap past 2^100 changes no score that fp32 can tell from its neighbour, and would overflow)
-  return p.a.softcap > 0.0f && p.a.softcap < 0x1p100f ? launch_groups<NR, true>(p, grid, stream) : launch_groups<NR, false>(p, grid, stream);
+  return p.a.softcap > 0.0f && p.a.softcap < 0x1p100f ? launch_groups<NR, true, kPerSm>(p, grid, stream)
+                                                         : launch_groups<NR, false, kPerSm>(p, grid, stream);
 }
 
 }  // namespace
 
 size_t paged_attn_workspace_bytes(int64_t, int64_t T, int64_t q_heads, int64_t kv_heads, int sm_count) {
   const int groups = row_groups(T * (q_heads / kv_heads));
-  const size_t grid = 2 * static_cast<size_t>(sm_count);
+  const size_t grid = (groups == 1 ? 3 : 2) * static_cast<size_t>(sm_count);
   return grid * 16 + 2 * grid * 8 * groups * (sizeof(Share) + kHeadDim * sizeof(float));
 }
 
@@ -1103,8 +1117,9 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, int* err, int sm_count, cu
   p.a.window = std::min<int64_t>(a.window, 1LL << 40);      // (further than any token)
   p.cap = a.softcap * kLog2e;
   p.per_cap = std::min(1.0f / a.softcap, FLT_MAX);
-  const int grid = 2 * sm_count;
   const int64_t segments = a.c.B * tiles * a.c.kv_heads, longest = a.c.max_pages * (a.c.page_size / 16);
+  const bool three = groups == 1 && short_contexts(segments, std::min(longest, p.a.window > 0 ? (p.a.window + a.T) / 16 + 2 : longest), 2 * sm_count);
+  const int grid = (three ? 3 : 2) * sm_count;
   p.planned = a.c.B <= 32 && segments <= ((1LL << 31) - 1 - 2 * kTile * grid) / longest;
   p.each = static_cast<int>(grid / segments);
   p.per_grid = ((1ULL << 40) + grid - 1) / grid;
@@ -1117,10 +1132,10 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, int* err, int sm_count, cu
   p.part_o = reinterpret_cast<float*>(ws + static_cast<size_t>(grid) * 16);
   p.part_share = reinterpret_cast<Share*>(p.part_o + 2 * static_cast<size_t>(grid) * 8 * groups * kHeadDim);
   switch (groups) {
-    case 1: return launch_cap<1>(p, grid, stream);
-    case 2: return launch_cap<2>(p, grid, stream);
-    case 3: return launch_cap<3>(p, grid, stream);
-    default: return launch_cap<4>(p, grid, stream);
+    case 1: return three ? launch_cap<1, 3>(p, grid, stream) : launch_cap<1, 2>(p, grid, stream);
+    case 2: return launch_cap<2, 2>(p, grid, stream);
+    case 3: return launch_cap<3, 2>(p, grid, stream);
+    default: return launch_cap<4, 2>(p, grid, stream);
   }
 }
 
