@@ -129,7 +129,7 @@ struct AttnParams {
   float cap, per_cap;  // of scores times log2(e); 1 / softcap
   int* err;
   // workspace: where the cut segments are, then their parts
-  int32_t* cuts;       // [grid][4]: segment, its first and last share, sequence; segment -1: none
+  int32_t* cuts;       // [grid][8]: segment (-1: none), its first and last share, sequence and its new tokens
   Share* part_share;   // [2 grid][rows]
   float* part_o;       // [2 grid][rows][128]
 };
@@ -398,7 +398,10 @@ __global__ void __launch_bounds__(kAttnThreads, kPerSm) attn_kernel(const AttnPa
         if (piece_at > 0 && piece_at <= plan.share) cut = make_int4(seg, c - 1, few_times(from - piece_at + of - 1, plan.share), b);
       }
     }
-    if (tid == 0) *reinterpret_cast<int4*>(p.cuts + 4 * c) = cut;
+    if (tid == 0) {
+      *reinterpret_cast<int4*>(p.cuts + 8 * c) = cut;
+      p.cuts[8 * c + 4] = walk.seq.fresh;
+    }
     if (!mine) return;
   } else {
     // Blocks of 16 of 256 sequences at a time: their running sum, which places
@@ -439,7 +442,7 @@ __global__ void __launch_bounds__(kAttnThreads, kPerSm) attn_kernel(const AttnPa
     const int64_t share = share_of(p, total, gridDim.x);
     const int64_t at = blockIdx.x * share;
     if (at >= total) {
-      if (tid == 0) p.cuts[4 * blockIdx.x] = -1;
+      if (tid == 0) p.cuts[8 * blockIdx.x] = -1;
       return;
     }
     for (int64_t b0 = 0, before = 0;; b0 += kAttnThreads) {
@@ -457,7 +460,8 @@ __global__ void __launch_bounds__(kAttnThreads, kPerSm) attn_kernel(const AttnPa
         // the first boundary inside a segment announces it
         const int64_t s0 = from + static_cast<int64_t>(start.seg) * n0;
         const int first = share_at(s0, share), last = share_at(s0 + n0 - 1, share);
-        *reinterpret_cast<int4*>(p.cuts + 4 * blockIdx.x) =
+        p.cuts[8 * blockIdx.x + 4] = seq.fresh;
+        *reinterpret_cast<int4*>(p.cuts + 8 * blockIdx.x) =
             make_int4(start.off > 0 && first == static_cast<int>(blockIdx.x) - 1 ? start.seg : -1, first, last, static_cast<int>(start.b));
       }
       before += all;
@@ -997,21 +1001,20 @@ struct Joined {
   }
 };
 
-// The parts of the cut segment that share x announces: a warp takes a row at a time.
+// The parts of the cut segment that share x + 1 announces, a warp a row: rows 8 y to
+// 8 y + 7.
 __global__ void __launch_bounds__(256) join_cuts_kernel(const AttnParams p, int tile_rows) {
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, in_tile = 8 * blockIdx.y + (threadIdx.x >> 5);
   grid_dep_wait();
   grid_dep_launch();
-  const int4 cut = __ldcg(reinterpret_cast<const int4*>(p.cuts + 4 * (blockIdx.x + 1)));
+  const int4 cut = __ldcg(reinterpret_cast<const int4*>(p.cuts + 8 * (blockIdx.x + 1)));
+  const int fresh = __ldcg(p.cuts + 8 * (blockIdx.x + 1) + 4);
   if (cut.x < 0) return;
-  const int fresh = seq_len(p.a.c, cut.w, p.a.T).fresh;
-  for (int in_tile = threadIdx.x >> 5; in_tile < tile_rows; in_tile += 8) {
-    const int row = cut.x % p.row_tiles * tile_rows + in_tile, t = row / p.G;
-    if (row >= static_cast<int>(p.a.T) * p.G || t >= fresh) return;
-    Joined j;
-    j.add_parts(p, cut.y, cut.z - cut.y + 1, 0, 1, tile_rows, in_tile, lane);
-    j.store(p, cut.w, cut.x, row, t, lane);
-  }
+  const int row = cut.x % p.row_tiles * tile_rows + in_tile, t = row / p.G;
+  if (row >= static_cast<int>(p.a.T) * p.G || t >= fresh) return;
+  Joined j;
+  j.add_parts(p, cut.y, cut.z - cut.y + 1, 0, 1, tile_rows, in_tile, lane);
+  j.store(p, cut.w, cut.x, row, t, lane);
 }
 
 // The same where there are few segments, of eight parts and more: a block takes
@@ -1087,7 +1090,7 @@ cudaError_t launch_groups(const AttnParams& p, int grid, cudaStream_t stream) {
   if (p.planned && few_segments(segments, grid))
     return launch_pdl(join_segments_kernel, dim3(static_cast<unsigned>(segments), static_cast<unsigned>(rows < 8 * NR ? rows : 8 * NR)),
                       dim3(32 * kJoinWarps), 0, stream, p, 8 * NR, grid);
-  return launch_pdl(join_cuts_kernel, dim3(static_cast<unsigned>(grid - 1)), dim3(256), 0, stream, p, 8 * NR);
+  return launch_pdl(join_cuts_kernel, dim3(static_cast<unsigned>(grid - 1), NR), dim3(256), 0, stream, p, 8 * NR);
 }
 
 template <int NR, int kPerSm>
@@ -1102,7 +1105,7 @@ cudaError_t launch_cap(const AttnParams& p, int grid, cudaStream_t stream) {
 size_t paged_attn_workspace_bytes(int64_t, int64_t T, int64_t q_heads, int64_t kv_heads, int sm_count) {
   const int groups = row_groups(T * (q_heads / kv_heads));
   const size_t grid = (groups == 1 ? 3 : 2) * static_cast<size_t>(sm_count);
-  return grid * 16 + 2 * grid * 8 * groups * (sizeof(Share) + kHeadDim * sizeof(float));
+  return grid * 32 + 2 * grid * 8 * groups * (sizeof(Share) + kHeadDim * sizeof(float));
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, int* err, int sm_count, cudaStream_t stream) {
@@ -1129,7 +1132,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, int* err, int sm_count, cu
   p.per_page = ((1ULL << 38) + in_page - 1) / in_page;      // (2^12 blocks at most, of 2^26)
   uint8_t* const ws = static_cast<uint8_t*>(a.workspace);
   p.cuts = reinterpret_cast<int32_t*>(ws);
-  p.part_o = reinterpret_cast<float*>(ws + static_cast<size_t>(grid) * 16);
+  p.part_o = reinterpret_cast<float*>(ws + static_cast<size_t>(grid) * 32);
   p.part_share = reinterpret_cast<Share*>(p.part_o + 2 * static_cast<size_t>(grid) * 8 * groups * kHeadDim);
   switch (groups) {
     case 1: return three ? launch_cap<1, 3>(p, grid, stream) : launch_cap<1, 2>(p, grid, stream);
