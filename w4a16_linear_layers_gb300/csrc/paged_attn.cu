@@ -179,8 +179,8 @@ __host__ __device__ inline bool few_segments(int64_t segments, int64_t grid) { r
 // ceil(n_s / share) of a segment of n_s blocks, are no more than the thread blocks.
 // That is done where it is at most kPieceBlocks over the even one (12 x 8 rows in a
 // window of 2048, 2 over 41: 28.3 us, 30.8 with even shares; of 1000 tokens 21.0 and
-// 23.2; at 8192, 15 over 126, 58.1 and 58.0), and where segments are few (then it is less than grid / (grid - segments) times the even
-// one, and the parts are joined by segment).
+// 23.2; at 8192, 15 over 126, 58.1 and 58.0), and where segments are few (then it is
+// less than grid / (grid - segments) times the even one).
 constexpr int kPieceBlocks = 5;
 struct Plan {
   SeqLen seq;              // the lane's
@@ -1087,8 +1087,13 @@ cudaError_t launch_groups(const AttnParams& p, int grid, cudaStream_t stream) {
   e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kAttnThreads), Shape<NR, kPerSm>::kBytes, stream, p);
   if (e != cudaSuccess) return e;
   const int64_t rows = p.a.T * p.G, segments = p.a.c.B * p.row_tiles * p.a.c.kv_heads;
-  if (p.planned && few_segments(segments, grid))
-    return launch_pdl(join_segments_kernel, dim3(static_cast<unsigned>(segments), static_cast<unsigned>(rows < 8 * NR ? rows : 8 * NR)),
+  // Segments of many parts are joined by a block for each of their rows, until those
+  // are more than run at once beside what is left of the attention (us so and by cuts:
+  // 1 x 8192 8.8 and 15.0, 8 x 8192 13.3 and 20.5, 5 x 3 at 1000, 450 blocks, 8.65 and 9.25;
+  // 4 x 4 at 1000, 512 blocks, 10.1 and 9.3, 4 x 8, 1024 blocks, 13.5 and 11.6).
+  const int64_t in_tile = std::min<int64_t>(rows, 8 * NR);
+  if (p.planned && few_segments(segments, grid) && segments * in_tile <= 480)
+    return launch_pdl(join_segments_kernel, dim3(static_cast<unsigned>(segments), static_cast<unsigned>(in_tile)),
                       dim3(32 * kJoinWarps), 0, stream, p, 8 * NR, grid);
   return launch_pdl(join_cuts_kernel, dim3(static_cast<unsigned>(grid - 1), NR), dim3(256), 0, stream, p, 8 * NR);
 }
