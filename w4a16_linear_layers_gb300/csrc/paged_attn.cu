@@ -39,9 +39,9 @@
 // Where the time goes (two thread blocks an SM): with 32 rows a tile of 128 tokens
 // takes one of them 4600 cycles, 1300 for scores, 700 weights, 300 the barrier, 700
 // the copies' issue, 1200 outputs; the tensor pipe is 37% busy over the call, and the
-// chain through a tile bounds it (12 x 8 tokens at 8192: 57.8 us, 2.8 TB/s; of 6 50.9, of
-// 4 40.7).  With 8 rows a tile takes 2200 to 3000 and the copies keep up (96 x 1 at
-// 4096: 104.2 us, 6.0 TB/s; 1 x 131072: 47.3 us, 5.9 TB/s).  Beginning a share takes 4 us
+// chain through a tile bounds it (12 x 8 tokens at 8192: 54.0 us, 3.0 TB/s; of 4 39.0).
+// With 8 rows a tile takes 2200 to 3000 and the copies keep up (96 x 1 at 4096: 103.7 us, 6.0 TB/s;
+// 1 x 131072: 47.3 us, 5.9 TB/s).  Beginning a share takes 4 us
 // (lengths, the plan, a page, the first blocks: loads one behind the other), ending a
 // piece 0.4: what short calls are made of (1 x 515: 6.4 us).
 //
@@ -178,8 +178,8 @@ __host__ __device__ inline bool few_segments(int64_t segments, int64_t grid) { r
 // than the others.  Then the share is the smallest for which the parts,
 // ceil(n_s / share) of a segment of n_s blocks, are no more than the thread blocks.
 // That is done where it is at most kPieceBlocks over the even one (12 x 8 rows in a
-// window of 2048, 2 over 41: 28.3 us, 30.8 with even shares; of 1000 tokens 21.0 and
-// 23.2; at 8192, 15 over 126, 58.1 and 58.0), and where segments are few (then it is
+// window of 2048, 2 over 41: 24.5 us, 27.0 with even shares; of 1000 tokens 17.4 and
+// 19.2; at 8192, 15 over 126, 54.2 and 53.9), and where segments are few (then it is
 // less than grid / (grid - segments) times the even one).
 constexpr int kPieceBlocks = 5;
 struct Plan {
