@@ -609,9 +609,10 @@ qlin_status_t qlin_kv_read_bf16(const void *cache, int64_t pages, int64_t page_s
  * |i - j| < window where window > 0.  A row that sees none gives zeros.
  *
  * fp32 accumulation; each exp(x_j) times its V scale is rounded to fp16
- * relative to the row's largest (V scales below 2^-90 to that: values that
- * small are off by up to 2^-107 each).  Cache bytes at places that no row sees have
- * no effect, whatever they hold.  Non-finite scales at seen tokens give
+ * relative to the row's largest such product.  V scales may have any size
+ * (values under scales below 2^-100 are off by up to 2^-142 each); an exp(x_j)
+ * below 2^-126 of the row's largest may count as 0.  Cache bytes at places that
+ * no row sees have no effect, whatever they hold.  Non-finite scales at seen tokens give
  * non-finite outputs for the rows that see them.  The result does not depend
  * on timing, but in its last bits on the batch and max_pages, which decide how
  * sequences are cut.

@@ -1,0 +1,130 @@
+"""The operators around the paged cache at the ends of their contract: value
+scales over fp32's whole range.
+
+The attention's tolerance is that of tests/test_paged_cache.py, all of whose terms
+hold here (n: the tokens of a row; a weight below fp16's normal range is at most a
+step of 2^-24 off where the row's largest is 1 or more), and, for values near
+fp32's end, half a step of a subnormal bf16, 2^-134, besides."""
+import numpy as np
+import pytest
+import torch
+
+import paged_ref as ref
+from helpers import from_dev_bits, to_dev, to_dev_bits
+from test_paged_cache import Attn, Batch, D, gpu, needs_gpu, tolerance  # noqa: F401
+from w4a16_linear_layers_gb300 import qlin
+
+PAGE = 64
+
+
+def one_head(x, vcodes, vs):
+    """A cache of one head and consecutive pages, whose token j has the score x[j] under
+    first() (exactly: its key's first code is 64, its scale x / 64) and codes and scale of
+    its value."""
+    n = len(x)
+    pages = -(-n // PAGE)
+    kcodes = np.full((pages * PAGE, D), 128, np.uint8)
+    kcodes[:n, 0] = 128 + 64
+    codes = np.full((pages * PAGE, D), 128, np.uint8)
+    codes[:n] = vcodes + 128
+    scales = np.zeros((2, pages * PAGE), np.float32)
+    scales[0, :n], scales[1, :n] = np.asarray(x, np.float32) / 64, vs
+    raw = np.zeros((pages * PAGE // 16, ref.BLOCK), np.uint8)
+    for w, c in enumerate((kcodes, codes)):
+        part = raw[:, 2048 * w:2048 * w + 2048]
+        for r in range(16):
+            part[:, ref.PLACES[r]] = c[r::16]
+        raw[:, 4096 + 64 * w:4160 + 64 * w] = scales[w].reshape(-1, 16).view(np.uint8)
+    return raw.reshape(pages, 1, PAGE // 16, ref.BLOCK)
+
+
+def first(rows=1):
+    """q whose only component, the first, is 1."""
+    q = np.zeros((rows, D))
+    q[:, 0] = 1.0
+    return ref.bf16(q)
+
+
+def expected(x, vcodes, vs):
+    """(out, A, big) of a row that sees all."""
+    x = np.asarray(x, np.float32).astype(np.float64)
+    v = vcodes.astype(np.float64) * np.asarray(vs, np.float32).astype(np.float64)[:, None]
+    p = np.exp(x - x.max())
+    p /= p.sum()
+    return p @ v, p @ np.abs(v), np.abs(v).max()
+
+
+def attend(raw, n, B=1, **kw):
+    """Rows of B sequences that all have the same pages."""
+    table = np.broadcast_to(np.arange(raw.shape[0], dtype=np.int32), (B, raw.shape[0]))
+    out = qlin.paged_attn_i8(to_dev_bits(first(B), torch.bfloat16), to_dev(raw), to_dev(table), to_dev(np.full(B, n, np.int32)),
+                             **{"scale": 1.0, **kw})
+    return ref.bf16_to_f64(from_dev_bits(out))
+
+
+def check_one_head(x, vcodes, vs, B=1):
+    out = attend(one_head(x, vcodes, vs), len(x), B)
+    o64, A, big = expected(x, vcodes, vs)
+    bound = tolerance(o64, A, np.abs(x).max(), big, len(x)) + 2.0 ** -134
+    bad = ~(np.abs(out - o64) <= bound)
+    assert not bad.any(), (np.argwhere(bad)[:4], out[bad][:4], np.broadcast_to(o64, out.shape)[bad][:4])
+
+
+# ------------------------------------------------ value scales of every size
+
+@needs_gpu
+@pytest.mark.parametrize("B", [1, 40, 320])
+@pytest.mark.parametrize("e", [-140, -120, -60, 0, 60, 96, 104, 110, 116, 120])
+def test_value_scales_of_one_size(gpu, e, B):
+    """One token of weight 2^13 among 8191 of weight 1, with the other sign, at the
+    beginning, within and at the end."""
+    rng = np.random.default_rng(e + 200)
+    n = 8192
+    for at in (0, 5000, n - 1):
+        x = np.zeros(n)
+        x[at] = 13 * np.log(2.0)
+        codes = np.full((n, D), -100)
+        codes[at] = 100
+        codes[:, 64:] = rng.integers(-127, 128, (n, 64))
+        check_one_head(x, codes, np.full(n, 2.0 ** e), B)
+
+
+@needs_gpu
+@pytest.mark.parametrize("order", ["random", "rising", "falling"])
+@pytest.mark.parametrize("B", [1, 320])
+def test_value_scales_of_all_sizes(gpu, B, order):
+    """Small values count in the denominator beside large ones, in whatever order they come."""
+    rng = np.random.default_rng(7)
+    for n, low, high in ((3000, -110, 110), (700, -126, 120), (1500, -20, 118), (900, -120, 10), (129, -149, 60)):
+        e = rng.uniform(low, high, n)
+        if order != "random":
+            e = np.sort(e) if order == "rising" else -np.sort(-e)
+        check_one_head(3 * rng.standard_normal(n), rng.integers(-127, 128, (n, D)), 2.0 ** e, B)
+
+
+@needs_gpu
+@pytest.mark.parametrize("B", [1, 320])
+@pytest.mark.parametrize("big", [1.0, 2.0 ** 60, 2.0 ** 120])
+def test_values_of_zero_beside_large_ones(gpu, B, big):
+    """Most tokens have values of zero (a scale of 0): they count in the denominator alone."""
+    rng = np.random.default_rng(8)
+    n = 2000
+    for at in (0, 900, n - 1):
+        vs = np.zeros(n)
+        vs[at] = big
+        check_one_head(rng.standard_normal(n), rng.integers(-127, 128, (n, D)), vs, B)
+
+
+@needs_gpu
+def test_values_written_and_read_by_attention_near_the_largest(gpu):
+    """Heads that the write accepts at 2e37 give scales that the attention takes."""
+    rng = np.random.default_rng(9)
+    T, Hq, Hkv = 40, 4, 2
+    x = rng.standard_normal((T, Hq + 2 * Hkv, D))
+    x[:, Hq + Hkv:] = (x[:, Hq + Hkv:] * 2e37).clip(-3e38, 3e38)
+    batch = Batch(10, 1, T, Hq, Hkv, 16, 3, [T], qkv=ref.bf16(x).reshape(T, -1))
+    q = batch.run()
+    batch.check(q)
+    a = Attn(11, 1, T, Hq, Hkv, 16, 3, [T])
+    a.raw, a.table, a.q = batch.cache.cpu().numpy(), batch.table, from_dev_bits(q)
+    a.check(a.run())

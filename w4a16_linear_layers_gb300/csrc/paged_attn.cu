@@ -4,8 +4,10 @@
 //   x_j = scale ks_j (q . kc_j)  (softcap tanh(x_j / softcap)),
 //   out = sum_j exp(x_j) vs_j vc_j / sum_j exp(x_j),
 // kc, vc the codes and ks, vs their scales, in one pass over the cache: sums of
-// 2^(y_j - m) (vs_j vc_j) and of 2^(y_j - m), y_j = x_j log2(e), under a
-// reference m of each row that follows the largest weight so far.
+// (2^(y_j - m) vs_j 2^-c) vc_j and of 2^(y_j - m), y_j = x_j log2(e), under two
+// references of each row: a score m, which follows the largest so far, and a power of
+// two 2^c, which follows the largest product of weight and value scale, so that this
+// fits fp16 whatever the scales are, and the denominator does not depend on them.
 //
 // What bounds it: HBM, 264 bytes a token and key/value head, which its rows (T
 // new tokens times G query heads of the group) share.
@@ -30,10 +32,10 @@
 // shared memory by eight warps a tile, that was busy 57% of the time (12 x 8 tokens at
 // 8192 65.0 us, four warps 58.8; 96 x 1 at 512 30.0 and 28.3).
 //
-// One barrier a tile: the reference m is raised only where a weight would pass
-// 2^15, and then to put the row's largest at 2^0, so that weights are formed and
-// written as if it held, and the barrier that they need anyway says whether it
-// did.  (With a running maximum exchanged before, two barriers and copies
+// One barrier a tile: references are raised only where a weight, with its scale or
+// without, would pass 2^15, and then to put the row's largest near 2^0, so that weights
+// are formed and written as if they held, and the barrier that they need anyway says
+// whether they did.  (With a running maximum exchanged before, two barriers and copies
 // through one producer warp a tile took twice the time.)
 //
 // Where the time goes (two thread blocks an SM): with 32 rows a tile of 128 tokens
@@ -50,10 +52,10 @@
 // and the rows, mostly 4 to 32, fill a fraction of its tile.
 //
 // Precision.  Codes are exact in fp16, and so is q up to 2^-39 of its row's
-// largest component.  The largest weight of what a row has seen stands between
-// 2^-1 (its logarithm is of a power of two above the value scale) and 2^15, so weights
-// have fp16's 11 bits down to 2^-13 of it, and are at most 2^-24 of it off below
-// that.  Scores, sums and outputs are fp32.
+// largest component.  The largest product of a weight and its value scale that a row
+// has seen stands between 2^-1 and 2^15, so these products have fp16's 11 bits down to
+// 2^-13 of it, and are at most 2^-24 of it off below that.  Scores, weights, sums and
+// outputs are fp32; a weight is 0 below 2^-126 of the row's largest.
 #include <cfloat>
 
 #include <algorithm>
@@ -77,13 +79,14 @@ constexpr int kPStride = 288;       // bytes of a row of weights: rows 32 bytes 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr float kNone = -1e30f;     // reference of a row that has seen nothing
-// Logarithms of the weights that a row's reference may let through, of one that a
-// reference set in passing is lifted at, and of a row's largest where one is set: 15
-// apart, so that few tiles set one (of 27 tiles of 32 rows one in ten; 11 apart one in
-// four, 4 apart one in three).
-constexpr float kMostWeight = 15.0f;
+// Weights times their scales: what a row's references may let through (of the weights
+// by themselves too), the logarithm of what a reference set in passing is lifted at, and
+// of a power of two above the row's largest where one is set: 14 apart, so that few tiles
+// set one (of 27 tiles of 32 rows one in ten; 11 apart one in four, 4 apart one in three).
+constexpr float kMostWeight = 32768.0f;
 constexpr float kLiftWeight = 4.0f;
-constexpr float kNewWeight = 0.0f;
+constexpr float kNewWeight = 1.0f;
+constexpr float kMostScale = 126.0f;      // c is between this and its negative
 
 template <int NR, int kPerSm>
 struct Shape {
@@ -100,8 +103,8 @@ struct Shape {
   static constexpr int kP = kSlots * kCacheBlock;
   static constexpr int kPair = kP + 2 * kRows * kPStride;      // float2 [warps][rows]: references; sums
   static constexpr int kRef = kPair + kAttnWarps * kRows * 8;     // float4 [rows / 2]: two rows' references
-  static constexpr int kKeep = kRef + kRows * 8;         // fp32 [rows]: what a raised reference leaves of the sums
-  static constexpr int kFactor = kKeep + kRows * 4;      // fp32 [rows]
+  static constexpr int kKeep = kRef + kRows * 8;         // float2 [rows]: what raised references leave of the sums, of the outputs
+  static constexpr int kFactor = kKeep + kRows * 8;      // fp32 [rows]
   // of two pieces:
   static constexpr int kTo = kFactor + kRows * 4;        // int32 [rows]: the row's head of the sequence's outputs, -1: none
   static constexpr int kLow = kTo + 2 * kRows * 4;       // int32 [rows]: first token seen
@@ -109,11 +112,9 @@ struct Shape {
   static constexpr int kBytes = kHigh + 2 * kRows * 4;
 };
 
-// A row's reference m + c and the sum under it, of a part of its tokens.
+// A row's references m and 2^c and the sum of weights under m, of a part of its tokens.
 struct alignas(16) Share {
   float m, c, l, none;
-  // its reference over m of others
-  __device__ __forceinline__ float over(float other) const { return (m - other) + c; }
 };
 
 struct AttnParams {
@@ -343,10 +344,15 @@ __device__ __forceinline__ float max_over_g(float v) {
   return fmaxf(v, __shfl_xor_sync(kAll, v, 16));
 }
 
-// log2 of a power of two above |v|; |v| below 2^-90 taken as that
+// log2 of a power of two above |v|, -126 for all smaller ones
 __device__ __forceinline__ float log2_above(float v) {
-  return static_cast<float>(max(static_cast<int>(__float_as_uint(v) >> 23 & 255u) - 126, -90));
+  return static_cast<float>(static_cast<int>(__float_as_uint(v) >> 23 & 255u) - 126);
 }
+
+// 2^c, c whole and between -126 and 127
+__device__ __forceinline__ float power_of_two(float c) { return __uint_as_float(static_cast<uint32_t>(static_cast<int>(c) + 127) << 23); }
+// and c of it
+__device__ __forceinline__ float log2_of(float f) { return static_cast<float>(static_cast<int>(__float_as_uint(f) >> 23) - 127); }
 
 template <int NR, bool kCap, int kPerSm>
 __global__ void __launch_bounds__(kAttnThreads, kPerSm) attn_kernel(const AttnParams p) {
@@ -588,14 +594,13 @@ __global__ void __launch_bounds__(kAttnThreads, kPerSm) attn_kernel(const AttnPa
   // Outputs: components 32 warp + 4 g .. + 3 of all rows.
   float2* const pairs = reinterpret_cast<float2*>(smem + S::kPair);
   float4* const refs = reinterpret_cast<float4*>(smem + S::kRef);
-  float* const keeps = reinterpret_cast<float*>(smem + S::kKeep);
+  float2* const keeps = reinterpret_cast<float2*>(smem + S::kKeep);
   int* const tos = reinterpret_cast<int*>(smem + S::kTo);
   float* const factors = reinterpret_cast<float*>(smem + S::kFactor);
   int* const lows = reinterpret_cast<int*>(smem + S::kLow);
   int* const highs = reinterpret_cast<int*>(smem + S::kHigh);
 
-  // A row's reference is a score (its negative is held) plus a small number, so
-  // that large scores do not swallow the logarithm of the value scale in it.
+  // Of a row's references -m and 2^-c are held.
   f32x2 sum[NR];
   uint4 qb[NR][4];
   auto q_part = [&](int turn, int r, int c) {  // operand B: components 16 (q + 4 (c / 2)) + 8 (c % 2) .. + 7
@@ -765,33 +770,26 @@ __global__ void __launch_bounds__(kAttnThreads, kPerSm) attn_kernel(const AttnPa
     }
     // ---- weights, as if the references held
     uint8_t* const weights = ps + turn * (S::kRows * kPStride);
-    float lv[kOf][2];
-#pragma unroll
-    for (int k = 0; k < kOf; ++k) lv[k][0] = log2_above(vs[k].x), lv[k][1] = log2_above(vs[k].y);
     f32x2 part[NR];
     for (bool raised = false;; raised = true) {
       // (a piece's first tile has no references yet)
       if (raised || !begins) {
-        float over = -INFINITY;
-        float most[kOf][2];
-#pragma unroll
-        for (int k = 0; k < kOf; ++k) most[k][0] = most[k][1] = -INFINITY;
+        float most = 0.0f;
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
           const ulonglong2 ref = *reinterpret_cast<const ulonglong2*>(refs + 4 * r + q);
 #pragma unroll
           for (int k = 0; k < kOf; ++k) {
             float w[4];
-            unpack2(sub2(add2(x[k][r][0], ref.x), ref.y), w[0], w[1]);
-            unpack2(sub2(add2(x[k][r][1], ref.x), ref.y), w[2], w[3]);
-            most[k][0] = fmaxf(most[k][0], fmaxf(w[0], w[1]));
-            most[k][1] = fmaxf(most[k][1], fmaxf(w[2], w[3]));
+            unpack2(add2(x[k][r][0], ref.x), w[0], w[1]);
+            unpack2(add2(x[k][r][1], ref.x), w[2], w[3]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) w[e] = ex2(w[e]);
             const f32x2 p0 = pack2(w[0], w[1]), p1 = pack2(w[2], w[3]);
             part[r] = k == 0 ? add2(p0, p1) : add2(part[r], add2(p0, p1));
-            unpack2(mul2(p0, both(vs[k].x)), w[0], w[1]);
-            unpack2(mul2(p1, both(vs[k].y)), w[2], w[3]);
+            // (2^-c last: no product with a finite scale is then NaN)
+            unpack2(mul2(mul2(p0, both(vs[k].x)), ref.y), w[0], w[1]);
+            unpack2(mul2(mul2(p1, both(vs[k].y)), ref.y), w[2], w[3]);
             if (!all_seen) {      // hidden weights 0, whatever the scale holds
               float v[4];
               unpack2(x[k][r][0], v[0], v[1]);
@@ -799,20 +797,25 @@ __global__ void __launch_bounds__(kAttnThreads, kPerSm) attn_kernel(const AttnPa
 #pragma unroll
               for (int e = 0; e < 4; ++e) w[e] = v[e] == -INFINITY ? 0.0f : w[e];
             }
+            most = fmaxf(most, fmaxf(fmaxf(fabsf(w[0]), fabsf(w[1])), fmaxf(fabsf(w[2]), fabsf(w[3]))));
             uint8_t* const to = weights + (8 * r + 2 * q) * kPStride + 2 * (16 * (warp + kAttnWarps * k) + tok);
             *reinterpret_cast<__half2*>(to) = __floats2half2_rn(w[0], w[2]);
             *reinterpret_cast<__half2*>(to + kPStride) = __floats2half2_rn(w[1], w[3]);
           }
+          float p0, p1;
+          unpack2(part[r], p0, p1);
+          most = fmaxf(most, fmaxf(p0, p1));
         }
-#pragma unroll
-        for (int k = 0; k < kOf; ++k) over = fmaxf(over, fmaxf(most[k][0] + lv[k][0], most[k][1] + lv[k][1]));
         // (behind this barrier all warps are done with the tile before this one)
-        const bool raise = __syncthreads_or(over > kMostWeight) != 0;
+        const bool raise = __syncthreads_or(most > kMostWeight) != 0;
         if (raised || !raise) break;
       }
       // References of the rows concerned up, what stands under them down.  Each
-      // warp's largest score and, over that, weight of a row; then the warps',
-      // lane by row.
+      // warp's largest score and, over that, weight times scale of a row; then the
+      // warps', lane by row.
+      float lv[kOf][2];
+#pragma unroll
+      for (int k = 0; k < kOf; ++k) lv[k][0] = log2_above(vs[k].x), lv[k][1] = log2_above(vs[k].y);
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
         float v[kOf][4];
@@ -842,35 +845,40 @@ __global__ void __launch_bounds__(kAttnThreads, kPerSm) attn_kernel(const AttnPa
         }
 #pragma unroll
         for (int w = 0; w < kAttnWarps; ++w) over = fmaxf(over, (of[w].x - most) + of[w].y);
-        over -= kNewWeight;
       }
       float* const ref = reinterpret_cast<float*>(refs + (lane >> 1)) + (lane & 1);
-      if (begins) {      // (each warp writes the same; nothing stands under it)
+      if (begins) {      // (each warp writes the same; nothing stands under them)
         if (lane < S::kRows) {
           ref[0] = -most;
-          ref[2] = over == -INFINITY ? 0.0f : over;
+          ref[2] = over == -INFINITY ? 1.0f : power_of_two(fminf(fmaxf(kNewWeight - ceilf(over), -kMostScale), kMostScale));
         }
         __syncwarp();
         continue;
       }
       if (warp == 0 && lane < S::kRows) {
-        const float m = ref[0], c = ref[2];
-        const bool up = (most + m) + (over + kNewWeight - c) > kLiftWeight;
-        keeps[lane] = up ? ex2((c - over) - (most + m)) : 1.0f;
+        const float m = -ref[0], c = -log2_of(ref[2]);
+        // m up wherever it is below a score, so that no weight passes 1
+        const bool up = most > m || (most - m) + over - c > kLiftWeight;
+        float2 keep = make_float2(1.0f, 1.0f);
         if (up) {
-          ref[0] = -most;
-          ref[2] = over;
+          const float to = fmaxf(m, most), down = m - to;
+          // (what stands under the references does not grow)
+          const float c_to = fminf(fmaxf(fmaxf(ceilf(over + (most - to)) - kNewWeight, ceilf(c + down)), -kMostScale), kMostScale);
+          keep = make_float2(ex2(down), ex2(down + (c - c_to)));
+          ref[0] = -to;
+          ref[2] = power_of_two(-c_to);
         }
+        keeps[lane] = keep;
       }
       __syncthreads();
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
-        const float2 keep = *reinterpret_cast<const float2*>(keeps + 8 * r + 2 * q);
-        sum[r] = mul2(sum[r], pack2(keep.x, keep.y));
+        const float4 keep = *reinterpret_cast<const float4*>(keeps + 8 * r + 2 * q);
+        sum[r] = mul2(sum[r], pack2(keep.x, keep.z));
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          o[0][r][k] *= (k & 1) ? keep.y : keep.x;
-          o[1][r][k] *= (k & 1) ? keep.y : keep.x;
+          o[0][r][k] *= (k & 1) ? keep.w : keep.y;
+          o[1][r][k] *= (k & 1) ? keep.w : keep.y;
         }
       }
     }
@@ -929,11 +937,12 @@ __global__ void __launch_bounds__(kAttnThreads, kPerSm) attn_kernel(const AttnPa
         for (int w = 0; w < kAttnWarps; ++w) l += pairs[w * S::kRows + lane].x;
       }
       const int64_t part = (2LL * blockIdx.x + (piece.cut > 0 ? 0 : 1)) * S::kRows;
-      if (!whole && warp == 0 && lane < S::kRows) {
-        const float* const ref = reinterpret_cast<const float*>(refs + (lane >> 1)) + (lane & 1);
-        p.part_share[part + lane] = Share{-ref[0], ref[2], l, 0.0f};
-      }
+      const float* const ref = reinterpret_cast<const float*>(refs + (lane >> 1)) + (lane & 1);
+      const float c_of = lane < S::kRows ? -log2_of(ref[2]) : 0.0f;
+      if (!whole && warp == 0 && lane < S::kRows) p.part_share[part + lane] = Share{-ref[0], c_of, l, 0.0f};
+      // (two factors: their product may be past fp32's range)
       const float back = !whole ? 1.0f : l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);      // 0: no token seen
+      const float scale = whole ? power_of_two(c_of) : 1.0f;
       uint16_t* const out = a.out + piece.b * a.T * a.q_heads * kHeadDim + 32 * warp + 4 * g;
       float* const part_o = p.part_o + part * kHeadDim + 32 * warp + 4 * g;
 #pragma unroll
@@ -941,8 +950,8 @@ __global__ void __launch_bounds__(kAttnThreads, kPerSm) attn_kernel(const AttnPa
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int in_tile = 8 * r + 2 * q + c, to = tos[odd * S::kRows + in_tile];
-          const float f = __shfl_sync(kAll, back, in_tile);
-          const float4 sums = make_float4(o[0][r][c] * f, o[0][r][2 + c] * f, o[1][r][c] * f, o[1][r][2 + c] * f);
+          const float f = __shfl_sync(kAll, back, in_tile), u = __shfl_sync(kAll, scale, in_tile);
+          const float4 sums = make_float4(o[0][r][c] * f * u, o[0][r][2 + c] * f * u, o[1][r][c] * f * u, o[1][r][2 + c] * f * u);
           if (to >= 0 && whole)
             *reinterpret_cast<uint2*>(out + static_cast<int64_t>(to) * kHeadDim) =
                 make_uint2(bf16x2_rn(sums.x, sums.y), bf16x2_rn(sums.z, sums.w));
@@ -963,16 +972,16 @@ __global__ void __launch_bounds__(kAttnThreads, kPerSm) attn_kernel(const AttnPa
   }
 }
 
-// A row's parts under one reference.
+// A row's parts under common references.
 struct Joined {
   Share all{kNone, -200.0f, 0.0f, 0.0f};      // below every part's
   float4 o = make_float4(0, 0, 0, 0);         // components 4 lane .. + 3
 
   __device__ __forceinline__ void add(const Share& s, const float4& v) {
-    const float m = fmaxf(all.m, s.m);
-    const float was = all.over(m), is = s.over(m), c = fmaxf(was, is);
+    const float m = fmaxf(all.m, s.m), was_m = all.m - m, is_m = s.m - m;
+    const float was = was_m + all.c, is = is_m + s.c, c = fmaxf(was, is);
     const float f = ex2(was - c), g = ex2(is - c);
-    all = Share{m, c, all.l * f + s.l * g, 0.0f};
+    all = Share{m, c, all.l * ex2(was_m) + s.l * ex2(is_m), 0.0f};
     o = make_float4(o.x * f + v.x * g, o.y * f + v.y * g, o.z * f + v.z * g, o.w * f + v.w * g);
   }
   // parts k, k + step, .. of those that shares first .. first + parts - 1 left
@@ -995,9 +1004,9 @@ struct Joined {
     }
   }
   __device__ __forceinline__ void store(const AttnParams& p, int64_t b, int seg, int row, int t, int lane) const {
-    const float back = all.l == 0.0f ? 0.0f : __fdiv_rn(1.0f, all.l);
+    const float back = all.l == 0.0f ? 0.0f : __fdiv_rn(1.0f, all.l), u = ex2(all.c);
     const int64_t to = ((b * p.a.T + t) * p.a.q_heads + seg / p.row_tiles * p.G + (row - t * p.G)) * kHeadDim + 4 * lane;
-    *reinterpret_cast<uint2*>(p.a.out + to) = make_uint2(bf16x2_rn(o.x * back, o.y * back), bf16x2_rn(o.z * back, o.w * back));
+    *reinterpret_cast<uint2*>(p.a.out + to) = make_uint2(bf16x2_rn(o.x * back * u, o.y * back * u), bf16x2_rn(o.z * back * u, o.w * back * u));
   }
 };
 
