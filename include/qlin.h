@@ -608,8 +608,10 @@ qlin_status_t qlin_kv_read_bf16(const void *cache, int64_t pages, int64_t page_s
  * over the tokens j < total_len[b] that it sees: j <= i if causal, and
  * |i - j| < window where window > 0.  A row that sees none gives zeros.
  *
- * fp32 accumulation; each exp(x_j) times its V scale is rounded to fp16
- * relative to the row's largest such product.  V scales may have any size
+ * fp32 accumulation; each exp(x_j) times its V scale is rounded relative to the
+ * row's largest such product: to 11 bits down to 2^-14 of that, below to a
+ * multiple of 2^-24 of it or less, up or down in turn, so that the sum of many
+ * small ones is kept.  V scales may have any size
  * (values under scales below 2^-100 are off by up to 2^-142 each); an exp(x_j)
  * below 2^-126 of the row's largest may count as 0.  Cache bytes at places that
  * no row sees have no effect, whatever they hold.  Non-finite scales at seen tokens give

@@ -1,5 +1,5 @@
 """The operators around the paged cache at the ends of their contract: value
-scales over fp32's whole range.
+scales over fp32's whole range, and long tails of small weights.
 
 The attention's tolerance is that of tests/test_paged_cache.py, all of whose terms
 hold here (n: the tokens of a row; a weight below fp16's normal range is at most a
@@ -128,3 +128,39 @@ def test_values_written_and_read_by_attention_near_the_largest(gpu):
     a = Attn(11, 1, T, Hq, Hkv, 16, 3, [T])
     a.raw, a.table, a.q = batch.cache.cpu().numpy(), batch.table, from_dev_bits(q)
     a.check(a.run())
+
+
+# ------------------------------------------------------- small weights, many
+
+@needs_gpu
+@pytest.mark.parametrize("n,B", [(130, 1), (2657, 1), (2657, 320), (40001, 320), (131072, 320)])
+def test_a_tail_of_small_weights(gpu, n, B):
+    """A token that outweighs each of many alike by 2^gap, at the beginning: their sum
+    is what components have in which that token has nothing, or the tail one sign."""
+    rng = np.random.default_rng(n)
+    for gap in (12.5, 15.3, 18.4, 20.7, 22.2, 24.0, 24.9, 25.5, 27.0):
+        x = np.zeros(n)
+        x[0] = gap * np.log(2.0)
+        codes = np.full((n, D), 127)
+        codes[0, :100] = 0
+        codes[:, 20:40] = rng.integers(0, 128, (n, 20))
+        codes[1:, 40:60] = rng.integers(0, 2, (n - 1, 1)) * 127
+        for i, step in enumerate((2, 4, 8, 16, 32, 64)):       # few of the tokens, at regular places
+            codes[1:, 60 + i] = 0
+            codes[1 + i::step, 60 + i] = 127
+        codes[1:, 66:100] *= -1
+        codes[0, :100] = 0
+        check_one_head(x, codes, np.full(n, 0.01), B)
+
+
+@needs_gpu
+@pytest.mark.parametrize("B", [1, 320])
+def test_a_tail_that_falls_and_one_that_rises(gpu, B):
+    """Weights over forty powers of two, the largest first or last."""
+    n = 20000
+    for slope in (1.0, -1.0):
+        x = np.linspace(0, 40 * slope, n) * np.log(2.0)
+        codes = np.full((n, D), 127)
+        codes[:, 64:] = np.arange(n)[:, None] % 128
+        codes[-1 if slope > 0 else 0, :32] = 0
+        check_one_head(x, codes, np.full(n, 0.3), B)

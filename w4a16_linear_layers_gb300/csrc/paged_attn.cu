@@ -53,9 +53,13 @@
 //
 // Precision.  Codes are exact in fp16, and so is q up to 2^-39 of its row's
 // largest component.  The largest product of a weight and its value scale that a row
-// has seen stands between 2^-1 and 2^15, so these products have fp16's 11 bits down to
-// 2^-13 of it, and are at most 2^-24 of it off below that.  Scores, weights, sums and
-// outputs are fp32; a weight is 0 below 2^-126 of the row's largest.
+// has seen stands between 1 and 2^15, so these products have fp16's 11 bits down to
+// 2^-14 of it, and are at most a step of 2^-24 off below that.  There a product gets,
+// before it is rounded, up to half a step more or less, by its token: of the products that
+// fall between two steps as many round up as their place between them says, so that a long
+// tail of small ones, alike or not, has its sum (without that the sum of 131072 at 2^-20.7
+// of the first was 5% off, at 2^-25.5 nothing).  Scores, weights, sums and outputs are
+// fp32; a weight is 0 below 2^-126 of the row's largest.
 #include <cfloat>
 
 #include <algorithm>
@@ -81,11 +85,13 @@ constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr float kNone = -1e30f;     // reference of a row that has seen nothing
 // Weights times their scales: what a row's references may let through (of the weights
 // by themselves too), the logarithm of what a reference set in passing is lifted at, and
-// of a power of two above the row's largest where one is set: 14 apart, so that few tiles
-// set one (of 27 tiles of 32 rows one in ten; 11 apart one in four, 4 apart one in three).
+// of a power of two above the row's largest, not more than four times that, where one is
+// set: 13 apart, so that few tiles set one, and not more, so that what is rounded to a step
+// of 2^-24 is small beside the row's largest (12 x 8 tokens at 8192: 13 apart 56.6 us, 11
+// apart 57.6, 9 apart 58.8).
 constexpr float kMostWeight = 32768.0f;
 constexpr float kLiftWeight = 4.0f;
-constexpr float kNewWeight = 1.0f;
+constexpr float kNewWeight = 2.0f;
 constexpr float kMostScale = 126.0f;      // c is between this and its negative
 
 template <int NR, int kPerSm>
@@ -516,7 +522,7 @@ __global__ void __launch_bounds__(kAttnThreads, kPerSm) attn_kernel(const AttnPa
   int first = 0, head_at = 0;        // the piece's first block of the sequence; the head's first block of a page
   int page[kOf], in_head[kOf];       // lane by tile: the blocks' pages, their places in the cache but for that
   int put = 0;
-  bool more = true;
+  bool coming = true;
   uint32_t on_page = 0;              // bits t % kTilesAhead, kOf each: the warp's blocks of tile t are on a page
   int to_send = 0, send_slot = warp; // the tile whose block is next, and where it goes
   int behind_total = 0, behind_fresh = 0;  // lane 0: see Walk
@@ -542,7 +548,7 @@ __global__ void __launch_bounds__(kAttnThreads, kPerSm) attn_kernel(const AttnPa
   };
   // tile: the one whose predecessors are done
   auto send = [&](int tile) {
-    if (!more || kTileBlocks * to_send >= kTileBlocks * tile + kSlots) return;
+    if (!coming || kTileBlocks * to_send >= kTileBlocks * tile + kSlots) return;
     const int from = next_i / kTileBlocks % 32;
     const int of = to_send % kTilesAhead;
 #pragma unroll
@@ -567,9 +573,9 @@ __global__ void __launch_bounds__(kAttnThreads, kPerSm) attn_kernel(const AttnPa
     if (next_i < next_n) {
       if (from == 31) look();
     } else {
-      more = ahead.left > next_n;
+      coming = ahead.left > next_n;
       __syncwarp();
-      if (more) {
+      if (coming) {
         if (lane == 0) ahead.next(a, behind_total, behind_fresh);
         __syncwarp();
         enter();
@@ -591,6 +597,12 @@ __global__ void __launch_bounds__(kAttnThreads, kPerSm) attn_kernel(const AttnPa
   // 2 u + 1, 4 chunks each) meet in no bank.
   const int tok = 2 * (g >> 1) + 8 * (g & 1);
   const int k_turn = 2 * ((tok >> 2) & 3);
+  // What is added to token t's products, in steps: the bits of t % 128 backwards as a
+  // fraction, so that any 2^i tokens in a row, or at equal distances of a power of two,
+  // have equally spaced ones; moved in the same way from tile to tile.  Here 1 more
+  // (the exponent's) and 1/2 - 1/256 as well.
+  const uint32_t jitter = 0x33800000u | __brev(tok + 16 * warp) >> 25 << 16;
+  constexpr float kJitterMid = 1.49609375f * 0x1p-24f;
   // Outputs: components 32 warp + 4 g .. + 3 of all rows.
   float2* const pairs = reinterpret_cast<float2*>(smem + S::kPair);
   float4* const refs = reinterpret_cast<float4*>(smem + S::kRef);
@@ -770,7 +782,15 @@ __global__ void __launch_bounds__(kAttnThreads, kPerSm) attn_kernel(const AttnPa
     }
     // ---- weights, as if the references held
     uint8_t* const weights = ps + turn * (S::kRows * kPStride);
-    f32x2 part[NR];
+    f32x2 more[kOf][2], part[NR];
+    {
+      const uint32_t moved = __brev(tile) >> 25 << 16;
+#pragma unroll
+      for (int k = 0; k < kOf; ++k) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) more[k][c] = both(__uint_as_float(jitter + (k << 16) ^ moved ^ c << 22) - kJitterMid);
+      }
+    }
     for (bool raised = false;; raised = true) {
       // (a piece's first tile has no references yet)
       if (raised || !begins) {
@@ -788,8 +808,8 @@ __global__ void __launch_bounds__(kAttnThreads, kPerSm) attn_kernel(const AttnPa
             const f32x2 p0 = pack2(w[0], w[1]), p1 = pack2(w[2], w[3]);
             part[r] = k == 0 ? add2(p0, p1) : add2(part[r], add2(p0, p1));
             // (2^-c last: no product with a finite scale is then NaN)
-            unpack2(mul2(mul2(p0, both(vs[k].x)), ref.y), w[0], w[1]);
-            unpack2(mul2(mul2(p1, both(vs[k].y)), ref.y), w[2], w[3]);
+            unpack2(fma2(mul2(p0, both(vs[k].x)), ref.y, more[k][0]), w[0], w[1]);
+            unpack2(fma2(mul2(p1, both(vs[k].y)), ref.y, more[k][1]), w[2], w[3]);
             if (!all_seen) {      // hidden weights 0, whatever the scale holds
               float v[4];
               unpack2(x[k][r][0], v[0], v[1]);
