@@ -1,5 +1,6 @@
 """The operators around the paged cache at the ends of their contract: value
-scales over fp32's whole range, and long tails of small weights.
+scales over fp32's whole range, long tails of small weights, and scales that
+are not finite.
 
 The attention's tolerance is that of tests/test_paged_cache.py, all of whose terms
 hold here (n: the tokens of a row; a weight below fp16's normal range is at most a
@@ -164,3 +165,26 @@ def test_a_tail_that_falls_and_one_that_rises(gpu, B):
         codes[:, 64:] = np.arange(n)[:, None] % 128
         codes[-1 if slope > 0 else 0, :32] = 0
         check_one_head(x, codes, np.full(n, 0.3), B)
+
+
+# -------------------------------------------------- scales that are not finite
+
+@needs_gpu
+@pytest.mark.parametrize("softcap", [0.0, 5.0])
+@pytest.mark.parametrize("total", [100, 700])
+@pytest.mark.parametrize("which", [0, 1])
+@pytest.mark.parametrize("value", [np.inf, -np.inf, np.nan])
+def test_scales_that_are_not_finite_reach_the_rows_that_see_them(gpu, which, value, total, softcap):
+    """A key's (0) or value's (1) at the third last token: the last three rows see it."""
+    for seed in (1, 2, 3):
+        a = Attn(seed, 1, 8, 4, 2, 16, 45, [total], softcap=softcap)
+        clean = a.raw.copy()
+        cache = ref.Cache(a.raw)
+        codes, s = cache.get(a.table, 0, total - 3)
+        s = s.copy()
+        s[which] = value
+        cache.put(a.table, 0, total - 3, codes, s)
+        o = ref.bf16_to_f64(from_dev_bits(a.run()))
+        assert not np.isfinite(o[5:]).any()
+        o64, A, X, big, _ = ref.attention(ref.bf16_to_f64(a.q), ref.Cache(clean), a.table, a.total, a.T, softcap=softcap)
+        assert (np.abs(o - o64) <= tolerance(o64, A, X, big, total))[:5].all()

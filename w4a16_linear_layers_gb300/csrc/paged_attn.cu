@@ -741,6 +741,8 @@ __global__ void __launch_bounds__(kAttnThreads, kPerSm) attn_kernel(const AttnPa
 #pragma unroll
       for (int k = 0; k < kOf; ++k) {
         ks[k] = *reinterpret_cast<const float2*>(keys[k] + kKScales + 4 * tok);
+        // (an infinite one gives NaN: its scores would be infinite, of weight 0, or at a cap)
+        ks[k] = make_float2(__fmaf_rn(ks[k].x, 0.0f, ks[k].x), __fmaf_rn(ks[k].y, 0.0f, ks[k].y));
         vs[k] = *reinterpret_cast<const float2*>(keys[k] + kVScales + 4 * tok);
       }
 #pragma unroll
