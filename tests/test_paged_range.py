@@ -1,6 +1,6 @@
 """The operators around the paged cache at the ends of their contract: value
-scales over fp32's whole range, long tails of small weights, and scales that
-are not finite.
+scales over fp32's whole range, long tails of small weights, scales that are not
+finite, and heads whose squares vanish.
 
 The attention's tolerance is that of tests/test_paged_cache.py, all of whose terms
 hold here (n: the tokens of a row; a weight below fp16's normal range is at most a
@@ -188,3 +188,16 @@ def test_scales_that_are_not_finite_reach_the_rows_that_see_them(gpu, which, val
         assert not np.isfinite(o[5:]).any()
         o64, A, X, big, _ = ref.attention(ref.bf16_to_f64(a.q), ref.Cache(clean), a.table, a.total, a.T, softcap=softcap)
         assert (np.abs(o - o64) <= tolerance(o64, A, X, big, total))[:5].all()
+
+
+# ------------------------------------------------------- heads of small numbers
+
+@needs_gpu
+@pytest.mark.parametrize("size", [2.0 ** -72, 2.0 ** -76, 2.0 ** -90, 2.0 ** -120])
+def test_write_normed_heads_whose_squares_vanish(gpu, size):
+    """eps alone is left under the root: 1 / sqrt(eps) for such heads."""
+    rng = np.random.default_rng(12)
+    for R in (0, 128):
+        x = rng.standard_normal((8, 6 * D)) * size
+        batch = Batch(13, 1, 8, 2, 2, 16, 2, [8], R=R, norm=True, eps=1e-6, qkv=ref.bf16(x))
+        batch.check(batch.run())

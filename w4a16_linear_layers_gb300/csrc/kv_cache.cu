@@ -305,7 +305,8 @@ __global__ void __launch_bounds__(32, kWritesAtOnce) kv_write_kernel(const __gri
         unpack2(two, lo, hi);
         const float sum = head_sum(lo + hi);
         // a head of zeros stays one with eps = 0; a sum past fp32's range gives NaN
-        rho = sum == 0.0f ? 0.0f : sum < INFINITY ? rsqrtf(__fmaf_rn(sum, 1.0f / kHeadDim, a.eps)) : NAN;
+        const float mean = __fmaf_rn(sum, 1.0f / kHeadDim, a.eps);
+        rho = mean == 0.0f ? 0.0f : mean < INFINITY ? rsqrtf(mean) : NAN;
         y[0].times(gain[0]);
         y[1].times(gain[1]);
       }
