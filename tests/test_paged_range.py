@@ -1,6 +1,6 @@
 """The operators around the paged cache at the ends of their contract: value
 scales over fp32's whole range, long tails of small weights, scales that are not
-finite, and heads whose squares vanish.
+finite, heads whose squares vanish, and capped scores of either sign.
 
 The attention's tolerance is that of tests/test_paged_cache.py, all of whose terms
 hold here (n: the tokens of a row; a weight below fp16's normal range is at most a
@@ -201,3 +201,24 @@ def test_write_normed_heads_whose_squares_vanish(gpu, size):
         x = rng.standard_normal((8, 6 * D)) * size
         batch = Batch(13, 1, 8, 2, 2, 16, 2, [8], R=R, norm=True, eps=1e-6, qkv=ref.bf16(x))
         batch.check(batch.run())
+
+
+# ---------------------------------------------------------------- capped scores
+
+@needs_gpu
+def test_capped_scores_are_odd(gpu):
+    """Two tokens of opposite values under scores of either sign: the tanh of both signs
+    is the same but for its sign, so outputs of q and -q are too, up to the roundings of
+    the weights (at most 2^-11) and of the outputs."""
+    rng = np.random.default_rng(14)
+    B, cap = 4000, 2.0 ** 17
+    x = -cap * rng.uniform(0.4, 1.5, B)
+    raw = np.concatenate([one_head([s, s + d], np.array([[100] * D, [-100] * D]), [0.01, 0.01])[:, :, :1]
+                          for s, d in zip(x, rng.uniform(-1.5, 1.5, B))])
+    table = to_dev(np.arange(B, dtype=np.int32)[:, None])
+    q = to_dev_bits(first(B), torch.bfloat16)
+    o = [ref.bf16_to_f64(from_dev_bits(qlin.paged_attn_i8(t, to_dev(raw), table, to_dev(np.full(B, 2, np.int32)), scale=1.0, softcap=cap)))
+         for t in (q, -q)]
+    assert (np.abs(o[0]) < 0.9).any() and (np.abs(o[0]) > 0.1).any()
+    bound = 2.0 ** -11 + 2.0 ** -8 * np.abs(o[0])
+    assert (np.abs(o[0] + o[1]) <= bound).all(), np.abs(o[0] + o[1]).max()

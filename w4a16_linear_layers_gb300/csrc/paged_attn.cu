@@ -304,11 +304,14 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// cap tanh(x / cap) of four, 2^-22 of it off at most.  With y = x / cap:
+// cap tanh(x / cap) of four, 2^-20 of it off at most.  With y = |x| / cap:
 // below 0.6 y + y^3 p(y^2), p of degree 4 fitted to it (2^-28); from there on
-// 1 - 2 / (1 + e^2y), which would cancel below.  Scores are mostly well below their
-// caps, so a warp forms the second only where one of its scores needs it (12 x 8 tokens
-// at 8192 under a cap of 30: 70.0 us, 72.0 with both always, 64.7 without a cap).
+// 1 - 2 / (1 + e^2y), which would cancel below (at 0.6, where tanh is 0.537: e^2y 1.6
+// steps of 2^-22 off by its argument and ex2, its sum half, the quotient of 0.463 one by
+// its division: 1.2 in all), with the sign of x (for y below 0 it would cancel too, and
+// be twice as far off).  Scores are mostly well below their
+// caps, so a warp forms the second only where one of its scores needs it (12 x 8 tokens,
+// all at 8192: 79.0 us under a cap of 30, 80.2 under one of 2, 71.2 without a cap).
 constexpr float kSmall = 0.6f;
 __device__ __forceinline__ void cap_scores(float (&v)[4], float cap, float per_cap) {
   float y[4], most = 0.0f;
@@ -326,8 +329,8 @@ __device__ __forceinline__ void cap_scores(float (&v)[4], float cap, float per_c
   if (__any_sync(kAll, most >= kSmall)) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float l = 1.0f - __fdividef(2.0f, 1.0f + ex2(y[k] * (2.0f * kLog2e)));
-      v[k] = fabsf(y[k]) < kSmall ? v[k] : l;
+      const float l = 1.0f - __fdividef(2.0f, 1.0f + ex2(fabsf(y[k]) * (2.0f * kLog2e)));
+      v[k] = fabsf(y[k]) < kSmall ? v[k] : copysignf(l, y[k]);
     }
   }
 #pragma unroll
@@ -1131,7 +1134,7 @@ cudaError_t launch_groups(const AttnParams& p, int grid, cudaStream_t stream) {
 
 template <int NR, int kPerSm>
 cudaError_t launch_cap(const AttnParams& p, int grid, cudaStream_t stream) {
-  // (a cap past 2^100 changes no score that fp32 can tell from its neighbour, and would overflow)
+  // (a cap past 2^100 changes no score below 2^87 that fp32 can tell from its neighbour, and would overflow)
   return p.a.softcap > 0.0f && p.a.softcap < 0x1p100f ? launch_groups<NR, true, kPerSm>(p, grid, stream)
                                                          : launch_groups<NR, false, kPerSm>(p, grid, stream);
 }
