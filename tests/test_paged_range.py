@@ -1,6 +1,6 @@
 """The operators around the paged cache at the ends of their contract: value
 scales over fp32's whole range, long tails of small weights, scales that are not
-finite, heads whose squares vanish, and capped scores of either sign.
+finite, heads whose squares vanish, capped scores of either sign.
 
 The attention's tolerance is that of tests/test_paged_cache.py, all of whose terms
 hold here (n: the tokens of a row; a weight below fp16's normal range is at most a
@@ -12,7 +12,7 @@ import torch
 
 import paged_ref as ref
 from helpers import from_dev_bits, to_dev, to_dev_bits
-from test_paged_cache import Attn, Batch, D, gpu, needs_gpu, tolerance  # noqa: F401
+from test_paged_cache import Attn, Batch, D, attn_of, gpu, needs_gpu, step_state, tolerance  # noqa: F401
 from w4a16_linear_layers_gb300 import qlin
 
 PAGE = 64
@@ -222,3 +222,13 @@ def test_capped_scores_are_odd(gpu):
     assert (np.abs(o[0]) < 0.9).any() and (np.abs(o[0]) > 0.1).any()
     bound = 2.0 ** -11 + 2.0 ** -8 * np.abs(o[0])
     assert (np.abs(o[0] + o[1]) <= bound).all(), np.abs(o[0] + o[1]).max()
+
+
+@needs_gpu
+def test_a_softcap_that_fp32_does_not_hold(gpu):
+    """One below fp32's smallest number is refused and not taken as none."""
+    s = attn_of(step_state(5))
+    for cap in (1e-46, 1e-300):
+        with pytest.raises(ValueError, match="softcap"):
+            qlin.paged_attn_i8(s["q"], s["cache"], s["table"], s["total"], softcap=cap)
+    qlin.paged_attn_i8(s["q"], s["cache"], s["table"], s["total"], softcap=1.5e-45)

@@ -514,6 +514,10 @@ PyObject* paged_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!cache_of(c, a[1], a[2], a[3], a[4], index) || !rows_of(M, c.B, "q", T) || (!is_none(a[5]) && !real(a[5], scale)) ||
       !real(a[6], softcap) || !whole(a[7], window))
     return nullptr;
+  if (softcap == 0.0f && PyFloat_AsDouble(a[6]) != 0.0) {      // (0 would be no cap)
+    PyErr_SetString(PyExc_ValueError, "softcap must be 0 or at least fp32's smallest number");
+    return nullptr;
+  }
   const int causal = PyObject_IsTrue(a[8]);
   if (causal < 0) return nullptr;
   if (width == 0 || c.kv_heads == 0 || width % (128 * c.kv_heads) != 0) {
