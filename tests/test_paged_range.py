@@ -1,6 +1,7 @@
 """The operators around the paged cache at the ends of their contract: value
 scales over fp32's whole range, long tails of small weights, scales that are not
-finite, heads whose squares vanish, capped scores of either sign.
+finite, heads whose squares vanish, capped scores of either sign, and calls that
+follow one another closely.
 
 The attention's tolerance is that of tests/test_paged_cache.py, all of whose terms
 hold here (n: the tokens of a row; a weight below fp16's normal range is at most a
@@ -12,7 +13,7 @@ import torch
 
 import paged_ref as ref
 from helpers import from_dev_bits, to_dev, to_dev_bits
-from test_paged_cache import Attn, Batch, D, attn_of, gpu, needs_gpu, step_state, tolerance  # noqa: F401
+from test_paged_cache import Attn, Batch, D, attn_of, gpu, needs_gpu, random_cache, step_state, tolerance  # noqa: F401
 from w4a16_linear_layers_gb300 import qlin
 
 PAGE = 64
@@ -232,3 +233,37 @@ def test_a_softcap_that_fp32_does_not_hold(gpu):
         with pytest.raises(ValueError, match="softcap"):
             qlin.paged_attn_i8(s["q"], s["cache"], s["table"], s["total"], softcap=cap)
     qlin.paged_attn_i8(s["q"], s["cache"], s["table"], s["total"], softcap=1.5e-45)
+
+
+# ------------------------------------------------- calls close behind one another
+
+@needs_gpu
+@pytest.mark.parametrize("before,T", [(512, 512), (512, 1), (4096, 64), (20000, 512)])
+def test_reads_around_a_write(gpu, before, T):
+    """A read, a write of tokens that it read and a read of those, one close behind the
+    other: the last one gives what was written, whatever the first left in caches."""
+    rng = np.random.default_rng(15)
+    Hkv, page = 8, 64
+    per = -(-before // page)
+    cache = to_dev(random_cache(rng, per, Hkv, page))
+    table = to_dev(rng.permutation(per).astype(np.int32)[None])
+    total = to_dev(np.array([before], np.int32))
+    start = total - T
+    rows = [to_dev_bits(ref.bf16(rng.standard_normal((T, 2 * Hkv * D))), torch.bfloat16) for _ in range(2)]
+    want = []
+    for x in rows:
+        qlin.kv_write_i8(x, cache, table, total, 0)
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in qlin.kv_read_bf16(cache, table, total, T, start=start)])
+        torch.cuda.synchronize()
+    k, v = (torch.empty((1, before, Hkv, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(300):
+        if i % 10 == 0:
+            torch.cuda._sleep(200_000)
+        qlin.kv_read_bf16(cache, table, total, before, k=k, v=v)
+        qlin.kv_write_i8(rows[i % 2], cache, table, total, 0)
+        got = qlin.kv_read_bf16(cache, table, total, T, start=start)
+        for g, w in zip(got, want[i % 2]):
+            wrong += (g != w).any()
+    assert int(wrong) == 0

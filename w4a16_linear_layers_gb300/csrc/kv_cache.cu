@@ -44,6 +44,10 @@ namespace {
 // themselves: writes in blocks of one warp (12 x 8 rows 4.2 us, 4.6 in blocks of two or
 // four; 8192 rows 39.7, 40.3, 40.5), reads of two (515 tokens 2.5 us, 2.8 in four;
 // 12 x 8192 in blocks of one 93.1, of two 90.6).
+//
+// What kernels of this library write (rows of qkv, the cache) is read past L1: a kernel
+// may start before the one in front of it, which writes them, and beside the one in front
+// of that, whose reads could leave older lines in the L1 that they share.
 constexpr int kReadWarps = 2;
 constexpr int64_t kWritesAtOnce = 20;     // blocks of a write on an SM, which is what 96 registers allow
 constexpr uint32_t kAll = 0xFFFFFFFFu;
@@ -197,7 +201,7 @@ __device__ __forceinline__ Pair exact_turn(float u, float c, float p, float s) {
   return {hi, __fsub_rn(l, __fsub_rn(hi, h))};
 }
 
-__device__ __forceinline__ float bf16_at(const uint16_t* p) { return __uint_as_float(static_cast<uint32_t>(__ldg(p)) << 16); }
+__device__ __forceinline__ float bf16_value(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
 
 // Component e of a lane's 16 of the head at x, times `scaled`, as an
 // unevaluated pair; formed again from memory, as few are asked for.
@@ -205,8 +209,8 @@ __device__ __forceinline__ Pair exact_component(const KvWriteArgs& a, uint32_t r
                                                 bool turned, const Place& place, int e, float scaled) {
   const int i = e & 7, d0 = 8 * place.at[0] + i, d1 = 8 * place.at[1] + i;
   // (the scaling first: a subnormal product would lose bits)
-  float u0 = bf16_at(x + d0) * scaled, u1 = bf16_at(x + d1) * scaled;
-  if (gamma != nullptr) u0 *= bf16_at(gamma + d0), u1 *= bf16_at(gamma + d1);
+  float u0 = bf16_value(__ldcg(x + d0)) * scaled, u1 = bf16_value(__ldcg(x + d1)) * scaled;
+  if (gamma != nullptr) u0 *= bf16_value(__ldg(gamma + d0)), u1 *= bf16_value(__ldg(gamma + d1));
   if (!turned) return {e < 8 ? u0 : u1, 0.0f};
   const int R = static_cast<int>(a.R);
   int at = pos;
@@ -243,7 +247,7 @@ __global__ void __launch_bounds__(32, kWritesAtOnce) kv_write_kernel(const __gri
   uint4 next[2];
   auto load = [&](int heads) {
 #pragma unroll
-    for (int w = 0; w < 2; ++w) next[w] = at < heads ? __ldg(reinterpret_cast<const uint4*>(x) + place.at[w]) : make_uint4(0, 0, 0, 0);
+    for (int w = 0; w < 2; ++w) next[w] = at < heads ? __ldcg(reinterpret_cast<const uint4*>(x) + place.at[w]) : make_uint4(0, 0, 0, 0);
   };
   auto enter = [&](int group) {
     const bool query = group < q_groups, value = group >= k_end;
@@ -484,8 +488,8 @@ __global__ void __launch_bounds__(32 * kReadWarps) kv_read_kernel(const CacheArg
       code[w][j] = make_uint4(0, 0, 0, 0);
       scale[w][j] = 0.0f;
       if (block != nullptr && tok0 + r < len && (w == 0 ? k : v) != nullptr) {
-        code[w][j] = __ldg(reinterpret_cast<const uint4*>(block + w * kVCodes + r * kHeadDim + code_place(r, 16 * chunk)));
-        scale[w][j] = __ldg(reinterpret_cast<const float*>(block + (w == 0 ? kKScales : kVScales)) + r);
+        code[w][j] = __ldcg(reinterpret_cast<const uint4*>(block + w * kVCodes + r * kHeadDim + code_place(r, 16 * chunk)));
+        scale[w][j] = __ldcg(reinterpret_cast<const float*>(block + (w == 0 ? kKScales : kVScales)) + r);
       }
     }
   }
