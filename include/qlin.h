@@ -556,7 +556,9 @@ size_t qlin_kv_cache_bytes(int64_t pages, int64_t kv_heads, int64_t page_size);
  * q and the scales come from fp32 arithmetic (scales within 2^-20 of their
  * value), the codes are exact.  A head of zeros gives codes and scale 0.  A key
  * or value head with a NaN or an infinity, or whose sums leave fp32's range,
- * gives scale NaN (its codes mean nothing), a query head NaN.  Outside the
+ * gives scale NaN (its codes mean nothing).  Such a query head gives NaN
+ * everywhere under a norm, else non-finite values in the components that are
+ * not finite and their partners in the rotation, no others.  Outside the
  * contract: heads, other than zero ones, whose mean of x^2 plus eps is below
  * 2^-100 under a norm, and non-finite gamma, cos or sin.
  *

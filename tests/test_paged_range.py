@@ -204,6 +204,33 @@ def test_write_normed_heads_whose_squares_vanish(gpu, size):
         batch.check(batch.run())
 
 
+@needs_gpu
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("value", [np.inf, -np.inf, np.nan])
+@pytest.mark.parametrize("R", [0, 64, 128])
+def test_query_heads_that_are_not_finite(gpu, R, value, norm):
+    """NaN everywhere under a norm; else the component, with its partner in the rotation, and no other."""
+    rng = np.random.default_rng(16)
+    T, Hq = 6, 2
+    x = rng.standard_normal((T, Hq + 2, D))
+    at = [0, 31, 40, 64, 100, 127]
+    x[np.arange(T), 0, at] = value
+    batch = Batch(17, 1, T, Hq, 1, 16, 1, [T], R=R, norm=norm, qkv=ref.bf16(x).reshape(T, -1))
+    q = ref.bf16_to_f64(from_dev_bits(batch.run())).reshape(T, Hq, D)
+    with np.errstate(invalid="ignore"):
+        want = list(batch.expect())
+    for row, _, _, q64, S, _, _ in want:
+        hit = np.zeros((Hq, D), bool)
+        hit[0, at[row]] = True
+        if at[row] < R:
+            hit[0, (at[row] + R // 2) % R] = True
+        if norm:
+            hit[0] = True
+        assert np.isnan(q[row][hit]).all() if norm else not np.isfinite(q[row][hit]).any()
+        with np.errstate(invalid="ignore"):
+            assert (np.abs(q[row] - q64) <= 2.0 ** -8 * np.abs(q64) + 2.0 ** -20 * S)[~hit].all()
+
+
 # ---------------------------------------------------------------- capped scores
 
 @needs_gpu

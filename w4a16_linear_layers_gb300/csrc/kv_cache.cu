@@ -75,10 +75,6 @@ __device__ __forceinline__ float head_max(float v) {
 // 8 components, two at a time
 struct Part {
   f32x2 v[4];
-  __device__ __forceinline__ void fill(float x) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = pack2(x, x);
-  }
   __device__ __forceinline__ void widen(const uint4& w) {
     v[0] = widen2(w.x);
     v[1] = widen2(w.y);
@@ -115,16 +111,13 @@ struct Place {
   }
 };
 
-// cosines and sines of a lane's first vector: y0 = u0 c - u1 s, y1 = u1 c + u0 s
+// cosines and sines of a turned lane's first vector: y0 = u0 c - u1 s, y1 = u1 c + u0 s
 struct Turn {
   Part c, s;
 };
 
 __device__ __forceinline__ Turn load_turn(const KvWriteArgs& a, int64_t row, int pos, const Place& place) {
   Turn t;
-  t.c.fill(1.0f);
-  t.s.fill(0.0f);
-  if (!place.turned) return t;
   const int R = static_cast<int>(a.R), half = R / 2;
   const int pair0 = 8 * place.at[0];
   const int last = static_cast<int>(a.P) - 1;
@@ -264,7 +257,7 @@ __global__ void __launch_bounds__(32, kWritesAtOnce) kv_write_kernel(const __gri
   const int pos = seq.len - seq.fresh + t;
   const bool turned = a.R != 0;
   Turn turn;
-  if (turned) turn = load_turn(a, row, pos, place);
+  if (place.turned) turn = load_turn(a, row, pos, place);
   const int place_of = pos & 15;
   const int64_t head_step = (a.c.page_size >> 4) * kCacheBlock;
   uint8_t* block = nullptr;       // of head 0
@@ -314,7 +307,7 @@ __global__ void __launch_bounds__(32, kWritesAtOnce) kv_write_kernel(const __gri
         y[0].times(gain[0]);
         y[1].times(gain[1]);
       }
-      if (turned && kKind != 2) {
+      if (place.turned && kKind != 2) {      // (the others' would be u1 * 0 off: NaN beside an infinity)
         const Part u[2] = {y[0], y[1]};
         turn_heads(u, turn, y);
       }
