@@ -527,8 +527,9 @@ qlin_status_t qlin_adjust_logits_f32(const float *logits, int64_t M, int64_t V,
  *   new_len       int32 [B] or NULL (T of each): new tokens, the last ones of
  *                 the sequence, in rows t < new_len[b]; lengths outside
  *                 [0, min(T, total_len[b])] are taken as the nearer end.  Rows
- *                 from new_len[b] on are padding: nothing is read from them,
- *                 and their outputs are left as they were.
+ *                 from new_len[b] on are padding: what they hold has no effect
+ *                 (but they are part of the buffers and may be loaded), and their
+ *                 outputs are left as they were.
  * Row b T + t is thus token total_len[b] - new_len[b] + t.  int32, uint8 and
  * fp32 arrays are 4-byte aligned except where stated, all else 16-byte.  Where
  * B or T is 0 the calls do nothing.
