@@ -294,3 +294,74 @@ def test_reads_around_a_write(gpu, before, T):
         for g, w in zip(got, want[i % 2]):
             wrong += (g != w).any()
     assert int(wrong) == 0
+
+# ------------------------------------------------ the ends of what scales may be
+
+@needs_gpu
+@pytest.mark.parametrize("B", [1, 320])
+@pytest.mark.parametrize("size", [3.3e38, 2.0 ** 124, 2.0 ** -126])
+def test_value_scales_at_the_very_ends(gpu, size, B):
+    """Products that leave fp32's range where weights stand above 1: scores rise all along."""
+    rng = np.random.default_rng(18)
+    n = 4000
+    check_one_head(np.linspace(0, 40, n), rng.integers(-1, 2, (n, D)), np.full(n, size), B)
+    check_one_head(rng.standard_normal(n), rng.integers(-1, 2, (n, D)), np.where(rng.random(n) < 0.3, size, 1.0), B)
+
+
+@needs_gpu
+@pytest.mark.parametrize("B", [1, 320])
+def test_negative_scales(gpu, B):
+    """As the formula has them, although no write makes them."""
+    rng = np.random.default_rng(19)
+    n = 3000
+    vs = np.exp(rng.standard_normal(n)) * rng.choice([-1.0, 1.0], n) / 90
+    check_one_head(-4 + 3 * rng.standard_normal(n), rng.integers(-127, 128, (n, D)), vs, B)
+
+
+# --------------------------------------------------------------- many new tokens
+
+@needs_gpu
+@pytest.mark.parametrize("T,Hq,Hkv,total,new,wide,kw", [
+    # a prompt; one behind a prefix and padded; in a window, both ways
+    (2000, 8, 2, 2000, 2000, 0, {}), (1500, 6, 2, 3300, 1471, 0, {}), (1500, 8, 2, 1700, 1500, 0, {"window": 300, "causal": False}),
+    # row tiles past 2^16, with tables of any width
+    (4100, 512, 1, 4100, 4100, 0, {"window": 500}), (4100, 512, 1, 1200, 1200, 60000, {}),
+    # rows of a segment past 2^24
+    (1100, 16384, 1, 1100, 1100, 0, {"window": 16})])
+def test_many_new_tokens(gpu, T, Hq, Hkv, total, new, wide, kw):
+    """Rows at both ends, at random and around every power of two of row tiles against
+    binary64; padding as it was."""
+    rng = np.random.default_rng(T + Hq)
+    page = 64
+    per = -(-total // page)
+    raw = random_cache(rng, per, Hkv, page)
+    table = rng.permutation(per).astype(np.int32)[None]
+    cache = ref.Cache(raw)
+    if wide:
+        table = np.concatenate([table, np.full((1, wide), -1, np.int32)], 1)
+    g = torch.Generator("cuda").manual_seed(T)
+    q = torch.randn((T, Hq * D), generator=g, device="cuda", dtype=torch.bfloat16)
+    out = torch.full_like(q, 7.0)
+    qlin.paged_attn_i8(q, to_dev(raw), to_dev(table), to_dev(np.array([total], np.int32)), new_len=to_dev(np.array([new], np.int32)),
+                       out=out, **kw)
+    k, v, _ = cache.values(table, 0, 0, total)
+    G = Hq // Hkv
+    at = [0, new * G - 1] + [r + d for i in range(25) for r in (32 << i,) for d in (-1, 0) if r + d < new * G]
+    at += list(rng.integers(0, new * G, 60))
+    for r in at:
+        t, h = r // G, int(rng.integers(0, Hkv)) * G + r % G
+        i = total - new + t
+        j = np.arange(total)
+        see = (j <= i) | (not kw.get("causal", True))
+        if kw.get("window"):
+            see &= np.abs(i - j) < kw["window"]
+        kk, vv = k[see, h // G], v[see, h // G]
+        qr = q[t, h * D:(h + 1) * D].double().cpu().numpy()
+        x = D ** -0.5 * (kk @ qr)
+        p = np.exp(x - x.max())
+        p /= p.sum()
+        o64 = p @ vv
+        X = D ** -0.5 * (np.abs(kk) @ np.abs(qr)).max()
+        o = out[t, h * D:(h + 1) * D].double().cpu().numpy()
+        assert (np.abs(o - o64) <= tolerance(o64, p @ np.abs(vv), X, np.abs(vv).max(), int(see.sum()))).all(), (r, t, h)
+    assert bool((out[new:] == 7.0).all())
