@@ -318,6 +318,20 @@ def test_negative_scales(gpu, B):
     check_one_head(-4 + 3 * rng.standard_normal(n), rng.integers(-127, 128, (n, D)), vs, B)
 
 
+@needs_gpu
+@pytest.mark.parametrize("B", [1, 320])
+@pytest.mark.parametrize("size", [1e28, 1e31, 1e36])
+def test_scores_far_below_zero(gpu, size, B):
+    """The largest is all that counts, however low it is: its value comes out."""
+    rng = np.random.default_rng(20)
+    for n in (3, 200, 5000):
+        x = -size * (1.0 + 1e-3 * rng.permutation(n))
+        codes = rng.integers(-127, 128, (n, D))
+        out = attend(one_head(x, codes, np.full(n, 0.01)), n, B)
+        want = codes[x.argmax()] * float(np.float32(0.01))
+        assert (np.abs(out - want) <= (2.0 ** -8 + 2.0 ** -10) * np.abs(want)).all()
+
+
 # --------------------------------------------------------------- many new tokens
 
 @needs_gpu

@@ -82,7 +82,7 @@ constexpr int kMinShare = kTileBlocks;
 constexpr int kPStride = 288;       // bytes of a row of weights: rows 32 bytes apart mod 128
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
-constexpr float kNone = -1e30f;     // reference of a row that has seen nothing
+constexpr float kNone = -FLT_MAX;     // reference of a row that has seen nothing: no score is below it
 // Weights times their scales: what a row's references may let through (of the weights
 // by themselves too), the logarithm of what a reference set in passing is lifted at, and
 // of a power of two above the row's largest, not more than four times that, where one is
