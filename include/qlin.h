@@ -620,7 +620,12 @@ qlin_status_t qlin_kv_read_bf16(const void *cache, int64_t pages, int64_t page_s
  * no row sees have no effect, whatever they hold.  Non-finite scales at seen tokens give
  * non-finite outputs for the rows that see them.  The result does not depend
  * on timing, but in its last bits on the batch and max_pages, which decide how
- * sequences are cut.
+ * sequences are cut.  Scores are fp32: beyond its range they are infinite.
+ *
+ * Made for one new token or a drafted block: up to 32 rows of a key/value head
+ * (T * q_heads / kv_heads) read the cache once; more go in tiles of 32, each
+ * through all tokens that any new one of the sequence sees.  Contexts of a few
+ * hundred tokens take 5 to 25% less time in a table not much wider than they are.
  *
  *   q        bf16 [B T, q_heads * 128]  (rotated, qlin_kv_write_i8)
  *   q_heads  a positive multiple of kv_heads, at most 65535

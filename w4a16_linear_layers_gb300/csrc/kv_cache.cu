@@ -24,13 +24,15 @@
 // three steps of a reduction.  A warp goes through heads of one row four at a
 // time, the next four on their way, with the rotation's factors in registers.
 //
-// Long calls are bound by memory: 8192 rows of 32 + 16 heads take 39.7 us, 4.7 TB/s
-// of what has to move, and 36.4 us where nothing is normalised or turned.  With a half warp a head, partners R/16 lanes away and whole heads
-// decided again where one code was near a half-integer it took 98.6.  Warps that
-// stay and take rows in turn took 42 to 46 us, two or three groups ahead 46 to 48;
-// 16 warps an SM 46, 24 with spilled registers 46 to 49.  Short calls are a chain
-// of loads (length, angles or page, the head) and take 3.6 us, 1.5 of them above
-// an empty launch.
+// Long calls wait for their loads: 8192 rows of 32 + 16 heads take 39.8 us, 4.6 TB/s of
+// what has to move and 3.7 TB/s of DRAM traffic (what is written last stays in L2), 36.4 us
+// where nothing is normalised or turned.  Memory is not full, nor is issue (53%): 20 warps
+// an SM with one group each on its way, in 2.7 rounds of blocks.  With a half warp a head,
+// partners R/16 lanes away and whole heads decided again where one code was near a
+// half-integer it took 98.6.  Warps that stay and take rows in turn took 42 to 46 us, two
+// or three groups ahead 46 to 48; 16 warps an SM 46, 24 with spilled registers 46 to 49.
+// Short calls are a chain of loads (length, angles or page, the head) and take 3.6 us, 1.5
+// of them above an empty launch.
 #include <algorithm>
 #include <type_traits>
 

@@ -481,7 +481,9 @@ def paged_attn_i8(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
 
     scale: default 1 / sqrt(128).  softcap > 0: scores capped to softcap *
     tanh(score / softcap).  A token sees those up to itself (causal) or all,
-    with window > 0 those less than window away.  workspace: a uint8 tensor of
+    with window > 0 those less than window away.  Made for one new token or a
+    drafted block; a long prompt goes in tiles of 32 rows of a key/value head,
+    each through the whole context.  workspace: a uint8 tensor of
     paged_attn_workspace_bytes(B, T, q_heads, kv_heads) bytes; allocated for the
     call when not given."""
     call = (_torch_calls or _calls()).paged_attn
