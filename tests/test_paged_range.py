@@ -132,6 +132,41 @@ def test_values_written_and_read_by_attention_near_the_largest(gpu):
     a.check(a.run())
 
 
+@needs_gpu
+@pytest.mark.parametrize("B", [1, 320])
+@pytest.mark.parametrize("rise", [0.5, 0.9, 1.5])
+def test_small_values_under_rising_scores(gpu, rise, B):
+    """Two rows of a head.  The first one's scores rise by 16 powers of two every 128 tokens.
+    The second sees tokens of values of ordinary size at a score of 0 all along, and others,
+    whose scores rise slowly and whose values are 2^-100 of those: they count in its
+    denominator alone, and the products of the others, the largest, keep their precision."""
+    rng = np.random.default_rng(21)
+    n = 60 * 128
+    tile = np.arange(n) // 128
+    slow = rng.random(n) < 0.3
+    vs = np.where(slow, 2.0 ** -100, 1.0) / 64
+    codes = rng.integers(-127, 128, (n, D))
+    raw = one_head(np.full(n, 64 * 16 * np.log(2.0)), codes, vs)
+    flat = raw.reshape(-1, ref.BLOCK)
+    for d, c in ((0, tile), (1, np.where(slow, tile, 0))):
+        for r in range(16):
+            flat[:, ref.PLACES[r][d]] = 128 + c[r::16]
+    q = np.zeros((B, 2, D))
+    q[:, 0, 0], q[:, 1, 1] = 1.0, rise / 16
+    q = ref.bf16(q.reshape(B, -1))
+    table = np.broadcast_to(np.arange(raw.shape[0], dtype=np.int32), (B, raw.shape[0])).copy()
+    out = qlin.paged_attn_i8(to_dev_bits(q, torch.bfloat16), to_dev(raw), to_dev(table), to_dev(np.full(B, n, np.int32)), scale=1.0)
+    out = ref.bf16_to_f64(from_dev_bits(out)).reshape(B, 2, D)
+    step = float(np.float32(16 * np.log(2.0)))
+    q64 = ref.bf16_to_f64(q).reshape(B, 2, D)[0]
+    for row, x in ((0, tile * step), (1, np.where(slow, tile, 0) * step * q64[1, 1])):
+        o64, A, _ = expected(x, codes, vs)
+        # (of what is rounded to steps each is 2^-24 of the largest product with a scale)
+        p = np.exp(x - x.max())
+        big = 127 * (p / p.sum() * vs).max()
+        assert (np.abs(out[:, row] - o64) <= tolerance(o64, A, np.abs(x).max(), big, n)).all(), (row, out[0, row, :4], o64[:4])
+
+
 # ------------------------------------------------------- small weights, many
 
 @needs_gpu

@@ -885,13 +885,16 @@ __global__ void __launch_bounds__(kAttnThreads, kPerSm) attn_kernel(const AttnPa
       }
       if (warp == 0 && lane < S::kRows) {
         const float m = -ref[0], c = -log2_of(ref[2]);
-        // m up wherever it is below a score, so that no weight passes 1
+        // m up wherever it is below a score, so that no weight passes 1: by a whole number,
+        // which c, where no product is larger than before, goes down by (a little more or
+        // less, where fp32 rounded m, does not round it up), so that products stay where they
+        // are however often m goes up; or, where nothing is left of what was, to the score
         const bool up = most > m || (most - m) + over - c > kLiftWeight;
         float2 keep = make_float2(1.0f, 1.0f);
         if (up) {
-          const float to = fmaxf(m, most), down = m - to;
-          // (what stands under the references does not grow)
-          const float c_to = fminf(fmaxf(fmaxf(ceilf(over + (most - to)) - kNewWeight, ceilf(c + down)), -kMostScale), kMostScale);
+          const float rise = most - m;
+          const float to = !(rise > 0.0f) ? m : rise < 0x1p20f ? m + ceilf(rise) : most, down = m - to;
+          const float c_to = fminf(fmaxf(fmaxf(ceilf(over + (most - to)) - kNewWeight, ceilf(c + down - 0x1p-6f)), -kMostScale), kMostScale);
           keep = make_float2(ex2(down), ex2(down + (c - c_to)));
           ref[0] = -to;
           ref[2] = power_of_two(-c_to);
