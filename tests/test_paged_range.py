@@ -58,7 +58,7 @@ def expected(x, vcodes, vs):
 
 def attend(raw, n, B=1, **kw):
     """Rows of B sequences that all have the same pages."""
-    table = np.broadcast_to(np.arange(raw.shape[0], dtype=np.int32), (B, raw.shape[0]))
+    table = np.broadcast_to(np.arange(raw.shape[0], dtype=np.int32), (B, raw.shape[0])).copy()
     out = qlin.paged_attn_i8(to_dev_bits(first(B), torch.bfloat16), to_dev(raw), to_dev(table), to_dev(np.full(B, n, np.int32)),
                              **{"scale": 1.0, **kw})
     return ref.bf16_to_f64(from_dev_bits(out))
